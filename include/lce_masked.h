@@ -79,9 +79,16 @@ extern "C" {
                                        buffer of the call, other than the documented in-place
                                        case of the CE backward                                   */
 #define LCE_ERR_SCRATCH_LIMIT   10  /* n > LCE_NOALLOC_MAX_ROWS (allocation-free call only)      */
+#define LCE_ERR_BAD_DTYPE       11  /* unknown element type, or a pair of types a call lacks     */
 
 /* bits of *status_out */
 #define LCE_STATUS_BAD_LABEL     1  /* some label was neither ignore_index nor in [0, V)          */
+#define LCE_STATUS_BAD_TOKEN     1  /* the same bit, for the tokens of embed_*                    */
+
+/* element types of the embedding and layer norm calls */
+#define LCE_DTYPE_BF16           0
+#define LCE_DTYPE_F16            1
+#define LCE_DTYPE_F32            2
 
 /* flce flags */
 #define FLCE_RECOMPUTE           1u /* do not store the chunk's logits; recompute the logits
@@ -290,6 +297,82 @@ int flce_bwd(const uint16_t* hidden, const uint16_t* weight, const float* bias,
              const float* grad_output, uint16_t* grad_hidden, float* grad_weight,
              float* grad_bias, int32_t* status_out, void* workspace, size_t workspace_bytes,
              void* stream);
+
+/* ------------------------------------------------------------------ embedding */
+
+/* The lookup in front of the model and its gradient. The table is often the lm_head weight too
+ * (Liger-Kernel issue #941), so its gradient can be added into the buffer that FLCE_ACCUMULATE
+ * adds into. Tokens follow the rules of labels: int32; a row carries a token when
+ * token != ignore_index and 0 <= token < v; any other token that is not ignore_index sets
+ * LCE_STATUS_BAD_TOKEN in *status_out and its row is treated as ignored.
+ *
+ * embed_fwd: out[i, :] = scale * weight[token_i, :], computed in fp32 and rounded once to the
+ * table's type; exactly 0 for rows without a token.
+ *   weight   dtype [v, ldw], first h columns      tokens  int32 [n]
+ *   out      dtype [n, ldo], first h columns; the columns past h are left as they are
+ * Any row stride >= h and any alignment of an element are accepted. n == 0 is valid. */
+int embed_fwd(const void* weight, int dtype, int64_t v, int64_t h, int64_t ldw,
+              const int32_t* tokens, int64_t n, int32_t ignore_index, float scale, void* out,
+              int64_t ldo, int32_t* status_out, void* stream);
+
+/* flags of embed_bwd */
+#define EMBED_ACCUMULATE         1u /* add into grad_weight instead of overwriting it            */
+
+/* Workspace bytes of embed_bwd: the positions sorted by token (twice past 8192 of them) and the
+ * partial sums of tokens whose rows are added in several places. Host-only. */
+int embed_workspace_size(int64_t n, int64_t h, int64_t v, size_t* bytes);
+
+/* grad_weight[v, :] (=|+=) scale * (sum of grad[i, :] over the rows i with token v). The sums are
+ * fp32, in an order that depends on n and on the tokens alone, without atomics (bitwise
+ * repeatable), rounded once to grad_weight's type. Without EMBED_ACCUMULATE every row of
+ * grad_weight is written, with 0 where no row has its token; with it, rows without a token are
+ * not touched. Rows of grad without a token are not read.
+ *   grad         dtype [n, ldg], first h columns
+ *   grad_weight  grad_dtype [v, ldw], first h columns; grad_dtype is dtype or LCE_DTYPE_F32 */
+int embed_bwd(const void* grad, int dtype, int64_t ldg, const int32_t* tokens, int64_t n,
+              int64_t h, int64_t v, int32_t ignore_index, float scale, uint32_t flags,
+              void* grad_weight, int grad_dtype, int64_t ldw, int32_t* status_out,
+              void* workspace, size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------ layer norm */
+
+/* The norm in front of the head: y is the hidden operand of the fused linear CE. */
+#define LAYERNORM_MAX_H          32768
+
+/* y = (x - mean) * rstd * weight + bias per row, mean and rstd = 1 / sqrt(variance + eps) over
+ * the row's h elements (the variance about the mean, divided by h), all in fp32, rounded once.
+ *   x, y          dtype [n, ldx] / [n, ldy], first h columns; y == x with ldy == ldx is the
+ *                 in-place case
+ *   weight, bias  param_dtype [h] or NULL (1 and 0); param_dtype is dtype or LCE_DTYPE_F32
+ *   mean_out, rstd_out  fp32 [n] or NULL, what the backward needs
+ * 1 <= h <= LAYERNORM_MAX_H, any alignment of an element. n == 0 is valid. */
+int layernorm_fwd(const void* x, int dtype, int64_t n, int64_t h, int64_t ldx, const void* weight,
+                  const void* bias, int param_dtype, float eps, void* y, int64_t ldy,
+                  float* mean_out, float* rstd_out, void* stream);
+
+/* flags of layernorm_bwd */
+#define LAYERNORM_ACCUMULATE     1u /* add into grad_weight and grad_bias                        */
+
+/* Workspace bytes of layernorm_bwd: one partial row of each parameter gradient for at most 256
+ * workgroups. Host-only. */
+int layernorm_workspace_size(int64_t n, int64_t h, size_t* bytes);
+
+/* Gradients of layernorm_fwd from its x, mean and rstd. With u = grad * weight and
+ * xhat = (x - mean) * rstd:  grad_x = rstd * (u - mean(u) - xhat * mean(u * xhat)),
+ * grad_weight (=|+=) sum over rows of grad * xhat, grad_bias (=|+=) sum over rows of grad; fp32
+ * sums in an order that depends on n and h alone, without atomics.
+ *   grad, grad_x  dtype [n, ldg] / [n, lddx]; grad_x == grad with lddx == ldg is the in-place
+ *                 case; grad_x may be NULL
+ *   weight        as in the forward
+ *   grad_weight, grad_bias  grad_param_dtype [h] or NULL; grad_param_dtype is param_dtype or
+ *                 LCE_DTYPE_F32. With n == 0 they are set to 0, or left as they are with
+ *                 LAYERNORM_ACCUMULATE.
+ * The workspace is needed only where grad_weight or grad_bias is asked for. */
+int layernorm_bwd(const void* grad, int dtype, int64_t ldg, const void* x, int64_t ldx,
+                  const float* mean, const float* rstd, const void* weight, int param_dtype,
+                  int64_t n, int64_t h, uint32_t flags, void* grad_x, int64_t lddx,
+                  void* grad_weight, void* grad_bias, int grad_param_dtype, void* workspace,
+                  size_t workspace_bytes, void* stream);
 
 /* ------------------------------------------------------------------ measurement aid */
 

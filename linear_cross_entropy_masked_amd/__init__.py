@@ -8,7 +8,9 @@ function whose library is missing raises.
 
 Entry points (same names as the C ABI):
     ce_chunked_fwd, ce_chunked_bwd, ce_chunked_bwd_inplace, flce_fwd_bwd, flce_fwd, flce_bwd,
-    ce_chunked_workspace_size, flce_workspace_size, lce_status_str
+    embed_fwd, embed_bwd, layernorm_fwd, layernorm_bwd,
+    ce_chunked_workspace_size, flce_workspace_size, embed_workspace_size,
+    layernorm_workspace_size, lce_status_str
 """
 from __future__ import annotations
 
@@ -23,12 +25,19 @@ __all__ = [
     "flce_workspace_size", "flce_fwd_bwd", "flce_fwd", "flce_bwd", "lce_status_str",
     "flce_status_str",
     "FLCE_RECOMPUTE", "FLCE_ACCUMULATE", "LCE_STATUS_BAD_LABEL",
+    "embed_fwd", "embed_workspace_size", "embed_bwd", "EMBED_ACCUMULATE", "LCE_STATUS_BAD_TOKEN",
+    "layernorm_fwd", "layernorm_workspace_size", "layernorm_bwd", "LAYERNORM_ACCUMULATE",
+    "LAYERNORM_MAX_H",
     "lce_timing_enable", "lce_timing_read",
 ]
 
 FLCE_RECOMPUTE = 1
 FLCE_ACCUMULATE = 2
 LCE_STATUS_BAD_LABEL = 1
+LCE_STATUS_BAD_TOKEN = 1
+EMBED_ACCUMULATE = 1
+LAYERNORM_ACCUMULATE = 1
+LAYERNORM_MAX_H = 32768
 LCE_NOALLOC_MAX_ROWS = 1 << 20  # rows the allocation-free CE step's static scratch holds
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -57,6 +66,7 @@ def load_library() -> ctypes.CDLL:
             "(the HIP library is the only implementation; there is no fallback)")
     lib = ctypes.CDLL(path)
     i64, i32, u32, sz, vp = ctypes.c_int64, ctypes.c_int32, ctypes.c_uint32, ctypes.c_size_t, ctypes.c_void_p
+    f32, dt = ctypes.c_float, ctypes.c_int
     psz = ctypes.POINTER(ctypes.c_size_t)
     sigs = {
         "lce_status_str": (ctypes.c_char_p, [ctypes.c_int]),
@@ -79,6 +89,15 @@ def load_library() -> ctypes.CDLL:
                                     sz, vp]),
         "flce_bwd": (ctypes.c_int, [vp, vp, vp, vp, vp, i64, i64, i64, i32, i64, i64, u32, vp, vp,
                                     vp, vp, vp, vp, sz, vp]),
+        "embed_fwd": (ctypes.c_int, [vp, dt, i64, i64, i64, vp, i64, i32, f32, vp, i64, vp, vp]),
+        "embed_workspace_size": (ctypes.c_int, [i64, i64, i64, psz]),
+        "embed_bwd": (ctypes.c_int, [vp, dt, i64, vp, i64, i64, i64, i32, f32, u32, vp, dt, i64, vp,
+                                     vp, sz, vp]),
+        "layernorm_fwd": (ctypes.c_int, [vp, dt, i64, i64, i64, vp, vp, dt, f32, vp, i64, vp, vp,
+                                         vp]),
+        "layernorm_workspace_size": (ctypes.c_int, [i64, i64, psz]),
+        "layernorm_bwd": (ctypes.c_int, [vp, dt, i64, vp, i64, vp, vp, vp, dt, i64, i64, u32, vp,
+                                         i64, vp, vp, dt, vp, sz, vp]),
         "lce_timing_enable": (ctypes.c_int, [ctypes.c_int]),
         "lce_timing_read": (ctypes.c_int, [ctypes.c_int, ctypes.POINTER(ctypes.c_char_p),
                                            ctypes.POINTER(ctypes.c_double),
@@ -502,6 +521,226 @@ def flce_bwd(hidden, weight, labels, lse, bias=None, *, ignore_index: int = -100
     return gh, gw, gb
 
 
+def _call(fn, device, *args):
+    """fn(*args) with ``device`` current (the library checks and launches on the current one);
+    raises on a status code. The stream, the last argument, is the caller's current one there."""
+    import torch
+    f = getattr(load_library(), fn)
+    if device.index == torch.cuda.current_device():
+        code = f(*args, torch.cuda.current_stream(device).cuda_stream)
+    else:
+        with torch.cuda.device(device):
+            code = f(*args, torch.cuda.current_stream(device).cuda_stream)
+    if code != 0:
+        raise LceError(fn, code)
+
+
+def _adr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _dtype_code(dtype, name):
+    import torch
+    code = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}.get(dtype)
+    if code is None:
+        raise TypeError(f"{name} must be bfloat16, float16 or float32, got {dtype}")
+    return code
+
+
+def _rows_2d(t, name, dtype=None, shape=None, device=None):
+    """The row stride of a 2-d tensor whose rows are contiguous."""
+    _require(t, name, dtype, 2, device)
+    n, h = t.shape
+    if shape is not None and (n, h) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {(n, h)}")
+    if h > 1 and n > 0 and t.stride(1) != 1:
+        raise ValueError(f"{name} rows must be contiguous (stride(1) == 1)")
+    return t.stride(0) if n > 1 else h
+
+
+def _status_ptr(status, device):
+    if status is None:
+        return None
+    import torch
+    _require(status, "status", torch.int32, status.dim(), device)
+    if status.numel() < 1:
+        raise ValueError("status must hold one int32")
+    return status.data_ptr()
+
+
+def _bytes_of(workspace):
+    return workspace.numel() * workspace.element_size()
+
+
+def embed_fwd(weight, tokens, *, scale: float = 1.0, ignore_index: int = -100, out=None,
+              status=None):
+    """Embedding lookup: row i of the result is scale · weight[tokens[i]], 0 where the token is
+    ``ignore_index`` or outside the table (then LCE_STATUS_BAD_TOKEN is set in ``status``).
+    weight bf16 / fp16 / fp32 [v, h], tokens int32 or int64 [n]; returns ``out`` [n, h]."""
+    import torch
+    code = _dtype_code(getattr(weight, "dtype", None), "weight")
+    ldw = _rows_2d(weight, "weight")
+    dev = weight.device
+    v, h = weight.shape
+    tokens = _tokens_i32(tokens, dev, ignore_index)
+    n = tokens.shape[0]
+    if out is None:
+        out = torch.empty((n, h), dtype=weight.dtype, device=dev)
+    ldo = _rows_2d(out, "out", weight.dtype, (n, h), dev)
+    _call("embed_fwd", dev, weight.data_ptr(), code, v, h, ldw, tokens.data_ptr(), n,
+          ignore_index, scale, out.data_ptr(), ldo, _status_ptr(status, dev))
+    return out
+
+
+def _tokens_i32(tokens, device, ignore_index):
+    import torch
+    _require(tokens, "tokens", None, 1, device)
+    if tokens.dtype == torch.int32:
+        return tokens.contiguous()
+    if tokens.dtype != torch.int64:
+        raise TypeError("tokens must be int32 or int64")
+    return _labels_i32(tokens, tokens.shape[0], device, ignore_index)
+
+
+def embed_workspace_size(n: int, h: int, v: int) -> int:
+    out = ctypes.c_size_t()
+    _check("embed_workspace_size",
+           load_library().embed_workspace_size(n, h, v, ctypes.byref(out)))
+    return out.value
+
+
+def embed_bwd(grad, tokens, num_embeddings: int, *, scale: float = 1.0, ignore_index: int = -100,
+              grad_weight=None, dtype=None, accumulate: bool = False, status=None,
+              workspace=None):
+    """Gradient of :func:`embed_fwd` for its table: row v of the result is scale times the sum of
+    the rows of ``grad`` [n, h] whose token is v, summed in fp32 in a fixed order. Written to
+    ``grad_weight`` [num_embeddings, h] (added to it with ``accumulate``), or to a new tensor of
+    ``dtype`` (default: grad's). Its type is grad's or float32."""
+    import torch
+    code = _dtype_code(getattr(grad, "dtype", None), "grad")
+    ldg = _rows_2d(grad, "grad")
+    dev = grad.device
+    n, h = grad.shape
+    v = int(num_embeddings)
+    tokens = _tokens_i32(tokens, dev, ignore_index)
+    if tokens.shape[0] != n:
+        raise ValueError(f"tokens has {tokens.shape[0]} entries, expected {n}")
+    if grad_weight is None:
+        if accumulate:
+            raise ValueError("accumulate=True needs an existing grad_weight tensor")
+        grad_weight = torch.empty((v, h), dtype=dtype or grad.dtype, device=dev)
+    elif dtype is not None and grad_weight.dtype != dtype:
+        raise TypeError(f"grad_weight must be {dtype}, got {grad_weight.dtype}")
+    ldw = _rows_2d(grad_weight, "grad_weight", None, (v, h), dev)
+    ws = _workspace(embed_workspace_size(n, h, v), dev, workspace)
+    _call("embed_bwd", dev, grad.data_ptr(), code, ldg, tokens.data_ptr(), n, h, v, ignore_index,
+          scale, EMBED_ACCUMULATE if accumulate else 0, grad_weight.data_ptr(),
+          _dtype_code(grad_weight.dtype, "grad_weight"), ldw, _status_ptr(status, dev),
+          ws.data_ptr(), _bytes_of(ws))
+    return grad_weight
+
+
+def _norm_param(t, name, h, device):
+    _require(t, name, None, 1, device)
+    if t.shape[0] != h:
+        raise ValueError(f"{name} must have {h} entries, got {t.shape[0]}")
+    return t.contiguous()
+
+
+def layernorm_fwd(x, weight=None, bias=None, *, eps: float = 1e-5, out=None,
+                  return_stats: bool = True):
+    """Layer norm over the last dimension of x [n, h] (bf16 / fp16 / fp32). weight and bias: [h],
+    of x's type or float32 (both the same type), or None. ``out`` may be x itself. Returns
+    (y, mean, rstd), the fp32 [n] statistics None without ``return_stats``."""
+    import torch
+    code = _dtype_code(getattr(x, "dtype", None), "x")
+    ldx = _rows_2d(x, "x")
+    dev = x.device
+    n, h = x.shape
+    pdtype = x.dtype
+    if weight is not None:
+        weight = _norm_param(weight, "weight", h, dev)
+        pdtype = weight.dtype
+    if bias is not None:
+        bias = _norm_param(bias, "bias", h, dev)
+        if weight is not None and bias.dtype != pdtype:
+            raise TypeError(f"bias is {bias.dtype}, weight {pdtype}: they must be of one type")
+        pdtype = bias.dtype
+    if out is None:
+        out = torch.empty((n, h), dtype=x.dtype, device=dev)
+    ldy = _rows_2d(out, "out", x.dtype, (n, h), dev)
+    mean = rstd = None
+    if return_stats:
+        mean = torch.empty(n, dtype=torch.float32, device=dev)
+        rstd = torch.empty(n, dtype=torch.float32, device=dev)
+    _call("layernorm_fwd", dev, x.data_ptr(), code, n, h, ldx, _adr(weight), _adr(bias),
+          _dtype_code(pdtype, "weight"), eps, out.data_ptr(), ldy, _adr(mean), _adr(rstd))
+    return out, mean, rstd
+
+
+def layernorm_workspace_size(n: int, h: int) -> int:
+    out = ctypes.c_size_t()
+    _check("layernorm_workspace_size",
+           load_library().layernorm_workspace_size(n, h, ctypes.byref(out)))
+    return out.value
+
+
+def layernorm_bwd(grad, x, mean, rstd, weight=None, *, grad_x=True, grad_weight=None,
+                  grad_bias=None, accumulate: bool = False, workspace=None):
+    """Gradients of :func:`layernorm_fwd` from its x and statistics. ``grad_x`` /
+    ``grad_weight`` / ``grad_bias``: True to allocate (the parameter gradients in the weight's
+    type), False to skip, or a tensor to write into (grad_x may be ``grad`` itself; the
+    parameter gradients may be float32, and are added to with ``accumulate``). grad_weight
+    defaults to True when a weight is given, grad_bias to False. Returns (grad_x, grad_weight,
+    grad_bias)."""
+    import torch
+    code = _dtype_code(getattr(x, "dtype", None), "x")
+    ldx = _rows_2d(x, "x")
+    dev = x.device
+    n, h = x.shape
+    ldg = _rows_2d(grad, "grad", x.dtype, (n, h), dev)
+    for t, name in ((mean, "mean"), (rstd, "rstd")):
+        _require(t, name, torch.float32, 1, dev)
+        if t.shape[0] != n or (n > 1 and t.stride(0) != 1):
+            raise ValueError(f"{name} must be a contiguous float32 [{n}] tensor")
+    pdtype = x.dtype
+    if weight is not None:
+        weight = _norm_param(weight, "weight", h, dev)
+        pdtype = weight.dtype
+    if grad_weight is None:
+        grad_weight = weight is not None
+
+    def param_out(spec, name):
+        if spec is True:
+            if accumulate:
+                raise ValueError(f"accumulate=True needs an existing {name} tensor")
+            return torch.empty(h, dtype=pdtype, device=dev)
+        if spec is False or spec is None:
+            return None
+        _require(spec, name, None, 1, dev)
+        if spec.shape[0] != h or (h > 1 and spec.stride(0) != 1):
+            raise ValueError(f"{name} must be a contiguous [{h}] tensor")
+        return spec
+
+    if grad_x is True:
+        grad_x = torch.empty((n, h), dtype=x.dtype, device=dev)
+    elif grad_x is False:
+        grad_x = None
+    lddx = h if grad_x is None else _rows_2d(grad_x, "grad_x", x.dtype, (n, h), dev)
+    gw, gb = param_out(grad_weight, "grad_weight"), param_out(grad_bias, "grad_bias")
+    if gw is not None and gb is not None and gw.dtype != gb.dtype:
+        raise TypeError("grad_weight and grad_bias must be of one type")
+    gdtype = gw.dtype if gw is not None else gb.dtype if gb is not None else pdtype
+    ws = None
+    if gw is not None or gb is not None:
+        ws = _workspace(layernorm_workspace_size(n, h), dev, workspace)
+    _call("layernorm_bwd", dev, grad.data_ptr(), code, ldg, x.data_ptr(), ldx, mean.data_ptr(),
+          rstd.data_ptr(), _adr(weight), _dtype_code(pdtype, "weight"), n, h,
+          LAYERNORM_ACCUMULATE if accumulate else 0, _adr(grad_x), lddx, _adr(gw), _adr(gb),
+          _dtype_code(gdtype, "grad_weight"), _adr(ws), 0 if ws is None else _bytes_of(ws))
+    return grad_x, gw, gb
+
+
 def lce_timing_enable(on: bool = True) -> None:
     """Bracket every library launch with hipEvents (measurement aid; off by default)."""
     _check("lce_timing_enable", load_library().lce_timing_enable(1 if on else 0))
@@ -510,7 +749,7 @@ def lce_timing_enable(on: bool = True) -> None:
 def lce_timing_read() -> list[tuple[str, float, int]]:
     """(kernel name, total ms, launches) per kernel since the previous read; resets totals."""
     lib = load_library()
-    cap = 32
+    cap = 64
     names = (ctypes.c_char_p * cap)()
     ms = (ctypes.c_double * cap)()
     cnt = (ctypes.c_longlong * cap)()

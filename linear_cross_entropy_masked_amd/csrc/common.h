@@ -111,6 +111,13 @@ enum KernelId {
   K_CE_FUSED_ROWS,
   K_FLCE_LOSS_ACC,
   K_FLCE_PROBS_TRANSPOSED,
+  K_EMBED_FWD,
+  K_EMBED_SORT,
+  K_EMBED_GRAD,
+  K_EMBED_JOIN,
+  K_NORM_FWD,
+  K_NORM_BWD,
+  K_NORM_PARAM_REDUCE,
   K_COUNT
 };
 

@@ -1,0 +1,509 @@
+// Embedding lookup with scaling and its gradient, for gfx950.
+//
+//   lookup    out[i, :] = scale · W[t_i, :]        (0 for a row whose token is ignored or bad)
+//   gradient  dW[v, :] (=|+=) scale · Σ_{i: t_i = v} g[i, :]
+//
+// Both are memory-bound: the lookup reads and writes n rows, the gradient reads n rows and, when
+// it overwrites dW, writes all v of them. Every multiply and sum is fp32, rounded once on the
+// way out, and a token's rows are added in increasing position without atomics, so a result
+// does not change from run to run.
+//
+// The gradient puts the positions in the order of their tokens first (stable), then walks the
+// sorted list in chunks of equal length, so that a token that fills half the batch costs no
+// more than the same number of rare ones:
+//   1. rank_sort_kernel: runs of kRun positions, each sorted by counting for every key the keys
+//      of its run below it;
+//   2. merge_runs_kernel: up to kMergeWays sorted runs become one per launch, every element
+//      finding its place by binary searches (none for n <= kRun);
+//   3. segment_sums_kernel: one chunk of sorted positions and one block of columns per thread
+//      group; a token wholly inside a chunk is finished there, one that crosses a chunk border
+//      leaves a partial sum per chunk. The same launch zeroes the rows no position names;
+//   4. join_chunks_kernel: the partial sums of each crossing token, added in chunk order.
+#include <algorithm>
+
+#include "common.h"
+#include "elem.h"
+#include "ops.h"
+
+namespace lce {
+
+namespace {
+
+constexpr int kRun = 8192;       // positions per sorted run
+constexpr int kRankWaves = 16;   // wavefronts that share one ranking workgroup's keys
+constexpr int kMergeWays = 16;
+constexpr int kThreads = 256;
+constexpr int kFillRows = 16;    // vocabulary rows per zeroing workgroup
+
+__device__ __forceinline__ bool token_ok(int32_t t, int64_t v, int32_t ignore_index) {
+  return t != ignore_index && t >= 0 && int64_t(t) < v;
+}
+
+// ------------------------------------------------------------------ lookup
+
+// tpr lanes (a power of two) per row, kVecs vectors each; 256 / tpr rows per workgroup.
+constexpr int kLookupVecs = 4;
+template <class T>
+__global__ void __launch_bounds__(kThreads) embed_fwd_kernel(
+    const T* __restrict__ w, int64_t v, int64_t h, int64_t ldw,
+    const int32_t* __restrict__ tokens, int64_t n, int32_t ignore_index, float scale,
+    T* __restrict__ out, int64_t ldo, int tpr, int64_t colblocks) {
+  constexpr int VE = Elem<T>::kVec;
+  const int64_t rb = int64_t(blockIdx.x) / colblocks, cb = int64_t(blockIdx.x) % colblocks;
+  const int64_t i = rb * (kThreads / tpr) + threadIdx.x / tpr;
+  if (i >= n) return;
+  const int32_t t = tokens[i];
+  const bool ok = token_ok(t, v, ignore_index);
+  const T* src = w + (ok ? int64_t(t) : 0) * ldw;
+  T* dst = out + i * ldo;
+  const int64_t c0 = (cb * tpr * kLookupVecs + threadIdx.x % tpr) * VE;
+  float x[kLookupVecs][VE];
+#pragma unroll
+  for (int k = 0; k < kLookupVecs; ++k) {
+    const int64_t c = c0 + int64_t(k) * tpr * VE;
+    if (c < h) load_some<T, VE>(src + c, h - c, x[k]);
+  }
+#pragma unroll
+  for (int k = 0; k < kLookupVecs; ++k) {
+    const int64_t c = c0 + int64_t(k) * tpr * VE;
+    if (c >= h) continue;
+#pragma unroll
+    for (int q = 0; q < VE; ++q) x[k][q] = ok ? x[k][q] * scale : 0.f;
+    store_some<T, VE>(dst + c, h - c, x[k]);
+  }
+}
+
+// One workgroup: *status = LCE_STATUS_BAD_LABEL if some token is neither ignored nor in [0, v).
+__global__ void __launch_bounds__(1024) token_status_kernel(const int32_t* __restrict__ tokens,
+                                                            int64_t n, int64_t v,
+                                                            int32_t ignore_index,
+                                                            int32_t* __restrict__ status) {
+  __shared__ int any;
+  if (threadIdx.x == 0) any = 0;
+  __syncthreads();
+  int bad = 0;
+  for (int64_t i = threadIdx.x; i < n; i += 1024) {
+    const int32_t t = tokens[i];
+    bad |= int(t != ignore_index && !token_ok(t, v, ignore_index));
+  }
+  if (bad) any = 1;  // every writer writes the same value
+  __syncthreads();
+  if (threadIdx.x == 0) *status = any;
+}
+
+// ------------------------------------------------------------------ sort by token
+
+// One run of kRun positions: position i's key is token · kRun + (i − run start), tokens that
+// carry no row counting as v, so keys are distinct and their order is the stable order by
+// token. A key's place is the number of keys below it. Workgroup b of a run places 64 of its
+// positions: kRankWaves wavefronts each count over one slice of the run's keys in LDS. Key is
+// uint32_t where (v + 1) · kRun fits, else uint64_t: the compare is most of the work.
+template <class Key>
+__global__ void __launch_bounds__(64 * kRankWaves) rank_sort_kernel(
+    const int32_t* __restrict__ tokens, int64_t n, int64_t v, int32_t ignore_index,
+    int32_t* __restrict__ stok, int32_t* __restrict__ spos) {
+  constexpr int kPer = 16 / sizeof(Key);  // keys of one 16-byte LDS read
+  __shared__ __attribute__((aligned(16))) Key k[kRun];
+  __shared__ int cnt[kRankWaves][64];
+  const int64_t run0 = int64_t(blockIdx.x) / (kRun / 64) * kRun;
+  const int64_t left = n - run0;
+  const int rows = left < kRun ? int(left) : kRun;
+  const int i0 = int(blockIdx.x % (kRun / 64)) * 64;
+  if (i0 >= rows) return;  // uniform over the workgroup
+  const int padded = (rows + kPer - 1) / kPer * kPer;
+  for (int i = threadIdx.x; i < padded; i += 64 * kRankWaves) {
+    Key key = ~Key(0);  // padding: below nothing
+    if (i < rows) {
+      const int32_t t = tokens[run0 + i];
+      key = Key(token_ok(t, v, ignore_index) ? int64_t(t) : v) * kRun + Key(i);
+    }
+    k[i] = key;
+  }
+  __syncthreads();
+  const int r = threadIdx.x & 63, q = threadIdx.x >> 6;
+  const int i = i0 + r;
+  int below = 0;
+  if (i < rows) {
+    const Key x = k[i];
+    const int groups = padded / kPer;
+    const int per = (groups + kRankWaves - 1) / kRankWaves;
+    const int lo = q * per, hi = lo + per < groups ? lo + per : groups;
+    struct alignas(16) Pack {
+      Key e[kPer];
+    };
+    const Pack* p = reinterpret_cast<const Pack*>(k);
+#pragma unroll 4
+    for (int g = lo; g < hi; ++g) {
+      const Pack c = p[g];
+#pragma unroll
+      for (int u = 0; u < kPer; ++u) below += int(c.e[u] < x);
+    }
+  }
+  cnt[q][r] = below;
+  __syncthreads();
+  if (q == 0 && i < rows) {
+    int place = 0;
+#pragma unroll
+    for (int w = 0; w < kRankWaves; ++w) place += cnt[w][r];
+    stok[run0 + place] = int32_t(k[i] / kRun);
+    spos[run0 + place] = int32_t(run0 + i);
+  }
+}
+
+// Sorted runs of `len` elements, kMergeWays at a time into one: an element's place is its own
+// index plus, for every other run of its group, the number of elements that come before it
+// there (equal tokens of an earlier run do, those of a later run do not).
+__global__ void __launch_bounds__(kThreads) merge_runs_kernel(
+    const int32_t* __restrict__ tok_in, const int32_t* __restrict__ pos_in,
+    int32_t* __restrict__ tok_out, int32_t* __restrict__ pos_out, int64_t n, int64_t len) {
+  const int64_t e = int64_t(blockIdx.x) * kThreads + threadIdx.x;
+  if (e >= n) return;
+  const int32_t t = tok_in[e];
+  const int64_t run = e / len, group = run / kMergeWays;
+  const int64_t g0 = group * kMergeWays * len;
+  int64_t place = g0 + (e - run * len);
+  for (int64_t o = group * kMergeWays; o < (group + 1) * kMergeWays; ++o) {
+    const int64_t b = o * len;
+    if (b >= n) break;
+    if (o == run) continue;
+    int64_t lo = b, hi = b + len < n ? b + len : n;
+    while (lo < hi) {
+      const int64_t mid = (lo + hi) >> 1;
+      const int32_t x = tok_in[mid];
+      if (x < t || (x == t && o < run))
+        lo = mid + 1;
+      else
+        hi = mid;
+    }
+    place += lo - b;
+  }
+  tok_out[place] = t;
+  pos_out[place] = pos_in[e];
+}
+
+// ------------------------------------------------------------------ sums over equal tokens
+
+struct SegArgs {
+  const void* grad;
+  int64_t ldg;
+  const int32_t* stok;
+  const int32_t* spos;
+  int64_t n, h, v;
+  float scale;
+  void* dw;
+  int64_t ldw;
+  float* part;       // [chunks][2][h] partial sums of the tokens that cross a chunk border
+  int64_t len;       // positions per chunk
+  int64_t chunks, colblocks, seg_blocks;
+  int tpr;           // lanes per chunk and column block (a power of two)
+};
+
+// The first index in [0, n) whose token is >= t, found by the 64 lanes of a wavefront together:
+// each step probes 64 places, so n = 2^18 takes three dependent loads instead of eighteen.
+__device__ __forceinline__ int64_t wave_lower_bound(const int32_t* __restrict__ stok, int64_t n,
+                                                    int32_t t) {
+  const int lane = threadIdx.x & 63;
+  int64_t lo = 0, hi = n;
+  while (lo < hi) {
+    const int64_t step = (hi - lo + 63) >> 6;
+    const int64_t p = lo + (lane + 1) * step - 1;
+    const bool less = p < hi && stok[p] < t;
+    const int64_t c = __popcll(__ballot(less));
+    lo += c * step;
+    const int64_t h2 = lo + step - 1;
+    if (h2 < hi) hi = h2;
+  }
+  return lo;
+}
+
+template <class TW, int N, bool ACC>
+__device__ __forceinline__ void put_sum(TW* p, int64_t cnt, float scale, const float (&acc)[N]) {
+  float x[N];
+  if constexpr (ACC) {
+    load_some<TW, N>(p, cnt, x);
+#pragma unroll
+    for (int q = 0; q < N; ++q) x[q] += scale * acc[q];
+  } else {
+#pragma unroll
+    for (int q = 0; q < N; ++q) x[q] = scale * acc[q];
+  }
+  store_some<TW, N>(p, cnt, x);
+}
+
+constexpr int kBatch = 8;  // rows of the gradient in flight per lane
+
+template <class T, class TW, bool ACC>
+__global__ void __launch_bounds__(kThreads) segment_sums_kernel(SegArgs a) {
+  constexpr int VE = Elem<T>::kVec;
+  TW* const dw = static_cast<TW*>(a.dw);
+  if (int64_t(blockIdx.x) >= a.seg_blocks) {
+    // rows that no position names: four per wavefront
+    if constexpr (!ACC) {
+      constexpr int kRows = kFillRows / (kThreads / 64);
+      const int lane = threadIdx.x & 63;
+      const int64_t r0 = (int64_t(blockIdx.x) - a.seg_blocks) * kFillRows +
+                         int64_t(threadIdx.x >> 6) * kRows;
+#pragma unroll
+      for (int k = 0; k < kRows; ++k) {
+        const int64_t r = r0 + k;
+        if (r >= a.v) break;
+        const int64_t p = wave_lower_bound(a.stok, a.n, int32_t(r));
+        if (p < a.n && a.stok[p] == int32_t(r)) continue;
+        constexpr int VW = Elem<TW>::kVec;
+        const float zero[VW] = {};
+        for (int64_t c = int64_t(lane) * VW; c < a.h; c += 64 * VW)
+          store_some<TW, VW>(dw + r * a.ldw + c, a.h - c, zero);
+      }
+    }
+    return;
+  }
+  const int64_t item = int64_t(blockIdx.x) * (kThreads / a.tpr) + threadIdx.x / a.tpr;
+  const int64_t chunk = item / a.colblocks, cb = item % a.colblocks;
+  if (chunk >= a.chunks) return;
+  const int64_t col = (cb * a.tpr + threadIdx.x % a.tpr) * VE;
+  if (col >= a.h) return;
+  const int64_t cnt = a.h - col;
+  const T* const g = static_cast<const T*>(a.grad) + col;
+  const int64_t p0 = chunk * a.len;
+  const int64_t p1 = p0 + a.len < a.n ? p0 + a.len : a.n;
+  const int32_t none = int32_t(a.v);  // sorted after every token: positions without a row
+  int32_t cur = a.stok[p0];
+  if (cur >= none) return;
+  bool from_left = p0 > 0 && a.stok[p0 - 1] == cur;
+  float acc[VE] = {};
+  auto flush = [&](bool to_right) {
+    if (from_left || to_right) {
+      float* p = a.part + (chunk * 2 + (from_left ? 0 : 1)) * a.h + col;
+#pragma unroll
+      for (int q = 0; q < VE; ++q)
+        if (q < cnt) p[q] = acc[q];
+    } else {
+      put_sum<TW, VE, ACC>(dw + int64_t(cur) * a.ldw + col, cnt, a.scale, acc);
+    }
+  };
+  for (int64_t p = p0; p < p1; p += kBatch) {
+    int32_t tok[kBatch];
+    float x[kBatch][VE];
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      tok[u] = p + u < p1 ? a.stok[p + u] : none;
+      const int64_t row = tok[u] < none ? a.spos[p + u] : 0;
+      if (tok[u] < none) load_some<T, VE>(g + row * a.ldg, cnt, x[u]);
+    }
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      if (tok[u] >= none) break;
+      if (tok[u] != cur) {
+        flush(false);
+        cur = tok[u];
+        from_left = false;
+#pragma unroll
+        for (int q = 0; q < VE; ++q) acc[q] = 0.f;
+      }
+#pragma unroll
+      for (int q = 0; q < VE; ++q) acc[q] += x[u][q];
+    }
+  }
+  flush(p1 < a.n && a.stok[p1] == cur);
+}
+
+// The token that starts in chunk c and runs past its end: its partial sums in chunk order.
+template <class T, class TW, bool ACC>
+__global__ void __launch_bounds__(kThreads) join_chunks_kernel(SegArgs a) {
+  constexpr int VE = Elem<T>::kVec;
+  const int64_t item = int64_t(blockIdx.x) * (kThreads / a.tpr) + threadIdx.x / a.tpr;
+  const int64_t chunk = item / a.colblocks, cb = item % a.colblocks;
+  if (chunk + 1 >= a.chunks) return;
+  const int64_t p0 = chunk * a.len, p1 = p0 + a.len;  // a later chunk exists: p1 < n
+  const int32_t cur = a.stok[p1 - 1];
+  if (cur >= int32_t(a.v) || a.stok[p1] != cur) return;
+  if (p0 > 0 && a.stok[p0 - 1] == cur) return;  // it starts in an earlier chunk
+  const int64_t col = (cb * a.tpr + threadIdx.x % a.tpr) * VE;
+  if (col >= a.h) return;
+  const int64_t cnt = a.h - col;
+  float acc[VE];
+  load_some<float, VE>(a.part + (chunk * 2 + 1) * a.h + col, cnt, acc);
+  bool more = true;
+  for (int64_t c = chunk + 1; more; c += kBatch) {
+    float x[kBatch][VE];
+    bool goes_on[kBatch];  // whether chunk c + u's first token is followed into the next chunk
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int64_t e = (c + u + 1) * a.len;
+      goes_on[u] = e < a.n && a.stok[e] == cur;
+      if (c + u < a.chunks) load_some<float, VE>(a.part + (c + u) * 2 * a.h + col, cnt, x[u]);
+    }
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      if (!more) break;
+#pragma unroll
+      for (int q = 0; q < VE; ++q) acc[q] += x[u][q];
+      more = goes_on[u];
+    }
+  }
+  put_sum<TW, VE, ACC>(static_cast<TW*>(a.dw) + int64_t(cur) * a.ldw + col, cnt, a.scale, acc);
+}
+
+int pow2_at_least(int64_t x, int cap) {
+  int p = 1;
+  while (p < cap && p < x) p <<= 1;
+  return p;
+}
+
+// Positions per chunk: about 1024 chunks, at least 8 positions (the rows one lane has in
+// flight) and at most 512 (so that the partial sums of one chunk border stay a small share of
+// the rows read).
+int64_t chunk_len(int64_t n) { return pow2_at_least(std::max<int64_t>(8, (n + 1023) / 1024), 512); }
+
+size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
+
+struct EmbedWs {
+  int32_t *tok[2], *pos[2];
+  float* part;
+  size_t bytes;
+};
+EmbedWs carve(void* base, int64_t n, int64_t h) {
+  char* b = static_cast<char*>(base);
+  EmbedWs w{};
+  size_t off = 0;
+  auto take = [&](size_t bytes) {
+    char* p = b + off;
+    off += align256(bytes);
+    return p;
+  };
+  const int bufs = n > kRun ? 2 : 1;
+  for (int k = 0; k < bufs; ++k) {
+    w.tok[k] = reinterpret_cast<int32_t*>(take(size_t(n) * 4));
+    w.pos[k] = reinterpret_cast<int32_t*>(take(size_t(n) * 4));
+  }
+  const int64_t len = chunk_len(n), chunks = (n + len - 1) / len;
+  w.part = reinterpret_cast<float*>(take(size_t(chunks) * 2 * size_t(h) * 4));
+  w.bytes = std::max<size_t>(off, 256);
+  return w;
+}
+
+template <class T, class TW, bool ACC>
+hipError_t run_segments(const SegArgs& a, int64_t fill_blocks, hipStream_t s) {
+  hipError_t e;
+  if (a.seg_blocks + fill_blocks > 0) {
+    TimedLaunch t(s, K_EMBED_GRAD);
+    hipLaunchKernelGGL((segment_sums_kernel<T, TW, ACC>),
+                       dim3(unsigned(a.seg_blocks + fill_blocks)), dim3(kThreads), 0, s, a);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+  }
+  if (a.chunks > 1) {
+    TimedLaunch t(s, K_EMBED_JOIN);
+    hipLaunchKernelGGL((join_chunks_kernel<T, TW, ACC>), dim3(unsigned(a.seg_blocks)),
+                       dim3(kThreads), 0, s, a);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
+template <class T, class TW>
+hipError_t run_segments_acc(const SegArgs& a, bool acc, int64_t fill_blocks, hipStream_t s) {
+  return acc ? run_segments<T, TW, true>(a, 0, s) : run_segments<T, TW, false>(a, fill_blocks, s);
+}
+
+template <class T>
+hipError_t run_lookup(const EmbedFwdArgs& a, hipStream_t s) {
+  constexpr int VE = Elem<T>::kVec;
+  const int64_t vecs = (a.h + VE - 1) / VE;
+  const int tpr = pow2_at_least((vecs + kLookupVecs - 1) / kLookupVecs, kThreads);
+  const int64_t colblocks = (vecs + int64_t(tpr) * kLookupVecs - 1) / (int64_t(tpr) * kLookupVecs);
+  const int64_t rpw = kThreads / tpr, blocks = (a.n + rpw - 1) / rpw * colblocks;
+  TimedLaunch t(s, K_EMBED_FWD);
+  hipLaunchKernelGGL((embed_fwd_kernel<T>), dim3(unsigned(blocks)), dim3(kThreads), 0, s,
+                     static_cast<const T*>(a.weight), a.v, a.h, a.ldw, a.tokens, a.n,
+                     a.ignore_index, a.scale, static_cast<T*>(a.out), a.ldo, tpr, colblocks);
+  return hipGetLastError();
+}
+
+hipError_t token_status(const int32_t* tokens, int64_t n, int64_t v, int32_t ignore_index,
+                        int32_t* status, hipStream_t s) {
+  if (!status) return hipSuccess;
+  TimedLaunch t(s, K_LABEL_PREP);
+  hipLaunchKernelGGL(token_status_kernel, dim3(1), dim3(1024), 0, s, tokens, n, v, ignore_index,
+                     status);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t embed_fwd_run(const EmbedFwdArgs& a, hipStream_t s) {
+  hipError_t e = token_status(a.tokens, a.n, a.v, a.ignore_index, a.status_out, s);
+  if (e != hipSuccess || a.n == 0) return e;
+  switch (a.dtype) {
+    case kBF16: return run_lookup<Bf16>(a, s);
+    case kF16: return run_lookup<_Float16>(a, s);
+    default: return run_lookup<float>(a, s);
+  }
+}
+
+size_t embed_workspace_bytes(int64_t n, int64_t h) { return carve(nullptr, n, h).bytes; }
+
+hipError_t embed_bwd_run(const EmbedBwdArgs& a, hipStream_t s) {
+  hipError_t e = token_status(a.tokens, a.n, a.v, a.ignore_index, a.status_out, s);
+  if (e != hipSuccess) return e;
+  const EmbedWs ws = carve(a.workspace, a.n, a.h);
+  int cur = 0;
+  if (a.n > 0) {
+    const int64_t runs = (a.n + kRun - 1) / kRun;
+    const int64_t last = a.n - (runs - 1) * kRun;
+    const int64_t blocks = (runs - 1) * (kRun / 64) + (last + 63) / 64;
+    {
+      TimedLaunch t(s, K_EMBED_SORT);
+      if (a.v + 1 <= int64_t(0xffffffffLL) / kRun)
+        hipLaunchKernelGGL((rank_sort_kernel<uint32_t>), dim3(unsigned(blocks)),
+                           dim3(64 * kRankWaves), 0, s, a.tokens, a.n, a.v, a.ignore_index,
+                           ws.tok[0], ws.pos[0]);
+      else
+        hipLaunchKernelGGL((rank_sort_kernel<uint64_t>), dim3(unsigned(blocks)),
+                           dim3(64 * kRankWaves), 0, s, a.tokens, a.n, a.v, a.ignore_index,
+                           ws.tok[0], ws.pos[0]);
+      if ((e = hipGetLastError()) != hipSuccess) return e;
+    }
+    for (int64_t len = kRun; len < a.n; len *= kMergeWays) {
+      TimedLaunch t(s, K_EMBED_SORT);
+      hipLaunchKernelGGL(merge_runs_kernel, dim3(unsigned((a.n + kThreads - 1) / kThreads)),
+                         dim3(kThreads), 0, s, ws.tok[cur], ws.pos[cur], ws.tok[cur ^ 1],
+                         ws.pos[cur ^ 1], a.n, len);
+      if ((e = hipGetLastError()) != hipSuccess) return e;
+      cur ^= 1;
+    }
+  }
+  SegArgs g{};
+  g.grad = a.grad;
+  g.ldg = a.ldg;
+  g.stok = ws.tok[cur];
+  g.spos = ws.pos[cur];
+  g.n = a.n;
+  g.h = a.h;
+  g.v = a.v;
+  g.scale = a.scale;
+  g.dw = a.grad_weight;
+  g.ldw = a.ldw;
+  g.part = ws.part;
+  g.len = chunk_len(a.n);
+  g.chunks = (a.n + g.len - 1) / g.len;
+  const int ve = a.dtype == kF32 ? 4 : 8;
+  const int64_t vecs = (a.h + ve - 1) / ve;
+  g.tpr = pow2_at_least(vecs, kThreads);
+  g.colblocks = (vecs + g.tpr - 1) / g.tpr;
+  const int64_t per = kThreads / g.tpr;
+  g.seg_blocks = (g.chunks * g.colblocks + per - 1) / per;
+  const bool acc = (a.flags & EMBED_ACCUMULATE) != 0;
+  const int64_t fill = acc ? 0 : (a.v + kFillRows - 1) / kFillRows;
+  const bool wide = a.grad_dtype == kF32;
+  switch (a.dtype) {
+    case kBF16:
+      return wide ? run_segments_acc<Bf16, float>(g, acc, fill, s)
+                  : run_segments_acc<Bf16, Bf16>(g, acc, fill, s);
+    case kF16:
+      return wide ? run_segments_acc<_Float16, float>(g, acc, fill, s)
+                  : run_segments_acc<_Float16, _Float16>(g, acc, fill, s);
+    default: return run_segments_acc<float, float>(g, acc, fill, s);
+  }
+}
+
+}  // namespace lce

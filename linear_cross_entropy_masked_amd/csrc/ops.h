@@ -1,0 +1,81 @@
+// Internal interface of the embedding (embed_kernels.hip) and layer norm (norm_kernels.hip)
+// operators, between their C-ABI entry points and their launch code.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "lce_masked.h"
+
+namespace lce {
+
+struct EmbedFwdArgs {
+  const void* weight;
+  int dtype;
+  int64_t v, h, ldw;
+  const int32_t* tokens;
+  int64_t n;
+  int32_t ignore_index;
+  float scale;
+  void* out;
+  int64_t ldo;
+  int32_t* status_out;
+};
+hipError_t embed_fwd_run(const EmbedFwdArgs& a, hipStream_t s);
+
+struct EmbedBwdArgs {
+  const void* grad;
+  int dtype;
+  int64_t ldg;
+  const int32_t* tokens;
+  int64_t n, h, v;
+  int32_t ignore_index;
+  float scale;
+  uint32_t flags;
+  void* grad_weight;
+  int grad_dtype;
+  int64_t ldw;
+  int32_t* status_out;
+  void* workspace;
+};
+size_t embed_workspace_bytes(int64_t n, int64_t h);
+hipError_t embed_bwd_run(const EmbedBwdArgs& a, hipStream_t s);
+
+struct NormFwdArgs {
+  const void* x;
+  int dtype;
+  int64_t n, h, ldx;
+  const void* weight;
+  const void* bias;
+  int param_dtype;
+  float eps;
+  void* y;
+  int64_t ldy;
+  float* mean_out;
+  float* rstd_out;
+};
+hipError_t layernorm_fwd_run(const NormFwdArgs& a, hipStream_t s);
+
+struct NormBwdArgs {
+  const void* grad;
+  int dtype;
+  int64_t ldg;
+  const void* x;
+  int64_t ldx;
+  const float* mean;
+  const float* rstd;
+  const void* weight;
+  int param_dtype;
+  int64_t n, h;
+  uint32_t flags;
+  void* grad_x;
+  int64_t lddx;
+  void* grad_weight;
+  void* grad_bias;
+  int grad_param_dtype;
+  void* workspace;
+};
+size_t layernorm_workspace_bytes(int64_t n, int64_t h);
+hipError_t layernorm_bwd_run(const NormBwdArgs& a, hipStream_t s);
+
+}  // namespace lce

@@ -41,6 +41,9 @@ const char* kNames[K_COUNT] = {
     "flce_gemm_grad_weight", "flce_onehot_fix",    "fill_zero",
     "flce_grad_hidden_reduce", "flce_gemm_probs", "flce_label_sort",
     "ce_fused_rows",      "flce_loss_acc",         "flce_probs_transposed",
+    "embed_fwd",          "embed_sort",            "embed_grad",
+    "embed_join",         "layernorm_fwd",         "layernorm_bwd",
+    "layernorm_param_reduce",
 };
 
 }  // namespace

@@ -1,0 +1,128 @@
+"""CPU checks of the embedding and layer norm entry points: bad arguments are refused with the
+documented status codes before anything touches a GPU (fake device addresses, as in
+test_boundary.py), and the binding's own refusals."""
+import ctypes
+import os
+
+import pytest
+import torch
+
+import linear_cross_entropy_masked_amd as lce
+
+OK, NULL_ARG, BAD_SHAPE, _, WORKSPACE, HIP, DEVICE, BAD_FLAGS, ALIGN, OVERLAP = range(10)
+BAD_DTYPE = 11
+A = [0x10000000 * (k + 1) for k in range(12)]  # distinct 256-aligned fake buffers
+AT_DEVICE_CHECK = (HIP, DEVICE)
+BIG = 1 << 30
+
+
+def no_gpu():
+    return torch.cuda.device_count() == 0
+
+
+@pytest.fixture(scope="module")
+def lib():
+    if not os.path.exists(lce.library_path()):
+        pytest.skip("library not built")
+    return lce.load_library()
+
+
+def caller(f, base):
+    def call(**kw):
+        assert set(kw) <= set(base)
+        return f(*dict(base, **kw).values())
+    return call
+
+
+def test_status_string_of_the_new_code(lib):
+    assert "type" in lce.lce_status_str(BAD_DTYPE)
+
+
+def test_embed_fwd_refusals(lib):
+    call = caller(lib.embed_fwd, dict(w=A[0], dtype=0, v=10, h=16, ldw=16, tok=A[1], n=4, ign=-100,
+                                      scale=1.0, out=A[2], ldo=16, status=None, stream=None))
+    assert call(n=-1) == BAD_SHAPE and call(v=0) == BAD_SHAPE and call(h=0) == BAD_SHAPE
+    assert call(ldw=15) == BAD_SHAPE and call(ldo=15) == BAD_SHAPE
+    assert call(v=1 << 31) == BAD_SHAPE and call(n=1 << 31) == BAD_SHAPE
+    assert call(n=(1 << 31) - 1, h=1 << 20, ldw=1 << 20, ldo=1 << 20) == BAD_SHAPE
+    assert call(ldw=1 << 62) == BAD_SHAPE
+    assert call(dtype=3) == BAD_DTYPE and call(dtype=-1) == BAD_DTYPE
+    assert call(w=None) == NULL_ARG and call(tok=None) == NULL_ARG and call(out=None) == NULL_ARG
+    assert call(w=A[0] + 1) == ALIGN and call(out=A[2] + 2, dtype=2) == ALIGN
+    assert call(tok=A[1] + 2) == ALIGN and call(status=A[3] + 1) == ALIGN
+    assert call(out=A[0] + 32) == OVERLAP and call(out=A[1]) == OVERLAP
+    assert call(status=A[2] + 4) == OVERLAP
+    if no_gpu():
+        assert call() in AT_DEVICE_CHECK
+        assert call(n=0, tok=None, out=None) in AT_DEVICE_CHECK
+        assert call(w=A[0] + 2, out=A[2] + 6, ldw=17, ldo=31) in AT_DEVICE_CHECK
+
+
+def test_embed_bwd_refusals(lib):
+    out = ctypes.c_size_t()
+    assert lib.embed_workspace_size(4, 16, 10, None) == NULL_ARG
+    assert lib.embed_workspace_size(-1, 16, 10, ctypes.byref(out)) == BAD_SHAPE
+    assert lib.embed_workspace_size(4, 16, 10, ctypes.byref(out)) == OK and out.value >= 32
+    call = caller(lib.embed_bwd, dict(g=A[0], dtype=0, ldg=16, tok=A[1], n=4, h=16, v=10, ign=-100,
+                                      scale=1.0, flags=0, gw=A[2], gdtype=2, ldw=16, status=None,
+                                      ws=A[3], wsb=BIG, stream=None))
+    assert call(flags=2) == BAD_FLAGS
+    assert call(h=0) == BAD_SHAPE and call(ldg=8) == BAD_SHAPE and call(ldw=8) == BAD_SHAPE
+    assert call(h=(1 << 20) + 1, ldg=1 << 21, ldw=1 << 21) == BAD_SHAPE
+    assert call(dtype=2, gdtype=0) == BAD_DTYPE and call(gdtype=1) == BAD_DTYPE
+    assert call(dtype=7) == BAD_DTYPE
+    assert call(g=None) == NULL_ARG and call(gw=None) == NULL_ARG and call(tok=None) == NULL_ARG
+    assert call(ws=None) == WORKSPACE and call(wsb=out.value - 1) == WORKSPACE
+    assert call(ws=A[3] + 64) == ALIGN and call(gw=A[2] + 2) == ALIGN
+    assert call(gw=A[0]) == OVERLAP and call(ws=A[2]) == OVERLAP and call(status=A[3]) == OVERLAP
+    if no_gpu():
+        assert call(wsb=out.value, flags=1) in AT_DEVICE_CHECK
+        assert call(n=0, g=None, tok=None) in AT_DEVICE_CHECK
+
+
+def test_layernorm_refusals(lib):
+    call = caller(lib.layernorm_fwd, dict(x=A[0], dtype=0, n=4, h=16, ldx=16, w=A[1], b=A[2],
+                                          pd=0, eps=1e-5, y=A[3], ldy=16, mean=A[4], rstd=A[5],
+                                          stream=None))
+    assert call(n=-1) == BAD_SHAPE and call(h=0) == BAD_SHAPE and call(ldx=15) == BAD_SHAPE
+    assert call(ldy=3) == BAD_SHAPE and call(eps=-1.0) == BAD_SHAPE
+    assert call(eps=float("nan")) == BAD_SHAPE
+    assert call(h=lce.LAYERNORM_MAX_H + 1, ldx=BIG, ldy=BIG) == BAD_SHAPE
+    assert call(dtype=5) == BAD_DTYPE and call(pd=1) == BAD_DTYPE and call(dtype=2) == BAD_DTYPE
+    assert call(x=None) == NULL_ARG and call(y=None) == NULL_ARG
+    assert call(x=A[0] + 1) == ALIGN and call(mean=A[4] + 2) == ALIGN
+    assert call(y=A[0] + 2) == OVERLAP and call(y=A[0], ldx=18) == OVERLAP
+    assert call(mean=A[3]) == OVERLAP and call(rstd=A[4] + 4) == OVERLAP
+    if no_gpu():
+        assert call() in AT_DEVICE_CHECK and call(y=A[0]) in AT_DEVICE_CHECK
+        assert call(w=None, b=None, mean=None, rstd=None, pd=2) in AT_DEVICE_CHECK
+    out = ctypes.c_size_t()
+    assert lib.layernorm_workspace_size(4, 16, None) == NULL_ARG
+    assert lib.layernorm_workspace_size(4, 0, ctypes.byref(out)) == BAD_SHAPE
+    assert lib.layernorm_workspace_size(4, 16, ctypes.byref(out)) == OK
+    call = caller(lib.layernorm_bwd, dict(g=A[0], dtype=0, ldg=16, x=A[1], ldx=16, mean=A[2],
+                                          rstd=A[3], w=A[4], pd=0, n=4, h=16, flags=0, gx=A[5],
+                                          lddx=16, gw=A[6], gb=A[7], gd=2, ws=A[8], wsb=BIG,
+                                          stream=None))
+    assert call(flags=4) == BAD_FLAGS and call(lddx=15) == BAD_SHAPE and call(h=0) == BAD_SHAPE
+    assert call(gd=1) == BAD_DTYPE and call(pd=2, gd=0) == BAD_DTYPE
+    assert call(mean=None) == NULL_ARG and call(x=None) == NULL_ARG and call(g=None) == NULL_ARG
+    assert call(ws=None) == WORKSPACE and call(wsb=out.value - 1) == WORKSPACE
+    assert call(gw=A[6] + 2) == ALIGN and call(ws=A[8] + 4) == ALIGN
+    assert call(gx=A[1]) == OVERLAP and call(gw=A[7]) == OVERLAP and call(gx=A[0], ldg=20) == OVERLAP
+    if no_gpu():
+        assert call(gx=A[0]) in AT_DEVICE_CHECK
+        assert call(gx=None, gw=None, gb=None, ws=None, lddx=0) in AT_DEVICE_CHECK
+
+
+def test_binding_refuses_host_tensors_and_wrong_types():
+    with pytest.raises(ValueError, match="HIP device"):
+        lce.embed_fwd(torch.zeros(3, 4), torch.zeros(2, dtype=torch.int32))
+    with pytest.raises(TypeError, match="bfloat16"):
+        lce.embed_fwd(torch.zeros(3, 4, dtype=torch.float64), torch.zeros(2, dtype=torch.int32))
+    with pytest.raises(ValueError, match="HIP device"):
+        lce.embed_bwd(torch.zeros(3, 4), torch.zeros(3, dtype=torch.int32), 9)
+    with pytest.raises(ValueError, match="HIP device"):
+        lce.layernorm_fwd(torch.zeros(3, 4))
+    with pytest.raises(TypeError, match="float32"):
+        lce.layernorm_bwd(torch.zeros(3, 4), torch.zeros(3, 4, dtype=torch.int8), None, None)
