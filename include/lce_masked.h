@@ -85,7 +85,7 @@ extern "C" {
 #define LCE_STATUS_BAD_LABEL     1  /* some label was neither ignore_index nor in [0, V)          */
 #define LCE_STATUS_BAD_TOKEN     1  /* the same bit, for the tokens of embed_*                    */
 
-/* element types of the embedding and layer norm calls */
+/* element types of the embedding, layer norm and vocabulary-piece calls */
 #define LCE_DTYPE_BF16           0
 #define LCE_DTYPE_F16            1
 #define LCE_DTYPE_F32            2
@@ -297,6 +297,72 @@ int flce_bwd(const uint16_t* hidden, const uint16_t* weight, const float* bias,
              const float* grad_output, uint16_t* grad_hidden, float* grad_weight,
              float* grad_bias, int32_t* status_out, void* workspace, size_t workspace_bytes,
              void* stream);
+
+/* ------------------------------------------------------------------ in pieces of the vocabulary
+ *
+ * The fused linear CE for a weight that is held, or wanted, in pieces of consecutive vocabulary
+ * rows: several tensors (a base vocabulary and tokens added to it), the shards of a head that is
+ * split over the vocabulary, or slices of one tensor that bound the working memory. Piece k
+ * holds the classes v_start .. v_start + v - 1 of a vocabulary of `vocab`. Per row the pieces
+ * share 12 bytes of state; nothing else of the vocabulary's size is kept between them:
+ *   1. flce_piece_fwd for every piece, in any order, the first with FLCE_PIECE_FIRST;
+ *   2. flce_piece_loss: loss, lse and per-row terms from the state;
+ *   3. flce_piece_bwd for every piece, in any order, from the lse.
+ * A piece's weight gradient is finished by its own call, in bf16 or fp32 (a split by rows, as in
+ * flce_fwd_bwd, has to carry an fp32 [V, H] accumulator from chunk to chunk); what is carried is
+ * the hidden gradient, fp32 [n, h].
+ *
+ * Labels are classes of the whole vocabulary. A row carries a label when label != ignore_index
+ * and 0 <= label < vocab. Rows without one take no part in any product, whatever they hold.
+ * Limits: h a multiple of 8, h <= 2^20, n <= 2^23, 1 <= v, 0 <= v_start, v_start + v <= vocab
+ * < 2^31. A bias of minus infinity masks a class. hidden, weight, bias and the gradients are
+ * contiguous; 16-byte aligned where they are bf16 or the fp32 hidden_acc / grad_weight. */
+
+#define FLCE_PIECE_FIRST         1u /* the first piece: state / hidden_acc are overwritten        */
+#define FLCE_PIECE_LAST          2u /* flce_piece_bwd: the last piece, grad_hidden is written     */
+#define FLCE_PIECE_ACCUMULATE    4u /* flce_piece_bwd: add into grad_weight and grad_bias         */
+
+int flce_piece_fwd_workspace_size(int64_t n, int64_t h, int64_t v, size_t* bytes);
+int flce_piece_loss_workspace_size(int64_t n, size_t* bytes);
+/* The bf16 [n, v] logit gradients of the piece are most of it. */
+int flce_piece_bwd_workspace_size(int64_t n, int64_t h, int64_t v, size_t* bytes);
+
+/* Takes one piece into the state: fp32 [3, n] holding per row the largest logit so far, the sum
+ * of exp(z - that), and the label's logit (0 until its piece has come). Rows without a label hold
+ * (-inf, 0, 0). flags: FLCE_PIECE_FIRST. Up to 64 rows take a kernel of their own, bound by
+ * reading the weight once. States over disjoint pieces of one vocabulary, as the ranks of a split
+ * head hold them, combine to (m, s, z) = (max of m, sum of s * exp(m_k - m), sum of z). */
+int flce_piece_fwd(const uint16_t* hidden, const uint16_t* weight, const float* bias,
+                   const int32_t* labels, int64_t n, int64_t h, int64_t v, int64_t v_start,
+                   int64_t vocab, int32_t ignore_index, uint32_t flags, float* state,
+                   void* workspace, size_t workspace_bytes, void* stream);
+
+/* loss_out (fp32 scalar or NULL) = the sum of lse_i - z_{i,y_i} over labelled rows, in fp64 in a
+ * fixed order, divided by T (0 when T = 0); lse_out and row_loss_out (fp32 [n] or NULL) receive
+ * lse_i and the terms, 0 for rows without a label. T as in flce_fwd_bwd. */
+int flce_piece_loss(const float* state, const int32_t* labels, int64_t n, int64_t vocab,
+                    int32_t ignore_index, int64_t num_label_tokens, float* loss_out,
+                    float* lse_out, float* row_loss_out, int32_t* status_out, void* workspace,
+                    size_t workspace_bytes, void* stream);
+
+/* Gradients of one piece from the lse over the whole vocabulary:
+ *   grad of the logits  d_iv = c_i * (exp(z_iv - lse_i) - [y_i = v]), rounded to bf16 once;
+ *                       c_i = g / T, or grad_rows[i] (fp32 [n], the upstream gradient of each
+ *                       row's term; grad_output and num_label_tokens are then not used)
+ *   hidden_acc   fp32 [n, h]: += d * weight (FLCE_PIECE_FIRST: =). Needed where grad_hidden is
+ *                wanted from more than one piece, or partial sums are (no FLCE_PIECE_LAST)
+ *   grad_hidden  bf16 [n, h], written with FLCE_PIECE_LAST: hidden_acc plus this piece, rounded
+ *                once; 0 for rows without a label. NULL with FLCE_PIECE_LAST: no hidden gradient
+ *                of this piece is formed
+ *   grad_weight  [v, h] bf16 (LCE_DTYPE_BF16) or fp32 (LCE_DTYPE_F32), or NULL: dT * hidden
+ *   grad_bias    fp32 [v] or NULL (needs bias): column sums of the fp32 d */
+int flce_piece_bwd(const uint16_t* hidden, const uint16_t* weight, const float* bias,
+                   const int32_t* labels, const float* lse, int64_t n, int64_t h, int64_t v,
+                   int64_t v_start, int64_t vocab, int32_t ignore_index,
+                   int64_t num_label_tokens, uint32_t flags, const float* grad_output,
+                   const float* grad_rows, float* hidden_acc, uint16_t* grad_hidden,
+                   void* grad_weight, int grad_weight_dtype, float* grad_bias, void* workspace,
+                   size_t workspace_bytes, void* stream);
 
 /* ------------------------------------------------------------------ embedding */
 

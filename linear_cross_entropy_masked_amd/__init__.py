@@ -8,9 +8,11 @@ function whose library is missing raises.
 
 Entry points (same names as the C ABI):
     ce_chunked_fwd, ce_chunked_bwd, ce_chunked_bwd_inplace, flce_fwd_bwd, flce_fwd, flce_bwd,
-    embed_fwd, embed_bwd, layernorm_fwd, layernorm_bwd,
+    flce_piece_fwd, flce_piece_loss, flce_piece_bwd, embed_fwd, embed_bwd, layernorm_fwd,
+    layernorm_bwd,
     ce_chunked_workspace_size, flce_workspace_size, embed_workspace_size,
-    layernorm_workspace_size, lce_status_str
+    layernorm_workspace_size, flce_piece_{fwd,loss,bwd}_workspace_size, lce_status_str
+and over all pieces of a vocabulary: flce_pieces_fwd, flce_pieces_bwd
 """
 from __future__ import annotations
 
@@ -25,6 +27,10 @@ __all__ = [
     "flce_workspace_size", "flce_fwd_bwd", "flce_fwd", "flce_bwd", "lce_status_str",
     "flce_status_str",
     "FLCE_RECOMPUTE", "FLCE_ACCUMULATE", "LCE_STATUS_BAD_LABEL",
+    "flce_pieces_fwd", "flce_pieces_bwd", "flce_piece_fwd", "flce_piece_loss", "flce_piece_bwd",
+    "flce_piece_fwd_workspace_size", "flce_piece_loss_workspace_size",
+    "flce_piece_bwd_workspace_size", "FLCE_PIECE_FIRST", "FLCE_PIECE_LAST",
+    "FLCE_PIECE_ACCUMULATE",
     "embed_fwd", "embed_workspace_size", "embed_bwd", "EMBED_ACCUMULATE", "LCE_STATUS_BAD_TOKEN",
     "layernorm_fwd", "layernorm_workspace_size", "layernorm_bwd", "LAYERNORM_ACCUMULATE",
     "LAYERNORM_MAX_H",
@@ -35,6 +41,9 @@ FLCE_RECOMPUTE = 1
 FLCE_ACCUMULATE = 2
 LCE_STATUS_BAD_LABEL = 1
 LCE_STATUS_BAD_TOKEN = 1
+FLCE_PIECE_FIRST = 1
+FLCE_PIECE_LAST = 2
+FLCE_PIECE_ACCUMULATE = 4
 EMBED_ACCUMULATE = 1
 LAYERNORM_ACCUMULATE = 1
 LAYERNORM_MAX_H = 32768
@@ -89,6 +98,14 @@ def load_library() -> ctypes.CDLL:
                                     sz, vp]),
         "flce_bwd": (ctypes.c_int, [vp, vp, vp, vp, vp, i64, i64, i64, i32, i64, i64, u32, vp, vp,
                                     vp, vp, vp, vp, sz, vp]),
+        "flce_piece_fwd_workspace_size": (ctypes.c_int, [i64, i64, i64, psz]),
+        "flce_piece_loss_workspace_size": (ctypes.c_int, [i64, psz]),
+        "flce_piece_bwd_workspace_size": (ctypes.c_int, [i64, i64, i64, psz]),
+        "flce_piece_fwd": (ctypes.c_int, [vp, vp, vp, vp, i64, i64, i64, i64, i64, i32, u32, vp, vp,
+                                          sz, vp]),
+        "flce_piece_loss": (ctypes.c_int, [vp, vp, i64, i64, i32, i64, vp, vp, vp, vp, vp, sz, vp]),
+        "flce_piece_bwd": (ctypes.c_int, [vp, vp, vp, vp, vp, i64, i64, i64, i64, i64, i32, i64, u32,
+                                          vp, vp, vp, vp, vp, dt, vp, vp, sz, vp]),
         "embed_fwd": (ctypes.c_int, [vp, dt, i64, i64, i64, vp, i64, i32, f32, vp, i64, vp, vp]),
         "embed_workspace_size": (ctypes.c_int, [i64, i64, i64, psz]),
         "embed_bwd": (ctypes.c_int, [vp, dt, i64, vp, i64, i64, i64, i32, f32, u32, vp, dt, i64, vp,
@@ -739,6 +756,255 @@ def layernorm_bwd(grad, x, mean, rstd, weight=None, *, grad_x=True, grad_weight=
           LAYERNORM_ACCUMULATE if accumulate else 0, _adr(grad_x), lddx, _adr(gw), _adr(gb),
           _dtype_code(gdtype, "grad_weight"), _adr(ws), 0 if ws is None else _bytes_of(ws))
     return grad_x, gw, gb
+
+
+def _size(fn, *args):
+    out = ctypes.c_size_t()
+    _check(fn, getattr(load_library(), fn)(*args, ctypes.byref(out)))
+    return out.value
+
+
+def flce_piece_fwd_workspace_size(n: int, h: int, v: int) -> int:
+    return _size("flce_piece_fwd_workspace_size", n, h, v)
+
+
+def flce_piece_loss_workspace_size(n: int) -> int:
+    return _size("flce_piece_loss_workspace_size", n)
+
+
+def flce_piece_bwd_workspace_size(n: int, h: int, v: int) -> int:
+    return _size("flce_piece_bwd_workspace_size", n, h, v)
+
+
+def _piece_operands(hidden, weight, bias):
+    import torch
+    _require(hidden, "hidden", torch.bfloat16, 2)
+    dev = hidden.device
+    _require(weight, "weight", torch.bfloat16, 2, dev)
+    if weight.shape[1] != hidden.shape[1]:
+        raise ValueError(f"hidden has {hidden.shape[1]} columns but weight has {weight.shape[1]}")
+    if bias is not None:
+        _require(bias, "bias", torch.float32, 1, dev)
+        if bias.shape[0] != weight.shape[0]:
+            raise ValueError("bias must have one entry per row of weight")
+        bias = bias.contiguous()
+    return hidden.contiguous(), weight.contiguous(), bias, dev
+
+
+def _contiguous_f32(t, name, shape, device):
+    import torch
+    _require(t, name, torch.float32, len(shape), device)
+    if tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous float32 tensor of shape {tuple(shape)}")
+    return t
+
+
+def flce_piece_fwd(hidden, weight, labels, state, bias=None, *, v_start: int, vocab: int,
+                   first: bool, ignore_index: int = -100, workspace=None):
+    """Takes the logits over one piece of the vocabulary, the classes v_start ... of ``vocab``,
+    into ``state`` (fp32 [3, n]: maximum, sum of exponentials, label logit per row; overwritten
+    with ``first``). Returns state."""
+    hidden, weight, bias, dev = _piece_operands(hidden, weight, bias)
+    n, h = hidden.shape
+    v = weight.shape[0]
+    labels = _labels_i32(labels, n, dev, ignore_index)
+    _contiguous_f32(state, "state", (3, n), dev)
+    ws = _workspace(flce_piece_fwd_workspace_size(n, h, v), dev, workspace)
+    _call("flce_piece_fwd", dev, hidden.data_ptr(), weight.data_ptr(), _adr(bias),
+          labels.data_ptr(), n, h, v, v_start, vocab, ignore_index,
+          FLCE_PIECE_FIRST if first else 0, state.data_ptr(), ws.data_ptr(), _bytes_of(ws))
+    return state
+
+
+def flce_piece_loss(state, labels, *, vocab: int, ignore_index: int = -100,
+                    num_label_tokens: int | None = None, return_rows: bool = False, status=None,
+                    workspace=None):
+    """(loss, lse, rows) from the state over all pieces: the fp32 scalar divided by
+    num_label_tokens (None: by the number of labelled rows), and fp32 [n] per-row logsumexp and
+    terms (rows is None without ``return_rows``)."""
+    import torch
+    _require(state, "state", torch.float32, 2)
+    dev = state.device
+    n = state.shape[1]
+    _contiguous_f32(state, "state", (3, n), dev)
+    labels = _labels_i32(labels, n, dev, ignore_index)
+    loss = torch.empty((), dtype=torch.float32, device=dev)
+    lse = torch.empty(n, dtype=torch.float32, device=dev)
+    rows = torch.empty(n, dtype=torch.float32, device=dev) if return_rows else None
+    ws = _workspace(flce_piece_loss_workspace_size(n), dev, workspace)
+    _call("flce_piece_loss", dev, state.data_ptr(), labels.data_ptr(), n, vocab, ignore_index,
+          _count_arg(num_label_tokens), loss.data_ptr(), lse.data_ptr(), _adr(rows),
+          _status_ptr(status, dev), ws.data_ptr(), _bytes_of(ws))
+    return loss, lse, rows
+
+
+def flce_piece_bwd(hidden, weight, labels, lse, bias=None, *, v_start: int, vocab: int,
+                   first: bool, last: bool, ignore_index: int = -100,
+                   num_label_tokens: int | None = None, accumulate: bool = False,
+                   grad_output=None, grad_rows=None, hidden_acc=None, grad_hidden=None,
+                   grad_weight=None, grad_bias=None, workspace=None):
+    """Gradients of one piece from the lse over the whole vocabulary, written into the tensors
+    given (None: not computed): ``hidden_acc`` fp32 [n, h], carried from the first piece to the
+    last; ``grad_hidden`` bf16 [n, h], written with ``last``; ``grad_weight`` bf16 or fp32 and
+    ``grad_bias`` fp32, of the piece's size. ``grad_rows`` fp32 [n]: the upstream gradient of
+    each row's term, in place of grad_output / num_label_tokens."""
+    import torch
+    hidden, weight, bias, dev = _piece_operands(hidden, weight, bias)
+    n, h = hidden.shape
+    v = weight.shape[0]
+    labels = _labels_i32(labels, n, dev, ignore_index)
+    _contiguous_f32(lse, "lse", (n,), dev)
+    if grad_output is not None:
+        _require(grad_output, "grad_output", torch.float32, 0, dev)
+    if grad_rows is not None:
+        _contiguous_f32(grad_rows, "grad_rows", (n,), dev)
+    if hidden_acc is not None:
+        _contiguous_f32(hidden_acc, "hidden_acc", (n, h), dev)
+    if grad_hidden is not None:
+        _require(grad_hidden, "grad_hidden", torch.bfloat16, 2, dev)
+        if tuple(grad_hidden.shape) != (n, h) or not grad_hidden.is_contiguous():
+            raise ValueError(f"grad_hidden must be a contiguous {(n, h)} tensor")
+    if grad_weight is not None:
+        _require(grad_weight, "grad_weight", None, 2, dev)
+        if tuple(grad_weight.shape) != (v, h) or not grad_weight.is_contiguous():
+            raise ValueError(f"grad_weight must be a contiguous {(v, h)} tensor")
+    if grad_bias is not None:
+        _contiguous_f32(grad_bias, "grad_bias", (v,), dev)
+    flags = ((FLCE_PIECE_FIRST if first else 0) | (FLCE_PIECE_LAST if last else 0)
+             | (FLCE_PIECE_ACCUMULATE if accumulate else 0))
+    ws = _workspace(flce_piece_bwd_workspace_size(n, h, v), dev, workspace)
+    wcode = 0 if grad_weight is None else _dtype_code(grad_weight.dtype, "grad_weight")
+    _call("flce_piece_bwd", dev, hidden.data_ptr(), weight.data_ptr(), _adr(bias),
+          labels.data_ptr(), lse.data_ptr(), n, h, v, v_start, vocab, ignore_index,
+          _count_arg(num_label_tokens), flags, _adr(grad_output), _adr(grad_rows),
+          _adr(hidden_acc), _adr(grad_hidden), _adr(grad_weight), wcode, _adr(grad_bias),
+          ws.data_ptr(), _bytes_of(ws))
+
+
+def _as_pieces(weight, bias):
+    """([(weight, bias or None), ...], whether a sequence was given)."""
+    many = isinstance(weight, (list, tuple))
+    weights = list(weight) if many else [weight]
+    if not weights:
+        raise ValueError("weight holds no pieces")
+    if bias is None:
+        biases = [None] * len(weights)
+    else:
+        biases = list(bias) if isinstance(bias, (list, tuple)) else [bias]
+        if len(biases) != len(weights):
+            raise ValueError(f"{len(weights)} weight pieces but {len(biases)} biases")
+    return list(zip(weights, biases)), many
+
+
+def flce_pieces_fwd(hidden, weight, labels, bias=None, *, ignore_index: int = -100,
+                    num_label_tokens: int | None = None, return_rows: bool = False, status=None):
+    """Linear CE forward over a weight [v, h] or a sequence of weights that hold consecutive
+    classes (with a sequence of biases, or None). Returns (loss, lse, rows) as
+    :func:`flce_piece_loss`; keep lse for :func:`flce_pieces_bwd`."""
+    import torch
+    pieces, _ = _as_pieces(weight, bias)
+    _require(hidden, "hidden", torch.bfloat16, 2)
+    dev = hidden.device
+    n = hidden.shape[0]
+    labels = _labels_i32(labels, n, dev, ignore_index)
+    vocab = sum(w.shape[0] for w, _ in pieces)
+    state = torch.empty((3, n), dtype=torch.float32, device=dev)
+    start = 0
+    for w, b in pieces:
+        flce_piece_fwd(hidden, w, labels, state, b, v_start=start, vocab=vocab, first=start == 0,
+                       ignore_index=ignore_index)
+        start += w.shape[0]
+    return flce_piece_loss(state, labels, vocab=vocab, ignore_index=ignore_index,
+                           num_label_tokens=num_label_tokens, return_rows=return_rows,
+                           status=status)
+
+
+# Bytes of the bf16 logit gradients that flce_pieces_bwd takes at a time by default.
+_PIECE_BYTES = 512 << 20
+
+
+def _piece_rows(n, v, piece_size):
+    """Classes per piece: ``piece_size``, or as many as keep the logit gradients of a piece
+    within _PIECE_BYTES, in equal parts of whole 256-column tiles."""
+    if piece_size is not None:
+        if piece_size < 1:
+            raise ValueError("piece_size must be at least 1")
+        return piece_size
+    most = max(4096, _PIECE_BYTES // (2 * max(n, 256)))
+    parts = -(-v // most)
+    return -(-v // (256 * parts)) * 256
+
+
+def flce_pieces_bwd(hidden, weight, labels, lse, bias=None, *, piece_size: int | None = None,
+                    ignore_index: int = -100, num_label_tokens: int | None = None,
+                    accumulate: bool = False, grad_output=None, grad_rows=None, grad_hidden=True,
+                    grad_weight=True, grad_bias=None):
+    """Gradients of :func:`flce_pieces_fwd` from its lse. Each weight is taken ``piece_size``
+    classes at a time (default: so that a piece's bf16 logit gradients stay within 512 MiB).
+    ``grad_rows`` fp32 [n]: the upstream gradient of each row's term, for per-row losses.
+
+    ``grad_hidden`` / ``grad_weight`` / ``grad_bias``: True to allocate, False to skip, or what to
+    write into; grad_weight (bf16, or fp32 where given so) and grad_bias are sequences where
+    weight is one, and are added to with ``accumulate``. grad_bias defaults to True when a bias
+    is given. Returns (grad_hidden, grad_weight, grad_bias)."""
+    import torch
+    pieces, many = _as_pieces(weight, bias)
+    _require(hidden, "hidden", torch.bfloat16, 2)
+    hidden = hidden.contiguous()
+    dev = hidden.device
+    n, h = hidden.shape
+    labels = _labels_i32(labels, n, dev, ignore_index)
+    if grad_bias is None:
+        grad_bias = bias is not None
+
+    def outs(spec, name, shapes, dtype):
+        if spec is True:
+            if accumulate:
+                raise ValueError(f"accumulate=True needs an existing {name}")
+            return [torch.empty(s, dtype=dtype, device=dev) for s in shapes]
+        if spec is False or spec is None:
+            return [None] * len(shapes)
+        spec = list(spec) if many else [spec]
+        if len(spec) != len(shapes):
+            raise ValueError(f"{len(shapes)} weight pieces but {len(spec)} of {name}")
+        return spec
+
+    if grad_bias is not False and bias is None:
+        raise ValueError("grad_bias needs a bias")
+    gws = outs(grad_weight, "grad_weight", [tuple(w.shape) for w, _ in pieces], torch.bfloat16)
+    gbs = outs(grad_bias, "grad_bias", [(w.shape[0],) for w, _ in pieces], torch.float32)
+    gh = grad_hidden
+    if gh is True:
+        gh = torch.empty((n, h), dtype=torch.bfloat16, device=dev)
+    elif gh is False:
+        gh = None
+    vocab = sum(w.shape[0] for w, _ in pieces)
+    jobs = []  # (weight, bias, grad_weight, grad_bias, first class)
+    start = 0
+    for (w, b), gw, gb in zip(pieces, gws, gbs):
+        v = w.shape[0]
+        for t, name in ((gw, "grad_weight"), (gb, "grad_bias")):
+            if t is not None and (t.shape[:1] != w.shape[:1] or not t.is_contiguous()):
+                raise ValueError(f"{name} must be contiguous and of its weight's size")
+        step = _piece_rows(n, v, piece_size)
+        w = w.contiguous()
+        for lo in range(0, v, step):
+            part = slice(lo, min(v, lo + step))
+            jobs.append((w[part], *(None if t is None else t[part] for t in (b, gw, gb)),
+                         start + lo))
+        start += v
+    acc = None
+    if gh is not None and len(jobs) > 1:
+        acc = torch.empty((n, h), dtype=torch.float32, device=dev)
+    need = max((flce_piece_bwd_workspace_size(n, h, w.shape[0]) for w, *_ in jobs), default=0)
+    ws = _workspace(need, dev)
+    for k, (w, b, gw, gb, at) in enumerate(jobs):
+        flce_piece_bwd(hidden, w, labels, lse, b, v_start=at, vocab=vocab, first=k == 0,
+                       last=k == len(jobs) - 1, ignore_index=ignore_index,
+                       num_label_tokens=num_label_tokens, accumulate=accumulate,
+                       grad_output=grad_output, grad_rows=grad_rows, hidden_acc=acc,
+                       grad_hidden=gh, grad_weight=gw, grad_bias=gb, workspace=ws)
+    return gh, gws if many else gws[0], gbs if many else gbs[0]
 
 
 def lce_timing_enable(on: bool = True) -> None:

@@ -24,7 +24,7 @@ LIB_PATH = os.path.join(PKG, LIB_NAME)
 ARCH = "gfx950"
 
 SOURCES = ["capi.hip", "capi_ops.hip", "ce_kernels.hip", "embed_kernels.hip",
-           "flce_kernels.hip", "norm_kernels.hip", "timing.hip"]
+           "flce_kernels.hip", "flce_pieces.hip", "norm_kernels.hip", "timing.hip"]
 
 HIPCC_FLAGS = [
     f"--offload-arch={ARCH}",

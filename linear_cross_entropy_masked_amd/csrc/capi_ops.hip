@@ -1,9 +1,11 @@
-// extern "C" entry points of the embedding and layer norm operators: argument validation, all of
-// it before any HIP call, then the launch code in embed_kernels.hip / norm_kernels.hip.
+// extern "C" entry points of the embedding, layer norm and vocabulary-piece operators: argument
+// validation, all of it before any HIP call, then the launch code in embed_kernels.hip,
+// norm_kernels.hip and flce_pieces.hip.
 #include <limits>
 
 #include "capi_checks.h"
 #include "common.h"
+#include "flce_pieces.h"
 #include "lce_masked.h"
 #include "ops.h"
 
@@ -31,6 +33,19 @@ int embed_check_shape(int64_t n, int64_t h, int64_t v) {
 
 int norm_check_shape(int64_t n, int64_t h) {
   return n < 0 || n > kI32Max || h < 1 || h > LAYERNORM_MAX_H ? LCE_ERR_BAD_SHAPE : LCE_OK;
+}
+
+// The row limit keeps every byte offset inside one K slice of a 64-column panel below 2^32.
+int piece_check_shape(int64_t n, int64_t h, int64_t v) {
+  if (n < 0 || n > (int64_t(1) << 23) || h < 1 || h % 8 != 0 || h > (int64_t(1) << 20) || v < 1 ||
+      v > kI32Max)
+    return LCE_ERR_BAD_SHAPE;
+  return LCE_OK;
+}
+int piece_check_vocab(int64_t v, int64_t v_start, int64_t vocab) {
+  return vocab < 1 || vocab > kI32Max || v_start < 0 || v > vocab || v_start > vocab - v
+             ? LCE_ERR_BAD_SHAPE
+             : LCE_OK;
 }
 
 }  // namespace
@@ -172,6 +187,124 @@ int layernorm_bwd(const void* grad, int dtype, int64_t ldg, const void* x, int64
   const NormBwdArgs a{grad, dtype, ldg, x, ldx, mean, rstd, weight, param_dtype, n, h, flags,
                       grad_x, lddx, grad_weight, grad_bias, grad_param_dtype, workspace};
   LCE_TRY_HIP(layernorm_bwd_run(a, static_cast<hipStream_t>(stream)));
+  return LCE_OK;
+}
+
+int flce_piece_fwd_workspace_size(int64_t n, int64_t h, int64_t v, size_t* bytes) {
+  if (!bytes) return LCE_ERR_NULL_ARG;
+  const int rc = piece_check_shape(n, h, v);
+  if (rc != LCE_OK) return rc;
+  *bytes = piece_fwd_workspace_bytes(n, h, v);
+  return LCE_OK;
+}
+
+int flce_piece_loss_workspace_size(int64_t n, size_t* bytes) {
+  if (!bytes) return LCE_ERR_NULL_ARG;
+  const int rc = piece_check_shape(n, 8, 1);
+  if (rc != LCE_OK) return rc;
+  *bytes = piece_loss_workspace_bytes(n);
+  return LCE_OK;
+}
+
+int flce_piece_bwd_workspace_size(int64_t n, int64_t h, int64_t v, size_t* bytes) {
+  if (!bytes) return LCE_ERR_NULL_ARG;
+  const int rc = piece_check_shape(n, h, v);
+  if (rc != LCE_OK) return rc;
+  *bytes = piece_bwd_workspace_bytes(n, h, v);
+  return LCE_OK;
+}
+
+int flce_piece_fwd(const uint16_t* hidden, const uint16_t* weight, const float* bias,
+                   const int32_t* labels, int64_t n, int64_t h, int64_t v, int64_t v_start,
+                   int64_t vocab, int32_t ignore_index, uint32_t flags, float* state,
+                   void* workspace, size_t workspace_bytes, void* stream) {
+  if (flags & ~FLCE_PIECE_FIRST) return LCE_ERR_BAD_FLAGS;
+  int rc = piece_check_shape(n, h, v);
+  if (rc != LCE_OK || (rc = piece_check_vocab(v, v_start, vocab)) != LCE_OK) return rc;
+  if (!weight || (n > 0 && (!hidden || !labels || !state))) return LCE_ERR_NULL_ARG;
+  const size_t need = piece_fwd_workspace_bytes(n, h, v);
+  if (!workspace || workspace_bytes < need) return LCE_ERR_WORKSPACE;
+  if (!aligned(hidden, 16) || !aligned(weight, 16) || !aligned(bias, 4) || !aligned(labels, 4) ||
+      !aligned(state, 4) || !aligned(workspace, 256))
+    return LCE_ERR_ALIGNMENT;
+  {
+    const Span wr[] = {span(workspace, int64_t(need)), span(state, 12 * n)};
+    const Span rd[] = {span(hidden, 2 * n * h), span(weight, 2 * v * h), span(bias, 4 * v),
+                       span(labels, 4 * n)};
+    if ((rc = check_disjoint(wr, rd)) != LCE_OK) return rc;
+  }
+  if ((rc = check_device()) != LCE_OK) return rc;
+  const PieceFwdArgs a{hidden, weight, bias, labels, n, h, v, v_start, vocab, ignore_index, flags,
+                       state, workspace};
+  LCE_TRY_HIP(piece_fwd_run(a, static_cast<hipStream_t>(stream)));
+  return LCE_OK;
+}
+
+int flce_piece_loss(const float* state, const int32_t* labels, int64_t n, int64_t vocab,
+                    int32_t ignore_index, int64_t num_label_tokens, float* loss_out,
+                    float* lse_out, float* row_loss_out, int32_t* status_out, void* workspace,
+                    size_t workspace_bytes, void* stream) {
+  int rc = piece_check_shape(n, 8, 1);
+  if (rc != LCE_OK || (rc = piece_check_vocab(1, 0, vocab)) != LCE_OK) return rc;
+  if (n > 0 && (!state || !labels)) return LCE_ERR_NULL_ARG;
+  const size_t need = piece_loss_workspace_bytes(n);
+  if (!workspace || workspace_bytes < need) return LCE_ERR_WORKSPACE;
+  if (!aligned(state, 4) || !aligned(labels, 4) || !aligned(loss_out, 4) || !aligned(lse_out, 4) ||
+      !aligned(row_loss_out, 4) || !aligned(status_out, 4) || !aligned(workspace, 256))
+    return LCE_ERR_ALIGNMENT;
+  {
+    const Span wr[] = {span(workspace, int64_t(need)), span(loss_out, 4), span(lse_out, 4 * n),
+                       span(row_loss_out, 4 * n), span(status_out, 4)};
+    const Span rd[] = {span(state, 12 * n), span(labels, 4 * n)};
+    if ((rc = check_disjoint(wr, rd)) != LCE_OK) return rc;
+  }
+  if ((rc = check_device()) != LCE_OK) return rc;
+  const PieceLossArgs a{state, labels, n, vocab, ignore_index, num_label_tokens, loss_out,
+                        lse_out, row_loss_out, status_out, workspace};
+  LCE_TRY_HIP(piece_loss_run(a, static_cast<hipStream_t>(stream)));
+  return LCE_OK;
+}
+
+int flce_piece_bwd(const uint16_t* hidden, const uint16_t* weight, const float* bias,
+                   const int32_t* labels, const float* lse, int64_t n, int64_t h, int64_t v,
+                   int64_t v_start, int64_t vocab, int32_t ignore_index,
+                   int64_t num_label_tokens, uint32_t flags, const float* grad_output,
+                   const float* grad_rows, float* hidden_acc, uint16_t* grad_hidden,
+                   void* grad_weight, int grad_weight_dtype, float* grad_bias, void* workspace,
+                   size_t workspace_bytes, void* stream) {
+  if (flags & ~(FLCE_PIECE_FIRST | FLCE_PIECE_LAST | FLCE_PIECE_ACCUMULATE))
+    return LCE_ERR_BAD_FLAGS;
+  int rc = piece_check_shape(n, h, v);
+  if (rc != LCE_OK || (rc = piece_check_vocab(v, v_start, vocab)) != LCE_OK) return rc;
+  if (grad_weight && grad_weight_dtype != LCE_DTYPE_BF16 && grad_weight_dtype != LCE_DTYPE_F32)
+    return LCE_ERR_BAD_DTYPE;
+  const bool first = flags & FLCE_PIECE_FIRST, last = flags & FLCE_PIECE_LAST;
+  if (!weight || (n > 0 && (!hidden || !labels || !lse)) || (grad_bias && !bias) ||
+      (last && !first && grad_hidden && !hidden_acc))
+    return LCE_ERR_NULL_ARG;
+  const size_t need = piece_bwd_workspace_bytes(n, h, v);
+  if (!workspace || workspace_bytes < need) return LCE_ERR_WORKSPACE;
+  if (!aligned(hidden, 16) || !aligned(weight, 16) || !aligned(bias, 4) || !aligned(labels, 4) ||
+      !aligned(lse, 4) || !aligned(grad_output, 4) || !aligned(grad_rows, 4) ||
+      !aligned(hidden_acc, 16) || !aligned(grad_hidden, 16) || !aligned(grad_weight, 16) ||
+      !aligned(grad_bias, 4) || !aligned(workspace, 256))
+    return LCE_ERR_ALIGNMENT;
+  {
+    const int64_t wl = grad_weight_dtype == LCE_DTYPE_F32 ? 4 : 2;
+    const Span wr[] = {span(workspace, int64_t(need)), span(hidden_acc, 4 * n * h),
+                       span(grad_hidden, 2 * n * h), span(grad_weight, wl * v * h),
+                       span(grad_bias, 4 * v)};
+    const Span rd[] = {span(hidden, 2 * n * h), span(weight, 2 * v * h), span(bias, 4 * v),
+                       span(labels, 4 * n), span(lse, 4 * n), span(grad_output, 4),
+                       span(grad_rows, 4 * n)};
+    if ((rc = check_disjoint(wr, rd)) != LCE_OK) return rc;
+  }
+  if ((rc = check_device()) != LCE_OK) return rc;
+  const PieceBwdArgs a{hidden, weight, bias, labels, lse, n, h, v, v_start, vocab, ignore_index,
+                       num_label_tokens >= 0 ? num_label_tokens : -1, flags, grad_output,
+                       grad_rows, hidden_acc, grad_hidden, grad_weight, grad_weight_dtype,
+                       grad_bias, workspace};
+  LCE_TRY_HIP(piece_bwd_run(a, static_cast<hipStream_t>(stream)));
   return LCE_OK;
 }
 

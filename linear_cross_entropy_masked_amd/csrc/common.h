@@ -118,6 +118,13 @@ enum KernelId {
   K_NORM_FWD,
   K_NORM_BWD,
   K_NORM_PARAM_REDUCE,
+  K_PIECE_GATHER,
+  K_PIECE_LOGITS,
+  K_PIECE_STATE,
+  K_PIECE_GRAD_LOGITS,
+  K_PIECE_GRAD_HIDDEN,
+  K_PIECE_GRAD_WEIGHT,
+  K_PIECE_GRAD_BIAS,
   K_COUNT
 };
 

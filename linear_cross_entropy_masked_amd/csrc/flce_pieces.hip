@@ -1,0 +1,933 @@
+// Linear cross entropy taken in pieces of the vocabulary, for gfx950.
+//
+// z = hidden · Wᵀ + b over a piece W of consecutive vocabulary rows; per row the state
+// (max, Σ exp(z − max), label logit) is carried from piece to piece, so neither the logits nor
+// anything else of the vocabulary's size is kept. The backward takes each piece by itself:
+//   D = c_i · (exp(z − lse) − [v = y])      logits recomputed, bf16, the piece's only big buffer
+//   dH (+)= s · D · W                       fp32 over the pieces, bf16 after the last
+//   dW  =   s · Dᵀ · hidden                 finished: a piece sees every row
+//   db  =   s · Σ_i D                       from the fp32 values
+// with s = g / T and c_i = 1 (summed loss) or s = 1 and c_i the row's own upstream gradient.
+// Four products of 2 · N · H · V flop in all, on the MFMA tile of gemm_tile.h.
+//
+// Rows without a label are left out of every product: piece_rows_kernel numbers the labelled
+// rows, gather_rows_kernel copies their hidden rows together, and the products stop at the
+// count it leaves in device memory. That also keeps whatever such rows hold (NaN in a padded
+// position) out of dW. The copy costs 4 · N · H bytes against 2 · N · H · V flop.
+//
+// D is rounded to bf16 (an MFMA operand) once, unscaled where the loss is summed, so that the
+// rounding is independent from element to element: a common factor would be rounded the same
+// way in every label element. Half a bf16 step per element, as the outputs' own rounding.
+//
+// With at most kScoreRows rows the forward is bound by reading W once, and score_kernel streams
+// it past the rows instead.
+#include <algorithm>
+
+#include "common.h"
+#include "flce_pieces.h"
+#include "gemm_tile.h"
+#include "lce_masked.h"
+
+namespace lce {
+
+namespace {
+
+using gemm::View;
+using gemm::f32x4_t;
+using Wide = gemm::v2::CfgWide;
+
+__host__ __device__ inline int64_t up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
+
+constexpr int kTile = Wide::BM;  // rows of an output tile; the gathered rows are padded to it
+constexpr int kScoreRows = 64;
+
+__device__ __forceinline__ bool labelled(int32_t y, int64_t vocab, int32_t ignore_index) {
+  return y != ignore_index && y >= 0 && int64_t(y) < vocab;
+}
+
+// s = g / T; 0 when T = 0. With per-row upstream gradients s = 1.
+__device__ __forceinline__ float loss_scale(const int32_t* count, long long t_host,
+                                            const float* gout, bool rows) {
+  if (rows) return 1.f;
+  const long long t = t_host >= 0 ? t_host : *count;
+  return t > 0 ? float(double(gout ? *gout : 1.f) / double(t)) : 0.f;
+}
+
+// A logit of minus infinity (a vocabulary entry that the bias masks) takes part as the lowest
+// finite value: its exponential is 0 beside any other, and a tile of nothing else has a maximum
+// that can be subtracted. NaN stays NaN.
+__device__ __forceinline__ float finite_low(float z) {
+  return z == -INFINITY ? -3.4028234663852886e38f : z;
+}
+
+// ------------------------------------------------------------------ the labelled rows
+
+// Numbers the rows that carry a label in their order: cidx[i] = the row's number or −1, and for
+// the m-th of them row[m] = i and ylab[m] = its label relative to the piece (−1 outside it);
+// *count of them. With `state`, the other rows' state is set to (−inf, 0, 0). One workgroup,
+// kRowsPer rows a thread and round.
+constexpr int kRowsPer = 8;
+__global__ void __launch_bounds__(1024) piece_rows_kernel(
+    const int32_t* __restrict__ labels, int64_t n, int64_t v, int64_t v_start, int64_t vocab,
+    int32_t ignore_index, int32_t* __restrict__ count, int32_t* __restrict__ cidx,
+    int32_t* __restrict__ row, int32_t* __restrict__ ylab, float* __restrict__ state,
+    int32_t* __restrict__ status) {
+  __shared__ int wave_sum[16];
+  __shared__ int any_bad;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  if (threadIdx.x == 0) any_bad = 0;
+  int done = 0;
+  bool bad = false;
+  for (int64_t base = 0; base < n; base += 1024 * kRowsPer) {
+    const int64_t i0 = base + int64_t(threadIdx.x) * kRowsPer;
+    int32_t y[kRowsPer];
+    int mine = 0;
+#pragma unroll
+    for (int k = 0; k < kRowsPer; ++k) {
+      y[k] = i0 + k < n ? labels[i0 + k] : ignore_index;
+      const bool ok = labelled(y[k], vocab, ignore_index);
+      bad |= !ok && y[k] != ignore_index;
+      mine += ok;
+    }
+    int upto = mine;  // inclusive sum over the wavefront
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) {
+      const int o = __shfl_up(upto, off, 64);
+      if (lane >= off) upto += o;
+    }
+    __syncthreads();  // the last round's sums have been read
+    if (lane == 63) wave_sum[wave] = upto;
+    __syncthreads();
+    int before = done, total = 0;
+    for (int w = 0; w < 16; ++w) {
+      if (w < wave) before += wave_sum[w];
+      total += wave_sum[w];
+    }
+    int m = before + upto - mine;
+#pragma unroll
+    for (int k = 0; k < kRowsPer; ++k) {
+      const int64_t i = i0 + k;
+      if (i >= n) break;
+      if (labelled(y[k], vocab, ignore_index)) {
+        const int64_t d = int64_t(y[k]) - v_start;
+        cidx[i] = m;
+        row[m] = int32_t(i);
+        ylab[m] = d >= 0 && d < v ? int32_t(d) : -1;
+        ++m;
+      } else {
+        cidx[i] = -1;
+        if (state) {
+          state[i] = -INFINITY;
+          state[n + i] = 0.f;
+          state[2 * n + i] = 0.f;
+        }
+      }
+    }
+    done += total;
+  }
+  if (status) {
+    __syncthreads();
+    if (bad) any_bad = 1;
+    __syncthreads();
+    if (threadIdx.x == 0) *status = any_bad ? LCE_STATUS_BAD_LABEL : 0;
+  }
+  if (threadIdx.x == 0) *count = done;
+}
+
+struct GatherArgs {
+  const uint16_t* hidden;
+  int64_t n, h, h64;
+  const int32_t* count;
+  const int32_t* cidx;
+  int32_t* ylab;
+  uint16_t* hc;            // [up(n, kTile)][h64]
+  // backward only
+  const float* lse;
+  const float* grad_rows;
+  float* lse_c;
+  float* coef_c;
+  float* zero_acc;         // rows without a label are zeroed here (NULL: not)
+  uint16_t* zero_grad;
+};
+
+// Workgroup i < n: the hidden row of a labelled row to its place, zero-padded to h64 columns;
+// the outputs of a row without a label to 0. Workgroups n .. n + kTile − 1: the rows between the
+// count and the next multiple of the tile, as rows that contribute nothing.
+__global__ void __launch_bounds__(256) gather_rows_kernel(GatherArgs a) {
+  const int64_t i = blockIdx.x;
+  const uint4 zero = {0u, 0u, 0u, 0u};
+  if (i >= a.n) {
+    const int64_t count = *a.count, m = count + (i - a.n);
+    if (m >= up(count, kTile)) return;
+    for (int64_t c = 8 * int64_t(threadIdx.x); c < a.h64; c += 8 * 256)
+      *reinterpret_cast<uint4*>(a.hc + m * a.h64 + c) = zero;
+    if (threadIdx.x == 0) {
+      a.ylab[m] = -1;
+      if (a.lse_c) a.lse_c[m] = INFINITY;
+      if (a.coef_c) a.coef_c[m] = 0.f;
+    }
+    return;
+  }
+  const int64_t m = a.cidx[i];
+  if (m < 0) {
+    if (a.zero_acc)
+      for (int64_t c = 4 * int64_t(threadIdx.x); c < a.h; c += 4 * 256)
+        *reinterpret_cast<uint4*>(a.zero_acc + i * a.h + c) = zero;
+    if (a.zero_grad)
+      for (int64_t c = 8 * int64_t(threadIdx.x); c < a.h; c += 8 * 256)
+        *reinterpret_cast<uint4*>(a.zero_grad + i * a.h + c) = zero;
+    return;
+  }
+  for (int64_t c = 8 * int64_t(threadIdx.x); c < a.h64; c += 8 * 256)
+    *reinterpret_cast<uint4*>(a.hc + m * a.h64 + c) =
+        c < a.h ? *reinterpret_cast<const uint4*>(a.hidden + i * a.h + c) : zero;
+  if (threadIdx.x == 0) {
+    if (a.lse_c) a.lse_c[m] = a.lse[i];
+    if (a.coef_c) a.coef_c[m] = a.grad_rows[i];
+  }
+}
+
+// W [v, h] to [v, h64], zero-padded (h not a multiple of the K slice).
+__global__ void __launch_bounds__(256) pad_rows_kernel(const uint16_t* __restrict__ w, int64_t h,
+                                                       int64_t h64, uint16_t* __restrict__ out) {
+  const int64_t r = blockIdx.x;
+  for (int64_t c = 8 * int64_t(threadIdx.x); c < h64; c += 8 * 256)
+    *reinterpret_cast<uint4*>(out + r * h64 + c) =
+        c < h ? *reinterpret_cast<const uint4*>(w + r * h + c) : uint4{0u, 0u, 0u, 0u};
+}
+
+// ------------------------------------------------------------------ forward
+
+__device__ __forceinline__ f32x4_t bias4(const float* bias, int64_t n, int64_t v) {
+  f32x4_t b{0.f, 0.f, 0.f, 0.f};
+  if (bias) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      if (n + q < v) b[q] = bias[n + q];
+  }
+  return b;
+}
+
+// The logits tile reduced to each row's (max, Σ exp(z − max)), and the label's logit.
+struct EpiPieceLse {
+  static constexpr bool kRowStats = true, kColSums = false, kTileMax = false, kRowTag = true;
+  static constexpr bool kRowLimit = true;
+  const float* bias;
+  int64_t v;
+  const int32_t* ylab;
+  const int32_t* count;
+  float2* part;
+  int64_t tiles;
+  float* zy;
+  struct Aux {
+    f32x4_t b;
+    int y;
+  };
+  __device__ void begin(int64_t) {}
+  __device__ __forceinline__ int64_t row_limit() const { return *count; }
+  __device__ __forceinline__ int row_tag(int64_t m) const { return ylab[m]; }
+  __device__ __forceinline__ Aux load4(int64_t, int64_t n) const { return {bias4(bias, n, v), -1}; }
+  __device__ __forceinline__ Aux load4t(int64_t, int64_t n, int y) const {
+    return {bias4(bias, n, v), y};
+  }
+  __device__ __forceinline__ f32x4_t value4(f32x4_t a, const Aux& x) const {
+    f32x4_t z = a + x.b;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) z[q] = finite_low(z[q]);
+    return z;
+  }
+  __device__ __forceinline__ float value1(int64_t n, float a) const {
+    return finite_low(bias ? a + bias[n] : a);
+  }
+  __device__ __forceinline__ void store4(int64_t m, int64_t n, f32x4_t a, const Aux& x) {
+    const int64_t d = int64_t(x.y) - n;
+    if (x.y >= 0 && d >= 0 && d < 4) {
+      const f32x4_t z = a + x.b;
+      zy[m] = d == 0 ? z[0] : d == 1 ? z[1] : d == 2 ? z[2] : z[3];
+    }
+  }
+  __device__ __forceinline__ void operator()(int64_t m, int64_t n, float a) {
+    if (int64_t(ylab[m]) == n) zy[m] = bias ? a + bias[n] : a;
+  }
+  __device__ __forceinline__ void row_stats(int64_t m, int64_t t, float mx, float sum) {
+    part[m * tiles + t] = float2{mx, sum};
+  }
+};
+
+// The same for few rows: z of 64 vocabulary rows and up to 16 · NB hidden rows per workgroup,
+// without staging. The four wavefronts split the columns; each takes v_mfma_f32_16x16x32_bf16
+// with the weight rows as its first operand, so a lane's accumulator is one hidden row's column.
+// A lane loads 32 consecutive bytes of a weight row per 64 columns (four lanes a full 128-byte
+// line) and the two operands share whatever order of k that is. Rows past v and past n repeat
+// the last one; columns past h are zero in both operands.
+constexpr int kScoreCols = 64;  // vocabulary rows per workgroup
+template <int NB>
+__global__ void __launch_bounds__(256) score_kernel(
+    const uint16_t* __restrict__ hidden, const uint16_t* __restrict__ w,
+    const float* __restrict__ bias, const int32_t* __restrict__ labels, int64_t n, int64_t h,
+    int64_t v, int64_t v_start, float2* __restrict__ part, int64_t tiles,
+    float* __restrict__ zy) {
+  constexpr int T = 16 * NB, RB = kScoreCols / 16;
+  __shared__ float z[4][kScoreCols][T + 1];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t r0 = int64_t(blockIdx.x) * kScoreCols;
+  const int64_t span = up((h + 3) / 4, 64);  // columns of one wavefront
+  const int64_t k_lo = wave * span + 16 * (lane >> 4);
+  const int64_t k_hi = (wave + 1) * span < h ? (wave + 1) * span : h;
+  const uint16_t* wp[RB];
+  const uint16_t* hp[NB];
+#pragma unroll
+  for (int i = 0; i < RB; ++i) {
+    const int64_t r = r0 + 16 * i + (lane & 15);
+    wp[i] = w + (r < v ? r : v - 1) * h;
+  }
+#pragma unroll
+  for (int j = 0; j < NB; ++j) {
+    const int64_t r = 16 * j + (lane & 15);
+    hp[j] = hidden + (r < n ? r : n - 1) * h;
+  }
+  f32x4_t acc[RB][NB];
+#pragma unroll
+  for (int i = 0; i < RB; ++i)
+#pragma unroll
+    for (int j = 0; j < NB; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  auto load = [&](const uint16_t* p, int64_t k) {
+    const uint4 x = k < h ? *reinterpret_cast<const uint4*>(p + k) : uint4{0u, 0u, 0u, 0u};
+    return __builtin_bit_cast(gemm::bf16x8_t, x);
+  };
+  for (int64_t k0 = wave * span; k0 < k_hi; k0 += 64) {
+    const int64_t k = k_lo + (k0 - wave * span);
+    gemm::bf16x8_t a[RB][2], b[NB][2];
+#pragma unroll
+    for (int i = 0; i < RB; ++i) {
+      a[i][0] = load(wp[i], k);
+      a[i][1] = load(wp[i], k + 8);
+    }
+#pragma unroll
+    for (int j = 0; j < NB; ++j) {
+      b[j][0] = load(hp[j], k);
+      b[j][1] = load(hp[j], k + 8);
+    }
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int i = 0; i < RB; ++i)
+#pragma unroll
+        for (int j = 0; j < NB; ++j)
+          acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[i][u], b[j][u], acc[i][j], 0, 0, 0);
+  }
+#pragma unroll
+  for (int i = 0; i < RB; ++i)
+#pragma unroll
+    for (int j = 0; j < NB; ++j)
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        z[wave][16 * i + 4 * (lane >> 4) + q][16 * j + (lane & 15)] = acc[i][j][q];
+  __syncthreads();
+  // 256 / T neighbouring threads share a hidden row, T / 4 vocabulary rows each
+  constexpr int kShare = 256 / T, kEach = kScoreCols / kShare;
+  const int t = threadIdx.x / kShare, sub = threadIdx.x % kShare;
+  const int32_t y = t < n ? labels[t] : -1;
+  float x[kEach];
+  float m = -INFINITY, s = 0.f;
+#pragma unroll
+  for (int e = 0; e < kEach; ++e) {
+    const int c = e * kShare + sub;
+    const int64_t r = r0 + c;
+    x[e] = ((z[0][c][t] + z[1][c][t]) + z[2][c][t]) + z[3][c][t];
+    if (r < v && bias) x[e] += bias[r];
+    if (r < v && t < n && int64_t(y) == v_start + r) zy[t] = x[e];
+    x[e] = finite_low(x[e]);
+    if (r < v) m = fmaxf(m, x[e]);
+  }
+#pragma unroll
+  for (int e = 0; e < kEach; ++e)
+    if (r0 + e * kShare + sub < v) s += fast_exp2((x[e] - m) * kLog2e);
+#pragma unroll
+  for (int off = kShare / 2; off >= 1; off >>= 1) {
+    const float m2 = __shfl_xor(m, off, 64), s2 = __shfl_xor(s, off, 64);
+    lse_merge(m, s, m2, s2);
+  }
+  if (sub == 0 && t < n) part[t * tiles + blockIdx.x] = float2{m, s};
+}
+
+// One workgroup per row: its tiles' (max, Σ exp) pairs merged in a fixed order, and into the
+// state of the pieces before (unless this is the first). `row` maps the rows of `part` to rows
+// of the state (NULL: the same, rows without a label set to (−inf, 0, 0)).
+__global__ void __launch_bounds__(256) merge_state_kernel(
+    const float2* __restrict__ part, int64_t tiles, const float* __restrict__ zy,
+    const int32_t* __restrict__ row, const int32_t* __restrict__ count,
+    const int32_t* __restrict__ ylab, const int32_t* __restrict__ labels, int64_t n, int64_t v,
+    int64_t v_start, int64_t vocab, int32_t ignore_index, int first, float* __restrict__ state) {
+  const int64_t m = blockIdx.x;
+  int64_t i = m;
+  bool here;
+  if (row) {
+    if (m >= *count) return;
+    i = row[m];
+    here = ylab[m] >= 0;
+  } else {
+    const int32_t y = labels[m];
+    if (!labelled(y, vocab, ignore_index)) {
+      if (first && threadIdx.x == 0) {
+        state[i] = -INFINITY;
+        state[n + i] = 0.f;
+        state[2 * n + i] = 0.f;
+      }
+      return;
+    }
+    here = int64_t(y) >= v_start && int64_t(y) < v_start + v;
+  }
+  float mx = -INFINITY, sum = 0.f;
+  for (int64_t t = threadIdx.x; t < tiles; t += 256) {
+    const float2 p = part[m * tiles + t];
+    lse_merge(mx, sum, p.x, p.y);
+  }
+  wave_lse_reduce(mx, sum);
+  __shared__ float sm[4], ss[4];
+  if ((threadIdx.x & 63) == 0) {
+    sm[threadIdx.x >> 6] = mx;
+    ss[threadIdx.x >> 6] = sum;
+  }
+  __syncthreads();
+  if (threadIdx.x != 0) return;
+  mx = sm[0];
+  sum = ss[0];
+  for (int w = 1; w < 4; ++w) lse_merge(mx, sum, sm[w], ss[w]);
+  float z = here ? zy[m] : 0.f;
+  if (!first) {
+    float m0 = state[i], s0 = state[n + i];
+    lse_merge(m0, s0, mx, sum);
+    mx = m0;
+    sum = s0;
+    if (!here) z = state[2 * n + i];
+  }
+  state[i] = mx;
+  state[n + i] = sum;
+  state[2 * n + i] = z;
+}
+
+// ------------------------------------------------------------------ loss from the state
+
+struct LossArgs {
+  const float* state;
+  const int32_t* labels;
+  int64_t n, vocab;
+  int32_t ignore_index;
+  float *lse_out, *row_out;  // NULL: not asked for
+};
+// Row i's loss term lse − z_y (0 without a label); lse_out and row_out on the way.
+__device__ __forceinline__ float loss_term(const LossArgs& a, int64_t i) {
+  const int32_t y = a.labels[i];
+  float lse = 0.f, term = 0.f;
+  if (labelled(y, a.vocab, a.ignore_index)) {
+    lse = a.state[i] + fast_log2(a.state[a.n + i]) * kLn2;
+    term = lse - a.state[2 * a.n + i];
+  }
+  if (a.lse_out) a.lse_out[i] = lse;
+  if (a.row_out) a.row_out[i] = term;
+  return term;
+}
+
+// Everything in one workgroup, for few rows: terms, their fp64 sum in a fixed order, the count.
+constexpr int kSmallLoss = 4096;
+__global__ void __launch_bounds__(1024) small_loss_kernel(LossArgs a, long long t_host,
+                                                          float* __restrict__ loss,
+                                                          int32_t* __restrict__ status) {
+  __shared__ double part[16];
+  __shared__ int counts[16];
+  __shared__ int any_bad;
+  if (threadIdx.x == 0) any_bad = 0;
+  __syncthreads();
+  double sum = 0.0;
+  int count = 0;
+  for (int64_t i = threadIdx.x; i < a.n; i += 1024) {
+    const int32_t y = a.labels[i];
+    if (labelled(y, a.vocab, a.ignore_index))
+      ++count;
+    else if (y != a.ignore_index)
+      any_bad = 1;  // every writer writes the same value
+    sum += double(loss_term(a, i));
+  }
+  sum = wave_sum_f64(sum);
+#pragma unroll
+  for (int off = 32; off >= 1; off >>= 1) count += __shfl_xor(count, off, 64);
+  if ((threadIdx.x & 63) == 0) {
+    part[threadIdx.x >> 6] = sum;
+    counts[threadIdx.x >> 6] = count;
+  }
+  __syncthreads();
+  if (threadIdx.x != 0) return;
+  double total = 0.0;
+  long long c = 0;
+  for (int w = 0; w < 16; ++w) {
+    total += part[w];
+    c += counts[w];
+  }
+  const long long t = t_host >= 0 ? t_host : c;
+  if (loss) *loss = t > 0 ? float(total / double(t)) : 0.f;
+  if (status) *status = any_bad ? LCE_STATUS_BAD_LABEL : 0;
+}
+
+__global__ void __launch_bounds__(256) loss_terms_kernel(LossArgs a, float* __restrict__ terms) {
+  const int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x;
+  if (i >= a.n) return;
+  const float t = loss_term(a, i);
+  terms[i] = t;
+}
+
+// ------------------------------------------------------------------ backward
+
+// D = c · (exp(z − lse) − [v = y]) in bf16, in panels of 64 columns ([np][64] each, so that both
+// products read whole 128-byte lines one after the other); 0 in the columns v .. up(v, 64) − 1
+// and in the padding rows. BIAS: each tile's column sums of the fp32 values. ROWS: c is the
+// row's own coefficient, else 1.
+template <bool BIAS, bool ROWS>
+struct EpiPieceGrad {
+  static constexpr bool kRowStats = false, kColSums = BIAS, kTileMax = false, kRowTag = true;
+  static constexpr bool kRowLimit = true;
+  uint16_t* d;
+  int64_t np;
+  const float* bias;
+  int64_t v;
+  const int32_t* ylab;
+  const int32_t* count;
+  const float* lse;
+  const float* coef;
+  float* colsum;
+  int64_t v64;
+  struct Aux {
+    f32x4_t b;
+    float lse, c;
+    int y;
+  };
+  __device__ void begin(int64_t) {}
+  __device__ __forceinline__ int64_t row_limit() const { return *count; }
+  __device__ __forceinline__ int row_tag(int64_t m) const { return ylab[m]; }
+  __device__ __forceinline__ Aux load4t(int64_t m, int64_t n, int y) const {
+    return {bias4(bias, n, v), lse[m], ROWS ? coef[m] : 1.f, y};
+  }
+  __device__ __forceinline__ f32x4_t colvalue4(f32x4_t a, const Aux& x, int64_t n) const {
+    f32x4_t r;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      float p = fast_exp2(((a[q] + x.b[q]) - x.lse) * kLog2e);
+      if (int64_t(x.y) == n + q) p -= 1.f;
+      if (ROWS) p *= x.c;
+      r[q] = n + q < v ? p : 0.f;
+    }
+    return r;
+  }
+  __device__ __forceinline__ void store4(int64_t m, int64_t n, f32x4_t a, Aux& x) {
+    const f32x4_t r = colvalue4(a, x, n);
+    *reinterpret_cast<uint2*>(d + (n >> 6) * np * 64 + m * 64 + (n & 63)) =
+        uint2{pack_bf16x2(r[0], r[1]), pack_bf16x2(r[2], r[3])};
+    x.b = r;  // for the column sums
+  }
+  __device__ __forceinline__ f32x4_t colvalue4(f32x4_t, const Aux& x) const { return x.b; }
+  __device__ __forceinline__ void operator()(int64_t, int64_t, float) {}  // N % 4 == 0: unused
+  __device__ __forceinline__ void col_sums(int64_t mt, int64_t n, float sum) {
+    colsum[mt * v64 + n] = sum;
+  }
+};
+
+// Where the rows of dH go. The product's row m is the batch's row row[m].
+struct HiddenOut {
+  const int32_t* row;
+  const int32_t* count;
+  float* acc;       // fp32 [n, h] over the pieces; NULL with a single piece
+  uint16_t* grad;   // bf16 [n, h], written with the last piece (NULL: not)
+  int64_t h;
+  int first;
+  long long t_host;
+  const float* gout;
+  int rows;
+  __device__ __forceinline__ float scale() const { return loss_scale(count, t_host, gout, rows); }
+  __device__ __forceinline__ f32x4_t old(int64_t i, int64_t n) const {
+    if (first) return f32x4_t{0.f, 0.f, 0.f, 0.f};
+    return *reinterpret_cast<const f32x4_t*>(acc + i * h + n);
+  }
+  __device__ __forceinline__ void put(int64_t i, int64_t n, f32x4_t x) const {
+    if (grad)
+      *reinterpret_cast<uint2*>(grad + i * h + n) =
+          uint2{pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3])};
+    else
+      *reinterpret_cast<f32x4_t*>(acc + i * h + n) = x;
+  }
+};
+
+struct EpiPieceHidden {
+  static constexpr bool kRowStats = false, kColSums = false, kTileMax = false, kRowTag = true;
+  static constexpr bool kRowLimit = true;
+  HiddenOut o;
+  float s;
+  struct Aux {
+    f32x4_t old;
+    int i;
+  };
+  __device__ void begin(int64_t) { s = o.scale(); }
+  __device__ __forceinline__ int64_t row_limit() const { return *o.count; }
+  __device__ __forceinline__ int row_tag(int64_t m) const {
+    return m < int64_t(*o.count) ? o.row[m] : -1;
+  }
+  __device__ __forceinline__ Aux load4t(int64_t, int64_t n, int i) const {
+    return {i >= 0 ? o.old(i, n) : f32x4_t{0.f, 0.f, 0.f, 0.f}, i};
+  }
+  __device__ __forceinline__ void store4(int64_t, int64_t n, f32x4_t a, const Aux& x) {
+    if (x.i >= 0) o.put(x.i, n, x.old + s * a);
+  }
+  __device__ __forceinline__ void operator()(int64_t, int64_t, float) {}  // h % 4 == 0: unused
+};
+
+// The product split over K: partial sums [splits][np][h], then added in split order.
+struct EpiPiecePartial {
+  static constexpr bool kRowStats = false, kColSums = false, kTileMax = false;
+  static constexpr bool kRowLimit = true;
+  float* part;
+  int64_t np, h;
+  const int32_t* count;
+  int64_t kz;
+  struct Aux {};
+  __device__ void begin(int64_t z) { kz = z; }
+  __device__ __forceinline__ int64_t row_limit() const { return *count; }
+  __device__ __forceinline__ Aux load4(int64_t, int64_t) const { return Aux{}; }
+  __device__ __forceinline__ void store4(int64_t m, int64_t n, f32x4_t a, Aux) {
+    *reinterpret_cast<f32x4_t*>(part + (kz * np + m) * h + n) = a;
+  }
+  __device__ __forceinline__ void operator()(int64_t, int64_t, float) {}
+};
+__global__ void __launch_bounds__(256) hidden_reduce_kernel(const float* __restrict__ part,
+                                                            int64_t np, int64_t splits,
+                                                            HiddenOut o) {
+  const int64_t e = (int64_t(blockIdx.x) * 256 + threadIdx.x) * 4;
+  const int64_t m = e / o.h, n = e % o.h;
+  if (m >= int64_t(*o.count)) return;
+  f32x4_t a{0.f, 0.f, 0.f, 0.f};
+  for (int64_t z = 0; z < splits; ++z)
+    a += *reinterpret_cast<const f32x4_t*>(part + (z * np + m) * o.h + n);
+  const int64_t i = o.row[m];
+  o.put(i, n, o.old(i, n) + o.scale() * a);
+}
+
+// dW (=|+=) s · acc, in bf16 or fp32; the contraction runs over the labelled rows.
+template <class TW, bool ACC>
+struct EpiPieceWeight {
+  static constexpr bool kRowStats = false, kColSums = false, kTileMax = false;
+  static constexpr bool kKLimit = true;
+  TW* dw;
+  int64_t h;
+  const int32_t* count;
+  long long t_host;
+  const float* gout;
+  int rows;
+  float s;
+  using Aux = f32x4_t;
+  __device__ void begin(int64_t) { s = loss_scale(count, t_host, gout, rows); }
+  __device__ __forceinline__ int64_t k_limit() const { return *count; }
+  __device__ __forceinline__ Aux load4(int64_t m, int64_t n) const {
+    if constexpr (!ACC) {
+      return Aux{0.f, 0.f, 0.f, 0.f};
+    } else if constexpr (sizeof(TW) == 4) {
+      return *reinterpret_cast<const f32x4_t*>(dw + m * h + n);
+    } else {
+      const uint2 x = *reinterpret_cast<const uint2*>(dw + m * h + n);
+      return Aux{bf16_lo(x.x), bf16_hi(x.x), bf16_lo(x.y), bf16_hi(x.y)};
+    }
+  }
+  __device__ __forceinline__ void store4(int64_t m, int64_t n, f32x4_t a, Aux old) {
+    const f32x4_t x = ACC ? old + s * a : s * a;
+    if constexpr (sizeof(TW) == 4)
+      *reinterpret_cast<f32x4_t*>(dw + m * h + n) = x;
+    else
+      *reinterpret_cast<uint2*>(dw + m * h + n) =
+          uint2{pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3])};
+  }
+  __device__ __forceinline__ void operator()(int64_t, int64_t, float) {}  // h % 4 == 0: unused
+};
+
+// db (=|+=) s · the column sums of the row tiles, in tile order.
+__global__ void __launch_bounds__(256) piece_bias_kernel(
+    const float* __restrict__ colsum, int64_t v, int64_t v64, const int32_t* __restrict__ count,
+    long long t_host, const float* __restrict__ gout, int rows, int accumulate,
+    float* __restrict__ db) {
+  const int64_t c = int64_t(blockIdx.x) * 256 + threadIdx.x;
+  if (c >= v) return;
+  const int64_t tiles = (int64_t(*count) + kTile - 1) / kTile;
+  float sum = 0.f;
+#pragma unroll 4
+  for (int64_t t = 0; t < tiles; ++t) sum += colsum[t * v64 + c];
+  const float x = loss_scale(count, t_host, gout, rows) * sum;
+  db[c] = accumulate ? db[c] + x : x;
+}
+
+// ------------------------------------------------------------------ workspaces
+
+size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
+
+// Hidden-gradient splits over K for few output tiles: enough to fill the CUs, each at least
+// 1024 vocabulary rows long.
+int64_t hidden_splits(int64_t n, int64_t h, int64_t v) {
+  const int64_t tiles = (n + kTile - 1) / kTile * ((h + Wide::BN - 1) / Wide::BN);
+  return std::max<int64_t>(1, std::min<int64_t>(256 / std::max<int64_t>(tiles, 1), v / 1024));
+}
+
+struct PieceWs {
+  int32_t *count, *cidx, *row, *ylab;
+  float *zy, *lse_c, *coef_c, *colsum, *split;
+  float2* part;
+  uint16_t *hc, *wpad, *d;
+  size_t bytes;
+};
+
+struct Carver {
+  char* base;
+  size_t off = 0;
+  template <class T>
+  T* take(int64_t count) {
+    T* p = reinterpret_cast<T*>(base + off);
+    off += align256(size_t(count) * sizeof(T));
+    return p;
+  }
+};
+
+PieceWs carve_fwd(void* base, int64_t n, int64_t h, int64_t v) {
+  PieceWs w{};
+  Carver c{static_cast<char*>(base)};
+  if (n <= kScoreRows) {
+    w.zy = c.take<float>(n);
+    w.part = c.take<float2>(n * ((v + kScoreCols - 1) / kScoreCols));
+  } else {
+    const int64_t np = up(n, kTile), h64 = up(h, Wide::BK);
+    w.count = c.take<int32_t>(1);
+    w.cidx = c.take<int32_t>(n);
+    w.row = c.take<int32_t>(np);
+    w.ylab = c.take<int32_t>(np);
+    w.zy = c.take<float>(np);
+    w.part = c.take<float2>(np * ((v + Wide::BN - 1) / Wide::BN));
+    w.hc = c.take<uint16_t>(np * h64);
+    if (h64 != h) w.wpad = c.take<uint16_t>(v * h64);
+  }
+  w.bytes = std::max<size_t>(c.off, 256);
+  return w;
+}
+
+PieceWs carve_bwd(void* base, int64_t n, int64_t h, int64_t v) {
+  PieceWs w{};
+  Carver c{static_cast<char*>(base)};
+  const int64_t np = up(n, kTile), h64 = up(h, Wide::BK), v64 = up(v, 64);
+  w.count = c.take<int32_t>(1);
+  w.cidx = c.take<int32_t>(n);
+  w.row = c.take<int32_t>(np);
+  w.ylab = c.take<int32_t>(np);
+  w.lse_c = c.take<float>(np);
+  w.coef_c = c.take<float>(np);
+  w.hc = c.take<uint16_t>(np * h64);
+  if (h64 != h) w.wpad = c.take<uint16_t>(v * h64);
+  w.d = c.take<uint16_t>(np * v64);
+  w.colsum = c.take<float>(np / kTile * v64);
+  const int64_t splits = hidden_splits(n, h, v);
+  if (splits > 1) w.split = c.take<float>(splits * np * h);
+  w.bytes = std::max<size_t>(c.off, 256);
+  return w;
+}
+
+#define PIECE_TRY(expr)                    \
+  do {                                     \
+    const hipError_t e_ = (expr);          \
+    if (e_ != hipSuccess) return e_;       \
+  } while (0)
+
+hipError_t rows_and_gather(const uint16_t* hidden, const int32_t* labels, int64_t n, int64_t h,
+                           int64_t v, int64_t v_start, int64_t vocab, int32_t ignore_index,
+                           const PieceWs& w, float* state, int32_t* status, GatherArgs g,
+                           hipStream_t s) {
+  TimedLaunch t(s, K_PIECE_GATHER);
+  hipLaunchKernelGGL(piece_rows_kernel, dim3(1), dim3(1024), 0, s, labels, n, v, v_start, vocab,
+                     ignore_index, w.count, w.cidx, w.row, w.ylab, state, status);
+  PIECE_TRY(hipGetLastError());
+  g.hidden = hidden;
+  g.n = n;
+  g.h = h;
+  g.h64 = up(h, Wide::BK);
+  g.count = w.count;
+  g.cidx = w.cidx;
+  g.ylab = w.ylab;
+  g.hc = w.hc;
+  hipLaunchKernelGGL(gather_rows_kernel, dim3(unsigned(n + kTile)), dim3(256), 0, s, g);
+  return hipGetLastError();
+}
+
+hipError_t pad_weight(const uint16_t* weight, int64_t h, int64_t v, uint16_t* out, hipStream_t s) {
+  TimedLaunch t(s, K_PIECE_GATHER);
+  hipLaunchKernelGGL(pad_rows_kernel, dim3(unsigned(v)), dim3(256), 0, s, weight, h,
+                     up(h, Wide::BK), out);
+  return hipGetLastError();
+}
+
+template <bool BIAS, bool ROWS>
+hipError_t grad_logits(const PieceBwdArgs& a, const PieceWs& w, const View& hv, const View& wv,
+                       hipStream_t s) {
+  const int64_t np = up(a.n, kTile), v64 = up(a.v, 64), h64 = up(a.h, Wide::BK);
+  EpiPieceGrad<BIAS, ROWS> e{w.d, np, a.bias, a.v, w.ylab, w.count, w.lse_c, w.coef_c, w.colsum,
+                             v64};
+  TimedLaunch t(s, K_PIECE_GRAD_LOGITS);
+  return gemm::v2::launch<Wide, true, true>(hv, wv, np, v64, h64, 1, true, e, s);
+}
+
+template <class TW, bool ACC>
+hipError_t grad_weight_product(const PieceBwdArgs& a, const PieceWs& w, const View& dv,
+                               const View& hv, hipStream_t s) {
+  EpiPieceWeight<TW, ACC> e{static_cast<TW*>(a.grad_weight), a.h, w.count, a.num_label_tokens,
+                            a.grad_output, int(a.grad_rows != nullptr), 0.f};
+  TimedLaunch t(s, K_PIECE_GRAD_WEIGHT);
+  return gemm::v2::launch<Wide, false, false>(dv, hv, a.v, a.h, up(a.n, kTile), 1, true, e, s,
+                                              true);
+}
+
+}  // namespace
+
+size_t piece_fwd_workspace_bytes(int64_t n, int64_t h, int64_t v) {
+  return carve_fwd(nullptr, n, h, v).bytes;
+}
+size_t piece_bwd_workspace_bytes(int64_t n, int64_t h, int64_t v) {
+  return carve_bwd(nullptr, n, h, v).bytes;
+}
+size_t piece_loss_workspace_bytes(int64_t n) { return ce_workspace_bytes(n); }
+
+hipError_t piece_fwd_run(const PieceFwdArgs& a, hipStream_t s) {
+  if (a.n == 0) return hipSuccess;
+  const PieceWs w = carve_fwd(a.workspace, a.n, a.h, a.v);
+  const int first = (a.flags & FLCE_PIECE_FIRST) != 0;
+  int64_t tiles;
+  if (a.n <= kScoreRows) {
+    tiles = (a.v + kScoreCols - 1) / kScoreCols;
+    TimedLaunch t(s, K_PIECE_LOGITS);
+    auto launch = [&](auto kernel) {
+      hipLaunchKernelGGL(kernel, dim3(unsigned(tiles)), dim3(256), 0, s, a.hidden, a.weight,
+                         a.bias, a.labels, a.n, a.h, a.v, a.v_start, w.part, tiles, w.zy);
+    };
+    if (a.n <= 16)
+      launch(score_kernel<1>);
+    else if (a.n <= 32)
+      launch(score_kernel<2>);
+    else
+      launch(score_kernel<4>);
+    PIECE_TRY(hipGetLastError());
+  } else {
+    tiles = (a.v + Wide::BN - 1) / Wide::BN;
+    const int64_t np = up(a.n, kTile), h64 = up(a.h, Wide::BK);
+    PIECE_TRY(rows_and_gather(a.hidden, a.labels, a.n, a.h, a.v, a.v_start, a.vocab,
+                              a.ignore_index, w, first ? a.state : nullptr, nullptr,
+                              GatherArgs{}, s));
+    const uint16_t* weight = a.weight;
+    if (w.wpad) {
+      PIECE_TRY(pad_weight(a.weight, a.h, a.v, w.wpad, s));
+      weight = w.wpad;
+    }
+    View hv{w.hc, h64, 64, np, h64};
+    View wv{weight, h64, 64, a.v, h64};
+    EpiPieceLse e{a.bias, a.v, w.ylab, w.count, w.part, tiles, w.zy};
+    TimedLaunch t(s, K_PIECE_LOGITS);
+    PIECE_TRY((gemm::v2::launch<Wide, true, true>(hv, wv, np, a.v, h64, 1, true, e, s)));
+  }
+  TimedLaunch t(s, K_PIECE_STATE);
+  hipLaunchKernelGGL(merge_state_kernel, dim3(unsigned(a.n)), dim3(256), 0, s, w.part, tiles, w.zy,
+                     w.row, w.count, w.ylab, a.labels, a.n, a.v, a.v_start, a.vocab,
+                     a.ignore_index, first, a.state);
+  return hipGetLastError();
+}
+
+hipError_t piece_loss_run(const PieceLossArgs& a, hipStream_t s) {
+  const LossArgs l{a.state, a.labels, a.n, a.vocab, a.ignore_index, a.lse_out, a.row_loss_out};
+  const long long th = a.num_label_tokens >= 0 ? a.num_label_tokens : -1;
+  if (a.n <= kSmallLoss) {
+    TimedLaunch t(s, K_PIECE_STATE);
+    hipLaunchKernelGGL(small_loss_kernel, dim3(1), dim3(1024), 0, s, l, th, a.loss_out,
+                       a.status_out);
+    return hipGetLastError();
+  }
+  const CeWorkspace ws = ce_workspace_carve(a.workspace, a.n);
+  PIECE_TRY(launch_label_prep(a.labels, a.n, a.vocab, a.ignore_index, ws.count, a.status_out, s));
+  {
+    TimedLaunch t(s, K_PIECE_STATE);
+    hipLaunchKernelGGL(loss_terms_kernel, dim3(unsigned((a.n + 255) / 256)), dim3(256), 0, s, l,
+                       ws.row_loss);
+    PIECE_TRY(hipGetLastError());
+  }
+  if (!a.loss_out) return hipSuccess;
+  return launch_loss_reduce(ws.row_loss, a.n, ws.count, th, a.loss_out, s);
+}
+
+hipError_t piece_bwd_run(const PieceBwdArgs& a, hipStream_t s) {
+  const bool first = (a.flags & FLCE_PIECE_FIRST) != 0, last = (a.flags & FLCE_PIECE_LAST) != 0;
+  const bool accumulate = (a.flags & FLCE_PIECE_ACCUMULATE) != 0;
+  const PieceWs w = carve_bwd(a.workspace, a.n, a.h, a.v);
+  const int64_t np = up(a.n, kTile), h64 = up(a.h, Wide::BK), v64 = up(a.v, 64);
+  const bool rows = a.grad_rows != nullptr;
+  GatherArgs g{};
+  g.lse = a.lse;
+  g.grad_rows = a.grad_rows;
+  g.lse_c = w.lse_c;
+  g.coef_c = rows ? w.coef_c : nullptr;
+  g.zero_acc = first && !last ? a.hidden_acc : nullptr;
+  g.zero_grad = last ? a.grad_hidden : nullptr;
+  PIECE_TRY(rows_and_gather(a.hidden, a.labels, a.n, a.h, a.v, a.v_start, a.vocab, a.ignore_index,
+                            w, nullptr, nullptr, g, s));
+  const uint16_t* weight = a.weight;
+  if (w.wpad) {
+    PIECE_TRY(pad_weight(a.weight, a.h, a.v, w.wpad, s));
+    weight = w.wpad;
+  }
+  View hv{w.hc, h64, 64, np, h64};
+  View wv{weight, h64, 64, a.v, h64};
+  if (a.n > 0) {
+    if (a.grad_bias)
+      PIECE_TRY((rows ? grad_logits<true, true>(a, w, hv, wv, s)
+                      : grad_logits<true, false>(a, w, hv, wv, s)));
+    else
+      PIECE_TRY((rows ? grad_logits<false, true>(a, w, hv, wv, s)
+                      : grad_logits<false, false>(a, w, hv, wv, s)));
+  }
+  View dv{w.d, 64, np * 64, np, a.v};
+  dv.ext = np * v64;
+  if (a.n > 0 && (last ? static_cast<void*>(a.grad_hidden) : a.hidden_acc)) {
+    const HiddenOut o{w.row, w.count, a.hidden_acc, last ? a.grad_hidden : nullptr, a.h,
+                      int(first), a.num_label_tokens, a.grad_output, int(rows)};
+    const int64_t splits = hidden_splits(a.n, a.h, a.v);
+    View wk{weight, h64, 64, a.v, a.h};
+    if (splits == 1) {
+      EpiPieceHidden e{o, 0.f};
+      TimedLaunch t(s, K_PIECE_GRAD_HIDDEN);
+      PIECE_TRY((gemm::v2::launch<Wide, true, false>(dv, wk, np, a.h, a.v, 1, true, e, s, true)));
+    } else {
+      EpiPiecePartial e{w.split, np, a.h, w.count, 0};
+      {
+        TimedLaunch t(s, K_PIECE_GRAD_HIDDEN);
+        PIECE_TRY((gemm::v2::launch<Wide, true, false>(dv, wk, np, a.h, a.v, splits, true, e, s)));
+      }
+      TimedLaunch t(s, K_PIECE_GRAD_HIDDEN);
+      hipLaunchKernelGGL(hidden_reduce_kernel, dim3(unsigned((a.n * a.h / 4 + 255) / 256)),
+                         dim3(256), 0, s, w.split, np, splits, o);
+      PIECE_TRY(hipGetLastError());
+    }
+  }
+  if (a.grad_weight && !(a.n == 0 && accumulate)) {
+    View hk{w.hc, h64, 64, np, a.h};
+    if (a.grad_weight_dtype == LCE_DTYPE_F32)
+      PIECE_TRY((accumulate ? grad_weight_product<float, true>(a, w, dv, hk, s)
+                            : grad_weight_product<float, false>(a, w, dv, hk, s)));
+    else
+      PIECE_TRY((accumulate ? grad_weight_product<uint16_t, true>(a, w, dv, hk, s)
+                            : grad_weight_product<uint16_t, false>(a, w, dv, hk, s)));
+  }
+  if (a.grad_bias && !(a.n == 0 && accumulate)) {
+    TimedLaunch t(s, K_PIECE_GRAD_BIAS);
+    hipLaunchKernelGGL(piece_bias_kernel, dim3(unsigned((a.v + 255) / 256)), dim3(256), 0, s,
+                       w.colsum, a.v, v64, w.count, a.num_label_tokens, a.grad_output, int(rows),
+                       int(accumulate), a.grad_bias);
+    PIECE_TRY(hipGetLastError());
+  }
+  return hipSuccess;
+}
+
+}  // namespace lce

@@ -541,6 +541,26 @@ struct RowTagged<E, std::void_t<decltype(E::kRowTag)>> {
   static constexpr bool value = E::kRowTag;
 };
 
+// Epilogues that set kRowLimit hold the number of output rows that count in device memory
+// (row_limit(), at most M): tiles wholly past it are skipped. Those that set kKLimit hold the
+// length of the contraction there (k_limit(), at most K).
+template <class E, class = void>
+struct RowLimited {
+  static constexpr bool value = false;
+};
+template <class E>
+struct RowLimited<E, std::void_t<decltype(E::kRowLimit)>> {
+  static constexpr bool value = E::kRowLimit;
+};
+template <class E, class = void>
+struct KLimited {
+  static constexpr bool value = false;
+};
+template <class E>
+struct KLimited<E, std::void_t<decltype(E::kKLimit)>> {
+  static constexpr bool value = E::kKLimit;
+};
+
 // Tile coordinates (m-tile, n-tile, K split) of workgroup w; false for a workgroup with no
 // tile (the XCD-block mapping pads every XCD to the largest block).
 struct TileCoord {
@@ -845,6 +865,13 @@ __global__ void __launch_bounds__(C::THREADS, C::OCC)
   __shared__ __attribute__((aligned(1024))) char lds[C::LdsBytes];
   TileCoord tc;
   if (!tile_coord(tm, blockIdx.x, tc)) return;  // uniform over the workgroup
+  if constexpr (RowLimited<Epi>::value) {
+    if (tc.mt * C::BM >= epi.row_limit()) return;
+  }
+  if constexpr (KLimited<Epi>::value) {
+    const int64_t k = epi.k_limit();
+    if (k < K) K = k;
+  }
   run_tile<C, AK, BKM, Epi, SEGA>(A, B, M, N, K, ksplit, tc, epi, lds);
 }
 

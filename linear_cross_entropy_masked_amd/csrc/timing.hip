@@ -43,7 +43,9 @@ const char* kNames[K_COUNT] = {
     "ce_fused_rows",      "flce_loss_acc",         "flce_probs_transposed",
     "embed_fwd",          "embed_sort",            "embed_grad",
     "embed_join",         "layernorm_fwd",         "layernorm_bwd",
-    "layernorm_param_reduce",
+    "layernorm_param_reduce", "piece_gather",      "piece_logits",
+    "piece_state",        "piece_grad_logits",     "piece_grad_hidden",
+    "piece_grad_weight",  "piece_grad_bias",
 };
 
 }  // namespace

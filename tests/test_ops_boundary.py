@@ -1,4 +1,4 @@
-"""CPU checks of the embedding and layer norm entry points: bad arguments are refused with the
+"""CPU checks of the embedding, layer norm and vocabulary-piece entry points: bad arguments are refused with the
 documented status codes before anything touches a GPU (fake device addresses, as in
 test_boundary.py), and the binding's own refusals."""
 import ctypes
@@ -115,6 +115,68 @@ def test_layernorm_refusals(lib):
         assert call(gx=None, gw=None, gb=None, ws=None, lddx=0) in AT_DEVICE_CHECK
 
 
+def test_piece_refusals(lib):
+    out = ctypes.c_size_t()
+    ref = ctypes.byref(out)
+    assert lib.flce_piece_fwd_workspace_size(4, 16, 10, None) == NULL_ARG
+    assert lib.flce_piece_fwd_workspace_size(4, 12, 10, ref) == BAD_SHAPE
+    assert lib.flce_piece_loss_workspace_size((1 << 23) + 1, ref) == BAD_SHAPE
+    assert lib.flce_piece_bwd_workspace_size(4, 16, 0, ref) == BAD_SHAPE
+    # the backward's workspace holds the piece's bf16 logit gradients, not the vocabulary's
+    assert lib.flce_piece_bwd_workspace_size(8192, 4096, 16384, ref) == OK
+    assert out.value >= 8192 * 16384 * 2 and out.value <= 8192 * 16384 * 2 + 8192 * 4096 * 3
+    assert lib.flce_piece_bwd_workspace_size(4, 16, 10, ref) == OK
+    need = out.value
+    call = caller(lib.flce_piece_fwd, dict(hid=A[0], w=A[1], b=A[2], lab=A[3], n=4, h=16, v=10,
+                                           start=0, vocab=10, ign=-100, flags=1, state=A[4],
+                                           ws=A[5], wsb=BIG, stream=None))
+    assert call(flags=2) == BAD_FLAGS and call(h=12) == BAD_SHAPE and call(n=-1) == BAD_SHAPE
+    assert call(start=1) == BAD_SHAPE and call(start=-1) == BAD_SHAPE
+    assert call(vocab=9) == BAD_SHAPE and call(vocab=1 << 31) == BAD_SHAPE
+    assert call(n=(1 << 23) + 1) == BAD_SHAPE and call(h=(1 << 20) + 8) == BAD_SHAPE
+    assert call(hid=None) == NULL_ARG and call(w=None) == NULL_ARG and call(state=None) == NULL_ARG
+    assert call(ws=None) == WORKSPACE and call(wsb=1) == WORKSPACE
+    assert call(hid=A[0] + 8) == ALIGN and call(w=A[1] + 2) == ALIGN and call(ws=A[5] + 8) == ALIGN
+    assert call(state=A[3]) == OVERLAP and call(ws=A[1]) == OVERLAP
+    if no_gpu():
+        assert call(start=90, vocab=100, flags=0, b=None) in AT_DEVICE_CHECK
+        assert call(n=0, hid=None, lab=None, state=None) in AT_DEVICE_CHECK
+    call = caller(lib.flce_piece_loss, dict(state=A[0], lab=A[1], n=4, vocab=10, ign=-100, t=-1,
+                                            loss=A[2], lse=A[3], rows=A[4], status=A[5], ws=A[6],
+                                            wsb=BIG, stream=None))
+    assert call(vocab=0) == BAD_SHAPE and call(n=-1) == BAD_SHAPE
+    assert call(state=None) == NULL_ARG and call(lab=None) == NULL_ARG
+    assert call(wsb=8) == WORKSPACE and call(loss=A[2] + 2) == ALIGN
+    assert call(lse=A[0]) == OVERLAP and call(rows=A[3] + 4) == OVERLAP
+    if no_gpu():
+        assert call(loss=None, lse=None, rows=None, status=None) in AT_DEVICE_CHECK
+    call = caller(lib.flce_piece_bwd, dict(hid=A[0], w=A[1], b=A[2], lab=A[3], lse=A[4], n=4, h=16,
+                                           v=10, start=0, vocab=10, ign=-100, t=-1, flags=3,
+                                           gout=None, grows=None, acc=A[5], gh=A[6], gw=A[7], wd=0,
+                                           gb=A[8], ws=A[9], wsb=BIG, stream=None))
+    assert call(flags=8) == BAD_FLAGS and call(h=0) == BAD_SHAPE and call(vocab=5) == BAD_SHAPE
+    assert call(wd=1) == BAD_DTYPE
+    assert call(b=None) == NULL_ARG  # grad_bias needs one
+    assert call(lse=None) == NULL_ARG and call(flags=2, acc=None) == NULL_ARG
+    assert call(wsb=need - 1) == WORKSPACE
+    assert call(gh=A[6] + 8) == ALIGN and call(gw=A[7] + 2) == ALIGN and call(acc=A[5] + 4) == ALIGN
+    assert call(gh=A[0]) == OVERLAP and call(acc=A[6]) == OVERLAP and call(gb=A[4]) == OVERLAP
+    assert call(grows=A[9]) == OVERLAP
+    if no_gpu():
+        assert call(wsb=need) in AT_DEVICE_CHECK and call(acc=None) in AT_DEVICE_CHECK
+        assert call(gh=None, gw=None, gb=None, b=None, flags=0, acc=None) in AT_DEVICE_CHECK
+
+
+def test_piece_size_rule():
+    """Default pieces: whole 256-column tiles, equal parts, within the byte budget."""
+    assert lce._piece_rows(8192, 128256, None) == 32256
+    assert lce._piece_rows(64, 32777, None) == 33024
+    assert lce._piece_rows(1 << 20, 128256, None) <= 4096
+    assert lce._piece_rows(10, 100, 7) == 7
+    with pytest.raises(ValueError, match="piece_size"):
+        lce._piece_rows(10, 100, 0)
+
+
 def test_binding_refuses_host_tensors_and_wrong_types():
     with pytest.raises(ValueError, match="HIP device"):
         lce.embed_fwd(torch.zeros(3, 4), torch.zeros(2, dtype=torch.int32))
@@ -126,3 +188,11 @@ def test_binding_refuses_host_tensors_and_wrong_types():
         lce.layernorm_fwd(torch.zeros(3, 4))
     with pytest.raises(TypeError, match="float32"):
         lce.layernorm_bwd(torch.zeros(3, 4), torch.zeros(3, 4, dtype=torch.int8), None, None)
+    hid = torch.zeros(3, 8, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="HIP device"):
+        lce.flce_pieces_fwd(hid, hid, torch.zeros(3, dtype=torch.int32))
+    with pytest.raises(ValueError, match="no pieces"):
+        lce.flce_pieces_fwd(hid, [], torch.zeros(3, dtype=torch.int32))
+    with pytest.raises(ValueError, match="biases"):
+        lce.flce_pieces_fwd(hid, [hid, hid], torch.zeros(3, dtype=torch.int32),
+                            [torch.zeros(3)])
