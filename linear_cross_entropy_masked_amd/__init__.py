@@ -538,27 +538,46 @@ def flce_bwd(hidden, weight, labels, lse, bias=None, *, ignore_index: int = -100
     return gh, gw, gb
 
 
+_FNS: dict = {}  # C entry points looked up so far
+
+
 def _call(fn, device, *args):
     """fn(*args) with ``device`` current (the library checks and launches on the current one);
     raises on a status code. The stream, the last argument, is the caller's current one there."""
     import torch
-    f = getattr(load_library(), fn)
-    if device.index == torch.cuda.current_device():
-        code = f(*args, torch.cuda.current_stream(device).cuda_stream)
+    f = _FNS.get(fn)
+    if f is None:
+        f = _FNS[fn] = getattr(load_library(), fn)
+    index = device.index
+    if index == torch.cuda.current_device():
+        code = f(*args, _raw_stream(torch, index))
     else:
         with torch.cuda.device(device):
-            code = f(*args, torch.cuda.current_stream(device).cuda_stream)
+            code = f(*args, _raw_stream(torch, index))
     if code != 0:
         raise LceError(fn, code)
+
+
+def _raw_stream(torch, index):
+    """The current stream's handle; without building a Stream object where torch lets us, which
+    takes 2 us, a sixth of a small call."""
+    get = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return get(index) if get is not None else torch.cuda.current_stream(index).cuda_stream
 
 
 def _adr(t):
     return None if t is None else t.data_ptr()
 
 
+_DTYPE_CODES: dict = {}
+
+
 def _dtype_code(dtype, name):
-    import torch
-    code = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}.get(dtype)
+    code = _DTYPE_CODES.get(dtype)
+    if code is None:
+        import torch
+        _DTYPE_CODES.update({torch.bfloat16: 0, torch.float16: 1, torch.float32: 2})
+        code = _DTYPE_CODES.get(dtype)
     if code is None:
         raise TypeError(f"{name} must be bfloat16, float16 or float32, got {dtype}")
     return code
@@ -568,11 +587,12 @@ def _rows_2d(t, name, dtype=None, shape=None, device=None):
     """The row stride of a 2-d tensor whose rows are contiguous."""
     _require(t, name, dtype, 2, device)
     n, h = t.shape
-    if shape is not None and (n, h) != tuple(shape):
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {(n, h)}")
-    if h > 1 and n > 0 and t.stride(1) != 1:
+    if shape is not None and (n, h) != shape:
+        raise ValueError(f"{name} must have shape {shape}, got {(n, h)}")
+    ld, step = t.stride()
+    if step != 1 and h > 1 and n > 0:
         raise ValueError(f"{name} rows must be contiguous (stride(1) == 1)")
-    return t.stride(0) if n > 1 else h
+    return ld if n > 1 else h
 
 
 def _status_ptr(status, device):
@@ -602,8 +622,9 @@ def embed_fwd(weight, tokens, *, scale: float = 1.0, ignore_index: int = -100, o
     tokens = _tokens_i32(tokens, dev, ignore_index)
     n = tokens.shape[0]
     if out is None:
-        out = torch.empty((n, h), dtype=weight.dtype, device=dev)
-    ldo = _rows_2d(out, "out", weight.dtype, (n, h), dev)
+        out, ldo = torch.empty((n, h), dtype=weight.dtype, device=dev), h
+    else:
+        ldo = _rows_2d(out, "out", weight.dtype, (n, h), dev)
     _call("embed_fwd", dev, weight.data_ptr(), code, v, h, ldw, tokens.data_ptr(), n,
           ignore_index, scale, out.data_ptr(), ldo, _status_ptr(status, dev))
     return out
@@ -645,10 +666,11 @@ def embed_bwd(grad, tokens, num_embeddings: int, *, scale: float = 1.0, ignore_i
     if grad_weight is None:
         if accumulate:
             raise ValueError("accumulate=True needs an existing grad_weight tensor")
-        grad_weight = torch.empty((v, h), dtype=dtype or grad.dtype, device=dev)
+        grad_weight, ldw = torch.empty((v, h), dtype=dtype or grad.dtype, device=dev), h
     elif dtype is not None and grad_weight.dtype != dtype:
         raise TypeError(f"grad_weight must be {dtype}, got {grad_weight.dtype}")
-    ldw = _rows_2d(grad_weight, "grad_weight", None, (v, h), dev)
+    else:
+        ldw = _rows_2d(grad_weight, "grad_weight", None, (v, h), dev)
     ws = _workspace(embed_workspace_size(n, h, v), dev, workspace)
     _call("embed_bwd", dev, grad.data_ptr(), code, ldg, tokens.data_ptr(), n, h, v, ignore_index,
           scale, EMBED_ACCUMULATE if accumulate else 0, grad_weight.data_ptr(),
@@ -684,8 +706,9 @@ def layernorm_fwd(x, weight=None, bias=None, *, eps: float = 1e-5, out=None,
             raise TypeError(f"bias is {bias.dtype}, weight {pdtype}: they must be of one type")
         pdtype = bias.dtype
     if out is None:
-        out = torch.empty((n, h), dtype=x.dtype, device=dev)
-    ldy = _rows_2d(out, "out", x.dtype, (n, h), dev)
+        out, ldy = torch.empty((n, h), dtype=x.dtype, device=dev), h
+    else:
+        ldy = _rows_2d(out, "out", x.dtype, (n, h), dev)
     mean = rstd = None
     if return_stats:
         mean = torch.empty(n, dtype=torch.float32, device=dev)
@@ -739,11 +762,13 @@ def layernorm_bwd(grad, x, mean, rstd, weight=None, *, grad_x=True, grad_weight=
             raise ValueError(f"{name} must be a contiguous [{h}] tensor")
         return spec
 
+    lddx = h
     if grad_x is True:
         grad_x = torch.empty((n, h), dtype=x.dtype, device=dev)
     elif grad_x is False:
         grad_x = None
-    lddx = h if grad_x is None else _rows_2d(grad_x, "grad_x", x.dtype, (n, h), dev)
+    elif grad_x is not None:
+        lddx = _rows_2d(grad_x, "grad_x", x.dtype, (n, h), dev)
     gw, gb = param_out(grad_weight, "grad_weight"), param_out(grad_bias, "grad_bias")
     if gw is not None and gb is not None and gw.dtype != gb.dtype:
         raise TypeError("grad_weight and grad_bias must be of one type")

@@ -89,6 +89,17 @@ __device__ __forceinline__ void store_raw(T* p, raw4 r) {
   *reinterpret_cast<typename Elem<T>::Raw*>(p) = r;
 }
 
+// The same for rows that are read or written once (non-temporal).
+template <class T>
+__device__ __forceinline__ raw4 load_stream(const T* p) {
+  return __builtin_nontemporal_load(reinterpret_cast<const typename Elem<T>::Raw*>(p));
+}
+template <class T>
+__device__ __forceinline__ void store_stream(T* p, raw4 r) {
+  __builtin_nontemporal_store(static_cast<typename Elem<T>::Raw>(r),
+                              reinterpret_cast<typename Elem<T>::Raw*>(p));
+}
+
 // `cnt` elements at p into x (the others 0); cnt >= N: one vector access.
 template <class T, int N>
 __device__ __forceinline__ void load_some(const T* p, int64_t cnt, float (&x)[N]) {

@@ -5,10 +5,12 @@
 //             dx = r · (u − mean(u) − x̂ · mean(u · x̂))            per row
 //             dw (=|+=) Σ_rows g · x̂,   db (=|+=) Σ_rows g
 //
-// Memory-bound: 2 · n · h elements move in the forward, 3 · n · h in the backward. A row lives in
+// Memory-bound: 2 · n · h elements move in the forward ([32768, 8192] bf16: 188 us, 5.7 TB/s; a
+// copy of 2 GiB reaches 4.9), 3 · n · h in the backward ([8192, 4096] bf16: 50 us, 4.0 TB/s,
+// what is left being the partial rows below and the start of each workgroup). A row lives in
 // the registers of WPR wavefronts (at most 32 elements a lane) from its one read to its one
 // write; the mean is known before the squares are summed, so the variance does not cancel. Rows
-// are dealt to a fixed grid. In the backward every lane keeps the columns it owns for all of its
+// are dealt to a fixed grid, each lane loading the next row's vectors before the sums of this. In the backward every lane keeps the columns it owns for all of its
 // rows and adds their dw and db terms in fp32 registers; each workgroup writes one partial row
 // of each, and param_reduce_kernel adds those in workgroup order (no atomics: a result does not
 // change from run to run).
@@ -22,14 +24,44 @@ namespace lce {
 
 namespace {
 
+// Launch shapes, measured on the [32768, 8192] bf16 forward and the [8192, 4096] bf16 and
+// [4099, 2051] fp16 backward: the forward takes rows in workgroups of at least 512 threads with
+// 32 elements a lane (190 us; 256 threads 206, 16 elements 200), the backward in workgroups of
+// at least 256 threads with 16 or 24 (50 and 27 us; 512 threads and 32 elements 55 and 50: its
+// running dw and db take two registers an element, and fewer rows are in flight at once). The
+// backward's grid fills the CUs twice over; each workgroup costs one partial row of dw and of db
+// (grids of 256 / 768: 66 / 52 and 40 / 33 us).
+constexpr int kFwdThreads = 512, kFwdElems = 32;
+constexpr int kBwdThreads = 256, kBwdElems = 16;
+constexpr int64_t kFwdGrid = 2048;
+constexpr int64_t kBwdGrid = 512;
+// A forward of whole vectors that moves more than this passes by the caches (non-temporal loads
+// and stores): 1 GiB takes 188 us so and 199 without, 256 MiB 54 either way, 128 MiB 31 so and
+// 28 without.
+constexpr int64_t kStreamBytes = int64_t(512) << 20;
+
+// Sum over a wavefront, the same bits in every lane. The steps within 16 lanes are data-parallel
+// moves of the VALU and the last two exchange rows of lanes between two registers, so none goes
+// through the LDS permute that a shuffle is: the sums of a row are on its critical path.
+template <int CTRL>
+__device__ __forceinline__ float add_lanes(float x) {
+  const int y = __builtin_amdgcn_update_dpp(0, __float_as_int(x), CTRL, 0xf, 0xf, true);
+  return x + __int_as_float(y);
+}
 __device__ __forceinline__ float wave_sum(float x) {
-#pragma unroll
-  for (int off = 32; off >= 1; off >>= 1) x += __shfl_xor(x, off, 64);
-  return x;
+  x = add_lanes<0xB1>(x);   // lane ^ 1
+  x = add_lanes<0x4E>(x);   // lane ^ 2
+  x = add_lanes<0x141>(x);  // mirrored within 8: the other four
+  x = add_lanes<0x140>(x);  // mirrored within 16: the other eight
+  const auto r = __builtin_amdgcn_permlane16_swap(__float_as_int(x), __float_as_int(x), false, false);
+  x = __int_as_float(r[0]) + __int_as_float(r[1]);
+  const auto h = __builtin_amdgcn_permlane32_swap(__float_as_int(x), __float_as_int(x), false, false);
+  return __int_as_float(h[0]) + __int_as_float(h[1]);
 }
 
-// Threads of a workgroup for rows of WPR wavefronts.
-constexpr int norm_threads(int wpr) { return wpr > 8 ? 64 * wpr : 512; }
+// Threads of a workgroup for rows of WPR wavefronts: several rows side by side where few
+// wavefronts hold one.
+constexpr int norm_threads(int wpr, int least) { return 64 * wpr > least ? 64 * wpr : least; }
 
 // The sums of K values over the WPR wavefronts that share a row, in wavefront order. `red` is
 // used for one reduction at a time: the caller alternates two of them, so that a wavefront that
@@ -55,67 +87,115 @@ __device__ __forceinline__ void row_sums(float (&x)[K], float (*red)[K]) {
   }
 }
 
-template <class T, class P, int WPR, int EPL>
-__global__ void __launch_bounds__(norm_threads(WPR)) layernorm_fwd_kernel(
-    const T* x, int64_t n, int64_t h, int64_t ldx, const P* __restrict__ weight,
+// The vectors a lane owns of a row of h elements: vector j starts at column at[j], and its
+// elements from skip[j] on are the lane's to count (none where the vector lies past the row).
+// Where h is no multiple of the vector, the row's last vector is moved back to end with the row
+// and skips what the one before it holds (both lanes compute and store the same values there), so
+// that every access is a whole vector; a vector past the row reads the row's first and is not
+// stored. FULL: h is a multiple of the vector, a vector counts wholly or not at all.
+template <int VE, int NV, int LANES, bool FULL>
+struct Columns {
+  int h, at[NV], skip[NV];
+  __device__ __forceinline__ Columns(int lane, int h_) : h(h_) {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int c = (lane + j * LANES) * VE;
+      at[j] = c >= h ? 0 : c + VE <= h ? c : h < VE ? 0 : h - VE;
+      skip[j] = c >= h ? VE : c - at[j];
+    }
+  }
+  __device__ __forceinline__ bool live(int j) const { return skip[j] < VE; }
+  __device__ __forceinline__ bool counts(int j, int q) const {
+    return FULL ? skip[j] == 0 : q >= skip[j] && q < h;
+  }
+  template <bool STREAM = false, class T>
+  __device__ __forceinline__ raw4 load(const T* row, int j) const {
+    if (!FULL && h < VE) {  // a row shorter than a vector, uniformly
+      float x[VE];
+#pragma unroll
+      for (int q = 0; q < VE; ++q) x[q] = q < h ? Elem<T>::to_f32(row[q]) : 0.f;
+      return Elem<T>::pack(x);
+    }
+    return STREAM ? load_stream(row + at[j]) : load_raw(row + at[j]);
+  }
+  template <bool STREAM = false, class T>
+  __device__ __forceinline__ void store(T* row, int j, const float (&x)[VE]) const {
+    if (!FULL && h < VE) {
+#pragma unroll
+      for (int q = 0; q < VE; ++q)
+        if (q < h) row[q] = Elem<T>::from_f32(x[q]);
+    } else {
+      if (STREAM)
+        store_stream(row + at[j], Elem<T>::pack(x));
+      else
+        store_raw(row + at[j], Elem<T>::pack(x));
+    }
+  }
+  // A parameter at the lane's columns, `none` where there is none.
+  template <class P>
+  __device__ __forceinline__ void param(const P* p, int j, float none, float (&x)[VE]) const {
+    if (p) {
+      load_some<P, VE>(p + at[j], !FULL && h < VE ? h : VE, x);
+    } else {
+#pragma unroll
+      for (int q = 0; q < VE; ++q) x[q] = none;
+    }
+  }
+};
+
+template <class T, class P, int WPR, int EPL, bool FULL, bool STREAM>
+__global__ void __launch_bounds__(norm_threads(WPR, kFwdThreads)) layernorm_fwd_kernel(
+    const T* x, int64_t n, int h, int64_t ldx, const P* __restrict__ weight,
     const P* __restrict__ bias, float eps, T* y, int64_t ldy, float* __restrict__ mean_out,
     float* __restrict__ rstd_out) {
   // x and y may be the same rows: a row is in registers before any of it is written
-  constexpr int VE = Elem<T>::kVec, NV = EPL / VE, RG = norm_threads(WPR) / (64 * WPR);
-  __shared__ float red[2][norm_threads(WPR) / 64][1];
+  constexpr int VE = Elem<T>::kVec, NV = EPL / VE, RG = norm_threads(WPR, kFwdThreads) / (64 * WPR);
+  __shared__ float red[2][norm_threads(WPR, kFwdThreads) / 64][1];
   const int lane = threadIdx.x % (64 * WPR), group = threadIdx.x / (64 * WPR);
   const float fh = float(h);
-  for (int64_t base = int64_t(blockIdx.x) * RG; base < n; base += int64_t(gridDim.x) * RG) {
-    const int64_t r = base + group;
-    const bool live = r < n;
-    const T* xr = x + (live ? r : 0) * ldx;
+  const Columns<VE, NV, 64 * WPR, FULL> col(lane, h);
+  const int64_t step = int64_t(gridDim.x) * RG;
+  int64_t r = int64_t(blockIdx.x) * RG + group;
+  raw4 next[NV];  // the row after the one being worked on
+#pragma unroll
+  for (int j = 0; j < NV; ++j) next[j] = col.template load<STREAM>(x + (r < n ? r : 0) * ldx, j);
+  for (int64_t base = int64_t(blockIdx.x) * RG; base < n; base += step, r += step) {
     float v[NV][VE];
     float s[1] = {0.f};
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int64_t c = int64_t(lane + j * 64 * WPR) * VE;
-      if (c < h) {
-        load_some<T, VE>(xr + c, h - c, v[j]);
-      } else {
+    for (int j = 0; j < NV; ++j) Elem<T>::unpack(next[j], v[j]);
+    if (base + step < n) {
+      const T* xn = x + (r + step < n ? r + step : 0) * ldx;
 #pragma unroll
-        for (int q = 0; q < VE; ++q) v[j][q] = 0.f;
-      }
+      for (int j = 0; j < NV; ++j) next[j] = col.template load<STREAM>(xn, j);
     }
 #pragma unroll
     for (int j = 0; j < NV; ++j)
 #pragma unroll
-      for (int q = 0; q < VE; ++q) s[0] += v[j][q];
+      for (int q = 0; q < VE; ++q) s[0] += col.counts(j, q) ? v[j][q] : 0.f;
     row_sums<WPR, 1>(s, red[0]);
     const float mean = s[0] / fh;  // divided, not multiplied by 1 / h: exact for a constant row
     float ss[1] = {0.f};
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int64_t c = int64_t(lane + j * 64 * WPR) * VE;
+    for (int j = 0; j < NV; ++j)
 #pragma unroll
       for (int q = 0; q < VE; ++q) {
         v[j][q] -= mean;
-        if (c + q < h) ss[0] += v[j][q] * v[j][q];
+        ss[0] += col.counts(j, q) ? v[j][q] * v[j][q] : 0.f;
       }
-    }
     row_sums<WPR, 1>(ss, red[1]);
     const float rstd = 1.f / sqrtf(ss[0] / fh + eps);
-    if (!live) continue;
+    if (r >= n) continue;
     T* yr = y + r * ldy;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int64_t c = int64_t(lane + j * 64 * WPR) * VE;
-      if (c >= h) continue;
+      if (!col.live(j)) continue;
       float w[VE], b[VE];
-#pragma unroll
-      for (int q = 0; q < VE; ++q) {
-        w[q] = 1.f;
-        b[q] = 0.f;
-      }
-      if (weight) load_some<P, VE>(weight + c, h - c, w);
-      if (bias) load_some<P, VE>(bias + c, h - c, b);
+      col.param(weight, j, 1.f, w);
+      col.param(bias, j, 0.f, b);
 #pragma unroll
       for (int q = 0; q < VE; ++q) w[q] = v[j][q] * rstd * w[q] + b[q];
-      store_some<T, VE>(yr + c, h - c, w);
+      col.template store<STREAM>(yr, j, w);
     }
     if (lane == 0) {
       if (mean_out) mean_out[r] = mean;
@@ -124,49 +204,58 @@ __global__ void __launch_bounds__(norm_threads(WPR)) layernorm_fwd_kernel(
   }
 }
 
-template <class T, class P, int WPR, int EPL>
-__global__ void __launch_bounds__(norm_threads(WPR)) layernorm_bwd_kernel(
+template <class T, class P, int WPR, int EPL, bool FULL>
+__global__ void __launch_bounds__(norm_threads(WPR, kBwdThreads)) layernorm_bwd_kernel(
     const T* g, int64_t ldg, const T* __restrict__ x, int64_t ldx, const float* __restrict__ mean,
-    const float* __restrict__ rstd, const P* __restrict__ weight, int64_t n, int64_t h, T* dx,
+    const float* __restrict__ rstd, const P* __restrict__ weight, int64_t n, int h, T* dx,
     int64_t lddx, float* __restrict__ part_w, float* __restrict__ part_b) {
   // g and dx may be the same rows, as x and y in the forward
-  constexpr int VE = Elem<T>::kVec, NV = EPL / VE, RG = norm_threads(WPR) / (64 * WPR);
-  __shared__ float red[2][norm_threads(WPR) / 64][2];
+  constexpr int VE = Elem<T>::kVec, NV = EPL / VE, RG = norm_threads(WPR, kBwdThreads) / (64 * WPR);
+  __shared__ float red[2][norm_threads(WPR, kBwdThreads) / 64][2];
   const int lane = threadIdx.x % (64 * WPR), group = threadIdx.x / (64 * WPR);
   const float inv_h = 1.f / float(h);
+  const Columns<VE, NV, 64 * WPR, FULL> col(lane, h);
   float dw[NV][VE] = {}, db[NV][VE] = {};
+  const int64_t step = int64_t(gridDim.x) * RG;
+  int64_t r = int64_t(blockIdx.x) * RG + group;
+  raw4 nx[NV], ng[NV];  // the row after the one being worked on
+  float nmu, nrs;
+  auto fetch = [&](int64_t row) {
+    row = row < n ? row : 0;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) nx[j] = col.load(x + row * ldx, j);
+#pragma unroll
+    for (int j = 0; j < NV; ++j) ng[j] = col.load(g + row * ldg, j);
+    nmu = mean[row];
+    nrs = rstd[row];
+  };
+  fetch(r);
   int parity = 0;
-  for (int64_t base = int64_t(blockIdx.x) * RG; base < n; base += int64_t(gridDim.x) * RG) {
-    const int64_t r = base + group;
+  for (int64_t base = int64_t(blockIdx.x) * RG; base < n; base += step, r += step) {
     const bool live = r < n;
-    const float mu = live ? mean[r] : 0.f, rs = live ? rstd[r] : 0.f;
+    const float mu = nmu, rs = nrs;
     float xh[NV][VE], u[NV][VE];
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int64_t c = int64_t(lane + j * 64 * WPR) * VE;
-#pragma unroll
-      for (int q = 0; q < VE; ++q) xh[j][q] = u[j][q] = 0.f;
-      if (live && c < h) {
-        load_some<T, VE>(x + r * ldx + c, h - c, xh[j]);
-        load_some<T, VE>(g + r * ldg + c, h - c, u[j]);
-      }
+      Elem<T>::unpack(nx[j], xh[j]);
+      Elem<T>::unpack(ng[j], u[j]);
     }
+    if (base + step < n) fetch(r + step);
     float s[2] = {0.f, 0.f};
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int64_t c = int64_t(lane + j * 64 * WPR) * VE;
       float w[VE];
-#pragma unroll
-      for (int q = 0; q < VE; ++q) w[q] = 1.f;
-      if (weight && c < h) load_some<P, VE>(weight + c, h - c, w);
+      col.param(weight, j, 1.f, w);
 #pragma unroll
       for (int q = 0; q < VE; ++q) {
         xh[j][q] = (xh[j][q] - mu) * rs;
-        dw[j][q] += u[j][q] * xh[j][q];
-        db[j][q] += u[j][q];
+        if (live) {
+          dw[j][q] += u[j][q] * xh[j][q];
+          db[j][q] += u[j][q];
+        }
         u[j][q] *= w[q];
-        s[0] += u[j][q];
-        s[1] += u[j][q] * xh[j][q];
+        s[0] += col.counts(j, q) ? u[j][q] : 0.f;
+        s[1] += col.counts(j, q) ? u[j][q] * xh[j][q] : 0.f;
       }
     }
     row_sums<WPR, 2>(s, red[parity]);
@@ -175,11 +264,10 @@ __global__ void __launch_bounds__(norm_threads(WPR)) layernorm_bwd_kernel(
     const float a = s[0] * inv_h, b = s[1] * inv_h;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int64_t c = int64_t(lane + j * 64 * WPR) * VE;
-      if (c >= h) continue;
+      if (!col.live(j)) continue;
 #pragma unroll
       for (int q = 0; q < VE; ++q) u[j][q] = rs * (u[j][q] - a - xh[j][q] * b);
-      store_some<T, VE>(dx + r * lddx + c, h - c, u[j]);
+      col.store(dx + r * lddx, j, u[j]);
     }
   }
   if (!part_w) return;
@@ -191,21 +279,28 @@ __global__ void __launch_bounds__(norm_threads(WPR)) layernorm_bwd_kernel(
     if (group != k) continue;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int64_t c = int64_t(lane + j * 64 * WPR) * VE;
-      if (c >= h) continue;
-      float t[VE];
-      if (k > 0) {
+      if (col.skip[j] == 0 && (FULL || h >= VE)) {
+        float* p[2] = {pw + col.at[j], pb + col.at[j]};
 #pragma unroll
-        for (int q = 0; q < VE; ++q) t[q] = c + q < h ? pw[c + q] : 0.f;
+        for (int t = 0; t < 2; ++t) {
+          float(&d)[VE] = t ? db[j] : dw[j];
+          if (k > 0) {
+            float old[VE];
+            load_some<float, VE>(p[t], VE, old);
 #pragma unroll
-        for (int q = 0; q < VE; ++q) dw[j][q] += t[q];
+            for (int q = 0; q < VE; ++q) d[q] += old[q];
+          }
+          store_some<float, VE>(p[t], VE, d);
+        }
+      } else if (!FULL && col.live(j)) {  // the row's last vector, or a row shorter than one
 #pragma unroll
-        for (int q = 0; q < VE; ++q) t[q] = c + q < h ? pb[c + q] : 0.f;
-#pragma unroll
-        for (int q = 0; q < VE; ++q) db[j][q] += t[q];
+        for (int q = 0; q < VE; ++q) {
+          if (!col.counts(j, q)) continue;
+          const int c = col.at[j] + q;
+          pw[c] = k > 0 ? pw[c] + dw[j][q] : dw[j][q];
+          pb[c] = k > 0 ? pb[c] + db[j][q] : db[j][q];
+        }
       }
-      store_some<float, VE>(pw + c, h - c, dw[j]);
-      store_some<float, VE>(pb + c, h - c, db[j]);
     }
   }
 }
@@ -239,36 +334,58 @@ __global__ void __launch_bounds__(kRedCols* kRedGroups) param_reduce_kernel(
   }
 }
 
-constexpr int64_t kFwdGrid = 2048;  // workgroups the forward's rows are dealt to
-constexpr int64_t kBwdGrid = 256;   // workgroups of the backward: one partial row each
-
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
-// Calls f with the row shape (WPR, EPL) for rows of h elements: 32 elements a lane, fewer where
-// one wavefront holds the row with fewer; wavefronts per row doubled until the row fits.
-template <class F>
+// Calls f with the row shape (WPR, EPL) for rows of h elements: up to E elements a lane, fewer
+// where one wavefront holds the row with fewer; wavefronts per row doubled until the row fits.
+// For E = 16, rows that leave a quarter or more of the next shape empty take half the wavefronts
+// with 24 elements a lane. Rows past 1024 · E take 32.
+template <int E, class F>
 hipError_t with_shape(int64_t h, F&& f) {
   using std::integral_constant;
-  if (h <= 512) return f(integral_constant<int, 1>{}, integral_constant<int, 8>{});
-  if (h <= 1024) return f(integral_constant<int, 1>{}, integral_constant<int, 16>{});
-  if (h <= 2048) return f(integral_constant<int, 1>{}, integral_constant<int, 32>{});
-  if (h <= 4096) return f(integral_constant<int, 2>{}, integral_constant<int, 32>{});
-  if (h <= 8192) return f(integral_constant<int, 4>{}, integral_constant<int, 32>{});
-  if (h <= 16384) return f(integral_constant<int, 8>{}, integral_constant<int, 32>{});
-  return f(integral_constant<int, 16>{}, integral_constant<int, 32>{});
+  using W1 = integral_constant<int, 1>;
+  using W2 = integral_constant<int, 2>;
+  using W4 = integral_constant<int, 4>;
+  using W8 = integral_constant<int, 8>;
+  using W16 = integral_constant<int, 16>;
+  using EE = integral_constant<int, E>;
+  using E24 = integral_constant<int, 24>;
+  if (h <= 512) return f(W1{}, integral_constant<int, 8>{});
+  if (h <= 1024) return f(W1{}, integral_constant<int, 16>{});
+  if (E > 16 && h <= 64 * E) return f(W1{}, EE{});
+  if constexpr (E == 16) {
+    if (h <= 64 * 24) return f(W1{}, E24{});
+    if (h <= 128 * 16) return f(W2{}, EE{});
+    if (h <= 128 * 24) return f(W2{}, E24{});
+    if (h <= 256 * 16) return f(W4{}, EE{});
+    if (h <= 256 * 24) return f(W4{}, E24{});
+  }
+  if (h <= 128 * E) return f(W2{}, EE{});
+  if (h <= 256 * E) return f(W4{}, EE{});
+  if (h <= 512 * E) return f(W8{}, EE{});
+  if (h <= 1024 * E) return f(W16{}, EE{});
+  return f(W16{}, integral_constant<int, 32>{});
 }
 
 template <class T, class P>
 hipError_t run_fwd(const NormFwdArgs& a, hipStream_t s) {
-  return with_shape(a.h, [&](auto wpr, auto epl) {
+  return with_shape<kFwdElems>(a.h, [&](auto wpr, auto epl) {
     constexpr int WPR = decltype(wpr)::value, EPL = decltype(epl)::value;
-    constexpr int RG = norm_threads(WPR) / (64 * WPR);
+    constexpr int RG = norm_threads(WPR, kFwdThreads) / (64 * WPR);
     const int64_t grid = std::min<int64_t>((a.n + RG - 1) / RG, kFwdGrid);
     TimedLaunch t(s, K_NORM_FWD);
-    hipLaunchKernelGGL((layernorm_fwd_kernel<T, P, WPR, EPL>), dim3(unsigned(grid)),
-                       dim3(norm_threads(WPR)), 0, s, static_cast<const T*>(a.x), a.n, a.h, a.ldx,
-                       static_cast<const P*>(a.weight), static_cast<const P*>(a.bias), a.eps,
-                       static_cast<T*>(a.y), a.ldy, a.mean_out, a.rstd_out);
+    auto launch = [&](auto kernel) {
+      hipLaunchKernelGGL(kernel, dim3(unsigned(grid)), dim3(norm_threads(WPR, kFwdThreads)), 0, s,
+                         static_cast<const T*>(a.x), a.n, int(a.h), a.ldx,
+                         static_cast<const P*>(a.weight), static_cast<const P*>(a.bias), a.eps,
+                         static_cast<T*>(a.y), a.ldy, a.mean_out, a.rstd_out);
+    };
+    if (a.h % Elem<T>::kVec != 0)
+      launch(layernorm_fwd_kernel<T, P, WPR, EPL, false, false>);
+    else if (2 * a.n * a.h * int64_t(sizeof(T)) <= kStreamBytes)
+      launch(layernorm_fwd_kernel<T, P, WPR, EPL, true, false>);
+    else
+      launch(layernorm_fwd_kernel<T, P, WPR, EPL, true, true>);
     return hipGetLastError();
   });
 }
@@ -276,18 +393,23 @@ hipError_t run_fwd(const NormFwdArgs& a, hipStream_t s) {
 template <class T, class P>
 hipError_t run_bwd_rows(const NormBwdArgs& a, float* part_w, float* part_b, int64_t* rows,
                         hipStream_t s) {
-  return with_shape(a.h, [&](auto wpr, auto epl) {
+  return with_shape<kBwdElems>(a.h, [&](auto wpr, auto epl) {
     constexpr int WPR = decltype(wpr)::value, EPL = decltype(epl)::value;
-    constexpr int RG = norm_threads(WPR) / (64 * WPR);
+    constexpr int RG = norm_threads(WPR, kBwdThreads) / (64 * WPR);
     const int64_t grid = std::min<int64_t>((a.n + RG - 1) / RG, kBwdGrid);
     *rows = grid;
     if (grid == 0) return hipSuccess;
     TimedLaunch t(s, K_NORM_BWD);
-    hipLaunchKernelGGL((layernorm_bwd_kernel<T, P, WPR, EPL>), dim3(unsigned(grid)),
-                       dim3(norm_threads(WPR)), 0, s, static_cast<const T*>(a.grad), a.ldg,
-                       static_cast<const T*>(a.x), a.ldx, a.mean, a.rstd,
-                       static_cast<const P*>(a.weight), a.n, a.h, static_cast<T*>(a.grad_x),
-                       a.lddx, part_w, part_b);
+    auto launch = [&](auto kernel) {
+      hipLaunchKernelGGL(kernel, dim3(unsigned(grid)), dim3(norm_threads(WPR, kBwdThreads)), 0, s,
+                         static_cast<const T*>(a.grad), a.ldg, static_cast<const T*>(a.x), a.ldx,
+                         a.mean, a.rstd, static_cast<const P*>(a.weight), a.n, int(a.h),
+                         static_cast<T*>(a.grad_x), a.lddx, part_w, part_b);
+    };
+    if (a.h % Elem<T>::kVec == 0)
+      launch(layernorm_bwd_kernel<T, P, WPR, EPL, true>);
+    else
+      launch(layernorm_bwd_kernel<T, P, WPR, EPL, false>);
     return hipGetLastError();
   });
 }

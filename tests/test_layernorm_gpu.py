@@ -83,6 +83,19 @@ def test_forward_many_rows_and_offset(dev):
     check_forward(x, w, b, *lce.layernorm_fwd(x, w, b, eps=EPS))
 
 
+def test_forward_past_the_caches(dev):
+    """More than 512 MiB of rows: non-temporal loads and stores, and offsets past 2^31 bytes."""
+    for dtype, n, h in ((torch.float32, 17000, 4096), (torch.bfloat16, 140000, 8192)):
+        x, w, b, _ = inputs(64, h, dtype, dtype, dev)
+        many = x.repeat(n // 64 + 1, 1)[:n]
+        y, mean, rstd = lce.layernorm_fwd(many, w, b, eps=EPS)
+        check_forward(x, w, b, y[:64], mean[:64], rstd[:64])
+        whole = n // 64 * 64
+        assert torch.equal(y[:whole].view(-1, 64, h), y[:64].expand(n // 64, 64, h))
+        assert torch.equal(y[whole:], y[:n - whole])
+        assert torch.equal(mean[:whole].view(-1, 64), mean[:64].expand(n // 64, 64))
+
+
 def test_forward_without_parameters_strided_and_in_place(dev):
     for dtype in DTYPES:
         x, w, b, _ = inputs(37, 300, dtype, dtype, dev)
