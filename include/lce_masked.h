@@ -384,7 +384,7 @@ int embed_fwd(const void* weight, int dtype, int64_t v, int64_t h, int64_t ldw,
 /* flags of embed_bwd */
 #define EMBED_ACCUMULATE         1u /* add into grad_weight instead of overwriting it            */
 
-/* Workspace bytes of embed_bwd: the positions sorted by token (twice past 8192 of them) and the
+/* Workspace bytes of embed_bwd: the positions sorted by token (twice past 2048 of them) and the
  * partial sums of tokens whose rows are added in several places. Host-only. */
 int embed_workspace_size(int64_t n, int64_t h, int64_t v, size_t* bytes);
 
