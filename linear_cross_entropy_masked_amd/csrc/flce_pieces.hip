@@ -198,12 +198,12 @@ __global__ void __launch_bounds__(256) pad_rows_kernel(const uint16_t* __restric
 
 // ------------------------------------------------------------------ forward
 
+// bias[n .. n + 3], the last class's past the end (those columns are not used).
 __device__ __forceinline__ f32x4_t bias4(const float* bias, int64_t n, int64_t v) {
   f32x4_t b{0.f, 0.f, 0.f, 0.f};
   if (bias) {
 #pragma unroll
-    for (int q = 0; q < 4; ++q)
-      if (n + q < v) b[q] = bias[n + q];
+    for (int q = 0; q < 4; ++q) b[q] = bias[n + q < v ? n + q : v - 1];
   }
   return b;
 }
@@ -211,7 +211,7 @@ __device__ __forceinline__ f32x4_t bias4(const float* bias, int64_t n, int64_t v
 // The logits tile reduced to each row's (max, Σ exp(z − max)), and the label's logit.
 struct EpiPieceLse {
   static constexpr bool kRowStats = true, kColSums = false, kTileMax = false, kRowTag = true;
-  static constexpr bool kRowLimit = true;
+  static constexpr bool kRowLimit = true, kColAux = true;
   const float* bias;
   int64_t v;
   const int32_t* ylab;
@@ -219,32 +219,24 @@ struct EpiPieceLse {
   float2* part;
   int64_t tiles;
   float* zy;
+  using Col = f32x4_t;
   struct Aux {
-    f32x4_t b;
     int y;
   };
   __device__ void begin(int64_t) {}
   __device__ __forceinline__ int64_t row_limit() const { return *count; }
   __device__ __forceinline__ int row_tag(int64_t m) const { return ylab[m]; }
-  __device__ __forceinline__ Aux load4(int64_t, int64_t n) const { return {bias4(bias, n, v), -1}; }
-  __device__ __forceinline__ Aux load4t(int64_t, int64_t n, int y) const {
-    return {bias4(bias, n, v), y};
-  }
-  __device__ __forceinline__ f32x4_t value4(f32x4_t a, const Aux& x) const {
-    f32x4_t z = a + x.b;
-#pragma unroll
-    for (int q = 0; q < 4; ++q) z[q] = finite_low(z[q]);
-    return z;
-  }
+  __device__ __forceinline__ Col load_col(int64_t n) const { return bias4(bias, n, v); }
+  __device__ __forceinline__ Aux load4t(int64_t, int64_t, int y) const { return {y}; }
+  __device__ __forceinline__ f32x4_t value4c(f32x4_t a, Col b) const { return a + b; }
   __device__ __forceinline__ float value1(int64_t n, float a) const {
-    return finite_low(bias ? a + bias[n] : a);
+    return bias ? a + bias[n] : a;
   }
-  __device__ __forceinline__ void store4(int64_t m, int64_t n, f32x4_t a, const Aux& x) {
-    const int64_t d = int64_t(x.y) - n;
-    if (x.y >= 0 && d >= 0 && d < 4) {
-      const f32x4_t z = a + x.b;
-      zy[m] = d == 0 ? z[0] : d == 1 ? z[1] : d == 2 ? z[2] : z[3];
-    }
+  __device__ __forceinline__ f32x4_t store4c(int64_t m, int64_t n, f32x4_t a, Aux x, Col b) {
+    const unsigned d = unsigned(x.y) - unsigned(n);
+    const f32x4_t z = a + b;
+    if (d < 4) zy[m] = d == 0 ? z[0] : d == 1 ? z[1] : d == 2 ? z[2] : z[3];
+    return z;
   }
   __device__ __forceinline__ void operator()(int64_t m, int64_t n, float a) {
     if (int64_t(ylab[m]) == n) zy[m] = bias ? a + bias[n] : a;
@@ -485,7 +477,7 @@ __global__ void __launch_bounds__(256) loss_terms_kernel(LossArgs a, float* __re
 template <bool BIAS, bool ROWS>
 struct EpiPieceGrad {
   static constexpr bool kRowStats = false, kColSums = BIAS, kTileMax = false, kRowTag = true;
-  static constexpr bool kRowLimit = true;
+  static constexpr bool kRowLimit = true, kColAux = true;
   uint16_t* d;
   int64_t np;
   const float* bias;
@@ -496,35 +488,38 @@ struct EpiPieceGrad {
   const float* coef;
   float* colsum;
   int64_t v64;
+  using Col = f32x4_t;
   struct Aux {
-    f32x4_t b;
     float lse, c;
     int y;
   };
   __device__ void begin(int64_t) {}
   __device__ __forceinline__ int64_t row_limit() const { return *count; }
   __device__ __forceinline__ int row_tag(int64_t m) const { return ylab[m]; }
-  __device__ __forceinline__ Aux load4t(int64_t m, int64_t n, int y) const {
-    return {bias4(bias, n, v), lse[m], ROWS ? coef[m] : 1.f, y};
+  // past the last class: a bias that makes the exponential 0
+  __device__ __forceinline__ Col load_col(int64_t n) const {
+    Col b = bias4(bias, n, v);
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      if (n + q >= v) b[q] = -INFINITY;
+    return b;
   }
-  __device__ __forceinline__ f32x4_t colvalue4(f32x4_t a, const Aux& x, int64_t n) const {
+  __device__ __forceinline__ Aux load4t(int64_t m, int64_t, int y) const {
+    return {lse[m], ROWS ? coef[m] : 1.f, y};
+  }
+  __device__ __forceinline__ f32x4_t store4c(int64_t m, int64_t n, f32x4_t a, const Aux& x, Col b) {
+    const unsigned at = unsigned(x.y) - unsigned(n);
     f32x4_t r;
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-      float p = fast_exp2(((a[q] + x.b[q]) - x.lse) * kLog2e);
-      if (int64_t(x.y) == n + q) p -= 1.f;
-      if (ROWS) p *= x.c;
-      r[q] = n + q < v ? p : 0.f;
+      r[q] = fast_exp2(((a[q] + b[q]) - x.lse) * kLog2e);
+      if (at == unsigned(q)) r[q] -= 1.f;
+      if (ROWS) r[q] *= x.c;
     }
-    return r;
-  }
-  __device__ __forceinline__ void store4(int64_t m, int64_t n, f32x4_t a, Aux& x) {
-    const f32x4_t r = colvalue4(a, x, n);
     *reinterpret_cast<uint2*>(d + (n >> 6) * np * 64 + m * 64 + (n & 63)) =
         uint2{pack_bf16x2(r[0], r[1]), pack_bf16x2(r[2], r[3])};
-    x.b = r;  // for the column sums
+    return r;
   }
-  __device__ __forceinline__ f32x4_t colvalue4(f32x4_t, const Aux& x) const { return x.b; }
   __device__ __forceinline__ void operator()(int64_t, int64_t, float) {}  // N % 4 == 0: unused
   __device__ __forceinline__ void col_sums(int64_t mt, int64_t n, float sum) {
     colsum[mt * v64 + n] = sum;

@@ -542,8 +542,9 @@ struct RowTagged<E, std::void_t<decltype(E::kRowTag)>> {
 };
 
 // Epilogues that set kRowLimit hold the number of output rows that count in device memory
-// (row_limit(), at most M): tiles wholly past it are skipped. Those that set kKLimit hold the
-// length of the contraction there (k_limit(), at most K).
+// (row_limit(), at most M): the tile order is that of a product with so many rows, and the
+// workgroups left over end at once. Those that set kKLimit hold the length of the contraction
+// there (k_limit(), at most K).
 template <class E, class = void>
 struct RowLimited {
   static constexpr bool value = false;
@@ -559,6 +560,22 @@ struct KLimited {
 template <class E>
 struct KLimited<E, std::void_t<decltype(E::kKLimit)>> {
   static constexpr bool value = E::kKLimit;
+};
+
+// Epilogues that set kColAux get what depends on the column alone (e.g. the bias) loaded once
+// per tile, as load_col(n) for the 4 columns from n: value4c(a, col) in place of value4, and
+// store4c(m, n, a, aux, col), which returns the 4 values that kColSums adds up. Their row
+// statistics are taken about at least the lowest finite number, so that a tile whose values are
+// all minus infinity leaves the sum 0.
+template <class E, class = void>
+struct ColAux {
+  static constexpr bool value = false;
+  struct Col {};
+};
+template <class E>
+struct ColAux<E, std::void_t<decltype(E::kColAux)>> {
+  static constexpr bool value = true;
+  using Col = typename E::Col;
 };
 
 // Tile coordinates (m-tile, n-tile, K split) of workgroup w; false for a workgroup with no
@@ -694,6 +711,15 @@ __device__ __forceinline__ void run_tile(const View& A, const View& B, int64_t M
       if (gm < M) rtag[i] = epi.row_tag(gm);
     }
   }
+  constexpr bool kCols = ColAux<Epi>::value;
+  typename ColAux<Epi>::Col col[TN];
+  if constexpr (kCols) {
+#pragma unroll
+    for (int j = 0; j < TN; ++j) {
+      const int64_t gn = n0 + wn * (C::BN / C::WN) + 16 * j + 4 * (lane >> 4);
+      if (gn + 4 <= N) col[j] = epi.load_col(gn);
+    }
+  }
   // Each row's maximum over this wavefront's valid columns (the four lanes sharing the row
   // reduced with shuffles): the shift of the row statistics and the start of the tile maximum.
   float wmax[TM];
@@ -709,7 +735,11 @@ __device__ __forceinline__ void run_tile(const View& A, const View& B, int64_t M
         for (int j = 0; j < TN; ++j) {
           const int64_t gn = n0 + wn * (C::BN / C::WN) + 16 * j + 4 * (lane >> 4);
           if (gn + 4 <= N) {
-            const f32x4_t z = epi.value4(acc[i][j], epi.load4(gm, gn));
+            f32x4_t z;
+            if constexpr (kCols)
+              z = epi.value4c(acc[i][j], col[j]);
+            else
+              z = epi.value4(acc[i][j], epi.load4(gm, gn));
             mx = fmaxf(mx, fmaxf(fmaxf(z[0], z[1]), fmaxf(z[2], z[3])));
           } else {
 #pragma unroll
@@ -720,6 +750,7 @@ __device__ __forceinline__ void run_tile(const View& A, const View& B, int64_t M
       }
       mx = fmaxf(mx, __shfl_xor(mx, 16, 64));
       wmax[i] = fmaxf(mx, __shfl_xor(mx, 32, 64));
+      if constexpr (kCols) wmax[i] = fmaxf(wmax[i], -3.4028234663852886e38f);
     }
   }
   if constexpr (Epi::kTileMax) {
@@ -775,14 +806,22 @@ __device__ __forceinline__ void run_tile(const View& A, const View& B, int64_t M
       for (int j = 0; j < TN; ++j) {
         const int64_t gn = n0 + wn * (C::BN / C::WN) + 16 * j + 4 * (lane >> 4);
         if (gn + 4 <= N) {
-          if constexpr (Epi::kTileMax)
+          if constexpr (Epi::kTileMax) {
             epi.store4m(gm, gn, acc[i0 + di][j], aux[di][j], tmax[i0 + di], rtag[i0 + di]);
-          else
+          } else if constexpr (kCols) {
+            const f32x4_t x = epi.store4c(gm, gn, acc[i0 + di][j], aux[di][j], col[j]);
+            if constexpr (Epi::kColSums) cs[j] += x;
+          } else {
             epi.store4(gm, gn, acc[i0 + di][j], aux[di][j]);
-          if constexpr (Epi::kColSums) cs[j] += epi.colvalue4(acc[i0 + di][j], aux[di][j]);
+          }
+          if constexpr (Epi::kColSums && !kCols) cs[j] += epi.colvalue4(acc[i0 + di][j], aux[di][j]);
           if constexpr (Epi::kRowStats) {
             // shift as (z − max) · log2 e: the wavefront's row maximum contributes exactly 1
-            const f32x4_t z = epi.value4(acc[i0 + di][j], aux[di][j]);
+            f32x4_t z;
+            if constexpr (kCols)
+              z = epi.value4c(acc[i0 + di][j], col[j]);
+            else
+              z = epi.value4(acc[i0 + di][j], aux[di][j]);
             const float mw = wmax[i0 + di];
             float t = rs[i0 + di];
 #pragma unroll
@@ -864,10 +903,12 @@ __global__ void __launch_bounds__(C::THREADS, C::OCC)
                      TileMap tm, Epi epi) {
   __shared__ __attribute__((aligned(1024))) char lds[C::LdsBytes];
   TileCoord tc;
-  if (!tile_coord(tm, blockIdx.x, tc)) return;  // uniform over the workgroup
   if constexpr (RowLimited<Epi>::value) {
-    if (tc.mt * C::BM >= epi.row_limit()) return;
+    tm.m_tiles = (epi.row_limit() + C::BM - 1) / C::BM;
+    if (tm.m_tiles < 8) tm.xn = 0;  // too few for a block of tiles per XCD
+    if (tm.xn == 0 && int64_t(blockIdx.x) >= tm.m_tiles * tm.n_tiles * tm.splits) return;
   }
+  if (!tile_coord(tm, blockIdx.x, tc)) return;  // uniform over the workgroup
   if constexpr (KLimited<Epi>::value) {
     const int64_t k = epi.k_limit();
     if (k < K) K = k;
