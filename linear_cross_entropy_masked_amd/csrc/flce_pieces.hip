@@ -12,7 +12,7 @@
 //
 // Rows without a label are left out of every product: piece_rows_kernel numbers the labelled
 // rows, gather_rows_kernel copies their hidden rows together, and the products stop at the
-// count it leaves in device memory. That also keeps whatever such rows hold (NaN in a padded
+// count it leaves in device memory (gather_few_rows_kernel does both at once for short batches). That also keeps whatever such rows hold (NaN in a padded
 // position) out of dW. The copy costs 4 · N · H bytes against 2 · N · H · V flop.
 //
 // D is rounded to bf16 (an MFMA operand) once, unscaled where the loss is summed, so that the
@@ -20,7 +20,8 @@
 // way in every label element. Half a bf16 step per element, as the outputs' own rounding.
 //
 // With at most kScoreRows rows the forward is bound by reading W once, and score_kernel streams
-// it past the rows instead.
+// it past the rows instead; up to kNarrowRows rows take tiles of half the height with three K
+// slices in flight.
 #include <algorithm>
 
 #include "common.h"
@@ -35,11 +36,16 @@ namespace {
 using gemm::View;
 using gemm::f32x4_t;
 using Wide = gemm::v2::CfgWide;
+using Narrow = gemm::v2::Cfg<128, 256, 64, 3, 2, 4, 1>;
 
 __host__ __device__ inline int64_t up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
 
 constexpr int kTile = Wide::BM;  // rows of an output tile; the gathered rows are padded to it
-constexpr int kScoreRows = 64;
+// 32 / 64 rows of 4096 against 128256 classes take 222 / 276 us in the scoring kernel, 32 / 64 / 128
+// rows 221 / 223 / 221 on 128 x 256 tiles and 269 / 271 / 267 on 256 x 256 tiles (20 rows: 204,
+// 229, 275); 256 rows take 284 us on 256 x 256 tiles and 317 on 128 x 256.
+constexpr int kScoreRows = 32;
+constexpr int kNarrowRows = 128;
 
 __device__ __forceinline__ bool labelled(int32_t y, int64_t vocab, int32_t ignore_index) {
   return y != ignore_index && y >= 0 && int64_t(y) < vocab;
@@ -70,14 +76,10 @@ constexpr int kRowsPer = 8;
 __global__ void __launch_bounds__(1024) piece_rows_kernel(
     const int32_t* __restrict__ labels, int64_t n, int64_t v, int64_t v_start, int64_t vocab,
     int32_t ignore_index, int32_t* __restrict__ count, int32_t* __restrict__ cidx,
-    int32_t* __restrict__ row, int32_t* __restrict__ ylab, float* __restrict__ state,
-    int32_t* __restrict__ status) {
+    int32_t* __restrict__ row, int32_t* __restrict__ ylab, float* __restrict__ state) {
   __shared__ int wave_sum[16];
-  __shared__ int any_bad;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  if (threadIdx.x == 0) any_bad = 0;
   int done = 0;
-  bool bad = false;
   for (int64_t base = 0; base < n; base += 1024 * kRowsPer) {
     const int64_t i0 = base + int64_t(threadIdx.x) * kRowsPer;
     int32_t y[kRowsPer];
@@ -85,9 +87,7 @@ __global__ void __launch_bounds__(1024) piece_rows_kernel(
 #pragma unroll
     for (int k = 0; k < kRowsPer; ++k) {
       y[k] = i0 + k < n ? labels[i0 + k] : ignore_index;
-      const bool ok = labelled(y[k], vocab, ignore_index);
-      bad |= !ok && y[k] != ignore_index;
-      mine += ok;
+      mine += labelled(y[k], vocab, ignore_index);
     }
     int upto = mine;  // inclusive sum over the wavefront
 #pragma unroll
@@ -125,20 +125,15 @@ __global__ void __launch_bounds__(1024) piece_rows_kernel(
     }
     done += total;
   }
-  if (status) {
-    __syncthreads();
-    if (bad) any_bad = 1;
-    __syncthreads();
-    if (threadIdx.x == 0) *status = any_bad ? LCE_STATUS_BAD_LABEL : 0;
-  }
   if (threadIdx.x == 0) *count = done;
 }
 
 struct GatherArgs {
   const uint16_t* hidden;
   int64_t n, h, h64;
-  const int32_t* count;
-  const int32_t* cidx;
+  int32_t* count;
+  int32_t* cidx;
+  int32_t* row;
   int32_t* ylab;
   uint16_t* hc;            // [up(n, kTile)][h64]
   // backward only
@@ -150,40 +145,97 @@ struct GatherArgs {
   uint16_t* zero_grad;
 };
 
-// Workgroup i < n: the hidden row of a labelled row to its place, zero-padded to h64 columns;
-// the outputs of a row without a label to 0. Workgroups n .. n + kTile − 1: the rows between the
-// count and the next multiple of the tile, as rows that contribute nothing.
-__global__ void __launch_bounds__(256) gather_rows_kernel(GatherArgs a) {
-  const int64_t i = blockIdx.x;
+// Row i of the batch to its place m: its hidden row, zero-padded to h64 columns.
+__device__ __forceinline__ void gather_row(const GatherArgs& a, int64_t i, int64_t m) {
   const uint4 zero = {0u, 0u, 0u, 0u};
-  if (i >= a.n) {
-    const int64_t count = *a.count, m = count + (i - a.n);
-    if (m >= up(count, kTile)) return;
-    for (int64_t c = 8 * int64_t(threadIdx.x); c < a.h64; c += 8 * 256)
-      *reinterpret_cast<uint4*>(a.hc + m * a.h64 + c) = zero;
-    if (threadIdx.x == 0) {
-      a.ylab[m] = -1;
-      if (a.lse_c) a.lse_c[m] = INFINITY;
-      if (a.coef_c) a.coef_c[m] = 0.f;
-    }
-    return;
-  }
-  const int64_t m = a.cidx[i];
-  if (m < 0) {
-    if (a.zero_acc)
-      for (int64_t c = 4 * int64_t(threadIdx.x); c < a.h; c += 4 * 256)
-        *reinterpret_cast<uint4*>(a.zero_acc + i * a.h + c) = zero;
-    if (a.zero_grad)
-      for (int64_t c = 8 * int64_t(threadIdx.x); c < a.h; c += 8 * 256)
-        *reinterpret_cast<uint4*>(a.zero_grad + i * a.h + c) = zero;
-    return;
-  }
   for (int64_t c = 8 * int64_t(threadIdx.x); c < a.h64; c += 8 * 256)
     *reinterpret_cast<uint4*>(a.hc + m * a.h64 + c) =
         c < a.h ? *reinterpret_cast<const uint4*>(a.hidden + i * a.h + c) : zero;
   if (threadIdx.x == 0) {
     if (a.lse_c) a.lse_c[m] = a.lse[i];
     if (a.coef_c) a.coef_c[m] = a.grad_rows[i];
+  }
+}
+// The outputs of a row without a label.
+__device__ __forceinline__ void clear_row(const GatherArgs& a, int64_t i) {
+  const uint4 zero = {0u, 0u, 0u, 0u};
+  if (a.zero_acc)
+    for (int64_t c = 4 * int64_t(threadIdx.x); c < a.h; c += 4 * 256)
+      *reinterpret_cast<uint4*>(a.zero_acc + i * a.h + c) = zero;
+  if (a.zero_grad)
+    for (int64_t c = 8 * int64_t(threadIdx.x); c < a.h; c += 8 * 256)
+      *reinterpret_cast<uint4*>(a.zero_grad + i * a.h + c) = zero;
+}
+// Row m past the count, up to the next multiple of the tile: one that contributes nothing.
+__device__ __forceinline__ void pad_row(const GatherArgs& a, int64_t m, int64_t count) {
+  if (m >= up(count, kTile)) return;
+  for (int64_t c = 8 * int64_t(threadIdx.x); c < a.h64; c += 8 * 256)
+    *reinterpret_cast<uint4*>(a.hc + m * a.h64 + c) = uint4{0u, 0u, 0u, 0u};
+  if (threadIdx.x == 0) {
+    a.ylab[m] = -1;
+    if (a.lse_c) a.lse_c[m] = INFINITY;
+    if (a.coef_c) a.coef_c[m] = 0.f;
+  }
+}
+
+// One workgroup per row of the batch, numbered by piece_rows_kernel, then kTile for the padding.
+__global__ void __launch_bounds__(256) gather_rows_kernel(GatherArgs a) {
+  const int64_t i = blockIdx.x;
+  if (i >= a.n) {
+    const int64_t count = *a.count;
+    pad_row(a, count + (i - a.n), count);
+    return;
+  }
+  const int64_t m = a.cidx[i];
+  if (m >= 0)
+    gather_row(a, i, m);
+  else
+    clear_row(a, i);
+}
+
+// Numbering and gathering in one launch, for batches short enough that every workgroup can count
+// the labelled rows before its own: kFewEach rows per workgroup.
+constexpr int64_t kFewRows = 8192;
+constexpr int kFewEach = 8;
+__global__ void __launch_bounds__(256) gather_few_rows_kernel(
+    GatherArgs a, const int32_t* __restrict__ labels, int64_t v, int64_t v_start, int64_t vocab,
+    int32_t ignore_index, float* __restrict__ state) {
+  const int64_t batch = (a.n + kFewEach - 1) / kFewEach;
+  const bool padding = int64_t(blockIdx.x) >= batch;
+  const int64_t i0 = padding ? a.n : int64_t(blockIdx.x) * kFewEach;
+  int before = 0;
+  for (int64_t j = threadIdx.x; j < i0; j += 256)
+    before += labelled(labels[j], vocab, ignore_index);
+#pragma unroll
+  for (int off = 32; off >= 1; off >>= 1) before += __shfl_xor(before, off, 64);
+  __shared__ int wave_sum[4];
+  if ((threadIdx.x & 63) == 0) wave_sum[threadIdx.x >> 6] = before;
+  __syncthreads();
+  int64_t m = (wave_sum[0] + wave_sum[1]) + (wave_sum[2] + wave_sum[3]);
+  if (padding) {
+    if (int64_t(blockIdx.x) == batch && threadIdx.x == 0) *a.count = int32_t(m);
+    for (int k = 0; k < kFewEach; ++k)
+      pad_row(a, m + (int64_t(blockIdx.x) - batch) * kFewEach + k, m);
+    return;
+  }
+  for (int64_t i = i0; i < i0 + kFewEach && i < a.n; ++i) {
+    const int32_t y = labels[i];
+    if (labelled(y, vocab, ignore_index)) {
+      gather_row(a, i, m);
+      if (threadIdx.x == 0) {
+        const int64_t d = int64_t(y) - v_start;
+        a.row[m] = int32_t(i);
+        a.ylab[m] = d >= 0 && d < v ? int32_t(d) : -1;
+      }
+      ++m;
+    } else {
+      clear_row(a, i);
+      if (state && threadIdx.x == 0) {
+        state[i] = -INFINITY;
+        state[a.n + i] = 0.f;
+        state[2 * a.n + i] = 0.f;
+      }
+    }
   }
 }
 
@@ -574,32 +626,51 @@ struct EpiPieceHidden {
   __device__ __forceinline__ void operator()(int64_t, int64_t, float) {}  // h % 4 == 0: unused
 };
 
-// The product split over K: partial sums [splits][np][h], then added in split order.
+// The product split over K: partial sums [splits][rows of the tiles that count][h], then added in
+// split order. Where fewer rows carry a label than the launch has tiles for, K is cut into as many
+// more ranges, of at least kSplitK classes each: the same workgroups and the same memory.
+constexpr int64_t kSplitK = 1024;
+__host__ __device__ inline int64_t piece_splits(int64_t m_tiles, int64_t live, int64_t splits,
+                                                int64_t v) {
+  const int64_t most = v / kSplitK > splits ? v / kSplitK : splits;
+  const int64_t s = splits * m_tiles / live;
+  return s < most ? s : most;
+}
 struct EpiPiecePartial {
   static constexpr bool kRowStats = false, kColSums = false, kTileMax = false;
-  static constexpr bool kRowLimit = true;
+  static constexpr bool kRowLimit = true, kResplit = true;
   float* part;
-  int64_t np, h;
+  int64_t h, v;
   const int32_t* count;
-  int64_t kz;
+  int64_t kz, rows;
   struct Aux {};
-  __device__ void begin(int64_t z) { kz = z; }
+  __device__ void begin(int64_t z) {
+    kz = z;
+    rows = up(*count, kTile);
+  }
   __device__ __forceinline__ int64_t row_limit() const { return *count; }
+  __device__ __forceinline__ int64_t splits(int64_t m_tiles, int64_t live, int64_t s) const {
+    return piece_splits(m_tiles, live, s, v);
+  }
   __device__ __forceinline__ Aux load4(int64_t, int64_t) const { return Aux{}; }
   __device__ __forceinline__ void store4(int64_t m, int64_t n, f32x4_t a, Aux) {
-    *reinterpret_cast<f32x4_t*>(part + (kz * np + m) * h + n) = a;
+    *reinterpret_cast<f32x4_t*>(part + (kz * rows + m) * h + n) = a;
   }
   __device__ __forceinline__ void operator()(int64_t, int64_t, float) {}
 };
 __global__ void __launch_bounds__(256) hidden_reduce_kernel(const float* __restrict__ part,
-                                                            int64_t np, int64_t splits,
-                                                            HiddenOut o) {
+                                                            int64_t m_tiles, int64_t splits,
+                                                            int64_t v, HiddenOut o) {
   const int64_t e = (int64_t(blockIdx.x) * 256 + threadIdx.x) * 4;
   const int64_t m = e / o.h, n = e % o.h;
-  if (m >= int64_t(*o.count)) return;
+  const int64_t count = *o.count;
+  if (m >= count) return;
+  const int64_t live = (count + kTile - 1) / kTile;
+  splits = piece_splits(m_tiles, live, splits, v);
   f32x4_t a{0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
   for (int64_t z = 0; z < splits; ++z)
-    a += *reinterpret_cast<const f32x4_t*>(part + (z * np + m) * o.h + n);
+    a += *reinterpret_cast<const f32x4_t*>(part + (z * live * kTile + m) * o.h + n);
   const int64_t i = o.row[m];
   o.put(i, n, o.old(i, n) + o.scale() * a);
 }
@@ -660,10 +731,10 @@ __global__ void __launch_bounds__(256) piece_bias_kernel(
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
 // Hidden-gradient splits over K for few output tiles: enough to fill the CUs, each at least
-// 1024 vocabulary rows long.
+// kSplitK vocabulary rows long.
 int64_t hidden_splits(int64_t n, int64_t h, int64_t v) {
   const int64_t tiles = (n + kTile - 1) / kTile * ((h + Wide::BN - 1) / Wide::BN);
-  return std::max<int64_t>(1, std::min<int64_t>(256 / std::max<int64_t>(tiles, 1), v / 1024));
+  return std::max<int64_t>(1, std::min<int64_t>(256 / std::max<int64_t>(tiles, 1), v / kSplitK));
 }
 
 struct PieceWs {
@@ -734,20 +805,26 @@ PieceWs carve_bwd(void* base, int64_t n, int64_t h, int64_t v) {
 
 hipError_t rows_and_gather(const uint16_t* hidden, const int32_t* labels, int64_t n, int64_t h,
                            int64_t v, int64_t v_start, int64_t vocab, int32_t ignore_index,
-                           const PieceWs& w, float* state, int32_t* status, GatherArgs g,
-                           hipStream_t s) {
-  TimedLaunch t(s, K_PIECE_GATHER);
-  hipLaunchKernelGGL(piece_rows_kernel, dim3(1), dim3(1024), 0, s, labels, n, v, v_start, vocab,
-                     ignore_index, w.count, w.cidx, w.row, w.ylab, state, status);
-  PIECE_TRY(hipGetLastError());
+                           const PieceWs& w, float* state, GatherArgs g, hipStream_t s) {
   g.hidden = hidden;
   g.n = n;
   g.h = h;
   g.h64 = up(h, Wide::BK);
   g.count = w.count;
   g.cidx = w.cidx;
+  g.row = w.row;
   g.ylab = w.ylab;
   g.hc = w.hc;
+  TimedLaunch t(s, K_PIECE_GATHER);
+  if (n <= kFewRows) {
+    const int64_t blocks = (n + kFewEach - 1) / kFewEach + kTile / kFewEach;
+    hipLaunchKernelGGL(gather_few_rows_kernel, dim3(unsigned(blocks)), dim3(256), 0, s, g, labels,
+                       v, v_start, vocab, ignore_index, state);
+    return hipGetLastError();
+  }
+  hipLaunchKernelGGL(piece_rows_kernel, dim3(1), dim3(1024), 0, s, labels, n, v, v_start, vocab,
+                     ignore_index, w.count, w.cidx, w.row, w.ylab, state);
+  PIECE_TRY(hipGetLastError());
   hipLaunchKernelGGL(gather_rows_kernel, dim3(unsigned(n + kTile)), dim3(256), 0, s, g);
   return hipGetLastError();
 }
@@ -766,6 +843,8 @@ hipError_t grad_logits(const PieceBwdArgs& a, const PieceWs& w, const View& hv, 
   EpiPieceGrad<BIAS, ROWS> e{w.d, np, a.bias, a.v, w.ylab, w.count, w.lse_c, w.coef_c, w.colsum,
                              v64};
   TimedLaunch t(s, K_PIECE_GRAD_LOGITS);
+  if (a.n <= kNarrowRows)  // one row tile either way
+    return gemm::v2::launch<Narrow, true, true>(hv, wv, np, v64, h64, 1, true, e, s);
   return gemm::v2::launch<Wide, true, true>(hv, wv, np, v64, h64, 1, true, e, s);
 }
 
@@ -803,17 +882,14 @@ hipError_t piece_fwd_run(const PieceFwdArgs& a, hipStream_t s) {
     };
     if (a.n <= 16)
       launch(score_kernel<1>);
-    else if (a.n <= 32)
-      launch(score_kernel<2>);
     else
-      launch(score_kernel<4>);
+      launch(score_kernel<2>);
     PIECE_TRY(hipGetLastError());
   } else {
     tiles = (a.v + Wide::BN - 1) / Wide::BN;
     const int64_t np = up(a.n, kTile), h64 = up(a.h, Wide::BK);
     PIECE_TRY(rows_and_gather(a.hidden, a.labels, a.n, a.h, a.v, a.v_start, a.vocab,
-                              a.ignore_index, w, first ? a.state : nullptr, nullptr,
-                              GatherArgs{}, s));
+                              a.ignore_index, w, first ? a.state : nullptr, GatherArgs{}, s));
     const uint16_t* weight = a.weight;
     if (w.wpad) {
       PIECE_TRY(pad_weight(a.weight, a.h, a.v, w.wpad, s));
@@ -823,7 +899,10 @@ hipError_t piece_fwd_run(const PieceFwdArgs& a, hipStream_t s) {
     View wv{weight, h64, 64, a.v, h64};
     EpiPieceLse e{a.bias, a.v, w.ylab, w.count, w.part, tiles, w.zy};
     TimedLaunch t(s, K_PIECE_LOGITS);
-    PIECE_TRY((gemm::v2::launch<Wide, true, true>(hv, wv, np, a.v, h64, 1, true, e, s)));
+    if (a.n <= kNarrowRows)
+      PIECE_TRY((gemm::v2::launch<Narrow, true, true>(hv, wv, np, a.v, h64, 1, true, e, s)));
+    else
+      PIECE_TRY((gemm::v2::launch<Wide, true, true>(hv, wv, np, a.v, h64, 1, true, e, s)));
   }
   TimedLaunch t(s, K_PIECE_STATE);
   hipLaunchKernelGGL(merge_state_kernel, dim3(unsigned(a.n)), dim3(256), 0, s, w.part, tiles, w.zy,
@@ -867,7 +946,7 @@ hipError_t piece_bwd_run(const PieceBwdArgs& a, hipStream_t s) {
   g.zero_acc = first && !last ? a.hidden_acc : nullptr;
   g.zero_grad = last ? a.grad_hidden : nullptr;
   PIECE_TRY(rows_and_gather(a.hidden, a.labels, a.n, a.h, a.v, a.v_start, a.vocab, a.ignore_index,
-                            w, nullptr, nullptr, g, s));
+                            w, nullptr, g, s));
   const uint16_t* weight = a.weight;
   if (w.wpad) {
     PIECE_TRY(pad_weight(a.weight, a.h, a.v, w.wpad, s));
@@ -895,14 +974,14 @@ hipError_t piece_bwd_run(const PieceBwdArgs& a, hipStream_t s) {
       TimedLaunch t(s, K_PIECE_GRAD_HIDDEN);
       PIECE_TRY((gemm::v2::launch<Wide, true, false>(dv, wk, np, a.h, a.v, 1, true, e, s, true)));
     } else {
-      EpiPiecePartial e{w.split, np, a.h, w.count, 0};
+      EpiPiecePartial e{w.split, a.h, a.v, w.count, 0, 0};
       {
         TimedLaunch t(s, K_PIECE_GRAD_HIDDEN);
         PIECE_TRY((gemm::v2::launch<Wide, true, false>(dv, wk, np, a.h, a.v, splits, true, e, s)));
       }
       TimedLaunch t(s, K_PIECE_GRAD_HIDDEN);
       hipLaunchKernelGGL(hidden_reduce_kernel, dim3(unsigned((a.n * a.h / 4 + 255) / 256)),
-                         dim3(256), 0, s, w.split, np, splits, o);
+                         dim3(256), 0, s, w.split, np / kTile, splits, a.v, o);
       PIECE_TRY(hipGetLastError());
     }
   }

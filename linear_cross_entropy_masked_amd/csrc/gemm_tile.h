@@ -545,6 +545,8 @@ struct RowTagged<E, std::void_t<decltype(E::kRowTag)>> {
 // (row_limit(), at most M): the tile order is that of a product with so many rows, and the
 // workgroups left over end at once. Those that set kKLimit hold the length of the contraction
 // there (k_limit(), at most K).
+// Epilogues that set kResplit as well cut K into splits(m_tiles of the launch, of the rows that
+// count, splits of the launch) ranges, so that few rows still fill the chip.
 template <class E, class = void>
 struct RowLimited {
   static constexpr bool value = false;
@@ -552,6 +554,14 @@ struct RowLimited {
 template <class E>
 struct RowLimited<E, std::void_t<decltype(E::kRowLimit)>> {
   static constexpr bool value = E::kRowLimit;
+};
+template <class E, class = void>
+struct Resplit {
+  static constexpr bool value = false;
+};
+template <class E>
+struct Resplit<E, std::void_t<decltype(E::kResplit)>> {
+  static constexpr bool value = E::kResplit;
 };
 template <class E, class = void>
 struct KLimited {
@@ -904,7 +914,13 @@ __global__ void __launch_bounds__(C::THREADS, C::OCC)
   __shared__ __attribute__((aligned(1024))) char lds[C::LdsBytes];
   TileCoord tc;
   if constexpr (RowLimited<Epi>::value) {
-    tm.m_tiles = (epi.row_limit() + C::BM - 1) / C::BM;
+    const int64_t live = (epi.row_limit() + C::BM - 1) / C::BM;
+    if constexpr (Resplit<Epi>::value) {
+      if (live == 0) return;
+      tm.splits = epi.splits(tm.m_tiles, live, tm.splits);
+      ksplit = ((K + tm.splits - 1) / tm.splits + C::BK - 1) / C::BK * C::BK;
+    }
+    tm.m_tiles = live;
     if (tm.m_tiles < 8) tm.xn = 0;  // too few for a block of tiles per XCD
     if (tm.xn == 0 && int64_t(blockIdx.x) >= tm.m_tiles * tm.n_tiles * tm.splits) return;
   }

@@ -103,7 +103,8 @@ def check_bwd(e, gh, gw, gb):
 
 
 SHAPES = [(1, 8, 1), (1, 64, 3000), (3, 40, 255), (16, 768, 1000), (17, 72, 257), (33, 200, 64),
-          (64, 4096, 500), (65, 64, 1001), (130, 136, 4), (255, 1032, 700), (256, 256, 256),
+          (32, 136, 301), (64, 4096, 500), (65, 64, 1001), (128, 72, 900),
+          (130, 136, 4), (255, 1032, 700), (256, 256, 256),
           (300, 768, 5003), (1000, 64, 129), (600, 2048, 2300)]
 
 
@@ -295,6 +296,50 @@ def test_peaked_rows(dev):
     loss, lse, rows = lce.flce_pieces_fwd(hid, w, lab, b2, return_rows=True)
     check_fwd(e, loss, lse, rows)
     check_bwd(e, *lce.flce_pieces_bwd(hid, w, lab, lse, b2))
+
+
+def test_long_batches(dev):
+    """Past 8192 rows the labelled rows are numbered in a launch of their own."""
+    for masked in (0.3, 0.97):
+        hid, w, b, lab = make(dev, 9001, 64, 520, masked=masked)
+        hid[lab == IGN] = float("nan")
+        e = Exact(hid, w, b, lab)
+        loss, lse, rows = lce.flce_pieces_fwd(hid, w, lab, b, return_rows=True)
+        check_fwd(e, loss, lse, rows)
+        check_bwd(e, *lce.flce_pieces_bwd(hid, w, lab, lse, b))
+        check_bwd(e, *lce.flce_pieces_bwd(hid, w, lab, lse, b, piece_size=256))
+
+
+def test_few_labelled_rows_take_more_splits(dev):
+    """Many row tiles in the launch, few rows that count: the hidden gradient's contraction is cut
+    into more ranges, in the memory that was asked for."""
+    n, h, v = 1500, 64, 20000
+    hid, w, b, lab = make(dev, n, h, v, masked=0.9)
+    e = Exact(hid, w, b, lab)
+    loss, lse, _ = lce.flce_pieces_fwd(hid, w, lab, b)
+    need = lce.flce_piece_bwd_workspace_size(n, h, v)
+    ws = torch.full((need + 4096,), 0xFF, dtype=torch.uint8, device=dev)
+    gh = torch.empty(n, h, dtype=torch.bfloat16, device=dev)
+    lce.flce_piece_bwd(hid, w, lab, lse, b, v_start=0, vocab=v, first=True, last=True,
+                       grad_hidden=gh, workspace=ws[:need])
+    assert (ws[need:] == 0xFF).all()
+    near(gh, e.gh, e.dgh, "grad_hidden")
+    assert not gh[~e.keep].any()
+
+
+def test_a_piece_past_4_gib(dev):
+    """Logit gradients of one piece past 2^32 bytes: the same weight gradient, bit for bit, as in
+    pieces of a tenth, and the hidden gradient within its rounding."""
+    n, h, v = 17000, 64, 128256
+    hid, w, b, lab = make(dev, n, h, v, bias=False)
+    assert lce.flce_piece_bwd_workspace_size(n, h, v) > 2 ** 32
+    _, lse, _ = lce.flce_pieces_fwd(hid, w, lab)
+    gh, gw, _ = lce.flce_pieces_bwd(hid, w, lab, lse, piece_size=v)
+    gh2, gw2, _ = lce.flce_pieces_bwd(hid, w, lab, lse, piece_size=12800)
+    assert torch.equal(gw, gw2)
+    # two bf16 roundings, and fp32 sums of v products of which the label's is the largest
+    size = (w.float().abs().max() * 2 / int((lab != IGN).sum())).item()
+    assert ((gh.float() - gh2.float()).abs() <= 2 * B * gh.float().abs() + v * U * size).all()
 
 
 def test_agrees_with_the_loss_by_chunks_of_rows(dev):
