@@ -21,6 +21,11 @@ Behaviour follows NeMo Automodel PR #2996 (the masked CE loss with a chunk_size)
 The fused linear CE function uses the split calls (``flce_fwd`` in the forward, ``flce_bwd``
 in the backward): nothing of size [V, H] lives from the forward to the backward (Liger-Kernel
 issue #533, feature pitch), and the upstream gradient stays on the device.
+
+``linear_cross_entropy_pieces`` is the same loss over a weight in pieces of the vocabulary, with
+per-row terms as well. ``embedding`` and ``layer_norm`` are the model's other end of a tied table
+and the norm in front of the head; ``norm_linear_cross_entropy`` joins norm and loss without
+keeping the normalised hidden states, and ``TiedHead`` holds one table for both ends.
 """
 from __future__ import annotations
 
@@ -28,7 +33,8 @@ import torch
 from torch.autograd.function import once_differentiable
 
 from . import (ce_chunked_bwd, ce_chunked_bwd_inplace, ce_chunked_fwd, ce_rows_bwd, ce_rows_fwd,
-               flce_bwd, flce_fwd)
+               embed_bwd, embed_fwd, flce_bwd, flce_fwd, flce_pieces_bwd, flce_pieces_fwd,
+               layernorm_bwd, layernorm_fwd)
 
 REDUCTIONS = ("sum", "mean", "none")
 
@@ -255,3 +261,297 @@ def flce(hidden, weight, labels, bias=None, *, mask=None, ignore_index: int = -1
                                 ignore_index=ignore_index, chunk_size=chunk_size,
                                 num_label_tokens=num_label_tokens, reduction=reduction,
                                 weight_grad_buffer=weight_grad_buffer)
+
+
+# ---------------------------------------------------------------- embedding and layer norm
+
+def _rows(t):
+    """A 2-d tensor whose rows the kernels can walk: contiguous ones that do not share memory
+    (an upstream gradient may be a broadcast)."""
+    if t.shape[1] > 1 and t.stride(1) != 1 or t.shape[0] > 1 and t.stride(0) < t.shape[1]:
+        return t.contiguous()
+    return t
+
+
+def _check_buffer(buffer, weight, dtypes=(torch.float32,)):
+    if buffer is not None and (buffer.dtype not in dtypes
+                               or tuple(buffer.shape) != tuple(weight.shape)
+                               or not buffer.is_contiguous()):
+        raise ValueError("weight_grad_buffer must be a contiguous tensor of the weight's shape, "
+                         f"of type {' or '.join(str(d) for d in dtypes)}")
+
+
+class _Embedding(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, weight, tokens, scale, ignore_index, grad_buffer):
+        ctx.save_for_backward(tokens)
+        ctx.cfg = (weight.shape[0], weight.dtype, scale, ignore_index, grad_buffer)
+        return embed_fwd(_rows(weight), tokens, scale=scale, ignore_index=ignore_index)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, g):
+        (tokens,) = ctx.saved_tensors
+        v, dtype, scale, ignore_index, buffer = ctx.cfg
+        if buffer is not None:
+            embed_bwd(_rows(g), tokens, v, scale=scale, ignore_index=ignore_index,
+                      grad_weight=buffer, accumulate=True)
+            return None, None, None, None, None
+        grad = embed_bwd(_rows(g), tokens, v, scale=scale, ignore_index=ignore_index, dtype=dtype)
+        return grad, None, None, None, None
+
+
+def embedding(tokens, weight, *, scale: float = 1.0, ignore_index: int = -100,
+              weight_grad_buffer=None):
+    """scale · weight[tokens]: tokens [...] (int32 or int64), weight [V, H] in bf16, fp16 or fp32;
+    zero rows without a gradient where the token is ``ignore_index`` or outside the table.
+
+    With ``weight_grad_buffer`` (fp32 [V, H]) the table's gradient is added into that buffer and
+    ``weight.grad`` is left alone, as in :func:`linear_cross_entropy`: a table tied to the head
+    gives both functions the same buffer."""
+    _check_buffer(weight_grad_buffer, weight)
+    out = _Embedding.apply(weight, tokens.reshape(-1), float(scale), int(ignore_index),
+                           weight_grad_buffer)
+    return out.view(*tokens.shape, weight.shape[1])
+
+
+class _LayerNorm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, bias, eps):
+        x = _rows(x)
+        y, mean, rstd = layernorm_fwd(x, weight, bias, eps=eps)
+        ctx.save_for_backward(x, weight, mean, rstd)
+        return y
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, g):
+        x, weight, mean, rstd = ctx.saved_tensors
+        need_x, need_w, need_b = ctx.needs_input_grad[:3]
+        gx, gw, gb = _layernorm_grads(g, x, mean, rstd, weight, need_x, need_w, need_b, False)
+        return gx, gw, gb, None
+
+
+def _layernorm_grads(g, x, mean, rstd, weight, need_x, need_w, need_b, in_place):
+    g = _rows(g)
+    return layernorm_bwd(g, x, mean, rstd, weight, grad_x=g if need_x and in_place else need_x,
+                         grad_weight=need_w, grad_bias=need_b)
+
+
+def layer_norm(x, weight=None, bias=None, *, eps: float = 1e-5):
+    """Layer norm over the last dimension of x [..., H] in bf16, fp16 or fp32; weight and bias [H]
+    of x's type or fp32 (one type for both), or None."""
+    h = x.shape[-1]
+    return _LayerNorm.apply(x.reshape(-1, h), weight, bias, float(eps)).view(x.shape)
+
+
+class LayerNorm(torch.nn.Module):
+    """Module form of :func:`layer_norm` with the parameters of torch.nn.LayerNorm over one
+    dimension."""
+
+    def __init__(self, hidden: int, eps: float = 1e-5, *, bias: bool = True, device=None,
+                 dtype=None):
+        super().__init__()
+        self.eps = eps
+        self.weight = torch.nn.Parameter(torch.ones(hidden, device=device, dtype=dtype))
+        self.bias = (torch.nn.Parameter(torch.zeros(hidden, device=device, dtype=dtype))
+                     if bias else None)
+
+    def forward(self, x):
+        return layer_norm(x, self.weight, self.bias, eps=self.eps)
+
+
+# ---------------------------------------------------------------- loss in pieces of the vocabulary
+
+def _piece_grads(hidden, weights, biases, labels, lse, g, cfg, need_h, need_w, need_b):
+    """(grad_hidden, [grad per weight], [grad per bias]) with cfg as _LinearCEPieces keeps it."""
+    ignore_index, count, per_row, piece_size, buffers = cfg
+    if g.dtype != torch.float32:
+        g = g.to(torch.float32)
+    gws = [None] * len(weights)
+    gbs = [None] * len(weights)
+    for k, (w, need) in enumerate(zip(weights, need_w)):
+        if need:
+            gws[k] = buffers[k] if buffers is not None else torch.empty_like(
+                w, memory_format=torch.contiguous_format)
+    # accumulating covers the bias too: with buffers its gradient is added to zeros
+    make = torch.zeros_like if buffers is not None else torch.empty_like
+    for k, (b, need) in enumerate(zip(biases, need_b)):
+        if need:
+            gbs[k] = make(b, memory_format=torch.contiguous_format)
+    has_bias = biases[0] is not None
+    gh, _, _ = flce_pieces_bwd(
+        hidden, weights, labels, lse, biases if has_bias else None, piece_size=piece_size,
+        ignore_index=ignore_index, num_label_tokens=count, accumulate=buffers is not None,
+        grad_output=None if per_row else g, grad_rows=g.contiguous() if per_row else None,
+        grad_hidden=bool(need_h), grad_weight=gws, grad_bias=gbs if has_bias else False)
+    if buffers is not None:
+        gws = [None] * len(weights)
+    return gh, gws, gbs
+
+
+class _LinearCEPieces(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, hidden, labels, cfg, pieces, *tensors):
+        weights, biases = list(tensors[:pieces]), list(tensors[pieces:])
+        ignore_index, count, per_row, _, _ = cfg
+        loss, lse, rows = flce_pieces_fwd(
+            hidden, weights, labels, biases if biases[0] is not None else None,
+            ignore_index=ignore_index, num_label_tokens=count, return_rows=per_row)
+        ctx.save_for_backward(hidden, labels, lse, *tensors)
+        ctx.cfg, ctx.pieces = cfg, pieces
+        return rows if per_row else loss
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, g):
+        hidden, labels, lse, *tensors = ctx.saved_tensors
+        k = ctx.pieces
+        need = ctx.needs_input_grad
+        gh, gws, gbs = _piece_grads(hidden, tensors[:k], tensors[k:], labels, lse, g, ctx.cfg,
+                                    need[0], need[4:4 + k], need[4 + k:])
+        return gh, None, None, None, *gws, *gbs
+
+
+def _piece_inputs(weight, bias, buffer):
+    weights = list(weight) if isinstance(weight, (list, tuple)) else [weight]
+    if not weights:
+        raise ValueError("weight holds no pieces")
+    biases = ([None] * len(weights) if bias is None
+              else list(bias) if isinstance(bias, (list, tuple)) else [bias])
+    if len(biases) != len(weights):
+        raise ValueError(f"{len(weights)} weight pieces but {len(biases)} biases")
+    buffers = None
+    if buffer is not None:
+        buffers = list(buffer) if isinstance(buffer, (list, tuple)) else [buffer]
+        if len(buffers) != len(weights):
+            raise ValueError(f"{len(weights)} weight pieces but {len(buffers)} buffers")
+        for b, w in zip(buffers, weights):
+            _check_buffer(b, w, (torch.float32, torch.bfloat16))
+    return weights, biases, buffers
+
+
+def linear_cross_entropy_pieces(hidden, weight, labels, bias=None, *, mask=None,
+                                ignore_index: int = -100, num_label_tokens: int | None = None,
+                                reduction: str = "sum", piece_size: int | None = None,
+                                weight_grad_buffer=None):
+    """:func:`linear_cross_entropy` over a weight in pieces of the vocabulary: one bf16 [V, H]
+    tensor or a sequence of them holding consecutive classes (a base vocabulary and tokens added
+    to it), with fp32 biases likewise or None. The backward takes ``piece_size`` classes at a time
+    (default: so that their bf16 logit gradients stay within 512 MiB) and leaves each weight's
+    gradient in the weight's own type, without an fp32 [V, H] accumulator.
+
+    reduction: "sum", "mean" or "none" (the per-row terms, 0 for rows without a label; minus a
+    term is the log-probability of the row's label, with its gradient). Rows without a label take
+    no part in any product. ``weight_grad_buffer`` (fp32 or bf16, a sequence where weight is one):
+    the gradients are added into it and ``weight.grad`` is left alone."""
+    _check_reduction(reduction, num_label_tokens)
+    weights, biases, buffers = _piece_inputs(weight, bias, weight_grad_buffer)
+    h = hidden.shape[-1]
+    flat = hidden.reshape(-1, h)
+    lab = _flat_labels(labels, mask, flat.shape[0], ignore_index)
+    per_row = reduction == "none"
+    cfg = (int(ignore_index), _normaliser(reduction, num_label_tokens), per_row, piece_size,
+           buffers)
+    out = _LinearCEPieces.apply(flat, lab, cfg, len(weights), *weights, *biases)
+    return out.view(hidden.shape[:-1]) if per_row else out
+
+
+class LinearCrossEntropyPieces(torch.nn.Module):
+    """Module form of :func:`linear_cross_entropy_pieces` (weight and bias are passed in)."""
+
+    def __init__(self, *, ignore_index: int = -100, reduction: str = "sum",
+                 piece_size: int | None = None):
+        super().__init__()
+        _check_reduction(reduction, None)
+        self.ignore_index = ignore_index
+        self.reduction = reduction
+        self.piece_size = piece_size
+
+    def forward(self, hidden, weight, labels, bias=None, mask=None, num_label_tokens=None,
+                weight_grad_buffer=None):
+        return linear_cross_entropy_pieces(
+            hidden, weight, labels, bias, mask=mask, ignore_index=self.ignore_index,
+            num_label_tokens=num_label_tokens, reduction=self.reduction,
+            piece_size=self.piece_size, weight_grad_buffer=weight_grad_buffer)
+
+
+class _NormLinearCE(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, norm_weight, norm_bias, labels, eps, cfg, pieces, *tensors):
+        weights, biases = list(tensors[:pieces]), list(tensors[pieces:])
+        ignore_index, count, per_row, _, _ = cfg
+        x = _rows(x)
+        y, mean, rstd = layernorm_fwd(x, norm_weight, norm_bias, eps=eps)
+        loss, lse, rows = flce_pieces_fwd(
+            y, weights, labels, biases if biases[0] is not None else None,
+            ignore_index=ignore_index, num_label_tokens=count, return_rows=per_row)
+        ctx.save_for_backward(x, norm_weight, norm_bias, mean, rstd, labels, lse, *tensors)
+        ctx.cfg, ctx.pieces, ctx.eps = cfg, pieces, eps
+        return rows if per_row else loss
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, g):
+        x, nw, nb, mean, rstd, labels, lse, *tensors = ctx.saved_tensors
+        k = ctx.pieces
+        need = ctx.needs_input_grad
+        norm_grads = any(need[:3])
+        y, _, _ = layernorm_fwd(x, nw, nb, eps=ctx.eps, return_stats=False)
+        gy, gws, gbs = _piece_grads(y, tensors[:k], tensors[k:], labels, lse, g, ctx.cfg,
+                                    norm_grads, need[7:7 + k], need[7 + k:])
+        del y
+        gx = gnw = gnb = None
+        if norm_grads:
+            gx, gnw, gnb = _layernorm_grads(gy, x, mean, rstd, nw, need[0], need[1], need[2], True)
+        return gx, gnw, gnb, None, None, None, None, *gws, *gbs
+
+
+def norm_linear_cross_entropy(x, norm_weight, norm_bias, weight, labels, bias=None, *,
+                              eps: float = 1e-5, mask=None, ignore_index: int = -100,
+                              num_label_tokens: int | None = None, reduction: str = "sum",
+                              piece_size: int | None = None, weight_grad_buffer=None):
+    """:func:`layer_norm` of bf16 x [..., H], then :func:`linear_cross_entropy_pieces` of the
+    result. Between forward and backward only x (which the model holds anyway) and three fp32
+    values a row are kept: the backward normalises x again, and its hidden gradient becomes x's
+    in place."""
+    _check_reduction(reduction, num_label_tokens)
+    weights, biases, buffers = _piece_inputs(weight, bias, weight_grad_buffer)
+    flat = x.reshape(-1, x.shape[-1])
+    lab = _flat_labels(labels, mask, flat.shape[0], ignore_index)
+    per_row = reduction == "none"
+    cfg = (int(ignore_index), _normaliser(reduction, num_label_tokens), per_row, piece_size,
+           buffers)
+    out = _NormLinearCE.apply(flat, norm_weight, norm_bias, lab, float(eps), cfg, len(weights),
+                              *weights, *biases)
+    return out.view(x.shape[:-1]) if per_row else out
+
+
+class TiedHead(torch.nn.Module):
+    """Both ends of a language model on one bf16 table [V, H]: ``embed`` looks tokens up,
+    ``forward`` is the final norm and the loss against the same table (Liger-Kernel issue #941:
+    lm_head.weight shared with embed_tokens). ``main_grad`` (fp32 [V, H], zeros, on request)
+    collects both gradients of the table without a rounding between them, and ``weight.grad``
+    stays None; without it autograd adds the two in bf16."""
+
+    def __init__(self, vocab: int, hidden: int, *, scale: float = 1.0, eps: float = 1e-5,
+                 ignore_index: int = -100, main_grad: bool = False, device=None):
+        super().__init__()
+        self.scale, self.ignore_index = scale, ignore_index
+        self.weight = torch.nn.Parameter(
+            torch.empty(vocab, hidden, device=device, dtype=torch.bfloat16))
+        torch.nn.init.normal_(self.weight, std=0.02)
+        self.norm = LayerNorm(hidden, eps, device=device, dtype=torch.bfloat16)
+        self.register_buffer(
+            "main_grad", torch.zeros(vocab, hidden, device=device, dtype=torch.float32)
+            if main_grad else None, persistent=False)
+
+    def embed(self, tokens):
+        return embedding(tokens, self.weight, scale=self.scale, ignore_index=self.ignore_index,
+                         weight_grad_buffer=self.main_grad)
+
+    def forward(self, x, labels, mask=None, num_label_tokens=None, reduction: str = "mean"):
+        return norm_linear_cross_entropy(
+            x, self.norm.weight, self.norm.bias, self.weight, labels, eps=self.norm.eps,
+            mask=mask, ignore_index=self.ignore_index, num_label_tokens=num_label_tokens,
+            reduction=reduction, weight_grad_buffer=self.main_grad)

@@ -196,3 +196,32 @@ def test_binding_refuses_host_tensors_and_wrong_types():
     with pytest.raises(ValueError, match="biases"):
         lce.flce_pieces_fwd(hid, [hid, hid], torch.zeros(3, dtype=torch.int32),
                             [torch.zeros(3)])
+
+
+def test_calls_run_on_their_tensors_device(monkeypatch):
+    """A call for tensors of another device than the current one switches to it and takes that
+    device's stream."""
+    seen = []
+
+    class On:
+        def __init__(self, device):
+            self.device = device
+
+        def __enter__(self):
+            seen.append(("enter", self.device.index))
+
+        def __exit__(self, *a):
+            seen.append(("exit", self.device.index))
+
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(torch.cuda, "device", On)
+    monkeypatch.setattr(lce, "_raw_stream", lambda t, index: 1000 + index)
+    monkeypatch.setitem(lce._FNS, "embed_fwd", lambda *a: seen.append(("call", a)) or 0)
+    lce._call("embed_fwd", torch.device("cuda", 0), "x")
+    assert seen == [("call", ("x", 1000))]
+    seen.clear()
+    lce._call("embed_fwd", torch.device("cuda", 3), "x")
+    assert seen == [("enter", 3), ("call", ("x", 1003)), ("exit", 3)]
+    monkeypatch.setitem(lce._FNS, "embed_fwd", lambda *a: BAD_DTYPE)
+    with pytest.raises(lce.LceError, match="type"):
+        lce._call("embed_fwd", torch.device("cuda", 0))
