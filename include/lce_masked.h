@@ -315,7 +315,7 @@ int flce_bwd(const uint16_t* hidden, const uint16_t* weight, const float* bias,
  * Labels are classes of the whole vocabulary. A row carries a label when label != ignore_index
  * and 0 <= label < vocab. Rows without one take no part in any product, whatever they hold.
  * Limits: h a multiple of 8, h <= 2^20, n <= 2^23, 1 <= v, 0 <= v_start, v_start + v <= vocab
- * < 2^31. A bias of minus infinity masks a class. hidden, weight, bias and the gradients are
+ * < 2^31, and fewer than 2^23 tiles of 256 rows by 256 classes of a piece. A bias of minus infinity masks a class. hidden, weight, bias and the gradients are
  * contiguous; 16-byte aligned where they are bf16 or the fp32 hidden_acc / grad_weight. */
 
 #define FLCE_PIECE_FIRST         1u /* the first piece: state / hidden_acc are overwritten        */

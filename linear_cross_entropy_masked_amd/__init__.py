@@ -17,6 +17,7 @@ and over all pieces of a vocabulary: flce_pieces_fwd, flce_pieces_bwd
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 __all__ = [
@@ -541,6 +542,14 @@ def flce_bwd(hidden, weight, labels, lse, bias=None, *, ignore_index: int = -100
 _FNS: dict = {}  # C entry points looked up so far
 
 
+@functools.lru_cache(maxsize=512)
+def _size(fn, *args):
+    """A workspace size: a function of its arguments alone."""
+    out = ctypes.c_size_t()
+    _check(fn, getattr(load_library(), fn)(*args, ctypes.byref(out)))
+    return out.value
+
+
 def _call(fn, device, *args):
     """fn(*args) with ``device`` current (the library checks and launches on the current one);
     raises on a status code. The stream, the last argument, is the caller's current one there."""
@@ -641,10 +650,7 @@ def _tokens_i32(tokens, device, ignore_index):
 
 
 def embed_workspace_size(n: int, h: int, v: int) -> int:
-    out = ctypes.c_size_t()
-    _check("embed_workspace_size",
-           load_library().embed_workspace_size(n, h, v, ctypes.byref(out)))
-    return out.value
+    return _size("embed_workspace_size", n, h, v)
 
 
 def embed_bwd(grad, tokens, num_embeddings: int, *, scale: float = 1.0, ignore_index: int = -100,
@@ -719,10 +725,7 @@ def layernorm_fwd(x, weight=None, bias=None, *, eps: float = 1e-5, out=None,
 
 
 def layernorm_workspace_size(n: int, h: int) -> int:
-    out = ctypes.c_size_t()
-    _check("layernorm_workspace_size",
-           load_library().layernorm_workspace_size(n, h, ctypes.byref(out)))
-    return out.value
+    return _size("layernorm_workspace_size", n, h)
 
 
 def layernorm_bwd(grad, x, mean, rstd, weight=None, *, grad_x=True, grad_weight=None,
@@ -783,12 +786,6 @@ def layernorm_bwd(grad, x, mean, rstd, weight=None, *, grad_x=True, grad_weight=
     return grad_x, gw, gb
 
 
-def _size(fn, *args):
-    out = ctypes.c_size_t()
-    _check(fn, getattr(load_library(), fn)(*args, ctypes.byref(out)))
-    return out.value
-
-
 def flce_piece_fwd_workspace_size(n: int, h: int, v: int) -> int:
     return _size("flce_piece_fwd_workspace_size", n, h, v)
 
@@ -801,19 +798,18 @@ def flce_piece_bwd_workspace_size(n: int, h: int, v: int) -> int:
     return _size("flce_piece_bwd_workspace_size", n, h, v)
 
 
-def _piece_operands(hidden, weight, bias):
+def _piece_weight(weight, bias, h, dev):
     import torch
-    _require(hidden, "hidden", torch.bfloat16, 2)
-    dev = hidden.device
     _require(weight, "weight", torch.bfloat16, 2, dev)
-    if weight.shape[1] != hidden.shape[1]:
-        raise ValueError(f"hidden has {hidden.shape[1]} columns but weight has {weight.shape[1]}")
+    v, h2 = weight.shape
+    if h2 != h:
+        raise ValueError(f"hidden has {h} columns but weight has {h2}")
     if bias is not None:
         _require(bias, "bias", torch.float32, 1, dev)
-        if bias.shape[0] != weight.shape[0]:
+        if bias.shape[0] != v:
             raise ValueError("bias must have one entry per row of weight")
         bias = bias.contiguous()
-    return hidden.contiguous(), weight.contiguous(), bias, dev
+    return weight.contiguous(), bias, v
 
 
 def _contiguous_f32(t, name, shape, device):
@@ -824,20 +820,40 @@ def _contiguous_f32(t, name, shape, device):
     return t
 
 
+def _piece_fwd(hidden, weight, bias, labels, state, n, h, v, v_start, vocab, first, ignore_index,
+               ws, dev):
+    _call("flce_piece_fwd", dev, hidden.data_ptr(), weight.data_ptr(), _adr(bias),
+          labels.data_ptr(), n, h, v, v_start, vocab, ignore_index,
+          FLCE_PIECE_FIRST if first else 0, state.data_ptr(), ws.data_ptr(), _bytes_of(ws))
+
+
+def _piece_loss(state, labels, n, vocab, ignore_index, num_label_tokens, return_rows, status, ws,
+                dev):
+    import torch
+    loss = torch.empty((), dtype=torch.float32, device=dev)
+    lse = torch.empty(n, dtype=torch.float32, device=dev)
+    rows = torch.empty(n, dtype=torch.float32, device=dev) if return_rows else None
+    _call("flce_piece_loss", dev, state.data_ptr(), labels.data_ptr(), n, vocab, ignore_index,
+          _count_arg(num_label_tokens), loss.data_ptr(), lse.data_ptr(), _adr(rows),
+          _status_ptr(status, dev), ws.data_ptr(), _bytes_of(ws))
+    return loss, lse, rows
+
+
 def flce_piece_fwd(hidden, weight, labels, state, bias=None, *, v_start: int, vocab: int,
                    first: bool, ignore_index: int = -100, workspace=None):
     """Takes the logits over one piece of the vocabulary, the classes v_start ... of ``vocab``,
     into ``state`` (fp32 [3, n]: maximum, sum of exponentials, label logit per row; overwritten
     with ``first``). Returns state."""
-    hidden, weight, bias, dev = _piece_operands(hidden, weight, bias)
+    import torch
+    _require(hidden, "hidden", torch.bfloat16, 2)
+    dev = hidden.device
     n, h = hidden.shape
-    v = weight.shape[0]
+    weight, bias, v = _piece_weight(weight, bias, h, dev)
     labels = _labels_i32(labels, n, dev, ignore_index)
     _contiguous_f32(state, "state", (3, n), dev)
     ws = _workspace(flce_piece_fwd_workspace_size(n, h, v), dev, workspace)
-    _call("flce_piece_fwd", dev, hidden.data_ptr(), weight.data_ptr(), _adr(bias),
-          labels.data_ptr(), n, h, v, v_start, vocab, ignore_index,
-          FLCE_PIECE_FIRST if first else 0, state.data_ptr(), ws.data_ptr(), _bytes_of(ws))
+    _piece_fwd(hidden.contiguous(), weight, bias, labels, state, n, h, v, v_start, vocab, first,
+               ignore_index, ws, dev)
     return state
 
 
@@ -853,14 +869,44 @@ def flce_piece_loss(state, labels, *, vocab: int, ignore_index: int = -100,
     n = state.shape[1]
     _contiguous_f32(state, "state", (3, n), dev)
     labels = _labels_i32(labels, n, dev, ignore_index)
-    loss = torch.empty((), dtype=torch.float32, device=dev)
-    lse = torch.empty(n, dtype=torch.float32, device=dev)
-    rows = torch.empty(n, dtype=torch.float32, device=dev) if return_rows else None
     ws = _workspace(flce_piece_loss_workspace_size(n), dev, workspace)
-    _call("flce_piece_loss", dev, state.data_ptr(), labels.data_ptr(), n, vocab, ignore_index,
-          _count_arg(num_label_tokens), loss.data_ptr(), lse.data_ptr(), _adr(rows),
-          _status_ptr(status, dev), ws.data_ptr(), _bytes_of(ws))
-    return loss, lse, rows
+    return _piece_loss(state, labels, n, vocab, ignore_index, num_label_tokens, return_rows, status,
+                       ws, dev)
+
+
+def _piece_bwd(hidden, weight, bias, labels, lse, n, h, v, v_start, vocab, ignore_index, count,
+               flags, grad_output, grad_rows, hidden_acc, grad_hidden, grad_weight, grad_bias, ws,
+               dev):
+    wcode = 0 if grad_weight is None else _dtype_code(grad_weight.dtype, "grad_weight")
+    _call("flce_piece_bwd", dev, hidden.data_ptr(), weight.data_ptr(), _adr(bias),
+          labels.data_ptr(), lse.data_ptr(), n, h, v, v_start, vocab, ignore_index, count, flags,
+          _adr(grad_output), _adr(grad_rows), _adr(hidden_acc), _adr(grad_hidden),
+          _adr(grad_weight), wcode, _adr(grad_bias), ws.data_ptr(), _bytes_of(ws))
+
+
+def _bwd_inputs(lse, grad_output, grad_rows, n, dev):
+    import torch
+    _contiguous_f32(lse, "lse", (n,), dev)
+    if grad_output is not None:
+        _require(grad_output, "grad_output", torch.float32, 0, dev)
+    if grad_rows is not None:
+        _contiguous_f32(grad_rows, "grad_rows", (n,), dev)
+
+
+def _bwd_hidden(t, n, h, dev):
+    import torch
+    _require(t, "grad_hidden", torch.bfloat16, 2, dev)
+    if tuple(t.shape) != (n, h) or not t.is_contiguous():
+        raise ValueError(f"grad_hidden must be a contiguous {(n, h)} tensor")
+
+
+def _bwd_params(grad_weight, grad_bias, v, h, dev):
+    if grad_weight is not None:
+        _require(grad_weight, "grad_weight", None, 2, dev)
+        if tuple(grad_weight.shape) != (v, h) or not grad_weight.is_contiguous():
+            raise ValueError(f"grad_weight must be a contiguous {(v, h)} tensor")
+    if grad_bias is not None:
+        _contiguous_f32(grad_bias, "grad_bias", (v,), dev)
 
 
 def flce_piece_bwd(hidden, weight, labels, lse, bias=None, *, v_start: int, vocab: int,
@@ -874,36 +920,23 @@ def flce_piece_bwd(hidden, weight, labels, lse, bias=None, *, v_start: int, voca
     ``grad_bias`` fp32, of the piece's size. ``grad_rows`` fp32 [n]: the upstream gradient of
     each row's term, in place of grad_output / num_label_tokens."""
     import torch
-    hidden, weight, bias, dev = _piece_operands(hidden, weight, bias)
+    _require(hidden, "hidden", torch.bfloat16, 2)
+    dev = hidden.device
     n, h = hidden.shape
-    v = weight.shape[0]
+    weight, bias, v = _piece_weight(weight, bias, h, dev)
     labels = _labels_i32(labels, n, dev, ignore_index)
-    _contiguous_f32(lse, "lse", (n,), dev)
-    if grad_output is not None:
-        _require(grad_output, "grad_output", torch.float32, 0, dev)
-    if grad_rows is not None:
-        _contiguous_f32(grad_rows, "grad_rows", (n,), dev)
+    _bwd_inputs(lse, grad_output, grad_rows, n, dev)
     if hidden_acc is not None:
         _contiguous_f32(hidden_acc, "hidden_acc", (n, h), dev)
     if grad_hidden is not None:
-        _require(grad_hidden, "grad_hidden", torch.bfloat16, 2, dev)
-        if tuple(grad_hidden.shape) != (n, h) or not grad_hidden.is_contiguous():
-            raise ValueError(f"grad_hidden must be a contiguous {(n, h)} tensor")
-    if grad_weight is not None:
-        _require(grad_weight, "grad_weight", None, 2, dev)
-        if tuple(grad_weight.shape) != (v, h) or not grad_weight.is_contiguous():
-            raise ValueError(f"grad_weight must be a contiguous {(v, h)} tensor")
-    if grad_bias is not None:
-        _contiguous_f32(grad_bias, "grad_bias", (v,), dev)
+        _bwd_hidden(grad_hidden, n, h, dev)
+    _bwd_params(grad_weight, grad_bias, v, h, dev)
     flags = ((FLCE_PIECE_FIRST if first else 0) | (FLCE_PIECE_LAST if last else 0)
              | (FLCE_PIECE_ACCUMULATE if accumulate else 0))
     ws = _workspace(flce_piece_bwd_workspace_size(n, h, v), dev, workspace)
-    wcode = 0 if grad_weight is None else _dtype_code(grad_weight.dtype, "grad_weight")
-    _call("flce_piece_bwd", dev, hidden.data_ptr(), weight.data_ptr(), _adr(bias),
-          labels.data_ptr(), lse.data_ptr(), n, h, v, v_start, vocab, ignore_index,
-          _count_arg(num_label_tokens), flags, _adr(grad_output), _adr(grad_rows),
-          _adr(hidden_acc), _adr(grad_hidden), _adr(grad_weight), wcode, _adr(grad_bias),
-          ws.data_ptr(), _bytes_of(ws))
+    _piece_bwd(hidden.contiguous(), weight, bias, labels, lse, n, h, v, v_start, vocab,
+               ignore_index, _count_arg(num_label_tokens), flags, grad_output, grad_rows,
+               hidden_acc, grad_hidden, grad_weight, grad_bias, ws, dev)
 
 
 def _as_pieces(weight, bias):
@@ -929,19 +962,23 @@ def flce_pieces_fwd(hidden, weight, labels, bias=None, *, ignore_index: int = -1
     import torch
     pieces, _ = _as_pieces(weight, bias)
     _require(hidden, "hidden", torch.bfloat16, 2)
+    hidden = hidden.contiguous()
     dev = hidden.device
-    n = hidden.shape[0]
+    n, h = hidden.shape
     labels = _labels_i32(labels, n, dev, ignore_index)
-    vocab = sum(w.shape[0] for w, _ in pieces)
+    pieces = [_piece_weight(w, b, h, dev) for w, b in pieces]
+    vocab = sum(v for _, _, v in pieces)
     state = torch.empty((3, n), dtype=torch.float32, device=dev)
+    # one workspace for all of it: the calls follow one another on one stream
+    ws = _workspace(max(flce_piece_loss_workspace_size(n),
+                        *(flce_piece_fwd_workspace_size(n, h, v) for _, _, v in pieces)), dev)
     start = 0
-    for w, b in pieces:
-        flce_piece_fwd(hidden, w, labels, state, b, v_start=start, vocab=vocab, first=start == 0,
-                       ignore_index=ignore_index)
-        start += w.shape[0]
-    return flce_piece_loss(state, labels, vocab=vocab, ignore_index=ignore_index,
-                           num_label_tokens=num_label_tokens, return_rows=return_rows,
-                           status=status)
+    for w, b, v in pieces:
+        _piece_fwd(hidden, w, b, labels, state, n, h, v, start, vocab, start == 0, ignore_index,
+                   ws, dev)
+        start += v
+    return _piece_loss(state, labels, n, vocab, ignore_index, num_label_tokens, return_rows,
+                       status, ws, dev)
 
 
 # Bytes of the bf16 logit gradients that flce_pieces_bwd takes at a time by default.
@@ -979,56 +1016,59 @@ def flce_pieces_bwd(hidden, weight, labels, lse, bias=None, *, piece_size: int |
     dev = hidden.device
     n, h = hidden.shape
     labels = _labels_i32(labels, n, dev, ignore_index)
+    _bwd_inputs(lse, grad_output, grad_rows, n, dev)
     if grad_bias is None:
         grad_bias = bias is not None
+    if grad_bias is not False and bias is None:
+        raise ValueError("grad_bias needs a bias")
+    pieces = [_piece_weight(w, b, h, dev) for w, b in pieces]
 
-    def outs(spec, name, shapes, dtype):
+    def outs(spec, name, dtype, width):
         if spec is True:
             if accumulate:
                 raise ValueError(f"accumulate=True needs an existing {name}")
-            return [torch.empty(s, dtype=dtype, device=dev) for s in shapes]
+            return [torch.empty((v, *width), dtype=dtype, device=dev) for _, _, v in pieces]
         if spec is False or spec is None:
-            return [None] * len(shapes)
+            return [None] * len(pieces)
         spec = list(spec) if many else [spec]
-        if len(spec) != len(shapes):
-            raise ValueError(f"{len(shapes)} weight pieces but {len(spec)} of {name}")
+        if len(spec) != len(pieces):
+            raise ValueError(f"{len(pieces)} weight pieces but {len(spec)} of {name}")
         return spec
 
-    if grad_bias is not False and bias is None:
-        raise ValueError("grad_bias needs a bias")
-    gws = outs(grad_weight, "grad_weight", [tuple(w.shape) for w, _ in pieces], torch.bfloat16)
-    gbs = outs(grad_bias, "grad_bias", [(w.shape[0],) for w, _ in pieces], torch.float32)
+    gws = outs(grad_weight, "grad_weight", torch.bfloat16, (h,))
+    gbs = outs(grad_bias, "grad_bias", torch.float32, ())
     gh = grad_hidden
     if gh is True:
         gh = torch.empty((n, h), dtype=torch.bfloat16, device=dev)
     elif gh is False:
         gh = None
-    vocab = sum(w.shape[0] for w, _ in pieces)
-    jobs = []  # (weight, bias, grad_weight, grad_bias, first class)
+    elif gh is not None:
+        _bwd_hidden(gh, n, h, dev)
+    vocab = sum(v for _, _, v in pieces)
+    jobs = []  # (weight, bias, grad_weight, grad_bias, first class, classes)
     start = 0
-    for (w, b), gw, gb in zip(pieces, gws, gbs):
-        v = w.shape[0]
-        for t, name in ((gw, "grad_weight"), (gb, "grad_bias")):
-            if t is not None and (t.shape[:1] != w.shape[:1] or not t.is_contiguous()):
-                raise ValueError(f"{name} must be contiguous and of its weight's size")
+    for (w, b, v), gw, gb in zip(pieces, gws, gbs):
+        _bwd_params(gw, gb, v, h, dev)
         step = _piece_rows(n, v, piece_size)
-        w = w.contiguous()
-        for lo in range(0, v, step):
-            part = slice(lo, min(v, lo + step))
-            jobs.append((w[part], *(None if t is None else t[part] for t in (b, gw, gb)),
-                         start + lo))
+        if step >= v:
+            jobs.append((w, b, gw, gb, start, v))
+        else:
+            for lo in range(0, v, step):
+                part = slice(lo, min(v, lo + step))
+                jobs.append((*(None if t is None else t[part] for t in (w, b, gw, gb)),
+                             start + lo, part.stop - lo))
         start += v
     acc = None
     if gh is not None and len(jobs) > 1:
         acc = torch.empty((n, h), dtype=torch.float32, device=dev)
-    need = max((flce_piece_bwd_workspace_size(n, h, w.shape[0]) for w, *_ in jobs), default=0)
-    ws = _workspace(need, dev)
-    for k, (w, b, gw, gb, at) in enumerate(jobs):
-        flce_piece_bwd(hidden, w, labels, lse, b, v_start=at, vocab=vocab, first=k == 0,
-                       last=k == len(jobs) - 1, ignore_index=ignore_index,
-                       num_label_tokens=num_label_tokens, accumulate=accumulate,
-                       grad_output=grad_output, grad_rows=grad_rows, hidden_acc=acc,
-                       grad_hidden=gh, grad_weight=gw, grad_bias=gb, workspace=ws)
+    ws = _workspace(max(flce_piece_bwd_workspace_size(n, h, j[5]) for j in jobs), dev)
+    count = _count_arg(num_label_tokens)
+    for k, (w, b, gw, gb, at, v) in enumerate(jobs):
+        flags = ((FLCE_PIECE_FIRST if k == 0 else 0)
+                 | (FLCE_PIECE_LAST if k == len(jobs) - 1 else 0)
+                 | (FLCE_PIECE_ACCUMULATE if accumulate else 0))
+        _piece_bwd(hidden, w, b, labels, lse, n, h, v, at, vocab, ignore_index, count, flags,
+                   grad_output, grad_rows, acc, gh, gw, gb, ws, dev)
     return gh, gws if many else gws[0], gbs if many else gbs[0]
 
 

@@ -35,10 +35,11 @@ int norm_check_shape(int64_t n, int64_t h) {
   return n < 0 || n > kI32Max || h < 1 || h > LAYERNORM_MAX_H ? LCE_ERR_BAD_SHAPE : LCE_OK;
 }
 
-// The row limit keeps every byte offset inside one K slice of a 64-column panel below 2^32.
+// The row limit keeps every byte offset inside one K slice of a 64-column panel below 2^32, the
+// limit of 256 x 256 tiles a launch's threads (512 a tile).
 int piece_check_shape(int64_t n, int64_t h, int64_t v) {
   if (n < 0 || n > (int64_t(1) << 23) || h < 1 || h % 8 != 0 || h > (int64_t(1) << 20) || v < 1 ||
-      v > kI32Max)
+      v > kI32Max || (n + 255) / 256 * ((v + 255) / 256) >= (int64_t(1) << 23))
     return LCE_ERR_BAD_SHAPE;
   return LCE_OK;
 }

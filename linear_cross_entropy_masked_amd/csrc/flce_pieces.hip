@@ -36,6 +36,7 @@ namespace {
 using gemm::View;
 using gemm::f32x4_t;
 using Wide = gemm::v2::CfgWide;
+using Pair = gemm::v2::CfgPair;
 using Narrow = gemm::v2::Cfg<128, 256, 64, 3, 2, 4, 1>;
 
 __host__ __device__ inline int64_t up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
@@ -45,6 +46,11 @@ constexpr int kTile = Wide::BM;  // rows of an output tile; the gathered rows ar
 // rows 221 / 223 / 221 on 128 x 256 tiles and 269 / 271 / 267 on 256 x 256 tiles (20 rows: 204,
 // 229, 275); 256 rows take 284 us on 256 x 256 tiles and 317 on 128 x 256.
 constexpr int kScoreRows = 32;
+// The weight gradient's contraction is as long as the batch. Up to this many rows it is mostly
+// stores, and two 256 x 128 workgroups per CU overlap them (step of 60 rows of 2048 and 60000
+// classes 306 us against 323, of 500 rows and 32000 classes 338 against 344, of 1000 rows of 4096
+// 1005 against 994).
+constexpr int kShortK = 512;
 constexpr int kNarrowRows = 128;
 
 __device__ __forceinline__ bool labelled(int32_t y, int64_t vocab, int32_t ignore_index) {
@@ -194,15 +200,17 @@ __global__ void __launch_bounds__(256) gather_rows_kernel(GatherArgs a) {
 }
 
 // Numbering and gathering in one launch, for batches short enough that every workgroup can count
-// the labelled rows before its own: kFewEach rows per workgroup.
+// the labelled rows before its own: `each` rows per workgroup (one for the shortest batches, where
+// a row's copy is all latency, up to kFewEach; a divisor of kTile).
 constexpr int64_t kFewRows = 8192;
 constexpr int kFewEach = 8;
+int few_each(int64_t n) { return n <= 1024 ? 1 : n <= 4096 ? 4 : kFewEach; }
 __global__ void __launch_bounds__(256) gather_few_rows_kernel(
     GatherArgs a, const int32_t* __restrict__ labels, int64_t v, int64_t v_start, int64_t vocab,
-    int32_t ignore_index, float* __restrict__ state) {
-  const int64_t batch = (a.n + kFewEach - 1) / kFewEach;
+    int32_t ignore_index, int each, float* __restrict__ state) {
+  const int64_t batch = (a.n + each - 1) / each;
   const bool padding = int64_t(blockIdx.x) >= batch;
-  const int64_t i0 = padding ? a.n : int64_t(blockIdx.x) * kFewEach;
+  const int64_t i0 = padding ? a.n : int64_t(blockIdx.x) * each;
   int before = 0;
   for (int64_t j = threadIdx.x; j < i0; j += 256)
     before += labelled(labels[j], vocab, ignore_index);
@@ -214,11 +222,11 @@ __global__ void __launch_bounds__(256) gather_few_rows_kernel(
   int64_t m = (wave_sum[0] + wave_sum[1]) + (wave_sum[2] + wave_sum[3]);
   if (padding) {
     if (int64_t(blockIdx.x) == batch && threadIdx.x == 0) *a.count = int32_t(m);
-    for (int k = 0; k < kFewEach; ++k)
-      pad_row(a, m + (int64_t(blockIdx.x) - batch) * kFewEach + k, m);
+    for (int k = 0; k < each; ++k)
+      pad_row(a, m + (int64_t(blockIdx.x) - batch) * each + k, m);
     return;
   }
-  for (int64_t i = i0; i < i0 + kFewEach && i < a.n; ++i) {
+  for (int64_t i = i0; i < i0 + each && i < a.n; ++i) {
     const int32_t y = labels[i];
     if (labelled(y, vocab, ignore_index)) {
       gather_row(a, i, m);
@@ -240,12 +248,14 @@ __global__ void __launch_bounds__(256) gather_few_rows_kernel(
 }
 
 // W [v, h] to [v, h64], zero-padded (h not a multiple of the K slice).
-__global__ void __launch_bounds__(256) pad_rows_kernel(const uint16_t* __restrict__ w, int64_t h,
-                                                       int64_t h64, uint16_t* __restrict__ out) {
-  const int64_t r = blockIdx.x;
-  for (int64_t c = 8 * int64_t(threadIdx.x); c < h64; c += 8 * 256)
-    *reinterpret_cast<uint4*>(out + r * h64 + c) =
-        c < h ? *reinterpret_cast<const uint4*>(w + r * h + c) : uint4{0u, 0u, 0u, 0u};
+constexpr int64_t kPadGrid = 65536;
+__global__ void __launch_bounds__(256) pad_rows_kernel(const uint16_t* __restrict__ w, int64_t v,
+                                                       int64_t h, int64_t h64,
+                                                       uint16_t* __restrict__ out) {
+  for (int64_t r = blockIdx.x; r < v; r += gridDim.x)
+    for (int64_t c = 8 * int64_t(threadIdx.x); c < h64; c += 8 * 256)
+      *reinterpret_cast<uint4*>(out + r * h64 + c) =
+          c < h ? *reinterpret_cast<const uint4*>(w + r * h + c) : uint4{0u, 0u, 0u, 0u};
 }
 
 // ------------------------------------------------------------------ forward
@@ -628,8 +638,9 @@ struct EpiPieceHidden {
 
 // The product split over K: partial sums [splits][rows of the tiles that count][h], then added in
 // split order. Where fewer rows carry a label than the launch has tiles for, K is cut into as many
-// more ranges, of at least kSplitK classes each: the same workgroups and the same memory.
-constexpr int64_t kSplitK = 1024;
+// more ranges, of at least kSplitK classes each (a step of 100 rows of 256 and 2000 classes takes
+// 112 us with ranges of 1024, 82 with 256): the same workgroups and the same memory.
+constexpr int64_t kSplitK = 256;
 __host__ __device__ inline int64_t piece_splits(int64_t m_tiles, int64_t live, int64_t splits,
                                                 int64_t v) {
   const int64_t most = v / kSplitK > splits ? v / kSplitK : splits;
@@ -817,9 +828,10 @@ hipError_t rows_and_gather(const uint16_t* hidden, const int32_t* labels, int64_
   g.hc = w.hc;
   TimedLaunch t(s, K_PIECE_GATHER);
   if (n <= kFewRows) {
-    const int64_t blocks = (n + kFewEach - 1) / kFewEach + kTile / kFewEach;
+    const int each = few_each(n);
+    const int64_t blocks = (n + each - 1) / each + kTile / each;
     hipLaunchKernelGGL(gather_few_rows_kernel, dim3(unsigned(blocks)), dim3(256), 0, s, g, labels,
-                       v, v_start, vocab, ignore_index, state);
+                       v, v_start, vocab, ignore_index, each, state);
     return hipGetLastError();
   }
   hipLaunchKernelGGL(piece_rows_kernel, dim3(1), dim3(1024), 0, s, labels, n, v, v_start, vocab,
@@ -831,8 +843,8 @@ hipError_t rows_and_gather(const uint16_t* hidden, const int32_t* labels, int64_
 
 hipError_t pad_weight(const uint16_t* weight, int64_t h, int64_t v, uint16_t* out, hipStream_t s) {
   TimedLaunch t(s, K_PIECE_GATHER);
-  hipLaunchKernelGGL(pad_rows_kernel, dim3(unsigned(v)), dim3(256), 0, s, weight, h,
-                     up(h, Wide::BK), out);
+  hipLaunchKernelGGL(pad_rows_kernel, dim3(unsigned(std::min(v, kPadGrid))), dim3(256), 0, s,
+                     weight, v, h, up(h, Wide::BK), out);
   return hipGetLastError();
 }
 
@@ -854,6 +866,8 @@ hipError_t grad_weight_product(const PieceBwdArgs& a, const PieceWs& w, const Vi
   EpiPieceWeight<TW, ACC> e{static_cast<TW*>(a.grad_weight), a.h, w.count, a.num_label_tokens,
                             a.grad_output, int(a.grad_rows != nullptr), 0.f};
   TimedLaunch t(s, K_PIECE_GRAD_WEIGHT);
+  if (a.n <= kShortK)
+    return gemm::v2::launch<Pair, false, false>(dv, hv, a.v, a.h, up(a.n, kTile), 1, false, e, s);
   return gemm::v2::launch<Wide, false, false>(dv, hv, a.v, a.h, up(a.n, kTile), 1, true, e, s,
                                               true);
 }

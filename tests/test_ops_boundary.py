@@ -134,6 +134,7 @@ def test_piece_refusals(lib):
     assert call(start=1) == BAD_SHAPE and call(start=-1) == BAD_SHAPE
     assert call(vocab=9) == BAD_SHAPE and call(vocab=1 << 31) == BAD_SHAPE
     assert call(n=(1 << 23) + 1) == BAD_SHAPE and call(h=(1 << 20) + 8) == BAD_SHAPE
+    assert call(n=1 << 23, v=65536, vocab=65536) == BAD_SHAPE  # 2^23 tiles of 256 x 256
     assert call(hid=None) == NULL_ARG and call(w=None) == NULL_ARG and call(state=None) == NULL_ARG
     assert call(ws=None) == WORKSPACE and call(wsb=1) == WORKSPACE
     assert call(hid=A[0] + 8) == ALIGN and call(w=A[1] + 2) == ALIGN and call(ws=A[5] + 8) == ALIGN
