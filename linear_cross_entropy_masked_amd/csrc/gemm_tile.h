@@ -162,6 +162,8 @@ __device__ __forceinline__ int64_t xcd_tile(int64_t w, int64_t total) {
 struct TileMap {
   int64_t m_tiles, n_tiles, splits;
   bool m_fast;  // true: consecutive tiles walk m (sharing the B tile), else walk n
+  int band = 0;  // > 0 (pipelined kernel, one split): tiles go band after band of so many m-tiles,
+                 // m fastest within a band, so that the tiles in flight on an XCD form a block
   int xn = 0;   // > 0 (pipelined kernel, one split): the 8 XCDs own a (8 / xn) × xn grid of
                 // m × n tile blocks, so each XCD's L2 sees 1 / xn of the B operand
 };
@@ -608,6 +610,12 @@ __device__ __forceinline__ bool tile_coord(const TileMap& tm, int64_t w, TileCoo
   const int64_t mn = tm.m_tiles * tm.n_tiles;
   const int64_t tile = xcd_tile(w, mn * tm.splits);
   const int64_t rest = tile % mn;
+  if (tm.band > 0) {
+    const int64_t b = rest / (tm.band * tm.n_tiles), in = rest - b * tm.band * tm.n_tiles;
+    const int64_t left = tm.m_tiles - b * tm.band, wide = left < tm.band ? left : tm.band;
+    t = TileCoord{b * tm.band + in % wide, in / wide, tile / mn};
+    return true;
+  }
   t = TileCoord{tm.m_fast ? rest % tm.m_tiles : rest / tm.n_tiles,
                 tm.m_fast ? rest / tm.m_tiles : rest % tm.n_tiles, tile / mn};
   return true;
@@ -940,7 +948,8 @@ __global__ void __launch_bounds__(C::THREADS, C::OCC)
 // when B is re-read by every m-tile and too large for one L2.
 template <class C, bool AK, bool BKM, class Epi, bool SEGA = false>
 hipError_t launch(const View& A, const View& B, int64_t M, int64_t N, int64_t K, int64_t splits,
-                  bool m_fast, const Epi& epi, hipStream_t s, bool xcd_blocks = false) {
+                  bool m_fast, const Epi& epi, hipStream_t s, bool xcd_blocks = false,
+                  int band = 0) {
   // grouped K-major operands keep whole groups of 64 (see stream_at)
   if ((AK && A.gs < 64) || (BKM && B.gs < 64)) return hipErrorInvalidValue;
   // a two-segment A: MN-major rows or K-major panel columns, both segments given, split at a
@@ -952,6 +961,7 @@ hipError_t launch(const View& A, const View& B, int64_t M, int64_t N, int64_t K,
   TileMap tm{(M + C::BM - 1) / C::BM, (N + C::BN - 1) / C::BN, splits < 1 ? 1 : splits, m_fast};
   int64_t ksplit = (K + tm.splits - 1) / tm.splits;
   ksplit = (ksplit + C::BK - 1) / C::BK * C::BK;
+  tm.band = band;
   int64_t grid = tm.m_tiles * tm.n_tiles * tm.splits;
   if (xcd_blocks && tm.splits == 1 && tm.m_tiles >= 8) {
     tm.xn = tm.n_tiles % 4 == 0 ? 4 : (tm.n_tiles % 2 == 0 ? 2 : 1);
