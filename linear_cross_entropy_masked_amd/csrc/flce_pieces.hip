@@ -71,12 +71,9 @@ __device__ __forceinline__ float loss_scale(const int32_t* count, long long t_ho
   return t > 0 ? float(double(gout ? *gout : 1.f) / double(t)) : 0.f;
 }
 
-// A logit of minus infinity (a vocabulary entry that the bias masks) takes part as the lowest
-// finite value: its exponential is 0 beside any other, and a tile of nothing else has a maximum
-// that can be subtracted. NaN stays NaN.
-__device__ __forceinline__ float finite_low(float z) {
-  return z == -INFINITY ? -3.4028234663852886e38f : z;
-}
+// The least maximum a block's exponentials are taken about: where the bias masks every class of a
+// block with minus infinity, there is then a number to subtract, and the sum is 0.
+constexpr float kLeastMax = -3.4028234663852886e38f;
 
 // ------------------------------------------------------------------ the labelled rows
 
@@ -207,10 +204,10 @@ __global__ void __launch_bounds__(256) gather_rows_kernel(GatherArgs a) {
 
 // Numbering and gathering in one launch, for batches short enough that every workgroup can count
 // the labelled rows before its own: `each` rows per workgroup (one for the shortest batches, where
-// a row's copy is all latency, up to kFewEach; a divisor of kTile).
+// a row's copy is all latency, else kFewEach; a divisor of kTile).
 constexpr int64_t kFewRows = 8192;
-constexpr int kFewEach = 8;
-int few_each(int64_t n) { return n <= 1024 ? 1 : n <= 4096 ? 4 : kFewEach; }
+constexpr int kFewEach = 4;
+int few_each(int64_t n) { return n <= 1024 ? 1 : kFewEach; }
 __global__ void __launch_bounds__(256) gather_few_rows_kernel(
     GatherArgs a, const int32_t* __restrict__ labels, int64_t v, int64_t v_start, int64_t vocab,
     int32_t ignore_index, int each, float* __restrict__ state) {
@@ -397,9 +394,9 @@ __global__ void __launch_bounds__(256) score_kernel(
     x[e] = ((z[0][c][t] + z[1][c][t]) + z[2][c][t]) + z[3][c][t];
     if (r < v && bias) x[e] += bias[r];
     if (r < v && t < n && int64_t(y) == v_start + r) zy[t] = x[e];
-    x[e] = finite_low(x[e]);
     if (r < v) m = fmaxf(m, x[e]);
   }
+  m = fmaxf(m, kLeastMax);
 #pragma unroll
   for (int e = 0; e < kEach; ++e)
     if (r0 + e * kShare + sub < v) s += fast_exp2((x[e] - m) * kLog2e);

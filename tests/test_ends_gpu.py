@@ -247,7 +247,7 @@ def test_step_against_fp64_autograd(dev):
     rows = torch.logsumexp(z, 1) - z.gather(1, lab.cpu().clamp(min=0)[:, None])[:, 0]
     ref = rows[keep].mean()
     ref.backward()
-    assert abs(float(loss) - float(ref)) <= 2.0 ** -5 * abs(float(ref))
+    assert abs(loss.item() - ref.item()) <= 2.0 ** -5 * abs(ref.item())
     d = (head.main_grad.double().cpu() - w.grad).norm() / w.grad.norm()
     assert d <= 2.0 ** -5
 

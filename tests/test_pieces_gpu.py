@@ -242,6 +242,27 @@ def test_classes_masked_by_the_bias(dev, n):
         assert not cat(gw)[:700].any() and not cat(gb)[:700].any()
 
 
+@pytest.mark.parametrize("n", [20, 100, 300])
+def test_every_class_masked(dev, n):
+    """A bias of minus infinity throughout: the logsumexp is minus infinity, whichever kernel ran;
+    and one that leaves a single class gives that class's logit."""
+    hid, w, b, lab = make(dev, n, 64, 900, masked=0.0)
+    b[:] = float("-inf")
+    _, lse, _ = lce.flce_pieces_fwd(hid, w, lab, b)
+    assert torch.isneginf(lse).all()
+    b[700] = 0.25
+    lab[:] = 700
+    loss, lse, rows = lce.flce_pieces_fwd(hid, w, lab, b, return_rows=True)
+    assert float(loss) == 0 and not rows.any()
+    near(lse, hid.double() @ w[700].double() + 0.25,
+         67 * U * (hid.double().abs() @ w[700].double().abs()) + 2 * U, "lse")
+    gh, gw, gb = lce.flce_pieces_bwd(hid, w, lab, lse, b)
+    # the two forward kernels and the backward's product add a logit in different orders
+    off = float((67 * U * (hid.double().abs() @ w[700].double().abs())).max()) * 2 + 4 * U
+    assert (gw[:700] == 0).all() and (gw[701:] == 0).all()
+    assert float(gb.abs().max()) <= 2 * off
+
+
 @pytest.mark.parametrize("n", [12, 400])
 def test_row_gradients(dev, n):
     """Each row's term with its own upstream gradient, among them 0."""
@@ -296,6 +317,24 @@ def test_peaked_rows(dev):
     loss, lse, rows = lce.flce_pieces_fwd(hid, w, lab, b2, return_rows=True)
     check_fwd(e, loss, lse, rows)
     check_bwd(e, *lce.flce_pieces_bwd(hid, w, lab, lse, b2))
+
+
+@pytest.mark.parametrize("n,h,v", [(260, 64, 32777), (1003, 72, 32769), (2048, 64, 32784),
+                                   (300, 200, 32785)])
+@pytest.mark.parametrize("bias", [True, False])
+def test_classes_past_a_multiple_of_the_tile(dev, n, h, v, bias):
+    """A last tile of few classes, with labels and the largest bias among them."""
+    hid, w, b, lab = make(dev, n, h, v, bias=bias)
+    lab[::9] = torch.arange(len(lab[::9]), device=dev, dtype=torch.int32) % (v % 256) + v // 256 * 256
+    if bias:
+        b[v - 1] = 3.0
+    e = Exact(hid, w, b, lab)
+    loss, lse, rows = lce.flce_pieces_fwd(hid, w, lab, b, return_rows=True)
+    check_fwd(e, loss, lse, rows)
+    check_bwd(e, *lce.flce_pieces_bwd(hid, w, lab, lse, b))
+    g = torch.randn(n, device=dev)
+    check_bwd(Exact(hid, w, b, lab, rows=g),
+              *lce.flce_pieces_bwd(hid, w, lab, lse, b, grad_rows=g))
 
 
 def test_long_batches(dev):
