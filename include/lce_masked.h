@@ -329,7 +329,7 @@ int flce_piece_bwd_workspace_size(int64_t n, int64_t h, int64_t v, size_t* bytes
 
 /* Takes one piece into the state: fp32 [3, n] holding per row the largest logit so far, the sum
  * of exp(z - that), and the label's logit (0 until its piece has come). Rows without a label hold
- * (-inf, 0, 0). flags: FLCE_PIECE_FIRST. Up to 64 rows take a kernel of their own, bound by
+ * (-inf, 0, 0). flags: FLCE_PIECE_FIRST. Up to 32 rows take a kernel of their own, bound by
  * reading the weight once. States over disjoint pieces of one vocabulary, as the ranks of a split
  * head hold them, combine to (m, s, z) = (max of m, sum of s * exp(m_k - m), sum of z). */
 int flce_piece_fwd(const uint16_t* hidden, const uint16_t* weight, const float* bias,

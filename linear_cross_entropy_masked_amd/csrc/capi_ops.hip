@@ -177,7 +177,7 @@ int layernorm_bwd(const void* grad, int dtype, int64_t ldg, const void* x, int64
   {
     const bool inplace = grad == grad_x && ldg == lddx;
     const Span wr[] = {span(params ? workspace : nullptr, int64_t(need)),
-                       span(grad_x, matrix_bytes(n, lddx, h, el)), span(grad_weight, gl * h),
+                       span(grad_x, grad_x ? matrix_bytes(n, lddx, h, el) : 0), span(grad_weight, gl * h),
                        span(grad_bias, gl * h)};
     const Span rd[] = {span(inplace ? nullptr : grad, matrix_bytes(n, ldg, h, el)),
                        span(x, matrix_bytes(n, ldx, h, el)), span(mean, 4 * n),

@@ -6,14 +6,14 @@
 //             dw (=|+=) Σ_rows g · x̂,   db (=|+=) Σ_rows g
 //
 // Memory-bound: 2 · n · h elements move in the forward ([32768, 8192] bf16: 188 us, 5.7 TB/s; a
-// copy of 2 GiB reaches 4.9), 3 · n · h in the backward ([8192, 4096] bf16: 50 us, 4.0 TB/s,
+// copy of 2 GiB reaches 4.9), 3 · n · h in the backward ([8192, 4096] bf16: 47 us, 4.2 TB/s,
 // what is left being the partial rows below and the start of each workgroup). A row lives in
 // the registers of WPR wavefronts (at most 32 elements a lane) from its one read to its one
 // write; the mean is known before the squares are summed, so the variance does not cancel. Rows
-// are dealt to a fixed grid, each lane loading the next row's vectors before the sums of this. In the backward every lane keeps the columns it owns for all of its
-// rows and adds their dw and db terms in fp32 registers; each workgroup writes one partial row
-// of each, and param_reduce_kernel adds those in workgroup order (no atomics: a result does not
-// change from run to run).
+// are dealt to a fixed grid, each lane loading the next row's vectors before the sums of this. In
+// the backward every lane keeps the columns it owns for all of its rows and adds their dw and db
+// terms in fp32 registers; each workgroup writes one partial row of each, and param_reduce_kernel
+// adds those in workgroup order (no atomics: a result does not change from run to run).
 #include <algorithm>
 
 #include "common.h"
@@ -53,9 +53,10 @@ __device__ __forceinline__ float wave_sum(float x) {
   x = add_lanes<0x4E>(x);   // lane ^ 2
   x = add_lanes<0x141>(x);  // mirrored within 8: the other four
   x = add_lanes<0x140>(x);  // mirrored within 16: the other eight
-  const auto r = __builtin_amdgcn_permlane16_swap(__float_as_int(x), __float_as_int(x), false, false);
-  x = __int_as_float(r[0]) + __int_as_float(r[1]);
-  const auto h = __builtin_amdgcn_permlane32_swap(__float_as_int(x), __float_as_int(x), false, false);
+  int i = __float_as_int(x);
+  const auto r = __builtin_amdgcn_permlane16_swap(i, i, false, false);
+  i = __float_as_int(__int_as_float(r[0]) + __int_as_float(r[1]));
+  const auto h = __builtin_amdgcn_permlane32_swap(i, i, false, false);
   return __int_as_float(h[0]) + __int_as_float(h[1]);
 }
 
