@@ -314,9 +314,10 @@ int flce_bwd(const uint16_t* hidden, const uint16_t* weight, const float* bias,
  *
  * Labels are classes of the whole vocabulary. A row carries a label when label != ignore_index
  * and 0 <= label < vocab. Rows without one take no part in any product, whatever they hold.
- * Limits: h a multiple of 8, h <= 2^20, n <= 2^23, 1 <= v, 0 <= v_start, v_start + v <= vocab
- * < 2^31, and fewer than 2^23 tiles of 256 rows by 256 classes of a piece. A bias of minus infinity masks a class. hidden, weight, bias and the gradients are
- * contiguous; 16-byte aligned where they are bf16 or the fp32 hidden_acc / grad_weight. */
+ * Limits: h a multiple of 8, h <= 2^20, n <= 2^23, 1 <= v <= 2^29, 0 <= v_start,
+ * v_start + v <= vocab < 2^31, and fewer than 2^23 tiles of 256 rows by 256 classes of a piece.
+ * A bias of minus infinity masks a class. hidden, weight, bias and the gradients are contiguous;
+ * 16-byte aligned where they are bf16 or the fp32 hidden_acc / grad_weight. */
 
 #define FLCE_PIECE_FIRST         1u /* the first piece: state / hidden_acc are overwritten        */
 #define FLCE_PIECE_LAST          2u /* flce_piece_bwd: the last piece, grad_hidden is written     */
@@ -376,7 +377,8 @@ int flce_piece_bwd(const uint16_t* hidden, const uint16_t* weight, const float* 
  * table's type; exactly 0 for rows without a token.
  *   weight   dtype [v, ldw], first h columns      tokens  int32 [n]
  *   out      dtype [n, ldo], first h columns; the columns past h are left as they are
- * Any row stride >= h and any alignment of an element are accepted. n == 0 is valid. */
+ * Any row stride >= h and any alignment of an element are accepted. n == 0 is valid; h <= 2^20,
+ * n and v < 2^31, and out holds less than 128 GiB (64 bytes more a row counted). */
 int embed_fwd(const void* weight, int dtype, int64_t v, int64_t h, int64_t ldw,
               const int32_t* tokens, int64_t n, int32_t ignore_index, float scale, void* out,
               int64_t ldo, int32_t* status_out, void* stream);
@@ -394,7 +396,8 @@ int embed_workspace_size(int64_t n, int64_t h, int64_t v, size_t* bytes);
  * grad_weight is written, with 0 where no row has its token; with it, rows without a token are
  * not touched. Rows of grad without a token are not read.
  *   grad         dtype [n, ldg], first h columns
- *   grad_weight  grad_dtype [v, ldw], first h columns; grad_dtype is dtype or LCE_DTYPE_F32 */
+ *   grad_weight  grad_dtype [v, ldw], first h columns; grad_dtype is dtype or LCE_DTYPE_F32
+ * h <= 2^20, n <= 2^28, v <= 2^27, v * h <= 2^36, n * (h + 512) < 2^40. */
 int embed_bwd(const void* grad, int dtype, int64_t ldg, const int32_t* tokens, int64_t n,
               int64_t h, int64_t v, int32_t ignore_index, float scale, uint32_t flags,
               void* grad_weight, int grad_dtype, int64_t ldw, int32_t* status_out,
@@ -419,7 +422,7 @@ int layernorm_fwd(const void* x, int dtype, int64_t n, int64_t h, int64_t ldx, c
 /* flags of layernorm_bwd */
 #define LAYERNORM_ACCUMULATE     1u /* add into grad_weight and grad_bias                        */
 
-/* Workspace bytes of layernorm_bwd: one partial row of each parameter gradient for at most 256
+/* Workspace bytes of layernorm_bwd: one partial row of each parameter gradient for at most 512
  * workgroups. Host-only. */
 int layernorm_workspace_size(int64_t n, int64_t h, size_t* bytes);
 

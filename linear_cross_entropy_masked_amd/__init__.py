@@ -639,8 +639,16 @@ def embed_fwd(weight, tokens, *, scale: float = 1.0, ignore_index: int = -100, o
     return out
 
 
+def _ignore_arg(ignore_index):
+    """ignore_index for the C ABI: one outside int32 would wrap onto a class."""
+    if not -(2 ** 31) <= ignore_index < 2 ** 31:
+        raise ValueError(f"ignore_index must fit in 32 bits, got {ignore_index}")
+    return ignore_index
+
+
 def _tokens_i32(tokens, device, ignore_index):
     import torch
+    _ignore_arg(ignore_index)
     _require(tokens, "tokens", None, 1, device)
     if tokens.dtype == torch.int32:
         return tokens.contiguous()
@@ -849,7 +857,7 @@ def flce_piece_fwd(hidden, weight, labels, state, bias=None, *, v_start: int, vo
     dev = hidden.device
     n, h = hidden.shape
     weight, bias, v = _piece_weight(weight, bias, h, dev)
-    labels = _labels_i32(labels, n, dev, ignore_index)
+    labels = _labels_i32(labels, n, dev, _ignore_arg(ignore_index))
     _contiguous_f32(state, "state", (3, n), dev)
     ws = _workspace(flce_piece_fwd_workspace_size(n, h, v), dev, workspace)
     _piece_fwd(hidden.contiguous(), weight, bias, labels, state, n, h, v, v_start, vocab, first,
@@ -868,7 +876,7 @@ def flce_piece_loss(state, labels, *, vocab: int, ignore_index: int = -100,
     dev = state.device
     n = state.shape[1]
     _contiguous_f32(state, "state", (3, n), dev)
-    labels = _labels_i32(labels, n, dev, ignore_index)
+    labels = _labels_i32(labels, n, dev, _ignore_arg(ignore_index))
     ws = _workspace(flce_piece_loss_workspace_size(n), dev, workspace)
     return _piece_loss(state, labels, n, vocab, ignore_index, num_label_tokens, return_rows, status,
                        ws, dev)
@@ -924,7 +932,7 @@ def flce_piece_bwd(hidden, weight, labels, lse, bias=None, *, v_start: int, voca
     dev = hidden.device
     n, h = hidden.shape
     weight, bias, v = _piece_weight(weight, bias, h, dev)
-    labels = _labels_i32(labels, n, dev, ignore_index)
+    labels = _labels_i32(labels, n, dev, _ignore_arg(ignore_index))
     _bwd_inputs(lse, grad_output, grad_rows, n, dev)
     if hidden_acc is not None:
         _contiguous_f32(hidden_acc, "hidden_acc", (n, h), dev)
@@ -957,7 +965,7 @@ def _as_pieces(weight, bias):
 def flce_pieces_fwd(hidden, weight, labels, bias=None, *, ignore_index: int = -100,
                     num_label_tokens: int | None = None, return_rows: bool = False, status=None):
     """Linear CE forward over a weight [v, h] or a sequence of weights that hold consecutive
-    classes (with a sequence of biases, or None). Returns (loss, lse, rows) as
+    classes (with a sequence of biases, any of them None, or None). Returns (loss, lse, rows) as
     :func:`flce_piece_loss`; keep lse for :func:`flce_pieces_bwd`."""
     import torch
     pieces, _ = _as_pieces(weight, bias)
@@ -965,7 +973,7 @@ def flce_pieces_fwd(hidden, weight, labels, bias=None, *, ignore_index: int = -1
     hidden = hidden.contiguous()
     dev = hidden.device
     n, h = hidden.shape
-    labels = _labels_i32(labels, n, dev, ignore_index)
+    labels = _labels_i32(labels, n, dev, _ignore_arg(ignore_index))
     pieces = [_piece_weight(w, b, h, dev) for w, b in pieces]
     vocab = sum(v for _, _, v in pieces)
     state = torch.empty((3, n), dtype=torch.float32, device=dev)
@@ -1008,14 +1016,14 @@ def flce_pieces_bwd(hidden, weight, labels, lse, bias=None, *, piece_size: int |
     ``grad_hidden`` / ``grad_weight`` / ``grad_bias``: True to allocate, False to skip, or what to
     write into; grad_weight (bf16, or fp32 where given so) and grad_bias are sequences where
     weight is one, and are added to with ``accumulate``. grad_bias defaults to True when a bias
-    is given. Returns (grad_hidden, grad_weight, grad_bias)."""
+    is given (None for the pieces without one). Returns (grad_hidden, grad_weight, grad_bias)."""
     import torch
     pieces, many = _as_pieces(weight, bias)
     _require(hidden, "hidden", torch.bfloat16, 2)
     hidden = hidden.contiguous()
     dev = hidden.device
     n, h = hidden.shape
-    labels = _labels_i32(labels, n, dev, ignore_index)
+    labels = _labels_i32(labels, n, dev, _ignore_arg(ignore_index))
     _bwd_inputs(lse, grad_output, grad_rows, n, dev)
     if grad_bias is None:
         grad_bias = bias is not None
@@ -1027,7 +1035,8 @@ def flce_pieces_bwd(hidden, weight, labels, lse, bias=None, *, piece_size: int |
         if spec is True:
             if accumulate:
                 raise ValueError(f"accumulate=True needs an existing {name}")
-            return [torch.empty((v, *width), dtype=dtype, device=dev) for _, _, v in pieces]
+            return [torch.empty((v, *width), dtype=dtype, device=dev) if width or b is not None
+                    else None for _, b, v in pieces]
         if spec is False or spec is None:
             return [None] * len(pieces)
         spec = list(spec) if many else [spec]

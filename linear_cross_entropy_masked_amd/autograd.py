@@ -379,12 +379,11 @@ def _piece_grads(hidden, weights, biases, labels, lse, g, cfg, need_h, need_w, n
     for k, (b, need) in enumerate(zip(biases, need_b)):
         if need:
             gbs[k] = make(b, memory_format=torch.contiguous_format)
-    has_bias = biases[0] is not None
     gh, _, _ = flce_pieces_bwd(
-        hidden, weights, labels, lse, biases if has_bias else None, piece_size=piece_size,
+        hidden, weights, labels, lse, _any(biases), piece_size=piece_size,
         ignore_index=ignore_index, num_label_tokens=count, accumulate=buffers is not None,
         grad_output=None if per_row else g, grad_rows=g.contiguous() if per_row else None,
-        grad_hidden=bool(need_h), grad_weight=gws, grad_bias=gbs if has_bias else False)
+        grad_hidden=bool(need_h), grad_weight=gws, grad_bias=_any(gbs) or False)
     if buffers is not None:
         gws = [None] * len(weights)
     return gh, gws, gbs
@@ -396,7 +395,7 @@ class _LinearCEPieces(torch.autograd.Function):
         weights, biases = list(tensors[:pieces]), list(tensors[pieces:])
         ignore_index, count, per_row, _, _ = cfg
         loss, lse, rows = flce_pieces_fwd(
-            hidden, weights, labels, biases if biases[0] is not None else None,
+            hidden, weights, labels, _any(biases),
             ignore_index=ignore_index, num_label_tokens=count, return_rows=per_row)
         ctx.save_for_backward(hidden, labels, lse, *tensors)
         ctx.cfg, ctx.pieces = cfg, pieces
@@ -411,6 +410,11 @@ class _LinearCEPieces(torch.autograd.Function):
         gh, gws, gbs = _piece_grads(hidden, tensors[:k], tensors[k:], labels, lse, g, ctx.cfg,
                                     need[0], need[4:4 + k], need[4 + k:])
         return gh, None, None, None, *gws, *gbs
+
+
+def _any(tensors):
+    """The list, None where it holds nothing."""
+    return tensors if any(t is not None for t in tensors) else None
 
 
 def _piece_inputs(weight, bias, buffer):
@@ -437,9 +441,10 @@ def linear_cross_entropy_pieces(hidden, weight, labels, bias=None, *, mask=None,
                                 weight_grad_buffer=None):
     """:func:`linear_cross_entropy` over a weight in pieces of the vocabulary: one bf16 [V, H]
     tensor or a sequence of them holding consecutive classes (a base vocabulary and tokens added
-    to it), with fp32 biases likewise or None. The backward takes ``piece_size`` classes at a time
-    (default: so that their bf16 logit gradients stay within 512 MiB) and leaves each weight's
-    gradient in the weight's own type, without an fp32 [V, H] accumulator.
+    to it), with fp32 biases likewise (any of them None) or None. The backward takes
+    ``piece_size`` classes at a time (default: so that their bf16 logit gradients stay within
+    512 MiB) and leaves each weight's gradient in the weight's own type, without an fp32 [V, H]
+    accumulator.
 
     reduction: "sum", "mean" or "none" (the per-row terms, 0 for rows without a label; minus a
     term is the log-probability of the row's label, with its gradient). Rows without a label take
@@ -484,7 +489,7 @@ class _NormLinearCE(torch.autograd.Function):
         x = _rows(x)
         y, mean, rstd = layernorm_fwd(x, norm_weight, norm_bias, eps=eps)
         loss, lse, rows = flce_pieces_fwd(
-            y, weights, labels, biases if biases[0] is not None else None,
+            y, weights, labels, _any(biases),
             ignore_index=ignore_index, num_label_tokens=count, return_rows=per_row)
         ctx.save_for_backward(x, norm_weight, norm_bias, mean, rstd, labels, lse, *tensors)
         ctx.cfg, ctx.pieces, ctx.eps = cfg, pieces, eps
@@ -514,7 +519,7 @@ def norm_linear_cross_entropy(x, norm_weight, norm_bias, weight, labels, bias=No
     """:func:`layer_norm` of bf16 x [..., H], then :func:`linear_cross_entropy_pieces` of the
     result. Between forward and backward only x (which the model holds anyway) and three fp32
     values a row are kept: the backward normalises x again, and its hidden gradient becomes x's
-    in place."""
+    in place. A row without a label adds nothing to any gradient as long as its x is finite."""
     _check_reduction(reduction, num_label_tokens)
     weights, biases, buffers = _piece_inputs(weight, bias, weight_grad_buffer)
     flat = x.reshape(-1, x.shape[-1])

@@ -24,22 +24,38 @@ bool matrix_fits(int64_t rows, int64_t ld) {
   return !mul_overflows(rows, ld) && !mul_overflows(rows * ld, 4);
 }
 
-// n rows of h columns; rows and 1024-column blocks of them are what a grid counts.
+constexpr int64_t kThreadsMax = std::numeric_limits<uint32_t>::max();  // of one launch
+
 int embed_check_shape(int64_t n, int64_t h, int64_t v) {
-  if (n < 0 || v < 1 || h < 1 || h > (int64_t(1) << 20)) return LCE_ERR_BAD_SHAPE;
-  if (v > kI32Max || n > kI32Max || n * ((h + 1023) / 1024) > kI32Max) return LCE_ERR_BAD_SHAPE;
-  return LCE_OK;
+  return n < 0 || n > kI32Max || v < 1 || v > kI32Max || h < 1 || h > (int64_t(1) << 20)
+             ? LCE_ERR_BAD_SHAPE
+             : LCE_OK;
+}
+// The lookup takes a power of two of threads a row, 64 bytes each, where 256 of them hold it, and
+// whole workgroups of 256.
+bool lookup_fits(int64_t n, int64_t h, int64_t el) {
+  return n * (h * el / 32 + 2) + 256 <= kThreadsMax;
+}
+// The gradient takes 8 threads a position to sort, 16 a table row to zero (one per 64 bytes where
+// there are no positions), and at most h + 512 per chunk of up to 512 positions to sum and join.
+int embed_bwd_check_shape(int64_t n, int64_t h, int64_t v) {
+  if (embed_check_shape(n, h, v) != LCE_OK) return LCE_ERR_BAD_SHAPE;
+  return n > (int64_t(1) << 28) || v > (int64_t(1) << 27) || v * h > (int64_t(1) << 36) ||
+                 n / 512 * (h + 512) > kThreadsMax / 2
+             ? LCE_ERR_BAD_SHAPE
+             : LCE_OK;
 }
 
 int norm_check_shape(int64_t n, int64_t h) {
   return n < 0 || n > kI32Max || h < 1 || h > LAYERNORM_MAX_H ? LCE_ERR_BAD_SHAPE : LCE_OK;
 }
 
-// The row limit keeps every byte offset inside one K slice of a 64-column panel below 2^32, the
-// limit of 256 x 256 tiles a launch's threads (512 a tile).
+// The row limit keeps every byte offset inside one K slice of a 64-column panel below 2^32; the
+// limits of classes and of 256 x 256 tiles the threads of a launch (4 a class where few rows are
+// scored, 512 a tile).
 int piece_check_shape(int64_t n, int64_t h, int64_t v) {
   if (n < 0 || n > (int64_t(1) << 23) || h < 1 || h % 8 != 0 || h > (int64_t(1) << 20) || v < 1 ||
-      v > kI32Max || (n + 255) / 256 * ((v + 255) / 256) >= (int64_t(1) << 23))
+      v > (int64_t(1) << 29) || (n + 255) / 256 * ((v + 255) / 256) >= (int64_t(1) << 23))
     return LCE_ERR_BAD_SHAPE;
   return LCE_OK;
 }
@@ -60,7 +76,9 @@ int embed_fwd(const void* weight, int dtype, int64_t v, int64_t h, int64_t ldw,
   if (rc != LCE_OK) return rc;
   const int64_t el = dtype_size(dtype);
   if (!el) return LCE_ERR_BAD_DTYPE;
-  if (ldw < h || ldo < h || !matrix_fits(v, ldw) || !matrix_fits(n, ldo)) return LCE_ERR_BAD_SHAPE;
+  if (ldw < h || ldo < h || !matrix_fits(v, ldw) || !matrix_fits(n, ldo) ||
+      !lookup_fits(n, h, el))
+    return LCE_ERR_BAD_SHAPE;
   if (!weight || (n > 0 && (!tokens || !out))) return LCE_ERR_NULL_ARG;
   if (!aligned(weight, el) || !aligned(out, el) || !aligned(tokens, 4) || !aligned(status_out, 4))
     return LCE_ERR_ALIGNMENT;
@@ -78,7 +96,7 @@ int embed_fwd(const void* weight, int dtype, int64_t v, int64_t h, int64_t ldw,
 
 int embed_workspace_size(int64_t n, int64_t h, int64_t v, size_t* bytes) {
   if (!bytes) return LCE_ERR_NULL_ARG;
-  const int rc = embed_check_shape(n, h, v);
+  const int rc = embed_bwd_check_shape(n, h, v);
   if (rc != LCE_OK) return rc;
   *bytes = embed_workspace_bytes(n, h);
   return LCE_OK;
@@ -89,7 +107,7 @@ int embed_bwd(const void* grad, int dtype, int64_t ldg, const int32_t* tokens, i
               void* grad_weight, int grad_dtype, int64_t ldw, int32_t* status_out,
               void* workspace, size_t workspace_bytes, void* stream) {
   if (flags & ~EMBED_ACCUMULATE) return LCE_ERR_BAD_FLAGS;
-  int rc = embed_check_shape(n, h, v);
+  int rc = embed_bwd_check_shape(n, h, v);
   if (rc != LCE_OK) return rc;
   const int64_t el = dtype_size(dtype), wl = dtype_size(grad_dtype);
   if (!el || !wl || (grad_dtype != dtype && grad_dtype != LCE_DTYPE_F32)) return LCE_ERR_BAD_DTYPE;
@@ -177,8 +195,8 @@ int layernorm_bwd(const void* grad, int dtype, int64_t ldg, const void* x, int64
   {
     const bool inplace = grad == grad_x && ldg == lddx;
     const Span wr[] = {span(params ? workspace : nullptr, int64_t(need)),
-                       span(grad_x, grad_x ? matrix_bytes(n, lddx, h, el) : 0), span(grad_weight, gl * h),
-                       span(grad_bias, gl * h)};
+                       span(grad_x, grad_x ? matrix_bytes(n, lddx, h, el) : 0),
+                       span(grad_weight, gl * h), span(grad_bias, gl * h)};
     const Span rd[] = {span(inplace ? nullptr : grad, matrix_bytes(n, ldg, h, el)),
                        span(x, matrix_bytes(n, ldx, h, el)), span(mean, 4 * n),
                        span(rstd, 4 * n), span(weight, pl * h)};

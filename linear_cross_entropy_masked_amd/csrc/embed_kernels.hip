@@ -83,7 +83,7 @@ __global__ void __launch_bounds__(kThreads) embed_fwd_kernel(
   }
 }
 
-// One workgroup: *status = LCE_STATUS_BAD_LABEL if some token is neither ignored nor in [0, v).
+// One workgroup: *status = LCE_STATUS_BAD_TOKEN if some token is neither ignored nor in [0, v).
 __global__ void __launch_bounds__(1024) token_status_kernel(const int32_t* __restrict__ tokens,
                                                             int64_t n, int64_t v,
                                                             int32_t ignore_index,
@@ -98,7 +98,7 @@ __global__ void __launch_bounds__(1024) token_status_kernel(const int32_t* __res
   }
   if (bad) any = 1;  // every writer writes the same value
   __syncthreads();
-  if (threadIdx.x == 0) *status = any;
+  if (threadIdx.x == 0) *status = any ? LCE_STATUS_BAD_TOKEN : 0;
 }
 
 // ------------------------------------------------------------------ sort by token

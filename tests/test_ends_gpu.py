@@ -303,3 +303,29 @@ def test_two_streams_at_once(dev):
     torch.cuda.synchronize()
     for k, g in enumerate(got):
         assert all(torch.equal(a, b) for a, b in zip(g, want[k % 2])), k
+
+
+@pytest.mark.parametrize("which", [0, 1])
+def test_piece_loss_with_a_bias_on_one_piece(dev, which):
+    """A bias of zeros adds nothing: pieces without one give the same loss and gradients, and the
+    one that has a bias gets its gradient."""
+    sizes = [300, 70]
+    _, lab = batch(dev, 90, sum(sizes))
+    b = torch.linspace(-1, 1, sizes[which], device=dev)
+
+    def run(mixed):
+        hid = bf16(dev, 90, 64, seed=1).requires_grad_()
+        ws = [bf16(dev, v, 64, seed=2 + k, std=0.3).requires_grad_() for k, v in enumerate(sizes)]
+        bs = [None if mixed else torch.zeros(v, device=dev) for v in sizes]
+        bs[which] = b.clone().requires_grad_()
+        loss = ag.linear_cross_entropy_pieces(hid, ws, lab, bs)
+        loss.backward()
+        return [loss.detach(), hid.grad, *(w.grad for w in ws), bs[which].grad]
+    for got, want in zip(run(True), run(False)):
+        assert torch.equal(got, want)
+    hid, ws = bf16(dev, 90, 64, seed=1), [bf16(dev, v, 64, seed=2 + k) for k, v in enumerate(sizes)]
+    bs = [None, None]
+    bs[which] = b
+    _, lse, _ = lce.flce_pieces_fwd(hid, ws, lab, bs)
+    _, _, gbs = lce.flce_pieces_bwd(hid, ws, lab, lse, bs)
+    assert gbs[1 - which] is None and gbs[which].shape == b.shape

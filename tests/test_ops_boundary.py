@@ -1,6 +1,6 @@
-"""CPU checks of the embedding, layer norm and vocabulary-piece entry points: bad arguments are refused with the
-documented status codes before anything touches a GPU (fake device addresses, as in
-test_boundary.py), and the binding's own refusals."""
+"""CPU checks of the embedding, layer norm and vocabulary-piece entry points: bad arguments are
+refused with the documented status codes before anything touches a GPU (fake device addresses, as
+in test_boundary.py), and the binding's own refusals."""
 import ctypes
 import os
 
@@ -226,3 +226,48 @@ def test_calls_run_on_their_tensors_device(monkeypatch):
     monkeypatch.setitem(lce._FNS, "embed_fwd", lambda *a: BAD_DTYPE)
     with pytest.raises(lce.LceError, match="type"):
         lce._call("embed_fwd", torch.device("cuda", 0))
+
+
+def test_sizes_past_a_launch_are_refused(lib):
+    """More threads than one launch holds (2^32 - 1) is a shape error, not the runtime's."""
+    out = ctypes.c_size_t()
+    ref = ctypes.byref(out)
+    assert lib.embed_workspace_size(1 << 28, 16, 1 << 27, ref) == OK
+    assert lib.embed_workspace_size((1 << 28) + 1, 16, 10, ref) == BAD_SHAPE
+    assert lib.embed_workspace_size(4, 16, (1 << 27) + 1, ref) == BAD_SHAPE
+    assert lib.embed_workspace_size(4, 1 << 20, (1 << 16) + 1, ref) == BAD_SHAPE
+    assert lib.embed_workspace_size(1 << 28, 1 << 13, 10, ref) == BAD_SHAPE
+    # weight, dtype, v, h, ldw, tokens, n, ignore_index, scale, out, ldo, status, stream
+    far = 1 << 50
+
+    def lookup(n, h, dtype=0):
+        return lib.embed_fwd(A[0], dtype, 10, h, h, A[1] + far, n, -100, 1.0, A[2] + 2 * far, h,
+                             None, None)
+    assert lookup(1 << 24, 4096) == BAD_SHAPE and lookup(1 << 23, 4096, 2) == BAD_SHAPE
+    assert lookup((1 << 31) - 1, 16) == BAD_SHAPE
+    if no_gpu():
+        assert lookup(15 << 20, 4096) in AT_DEVICE_CHECK
+    assert lib.flce_piece_fwd_workspace_size(4, 8, 1 << 29, ref) == OK
+    assert lib.flce_piece_fwd_workspace_size(4, 8, (1 << 29) + 1, ref) == BAD_SHAPE
+
+
+def test_binding_refuses_a_wide_ignore_index(monkeypatch):
+    monkeypatch.setattr(lce, "_require", lambda *a: None)
+    hid = torch.zeros(3, 8, dtype=torch.bfloat16)
+    idx = torch.zeros(3, dtype=torch.int64)
+    f = torch.zeros(3)
+    state = torch.zeros(3, 3)
+    for ignore in (1 << 31, -(1 << 31) - 1, 1 << 40):
+        kw = dict(ignore_index=ignore)
+        for call in (lambda: lce.embed_fwd(hid, idx, **kw),
+                     lambda: lce.embed_bwd(hid, idx, 5, **kw),
+                     lambda: lce.flce_pieces_fwd(hid, hid, idx, **kw),
+                     lambda: lce.flce_pieces_bwd(hid, hid, idx, f, **kw),
+                     lambda: lce.flce_piece_fwd(hid, hid, idx, state, v_start=0, vocab=3,
+                                                first=True, **kw),
+                     lambda: lce.flce_piece_loss(state, idx, vocab=3, **kw),
+                     lambda: lce.flce_piece_bwd(hid, hid, idx, f, v_start=0, vocab=3, first=True,
+                                                last=True, **kw)):
+            with pytest.raises(ValueError, match="32 bits"):
+                call()
+    assert lce._ignore_arg(-(1 << 31)) == -(1 << 31)
