@@ -321,6 +321,7 @@ class _LayerNorm(torch.autograd.Function):
         x = _rows(x)
         y, mean, rstd = layernorm_fwd(x, weight, bias, eps=eps)
         ctx.save_for_backward(x, weight, mean, rstd)
+        ctx.bias_dtype = None if bias is None else bias.dtype
         return y
 
     @staticmethod
@@ -328,14 +329,18 @@ class _LayerNorm(torch.autograd.Function):
     def backward(ctx, g):
         x, weight, mean, rstd = ctx.saved_tensors
         need_x, need_w, need_b = ctx.needs_input_grad[:3]
-        gx, gw, gb = _layernorm_grads(g, x, mean, rstd, weight, need_x, need_w, need_b, False)
+        gx, gw, gb = _layernorm_grads(g, x, mean, rstd, weight, need_x, need_w,
+                                      ctx.bias_dtype if need_b else None, False)
         return gx, gw, gb, None
 
 
-def _layernorm_grads(g, x, mean, rstd, weight, need_x, need_w, need_b, in_place):
+def _layernorm_grads(g, x, mean, rstd, weight, need_x, need_w, bias_dtype, in_place):
+    """bias_dtype: None where the bias needs no gradient (a bias without a weight may be fp32
+    beside 16-bit x)."""
     g = _rows(g)
+    gb = bias_dtype is not None and torch.empty(x.shape[1], dtype=bias_dtype, device=x.device)
     return layernorm_bwd(g, x, mean, rstd, weight, grad_x=g if need_x and in_place else need_x,
-                         grad_weight=need_w, grad_bias=need_b)
+                         grad_weight=need_w, grad_bias=gb)
 
 
 def layer_norm(x, weight=None, bias=None, *, eps: float = 1e-5):
@@ -508,7 +513,8 @@ class _NormLinearCE(torch.autograd.Function):
         del y
         gx = gnw = gnb = None
         if norm_grads:
-            gx, gnw, gnb = _layernorm_grads(gy, x, mean, rstd, nw, need[0], need[1], need[2], True)
+            gx, gnw, gnb = _layernorm_grads(gy, x, mean, rstd, nw, need[0], need[1],
+                                            nb.dtype if need[2] else None, True)
         return gx, gnw, gnb, None, None, None, None, *gws, *gbs
 
 

@@ -156,8 +156,8 @@ def test_gradient_of_one_token_and_of_none(dev, n):
 
 
 def test_gradient_with_a_vocabulary_past_32_bit_keys(dev):
-    """(v + 1) · 8192 past 2^32: the sort's keys are 64-bit."""
-    n, v = 9000, 700001
+    """(v + 1) · 2048 past 2^32: the sort's keys are 64-bit."""
+    n, v = 9000, 2200001
     gen = torch.Generator().manual_seed(5)
     g = torch.randn(n, 8, generator=gen).to(dev)
     tok = torch.randint(0, v, (n,), generator=gen, dtype=torch.int32).to(dev)
@@ -203,3 +203,22 @@ def test_gradient_against_differences(dev):
     tol = 8 * U32 * (3 * (w.abs() + d.abs()).double()[tok.long().clamp(min=0)]
                      * c.double().abs()).sum()
     assert (step - want).abs() <= tol
+
+
+def test_a_table_past_4_gib(dev):
+    """Rows whose bytes start past 2^32, looked up and added into."""
+    n, v, h = 3000, 1200003, 2048
+    w = torch.zeros(v, h, dtype=torch.bfloat16, device=dev)
+    gen = torch.Generator().manual_seed(9)
+    tok = (v - 1 - torch.randint(0, 900, (n,), generator=gen)).to(torch.int32).to(dev)
+    tok[:1000] = torch.randint(0, v, (1000,), generator=gen, dtype=torch.int32).to(dev)
+    rows = tok.unique().long()
+    w[rows] = torch.randn(len(rows), h, generator=gen).to(torch.bfloat16).to(dev)
+    assert torch.equal(lce.embed_fwd(w, tok), w[tok.long()])
+    g = torch.randn(n, h, generator=gen).to(torch.bfloat16).to(dev)
+    w.fill_(1.0)
+    lce.embed_bwd(g, tok, v, grad_weight=w)
+    small = torch.searchsorted(rows, tok.long()).to(torch.int32)
+    check_grad(g, small, len(rows), 1.0, w[rows])
+    w[rows] = 0
+    assert not w.any()

@@ -329,3 +329,23 @@ def test_piece_loss_with_a_bias_on_one_piece(dev, which):
     _, lse, _ = lce.flce_pieces_fwd(hid, ws, lab, bs)
     _, _, gbs = lce.flce_pieces_bwd(hid, ws, lab, lse, bs)
     assert gbs[1 - which] is None and gbs[which].shape == b.shape
+
+
+def test_layer_norm_with_a_bias_alone(dev):
+    """An fp32 bias beside bf16 rows and no weight: its gradient is not rounded to bf16."""
+    x = bf16(dev, 400, 96, seed=3)
+    b = torch.zeros(96, device=dev, requires_grad=True)
+    g = bf16(dev, 400, 96, seed=4)
+    ag.layer_norm(x, None, b).backward(g)
+    assert b.grad.dtype == torch.float32
+    exact = g.double().sum(0)
+    assert ((b.grad.double() - exact).abs() <= 401 * U * g.double().abs().sum(0)).all()
+    w = bf16(dev, 300, 96, seed=5, std=0.1)
+    _, lab = batch(dev, 400, 300)
+    b.grad = None
+    ag.norm_linear_cross_entropy(x, None, b, w, lab).backward()
+    y, _, _ = lce.layernorm_fwd(x, None, b.detach())
+    _, lse, _ = lce.flce_pieces_fwd(y, w, lab)
+    gy, _, _ = lce.flce_pieces_bwd(y, w, lab, lse, num_label_tokens=1, grad_weight=False)
+    exact = gy.double().sum(0)
+    assert ((b.grad.double() - exact).abs() <= 401 * U * gy.double().abs().sum(0)).all()

@@ -235,3 +235,29 @@ def test_gradients_against_differences(dev):
         third = t * t * (c.double().abs() * w.double().abs() * (1 + d.double().abs()) ** 3).sum()
         assert (step - want).abs() <= noise + third
     assert ((gb.double() - c.double().sum(0)).abs() <= 8 * U * c.double().abs().sum(0)).all()
+
+
+def test_rows_past_4_gib(dev):
+    """Rows whose bytes start past 2^32 are normalised, in place, as the same rows by themselves,
+    and so is their gradient."""
+    n, h, last = 600001, 4096, 70
+    x = torch.zeros(n, h, dtype=torch.bfloat16, device=dev)
+    x[-last:] = torch.randn(last, h, device=dev).to(torch.bfloat16)
+    w = torch.randn(h, device=dev).to(torch.bfloat16)
+    tail = x[-last:].clone()
+    y, mean, rstd = lce.layernorm_fwd(tail, w)
+    g = torch.randn(last, h, device=dev).to(torch.bfloat16)
+    gx, gw, _ = lce.layernorm_bwd(g, tail, mean, rstd, w)
+    got, m, r = lce.layernorm_fwd(x, w, out=x)
+    assert torch.equal(got[-last:], y) and not got[:-last].any()
+    assert torch.equal(m[-last:], mean) and torch.equal(r[-last:], rstd)
+    x[-last:] = tail
+    x[:-last] = 0
+    big = torch.zeros_like(x)
+    big[-last:] = g
+    bx, bw, _ = lce.layernorm_bwd(big, x, m, r, w, grad_x=big)
+    assert torch.equal(bx[-last:], gx) and not bx[:-last].any()
+    # two fp32 sums of the same terms (at most `last` that are not 0), each rounded to bf16
+    size = (g.float() * ((tail.float() - mean[:, None]) * rstd[:, None])).abs().sum(0)
+    assert ((bw.float() - gw.float()).abs() <= 2.0 ** -7 * gw.float().abs()
+            + 4 * last * 2.0 ** -24 * size).all()

@@ -466,3 +466,38 @@ def test_gradients_against_differences(dev):
     step = (f(hid, b + t * db) - f(hid, b - t * db)) / (2 * t)
     third = float(db.abs().max()) ** 3 * n * t * t
     assert abs(step - float((gb.double() * db).sum())) <= 2 * e.dloss / t + third + float((e.dgb * db.abs()).sum())
+
+
+@pytest.mark.parametrize("n", [20, 40, 300])
+def test_a_weight_past_4_gib(dev, n):
+    """Classes whose weight rows start past 2^32 bytes, through each of the logits kernels: the
+    terms against fp64, the gradients of one piece against those of four."""
+    h, v = 4096, 600011
+    gen = torch.Generator().manual_seed(n)
+    hid = torch.randn(n, h, generator=gen).to(torch.bfloat16).to(dev)
+    w = torch.randn(v, h, device=dev, dtype=torch.bfloat16).mul_(2.0 ** -6)
+    lab = (v - 1 - torch.randint(0, 50000, (n,), generator=gen)).to(torch.int32).to(dev)
+    lab[3] = IGN
+    _, lse, rows = lce.flce_pieces_fwd(hid, w, lab, return_rows=True)
+    hd = hid.double()
+    z, dz = [], []
+    for lo in range(0, v, 50000):
+        wd = w[lo:lo + 50000].double()
+        z.append(hd @ wd.t())
+        dz.append((h + 2) * U * (hd.abs() @ wd.abs().t()) + 2 * U * z[-1].abs())
+    z, dz = torch.cat(z, 1), torch.cat(dz, 1)
+    keep = lab != IGN
+    exact = torch.where(keep, torch.logsumexp(z, 1), torch.zeros_like(z[:, 0]))
+    dlse = dz.max(1).values + 2.0 ** -16 + 2 * U * exact.abs()
+    near(lse, exact, dlse, "lse")
+    y = lab.long().clamp(min=0)[:, None]
+    terms = torch.where(keep, exact - z.gather(1, y)[:, 0], torch.zeros_like(exact))
+    near(rows, terms, dlse + dz.gather(1, y)[:, 0] + 2 * U * terms.abs(), "rows")
+    del z, dz
+    gh, gw, _ = lce.flce_pieces_bwd(hid, w, lab, lse, piece_size=v)
+    gh2, gw2, _ = lce.flce_pieces_bwd(hid, w, lab, lse, piece_size=150003)
+    assert torch.equal(gw, gw2)
+    # two bf16 roundings, and fp32 sums of v products of which the label's is the largest
+    size = (w.float().abs().max() * 2 / int(keep.sum())).item()
+    assert ((gh.float() - gh2.float()).abs() <= 2 * B * gh.float().abs() + v * U * size).all()
+    assert gw[lab[keep].long()].any(1).all()
