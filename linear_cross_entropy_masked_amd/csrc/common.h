@@ -124,7 +124,8 @@ enum KernelId {
   K_PIECE_GRAD_LOGITS,
   K_PIECE_GRAD_HIDDEN,
   K_PIECE_GRAD_WEIGHT,
-  K_PIECE_GRAD_BIAS,
+  K_PIECE_GRAD_FINISH,
+  K_PIECE_GRADS,
   K_COUNT
 };
 

@@ -56,10 +56,10 @@ constexpr int kTile = Wide::BM;  // rows of an output tile; the gathered rows ar
 // 229, 275); 256 rows take 284 us on 256 x 256 tiles and 317 on 128 x 256.
 constexpr int kScoreRows = 32;
 constexpr int kNarrowRows = 128;
-// The weight gradient's contraction is as long as the batch. Up to this many rows it is mostly
-// stores, and two 256 x 128 workgroups per CU overlap them (step of 60 rows of 2048 and 60000
-// classes 306 us against 323, of 500 rows and 32000 classes 338 against 344, of 1000 rows of 4096
-// 1005 against 994).
+// The weight gradient's contraction is as long as the batch. Where it has a launch of its own, up
+// to this many rows it is mostly stores, and two 256 x 128 workgroups per CU overlap them (step of
+// 60 rows of 2048 and 60000 classes 306 us against 323, of 500 rows and 32000 classes 338 against
+// 344, of 1000 rows of 4096 1005 against 994).
 constexpr int kShortK = 512;
 
 __device__ __forceinline__ bool labelled(int32_t y, int64_t vocab, int32_t ignore_index) {
@@ -676,10 +676,10 @@ struct EpiPiecePartial {
   }
   __device__ __forceinline__ void operator()(int64_t, int64_t, float) {}
 };
-__global__ void __launch_bounds__(256) hidden_reduce_kernel(const float* __restrict__ part,
-                                                            int64_t m_tiles, int64_t splits,
-                                                            int64_t v, HiddenOut o) {
-  const int64_t e = (int64_t(blockIdx.x) * 256 + threadIdx.x) * 4;
+__device__ __forceinline__ void hidden_reduce(const float* __restrict__ part, int64_t m_tiles,
+                                              int64_t splits, int64_t v, const HiddenOut& o,
+                                              int64_t block) {
+  const int64_t e = (block * 256 + threadIdx.x) * 4;
   const int64_t m = e / o.h, n = e % o.h;
   const int64_t count = *o.count;
   if (m >= count) return;
@@ -730,18 +730,37 @@ struct EpiPieceWeight {
 };
 
 // db (=|+=) s · the column sums of the row tiles, in tile order.
-__global__ void __launch_bounds__(256) piece_bias_kernel(
-    const float* __restrict__ colsum, int64_t v, int64_t v64, const int32_t* __restrict__ count,
-    long long t_host, const float* __restrict__ gout, int rows, int accumulate,
-    float* __restrict__ db) {
-  const int64_t c = int64_t(blockIdx.x) * 256 + threadIdx.x;
-  if (c >= v) return;
-  const int64_t tiles = (int64_t(*count) + kTile - 1) / kTile;
+struct BiasOut {
+  const float* colsum;
+  int64_t v, v64;
+  const int32_t* count;
+  long long t_host;
+  const float* gout;
+  int rows, accumulate;
+  float* db;
+};
+__device__ __forceinline__ void bias_reduce(const BiasOut& o, int64_t block) {
+  const int64_t c = block * 256 + threadIdx.x;
+  if (c >= o.v) return;
+  const int64_t tiles = (int64_t(*o.count) + kTile - 1) / kTile;
   float sum = 0.f;
 #pragma unroll 4
-  for (int64_t t = 0; t < tiles; ++t) sum += colsum[t * v64 + c];
-  const float x = loss_scale(count, t_host, gout, rows) * sum;
-  db[c] = accumulate ? db[c] + x : x;
+  for (int64_t t = 0; t < tiles; ++t) sum += o.colsum[t * o.v64 + c];
+  const float x = loss_scale(o.count, o.t_host, o.gout, o.rows) * sum;
+  o.db[c] = o.accumulate ? o.db[c] + x : x;
+}
+
+// What is left after the products: the split hidden gradient added up in the first hidden_blocks
+// workgroups, the bias gradient in the others.
+__global__ void __launch_bounds__(256) piece_finish_kernel(const float* __restrict__ part,
+                                                           int64_t m_tiles, int64_t splits,
+                                                           int64_t v, HiddenOut h,
+                                                           int64_t hidden_blocks, BiasOut b) {
+  const int64_t w = blockIdx.x;
+  if (w < hidden_blocks)
+    hidden_reduce(part, m_tiles, splits, v, h, w);
+  else
+    bias_reduce(b, w - hidden_blocks);
 }
 
 // ------------------------------------------------------------------ workspaces
@@ -879,6 +898,23 @@ hipError_t grad_weight_product(const PieceBwdArgs& a, const PieceWs& w, const Vi
                                               true);
 }
 
+// The hidden gradient's product, split over K, and the weight gradient's in one launch: neither
+// fills its last round of CUs (steps of 100 rows of 256 and 2000 classes 64 us so and 73 apart, 1000
+// of 1024 and 50257 523 and 539, 1500 of 4096 and 32000 1354 and 1389).
+template <class TW, bool ACC>
+hipError_t grad_products(const PieceBwdArgs& a, const PieceWs& w, const View& dv, const View& wk,
+                         const View& hk, int64_t splits, hipStream_t s) {
+  const EpiPiecePartial eh{w.split, a.h, a.v, w.count, 0, 0};
+  const EpiPieceWeight<TW, ACC> ew{static_cast<TW*>(a.grad_weight), a.h, w.count,
+                                   a.num_label_tokens, a.grad_output,
+                                   int(a.grad_rows != nullptr), 0.f};
+  const int64_t np = up(a.n, kTile);
+  TimedLaunch t(s, K_PIECE_GRADS);
+  return gemm::v2::launch_two<Wide>(
+      gemm::v2::product<Wide, true, false>(dv, wk, np, a.h, a.v, splits, true, eh),
+      gemm::v2::product<Wide, false, false>(dv, hk, a.v, a.h, np, 1, false, ew), s);
+}
+
 }  // namespace
 
 size_t piece_fwd_workspace_bytes(int64_t n, int64_t h, int64_t v) {
@@ -986,41 +1022,49 @@ hipError_t piece_bwd_run(const PieceBwdArgs& a, hipStream_t s) {
   }
   View dv{w.d, 64, np * 64, np, a.v};
   dv.ext = np * v64;
-  if (a.n > 0 && (last ? static_cast<void*>(a.grad_hidden) : a.hidden_acc)) {
-    const HiddenOut o{w.row, w.count, a.hidden_acc, last ? a.grad_hidden : nullptr, a.h,
-                      int(first), a.num_label_tokens, a.grad_output, int(rows)};
-    const int64_t splits = hidden_splits(a.n, a.h, a.v);
-    View wk{weight, h64, 64, a.v, a.h};
+  View wk{weight, h64, 64, a.v, a.h};
+  View hk{w.hc, h64, 64, np, a.h};
+  const bool want_hidden = a.n > 0 && (last ? static_cast<void*>(a.grad_hidden) : a.hidden_acc);
+  const bool want_weight = a.grad_weight && !(a.n == 0 && accumulate);
+  const bool wide = a.grad_weight_dtype == LCE_DTYPE_F32;
+  const int64_t splits = hidden_splits(a.n, a.h, a.v);
+  const bool both = want_hidden && want_weight && splits > 1;
+  const HiddenOut o{w.row, w.count, a.hidden_acc, last ? a.grad_hidden : nullptr, a.h,
+                    int(first), a.num_label_tokens, a.grad_output, int(rows)};
+  if (both) {
+    if (wide)
+      PIECE_TRY((accumulate ? grad_products<float, true>(a, w, dv, wk, hk, splits, s)
+                            : grad_products<float, false>(a, w, dv, wk, hk, splits, s)));
+    else
+      PIECE_TRY((accumulate ? grad_products<uint16_t, true>(a, w, dv, wk, hk, splits, s)
+                            : grad_products<uint16_t, false>(a, w, dv, wk, hk, splits, s)));
+  } else if (want_hidden) {
+    TimedLaunch t(s, K_PIECE_GRAD_HIDDEN);
     if (splits == 1) {
       EpiPieceHidden e{o, 0.f};
-      TimedLaunch t(s, K_PIECE_GRAD_HIDDEN);
       PIECE_TRY((gemm::v2::launch<Wide, true, false>(dv, wk, np, a.h, a.v, 1, true, e, s, true)));
     } else {
       EpiPiecePartial e{w.split, a.h, a.v, w.count, 0, 0};
-      {
-        TimedLaunch t(s, K_PIECE_GRAD_HIDDEN);
-        PIECE_TRY((gemm::v2::launch<Wide, true, false>(dv, wk, np, a.h, a.v, splits, true, e, s)));
-      }
-      TimedLaunch t(s, K_PIECE_GRAD_HIDDEN);
-      hipLaunchKernelGGL(hidden_reduce_kernel, dim3(unsigned((a.n * a.h / 4 + 255) / 256)),
-                         dim3(256), 0, s, w.split, np / kTile, splits, a.v, o);
-      PIECE_TRY(hipGetLastError());
+      PIECE_TRY((gemm::v2::launch<Wide, true, false>(dv, wk, np, a.h, a.v, splits, true, e, s)));
     }
   }
-  if (a.grad_weight && !(a.n == 0 && accumulate)) {
-    View hk{w.hc, h64, 64, np, a.h};
-    if (a.grad_weight_dtype == LCE_DTYPE_F32)
+  if (want_weight && !both) {
+    if (wide)
       PIECE_TRY((accumulate ? grad_weight_product<float, true>(a, w, dv, hk, s)
                             : grad_weight_product<float, false>(a, w, dv, hk, s)));
     else
       PIECE_TRY((accumulate ? grad_weight_product<uint16_t, true>(a, w, dv, hk, s)
                             : grad_weight_product<uint16_t, false>(a, w, dv, hk, s)));
   }
-  if (a.grad_bias && !(a.n == 0 && accumulate)) {
-    TimedLaunch t(s, K_PIECE_GRAD_BIAS);
-    hipLaunchKernelGGL(piece_bias_kernel, dim3(unsigned((a.v + 255) / 256)), dim3(256), 0, s,
-                       w.colsum, a.v, v64, w.count, a.num_label_tokens, a.grad_output, int(rows),
-                       int(accumulate), a.grad_bias);
+  const bool want_bias = a.grad_bias && !(a.n == 0 && accumulate);
+  const int64_t hidden_blocks = want_hidden && splits > 1 ? (a.n * a.h / 4 + 255) / 256 : 0;
+  const int64_t bias_blocks = want_bias ? (a.v + 255) / 256 : 0;
+  if (hidden_blocks + bias_blocks > 0) {
+    const BiasOut b{w.colsum, a.v, v64, w.count, a.num_label_tokens, a.grad_output, int(rows),
+                    int(accumulate), a.grad_bias};
+    TimedLaunch t(s, K_PIECE_GRAD_FINISH);
+    hipLaunchKernelGGL(piece_finish_kernel, dim3(unsigned(hidden_blocks + bias_blocks)), dim3(256),
+                       0, s, w.split, np / kTile, splits, a.v, o, hidden_blocks, b);
     PIECE_TRY(hipGetLastError());
   }
   return hipSuccess;

@@ -915,11 +915,11 @@ __device__ __forceinline__ void run_tile(const View& A, const View& B, int64_t M
   }
 }
 
+// The tile of workgroup w of a product.
 template <class C, bool AK, bool BKM, class Epi, bool SEGA>
-__global__ void __launch_bounds__(C::THREADS, C::OCC)
-    gemm_pipe_kernel(View A, View B, int64_t M, int64_t N, int64_t K, int64_t ksplit,
-                     TileMap tm, Epi epi) {
-  __shared__ __attribute__((aligned(1024))) char lds[C::LdsBytes];
+__device__ __forceinline__ void run_workgroup(const View& A, const View& B, int64_t M, int64_t N,
+                                              int64_t K, int64_t ksplit, TileMap& tm, Epi& epi,
+                                              int64_t w, char* lds) {
   TileCoord tc;
   if constexpr (RowLimited<Epi>::value) {
     const int64_t live = (epi.row_limit() + C::BM - 1) / C::BM;
@@ -930,14 +930,51 @@ __global__ void __launch_bounds__(C::THREADS, C::OCC)
     }
     tm.m_tiles = live;
     if (tm.m_tiles < 8) tm.xn = 0;  // too few for a block of tiles per XCD
-    if (tm.xn == 0 && int64_t(blockIdx.x) >= tm.m_tiles * tm.n_tiles * tm.splits) return;
+    if (tm.xn == 0 && w >= tm.m_tiles * tm.n_tiles * tm.splits) return;
   }
-  if (!tile_coord(tm, blockIdx.x, tc)) return;  // uniform over the workgroup
+  if (!tile_coord(tm, w, tc)) return;  // uniform over the workgroup
   if constexpr (KLimited<Epi>::value) {
     const int64_t k = epi.k_limit();
     if (k < K) K = k;
   }
   run_tile<C, AK, BKM, Epi, SEGA>(A, B, M, N, K, ksplit, tc, epi, lds);
+}
+
+template <class C, bool AK, bool BKM, class Epi, bool SEGA>
+__global__ void __launch_bounds__(C::THREADS, C::OCC)
+    gemm_pipe_kernel(View A, View B, int64_t M, int64_t N, int64_t K, int64_t ksplit,
+                     TileMap tm, Epi epi) {
+  __shared__ __attribute__((aligned(1024))) char lds[C::LdsBytes];
+  run_workgroup<C, AK, BKM, Epi, SEGA>(A, B, M, N, K, ksplit, tm, epi, blockIdx.x, lds);
+}
+
+// One product with everything its launch takes.
+template <bool AK_, bool BKM_, class Epi_>
+struct Product {
+  static constexpr bool AK = AK_, BKM = BKM_;
+  using Epi = Epi_;
+  View A, B;
+  int64_t M, N, K, ksplit;
+  TileMap tm;
+  Epi epi;
+  int64_t tiles, grid;  // grid: tiles, rounded up to a multiple of the XCDs
+};
+
+// Two products in one launch, the workgroups of the second after those of the first (a multiple
+// of 8 of them, so that both keep their order over the XCDs): the CUs that the first leaves idle
+// in its last round start on the second.
+template <class C, class P, class Q>
+__global__ void __launch_bounds__(C::THREADS, C::OCC) gemm_two_kernel(P p, Q q) {
+  __shared__ __attribute__((aligned(1024))) char lds[C::LdsBytes];
+  const int64_t w = blockIdx.x;
+  if (w < p.grid) {
+    if (w < p.tiles)
+      run_workgroup<C, P::AK, P::BKM, typename P::Epi, false>(p.A, p.B, p.M, p.N, p.K, p.ksplit,
+                                                              p.tm, p.epi, w, lds);
+  } else if (w - p.grid < q.tiles) {
+    run_workgroup<C, Q::AK, Q::BKM, typename Q::Epi, false>(q.A, q.B, q.M, q.N, q.K, q.ksplit,
+                                                            q.tm, q.epi, w - p.grid, lds);
+  }
 }
 
 // C[M, N] = A · B over K with configuration C; `splits` > 1 cuts K into that many ranges
@@ -970,6 +1007,25 @@ hipError_t launch(const View& A, const View& B, int64_t M, int64_t N, int64_t K,
   }
   hipLaunchKernelGGL((gemm_pipe_kernel<C, AK, BKM, Epi, SEGA>), dim3(unsigned(grid)),
                      dim3(C::THREADS), 0, s, A, B, M, N, K, ksplit, tm, epi);
+  return hipGetLastError();
+}
+
+// A product as launch() takes it, for launch_two().
+template <class C, bool AK, bool BKM, class Epi>
+Product<AK, BKM, Epi> product(const View& A, const View& B, int64_t M, int64_t N, int64_t K,
+                              int64_t splits, bool m_fast, const Epi& epi) {
+  TileMap tm{(M + C::BM - 1) / C::BM, (N + C::BN - 1) / C::BN, splits < 1 ? 1 : splits, m_fast};
+  const int64_t ksplit = ((K + tm.splits - 1) / tm.splits + C::BK - 1) / C::BK * C::BK;
+  const int64_t tiles = tm.m_tiles * tm.n_tiles * tm.splits;
+  return Product<AK, BKM, Epi>{A, B, M, N, K, ksplit, tm, epi, tiles, (tiles + 7) / 8 * 8};
+}
+template <class C, class P, class Q>
+hipError_t launch_two(const P& p, const Q& q, hipStream_t s) {
+  if ((P::AK && p.A.gs < 64) || (P::BKM && p.B.gs < 64) || (Q::AK && q.A.gs < 64) ||
+      (Q::BKM && q.B.gs < 64))
+    return hipErrorInvalidValue;
+  hipLaunchKernelGGL((gemm_two_kernel<C, P, Q>), dim3(unsigned(p.grid + q.grid)),
+                     dim3(C::THREADS), 0, s, p, q);
   return hipGetLastError();
 }
 

@@ -45,7 +45,7 @@ const char* kNames[K_COUNT] = {
     "embed_join",         "layernorm_fwd",         "layernorm_bwd",
     "layernorm_param_reduce", "piece_gather",      "piece_logits",
     "piece_state",        "piece_grad_logits",     "piece_grad_hidden",
-    "piece_grad_weight",  "piece_grad_bias",
+    "piece_grad_weight",  "piece_grad_finish",   "piece_grads",
 };
 
 }  // namespace
