@@ -631,7 +631,7 @@ def embed_fwd(weight, tokens, *, scale: float = 1.0, ignore_index: int = -100, o
     tokens = _tokens_i32(tokens, dev, ignore_index)
     n = tokens.shape[0]
     if out is None:
-        out, ldo = torch.empty((n, h), dtype=weight.dtype, device=dev), h
+        out, ldo = weight.new_empty((n, h)), h
     else:
         ldo = _rows_2d(out, "out", weight.dtype, (n, h), dev)
     _call("embed_fwd", dev, weight.data_ptr(), code, v, h, ldw, tokens.data_ptr(), n,
@@ -693,6 +693,13 @@ def embed_bwd(grad, tokens, num_embeddings: int, *, scale: float = 1.0, ignore_i
     return grad_weight
 
 
+def _empty_rows(x):
+    """A new contiguous tensor of x's shape and type (empty_like is the cheapest call that makes
+    one, 1.2 us)."""
+    import torch
+    return torch.empty_like(x) if x.is_contiguous() else x.new_empty(x.shape)
+
+
 def _norm_param(t, name, h, device):
     _require(t, name, None, 1, device)
     if t.shape[0] != h:
@@ -720,13 +727,13 @@ def layernorm_fwd(x, weight=None, bias=None, *, eps: float = 1e-5, out=None,
             raise TypeError(f"bias is {bias.dtype}, weight {pdtype}: they must be of one type")
         pdtype = bias.dtype
     if out is None:
-        out, ldy = torch.empty((n, h), dtype=x.dtype, device=dev), h
+        out, ldy = _empty_rows(x), h
     else:
         ldy = _rows_2d(out, "out", x.dtype, (n, h), dev)
     mean = rstd = None
     if return_stats:
         mean = torch.empty(n, dtype=torch.float32, device=dev)
-        rstd = torch.empty(n, dtype=torch.float32, device=dev)
+        rstd = torch.empty_like(mean)
     _call("layernorm_fwd", dev, x.data_ptr(), code, n, h, ldx, _adr(weight), _adr(bias),
           _dtype_code(pdtype, "weight"), eps, out.data_ptr(), ldy, _adr(mean), _adr(rstd))
     return out, mean, rstd
@@ -765,7 +772,7 @@ def layernorm_bwd(grad, x, mean, rstd, weight=None, *, grad_x=True, grad_weight=
         if spec is True:
             if accumulate:
                 raise ValueError(f"accumulate=True needs an existing {name} tensor")
-            return torch.empty(h, dtype=pdtype, device=dev)
+            return x.new_empty(h) if weight is None else torch.empty_like(weight)
         if spec is False or spec is None:
             return None
         _require(spec, name, None, 1, dev)
@@ -775,7 +782,7 @@ def layernorm_bwd(grad, x, mean, rstd, weight=None, *, grad_x=True, grad_weight=
 
     lddx = h
     if grad_x is True:
-        grad_x = torch.empty((n, h), dtype=x.dtype, device=dev)
+        grad_x = _empty_rows(x)
     elif grad_x is False:
         grad_x = None
     elif grad_x is not None:

@@ -272,35 +272,44 @@ __global__ void __launch_bounds__(norm_threads(WPR, kBwdThreads)) layernorm_bwd_
     }
   }
   if (!part_w) return;
-  // this workgroup's partial rows: its row groups one after the other
-  float* pw = part_w + int64_t(blockIdx.x) * h;
-  float* pb = part_b + int64_t(blockIdx.x) * h;
-  for (int k = 0; k < RG; ++k) {
-    if (RG > 1) __syncthreads();
-    if (group != k) continue;
+  // this workgroup's partial rows: its row groups added through LDS, in group order
+  if constexpr (RG > 1) {
+    constexpr int LANES = 64 * WPR;
+    __shared__ float sums[RG - 1][2 * EPL][LANES];
+    if (group > 0) {
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      if (col.skip[j] == 0 && (FULL || h >= VE)) {
-        float* p[2] = {pw + col.at[j], pb + col.at[j]};
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          float(&d)[VE] = t ? db[j] : dw[j];
-          if (k > 0) {
-            float old[VE];
-            load_some<float, VE>(p[t], VE, old);
-#pragma unroll
-            for (int q = 0; q < VE; ++q) d[q] += old[q];
-          }
-          store_some<float, VE>(p[t], VE, d);
-        }
-      } else if (!FULL && col.live(j)) {  // the row's last vector, or a row shorter than one
+      for (int j = 0; j < NV; ++j)
 #pragma unroll
         for (int q = 0; q < VE; ++q) {
-          if (!col.counts(j, q)) continue;
-          const int c = col.at[j] + q;
-          pw[c] = k > 0 ? pw[c] + dw[j][q] : dw[j][q];
-          pb[c] = k > 0 ? pb[c] + db[j][q] : db[j][q];
+          sums[group - 1][j * VE + q][lane] = dw[j][q];
+          sums[group - 1][EPL + j * VE + q][lane] = db[j][q];
         }
+    }
+    __syncthreads();
+    if (group > 0) return;
+#pragma unroll
+    for (int k = 0; k < RG - 1; ++k)
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int q = 0; q < VE; ++q) {
+          dw[j][q] += sums[k][j * VE + q][lane];
+          db[j][q] += sums[k][EPL + j * VE + q][lane];
+        }
+  }
+  float* pw = part_w + int64_t(blockIdx.x) * h;
+  float* pb = part_b + int64_t(blockIdx.x) * h;
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    if (col.skip[j] == 0 && (FULL || h >= VE)) {
+      store_some<float, VE>(pw + col.at[j], VE, dw[j]);
+      store_some<float, VE>(pb + col.at[j], VE, db[j]);
+    } else if (!FULL && col.live(j)) {  // the row's last vector, or a row shorter than one
+#pragma unroll
+      for (int q = 0; q < VE; ++q) {
+        if (!col.counts(j, q)) continue;
+        pw[col.at[j] + q] = dw[j][q];
+        pb[col.at[j] + q] = db[j][q];
       }
     }
   }
