@@ -422,7 +422,7 @@ int layernorm_fwd(const void* x, int dtype, int64_t n, int64_t h, int64_t ldx, c
 /* flags of layernorm_bwd */
 #define LAYERNORM_ACCUMULATE     1u /* add into grad_weight and grad_bias                        */
 
-/* Workspace bytes of layernorm_bwd: one partial row of each parameter gradient for at most 512
+/* Workspace bytes of layernorm_bwd: one partial row of each parameter gradient for at most 1024
  * workgroups. Host-only. */
 int layernorm_workspace_size(int64_t n, int64_t h, size_t* bytes);
 

@@ -12,8 +12,9 @@
 // write; the mean is known before the squares are summed, so the variance does not cancel. Rows
 // are dealt to a fixed grid, each lane loading the next row's vectors before the sums of this. In
 // the backward every lane keeps the columns it owns for all of its rows and adds their dw and db
-// terms in fp32 registers; each workgroup writes one partial row of each, and param_reduce_kernel
-// adds those in workgroup order (no atomics: a result does not change from run to run).
+// terms in fp32 registers (the longest rows take a pass of their own for them, norm_columns_kernel);
+// each workgroup writes one partial row of each, and param_reduce_kernel adds those in workgroup
+// order (no atomics: a result does not change from run to run).
 #include <algorithm>
 
 #include "common.h"
@@ -28,13 +29,22 @@ namespace {
 // [4099, 2051] fp16 backward: the forward takes rows in workgroups of at least 512 threads with
 // 32 elements a lane (190 us; 256 threads 206, 16 elements 200), the backward in workgroups of
 // at least 256 threads with 16 or 24 (50 and 27 us; 512 threads and 32 elements 55 and 50: its
-// running dw and db take two registers an element, and fewer rows are in flight at once). The
-// backward's grid fills the CUs twice over; each workgroup costs one partial row of dw and of db
-// (grids of 256 / 768: 66 / 52 and 40 / 33 us).
+// running dw and db take two registers an element, and fewer rows are in flight at once).
 constexpr int kFwdThreads = 512, kFwdElems = 32;
 constexpr int kBwdThreads = 256, kBwdElems = 16;
 constexpr int64_t kFwdGrid = 2048;
-constexpr int64_t kBwdGrid = 512;
+// Workgroups of the backward, each of which costs one partial row of dw and of db: two per CU of
+// 256 threads (768 or 1024 of them: [8192, 4096] 47 or 55 against 47 us, [4099, 2051] fp16 28 or 30
+// against 23), one of 512 ([4096, 8192] 52 us, two 58), four where the partial rows are short
+// ([60000, 257] 34 us, two 42; [16384, 512] 19 either way). Past kRegRow elements a row's dw and db
+// do not fit the registers of a workgroup beside the row: they are summed by columns, in kColRows
+// groups of rows ([1024, 20011] bf16 110 us so and 254 in the rows' own pass).
+constexpr int64_t kShortRow = 512, kPairRow = 256 * 24, kRegRow = 512 * 32;
+constexpr int64_t kColRows = 64;
+int64_t bwd_grid(int64_t h) { return h <= kShortRow ? 1024 : h <= kPairRow ? 512 : 256; }
+int64_t part_rows(int64_t n, int64_t h) {
+  return std::min(n, h > kRegRow ? kColRows : bwd_grid(h));
+}
 // A forward of whole vectors that moves more than this passes by the caches (non-temporal loads
 // and stores): 1 GiB takes 188 us so and 199 without, 256 MiB 54 either way, 128 MiB 31 so and
 // 28 without.
@@ -205,7 +215,8 @@ __global__ void __launch_bounds__(norm_threads(WPR, kFwdThreads)) layernorm_fwd_
   }
 }
 
-template <class T, class P, int WPR, int EPL, bool FULL>
+// PARAMS: with the workgroup's partial rows of dw and db, where part_w is given.
+template <class T, class P, int WPR, int EPL, bool FULL, bool PARAMS>
 __global__ void __launch_bounds__(norm_threads(WPR, kBwdThreads)) layernorm_bwd_kernel(
     const T* g, int64_t ldg, const T* __restrict__ x, int64_t ldx, const float* __restrict__ mean,
     const float* __restrict__ rstd, const P* __restrict__ weight, int64_t n, int h, T* dx,
@@ -250,7 +261,7 @@ __global__ void __launch_bounds__(norm_threads(WPR, kBwdThreads)) layernorm_bwd_
 #pragma unroll
       for (int q = 0; q < VE; ++q) {
         xh[j][q] = (xh[j][q] - mu) * rs;
-        if (live) {
+        if (PARAMS && live) {
           dw[j][q] += u[j][q] * xh[j][q];
           db[j][q] += u[j][q];
         }
@@ -271,7 +282,7 @@ __global__ void __launch_bounds__(norm_threads(WPR, kBwdThreads)) layernorm_bwd_
       col.store(dx + r * lddx, j, u[j]);
     }
   }
-  if (!part_w) return;
+  if (!PARAMS || !part_w) return;
   // this workgroup's partial rows: its row groups added through LDS, in group order
   if constexpr (RG > 1) {
     constexpr int LANES = 64 * WPR;
@@ -315,6 +326,50 @@ __global__ void __launch_bounds__(norm_threads(WPR, kBwdThreads)) layernorm_bwd_
   }
 }
 
+// dw and db of long rows: a workgroup adds the rows blockIdx.y, blockIdx.y + gridDim.y, ... of its
+// 256 vectors of columns into partial row blockIdx.y.
+constexpr int kColBatch = 4;  // rows in flight per lane
+template <class T>
+__global__ void __launch_bounds__(256) norm_columns_kernel(
+    const T* __restrict__ g, int64_t ldg, const T* __restrict__ x, int64_t ldx,
+    const float* __restrict__ mean, const float* __restrict__ rstd, int64_t n, int64_t h,
+    float* __restrict__ part_w, float* __restrict__ part_b) {
+  constexpr int VE = Elem<T>::kVec;
+  const int64_t col = (int64_t(blockIdx.x) * 256 + threadIdx.x) * VE;
+  if (col >= h) return;
+  const int64_t cnt = h - col;
+  float dw[VE] = {}, db[VE] = {};
+  for (int64_t r0 = blockIdx.y; r0 < n; r0 += int64_t(kColBatch) * gridDim.y) {
+    float xs[kColBatch][VE], gs[kColBatch][VE], mu[kColBatch], rs[kColBatch];
+#pragma unroll
+    for (int k = 0; k < kColBatch; ++k) {
+      const int64_t r = r0 + int64_t(k) * gridDim.y;
+      if (r >= n) continue;
+      load_some<T, VE>(x + r * ldx + col, cnt, xs[k]);
+      load_some<T, VE>(g + r * ldg + col, cnt, gs[k]);
+      mu[k] = mean[r];
+      rs[k] = rstd[r];
+    }
+#pragma unroll
+    for (int k = 0; k < kColBatch; ++k) {
+      if (r0 + int64_t(k) * gridDim.y >= n) break;
+#pragma unroll
+      for (int q = 0; q < VE; ++q) {
+        dw[q] += gs[k][q] * ((xs[k][q] - mu[k]) * rs[k]);
+        db[q] += gs[k][q];
+      }
+    }
+  }
+  float* pw = part_w + int64_t(blockIdx.y) * h + col;
+  float* pb = part_b + int64_t(blockIdx.y) * h + col;
+#pragma unroll
+  for (int q = 0; q < VE; ++q) {
+    if (q >= cnt) break;
+    pw[q] = dw[q];
+    pb[q] = db[q];
+  }
+}
+
 // dw and db from the workgroups' partial rows: 32 columns per workgroup, the rows dealt to
 // eight thread groups, their sums added in group order. blockIdx.y: 0 weight, 1 bias.
 constexpr int kRedCols = 32, kRedGroups = 8;
@@ -349,7 +404,9 @@ size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 // Calls f with the row shape (WPR, EPL) for rows of h elements: up to E elements a lane, fewer
 // where one wavefront holds the row with fewer; wavefronts per row doubled until the row fits.
 // For E = 16, rows that leave a quarter or more of the next shape empty take half the wavefronts
-// with 24 elements a lane. Rows past 1024 · E take 32.
+// with 24 elements a lane, and eight wavefronts hold up to 32, since sixteen have half the registers
+// each and spill ([3000, 10001] fp16 71 us so and 123 on sixteen, [2048, 16384] bf16 56 and 73). Rows
+// past that take sixteen with 32.
 template <int E, class F>
 hipError_t with_shape(int64_t h, F&& f) {
   using std::integral_constant;
@@ -360,21 +417,26 @@ hipError_t with_shape(int64_t h, F&& f) {
   using W16 = integral_constant<int, 16>;
   using EE = integral_constant<int, E>;
   using E24 = integral_constant<int, 24>;
+  using E32 = integral_constant<int, 32>;
   if (h <= 512) return f(W1{}, integral_constant<int, 8>{});
   if (h <= 1024) return f(W1{}, integral_constant<int, 16>{});
-  if (E > 16 && h <= 64 * E) return f(W1{}, EE{});
   if constexpr (E == 16) {
     if (h <= 64 * 24) return f(W1{}, E24{});
     if (h <= 128 * 16) return f(W2{}, EE{});
     if (h <= 128 * 24) return f(W2{}, E24{});
     if (h <= 256 * 16) return f(W4{}, EE{});
     if (h <= 256 * 24) return f(W4{}, E24{});
+    if (h <= 512 * 16) return f(W8{}, EE{});
+    if (h <= 512 * 24) return f(W8{}, E24{});
+    if (h <= 512 * 32) return f(W8{}, E32{});
+  } else {
+    static_assert(E == 32, "E");
+    if (h <= 64 * 32) return f(W1{}, E32{});
+    if (h <= 128 * 32) return f(W2{}, E32{});
+    if (h <= 256 * 32) return f(W4{}, E32{});
+    if (h <= 512 * 32) return f(W8{}, E32{});
   }
-  if (h <= 128 * E) return f(W2{}, EE{});
-  if (h <= 256 * E) return f(W4{}, EE{});
-  if (h <= 512 * E) return f(W8{}, EE{});
-  if (h <= 1024 * E) return f(W16{}, EE{});
-  return f(W16{}, integral_constant<int, 32>{});
+  return f(W16{}, E32{});
 }
 
 template <class T, class P>
@@ -401,14 +463,25 @@ hipError_t run_fwd(const NormFwdArgs& a, hipStream_t s) {
 }
 
 template <class T, class P>
-hipError_t run_bwd_rows(const NormBwdArgs& a, float* part_w, float* part_b, int64_t* rows,
-                        hipStream_t s) {
+hipError_t run_bwd_rows(const NormBwdArgs& a, float* part_w, float* part_b, hipStream_t s) {
+  if (a.n == 0) return hipSuccess;
+  if (a.h > kRegRow && part_w) {
+    constexpr int VE = Elem<T>::kVec;
+    TimedLaunch t(s, K_NORM_BWD);
+    hipLaunchKernelGGL((norm_columns_kernel<T>),
+                       dim3(unsigned((a.h + 256 * VE - 1) / (256 * VE)),
+                            unsigned(part_rows(a.n, a.h))),
+                       dim3(256), 0, s, static_cast<const T*>(a.grad), a.ldg,
+                       static_cast<const T*>(a.x), a.ldx, a.mean, a.rstd, a.n, a.h, part_w,
+                       part_b);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess || !a.grad_x) return e;
+  }
   return with_shape<kBwdElems>(a.h, [&](auto wpr, auto epl) {
     constexpr int WPR = decltype(wpr)::value, EPL = decltype(epl)::value;
     constexpr int RG = norm_threads(WPR, kBwdThreads) / (64 * WPR);
-    const int64_t grid = std::min<int64_t>((a.n + RG - 1) / RG, kBwdGrid);
-    *rows = grid;
-    if (grid == 0) return hipSuccess;
+    constexpr bool PARAMS = 64 * WPR * EPL <= kRegRow;
+    const int64_t grid = std::min<int64_t>((a.n + RG - 1) / RG, bwd_grid(a.h));
     TimedLaunch t(s, K_NORM_BWD);
     auto launch = [&](auto kernel) {
       hipLaunchKernelGGL(kernel, dim3(unsigned(grid)), dim3(norm_threads(WPR, kBwdThreads)), 0, s,
@@ -417,11 +490,24 @@ hipError_t run_bwd_rows(const NormBwdArgs& a, float* part_w, float* part_b, int6
                          static_cast<T*>(a.grad_x), a.lddx, part_w, part_b);
     };
     if (a.h % Elem<T>::kVec == 0)
-      launch(layernorm_bwd_kernel<T, P, WPR, EPL, true>);
+      launch(layernorm_bwd_kernel<T, P, WPR, EPL, true, PARAMS>);
     else
-      launch(layernorm_bwd_kernel<T, P, WPR, EPL, false>);
+      launch(layernorm_bwd_kernel<T, P, WPR, EPL, false, PARAMS>);
     return hipGetLastError();
   });
+}
+
+// Partial rows that run_bwd_rows() leaves.
+int64_t rows_left(int64_t n, int64_t h) {
+  if (n == 0 || h > kRegRow) return part_rows(n, h);
+  int64_t rows = 0;
+  with_shape<kBwdElems>(h, [&](auto wpr, auto) {
+    constexpr int WPR = decltype(wpr)::value;
+    constexpr int RG = norm_threads(WPR, kBwdThreads) / (64 * WPR);
+    rows = std::min<int64_t>((n + RG - 1) / RG, bwd_grid(h));
+    return hipSuccess;
+  });
+  return rows;
 }
 
 template <class P>
@@ -453,7 +539,7 @@ hipError_t layernorm_fwd_run(const NormFwdArgs& a, hipStream_t s) {
 }
 
 size_t layernorm_workspace_bytes(int64_t n, int64_t h) {
-  const int64_t rows = std::min(n, kBwdGrid);
+  const int64_t rows = part_rows(n, h);
   return std::max<size_t>(2 * align256(size_t(rows) * size_t(h) * 4), 256);
 }
 
@@ -464,21 +550,21 @@ hipError_t layernorm_bwd_run(const NormBwdArgs& a, hipStream_t s) {
   if (params) {
     pw = static_cast<float*>(a.workspace);
     pb = reinterpret_cast<float*>(static_cast<char*>(a.workspace) +
-                                  align256(size_t(std::min(a.n, kBwdGrid)) * size_t(a.h) * 4));
+                                  align256(size_t(part_rows(a.n, a.h)) * size_t(a.h) * 4));
   }
-  int64_t rows = 0;
+  const int64_t rows = rows_left(a.n, a.h);
   const bool wide = a.param_dtype == kF32;
   hipError_t e;
   switch (a.dtype) {
     case kBF16:
-      e = wide ? run_bwd_rows<Bf16, float>(a, pw, pb, &rows, s)
-               : run_bwd_rows<Bf16, Bf16>(a, pw, pb, &rows, s);
+      e = wide ? run_bwd_rows<Bf16, float>(a, pw, pb, s)
+               : run_bwd_rows<Bf16, Bf16>(a, pw, pb, s);
       break;
     case kF16:
-      e = wide ? run_bwd_rows<_Float16, float>(a, pw, pb, &rows, s)
-               : run_bwd_rows<_Float16, _Float16>(a, pw, pb, &rows, s);
+      e = wide ? run_bwd_rows<_Float16, float>(a, pw, pb, s)
+               : run_bwd_rows<_Float16, _Float16>(a, pw, pb, s);
       break;
-    default: e = run_bwd_rows<float, float>(a, pw, pb, &rows, s);
+    default: e = run_bwd_rows<float, float>(a, pw, pb, s);
   }
   if (e != hipSuccess || !params) return e;
   switch (a.grad_param_dtype) {

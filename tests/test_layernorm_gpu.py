@@ -261,3 +261,35 @@ def test_rows_past_4_gib(dev):
     size = (g.float() * ((tail.float() - mean[:, None]) * rstd[:, None])).abs().sum(0)
     assert ((bw.float() - gw.float()).abs() <= 2.0 ** -7 * gw.float().abs()
             + 4 * last * 2.0 ** -24 * size).all()
+
+
+@pytest.mark.parametrize("h", [1000, 12288, 12289, 20011])
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_backward_of_long_rows_in_place_and_in_parts(dev, h, dtype):
+    """The parameter sums of the longest rows read the gradient that the rows' own pass overwrites
+    in place; each output alone equals its part of the whole."""
+    x, w, _, g = inputs(333, h, dtype, dtype, dev, seed=6)
+    mean, rstd = stats(x)
+    ref = lce.layernorm_bwd(g, x, mean, rstd, w, grad_bias=True)
+    check_backward(x, g, mean, rstd, w, *ref)
+    z = g.clone()
+    got = lce.layernorm_bwd(z, x, mean, rstd, w, grad_x=z, grad_bias=True)
+    assert got[0] is z and all(torch.equal(a, b) for a, b in zip(got, ref))
+    gx, gw, gb = lce.layernorm_bwd(g, x, mean, rstd, w, grad_weight=False)
+    assert gw is None and gb is None and torch.equal(gx, ref[0])
+    gx, gw, gb = lce.layernorm_bwd(g, x, mean, rstd, w, grad_x=False)
+    assert gx is None and gb is None and torch.equal(gw, ref[1])
+    old = (torch.randn(h, device=dev), torch.randn(h, device=dev))
+    gw, gb = old[0].clone(), old[1].clone()
+    need = lce.layernorm_workspace_size(333, h)
+    ws = torch.full((need + 4096,), 0xFF, dtype=torch.uint8, device=dev)
+    lce.layernorm_bwd(g, x, mean, rstd, w, grad_weight=gw, grad_bias=gb, accumulate=True,
+                      workspace=ws[:need])
+    check_backward(x, g, mean, rstd, w, None, gw, gb, old)
+    assert (ws[need:] == 0xFF).all()
+
+
+def test_backward_of_short_rows_fills_the_partial_rows(dev):
+    x, w, _, g = inputs(9000, 130, torch.float32, torch.float32, dev, seed=7)
+    mean, rstd = stats(x)
+    check_backward(x, g, mean, rstd, w, *lce.layernorm_bwd(g, x, mean, rstd, w, grad_bias=True))
