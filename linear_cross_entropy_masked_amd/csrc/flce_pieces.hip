@@ -24,7 +24,7 @@
 //
 // With at most kScoreRows rows the forward is bound by reading W once, and score_kernel streams
 // it past the rows instead; up to kNarrowRows rows take tiles of half the height with three K
-// slices in flight.
+// slices in the ring, and products of few tiles smaller ones.
 #include <algorithm>
 
 #include "common.h"
@@ -41,6 +41,7 @@ using gemm::f32x4_t;
 using Wide = gemm::v2::CfgWide;
 using Pair = gemm::v2::CfgPair;
 using Narrow = gemm::v2::Cfg<128, 256, 64, 3, 2, 4, 1>;
+using Small = gemm::v2::Cfg<128, 128, 64, 4, 2, 2, 1>;
 
 __host__ __device__ inline int64_t up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
 
@@ -61,6 +62,21 @@ constexpr int kNarrowRows = 128;
 // 60 rows of 2048 and 60000 classes 306 us against 323, of 500 rows and 32000 classes 338 against
 // 344, of 1000 rows of 4096 1005 against 994).
 constexpr int kShortK = 512;
+
+// Products whose 128 x 128 tiles all run at once take those, with three K slices in flight: with so
+// few tiles a product is a chain of slices, each as long as its loads (steps of 682 rows of 3840 and
+// 2066 classes 169 us so and 263 without, 3633 of 88 and 24693 331 and 367, losses of 189 rows of
+// 1904 and 2404 classes 43 and 68; twice as many tiles: 500 rows of 1024 and 15000 classes 153, 151
+// without).
+constexpr int64_t kFewTiles = 256;
+bool few_tiles(int64_t m, int64_t n) {
+  return (m + Small::BM - 1) / Small::BM * ((n + Small::BN - 1) / Small::BN) <= kFewTiles;
+}
+// Classes per tile of the forward's logits product, rows per tile of the backward's.
+int64_t lse_cols(int64_t n, int64_t v) { return few_tiles(n, v) ? Small::BN : Wide::BN; }
+int grad_rows(int64_t n, int64_t v) {
+  return few_tiles(n, v) || n <= kNarrowRows ? Small::BM : Wide::BM;
+}
 
 __device__ __forceinline__ bool labelled(int32_t y, int64_t vocab, int32_t ignore_index) {
   return y != ignore_index && y >= 0 && int64_t(y) < vocab;
@@ -736,13 +752,13 @@ struct BiasOut {
   const int32_t* count;
   long long t_host;
   const float* gout;
-  int rows, accumulate;
+  int rows, accumulate, tile;  // tile: rows that each row of colsum adds up
   float* db;
 };
 __device__ __forceinline__ void bias_reduce(const BiasOut& o, int64_t block) {
   const int64_t c = block * 256 + threadIdx.x;
   if (c >= o.v) return;
-  const int64_t tiles = (int64_t(*o.count) + kTile - 1) / kTile;
+  const int64_t tiles = (int64_t(*o.count) + o.tile - 1) / o.tile;
   float sum = 0.f;
 #pragma unroll 4
   for (int64_t t = 0; t < tiles; ++t) sum += o.colsum[t * o.v64 + c];
@@ -806,7 +822,7 @@ PieceWs carve_fwd(void* base, int64_t n, int64_t h, int64_t v) {
     w.row = c.take<int32_t>(np);
     w.ylab = c.take<int32_t>(np);
     w.zy = c.take<float>(np);
-    w.part = c.take<float2>(np * ((v + Wide::BN - 1) / Wide::BN));
+    w.part = c.take<float2>(np * ((v + lse_cols(n, v) - 1) / lse_cols(n, v)));
     w.hc = c.take<uint16_t>(np * h64);
     if (h64 != h) w.wpad = c.take<uint16_t>(v * h64);
   }
@@ -827,7 +843,7 @@ PieceWs carve_bwd(void* base, int64_t n, int64_t h, int64_t v) {
   w.hc = c.take<uint16_t>(np * h64);
   if (h64 != h) w.wpad = c.take<uint16_t>(v * h64);
   w.d = c.take<uint16_t>(np * v64);
-  w.colsum = c.take<float>(np / kTile * v64);
+  w.colsum = c.take<float>(np / grad_rows(n, v) * v64);
   const int64_t splits = hidden_splits(n, h, v);
   if (splits > 1) w.split = c.take<float>(splits * np * h);
   w.bytes = std::max<size_t>(c.off, 256);
@@ -881,6 +897,8 @@ hipError_t grad_logits(const PieceBwdArgs& a, const PieceWs& w, const View& hv, 
   EpiPieceGrad<BIAS, ROWS> e{w.d, np, a.bias, a.v, w.ylab, w.count, w.lse_c, w.coef_c, w.colsum,
                              v64};
   TimedLaunch t(s, K_PIECE_GRAD_LOGITS);
+  if (few_tiles(a.n, a.v))
+    return gemm::v2::launch<Small, true, true>(hv, wv, np, v64, h64, 1, true, e, s);
   if (a.n <= kNarrowRows)  // one row tile either way
     return gemm::v2::launch<Narrow, true, true>(hv, wv, np, v64, h64, 1, true, e, s);
   return gemm::v2::launch<Wide, true, true>(hv, wv, np, v64, h64, 1, true, e, s, false, kBand);
@@ -892,6 +910,8 @@ hipError_t grad_weight_product(const PieceBwdArgs& a, const PieceWs& w, const Vi
   EpiPieceWeight<TW, ACC> e{static_cast<TW*>(a.grad_weight), a.h, w.count, a.num_label_tokens,
                             a.grad_output, int(a.grad_rows != nullptr), 0.f};
   TimedLaunch t(s, K_PIECE_GRAD_WEIGHT);
+  if (few_tiles(a.v, a.h))
+    return gemm::v2::launch<Small, false, false>(dv, hv, a.v, a.h, up(a.n, kTile), 1, false, e, s);
   if (a.n <= kShortK)
     return gemm::v2::launch<Pair, false, false>(dv, hv, a.v, a.h, up(a.n, kTile), 1, false, e, s);
   return gemm::v2::launch<Wide, false, false>(dv, hv, a.v, a.h, up(a.n, kTile), 1, true, e, s,
@@ -943,7 +963,7 @@ hipError_t piece_fwd_run(const PieceFwdArgs& a, hipStream_t s) {
       launch(score_kernel<2>);
     PIECE_TRY(hipGetLastError());
   } else {
-    tiles = (a.v + Wide::BN - 1) / Wide::BN;
+    tiles = (a.v + lse_cols(a.n, a.v) - 1) / lse_cols(a.n, a.v);
     const int64_t np = up(a.n, kTile), h64 = up(a.h, Wide::BK);
     PIECE_TRY(rows_and_gather(a.hidden, a.labels, a.n, a.h, a.v, a.v_start, a.vocab,
                               a.ignore_index, w, first ? a.state : nullptr, GatherArgs{}, s));
@@ -956,7 +976,9 @@ hipError_t piece_fwd_run(const PieceFwdArgs& a, hipStream_t s) {
     View wv{weight, h64, 64, a.v, h64};
     EpiPieceLse e{a.bias, a.v, w.ylab, w.count, w.part, tiles, w.zy};
     TimedLaunch t(s, K_PIECE_LOGITS);
-    if (a.n <= kNarrowRows)
+    if (few_tiles(a.n, a.v))
+      PIECE_TRY((gemm::v2::launch<Small, true, true>(hv, wv, np, a.v, h64, 1, true, e, s)));
+    else if (a.n <= kNarrowRows)
       PIECE_TRY((gemm::v2::launch<Narrow, true, true>(hv, wv, np, a.v, h64, 1, true, e, s)));
     else
       PIECE_TRY((gemm::v2::launch<Wide, true, true>(hv, wv, np, a.v, h64, 1, true, e, s, false,
@@ -1028,7 +1050,7 @@ hipError_t piece_bwd_run(const PieceBwdArgs& a, hipStream_t s) {
   const bool want_weight = a.grad_weight && !(a.n == 0 && accumulate);
   const bool wide = a.grad_weight_dtype == LCE_DTYPE_F32;
   const int64_t splits = hidden_splits(a.n, a.h, a.v);
-  const bool both = want_hidden && want_weight && splits > 1;
+  const bool both = want_hidden && want_weight && splits > 1 && !few_tiles(a.v, a.h);
   const HiddenOut o{w.row, w.count, a.hidden_acc, last ? a.grad_hidden : nullptr, a.h,
                     int(first), a.num_label_tokens, a.grad_output, int(rows)};
   if (both) {
@@ -1061,7 +1083,7 @@ hipError_t piece_bwd_run(const PieceBwdArgs& a, hipStream_t s) {
   const int64_t bias_blocks = want_bias ? (a.v + 255) / 256 : 0;
   if (hidden_blocks + bias_blocks > 0) {
     const BiasOut b{w.colsum, a.v, v64, w.count, a.num_label_tokens, a.grad_output, int(rows),
-                    int(accumulate), a.grad_bias};
+                    int(accumulate), grad_rows(a.n, a.v), a.grad_bias};
     TimedLaunch t(s, K_PIECE_GRAD_FINISH);
     hipLaunchKernelGGL(piece_finish_kernel, dim3(unsigned(hidden_blocks + bias_blocks)), dim3(256),
                        0, s, w.split, np / kTile, splits, a.v, o, hidden_blocks, b);
