@@ -501,3 +501,44 @@ def test_a_weight_past_4_gib(dev, n):
     size = (w.float().abs().max() * 2 / int(keep.sum())).item()
     assert ((gh.float() - gh2.float()).abs() <= 2 * B * gh.float().abs() + v * U * size).all()
     assert gw[lab[keep].long()].any(1).all()
+
+
+# on either side of the sizes at which the products change their tiles: 128 x 128 ones up to 256
+# of them, else 128 rows up to 128 and 256 past that; the two gradient products apart or together
+EDGES = [(129, 64, 16384), (129, 64, 16385), (40, 72, 32768), (40, 72, 32769), (128, 136, 33001),
+         (8192, 64, 512), (8193, 64, 512), (300, 1000, 4096), (300, 1032, 4097), (700, 1024, 5003)]
+
+
+@pytest.mark.parametrize("n,h,v", EDGES)
+@pytest.mark.parametrize("masked", [0.1, 0.9])
+def test_tile_choices(dev, n, h, v, masked):
+    hid, w, b, lab = make(dev, n, h, v, masked=masked)
+    loss, lse, rows = lce.flce_pieces_fwd(hid, w, lab, b, return_rows=True)
+    e = Exact(hid, w, b, lab)
+    check_fwd(e, loss, lse, rows)
+    check_bwd(e, *lce.flce_pieces_bwd(hid, w, lab, lse, b))
+    check_bwd(e, *lce.flce_pieces_bwd(hid, w, lab, lse, b, grad_hidden=False))
+    check_bwd(e, *lce.flce_pieces_bwd(hid, w, lab, lse, b, grad_weight=False))
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("n,h,v", [(300, 1032, 4097), (100, 256, 2000)])
+def test_both_gradient_products_accumulate(dev, n, h, v, dtype):
+    """Weight gradients in fp32 and added to what is there, with the hidden gradient or without."""
+    hid, w, b, lab = make(dev, n, h, v)
+    _, lse, _ = lce.flce_pieces_fwd(hid, w, lab, b)
+    e = Exact(hid, w, b, lab)
+    fresh = torch.empty(v, h, dtype=dtype, device=dev)
+    gh, _, gb = lce.flce_pieces_bwd(hid, w, lab, lse, b, grad_weight=fresh)
+    check_bwd(e, gh, fresh, gb)
+    for hidden in (True, False):
+        old = torch.randn(v, h, device=dev).to(dtype)
+        buf, bias = old.clone(), torch.zeros(v, device=dev)
+        lce.flce_pieces_bwd(hid, w, lab, lse, b, grad_hidden=hidden, grad_weight=buf,
+                            grad_bias=bias, accumulate=True)
+        # one fp32 addition more, and the sum's rounding to the buffer's type
+        near(buf, e.gw + old.double(), e.dgw + U * (e.gw.abs() + old.double().abs()), "grad_weight")
+        near(bias, e.gb, e.dgb, "grad_bias")
+    none = torch.full_like(lab, IGN)
+    gh, gw, gb = lce.flce_pieces_bwd(hid, w, none, torch.zeros_like(lse), b)
+    assert not gh.any() and not gw.any() and not gb.any()
