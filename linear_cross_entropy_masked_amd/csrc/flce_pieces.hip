@@ -822,7 +822,11 @@ PieceWs carve_fwd(void* base, int64_t n, int64_t h, int64_t v) {
     w.row = c.take<int32_t>(np);
     w.ylab = c.take<int32_t>(np);
     w.zy = c.take<float>(np);
-    w.part = c.take<float2>(np * ((v + lse_cols(n, v) - 1) / lse_cols(n, v)));
+    // enough for any piece of fewer classes too, whose smaller tiles may be more
+    const int64_t few = kFewTiles / ((n + Small::BM - 1) / Small::BM);
+    const int64_t tiles = std::max((v + Wide::BN - 1) / Wide::BN,
+                                   std::min((v + Small::BN - 1) / Small::BN, few));
+    w.part = c.take<float2>(np * tiles);
     w.hc = c.take<uint16_t>(np * h64);
     if (h64 != h) w.wpad = c.take<uint16_t>(v * h64);
   }
@@ -843,7 +847,7 @@ PieceWs carve_bwd(void* base, int64_t n, int64_t h, int64_t v) {
   w.hc = c.take<uint16_t>(np * h64);
   if (h64 != h) w.wpad = c.take<uint16_t>(v * h64);
   w.d = c.take<uint16_t>(np * v64);
-  w.colsum = c.take<float>(np / grad_rows(n, v) * v64);
+  w.colsum = c.take<float>(np / Small::BM * v64);  // as in the forward: for any smaller piece too
   const int64_t splits = hidden_splits(n, h, v);
   if (splits > 1) w.split = c.take<float>(splits * np * h);
   w.bytes = std::max<size_t>(c.off, 256);

@@ -271,3 +271,18 @@ def test_binding_refuses_a_wide_ignore_index(monkeypatch):
             with pytest.raises(ValueError, match="32 bits"):
                 call()
     assert lce._ignore_arg(-(1 << 31)) == -(1 << 31)
+
+
+def test_workspace_of_the_largest_piece_serves_the_others(lib):
+    """At any batch the sizes grow with the piece, so that one workspace serves all pieces."""
+    for n in (1, 32, 33, 128, 129, 700, 2048, 8192, 8193, 40000):
+        for h in (64, 72, 1024):
+            last = (0, 0)
+            vs = sorted({1, 64, 100, 128, 2000, 65536} |
+                        {k * 128 + d for k in (2, 4, 15, 16, 17, 64, 127, 128, 255, 256, 257)
+                         for d in (0, 1)})
+            for v in vs:
+                size = (lce.flce_piece_fwd_workspace_size(n, h, v),
+                        lce.flce_piece_bwd_workspace_size(n, h, v))
+                assert size[0] >= last[0] and size[1] >= last[1], (n, h, v)
+                last = size
