@@ -7,7 +7,8 @@
 //   dH (+)= s · D · W                       fp32 over the pieces, bf16 after the last
 //   dW  =   s · Dᵀ · hidden                 finished: a piece sees every row
 //   db  =   s · Σ_i D                       from the fp32 values
-// with s = g / T and c_i = 1 (summed loss) or s = 1 and c_i the row's own upstream gradient.
+// with s = g / T and c_i = 1 (summed loss), or s the largest of the rows' own upstream gradients
+// and c_i the row's share of it.
 // Four products of 2 · N · H · V flop in all, on the MFMA tile of gemm_tile.h, and bound by them:
 // 8192 x 4096 x 128256, 5% of the rows without a label, takes 6.5 ms forward and 20 ms backward
 // (logits 7.0, dH 6.5, dW 6.5; 1.17 to 1.27 PFLOP/s).
@@ -18,9 +19,10 @@
 // whatever such rows hold (NaN in a padded position) out of dW. The copy costs 4 · N · H bytes
 // against 2 · N · H · V flop.
 //
-// D is rounded to bf16 (an MFMA operand) once, unscaled where the loss is summed, so that the
-// rounding is independent from element to element: a common factor would be rounded the same
-// way in every label element. Half a bf16 step per element, as the outputs' own rounding.
+// D is rounded to bf16 (an MFMA operand) once, without the factor s, so that the rounding is
+// independent from element to element: a common factor would be rounded the same way in every
+// label element, and scale both gradients with it (by 1.0025 for rows that all have 1 / 1003).
+// Half a bf16 step per element, as the outputs' own rounding.
 //
 // With at most kScoreRows rows the forward is bound by reading W once, and score_kernel streams
 // it past the rows instead; up to kNarrowRows rows take tiles of half the height with three K
@@ -82,17 +84,43 @@ __device__ __forceinline__ bool labelled(int32_t y, int64_t vocab, int32_t ignor
   return y != ignore_index && y >= 0 && int64_t(y) < vocab;
 }
 
-// s = g / T; 0 when T = 0. With per-row upstream gradients s = 1.
-__device__ __forceinline__ float loss_scale(const int32_t* count, long long t_host,
-                                            const float* gout, bool rows) {
-  if (rows) return 1.f;
-  const long long t = t_host >= 0 ? t_host : *count;
-  return t > 0 ? float(double(gout ? *gout : 1.f) / double(t)) : 0.f;
-}
+// Where the kernel that counts the labelled rows leaves s = g / T (0 when T = 0). out is NULL where
+// no s is asked for, or where row_scale_kernel has written it.
+struct ScaleOut {
+  float* out;
+  long long t_host;
+  const float* gout;
+  __device__ __forceinline__ void put(long long count) const {
+    if (!out) return;
+    const long long t = t_host >= 0 ? t_host : count;
+    *out = t > 0 ? float(double(gout ? *gout : 1.f) / double(t)) : 0.f;
+  }
+};
 
 // The least maximum a block's exponentials are taken about: where the bias masks every class of a
 // block with minus infinity, there is then a number to subtract, and the sum is 0.
 constexpr float kLeastMax = -3.4028234663852886e38f;
+
+// s for per-row upstream gradients, in one workgroup: the largest finite magnitude among the labelled
+// rows, 1 where that is 0. The other rows' may be anything; a row whose own is infinite or NaN gets
+// that into its gradient, and leaves s to the others.
+__global__ void __launch_bounds__(1024) row_scale_kernel(
+    const float* __restrict__ grad_rows, const int32_t* __restrict__ labels, int64_t n,
+    int64_t vocab, int32_t ignore_index, float* __restrict__ scale) {
+  __shared__ float most[16];
+  float m = 0.f;
+  for (int64_t i = threadIdx.x; i < n; i += 1024) {
+    const float c = fabsf(grad_rows[i]);
+    if (labelled(labels[i], vocab, ignore_index) && c < INFINITY) m = fmaxf(m, c);
+  }
+#pragma unroll
+  for (int off = 32; off >= 1; off >>= 1) m = fmaxf(m, __shfl_xor(m, off, 64));
+  if ((threadIdx.x & 63) == 0) most[threadIdx.x >> 6] = m;
+  __syncthreads();
+  if (threadIdx.x != 0) return;
+  for (int w = 1; w < 16; ++w) m = fmaxf(m, most[w]);
+  *scale = m > 0.f ? m : 1.f;
+}
 
 // ------------------------------------------------------------------ the labelled rows
 
@@ -104,7 +132,8 @@ constexpr int kRowsPer = 8;
 __global__ void __launch_bounds__(1024) piece_rows_kernel(
     const int32_t* __restrict__ labels, int64_t n, int64_t v, int64_t v_start, int64_t vocab,
     int32_t ignore_index, int32_t* __restrict__ count, int32_t* __restrict__ cidx,
-    int32_t* __restrict__ row, int32_t* __restrict__ ylab, float* __restrict__ state) {
+    int32_t* __restrict__ row, int32_t* __restrict__ ylab, float* __restrict__ state,
+    ScaleOut scale) {
   __shared__ int wave_sum[16];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   int done = 0;
@@ -153,7 +182,10 @@ __global__ void __launch_bounds__(1024) piece_rows_kernel(
     }
     done += total;
   }
-  if (threadIdx.x == 0) *count = done;
+  if (threadIdx.x == 0) {
+    *count = done;
+    scale.put(done);
+  }
 }
 
 struct GatherArgs {
@@ -167,6 +199,8 @@ struct GatherArgs {
   // backward only
   const float* lse;
   const float* grad_rows;
+  const float* row_scale;  // c_i = grad_rows[i] / *row_scale
+  ScaleOut scale;
   float* lse_c;
   float* coef_c;
   float* zero_acc;         // rows without a label are zeroed here (NULL: not)
@@ -181,7 +215,7 @@ __device__ __forceinline__ void gather_row(const GatherArgs& a, int64_t i, int64
         c < a.h ? *reinterpret_cast<const uint4*>(a.hidden + i * a.h + c) : zero;
   if (threadIdx.x == 0) {
     if (a.lse_c) a.lse_c[m] = a.lse[i];
-    if (a.coef_c) a.coef_c[m] = a.grad_rows[i];
+    if (a.coef_c) a.coef_c[m] = a.grad_rows[i] / *a.row_scale;
   }
 }
 // The outputs of a row without a label.
@@ -243,7 +277,10 @@ __global__ void __launch_bounds__(256) gather_few_rows_kernel(
   __syncthreads();
   int64_t m = (wave_sum[0] + wave_sum[1]) + (wave_sum[2] + wave_sum[3]);
   if (padding) {
-    if (int64_t(blockIdx.x) == batch && threadIdx.x == 0) *a.count = int32_t(m);
+    if (int64_t(blockIdx.x) == batch && threadIdx.x == 0) {
+      *a.count = int32_t(m);
+      a.scale.put(m);
+    }
     for (int k = 0; k < each; ++k)
       pad_row(a, m + (int64_t(blockIdx.x) - batch) * each + k, m);
     return;
@@ -619,10 +656,7 @@ struct HiddenOut {
   uint16_t* grad;   // bf16 [n, h], written with the last piece (NULL: not)
   int64_t h;
   int first;
-  long long t_host;
-  const float* gout;
-  int rows;
-  __device__ __forceinline__ float scale() const { return loss_scale(count, t_host, gout, rows); }
+  const float* scale;
   __device__ __forceinline__ f32x4_t old(int64_t i, int64_t n) const {
     if (first) return f32x4_t{0.f, 0.f, 0.f, 0.f};
     return *reinterpret_cast<const f32x4_t*>(acc + i * h + n);
@@ -645,7 +679,7 @@ struct EpiPieceHidden {
     f32x4_t old;
     int i;
   };
-  __device__ void begin(int64_t) { s = o.scale(); }
+  __device__ void begin(int64_t) { s = *o.scale; }
   __device__ __forceinline__ int64_t row_limit() const { return *o.count; }
   __device__ __forceinline__ int row_tag(int64_t m) const {
     return m < int64_t(*o.count) ? o.row[m] : -1;
@@ -706,7 +740,7 @@ __device__ __forceinline__ void hidden_reduce(const float* __restrict__ part, in
   for (int64_t z = 0; z < splits; ++z)
     a += *reinterpret_cast<const f32x4_t*>(part + (z * live * kTile + m) * o.h + n);
   const int64_t i = o.row[m];
-  o.put(i, n, o.old(i, n) + o.scale() * a);
+  o.put(i, n, o.old(i, n) + *o.scale * a);
 }
 
 // dW (=|+=) s · acc, in bf16 or fp32; the contraction runs over the labelled rows.
@@ -717,12 +751,10 @@ struct EpiPieceWeight {
   TW* dw;
   int64_t h;
   const int32_t* count;
-  long long t_host;
-  const float* gout;
-  int rows;
+  const float* scale;
   float s;
   using Aux = f32x4_t;
-  __device__ void begin(int64_t) { s = loss_scale(count, t_host, gout, rows); }
+  __device__ void begin(int64_t) { s = *scale; }
   __device__ __forceinline__ int64_t k_limit() const { return *count; }
   __device__ __forceinline__ Aux load4(int64_t m, int64_t n) const {
     if constexpr (!ACC) {
@@ -750,9 +782,8 @@ struct BiasOut {
   const float* colsum;
   int64_t v, v64;
   const int32_t* count;
-  long long t_host;
-  const float* gout;
-  int rows, accumulate, tile;  // tile: rows that each row of colsum adds up
+  const float* scale;
+  int accumulate, tile;  // tile: rows that each row of colsum adds up
   float* db;
 };
 __device__ __forceinline__ void bias_reduce(const BiasOut& o, int64_t block) {
@@ -762,7 +793,7 @@ __device__ __forceinline__ void bias_reduce(const BiasOut& o, int64_t block) {
   float sum = 0.f;
 #pragma unroll 4
   for (int64_t t = 0; t < tiles; ++t) sum += o.colsum[t * o.v64 + c];
-  const float x = loss_scale(o.count, o.t_host, o.gout, o.rows) * sum;
+  const float x = *o.scale * sum;
   o.db[c] = o.accumulate ? o.db[c] + x : x;
 }
 
@@ -792,7 +823,7 @@ int64_t hidden_splits(int64_t n, int64_t h, int64_t v) {
 
 struct PieceWs {
   int32_t *count, *cidx, *row, *ylab;
-  float *zy, *lse_c, *coef_c, *colsum, *split;
+  float *zy, *lse_c, *coef_c, *scale, *colsum, *split;
   float2* part;
   uint16_t *hc, *wpad, *d;
   size_t bytes;
@@ -844,6 +875,7 @@ PieceWs carve_bwd(void* base, int64_t n, int64_t h, int64_t v) {
   w.ylab = c.take<int32_t>(np);
   w.lse_c = c.take<float>(np);
   w.coef_c = c.take<float>(np);
+  w.scale = c.take<float>(1);
   w.hc = c.take<uint16_t>(np * h64);
   if (h64 != h) w.wpad = c.take<uint16_t>(v * h64);
   w.d = c.take<uint16_t>(np * v64);
@@ -881,7 +913,7 @@ hipError_t rows_and_gather(const uint16_t* hidden, const int32_t* labels, int64_
     return hipGetLastError();
   }
   hipLaunchKernelGGL(piece_rows_kernel, dim3(1), dim3(1024), 0, s, labels, n, v, v_start, vocab,
-                     ignore_index, w.count, w.cidx, w.row, w.ylab, state);
+                     ignore_index, w.count, w.cidx, w.row, w.ylab, state, g.scale);
   PIECE_TRY(hipGetLastError());
   hipLaunchKernelGGL(gather_rows_kernel, dim3(unsigned(n + kTile)), dim3(256), 0, s, g);
   return hipGetLastError();
@@ -911,8 +943,7 @@ hipError_t grad_logits(const PieceBwdArgs& a, const PieceWs& w, const View& hv, 
 template <class TW, bool ACC>
 hipError_t grad_weight_product(const PieceBwdArgs& a, const PieceWs& w, const View& dv,
                                const View& hv, hipStream_t s) {
-  EpiPieceWeight<TW, ACC> e{static_cast<TW*>(a.grad_weight), a.h, w.count, a.num_label_tokens,
-                            a.grad_output, int(a.grad_rows != nullptr), 0.f};
+  EpiPieceWeight<TW, ACC> e{static_cast<TW*>(a.grad_weight), a.h, w.count, w.scale, 0.f};
   TimedLaunch t(s, K_PIECE_GRAD_WEIGHT);
   if (few_tiles(a.v, a.h))
     return gemm::v2::launch<Small, false, false>(dv, hv, a.v, a.h, up(a.n, kTile), 1, false, e, s);
@@ -929,9 +960,7 @@ template <class TW, bool ACC>
 hipError_t grad_products(const PieceBwdArgs& a, const PieceWs& w, const View& dv, const View& wk,
                          const View& hk, int64_t splits, hipStream_t s) {
   const EpiPiecePartial eh{w.split, a.h, a.v, w.count, 0, 0};
-  const EpiPieceWeight<TW, ACC> ew{static_cast<TW*>(a.grad_weight), a.h, w.count,
-                                   a.num_label_tokens, a.grad_output,
-                                   int(a.grad_rows != nullptr), 0.f};
+  const EpiPieceWeight<TW, ACC> ew{static_cast<TW*>(a.grad_weight), a.h, w.count, w.scale, 0.f};
   const int64_t np = up(a.n, kTile);
   TimedLaunch t(s, K_PIECE_GRADS);
   return gemm::v2::launch_two<Wide>(
@@ -1027,8 +1056,16 @@ hipError_t piece_bwd_run(const PieceBwdArgs& a, hipStream_t s) {
   g.grad_rows = a.grad_rows;
   g.lse_c = w.lse_c;
   g.coef_c = rows ? w.coef_c : nullptr;
+  g.row_scale = w.scale;
+  g.scale = ScaleOut{rows ? nullptr : w.scale, a.num_label_tokens, a.grad_output};
   g.zero_acc = first && !last ? a.hidden_acc : nullptr;
   g.zero_grad = last ? a.grad_hidden : nullptr;
+  if (rows) {
+    TimedLaunch t(s, K_PIECE_GATHER);
+    hipLaunchKernelGGL(row_scale_kernel, dim3(1), dim3(1024), 0, s, a.grad_rows, a.labels, a.n,
+                       a.vocab, a.ignore_index, w.scale);
+    PIECE_TRY(hipGetLastError());
+  }
   PIECE_TRY(rows_and_gather(a.hidden, a.labels, a.n, a.h, a.v, a.v_start, a.vocab, a.ignore_index,
                             w, nullptr, g, s));
   const uint16_t* weight = a.weight;
@@ -1056,7 +1093,7 @@ hipError_t piece_bwd_run(const PieceBwdArgs& a, hipStream_t s) {
   const int64_t splits = hidden_splits(a.n, a.h, a.v);
   const bool both = want_hidden && want_weight && splits > 1 && !few_tiles(a.v, a.h);
   const HiddenOut o{w.row, w.count, a.hidden_acc, last ? a.grad_hidden : nullptr, a.h,
-                    int(first), a.num_label_tokens, a.grad_output, int(rows)};
+                    int(first), w.scale};
   if (both) {
     if (wide)
       PIECE_TRY((accumulate ? grad_products<float, true>(a, w, dv, wk, hk, splits, s)
@@ -1086,8 +1123,8 @@ hipError_t piece_bwd_run(const PieceBwdArgs& a, hipStream_t s) {
   const int64_t hidden_blocks = want_hidden && splits > 1 ? (a.n * a.h / 4 + 255) / 256 : 0;
   const int64_t bias_blocks = want_bias ? (a.v + 255) / 256 : 0;
   if (hidden_blocks + bias_blocks > 0) {
-    const BiasOut b{w.colsum, a.v, v64, w.count, a.num_label_tokens, a.grad_output, int(rows),
-                    int(accumulate), grad_rows(a.n, a.v), a.grad_bias};
+    const BiasOut b{w.colsum, a.v, v64, w.count, w.scale, int(accumulate), grad_rows(a.n, a.v),
+                    a.grad_bias};
     TimedLaunch t(s, K_PIECE_GRAD_FINISH);
     hipLaunchKernelGGL(piece_finish_kernel, dim3(unsigned(hidden_blocks + bias_blocks)), dim3(256),
                        0, s, w.split, np / kTile, splits, a.v, o, hidden_blocks, b);
