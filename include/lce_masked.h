@@ -348,7 +348,9 @@ int flce_piece_loss(const float* state, const int32_t* labels, int64_t n, int64_
 
 /* Gradients of one piece from the lse over the whole vocabulary:
  *   grad of the logits  d_iv = c_i * (exp(z_iv - lse_i) - [y_i = v]), rounded to bf16 once with a
- *                       common factor left out: g / T, or the largest finite |grad_rows|;
+ *                       common factor left out: g / T, or the largest finite |grad_rows|. What
+ *                       that takes from the label's element is added to the products, except
+ *                       to a bf16 grad_weight that is accumulated into;
  *                       c_i = g / T, or grad_rows[i] (fp32 [n], the upstream gradient of each
  *                       row's term; grad_output and num_label_tokens are then not used)
  *   hidden_acc   fp32 [n, h]: += d * weight (FLCE_PIECE_FIRST: =). Needed where grad_hidden is

@@ -253,6 +253,10 @@ struct SegArgs {
   int64_t join_blocks;  // column blocks of the join
   int64_t fill_from;  // rows from here on that no position names are zeroed by the sums' launch
   int tpr;           // lanes per chunk and column block (a power of two)
+  const float* coef;       // COEF: row i counts coef[i] times
+  const float* scale_dev;  // in place of scale (NULL: not)
+  int32_t* named;          // COEF: set to 1 for the tokens that have rows (NULL: not)
+  __device__ __forceinline__ float factor() const { return scale_dev ? *scale_dev : scale; }
 };
 
 // The first index in [0, n) whose token is >= t, found by the 64 lanes of a wavefront together:
@@ -273,23 +277,30 @@ __device__ __forceinline__ int64_t wave_lower_bound(const int32_t* __restrict__ 
   return lo;
 }
 
-template <class TW, int N, bool ACC>
+// A finished sum as it goes into the table. Weighted ones are rounded to bf16 whatever the table's
+// type, so that what is built on them is the same in both: for flce_pieces.hip half a step of a
+// remainder of half a step.
+template <bool COEF>
+__device__ __forceinline__ float finished(float scale, float acc) {
+  return scale * (COEF ? bf16_to_f32(f32_to_bf16(acc)) : acc);
+}
+template <class TW, int N, bool ACC, bool COEF>
 __device__ __forceinline__ void put_sum(TW* p, int64_t cnt, float scale, const float (&acc)[N]) {
   float x[N];
   if constexpr (ACC) {
     load_some<TW, N>(p, cnt, x);
 #pragma unroll
-    for (int q = 0; q < N; ++q) x[q] += scale * acc[q];
+    for (int q = 0; q < N; ++q) x[q] += finished<COEF>(scale, acc[q]);
   } else {
 #pragma unroll
-    for (int q = 0; q < N; ++q) x[q] = scale * acc[q];
+    for (int q = 0; q < N; ++q) x[q] = finished<COEF>(scale, acc[q]);
   }
   store_some<TW, N>(p, cnt, x);
 }
 
 constexpr int kBatch = 4;  // rows in flight per lane (8: 314 us, 16: 374 us where 4 take 306)
 
-template <class T, class TW, bool ACC>
+template <class T, class TW, bool ACC, bool COEF>
 __global__ void __launch_bounds__(kThreads) segment_sums_kernel(SegArgs a) {
   constexpr int VE = Elem<T>::kVec;
   TW* const dw = static_cast<TW*>(a.dw);
@@ -336,25 +347,28 @@ __global__ void __launch_bounds__(kThreads) segment_sums_kernel(SegArgs a) {
   int32_t cur = a.stok[p0];
   if (cur >= none) return;
   bool from_left = p0 > 0 && a.stok[p0 - 1] == cur;
+  const float scale = a.factor();
   float acc[VE] = {};
   auto flush = [&](bool to_right) {
+    if (COEF && a.named && col == 0) a.named[cur] = 1;
     if (from_left || to_right) {
       float* p = a.part + (chunk * 2 + (from_left ? 0 : 1)) * a.h + col;
 #pragma unroll
       for (int q = 0; q < VE; ++q)
         if (q < cnt) p[q] = acc[q];
     } else {
-      put_sum<TW, VE, ACC>(dw + int64_t(cur) * a.ldw + col, cnt, a.scale, acc);
+      put_sum<TW, VE, ACC, COEF>(dw + int64_t(cur) * a.ldw + col, cnt, scale, acc);
     }
   };
   for (int64_t p = p0; p < p1; p += kBatch) {
     int32_t tok[kBatch];
-    float x[kBatch][VE];
+    float x[kBatch][VE], c[kBatch];
 #pragma unroll
     for (int u = 0; u < kBatch; ++u) {
       tok[u] = p + u < p1 ? a.stok[p + u] : none;
       const int64_t row = tok[u] < none ? a.spos[p + u] : 0;
       if (tok[u] < none) load_some<T, VE>(g + row * a.ldg, cnt, x[u]);
+      c[u] = COEF && tok[u] < none ? a.coef[row] : 1.f;
     }
 #pragma unroll
     for (int u = 0; u < kBatch; ++u) {
@@ -367,7 +381,7 @@ __global__ void __launch_bounds__(kThreads) segment_sums_kernel(SegArgs a) {
         for (int q = 0; q < VE; ++q) acc[q] = 0.f;
       }
 #pragma unroll
-      for (int q = 0; q < VE; ++q) acc[q] += x[u][q];
+      for (int q = 0; q < VE; ++q) acc[q] += COEF ? c[u] * x[u][q] : x[u][q];
     }
   }
   flush(p1 < a.n && a.stok[p1] == cur);
@@ -377,7 +391,7 @@ __global__ void __launch_bounds__(kThreads) segment_sums_kernel(SegArgs a) {
 // a wavefront (every fourth chunk) and then in wavefront order. Four columns a lane, 256 a
 // workgroup; the token's end is searched for, so that the loads do not wait for one another.
 constexpr int kJoinCols = 256;
-template <class T, class TW, bool ACC>
+template <class T, class TW, bool ACC, bool COEF>
 __global__ void __launch_bounds__(256) join_chunks_kernel(SegArgs a) {
   const int64_t chunk = int64_t(blockIdx.x) / a.join_blocks;
   const int64_t p0 = chunk * a.len, p1 = p0 + a.len;  // a later chunk exists: p1 < n
@@ -419,11 +433,12 @@ __global__ void __launch_bounds__(256) join_chunks_kernel(SegArgs a) {
   for (int q = 0; q < 4; ++q)
     acc[q] = ((sum[0][4 * lane + q] + sum[1][4 * lane + q]) + sum[2][4 * lane + q]) +
              sum[3][4 * lane + q];
+  const float scale = a.factor();
   TW* d = static_cast<TW*>(a.dw) + int64_t(cur) * a.ldw + col;
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
     if (q >= cnt) break;
-    const float x = a.scale * acc[q];
+    const float x = finished<COEF>(scale, acc[q]);
     d[q] = Elem<TW>::from_f32(ACC ? Elem<TW>::to_f32(d[q]) + x : x);
   }
 }
@@ -437,7 +452,11 @@ int pow2_at_least(int64_t x, int cap) {
 // Positions per chunk: about 1024 chunks, at least 8 positions (the rows one lane has in
 // flight) and at most 512 (so that the partial sums of one chunk border stay a small share of
 // the rows read).
-int64_t chunk_len(int64_t n) { return pow2_at_least(std::max<int64_t>(8, (n + 1023) / 1024), 512); }
+// Weighted rows take about 512: half the partial sums, which stand beside the logit gradients there.
+constexpr int64_t kChunks = 1024, kWeightedChunks = 512;
+int64_t chunk_len(int64_t n, int64_t most) {
+  return pow2_at_least(std::max<int64_t>(8, (n + most - 1) / most), 512);
+}
 
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
@@ -446,7 +465,7 @@ struct EmbedWs {
   float* part;
   size_t bytes;
 };
-EmbedWs carve(void* base, int64_t n, int64_t h) {
+EmbedWs carve(void* base, int64_t n, int64_t h, int64_t most) {
   char* b = static_cast<char*>(base);
   EmbedWs w{};
   size_t off = 0;
@@ -460,44 +479,47 @@ EmbedWs carve(void* base, int64_t n, int64_t h) {
     w.tok[k] = reinterpret_cast<int32_t*>(take(size_t(n) * 4));
     w.pos[k] = reinterpret_cast<int32_t*>(take(size_t(n) * 4));
   }
-  const int64_t len = chunk_len(n), chunks = (n + len - 1) / len;
+  const int64_t len = chunk_len(n, most), chunks = (n + len - 1) / len;
   w.part = reinterpret_cast<float*>(take(size_t(chunks) * 2 * size_t(h) * 4));
   w.bytes = std::max<size_t>(off, 256);
   return w;
 }
 
-template <class T, class TW, bool ACC>
+template <class T, class TW, bool ACC, bool COEF>
 hipError_t run_segments(const SegArgs& a, hipStream_t s) {
   {
     TimedLaunch t(s, K_EMBED_GRAD);
-    const int64_t fill = ACC ? 0 : (a.v - a.fill_from + kFillRows - 1) / kFillRows;
-    hipLaunchKernelGGL((segment_sums_kernel<T, TW, ACC>), dim3(unsigned(a.seg_blocks + fill)),
+    const int64_t fill = ACC || COEF ? 0 : (a.v - a.fill_from + kFillRows - 1) / kFillRows;
+    hipLaunchKernelGGL((segment_sums_kernel<T, TW, ACC, COEF>), dim3(unsigned(a.seg_blocks + fill)),
                        dim3(kThreads), 0, s, a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || a.chunks <= 1) return e;
   }
   TimedLaunch t(s, K_EMBED_JOIN);
-  hipLaunchKernelGGL((join_chunks_kernel<T, TW, ACC>),
+  hipLaunchKernelGGL((join_chunks_kernel<T, TW, ACC, COEF>),
                      dim3(unsigned((a.chunks - 1) * a.join_blocks)), dim3(256), 0, s, a);
   return hipGetLastError();
 }
 
-template <class T, class TW>
-hipError_t run_bwd(const EmbedBwdArgs& a, hipStream_t s) {
-  const bool acc = (a.flags & EMBED_ACCUMULATE) != 0;
-  const EmbedWs ws = carve(a.workspace, a.n, a.h);
+template <class T, class TW, bool COEF = false>
+hipError_t run_bwd(const EmbedBwdArgs& a, hipStream_t s, const float* coef = nullptr,
+                   const float* scale_dev = nullptr, bool sorted = false,
+                   int32_t* named = nullptr) {
+  constexpr int64_t kMost = COEF ? kWeightedChunks : kChunks;
+  const bool acc = (a.flags & EMBED_ACCUMULATE) != 0, keep = acc || COEF;
+  const EmbedWs ws = carve(a.workspace, a.n, a.h, kMost);
   const int64_t runs = (a.n + kRun - 1) / kRun;
   const int64_t last = a.n - (runs - 1) * kRun;
   const int64_t sort_blocks =
       a.n > 0 ? (runs - 1) * (kRun / kRankRows) + (last + kRankRows - 1) / kRankRows : 0;
   // without positions there is no launch of the sums: all of dW at once
   const int64_t most = kZeroFirst / (a.h * int64_t(sizeof(TW)));
-  const int64_t first = acc ? 0 : a.n == 0 ? a.v : std::min(a.v, most);
+  const int64_t first = keep ? 0 : a.n == 0 ? a.v : std::min(a.v, most);
   ZeroArgs zero{a.grad_weight, first, a.h, a.ldw};
   if (a.ldw == a.h) zero = ZeroArgs{a.grad_weight, 1, first * a.h, 0};
-  const int64_t blocks = sort_blocks + (acc ? 0 : zero_blocks<TW>(zero));
+  const int64_t blocks = sort_blocks + (keep ? 0 : zero_blocks<TW>(zero));
   hipError_t e;
-  if (blocks > 0) {
+  if (blocks > 0 && !sorted) {
     TimedLaunch t(s, K_EMBED_SORT);
     auto launch = [&](auto kernel) {
       hipLaunchKernelGGL(kernel, dim3(unsigned(blocks)), dim3(64 * kRankWaves), 0, s, a.tokens,
@@ -511,7 +533,7 @@ hipError_t run_bwd(const EmbedBwdArgs& a, hipStream_t s) {
   }
   if (a.n == 0) return hipSuccess;
   int cur = 0;
-  for (int64_t len = kRun; len < a.n; len *= kMergeWays) {
+  for (int64_t len = kRun; len < a.n && !sorted; len *= kMergeWays) {
     TimedLaunch t(s, K_EMBED_SORT);
     hipLaunchKernelGGL(merge_runs_kernel,
                        dim3(unsigned((a.n + kMergeThreads - 1) / kMergeThreads)),
@@ -534,14 +556,17 @@ hipError_t run_bwd(const EmbedBwdArgs& a, hipStream_t s) {
   g.part = ws.part;
   g.join_blocks = (a.h + kJoinCols - 1) / kJoinCols;
   g.fill_from = first;
-  g.len = chunk_len(a.n);
+  g.len = chunk_len(a.n, kMost);
   g.chunks = (a.n + g.len - 1) / g.len;
   const int64_t vecs = (a.h + Elem<T>::kVec - 1) / Elem<T>::kVec;
   g.tpr = pow2_at_least(vecs, kThreads);
   g.colblocks = (vecs + g.tpr - 1) / g.tpr;
   const int64_t per = kThreads / g.tpr;
   g.seg_blocks = (g.chunks * g.colblocks + per - 1) / per;
-  return acc ? run_segments<T, TW, true>(g, s) : run_segments<T, TW, false>(g, s);
+  g.coef = coef;
+  g.scale_dev = scale_dev;
+  g.named = named;
+  return acc ? run_segments<T, TW, true, COEF>(g, s) : run_segments<T, TW, false, COEF>(g, s);
 }
 
 template <class T>
@@ -579,7 +604,12 @@ hipError_t embed_fwd_run(const EmbedFwdArgs& a, hipStream_t s) {
   }
 }
 
-size_t embed_workspace_bytes(int64_t n, int64_t h) { return carve(nullptr, n, h).bytes; }
+size_t embed_workspace_bytes(int64_t n, int64_t h) {
+  return carve(nullptr, n, h, kChunks).bytes;
+}
+size_t embed_weighted_workspace_bytes(int64_t n, int64_t h) {
+  return carve(nullptr, n, h, kWeightedChunks).bytes;
+}
 
 hipError_t embed_bwd_run(const EmbedBwdArgs& a, hipStream_t s) {
   hipError_t e = token_status(a.tokens, a.n, a.v, a.ignore_index, a.status_out, s);
@@ -590,6 +620,18 @@ hipError_t embed_bwd_run(const EmbedBwdArgs& a, hipStream_t s) {
     case kF16: return wide ? run_bwd<_Float16, float>(a, s) : run_bwd<_Float16, _Float16>(a, s);
     default: return run_bwd<float, float>(a, s);
   }
+}
+
+void embed_weighted_order(void* workspace, int64_t n, int64_t h, int32_t** tokens, int32_t** rows) {
+  const EmbedWs w = carve(workspace, n, h, kWeightedChunks);
+  *tokens = w.tok[0];
+  *rows = w.pos[0];
+}
+
+hipError_t embed_weighted_run(const EmbedBwdArgs& a, const float* coef, const float* scale,
+                              bool sorted, int32_t* named, hipStream_t s) {
+  return a.grad_dtype == kF32 ? run_bwd<Bf16, float, true>(a, s, coef, scale, sorted, named)
+                              : run_bwd<Bf16, Bf16, true>(a, s, coef, scale, sorted, named);
 }
 
 }  // namespace lce

@@ -22,7 +22,14 @@
 // D is rounded to bf16 (an MFMA operand) once, without the factor s, so that the rounding is
 // independent from element to element: a common factor would be rounded the same way in every
 // label element, and scale both gradients with it (by 1.0025 for rows that all have 1 / 1003).
-// Half a bf16 step per element, as the outputs' own rounding.
+// Half a bf16 step per element. A row's label element is as large as all its others together, and
+// what the rounding leaves of it is kept in fp32 (e_i) and added to the products: s · e_i · W[y_i] to
+// dH, s · e_i · hidden_i to row y_i of dW, the rows put in the order of their labels as for the
+// table's gradient (embed_kernels.hip; a bf16 dW that is added to has no bits for that). 1024 rows of
+// 768 and 32777 classes, label logits raised by 0 / 6 / 12: norm-wise error of dW in fp32 2.8e-5 /
+// 2.9e-5 / 3.1e-5, and 6.4e-5 / 1.1e-3 / 1.6e-3 without the remainder; of dW in bf16 1.47e-3 / 1.65e-3
+// / 1.66e-3, its own rounding, and 1.47e-3 / 1.99e-3 / 2.28e-3. It takes 28 of 387 us of the step of
+// 2048 x 768 x 32777 with half the rows labelled, 0.4 of 27.2 ms at 8192 x 4096 x 128256.
 //
 // With at most kScoreRows rows the forward is bound by reading W once, and score_kernel streams
 // it past the rows instead; up to kNarrowRows rows take tiles of half the height with three K
@@ -33,6 +40,7 @@
 #include "flce_pieces.h"
 #include "gemm_tile.h"
 #include "lce_masked.h"
+#include "ops.h"
 
 namespace lce {
 
@@ -40,6 +48,7 @@ namespace {
 
 using gemm::View;
 using gemm::f32x4_t;
+typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
 using Wide = gemm::v2::CfgWide;
 using Pair = gemm::v2::CfgPair;
 using Narrow = gemm::v2::Cfg<128, 256, 64, 3, 2, 4, 1>;
@@ -125,8 +134,8 @@ __global__ void __launch_bounds__(1024) row_scale_kernel(
 // ------------------------------------------------------------------ the labelled rows
 
 // Numbers the rows that carry a label in their order: cidx[i] = the row's number or −1, and for
-// the m-th of them row[m] = i and ylab[m] = its label relative to the piece (−1 outside it);
-// *count of them. With `state`, the other rows' state is set to (−inf, 0, 0). One workgroup,
+// the m-th of them row[m] = i and ylab[m] = its label relative to the piece (−1 outside it, and up
+// to up(n, kTile)); *count of them. With `state`, the other rows' state is set to (−inf, 0, 0). One workgroup,
 // kRowsPer rows a thread and round.
 constexpr int kRowsPer = 8;
 __global__ void __launch_bounds__(1024) piece_rows_kernel(
@@ -182,6 +191,7 @@ __global__ void __launch_bounds__(1024) piece_rows_kernel(
     }
     done += total;
   }
+  for (int64_t m = done + int64_t(threadIdx.x); m < up(n, kTile); m += 1024) ylab[m] = -1;
   if (threadIdx.x == 0) {
     *count = done;
     scale.put(done);
@@ -197,6 +207,9 @@ struct GatherArgs {
   int32_t* ylab;
   uint16_t* hc;            // [up(n, kTile)][h64]
   // backward only
+  int64_t v;
+  int32_t* named;          // zeroed here: v flags (NULL: not)
+  int32_t *stok, *spos;    // gather_few_rows_kernel: the rows in the order of ylab (NULL: not)
   const float* lse;
   const float* grad_rows;
   const float* row_scale;  // c_i = grad_rows[i] / *row_scale
@@ -234,15 +247,21 @@ __device__ __forceinline__ void pad_row(const GatherArgs& a, int64_t m, int64_t 
   for (int64_t c = 8 * int64_t(threadIdx.x); c < a.h64; c += 8 * 256)
     *reinterpret_cast<uint4*>(a.hc + m * a.h64 + c) = uint4{0u, 0u, 0u, 0u};
   if (threadIdx.x == 0) {
-    a.ylab[m] = -1;
     if (a.lse_c) a.lse_c[m] = INFINITY;
     if (a.coef_c) a.coef_c[m] = 0.f;
   }
 }
 
+__device__ __forceinline__ void clear_named(const GatherArgs& a) {
+  if (!a.named) return;
+  for (int64_t c = int64_t(blockIdx.x) * 256 + threadIdx.x; c < a.v; c += int64_t(gridDim.x) * 256)
+    a.named[c] = 0;
+}
+
 // One workgroup per row of the batch, numbered by piece_rows_kernel, then kTile for the padding.
 __global__ void __launch_bounds__(256) gather_rows_kernel(GatherArgs a) {
   const int64_t i = blockIdx.x;
+  clear_named(a);
   if (i >= a.n) {
     const int64_t count = *a.count;
     pad_row(a, count + (i - a.n), count);
@@ -257,7 +276,9 @@ __global__ void __launch_bounds__(256) gather_rows_kernel(GatherArgs a) {
 
 // Numbering and gathering in one launch, for batches short enough that every workgroup can count
 // the labelled rows before its own: `each` rows per workgroup (one for the shortest batches, where
-// a row's copy is all latency, else kFewEach; a divisor of kTile).
+// a row's copy is all latency, else kFewEach; a divisor of kTile). Where the order of the labels is
+// asked for, each workgroup finds its rows' places on the way: the number of rows whose label in the
+// piece is smaller, or the same and earlier (labels outside it count as v, after all others).
 constexpr int64_t kFewRows = 8192;
 constexpr int kFewEach = 4;
 int few_each(int64_t n) { return n <= 1024 ? 1 : kFewEach; }
@@ -267,19 +288,47 @@ __global__ void __launch_bounds__(256) gather_few_rows_kernel(
   const int64_t batch = (a.n + each - 1) / each;
   const bool padding = int64_t(blockIdx.x) >= batch;
   const int64_t i0 = padding ? a.n : int64_t(blockIdx.x) * each;
-  int before = 0;
-  for (int64_t j = threadIdx.x; j < i0; j += 256)
-    before += labelled(labels[j], vocab, ignore_index);
+  clear_named(a);
+  auto label_at = [&](int32_t y) {  // its class in the piece
+    const int64_t d = int64_t(y) - v_start;
+    return labelled(y, vocab, ignore_index) && d >= 0 && d < v ? int32_t(d) : int32_t(v);
+  };
+  __shared__ int wave_sum[4][1 + kFewEach];
+  int sum[1 + kFewEach] = {};  // labelled rows before i0, places of the rows from there
+  if (a.stok && !padding) {
+    int32_t key[kFewEach];
 #pragma unroll
-  for (int off = 32; off >= 1; off >>= 1) before += __shfl_xor(before, off, 64);
-  __shared__ int wave_sum[4];
-  if ((threadIdx.x & 63) == 0) wave_sum[threadIdx.x >> 6] = before;
+    for (int k = 0; k < kFewEach; ++k)
+      key[k] = k < each && i0 + k < a.n ? label_at(labels[i0 + k]) : -1;
+    for (int64_t j = threadIdx.x; j < a.n; j += 256) {
+      const int32_t y = labels[j], t = label_at(y);
+      sum[0] += j < i0 && labelled(y, vocab, ignore_index);
+#pragma unroll
+      for (int k = 0; k < kFewEach; ++k)
+        sum[1 + k] += t < key[k] || (t == key[k] && j < i0 + k);
+    }
+  } else {
+    for (int64_t j = threadIdx.x; j < i0; j += 256)
+      sum[0] += labelled(labels[j], vocab, ignore_index);
+  }
+#pragma unroll
+  for (int k = 0; k <= kFewEach; ++k) {
+#pragma unroll
+    for (int off = 32; off >= 1; off >>= 1) sum[k] += __shfl_xor(sum[k], off, 64);
+    if ((threadIdx.x & 63) == 0) wave_sum[threadIdx.x >> 6][k] = sum[k];
+  }
   __syncthreads();
-  int64_t m = (wave_sum[0] + wave_sum[1]) + (wave_sum[2] + wave_sum[3]);
+  auto total = [&](int k) {
+    return (wave_sum[0][k] + wave_sum[1][k]) + (wave_sum[2][k] + wave_sum[3][k]);
+  };
+  int64_t m = total(0);
   if (padding) {
-    if (int64_t(blockIdx.x) == batch && threadIdx.x == 0) {
-      *a.count = int32_t(m);
-      a.scale.put(m);
+    if (int64_t(blockIdx.x) == batch) {
+      for (int64_t j = m + threadIdx.x; j < up(a.n, kTile); j += 256) a.ylab[j] = -1;
+      if (threadIdx.x == 0) {
+        *a.count = int32_t(m);
+        a.scale.put(m);
+      }
     }
     for (int k = 0; k < each; ++k)
       pad_row(a, m + (int64_t(blockIdx.x) - batch) * each + k, m);
@@ -287,6 +336,11 @@ __global__ void __launch_bounds__(256) gather_few_rows_kernel(
   }
   for (int64_t i = i0; i < i0 + each && i < a.n; ++i) {
     const int32_t y = labels[i];
+    if (a.stok && threadIdx.x == 0) {
+      const int place = total(1 + int(i - i0));
+      a.stok[place] = label_at(y);
+      a.spos[place] = int32_t(m);
+    }
     if (labelled(y, vocab, ignore_index)) {
       gather_row(a, i, m);
       if (threadIdx.x == 0) {
@@ -594,8 +648,8 @@ __global__ void __launch_bounds__(256) loss_terms_kernel(LossArgs a, float* __re
 
 // D = c · (exp(z − lse) − [v = y]) in bf16, in panels of 64 columns ([np][64] each, so that both
 // products read whole 128-byte lines one after the other); 0 in the columns v .. up(v, 64) − 1
-// and in the padding rows. BIAS: each tile's column sums of the fp32 values. ROWS: c is the
-// row's own coefficient, else 1.
+// and in the padding rows. What the rounding takes from a label's element goes to left[m]. BIAS: each
+// tile's column sums of the fp32 values. ROWS: c is the row's own coefficient, else 1.
 template <bool BIAS, bool ROWS>
 struct EpiPieceGrad {
   static constexpr bool kRowStats = false, kColSums = BIAS, kTileMax = false, kRowTag = true;
@@ -608,6 +662,7 @@ struct EpiPieceGrad {
   const int32_t* count;
   const float* lse;
   const float* coef;
+  float* left;
   float* colsum;
   int64_t v64;
   using Col = f32x4_t;
@@ -633,10 +688,17 @@ struct EpiPieceGrad {
     const unsigned at = unsigned(x.y) - unsigned(n);
     f32x4_t r;
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      r[q] = fast_exp2(((a[q] + b[q]) - x.lse) * kLog2e);
-      if (at == unsigned(q)) r[q] -= 1.f;
-      if (ROWS) r[q] *= x.c;
+    for (int q = 0; q < 4; ++q) r[q] = fast_exp2(((a[q] + b[q]) - x.lse) * kLog2e);
+    if (at < 4) {  // once a row
+      float e = (at == 0 ? r[0] : at == 1 ? r[1] : at == 2 ? r[2] : r[3]) - 1.f;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) r[q] = at == unsigned(q) ? e : r[q];
+      if (ROWS) e *= x.c;
+      left[m] = e - bf16_to_f32(f32_to_bf16(e));
+    }
+    if (ROWS) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) r[q] *= x.c;
     }
     *reinterpret_cast<uint2*>(d + (n >> 6) * np * 64 + m * 64 + (n & 63)) =
         uint2{pack_bf16x2(r[0], r[1]), pack_bf16x2(r[2], r[3])};
@@ -657,9 +719,19 @@ struct HiddenOut {
   int64_t h;
   int first;
   const float* scale;
+  const int32_t* ylab;
+  const float* left;        // of the labels in this piece: what D's label element lacks
+  const uint16_t* weight;   // the piece's rows, ldw apart
+  int64_t ldw;
   __device__ __forceinline__ f32x4_t old(int64_t i, int64_t n) const {
     if (first) return f32x4_t{0.f, 0.f, 0.f, 0.f};
     return *reinterpret_cast<const f32x4_t*>(acc + i * h + n);
+  }
+  __device__ __forceinline__ f32x4_t label(int64_t m, int64_t n) const {
+    const int32_t y = ylab[m];
+    if (y < 0) return f32x4_t{0.f, 0.f, 0.f, 0.f};
+    const uint2 w = *reinterpret_cast<const uint2*>(weight + int64_t(y) * ldw + n);
+    return left[m] * f32x4_t{bf16_lo(w.x), bf16_hi(w.x), bf16_lo(w.y), bf16_hi(w.y)};
   }
   __device__ __forceinline__ void put(int64_t i, int64_t n, f32x4_t x) const {
     if (grad)
@@ -684,8 +756,8 @@ struct EpiPieceHidden {
   __device__ __forceinline__ int row_tag(int64_t m) const {
     return m < int64_t(*o.count) ? o.row[m] : -1;
   }
-  __device__ __forceinline__ Aux load4t(int64_t, int64_t n, int i) const {
-    return {i >= 0 ? o.old(i, n) : f32x4_t{0.f, 0.f, 0.f, 0.f}, i};
+  __device__ __forceinline__ Aux load4t(int64_t m, int64_t n, int i) const {
+    return {i >= 0 ? o.old(i, n) + s * o.label(m, n) : f32x4_t{0.f, 0.f, 0.f, 0.f}, i};
   }
   __device__ __forceinline__ void store4(int64_t, int64_t n, f32x4_t a, const Aux& x) {
     if (x.i >= 0) o.put(x.i, n, x.old + s * a);
@@ -740,19 +812,33 @@ __device__ __forceinline__ void hidden_reduce(const float* __restrict__ part, in
   for (int64_t z = 0; z < splits; ++z)
     a += *reinterpret_cast<const f32x4_t*>(part + (z * live * kTile + m) * o.h + n);
   const int64_t i = o.row[m];
-  o.put(i, n, o.old(i, n) + *o.scale * a);
+  o.put(i, n, o.old(i, n) + *o.scale * (a + o.label(m, n)));
 }
 
-// dW (=|+=) s · acc, in bf16 or fp32; the contraction runs over the labelled rows.
+// dW (=|+=) s · acc, in bf16 or fp32; the contraction runs over the labelled rows. Where dW is
+// overwritten, the rows of the classes that are some row's label (named) hold Σ e_i · hidden_i, what
+// D's label elements lack, and the sums start from that.
 template <class TW, bool ACC>
 struct EpiPieceWeight {
   static constexpr bool kRowStats = false, kColSums = false, kTileMax = false;
-  static constexpr bool kKLimit = true;
+  static constexpr bool kKLimit = true, kAccInit = !ACC;
   TW* dw;
   int64_t h;
   const int32_t* count;
+  const int32_t* named;
   const float* scale;
   float s;
+  using Init = std::conditional_t<sizeof(TW) == 4, f32x4_t, u32x2_t>;
+  __device__ __forceinline__ bool init_row(int64_t m) const { return named[m] != 0; }
+  __device__ __forceinline__ Init init_load(int64_t m, int64_t n) const {
+    return *reinterpret_cast<const Init*>(dw + m * h + n);
+  }
+  static __device__ __forceinline__ f32x4_t init_value(Init x) {
+    if constexpr (sizeof(TW) == 4)
+      return x;
+    else
+      return f32x4_t{bf16_lo(x[0]), bf16_hi(x[0]), bf16_lo(x[1]), bf16_hi(x[1])};
+  }
   using Aux = f32x4_t;
   __device__ void begin(int64_t) { s = *scale; }
   __device__ __forceinline__ int64_t k_limit() const { return *count; }
@@ -822,8 +908,9 @@ int64_t hidden_splits(int64_t n, int64_t h, int64_t v) {
 }
 
 struct PieceWs {
-  int32_t *count, *cidx, *row, *ylab;
-  float *zy, *lse_c, *coef_c, *scale, *colsum, *split;
+  int32_t *count, *cidx, *row, *ylab, *named;
+  void* order;
+  float *zy, *lse_c, *coef_c, *left, *scale, *colsum, *split;
   float2* part;
   uint16_t *hc, *wpad, *d;
   size_t bytes;
@@ -875,10 +962,13 @@ PieceWs carve_bwd(void* base, int64_t n, int64_t h, int64_t v) {
   w.ylab = c.take<int32_t>(np);
   w.lse_c = c.take<float>(np);
   w.coef_c = c.take<float>(np);
+  w.left = c.take<float>(np);
   w.scale = c.take<float>(1);
   w.hc = c.take<uint16_t>(np * h64);
   if (h64 != h) w.wpad = c.take<uint16_t>(v * h64);
   w.d = c.take<uint16_t>(np * v64);
+  w.named = c.take<int32_t>(v);
+  w.order = c.take<char>(int64_t(embed_weighted_workspace_bytes(n, h)));
   w.colsum = c.take<float>(np / Small::BM * v64);  // as in the forward: for any smaller piece too
   const int64_t splits = hidden_splits(n, h, v);
   if (splits > 1) w.split = c.take<float>(splits * np * h);
@@ -930,8 +1020,8 @@ template <bool BIAS, bool ROWS>
 hipError_t grad_logits(const PieceBwdArgs& a, const PieceWs& w, const View& hv, const View& wv,
                        hipStream_t s) {
   const int64_t np = up(a.n, kTile), v64 = up(a.v, 64), h64 = up(a.h, Wide::BK);
-  EpiPieceGrad<BIAS, ROWS> e{w.d, np, a.bias, a.v, w.ylab, w.count, w.lse_c, w.coef_c, w.colsum,
-                             v64};
+  EpiPieceGrad<BIAS, ROWS> e{w.d, np, a.bias, a.v, w.ylab, w.count, w.lse_c, w.coef_c, w.left,
+                             w.colsum, v64};
   TimedLaunch t(s, K_PIECE_GRAD_LOGITS);
   if (few_tiles(a.n, a.v))
     return gemm::v2::launch<Small, true, true>(hv, wv, np, v64, h64, 1, true, e, s);
@@ -943,7 +1033,7 @@ hipError_t grad_logits(const PieceBwdArgs& a, const PieceWs& w, const View& hv, 
 template <class TW, bool ACC>
 hipError_t grad_weight_product(const PieceBwdArgs& a, const PieceWs& w, const View& dv,
                                const View& hv, hipStream_t s) {
-  EpiPieceWeight<TW, ACC> e{static_cast<TW*>(a.grad_weight), a.h, w.count, w.scale, 0.f};
+  EpiPieceWeight<TW, ACC> e{static_cast<TW*>(a.grad_weight), a.h, w.count, w.named, w.scale, 0.f};
   TimedLaunch t(s, K_PIECE_GRAD_WEIGHT);
   if (few_tiles(a.v, a.h))
     return gemm::v2::launch<Small, false, false>(dv, hv, a.v, a.h, up(a.n, kTile), 1, false, e, s);
@@ -960,7 +1050,8 @@ template <class TW, bool ACC>
 hipError_t grad_products(const PieceBwdArgs& a, const PieceWs& w, const View& dv, const View& wk,
                          const View& hk, int64_t splits, hipStream_t s) {
   const EpiPiecePartial eh{w.split, a.h, a.v, w.count, 0, 0};
-  const EpiPieceWeight<TW, ACC> ew{static_cast<TW*>(a.grad_weight), a.h, w.count, w.scale, 0.f};
+  const EpiPieceWeight<TW, ACC> ew{static_cast<TW*>(a.grad_weight), a.h, w.count, w.named, w.scale,
+                                   0.f};
   const int64_t np = up(a.n, kTile);
   TimedLaunch t(s, K_PIECE_GRADS);
   return gemm::v2::launch_two<Wide>(
@@ -1051,7 +1142,17 @@ hipError_t piece_bwd_run(const PieceBwdArgs& a, hipStream_t s) {
   const PieceWs w = carve_bwd(a.workspace, a.n, a.h, a.v);
   const int64_t np = up(a.n, kTile), h64 = up(a.h, Wide::BK), v64 = up(a.v, 64);
   const bool rows = a.grad_rows != nullptr;
+  const bool want_weight = a.grad_weight && !(a.n == 0 && accumulate);
+  const bool wide = a.grad_weight_dtype == LCE_DTYPE_F32;
+  // what the labels' elements lack goes into the weight gradient too, but a bf16 one that is added
+  // to has no bits for it
+  const bool want_labels = want_weight && (wide || !accumulate);
   GatherArgs g{};
+  g.v = a.v;
+  if (want_labels) {
+    g.named = accumulate ? nullptr : w.named;
+    if (a.n <= kFewRows) embed_weighted_order(w.order, a.n, a.h, &g.stok, &g.spos);
+  }
   g.lse = a.lse;
   g.grad_rows = a.grad_rows;
   g.lse_c = w.lse_c;
@@ -1088,12 +1189,18 @@ hipError_t piece_bwd_run(const PieceBwdArgs& a, hipStream_t s) {
   View wk{weight, h64, 64, a.v, a.h};
   View hk{w.hc, h64, 64, np, a.h};
   const bool want_hidden = a.n > 0 && (last ? static_cast<void*>(a.grad_hidden) : a.hidden_acc);
-  const bool want_weight = a.grad_weight && !(a.n == 0 && accumulate);
-  const bool wide = a.grad_weight_dtype == LCE_DTYPE_F32;
   const int64_t splits = hidden_splits(a.n, a.h, a.v);
+  if (want_labels && a.n > 0) {
+    const EmbedBwdArgs e{w.hc, LCE_DTYPE_BF16, h64, w.ylab, a.n, a.h, a.v, -1, 1.f,
+                         accumulate ? EMBED_ACCUMULATE : 0, a.grad_weight, a.grad_weight_dtype,
+                         a.h, nullptr, w.order};
+    // overwritten, dW takes s with the product
+    PIECE_TRY(embed_weighted_run(e, w.left, accumulate ? w.scale : nullptr, g.stok != nullptr,
+                                 accumulate ? nullptr : w.named, s));
+  }
   const bool both = want_hidden && want_weight && splits > 1 && !few_tiles(a.v, a.h);
   const HiddenOut o{w.row, w.count, a.hidden_acc, last ? a.grad_hidden : nullptr, a.h,
-                    int(first), w.scale};
+                    int(first), w.scale, w.ylab, w.left, weight, h64};
   if (both) {
     if (wide)
       PIECE_TRY((accumulate ? grad_products<float, true>(a, w, dv, wk, hk, splits, s)

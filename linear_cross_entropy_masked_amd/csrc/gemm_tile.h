@@ -590,6 +590,19 @@ struct ColAux<E, std::void_t<decltype(E::kColAux)>> {
   using Col = typename E::Col;
 };
 
+// Epilogues that set kAccInit start the sums of some rows of the product from what memory holds:
+// init_load(m, n), of type Init, gives the 4 values from (m, n) as they are stored and init_value()
+// their fp32 values, for the rows with init_row(m). The loads run beside the first slice's, where
+// the same values read in the epilogue would be waited for in every batch of it.
+template <class E, class = void>
+struct AccInit {
+  static constexpr bool value = false;
+};
+template <class E>
+struct AccInit<E, std::void_t<decltype(E::kAccInit)>> {
+  static constexpr bool value = E::kAccInit;
+};
+
 // Tile coordinates (m-tile, n-tile, K split) of workgroup w; false for a workgroup with no
 // tile (the XCD-block mapping pads every XCD to the largest block).
 struct TileCoord {
@@ -688,6 +701,36 @@ __device__ __forceinline__ void run_tile(const View& A, const View& B, int64_t M
 #pragma unroll
   for (int s = 0; s < STAGES - 1; ++s)
     if (s < nk) issue();
+  if constexpr (AccInit<Epi>::value) {
+    bool from[TM];
+#pragma unroll
+    for (int i = 0; i < TM; ++i) {
+      const int64_t gm = m0 + wm * (C::BM / C::WM) + 16 * i + (lane & 15);
+      from[i] = gm < M && epi.init_row(gm);
+    }
+    typename Epi::Init x[TM][TN];
+#pragma unroll
+    for (int i = 0; i < TM; ++i) {
+#pragma unroll
+      for (int j = 0; j < TN; ++j) x[i][j] = typename Epi::Init{};
+      if (from[i]) {
+        const int64_t gm = m0 + wm * (C::BM / C::WM) + 16 * i + (lane & 15);
+#pragma unroll
+        for (int j = 0; j < TN; ++j) {
+          const int64_t gn = n0 + wn * (C::BN / C::WN) + 16 * j + 4 * (lane >> 4);
+          if (gn + 4 <= N) x[i][j] = epi.init_load(gm, gn);
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+      for (int j = 0; j < TN; ++j) {
+        // landed here, not at the first MFMA: a wait inside the main loop would be for its slices too
+        asm volatile("" : "+v"(x[i][j]));
+        acc[i][j] = Epi::init_value(x[i][j]);
+      }
+  }
   int rslot = 0;  // ring slot of slice kt
   for (int kt = 0; kt < nk; ++kt) {
     // slice kt has landed once at most the later slices' DMA is pending; then sync the
