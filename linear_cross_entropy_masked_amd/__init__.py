@@ -1014,7 +1014,7 @@ def _piece_rows(n, v, piece_size):
 
 def flce_pieces_bwd(hidden, weight, labels, lse, bias=None, *, piece_size: int | None = None,
                     ignore_index: int = -100, num_label_tokens: int | None = None,
-                    accumulate: bool = False, grad_output=None, grad_rows=None, grad_hidden=True,
+                    accumulate=False, grad_output=None, grad_rows=None, grad_hidden=True,
                     grad_weight=True, grad_bias=None):
     """Gradients of :func:`flce_pieces_fwd` from its lse. Each weight is taken ``piece_size``
     classes at a time (default: so that a piece's bf16 logit gradients stay within 512 MiB).
@@ -1022,8 +1022,8 @@ def flce_pieces_bwd(hidden, weight, labels, lse, bias=None, *, piece_size: int |
 
     ``grad_hidden`` / ``grad_weight`` / ``grad_bias``: True to allocate, False to skip, or what to
     write into; grad_weight (bf16, or fp32 where given so) and grad_bias are sequences where
-    weight is one, and are added to with ``accumulate``. grad_bias defaults to True when a bias
-    is given (None for the pieces without one). Returns (grad_hidden, grad_weight, grad_bias)."""
+    weight is one, and are added to with ``accumulate`` (True, or a sequence of one truth value per
+    weight). grad_bias defaults to True when a bias is given (None for the pieces without one). Returns (grad_hidden, grad_weight, grad_bias)."""
     import torch
     pieces, many = _as_pieces(weight, bias)
     _require(hidden, "hidden", torch.bfloat16, 2)
@@ -1037,10 +1037,15 @@ def flce_pieces_bwd(hidden, weight, labels, lse, bias=None, *, piece_size: int |
     if grad_bias is not False and bias is None:
         raise ValueError("grad_bias needs a bias")
     pieces = [_piece_weight(w, b, h, dev) for w, b in pieces]
+    adds = [bool(accumulate)] * len(pieces)
+    if isinstance(accumulate, (list, tuple)):
+        adds = [bool(a) for a in accumulate]
+        if len(adds) != len(pieces):
+            raise ValueError(f"{len(pieces)} weight pieces but {len(adds)} of accumulate")
 
     def outs(spec, name, dtype, width):
         if spec is True:
-            if accumulate:
+            if any(adds):
                 raise ValueError(f"accumulate=True needs an existing {name}")
             return [torch.empty((v, *width), dtype=dtype, device=dev) if width or b is not None
                     else None for _, b, v in pieces]
@@ -1061,28 +1066,28 @@ def flce_pieces_bwd(hidden, weight, labels, lse, bias=None, *, piece_size: int |
     elif gh is not None:
         _bwd_hidden(gh, n, h, dev)
     vocab = sum(v for _, _, v in pieces)
-    jobs = []  # (weight, bias, grad_weight, grad_bias, first class, classes)
+    jobs = []  # (weight, bias, grad_weight, grad_bias, first class, classes, whether added to)
     start = 0
-    for (w, b, v), gw, gb in zip(pieces, gws, gbs):
+    for (w, b, v), gw, gb, add in zip(pieces, gws, gbs, adds):
         _bwd_params(gw, gb, v, h, dev)
         step = _piece_rows(n, v, piece_size)
         if step >= v:
-            jobs.append((w, b, gw, gb, start, v))
+            jobs.append((w, b, gw, gb, start, v, add))
         else:
             for lo in range(0, v, step):
                 part = slice(lo, min(v, lo + step))
                 jobs.append((*(None if t is None else t[part] for t in (w, b, gw, gb)),
-                             start + lo, part.stop - lo))
+                             start + lo, part.stop - lo, add))
         start += v
     acc = None
     if gh is not None and len(jobs) > 1:
         acc = torch.empty((n, h), dtype=torch.float32, device=dev)
     ws = _workspace(max(flce_piece_bwd_workspace_size(n, h, j[5]) for j in jobs), dev)
     count = _count_arg(num_label_tokens)
-    for k, (w, b, gw, gb, at, v) in enumerate(jobs):
+    for k, (w, b, gw, gb, at, v, add) in enumerate(jobs):
         flags = ((FLCE_PIECE_FIRST if k == 0 else 0)
                  | (FLCE_PIECE_LAST if k == len(jobs) - 1 else 0)
-                 | (FLCE_PIECE_ACCUMULATE if accumulate else 0))
+                 | (FLCE_PIECE_ACCUMULATE if add else 0))
         _piece_bwd(hidden, w, b, labels, lse, n, h, v, at, vocab, ignore_index, count, flags,
                    grad_output, grad_rows, acc, gh, gw, gb, ws, dev)
     return gh, gws if many else gws[0], gbs if many else gbs[0]

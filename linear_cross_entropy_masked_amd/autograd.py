@@ -373,25 +373,25 @@ def _piece_grads(hidden, weights, biases, labels, lse, g, cfg, need_h, need_w, n
     ignore_index, count, per_row, piece_size, buffers = cfg
     if g.dtype != torch.float32:
         g = g.to(torch.float32)
+    if buffers is None:
+        buffers = [None] * len(weights)
+    into = [b is not None for b in buffers]  # a weight without a buffer gets its gradient as ever
     gws = [None] * len(weights)
     gbs = [None] * len(weights)
     for k, (w, need) in enumerate(zip(weights, need_w)):
         if need:
-            gws[k] = buffers[k] if buffers is not None else torch.empty_like(
+            gws[k] = buffers[k] if into[k] else torch.empty_like(
                 w, memory_format=torch.contiguous_format)
-    # accumulating covers the bias too: with buffers its gradient is added to zeros
-    make = torch.zeros_like if buffers is not None else torch.empty_like
     for k, (b, need) in enumerate(zip(biases, need_b)):
-        if need:
+        if need:  # accumulating covers the bias too: beside a buffer its gradient is added to zeros
+            make = torch.zeros_like if into[k] else torch.empty_like
             gbs[k] = make(b, memory_format=torch.contiguous_format)
     gh, _, _ = flce_pieces_bwd(
         hidden, weights, labels, lse, _any(biases), piece_size=piece_size,
-        ignore_index=ignore_index, num_label_tokens=count, accumulate=buffers is not None,
+        ignore_index=ignore_index, num_label_tokens=count, accumulate=into,
         grad_output=None if per_row else g, grad_rows=g.contiguous() if per_row else None,
         grad_hidden=bool(need_h), grad_weight=gws, grad_bias=_any(gbs) or False)
-    if buffers is not None:
-        gws = [None] * len(weights)
-    return gh, gws, gbs
+    return gh, [None if b else w for b, w in zip(into, gws)], gbs
 
 
 class _LinearCEPieces(torch.autograd.Function):
@@ -454,7 +454,8 @@ def linear_cross_entropy_pieces(hidden, weight, labels, bias=None, *, mask=None,
     reduction: "sum", "mean" or "none" (the per-row terms, 0 for rows without a label; minus a
     term is the log-probability of the row's label, with its gradient). Rows without a label take
     no part in any product. ``weight_grad_buffer`` (fp32 or bf16, a sequence where weight is one):
-    the gradients are added into it and ``weight.grad`` is left alone."""
+    the gradients are added into it and ``weight.grad`` is left alone; a weight whose entry in a
+    sequence is None gets its gradient in ``weight.grad``."""
     _check_reduction(reduction, num_label_tokens)
     weights, biases, buffers = _piece_inputs(weight, bias, weight_grad_buffer)
     h = hidden.shape[-1]

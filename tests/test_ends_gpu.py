@@ -349,3 +349,35 @@ def test_layer_norm_with_a_bias_alone(dev):
     gy, _, _ = lce.flce_pieces_bwd(y, w, lab, lse, num_label_tokens=1, grad_weight=False)
     exact = gy.double().sum(0)
     assert ((b.grad.double() - exact).abs() <= 401 * U * gy.double().abs().sum(0)).all()
+
+
+@pytest.mark.parametrize("which", [0, 1])
+@pytest.mark.parametrize("frozen", [False, True])
+def test_a_buffer_for_one_of_two_weights(dev, which, frozen):
+    """The weight with a buffer has its gradient added there, as with a buffer for both; the other
+    one gets its own in .grad, as without buffers (none where it is frozen)."""
+    n, h, sizes = 90, 64, [300, 77]
+    _, lab = batch(dev, n, sum(sizes))
+
+    def run(joined, buffers, freeze=False):
+        x = bf16(dev, n, h, seed=1).requires_grad_()
+        ws = [bf16(dev, v, h, seed=2 + k, std=0.3).requires_grad_(k == which or not freeze)
+              for k, v in enumerate(sizes)]
+        bs = [torch.zeros(v, device=dev, requires_grad=True) for v in sizes]
+        if joined:
+            loss = ag.norm_linear_cross_entropy(x, None, None, ws, lab, bs,
+                                                weight_grad_buffer=buffers)
+        else:
+            loss = ag.linear_cross_entropy_pieces(x, ws, lab, bs, weight_grad_buffer=buffers)
+        loss.backward()
+        return x.grad, [w.grad for w in ws], [b.grad for b in bs]
+    for joined in (False, True):
+        both = [torch.zeros(v, h, device=dev) for v in sizes]
+        run(joined, both)
+        gx, gws, gbs = run(joined, None)
+        one = [None, None]
+        one[which] = torch.zeros(sizes[which], h, device=dev)
+        gx2, gws2, gbs2 = run(joined, one, frozen)
+        assert gws2[which] is None and torch.equal(one[which], both[which])
+        assert gws2[1 - which] is None if frozen else torch.equal(gws2[1 - which], gws[1 - which])
+        assert torch.equal(gx2, gx) and all(torch.equal(a, b) for a, b in zip(gbs2, gbs))

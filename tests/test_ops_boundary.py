@@ -286,3 +286,26 @@ def test_workspace_of_the_largest_piece_serves_the_others(lib):
                         lce.flce_piece_bwd_workspace_size(n, h, v))
                 assert size[0] >= last[0] and size[1] >= last[1], (n, h, v)
                 last = size
+
+
+def test_weights_without_a_buffer_get_their_gradient(monkeypatch):
+    """None in a sequence of weight_grad_buffers: that weight's gradient is formed and returned
+    (None where it needs none); the others' are added into their buffers."""
+    from linear_cross_entropy_masked_amd import autograd as ag
+    seen = {}
+
+    def bwd(hidden, weights, labels, lse, bias, **kw):
+        seen.update(kw)
+        return "gh", None, None
+    monkeypatch.setattr(ag, "flce_pieces_bwd", bwd)
+    hid, lse = torch.zeros(3, 8, dtype=torch.bfloat16), torch.zeros(3)
+    ws = [torch.ones(5, 8, dtype=torch.bfloat16), torch.ones(4, 8, dtype=torch.bfloat16)]
+    buf = torch.full((4, 8), 2.0)
+    cfg = (-100, 1, False, None, [None, buf])
+    for need in (True, False):
+        gh, gws, gbs = ag._piece_grads(hid, ws, [None, None], None, lse, lse.sum(), cfg, True,
+                                       [need, True], [False, False])
+        assert seen["accumulate"] == [False, True] and seen["grad_weight"][1] is buf
+        assert gws[1] is None and gws[0] is seen["grad_weight"][0]
+        assert (gws[0] is not None) == need
+        assert not need or gws[0].dtype == torch.bfloat16 and gws[0].shape == (5, 8)
