@@ -299,7 +299,7 @@ int flce_piece_bwd(const uint16_t* hidden, const uint16_t* weight, const float* 
     return LCE_ERR_BAD_DTYPE;
   const bool first = flags & FLCE_PIECE_FIRST, last = flags & FLCE_PIECE_LAST;
   if (!weight || (n > 0 && (!hidden || !labels || !lse)) || (grad_bias && !bias) ||
-      (last && !first && grad_hidden && !hidden_acc))
+      (grad_hidden && !hidden_acc && !(first && last)))
     return LCE_ERR_NULL_ARG;
   const size_t need = piece_bwd_workspace_bytes(n, h, v);
   if (!workspace || workspace_bytes < need) return LCE_ERR_WORKSPACE;

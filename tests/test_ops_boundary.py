@@ -309,3 +309,15 @@ def test_weights_without_a_buffer_get_their_gradient(monkeypatch):
         assert gws[1] is None and gws[0] is seen["grad_weight"][0]
         assert (gws[0] is not None) == need
         assert not need or gws[0].dtype == torch.bfloat16 and gws[0].shape == (5, 8)
+
+
+def test_a_hidden_gradient_without_a_place_is_refused(lib):
+    """grad_hidden is written with the last piece: the pieces before need hidden_acc to carry it."""
+    call = caller(lib.flce_piece_bwd, dict(hid=A[0], w=A[1], b=A[2], lab=A[3], lse=A[4], n=4, h=16,
+                                           v=10, start=0, vocab=20, ign=-100, t=-1, flags=1,
+                                           gout=None, grows=None, acc=None, gh=A[6], gw=A[7], wd=0,
+                                           gb=A[8], ws=A[9], wsb=BIG, stream=None))
+    assert call() == NULL_ARG and call(flags=0) == NULL_ARG and call(flags=2) == NULL_ARG
+    if no_gpu():
+        assert call(acc=A[5]) in AT_DEVICE_CHECK and call(flags=3) in AT_DEVICE_CHECK
+        assert call(gh=None) in AT_DEVICE_CHECK
