@@ -353,11 +353,12 @@ int flce_piece_loss(const float* state, const int32_t* labels, int64_t n, int64_
  *                       to a bf16 grad_weight that is accumulated into;
  *                       c_i = g / T, or grad_rows[i] (fp32 [n], the upstream gradient of each
  *                       row's term; grad_output and num_label_tokens are then not used)
- *   hidden_acc   fp32 [n, h]: += d * weight (FLCE_PIECE_FIRST: =). Needed where grad_hidden is
- *                wanted from more than one piece, or partial sums are (no FLCE_PIECE_LAST)
+ *   hidden_acc   fp32 [n, h]: += d * weight (FLCE_PIECE_FIRST: =), 0 for rows without a label.
+ *                Needed where grad_hidden is wanted from more than one piece, or the sums
+ *                themselves are
  *   grad_hidden  bf16 [n, h], written with FLCE_PIECE_LAST: hidden_acc plus this piece, rounded
- *                once; 0 for rows without a label. Other pieces need hidden_acc with it. NULL
- *                with FLCE_PIECE_LAST: no hidden gradient of this piece is formed
+ *                once (hidden_acc is then left as it is); 0 for rows without a label. The other
+ *                pieces need hidden_acc with it. Without either no hidden gradient is formed
  *   grad_weight  [v, h] bf16 (LCE_DTYPE_BF16) or fp32 (LCE_DTYPE_F32), or NULL: dT * hidden
  *   grad_bias    fp32 [v] or NULL (needs bias): column sums of the fp32 d */
 int flce_piece_bwd(const uint16_t* hidden, const uint16_t* weight, const float* bias,

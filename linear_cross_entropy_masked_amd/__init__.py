@@ -931,7 +931,7 @@ def flce_piece_bwd(hidden, weight, labels, lse, bias=None, *, v_start: int, voca
                    grad_weight=None, grad_bias=None, workspace=None):
     """Gradients of one piece from the lse over the whole vocabulary, written into the tensors
     given (None: not computed): ``hidden_acc`` fp32 [n, h], carried from the first piece to the
-    last; ``grad_hidden`` bf16 [n, h], written with ``last``; ``grad_weight`` bf16 or fp32 and
+    last; ``grad_hidden`` bf16 [n, h], written with ``last`` from hidden_acc and that piece; ``grad_weight`` bf16 or fp32 and
     ``grad_bias`` fp32, of the piece's size. ``grad_rows`` fp32 [n]: the upstream gradient of
     each row's term, in place of grad_output / num_label_tokens."""
     import torch

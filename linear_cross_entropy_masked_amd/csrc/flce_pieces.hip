@@ -1159,8 +1159,9 @@ hipError_t piece_bwd_run(const PieceBwdArgs& a, hipStream_t s) {
   g.coef_c = rows ? w.coef_c : nullptr;
   g.row_scale = w.scale;
   g.scale = ScaleOut{rows ? nullptr : w.scale, a.num_label_tokens, a.grad_output};
-  g.zero_acc = first && !last ? a.hidden_acc : nullptr;
-  g.zero_grad = last ? a.grad_hidden : nullptr;
+  uint16_t* const grad_hidden = last ? a.grad_hidden : nullptr;
+  g.zero_acc = first && !grad_hidden ? a.hidden_acc : nullptr;
+  g.zero_grad = grad_hidden;
   if (rows) {
     TimedLaunch t(s, K_PIECE_GATHER);
     hipLaunchKernelGGL(row_scale_kernel, dim3(1), dim3(1024), 0, s, a.grad_rows, a.labels, a.n,
@@ -1188,7 +1189,7 @@ hipError_t piece_bwd_run(const PieceBwdArgs& a, hipStream_t s) {
   dv.ext = np * v64;
   View wk{weight, h64, 64, a.v, a.h};
   View hk{w.hc, h64, 64, np, a.h};
-  const bool want_hidden = a.n > 0 && (last ? static_cast<void*>(a.grad_hidden) : a.hidden_acc);
+  const bool want_hidden = a.n > 0 && (grad_hidden || a.hidden_acc);
   const int64_t splits = hidden_splits(a.n, a.h, a.v);
   if (want_labels && a.n > 0) {
     const EmbedBwdArgs e{w.hc, LCE_DTYPE_BF16, h64, w.ylab, a.n, a.h, a.v, -1, 1.f,
@@ -1199,7 +1200,7 @@ hipError_t piece_bwd_run(const PieceBwdArgs& a, hipStream_t s) {
                                  accumulate ? nullptr : w.named, s));
   }
   const bool both = want_hidden && want_weight && splits > 1 && !few_tiles(a.v, a.h);
-  const HiddenOut o{w.row, w.count, a.hidden_acc, last ? a.grad_hidden : nullptr, a.h,
+  const HiddenOut o{w.row, w.count, a.hidden_acc, grad_hidden, a.h,
                     int(first), w.scale, w.ylab, w.left, weight, h64};
   if (both) {
     if (wide)

@@ -187,3 +187,28 @@ def test_row_gradients_of_zero_and_of_infinity(dev):
         others = torch.arange(n, device=dev) != 5
         assert torch.equal(got[others], want[others])
         assert not got[5].isfinite().any()
+
+
+@pytest.mark.parametrize("n,h,v", [(70, 64, 600), (300, 1032, 4097)])
+def test_the_hidden_gradient_in_fp32(dev, n, h, v):
+    """Without grad_hidden, hidden_acc holds all pieces after the last, of several or of one."""
+    hid, w, b, lab = make(dev, n, h, v)
+    e = Sharp(hid, w, b, lab)
+    for parts in ([v], [v - 100, 100], [100, v - 200, 100]):
+        acc = torch.full((n, h), float("nan"), device=dev)
+        at = 0
+        for k, (ws, bs) in enumerate(zip(w.split(parts), b.split(parts))):
+            lce.flce_piece_bwd(hid, ws, lab, e.lse.float(), bs, v_start=at, vocab=v, first=k == 0,
+                               last=k == len(parts) - 1, hidden_acc=acc)
+            at += len(ws)
+        near(acc, e.gh, e.dgh + 4 * U * e.gh.abs(), "hidden_acc")
+        assert not acc[~e.keep].any()
+    # with grad_hidden the last piece goes there alone
+    acc, gh = torch.empty(n, h, device=dev), torch.empty(n, h, dtype=torch.bfloat16, device=dev)
+    lce.flce_piece_bwd(hid, w[:-100], lab, e.lse.float(), b[:-100], v_start=0, vocab=v, first=True,
+                       last=False, hidden_acc=acc, grad_hidden=gh)
+    before = acc.clone()
+    lce.flce_piece_bwd(hid, w[-100:], lab, e.lse.float(), b[-100:], v_start=v - 100, vocab=v,
+                       first=False, last=True, hidden_acc=acc, grad_hidden=gh)
+    assert torch.equal(acc, before)
+    near(gh, e.gh, e.dgh + 4 * U * e.gh.abs(), "grad_hidden")
