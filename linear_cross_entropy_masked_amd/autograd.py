@@ -448,7 +448,7 @@ def linear_cross_entropy_pieces(hidden, weight, labels, bias=None, *, mask=None,
     tensor or a sequence of them holding consecutive classes (a base vocabulary and tokens added
     to it), with fp32 biases likewise (any of them None) or None. The backward takes
     ``piece_size`` classes at a time (default: so that their bf16 logit gradients stay within
-    512 MiB) and leaves each weight's gradient in the weight's own type, without an fp32 [V, H]
+    512 MiB, but at least 4096, 8 KiB a row) and leaves each weight's gradient in the weight's own type, without an fp32 [V, H]
     accumulator.
 
     reduction: "sum", "mean" or "none" (the per-row terms, 0 for rows without a label; minus a

@@ -321,3 +321,12 @@ def test_a_hidden_gradient_without_a_place_is_refused(lib):
     if no_gpu():
         assert call(acc=A[5]) in AT_DEVICE_CHECK and call(flags=3) in AT_DEVICE_CHECK
         assert call(gh=None) in AT_DEVICE_CHECK
+
+
+def test_default_pieces_stay_within_the_budget():
+    """2 bytes a row (of whole tiles) and class, at least 4096 classes a piece."""
+    for n in (1, 256, 257, 5000, 8192, 20000, 50000, 54321, 65536, 65537, 1 << 20, 1 << 23):
+        up = -(-max(n, 1) // 256) * 256
+        for v in (1, 700, 4097, 32777, 128256, 262144, 1 << 22):
+            piece = lce._piece_rows(n, v, None)
+            assert piece % 256 == 0 and 2 * up * piece <= max(lce._PIECE_BYTES, 2 * up * 4096)
