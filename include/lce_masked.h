@@ -401,7 +401,8 @@ int embed_workspace_size(int64_t n, int64_t h, int64_t v, size_t* bytes);
  * not touched. Rows of grad without a token are not read.
  *   grad         dtype [n, ldg], first h columns
  *   grad_weight  grad_dtype [v, ldw], first h columns; grad_dtype is dtype or LCE_DTYPE_F32
- * h <= 2^20, n <= 2^28, v <= 2^27, v * h <= 2^36, n * (h + 512) < 2^40. */
+ * h <= 2^20, n <= 2^28, v <= 2^27, v * h <= 2^36 (2^36 - 2^30 with n == 0),
+ * n * (h + 512) < 2^40. */
 int embed_bwd(const void* grad, int dtype, int64_t ldg, const int32_t* tokens, int64_t n,
               int64_t h, int64_t v, int32_t ignore_index, float scale, uint32_t flags,
               void* grad_weight, int grad_dtype, int64_t ldw, int32_t* status_out,

@@ -36,11 +36,13 @@ int embed_check_shape(int64_t n, int64_t h, int64_t v) {
 bool lookup_fits(int64_t n, int64_t h, int64_t el) {
   return n * (h * el / 32 + 2) + 256 <= kThreadsMax;
 }
-// The gradient takes 8 threads a position to sort, 16 a table row to zero (one per 64 bytes where
-// there are no positions), and at most h + 512 per chunk of up to 512 positions to sum and join.
+// The gradient takes 8 threads a position to sort, 16 a table row to zero (where there are no
+// positions one per 64 bytes, of v * h / 16 + v / 4 at most), and at most h + 512 per chunk of up to
+// 512 positions to sum and join.
 int embed_bwd_check_shape(int64_t n, int64_t h, int64_t v) {
   if (embed_check_shape(n, h, v) != LCE_OK) return LCE_ERR_BAD_SHAPE;
   return n > (int64_t(1) << 28) || v > (int64_t(1) << 27) || v * h > (int64_t(1) << 36) ||
+                 (n == 0 && v * h > (int64_t(1) << 36) - (int64_t(1) << 30)) ||
                  n / 512 * (h + 512) > kThreadsMax / 2
              ? LCE_ERR_BAD_SHAPE
              : LCE_OK;

@@ -330,3 +330,17 @@ def test_default_pieces_stay_within_the_budget():
         for v in (1, 700, 4097, 32777, 128256, 262144, 1 << 22):
             piece = lce._piece_rows(n, v, None)
             assert piece % 256 == 0 and 2 * up * piece <= max(lce._PIECE_BYTES, 2 * up * 4096)
+
+
+def test_an_empty_batch_over_the_largest_table(lib):
+    """Without positions one launch zeroes the table, a thread per 64 bytes: 2^32 of them at 2^36
+    fp32 elements, one more than a launch holds."""
+    out = ctypes.c_size_t()
+    assert lib.embed_workspace_size(4, 1 << 20, 1 << 16, ctypes.byref(out)) == OK
+    assert lib.embed_workspace_size(0, 1 << 20, 1 << 16, ctypes.byref(out)) == BAD_SHAPE
+    call = caller(lib.embed_bwd, dict(g=None, dtype=2, ldg=1 << 20, tok=None, n=0, h=1 << 20,
+                                      v=1 << 16, ign=-100, scale=1.0, flags=0, gw=A[2], gdtype=2,
+                                      ldw=1 << 20, status=None, ws=1 << 45, wsb=BIG, stream=None))
+    assert call() == BAD_SHAPE
+    if no_gpu():
+        assert call(v=64000) in AT_DEVICE_CHECK
