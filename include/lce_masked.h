@@ -325,7 +325,11 @@ int flce_bwd(const uint16_t* hidden, const uint16_t* weight, const float* bias,
 
 int flce_piece_fwd_workspace_size(int64_t n, int64_t h, int64_t v, size_t* bytes);
 int flce_piece_loss_workspace_size(int64_t n, size_t* bytes);
-/* The bf16 [n, v] logit gradients of the piece are most of it. */
+/* The bf16 [n, v] logit gradients of the piece are most of it where v is well above h. Besides them
+ * the labelled rows of hidden (bf16 [n, h]), sums of 2 * h fp32 for each of up to 512 ranges of rows
+ * (one per 512 past 2^18), and fp32 partial sums of dH where it has few tiles. Where h is no multiple
+ * of 64 both this and the forward's hold a copy of the piece's weight too, in rows padded to one,
+ * made by every call: slices of a weight (or a multiple of 64) keep that small. */
 int flce_piece_bwd_workspace_size(int64_t n, int64_t h, int64_t v, size_t* bytes);
 
 /* Takes one piece into the state: fp32 [3, n] holding per row the largest logit so far, the sum

@@ -255,7 +255,7 @@ struct SegArgs {
   int tpr;           // lanes per chunk and column block (a power of two)
   const float* coef;       // COEF: row i counts coef[i] times
   const float* scale_dev;  // in place of scale (NULL: not)
-  int32_t* named;          // COEF: set to 1 for the tokens that have rows (NULL: not)
+  uint32_t* named;         // COEF: the bits of the tokens that have rows are set (NULL: not)
   __device__ __forceinline__ float factor() const { return scale_dev ? *scale_dev : scale; }
 };
 
@@ -350,7 +350,7 @@ __global__ void __launch_bounds__(kThreads) segment_sums_kernel(SegArgs a) {
   const float scale = a.factor();
   float acc[VE] = {};
   auto flush = [&](bool to_right) {
-    if (COEF && a.named && col == 0) a.named[cur] = 1;
+    if (COEF && a.named && col == 0) atomicOr(a.named + (cur >> 5), 1u << (cur & 31));
     if (from_left || to_right) {
       float* p = a.part + (chunk * 2 + (from_left ? 0 : 1)) * a.h + col;
 #pragma unroll
@@ -504,7 +504,7 @@ hipError_t run_segments(const SegArgs& a, hipStream_t s) {
 template <class T, class TW, bool COEF = false>
 hipError_t run_bwd(const EmbedBwdArgs& a, hipStream_t s, const float* coef = nullptr,
                    const float* scale_dev = nullptr, bool sorted = false,
-                   int32_t* named = nullptr) {
+                   uint32_t* named = nullptr) {
   constexpr int64_t kMost = COEF ? kWeightedChunks : kChunks;
   const bool acc = (a.flags & EMBED_ACCUMULATE) != 0, keep = acc || COEF;
   const EmbedWs ws = carve(a.workspace, a.n, a.h, kMost);
@@ -629,7 +629,7 @@ void embed_weighted_order(void* workspace, int64_t n, int64_t h, int32_t** token
 }
 
 hipError_t embed_weighted_run(const EmbedBwdArgs& a, const float* coef, const float* scale,
-                              bool sorted, int32_t* named, hipStream_t s) {
+                              bool sorted, uint32_t* named, hipStream_t s) {
   return a.grad_dtype == kF32 ? run_bwd<Bf16, float, true>(a, s, coef, scale, sorted, named)
                               : run_bwd<Bf16, Bf16, true>(a, s, coef, scale, sorted, named);
 }

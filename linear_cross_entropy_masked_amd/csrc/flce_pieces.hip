@@ -28,8 +28,10 @@
 // table's gradient (embed_kernels.hip; a bf16 dW that is added to has no bits for that). 1024 rows of
 // 768 and 32777 classes, label logits raised by 0 / 6 / 12: norm-wise error of dW in fp32 2.8e-5 /
 // 2.9e-5 / 3.1e-5, and 6.4e-5 / 1.1e-3 / 1.6e-3 without the remainder; of dW in bf16 1.47e-3 / 1.65e-3
-// / 1.66e-3, its own rounding, and 1.47e-3 / 1.99e-3 / 2.28e-3. It takes 28 of 387 us of the step of
-// 2048 x 768 x 32777 with half the rows labelled, 0.4 of 27.2 ms at 8192 x 4096 x 128256.
+// / 1.66e-3, its own rounding, and 1.47e-3 / 1.99e-3 / 2.28e-3. It takes 14 to 22 us a piece (the
+// order in the gather, two launches for the sums, the products' start), 20 of 376 us of the step of
+// 2048 x 768 x 32777 with half the rows labelled, 0.2 to 0.4 of 27 ms at 8192 x 4096 x 128256. Step
+// times that compare two forms below are without it on either side.
 //
 // With at most kScoreRows rows the forward is bound by reading W once, and score_kernel streams
 // it past the rows instead; up to kNarrowRows rows take tiles of half the height with three K
@@ -207,8 +209,8 @@ struct GatherArgs {
   int32_t* ylab;
   uint16_t* hc;            // [up(n, kTile)][h64]
   // backward only
-  int64_t v;
-  int32_t* named;          // zeroed here: v flags (NULL: not)
+  uint32_t* named;         // of so many words, cleared here (NULL: not)
+  int64_t words;
   int32_t *stok, *spos;    // gather_few_rows_kernel: the rows in the order of ylab (NULL: not)
   const float* lse;
   const float* grad_rows;
@@ -254,7 +256,8 @@ __device__ __forceinline__ void pad_row(const GatherArgs& a, int64_t m, int64_t 
 
 __device__ __forceinline__ void clear_named(const GatherArgs& a) {
   if (!a.named) return;
-  for (int64_t c = int64_t(blockIdx.x) * 256 + threadIdx.x; c < a.v; c += int64_t(gridDim.x) * 256)
+  for (int64_t c = int64_t(blockIdx.x) * 256 + threadIdx.x; c < a.words;
+       c += int64_t(gridDim.x) * 256)
     a.named[c] = 0;
 }
 
@@ -825,11 +828,15 @@ struct EpiPieceWeight {
   TW* dw;
   int64_t h;
   const int32_t* count;
-  const int32_t* named;
+  const uint32_t* named;  // a bit a class
   const float* scale;
   float s;
   using Init = std::conditional_t<sizeof(TW) == 4, f32x4_t, u32x2_t>;
-  __device__ __forceinline__ bool init_row(int64_t m) const { return named[m] != 0; }
+  __device__ __forceinline__ uint32_t init_rows(int64_t m) const {
+    // uniform, and read only in this launch: by the scalar unit, whose loads wait for no others
+    const auto* p = (const __attribute__((address_space(4))) uint32_t*)(named);
+    return p[m >> 5] >> (m & 31) & 0xffff;
+  }
   __device__ __forceinline__ Init init_load(int64_t m, int64_t n) const {
     return *reinterpret_cast<const Init*>(dw + m * h + n);
   }
@@ -908,7 +915,8 @@ int64_t hidden_splits(int64_t n, int64_t h, int64_t v) {
 }
 
 struct PieceWs {
-  int32_t *count, *cidx, *row, *ylab, *named;
+  int32_t *count, *cidx, *row, *ylab;
+  uint32_t* named;
   void* order;
   float *zy, *lse_c, *coef_c, *left, *scale, *colsum, *split;
   float2* part;
@@ -926,6 +934,9 @@ struct Carver {
     return p;
   }
 };
+
+// Words of a bit a class, for whole tiles.
+int64_t named_words(int64_t v) { return up(v, kTile) / 32; }
 
 PieceWs carve_fwd(void* base, int64_t n, int64_t h, int64_t v) {
   PieceWs w{};
@@ -967,7 +978,7 @@ PieceWs carve_bwd(void* base, int64_t n, int64_t h, int64_t v) {
   w.hc = c.take<uint16_t>(np * h64);
   if (h64 != h) w.wpad = c.take<uint16_t>(v * h64);
   w.d = c.take<uint16_t>(np * v64);
-  w.named = c.take<int32_t>(v);
+  w.named = c.take<uint32_t>(named_words(v));
   w.order = c.take<char>(int64_t(embed_weighted_workspace_bytes(n, h)));
   w.colsum = c.take<float>(np / Small::BM * v64);  // as in the forward: for any smaller piece too
   const int64_t splits = hidden_splits(n, h, v);
@@ -1148,7 +1159,7 @@ hipError_t piece_bwd_run(const PieceBwdArgs& a, hipStream_t s) {
   // to has no bits for it
   const bool want_labels = want_weight && (wide || !accumulate);
   GatherArgs g{};
-  g.v = a.v;
+  g.words = named_words(a.v);
   if (want_labels) {
     g.named = accumulate ? nullptr : w.named;
     if (a.n <= kFewRows) embed_weighted_order(w.order, a.n, a.h, &g.stok, &g.spos);

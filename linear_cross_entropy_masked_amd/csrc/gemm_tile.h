@@ -592,8 +592,9 @@ struct ColAux<E, std::void_t<decltype(E::kColAux)>> {
 
 // Epilogues that set kAccInit start the sums of some rows of the product from what memory holds:
 // init_load(m, n), of type Init, gives the 4 values from (m, n) as they are stored and init_value()
-// their fp32 values, for the rows with init_row(m). The loads run beside the first slice's, where
-// the same values read in the epilogue would be waited for in every batch of it.
+// their fp32 values, for the rows among m .. m + 15 (m a multiple of 16) whose bits init_rows(m)
+// has, the same in all lanes. The loads run beside the first slice's, where the same values read in
+// the epilogue would be waited for in every batch of it.
 template <class E, class = void>
 struct AccInit {
   static constexpr bool value = false;
@@ -688,6 +689,12 @@ __device__ __forceinline__ void run_tile(const View& A, const View& B, int64_t M
     }
   };
 
+  uint32_t from[TM];  // kAccInit: asked for ahead of the slices, which it would queue behind
+  if constexpr (AccInit<Epi>::value) {
+    const int64_t mw = m0 + int64_t(wv) / C::WN * (C::BM / C::WM);
+#pragma unroll
+    for (int i = 0; i < TM; ++i) from[i] = epi.init_rows(mw + 16 * i);
+  }
   int issued = 0;  // slices whose DMA has been issued (the same count in every wavefront)
   int wslot = 0;   // ring slot the next issue fills
   auto issue = [&]() {
@@ -702,34 +709,34 @@ __device__ __forceinline__ void run_tile(const View& A, const View& B, int64_t M
   for (int s = 0; s < STAGES - 1; ++s)
     if (s < nk) issue();
   if constexpr (AccInit<Epi>::value) {
-    bool from[TM];
+    uint32_t any = 0;
 #pragma unroll
-    for (int i = 0; i < TM; ++i) {
-      const int64_t gm = m0 + wm * (C::BM / C::WM) + 16 * i + (lane & 15);
-      from[i] = gm < M && epi.init_row(gm);
-    }
-    typename Epi::Init x[TM][TN];
+    for (int i = 0; i < TM; ++i) any |= from[i];
+    if (any) {
+      typename Epi::Init x[TM][TN];
 #pragma unroll
-    for (int i = 0; i < TM; ++i) {
+      for (int i = 0; i < TM; ++i) {
 #pragma unroll
-      for (int j = 0; j < TN; ++j) x[i][j] = typename Epi::Init{};
-      if (from[i]) {
-        const int64_t gm = m0 + wm * (C::BM / C::WM) + 16 * i + (lane & 15);
+        for (int j = 0; j < TN; ++j) x[i][j] = typename Epi::Init{};
+        if (from[i] >> (lane & 15) & 1) {
+          const int64_t gm = m0 + wm * (C::BM / C::WM) + 16 * i + (lane & 15);
 #pragma unroll
-        for (int j = 0; j < TN; ++j) {
-          const int64_t gn = n0 + wn * (C::BN / C::WN) + 16 * j + 4 * (lane >> 4);
-          if (gn + 4 <= N) x[i][j] = epi.init_load(gm, gn);
+          for (int j = 0; j < TN; ++j) {
+            const int64_t gn = n0 + wn * (C::BN / C::WN) + 16 * j + 4 * (lane >> 4);
+            if (gn + 4 <= N) x[i][j] = epi.init_load(gm, gn);
+          }
         }
       }
+#pragma unroll
+      for (int i = 0; i < TM; ++i)
+#pragma unroll
+        for (int j = 0; j < TN; ++j) {
+          // landed here, not at the first MFMA: a wait inside the main loop would be for its
+          // slices too
+          asm volatile("" : "+v"(x[i][j]));
+          acc[i][j] = Epi::init_value(x[i][j]);
+        }
     }
-#pragma unroll
-    for (int i = 0; i < TM; ++i)
-#pragma unroll
-      for (int j = 0; j < TN; ++j) {
-        // landed here, not at the first MFMA: a wait inside the main loop would be for its slices too
-        asm volatile("" : "+v"(x[i][j]));
-        acc[i][j] = Epi::init_value(x[i][j]);
-      }
   }
   int rslot = 0;  // ring slot of slice kt
   for (int kt = 0; kt < nk; ++kt) {

@@ -5,9 +5,10 @@
 //             dx = r · (u − mean(u) − x̂ · mean(u · x̂))            per row
 //             dw (=|+=) Σ_rows g · x̂,   db (=|+=) Σ_rows g
 //
-// Memory-bound: 2 · n · h elements move in the forward ([32768, 8192] bf16: 188 us, 5.7 TB/s; a
-// copy of 2 GiB reaches 4.9), 3 · n · h in the backward ([8192, 4096] bf16: 47 us, 4.2 TB/s,
-// what is left being the partial rows below and the start of each workgroup). A row lives in
+// Memory-bound: 2 · n · h elements move in the forward ([32768, 8192] bf16: 187 us in short runs, 5.8
+// TB/s, where a copy of 2 GiB reaches 4.9; in an unbroken run of forty the launches take 188 to 230),
+// 3 · n · h in the backward ([8192, 4096] bf16: 48 us, 4.2 TB/s, 44 of them in the rows' kernel; what
+// is left is the partial rows below and the start of each workgroup). A row lives in
 // the registers of WPR wavefronts (at most 32 elements a lane) from its one read to its one
 // write; the mean is known before the squares are summed, so the variance does not cancel. Rows
 // are dealt to a fixed grid, each lane loading the next row's vectors before the sums of this. In

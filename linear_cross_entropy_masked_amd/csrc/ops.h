@@ -42,13 +42,13 @@ size_t embed_workspace_bytes(int64_t n, int64_t h);
 hipError_t embed_bwd_run(const EmbedBwdArgs& a, hipStream_t s);
 // The same of bf16 rows, where row i counts coef[i] times and a sum, rounded to bf16 whatever the
 // table's type, *scale times (NULL: a.scale times). Rows of grad_weight that no position names are
-// left as they are; named[v] (NULL: not) becomes 1 for the others. `sorted`: the order is there
+// left as they are; bit v of named (NULL: not) is set for the others. `sorted`: the order is there
 // already, each position's token and row where embed_weighted_order() says, tokens that carry no row
 // being v.
 size_t embed_weighted_workspace_bytes(int64_t n, int64_t h);
 void embed_weighted_order(void* workspace, int64_t n, int64_t h, int32_t** tokens, int32_t** rows);
 hipError_t embed_weighted_run(const EmbedBwdArgs& a, const float* coef, const float* scale,
-                              bool sorted, int32_t* named, hipStream_t s);
+                              bool sorted, uint32_t* named, hipStream_t s);
 
 struct NormFwdArgs {
   const void* x;

@@ -212,3 +212,38 @@ def test_the_hidden_gradient_in_fp32(dev, n, h, v):
                        first=False, last=True, hidden_acc=acc, grad_hidden=gh)
     assert torch.equal(acc, before)
     near(gh, e.gh, e.dgh + 4 * U * e.gh.abs(), "grad_hidden")
+
+
+@pytest.mark.parametrize("n", [300, 9001])
+def test_replays_with_other_labels(dev, n):
+    """Fresh gradients in both types and row gradients, captured and replayed with other labels and
+    coefficients and eager work between: what one replay notes of its labels is gone in the next."""
+    h, v = 128, 700
+    hid, w, b, lab = make(dev, n, h, v)
+    g = torch.randn(n, device=dev)
+    lse = Sharp(hid, w, b, lab).lse.float()
+
+    def run():
+        gw = torch.empty(v, h, device=dev)
+        return (*lce.flce_pieces_bwd(hid, w, lab, lse, b),
+                *lce.flce_pieces_bwd(hid, w, lab, lse, b, grad_rows=g, grad_weight=gw))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        run()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = run()
+    for k in range(4):
+        lab.copy_(torch.randint(0, v if k % 2 else 40, (n,), device=dev, dtype=torch.int32))
+        lab[k::5] = IGN
+        g.copy_(torch.randn(n, device=dev))
+        lse.copy_(torch.logsumexp(hid.float() @ w.float().t() + b, 1))
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [o.clone() for o in out]
+        junk = torch.randn(1 << 20, device=dev).sum()
+        want = run()
+        torch.cuda.synchronize()
+        assert junk.isfinite() and all(torch.equal(x, y) for x, y in zip(got, want)), k
