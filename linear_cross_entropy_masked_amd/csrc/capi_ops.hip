@@ -37,8 +37,8 @@ bool lookup_fits(int64_t n, int64_t h, int64_t el) {
   return n * (h * el / 32 + 2) + 256 <= kThreadsMax;
 }
 // The gradient takes 8 threads a position to sort, 16 a table row to zero (where there are no
-// positions one per 64 bytes, of v * h / 16 + v / 4 at most), and at most h + 512 per chunk of up to
-// 512 positions to sum and join.
+// positions one per 64 bytes, at most v * h / 16 + v / 4), and at most h + 512 per chunk of up
+// to 512 positions to sum and join.
 int embed_bwd_check_shape(int64_t n, int64_t h, int64_t v) {
   if (embed_check_shape(n, h, v) != LCE_OK) return LCE_ERR_BAD_SHAPE;
   return n > (int64_t(1) << 28) || v > (int64_t(1) << 27) || v * h > (int64_t(1) << 36) ||

@@ -451,8 +451,8 @@ int pow2_at_least(int64_t x, int cap) {
 
 // Positions per chunk: about 1024 chunks, at least 8 positions (the rows one lane has in
 // flight) and at most 512 (so that the partial sums of one chunk border stay a small share of
-// the rows read).
-// Weighted rows take about 512: half the partial sums, which stand beside the logit gradients there.
+// the rows read). Weighted rows take about 512 chunks: half the partial sums, which stand beside the
+// logit gradients there.
 constexpr int64_t kChunks = 1024, kWeightedChunks = 512;
 int64_t chunk_len(int64_t n, int64_t most) {
   return pow2_at_least(std::max<int64_t>(8, (n + most - 1) / most), 512);

@@ -211,7 +211,7 @@ struct GatherArgs {
   // backward only
   uint32_t* named;         // of so many words, cleared here (NULL: not)
   int64_t words;
-  int32_t *stok, *spos;    // gather_few_rows_kernel: the rows in the order of ylab (NULL: not)
+  int32_t *stok, *spos;    // gather_few_rows_kernel<true>: the rows in the order of ylab
   const float* lse;
   const float* grad_rows;
   const float* row_scale;  // c_i = grad_rows[i] / *row_scale
@@ -279,12 +279,13 @@ __global__ void __launch_bounds__(256) gather_rows_kernel(GatherArgs a) {
 
 // Numbering and gathering in one launch, for batches short enough that every workgroup can count
 // the labelled rows before its own: `each` rows per workgroup (one for the shortest batches, where
-// a row's copy is all latency, else kFewEach; a divisor of kTile). Where the order of the labels is
-// asked for, each workgroup finds its rows' places on the way: the number of rows whose label in the
-// piece is smaller, or the same and earlier (labels outside it count as v, after all others).
+// a row's copy is all latency, else kFewEach; a divisor of kTile). ORDER: with the order of the
+// labels, for which each workgroup finds its rows' places on the way: the number of rows whose label
+// in the piece is smaller, or the same and earlier (labels outside it count as v, after all others).
 constexpr int64_t kFewRows = 8192;
 constexpr int kFewEach = 4;
 int few_each(int64_t n) { return n <= 1024 ? 1 : kFewEach; }
+template <bool ORDER>
 __global__ void __launch_bounds__(256) gather_few_rows_kernel(
     GatherArgs a, const int32_t* __restrict__ labels, int64_t v, int64_t v_start, int64_t vocab,
     int32_t ignore_index, int each, float* __restrict__ state) {
@@ -296,9 +297,10 @@ __global__ void __launch_bounds__(256) gather_few_rows_kernel(
     const int64_t d = int64_t(y) - v_start;
     return labelled(y, vocab, ignore_index) && d >= 0 && d < v ? int32_t(d) : int32_t(v);
   };
-  __shared__ int wave_sum[4][1 + kFewEach];
-  int sum[1 + kFewEach] = {};  // labelled rows before i0, places of the rows from there
-  if (a.stok && !padding) {
+  constexpr int kSums = ORDER ? 1 + kFewEach : 1;
+  __shared__ int wave_sum[4][kSums];
+  int sum[kSums] = {};  // labelled rows before i0, places of the rows from there
+  if constexpr (ORDER) {
     int32_t key[kFewEach];
 #pragma unroll
     for (int k = 0; k < kFewEach; ++k)
@@ -315,7 +317,7 @@ __global__ void __launch_bounds__(256) gather_few_rows_kernel(
       sum[0] += labelled(labels[j], vocab, ignore_index);
   }
 #pragma unroll
-  for (int k = 0; k <= kFewEach; ++k) {
+  for (int k = 0; k < kSums; ++k) {
 #pragma unroll
     for (int off = 32; off >= 1; off >>= 1) sum[k] += __shfl_xor(sum[k], off, 64);
     if ((threadIdx.x & 63) == 0) wave_sum[threadIdx.x >> 6][k] = sum[k];
@@ -339,10 +341,12 @@ __global__ void __launch_bounds__(256) gather_few_rows_kernel(
   }
   for (int64_t i = i0; i < i0 + each && i < a.n; ++i) {
     const int32_t y = labels[i];
-    if (a.stok && threadIdx.x == 0) {
-      const int place = total(1 + int(i - i0));
-      a.stok[place] = label_at(y);
-      a.spos[place] = int32_t(m);
+    if constexpr (ORDER) {
+      if (threadIdx.x == 0) {
+        const int place = total(1 + int(i - i0));
+        a.stok[place] = label_at(y);
+        a.spos[place] = int32_t(m);
+      }
     }
     if (labelled(y, vocab, ignore_index)) {
       gather_row(a, i, m);
@@ -1009,8 +1013,14 @@ hipError_t rows_and_gather(const uint16_t* hidden, const int32_t* labels, int64_
   if (n <= kFewRows) {
     const int each = few_each(n);
     const int64_t blocks = (n + each - 1) / each + kTile / each;
-    hipLaunchKernelGGL(gather_few_rows_kernel, dim3(unsigned(blocks)), dim3(256), 0, s, g, labels,
-                       v, v_start, vocab, ignore_index, each, state);
+    auto launch = [&](auto kernel) {
+      hipLaunchKernelGGL(kernel, dim3(unsigned(blocks)), dim3(256), 0, s, g, labels, v, v_start,
+                         vocab, ignore_index, each, state);
+    };
+    if (g.stok)
+      launch(gather_few_rows_kernel<true>);
+    else
+      launch(gather_few_rows_kernel<false>);
     return hipGetLastError();
   }
   hipLaunchKernelGGL(piece_rows_kernel, dim3(1), dim3(1024), 0, s, labels, n, v, v_start, vocab,
