@@ -85,7 +85,9 @@ extern "C" {
 #define LCE_STATUS_BAD_LABEL     1  /* some label was neither ignore_index nor in [0, V)          */
 #define LCE_STATUS_BAD_TOKEN     1  /* the same bit, for the tokens of embed_*                    */
 
-/* element types of the embedding, layer norm and vocabulary-piece calls */
+#define LCE_STATUS_BAD_LOGITS    1  /* the same bit, for beam_step: a NaN, or plus infinity       */
+
+/* element types of the embedding, norm, vocabulary-piece, 8-bit and beam search calls */
 #define LCE_DTYPE_BF16           0
 #define LCE_DTYPE_F16            1
 #define LCE_DTYPE_F32            2
@@ -451,6 +453,143 @@ int layernorm_bwd(const void* grad, int dtype, int64_t ldg, const void* x, int64
                   int64_t n, int64_t h, uint32_t flags, void* grad_x, int64_t lddx,
                   void* grad_weight, void* grad_bias, int grad_param_dtype, void* workspace,
                   size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------ root-mean-square norm */
+
+/* The norm behind a layer whose output is added to the residual stream:
+ *   s = x + residual, rounded to their type (s = x without a residual)
+ *   y = s * rstd * weight,  rstd = 1 / sqrt(mean(s^2) + eps) over the row's h elements of the
+ *   rounded s, in fp32, rounded once.
+ *   x, residual, y, residual_out  dtype, row strides ldx, ldr, ldy, ldro >= h, first h columns.
+ *                 residual and residual_out (where s goes) may be NULL. y, residual_out, x and
+ *                 residual may be the same rows (same pointer, same stride), except y and
+ *                 residual_out
+ *   weight        param_dtype [h] or NULL (1); param_dtype is dtype or LCE_DTYPE_F32
+ *   rstd_out      fp32 [n] or NULL, what the backward needs
+ * 1 <= h <= LAYERNORM_MAX_H, n < 2^31, any alignment of an element. n == 0 is valid. */
+int rmsnorm_fwd(const void* x, int dtype, int64_t n, int64_t h, int64_t ldx, const void* residual,
+                int64_t ldr, const void* weight, int param_dtype, float eps, void* y, int64_t ldy,
+                void* residual_out, int64_t ldro, float* rstd_out, void* stream);
+
+/* Types of the scales of 8-bit blocks: fp32, or a power of two held as its exponent byte e,
+ * 2^(e - 127) (255: NaN). */
+#define LCE_SCALE_F32            0
+#define LCE_SCALE_E8M0           1
+
+/* rmsnorm_fwd with y (before any rounding) in 8 bits (e4m3: 4 exponent bits, bias 7, 3 mantissa
+ * bits, largest 448, no infinities), one scale per row and block of 128 columns:
+ *   c = max(largest |y| of the block / 448, 2^-126), rounded up to a power of two for
+ *   LCE_SCALE_E8M0;  q = y / c, rounded to nearest even. A block that holds a NaN or an infinity
+ *   gets the scale NaN and NaN values.
+ *   q       [n, ldq], first h columns; shares no bytes with the other buffers
+ *   scales  [ceil(h / 128), lds], first n columns (block-major: scales of one block's rows lie
+ *           together), of scale_dtype, lds >= n */
+int rmsnorm_fp8_fwd(const void* x, int dtype, int64_t n, int64_t h, int64_t ldx,
+                    const void* residual, int64_t ldr, const void* weight, int param_dtype,
+                    float eps, uint8_t* q, int64_t ldq, void* scales, int scale_dtype,
+                    int64_t lds, void* residual_out, int64_t ldro, float* rstd_out, void* stream);
+
+/* flags of rmsnorm_bwd */
+#define RMSNORM_ACCUMULATE       1u /* add into grad_weight                                      */
+
+/* Workspace bytes of rmsnorm_bwd where grad_weight is asked for. Host-only. */
+int rmsnorm_workspace_size(int64_t n, int64_t h, size_t* bytes);
+
+/* Gradients of rmsnorm_fwd from x = the rounded sum s and rstd. With u = grad * weight and
+ * xhat = x * rstd:  grad_x = rstd * (u - xhat * mean(u * xhat)) + grad_residual, the gradient of
+ * both x and residual; grad_weight (=|+=) sum over rows of grad * xhat; fp32 sums in an order
+ * that depends on n and h alone, without atomics.
+ *   grad, x, grad_residual, grad_x  dtype, row strides >= h. grad_residual: the gradient of s
+ *                 where the model uses it further, or NULL. grad_x may be NULL, or the rows of
+ *                 grad or of grad_residual (same pointer, same stride)
+ *   grad_weight   grad_param_dtype [h] or NULL; param_dtype or LCE_DTYPE_F32. With n == 0 it is
+ *                 set to 0, or left as it is with RMSNORM_ACCUMULATE */
+int rmsnorm_bwd(const void* grad, int dtype, int64_t ldg, const void* x, int64_t ldx,
+                const float* rstd, const void* weight, int param_dtype, const void* grad_residual,
+                int64_t ldgr, int64_t n, int64_t h, uint32_t flags, void* grad_x, int64_t lddx,
+                void* grad_weight, int grad_param_dtype, void* workspace, size_t workspace_bytes,
+                void* stream);
+
+/* ------------------------------------------------------------------ 8-bit products */
+
+/* x in 8 bits, by the rules of rmsnorm_fp8_fwd. block_rows 1: one scale per row and block of 128
+ * columns, scales [ceil(h / 128), lds] block-major, lds >= n (an activation). block_rows 128: one
+ * scale per 128 x 128 block, scales [ceil(n / 128), lds] row-major, lds >= ceil(h / 128) (a
+ * weight). x dtype [n, ldx], q [n, ldq]; any strides >= h and any alignment of an element.
+ * n < 2^31, h <= 2^20, n * h <= 2^34. */
+int fp8_quantize(const void* x, int dtype, int64_t n, int64_t h, int64_t ldx, int64_t block_rows,
+                 uint8_t* q, int64_t ldq, void* scales, int scale_dtype, int64_t lds,
+                 void* stream);
+
+/* Workspace bytes of fp8_matmul: fp32 partial sums where few tiles make the product cut k, else
+ * 0. Host-only. */
+int fp8_matmul_workspace_size(int64_t m, int64_t n, int64_t k, size_t* bytes);
+
+/* out[m, n] = sum_b a_scales[b, m] * b_scales[n / 128, b] * (sum over the columns k of block b of
+ * a[m, k] * b[n, k]) + bias[n], the product of two matrices as fp8_quantize leaves them (a with
+ * block_rows 1, b with 128, both scale types alike). fp32 sums, rounded once to out_dtype. The
+ * logits of a head held in 8 bits; no gradients.
+ *   a  [m, lda], b [n, ldb]  e4m3, first k columns; 16-byte aligned, lda and ldb multiples of 16
+ *   a_scales  [ceil(k / 128), ldas]      b_scales  [ceil(n / 128), ldbs]
+ *   bias  fp32 [n] or NULL               out  out_dtype [m, ldo], first n columns
+ * k a multiple of 16; k <= 2^20, lda and ldb <= 2^22, m <= 2^23, n <= 2^28, fewer than 2^23 tiles
+ * of 256 x 256. With fp32 scales the product of a row's and a column's scale is formed in fp32.
+ * m == 0 is valid. */
+int fp8_matmul(const uint8_t* a, int64_t lda, const void* a_scales, int64_t ldas,
+               const uint8_t* b, int64_t ldb, const void* b_scales, int64_t ldbs, int scale_dtype,
+               const float* bias, int64_t m, int64_t n, int64_t k, void* out, int out_dtype,
+               int64_t ldo, void* workspace, size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------ beam search */
+
+#define BEAM_MAX_BEAMS           64
+#define BEAM_MAX_CANDIDATES      64
+
+/* Workspace bytes of beam_step: up to num candidates and two numbers per slice of a row of
+ * logits (2048 to 8192 of them). Host-only. */
+int beam_step_workspace_size(int64_t batch, int64_t beams, int64_t v, int64_t num, size_t* bytes);
+
+/* The best num continuations of each batch entry's beams. Candidate (j, t), token t after beam j,
+ * scores
+ *   scores[j] + (z[j, t] - lse_j),  lse_j = log sum_t exp(z[j, t]),
+ * compared in fp64 before it is rounded to fp32; equal ones come in the order of their beams,
+ * then (within a beam) of their logits, then of their tokens. A score of minus infinity (a class
+ * masked by a logit of minus infinity, a beam whose own score is that) is no candidate. A beam
+ * that is finished has one: token eos, its score unchanged, whatever its logits. A beam with a
+ * NaN or plus infinity among its logits or as its score has none and sets LCE_STATUS_BAD_LOGITS
+ * in *status_out.
+ *   logits     dtype, row batch * beams + beam at stride ldl, first v columns
+ *   scores     fp32 [batch, beams]            finished  0 or 1 [batch, beams], or NULL
+ *   eos        the token that finishes a beam, or negative for none (not with finished)
+ * Out, [batch, num], best first; where there are fewer candidates the score is minus infinity,
+ * the parent -1, the token ignore_index and finished 0:
+ *   scores_out fp32   parents_out int32, the beam   tokens_out int32
+ *   finished_out  or NULL: whether the parent is finished or the token is eos
+ * beams <= BEAM_MAX_BEAMS, num <= BEAM_MAX_CANDIDATES, v < 2^31, fewer than 2^23 slices. */
+int beam_step(const void* logits, int dtype, int64_t batch, int64_t beams, int64_t v, int64_t ldl,
+              const float* scores, const uint8_t* finished, int32_t eos, int64_t num,
+              int32_t ignore_index, float* scores_out, int32_t* parents_out, int32_t* tokens_out,
+              uint8_t* finished_out, int32_t* status_out, void* workspace, size_t workspace_bytes,
+              void* stream);
+
+/* One state of every beam: `segments` runs of segment_bytes bytes for each batch entry and beam
+ * (a cache [batch, beams, length, ...] is one run, [batch, beams, heads, length, dim] with room
+ * behind `length` one run per head). All strides in bytes. */
+typedef struct {
+  const void* in;
+  void* out;
+  int64_t in_entry, in_beam, in_segment;    /* strides of in: batch entry, beam, run           */
+  int64_t out_entry, out_beam, out_segment; /* the same of out                                 */
+  int64_t segments, segment_bytes;
+} lce_beam_state;
+
+/* States in the order of their beams: slot j of out is beam parents[b, j] of in, or zeros where
+ * parents[b, j] is outside 0 .. beams - 1. `states` is a host array; all of them share parents
+ * (int32 [batch, slots]). in == out with the same strides and slots == beams reorders in place
+ * (all states of a call or none); otherwise no out may share bytes with any in or other out.
+ * Runs of one state do not overlap. beams and slots <= BEAM_MAX_BEAMS. */
+int beam_reorder(const lce_beam_state* states, int64_t count, const int32_t* parents,
+                 int64_t batch, int64_t beams, int64_t slots, void* stream);
 
 /* ------------------------------------------------------------------ measurement aid */
 

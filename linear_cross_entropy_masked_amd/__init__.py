@@ -9,9 +9,11 @@ function whose library is missing raises.
 Entry points (same names as the C ABI):
     ce_chunked_fwd, ce_chunked_bwd, ce_chunked_bwd_inplace, flce_fwd_bwd, flce_fwd, flce_bwd,
     flce_piece_fwd, flce_piece_loss, flce_piece_bwd, embed_fwd, embed_bwd, layernorm_fwd,
-    layernorm_bwd,
+    layernorm_bwd, rmsnorm_fwd, rmsnorm_fp8_fwd, rmsnorm_bwd, fp8_quantize, fp8_matmul, beam_step,
+    beam_reorder,
     ce_chunked_workspace_size, flce_workspace_size, embed_workspace_size,
-    layernorm_workspace_size, flce_piece_{fwd,loss,bwd}_workspace_size, lce_status_str
+    layernorm_workspace_size, flce_piece_{fwd,loss,bwd}_workspace_size, rmsnorm_workspace_size,
+    fp8_matmul_workspace_size, beam_step_workspace_size, lce_status_str
 and over all pieces of a vocabulary: flce_pieces_fwd, flce_pieces_bwd
 """
 from __future__ import annotations
@@ -35,6 +37,11 @@ __all__ = [
     "embed_fwd", "embed_workspace_size", "embed_bwd", "EMBED_ACCUMULATE", "LCE_STATUS_BAD_TOKEN",
     "layernorm_fwd", "layernorm_workspace_size", "layernorm_bwd", "LAYERNORM_ACCUMULATE",
     "LAYERNORM_MAX_H",
+    "rmsnorm_fwd", "rmsnorm_fp8_fwd", "rmsnorm_workspace_size", "rmsnorm_bwd",
+    "RMSNORM_ACCUMULATE",
+    "fp8_quantize", "fp8_matmul_workspace_size", "fp8_matmul", "FP8_BLOCK",
+    "beam_step_workspace_size", "beam_step", "beam_reorder", "LCE_STATUS_BAD_LOGITS",
+    "BEAM_MAX_BEAMS", "BEAM_MAX_CANDIDATES",
     "lce_timing_enable", "lce_timing_read",
 ]
 
@@ -48,6 +55,11 @@ FLCE_PIECE_ACCUMULATE = 4
 EMBED_ACCUMULATE = 1
 LAYERNORM_ACCUMULATE = 1
 LAYERNORM_MAX_H = 32768
+RMSNORM_ACCUMULATE = 1
+LCE_STATUS_BAD_LOGITS = 1
+FP8_BLOCK = 128  # columns (and rows of a weight) that share a scale
+BEAM_MAX_BEAMS = 64
+BEAM_MAX_CANDIDATES = 64
 LCE_NOALLOC_MAX_ROWS = 1 << 20  # rows the allocation-free CE step's static scratch holds
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -116,6 +128,21 @@ def load_library() -> ctypes.CDLL:
         "layernorm_workspace_size": (ctypes.c_int, [i64, i64, psz]),
         "layernorm_bwd": (ctypes.c_int, [vp, dt, i64, vp, i64, vp, vp, vp, dt, i64, i64, u32, vp,
                                          i64, vp, vp, dt, vp, sz, vp]),
+        "rmsnorm_fwd": (ctypes.c_int, [vp, dt, i64, i64, i64, vp, i64, vp, dt, f32, vp, i64, vp, i64,
+                                       vp, vp]),
+        "rmsnorm_fp8_fwd": (ctypes.c_int, [vp, dt, i64, i64, i64, vp, i64, vp, dt, f32, vp, i64, vp,
+                                           dt, i64, vp, i64, vp, vp]),
+        "rmsnorm_workspace_size": (ctypes.c_int, [i64, i64, psz]),
+        "rmsnorm_bwd": (ctypes.c_int, [vp, dt, i64, vp, i64, vp, vp, dt, vp, i64, i64, i64, u32, vp,
+                                       i64, vp, dt, vp, sz, vp]),
+        "fp8_quantize": (ctypes.c_int, [vp, dt, i64, i64, i64, i64, vp, i64, vp, dt, i64, vp]),
+        "fp8_matmul_workspace_size": (ctypes.c_int, [i64, i64, i64, psz]),
+        "fp8_matmul": (ctypes.c_int, [vp, i64, vp, i64, vp, i64, vp, i64, dt, vp, i64, i64, i64, vp,
+                                      dt, i64, vp, sz, vp]),
+        "beam_step_workspace_size": (ctypes.c_int, [i64, i64, i64, i64, psz]),
+        "beam_step": (ctypes.c_int, [vp, dt, i64, i64, i64, i64, vp, vp, i32, i64, i32, vp, vp, vp,
+                                     vp, vp, vp, sz, vp]),
+        "beam_reorder": (ctypes.c_int, [vp, i64, vp, i64, i64, i64, vp]),
         "lce_timing_enable": (ctypes.c_int, [ctypes.c_int]),
         "lce_timing_read": (ctypes.c_int, [ctypes.c_int, ctypes.POINTER(ctypes.c_char_p),
                                            ctypes.POINTER(ctypes.c_double),
@@ -799,6 +826,353 @@ def layernorm_bwd(grad, x, mean, rstd, weight=None, *, grad_x=True, grad_weight=
           LAYERNORM_ACCUMULATE if accumulate else 0, _adr(grad_x), lddx, _adr(gw), _adr(gb),
           _dtype_code(gdtype, "grad_weight"), _adr(ws), 0 if ws is None else _bytes_of(ws))
     return grad_x, gw, gb
+
+
+def _rms_inputs(x, weight, residual, residual_out):
+    """(type code, device, n, h, ldx, ldr, weight, its type, residual_out, ldro)"""
+    code = _dtype_code(getattr(x, "dtype", None), "x")
+    ldx = _rows_2d(x, "x")
+    dev = x.device
+    n, h = x.shape
+    pdtype = x.dtype
+    if weight is not None:
+        weight = _norm_param(weight, "weight", h, dev)
+        pdtype = weight.dtype
+    ldr = ldro = h
+    if residual is not None:
+        ldr = _rows_2d(residual, "residual", x.dtype, (n, h), dev)
+        if residual_out is None:
+            residual_out = _empty_rows(x)
+        else:
+            ldro = _rows_2d(residual_out, "residual_out", x.dtype, (n, h), dev)
+    elif residual_out is not None:
+        raise ValueError("residual_out needs a residual")
+    return (code, dev, n, h, ldx, ldr, weight, _dtype_code(pdtype, "weight"), residual_out, ldro)
+
+
+def rmsnorm_fwd(x, weight=None, residual=None, *, eps: float = 1e-6, out=None, residual_out=None,
+                return_rstd: bool = True):
+    """Root-mean-square norm over the last dimension of s = x + residual [n, h] (bf16 / fp16 /
+    fp32; s is rounded to their type and that is what is normalised). weight: [h] of x's type or
+    float32, or None. ``residual_out``: where s goes, ``residual`` or x itself for in place; ``out``
+    may be x. Returns (y, s, rstd): s is x without a residual, rstd fp32 [n] or None."""
+    import torch
+    code, dev, n, h, ldx, ldr, weight, pcode, total, ldro = _rms_inputs(x, weight, residual,
+                                                                        residual_out)
+    if out is None:
+        out, ldy = _empty_rows(x), h
+    else:
+        ldy = _rows_2d(out, "out", x.dtype, (n, h), dev)
+    rstd = torch.empty(n, dtype=torch.float32, device=dev) if return_rstd else None
+    _call("rmsnorm_fwd", dev, x.data_ptr(), code, n, h, ldx, _adr(residual), ldr, _adr(weight),
+          pcode, eps, out.data_ptr(), ldy, _adr(total), ldro, _adr(rstd))
+    return out, (x if total is None else total), rstd
+
+
+_SCALE_CODES: dict = {}
+
+
+def _scale_code(dtype, name):
+    code = _SCALE_CODES.get(dtype)
+    if code is None:
+        import torch
+        _SCALE_CODES.update({torch.float32: 0, torch.float8_e8m0fnu: 1})
+        code = _SCALE_CODES.get(dtype)
+    if code is None:
+        raise TypeError(f"{name} must be float32 or float8_e8m0fnu, got {dtype}")
+    return code
+
+
+def _fp8_outputs(out, scales, scale_dtype, n, h, rows, cols, device):
+    """8-bit rows and the scales [rows, cols] beside them, allocated where not given."""
+    import torch
+    if scales is None:
+        if scale_dtype is None:
+            scale_dtype = torch.float8_e8m0fnu
+        code = _scale_code(scale_dtype, "scale_dtype")
+        scales, lds = torch.empty((rows, cols), dtype=scale_dtype, device=device), cols
+    else:
+        _require(scales, "scales", scale_dtype, 2, device)
+        code = _scale_code(scales.dtype, "scales")
+        lds = _rows_2d(scales, "scales", None, (rows, cols), device)
+    if out is None:
+        out, ldq = torch.empty((n, h), dtype=torch.float8_e4m3fn, device=device), h
+    else:
+        ldq = _rows_2d(out, "out", torch.float8_e4m3fn, (n, h), device)
+    return out, ldq, scales, code, lds
+
+
+def rmsnorm_fp8_fwd(x, weight=None, residual=None, *, eps: float = 1e-6, scale_dtype=None,
+                    out=None, scales=None, residual_out=None):
+    """:func:`rmsnorm_fwd` with its result in 8 bits (float8_e4m3fn) and a scale per row and block
+    of 128 columns: float8_e8m0fnu (the default, powers of two) or float32, [ceil(h / 128), n].
+    The left operand of :func:`fp8_matmul`. Returns (q, scales, s)."""
+    code, dev, n, h, ldx, ldr, weight, pcode, total, ldro = _rms_inputs(x, weight, residual,
+                                                                        residual_out)
+    out, ldq, scales, scode, lds = _fp8_outputs(out, scales, scale_dtype, n, h,
+                                                -(-h // FP8_BLOCK), n, dev)
+    _call("rmsnorm_fp8_fwd", dev, x.data_ptr(), code, n, h, ldx, _adr(residual), ldr,
+          _adr(weight), pcode, eps, out.data_ptr(), ldq, scales.data_ptr(), scode, lds,
+          _adr(total), ldro, None)
+    return out, scales, (x if total is None else total)
+
+
+def rmsnorm_workspace_size(n: int, h: int) -> int:
+    return _size("rmsnorm_workspace_size", n, h)
+
+
+def rmsnorm_bwd(grad, x, rstd, weight=None, *, grad_residual=None, grad_x=True, grad_weight=None,
+                accumulate: bool = False, workspace=None):
+    """Gradients of :func:`rmsnorm_fwd` from s (``x`` here) and rstd. ``grad_residual``: the
+    gradient of s where it is used further, added to grad_x, which is the gradient of both x and
+    residual. ``grad_x`` / ``grad_weight``: True to allocate (grad_weight in the weight's type),
+    False to skip, or a tensor to write into (grad_x may be ``grad`` or ``grad_residual`` itself;
+    grad_weight may be float32, and is added to with ``accumulate``). grad_weight defaults to
+    True when a weight is given. Returns (grad_x, grad_weight)."""
+    import torch
+    code = _dtype_code(getattr(x, "dtype", None), "x")
+    ldx = _rows_2d(x, "x")
+    dev = x.device
+    n, h = x.shape
+    ldg = _rows_2d(grad, "grad", x.dtype, (n, h), dev)
+    _require(rstd, "rstd", torch.float32, 1, dev)
+    if rstd.shape[0] != n or (n > 1 and rstd.stride(0) != 1):
+        raise ValueError(f"rstd must be a contiguous float32 [{n}] tensor")
+    pdtype = x.dtype
+    if weight is not None:
+        weight = _norm_param(weight, "weight", h, dev)
+        pdtype = weight.dtype
+    if grad_weight is None:
+        grad_weight = weight is not None
+    ldgr = lddx = h
+    if grad_residual is not None:
+        ldgr = _rows_2d(grad_residual, "grad_residual", x.dtype, (n, h), dev)
+    if grad_x is True:
+        grad_x = _empty_rows(x)
+    elif grad_x is False:
+        grad_x = None
+    elif grad_x is not None:
+        lddx = _rows_2d(grad_x, "grad_x", x.dtype, (n, h), dev)
+    if grad_weight is True:
+        if accumulate:
+            raise ValueError("accumulate=True needs an existing grad_weight tensor")
+        grad_weight = x.new_empty(h) if weight is None else torch.empty_like(weight)
+    elif grad_weight is False:
+        grad_weight = None
+    elif grad_weight is not None:
+        _require(grad_weight, "grad_weight", None, 1, dev)
+        if grad_weight.shape[0] != h or (h > 1 and grad_weight.stride(0) != 1):
+            raise ValueError(f"grad_weight must be a contiguous [{h}] tensor")
+    gdtype = pdtype if grad_weight is None else grad_weight.dtype
+    ws = None
+    if grad_weight is not None:
+        ws = _workspace(rmsnorm_workspace_size(n, h), dev, workspace)
+    _call("rmsnorm_bwd", dev, grad.data_ptr(), code, ldg, x.data_ptr(), ldx, rstd.data_ptr(),
+          _adr(weight), _dtype_code(pdtype, "weight"), _adr(grad_residual), ldgr, n, h,
+          RMSNORM_ACCUMULATE if accumulate else 0, _adr(grad_x), lddx, _adr(grad_weight),
+          _dtype_code(gdtype, "grad_weight"), _adr(ws), 0 if ws is None else _bytes_of(ws))
+    return grad_x, grad_weight
+
+
+def fp8_quantize(x, *, block_rows: int = 1, scale_dtype=None, out=None, scales=None):
+    """x [n, h] (bf16 / fp16 / fp32) in 8 bits (float8_e4m3fn) with a scale per block: of a row's
+    128 columns (``block_rows=1``, an activation: scales [ceil(h / 128), n]) or of 128 x 128
+    elements (``block_rows=128``, a weight: scales [ceil(n / 128), ceil(h / 128)]). Scales are
+    float8_e8m0fnu (the default, powers of two) or float32. Returns (q, scales)."""
+    code = _dtype_code(getattr(x, "dtype", None), "x")
+    ldx = _rows_2d(x, "x")
+    dev = x.device
+    n, h = x.shape
+    if block_rows not in (1, FP8_BLOCK):
+        raise ValueError(f"block_rows must be 1 or {FP8_BLOCK}, got {block_rows}")
+    across, down = -(-h // FP8_BLOCK), -(-n // FP8_BLOCK)
+    rows, cols = (across, n) if block_rows == 1 else (down, across)
+    out, ldq, scales, scode, lds = _fp8_outputs(out, scales, scale_dtype, n, h, rows, cols, dev)
+    _call("fp8_quantize", dev, x.data_ptr(), code, n, h, ldx, block_rows, out.data_ptr(), ldq,
+          scales.data_ptr(), scode, lds)
+    return out, scales
+
+
+def fp8_matmul_workspace_size(m: int, n: int, k: int) -> int:
+    return _size("fp8_matmul_workspace_size", m, n, k)
+
+
+def fp8_matmul(a, a_scales, b, b_scales, bias=None, *, out=None, dtype=None, workspace=None):
+    """a · bᵀ (+ bias) of 8-bit blocks as :func:`fp8_quantize` leaves them: a [m, k] with scales
+    [ceil(k / 128), m], b [n, k] with scales [ceil(n / 128), ceil(k / 128)], both scales of one
+    type; bias fp32 [n] or None. k is a multiple of 16, and rows start at multiples of 16 bytes.
+    Returns ``out`` [m, n], of ``dtype`` (default bfloat16; float16 or float32). No gradients."""
+    import torch
+    _require(a, "a", torch.float8_e4m3fn, 2)
+    dev = a.device
+    _require(b, "b", torch.float8_e4m3fn, 2, dev)
+    (m, k), (n, k2) = a.shape, b.shape
+    if k2 != k:
+        raise ValueError(f"a has {k} columns but b has {k2}")
+    lda, ldb = _rows_2d(a, "a"), _rows_2d(b, "b")
+    blocks = -(-k // FP8_BLOCK)
+    ldas = _rows_2d(a_scales, "a_scales", None, (blocks, m), dev)
+    ldbs = _rows_2d(b_scales, "b_scales", None, (-(-n // FP8_BLOCK), blocks), dev)
+    scode = _scale_code(a_scales.dtype, "a_scales")
+    if b_scales.dtype != a_scales.dtype:
+        raise TypeError(f"b_scales is {b_scales.dtype}, a_scales {a_scales.dtype}: they must be of "
+                        "one type")
+    if bias is not None:
+        _require(bias, "bias", torch.float32, 1, dev)
+        if bias.shape[0] != n:
+            raise ValueError("bias must have one entry per row of b")
+        bias = bias.contiguous()
+    if out is None:
+        out, ldo = torch.empty((m, n), dtype=dtype or torch.bfloat16, device=dev), n
+    else:
+        ldo = _rows_2d(out, "out", dtype, (m, n), dev)
+    ocode = _dtype_code(out.dtype, "out")
+    need = fp8_matmul_workspace_size(m, n, k)
+    ws = _workspace(need, dev, workspace) if need else None
+    _call("fp8_matmul", dev, a.data_ptr(), lda, a_scales.data_ptr(), ldas, b.data_ptr(), ldb,
+          b_scales.data_ptr(), ldbs, scode, _adr(bias), m, n, k, out.data_ptr(), ocode, ldo,
+          _adr(ws), 0 if ws is None else _bytes_of(ws))
+    return out
+
+
+def beam_step_workspace_size(batch: int, beams: int, v: int, num: int) -> int:
+    return _size("beam_step_workspace_size", batch, beams, v, num)
+
+
+def beam_step(logits, scores, *, num: int | None = None, finished=None, eos: int | None = None,
+              ignore_index: int = -100, status=None, workspace=None):
+    """The best ``num`` (default: as many as beams) continuations of each batch entry's beams.
+    logits [batch, beams, v] (bf16 / fp16 / fp32) of the beams' next tokens, scores fp32 [batch,
+    beams] their log-probabilities so far; a candidate scores scores + log_softmax(logits), in
+    64 bits until it is rounded. Equal scores: the lower beam, the larger logit, the lower token.
+
+    ``eos`` finishes a beam; ``finished`` (bool [batch, beams]): such a beam goes on as it is, with
+    eos as its token. Logits of minus infinity are no candidates; a beam with a NaN or plus infinity
+    has none and sets LCE_STATUS_BAD_LOGITS in ``status``.
+
+    Returns (scores fp32, parents int32, tokens int32, finished bool or None without eos), each
+    [batch, num], best first; places without a candidate hold minus infinity, -1, ``ignore_index``
+    (a zero row for :func:`embed_fwd`) and False."""
+    import torch
+    code = _dtype_code(getattr(logits, "dtype", None), "logits")
+    _require(logits, "logits", None, 3)
+    dev = logits.device
+    batch, beams, v = logits.shape
+    if v > 1 and logits.numel() and logits.stride(2) != 1:
+        raise ValueError("logits rows must be contiguous (stride(2) == 1)")
+    ld = logits.stride(1) if beams > 1 else logits.stride(0) if batch > 1 else v
+    if batch > 1 and beams > 1 and logits.stride(0) != beams * ld:
+        logits, ld = logits.contiguous(), v
+    if tuple(scores.shape) != (batch, beams):
+        raise ValueError(f"scores must have shape {(batch, beams)}, got {tuple(scores.shape)}")
+    _require(scores, "scores", torch.float32, 2, dev)
+    scores = scores.contiguous()
+    if eos is not None and not 0 <= eos < v:
+        raise ValueError(f"eos must be a token below {v}, got {eos}")
+    if finished is not None:
+        if eos is None:
+            raise ValueError("finished needs eos")
+        _require(finished, "finished", torch.bool, 2, dev)
+        if tuple(finished.shape) != (batch, beams):
+            raise ValueError(f"finished must have shape {(batch, beams)}, got "
+                             f"{tuple(finished.shape)}")
+        finished = finished.contiguous()
+    num = beams if num is None else int(num)
+    _ignore_arg(ignore_index)
+    ws = _workspace(beam_step_workspace_size(batch, beams, v, num), dev, workspace)
+    best = torch.empty((batch, num), dtype=torch.float32, device=dev)
+    parents = torch.empty((batch, num), dtype=torch.int32, device=dev)
+    tokens = torch.empty_like(parents)
+    done = None if eos is None else torch.empty((batch, num), dtype=torch.bool, device=dev)
+    _call("beam_step", dev, logits.data_ptr(), code, batch, beams, v, ld, scores.data_ptr(),
+          _adr(finished), -1 if eos is None else eos, num, ignore_index, best.data_ptr(),
+          parents.data_ptr(), tokens.data_ptr(), _adr(done), _status_ptr(status, dev),
+          ws.data_ptr(), _bytes_of(ws))
+    return best, parents, tokens, done
+
+
+def _runs(t, name):
+    """(segments, segment stride, segment bytes) of what a state holds per beam: dimensions 2 on,
+    as runs of contiguous elements at one stride."""
+    el = t.element_size()
+    run, seg, stride = 1, 1, 0
+    for size, step in zip(reversed(t.shape[2:]), reversed(t.stride()[2:])):
+        if size == 1:
+            continue
+        if seg == 1 and step == run:
+            run *= size
+        elif seg == 1:
+            seg, stride = size, step
+        elif step == seg * stride:
+            seg *= size
+        else:
+            raise ValueError(f"{name}: what a beam holds must be contiguous runs at one stride, got "
+                             f"shape {tuple(t.shape)} stride {tuple(t.stride())}")
+    if t.numel() == 0:
+        seg = run = 0
+    return seg, stride * el, run * el
+
+
+def beam_reorder(states, parents, *, out=None):
+    """Puts states [batch, beams, ...] of any type in the order of their beams: slot j of the
+    result is beam parents[b, j], zeros where that is outside the beams (parents int32 [batch,
+    slots], as :func:`beam_step` gives them). ``states`` is a sequence of tensors; ``out`` the
+    tensors [batch, slots, ...] to write (default: new ones), or ``states`` itself, which reorders
+    in place and moves only the beams that change. Returns the list of results."""
+    import torch
+    states = list(states)
+    _require(parents, "parents", torch.int32, 2)
+    dev = parents.device
+    batch, slots = parents.shape
+    parents = parents.contiguous()
+    if out is None:
+        out = [None] * len(states)
+    else:
+        out = list(out)
+        if len(out) != len(states):
+            raise ValueError(f"{len(states)} states but {len(out)} of out")
+    if not states:
+        return out
+    beams = None
+    rows = (_BeamState * len(states))()
+    for k, (x, y) in enumerate(zip(states, out)):
+        if not isinstance(x, torch.Tensor) or not x.is_cuda or x.device != dev or x.dim() < 2:
+            raise ValueError(f"states[{k}] must be a [batch, beams, ...] tensor on {dev}")
+        if x.shape[0] != batch or (beams is not None and x.shape[1] != beams):
+            raise ValueError(f"states[{k}] has shape {tuple(x.shape)}, expected "
+                             f"{(batch, beams or 'beams')} first")
+        beams = x.shape[1]
+        shape = (batch, slots, *x.shape[2:])
+        if y is None:
+            y = out[k] = torch.empty(shape, dtype=x.dtype, device=dev)
+        _require(y, f"out[{k}]", x.dtype, x.dim(), dev)
+        if tuple(y.shape) != shape:
+            raise ValueError(f"out[{k}] must have shape {shape}, got {tuple(y.shape)}")
+        (seg, sin, size), (seg_out, sout, size_out) = _runs(x, f"states[{k}]"), _runs(y, f"out[{k}]")
+        if size != size_out:  # runs of one may be several of the other
+            small = min(size, size_out)
+            if seg > 1 and size != small or seg_out > 1 and size_out != small or size % small \
+                    or size_out % small:
+                raise ValueError(f"out[{k}] must hold a beam in the runs that states[{k}] does")
+            if size != small:
+                seg, sin, size = size // small, small, small
+            else:
+                seg_out, sout, size_out = size_out // small, small, small
+        el = x.element_size()
+        r = rows[k]
+        r.src, r.dst, r.segments, r.segment_bytes = x.data_ptr(), y.data_ptr(), seg, size
+        r.in_entry, r.in_beam, r.in_segment = x.stride(0) * el, x.stride(1) * el, sin
+        r.out_entry, r.out_beam, r.out_segment = y.stride(0) * el, y.stride(1) * el, sout
+    _call("beam_reorder", dev, rows, len(states), parents.data_ptr(), batch, beams, slots)
+    return out
+
+
+class _BeamState(ctypes.Structure):
+    """lce_beam_state of the C ABI."""
+    _fields_ = [("src", ctypes.c_void_p), ("dst", ctypes.c_void_p)] + [
+        (name, ctypes.c_int64) for name in
+        ("in_entry", "in_beam", "in_segment", "out_entry", "out_beam", "out_segment", "segments",
+         "segment_bytes")]
 
 
 def flce_piece_fwd_workspace_size(n: int, h: int, v: int) -> int:

@@ -24,7 +24,8 @@ issue #533, feature pitch), and the upstream gradient stays on the device.
 
 ``linear_cross_entropy_pieces`` is the same loss over a weight in pieces of the vocabulary, with
 per-row terms as well. ``embedding`` and ``layer_norm`` are the model's other end of a tied table
-and the norm in front of the head; ``norm_linear_cross_entropy`` joins norm and loss without
+and the norm in front of the head (``rms_norm`` and ``add_rms_norm`` its root-mean-square form,
+with the residual's addition); ``norm_linear_cross_entropy`` joins norm and loss without
 keeping the normalised hidden states, and ``TiedHead`` holds one table for both ends.
 """
 from __future__ import annotations
@@ -34,7 +35,7 @@ from torch.autograd.function import once_differentiable
 
 from . import (ce_chunked_bwd, ce_chunked_bwd_inplace, ce_chunked_fwd, ce_rows_bwd, ce_rows_fwd,
                embed_bwd, embed_fwd, flce_bwd, flce_fwd, flce_pieces_bwd, flce_pieces_fwd,
-               layernorm_bwd, layernorm_fwd)
+               layernorm_bwd, layernorm_fwd, rmsnorm_bwd, rmsnorm_fwd)
 
 REDUCTIONS = ("sum", "mean", "none")
 
@@ -366,6 +367,80 @@ class LayerNorm(torch.nn.Module):
         return layer_norm(x, self.weight, self.bias, eps=self.eps)
 
 
+# ---------------------------------------------------------------- root-mean-square norm
+
+class _AddRMSNorm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, residual, weight, eps):
+        ctx.set_materialize_grads(False)
+        y, s, rstd = rmsnorm_fwd(_rows(x), weight, _rows(residual), eps=eps)
+        ctx.save_for_backward(s, weight, rstd)
+        return y, s
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, gy, gs):
+        s, weight, rstd = ctx.saved_tensors
+        need_x, need_r, need_w = ctx.needs_input_grad[:3]
+        if gy is None:
+            return gs if need_x else None, gs if need_r else None, None, None
+        g, gw = rmsnorm_bwd(_rows(gy), s, rstd, weight,
+                            grad_residual=None if gs is None else _rows(gs),
+                            grad_x=need_x or need_r, grad_weight=need_w)
+        return g if need_x else None, g if need_r else None, gw, None
+
+
+class _RMSNorm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, eps):
+        x = _rows(x)
+        y, _, rstd = rmsnorm_fwd(x, weight, eps=eps)
+        ctx.save_for_backward(x, weight, rstd)
+        return y
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, g):
+        x, weight, rstd = ctx.saved_tensors
+        gx, gw = rmsnorm_bwd(_rows(g), x, rstd, weight, grad_x=ctx.needs_input_grad[0],
+                             grad_weight=ctx.needs_input_grad[1])
+        return gx, gw, None
+
+
+def rms_norm(x, weight=None, *, eps: float = 1e-6):
+    """Root-mean-square norm over the last dimension of x [..., H] in bf16, fp16 or fp32; weight
+    [H] of x's type or fp32, or None."""
+    h = x.shape[-1]
+    return _RMSNorm.apply(x.reshape(-1, h), weight, float(eps)).view(x.shape)
+
+
+def add_rms_norm(x, residual, weight=None, *, eps: float = 1e-6):
+    """:func:`rms_norm` of s = x + residual, which a layer's output and the residual stream become
+    in one pass. Returns (the norm, s); s, rounded to their type, is what is normalised and what
+    the model carries on."""
+    if residual.shape != x.shape:
+        raise ValueError(f"residual has shape {tuple(residual.shape)}, x {tuple(x.shape)}")
+    h = x.shape[-1]
+    y, s = _AddRMSNorm.apply(x.reshape(-1, h), residual.reshape(-1, h), weight, float(eps))
+    return y.view(x.shape), s.view(x.shape)
+
+
+class RMSNorm(torch.nn.Module):
+    """Module form of :func:`rms_norm`, and of :func:`add_rms_norm` where a residual is given."""
+
+    bias = None
+
+    def __init__(self, hidden: int, eps: float = 1e-6, *, device=None, dtype=None):
+        super().__init__()
+        self.eps = eps
+        self.weight = torch.nn.Parameter(torch.ones(hidden, device=device, dtype=dtype))
+
+    def forward(self, x, residual=None):
+        if residual is None:
+            return rms_norm(x, self.weight, eps=self.eps)
+        return add_rms_norm(x, residual, self.weight, eps=self.eps)
+
+
 # ---------------------------------------------------------------- loss in pieces of the vocabulary
 
 def _piece_grads(hidden, weights, biases, labels, lse, g, cfg, need_h, need_w, need_b):
@@ -544,16 +619,20 @@ class TiedHead(torch.nn.Module):
     ``forward`` is the final norm and the loss against the same table (Liger-Kernel issue #941:
     lm_head.weight shared with embed_tokens). ``main_grad`` (fp32 [V, H], zeros, on request)
     collects both gradients of the table without a rounding between them, and ``weight.grad``
-    stays None; without it autograd adds the two in bf16."""
+    stays None; without it autograd adds the two in bf16. ``rms``: the final norm is a
+    root-mean-square one, and ``forward`` takes the residual stream that x is added to; such a head
+    is served in 8 bits by ``serving.Fp8Head.of(head)``."""
 
     def __init__(self, vocab: int, hidden: int, *, scale: float = 1.0, eps: float = 1e-5,
-                 ignore_index: int = -100, main_grad: bool = False, device=None):
+                 ignore_index: int = -100, main_grad: bool = False, rms: bool = False,
+                 device=None):
         super().__init__()
         self.scale, self.ignore_index = scale, ignore_index
         self.weight = torch.nn.Parameter(
             torch.empty(vocab, hidden, device=device, dtype=torch.bfloat16))
         torch.nn.init.normal_(self.weight, std=0.02)
-        self.norm = LayerNorm(hidden, eps, device=device, dtype=torch.bfloat16)
+        self.norm = (RMSNorm if rms else LayerNorm)(hidden, eps, device=device,
+                                                    dtype=torch.bfloat16)
         self.register_buffer(
             "main_grad", torch.zeros(vocab, hidden, device=device, dtype=torch.float32)
             if main_grad else None, persistent=False)
@@ -562,7 +641,16 @@ class TiedHead(torch.nn.Module):
         return embedding(tokens, self.weight, scale=self.scale, ignore_index=self.ignore_index,
                          weight_grad_buffer=self.main_grad)
 
-    def forward(self, x, labels, mask=None, num_label_tokens=None, reduction: str = "mean"):
+    def forward(self, x, labels, mask=None, num_label_tokens=None, reduction: str = "mean",
+                residual=None):
+        if isinstance(self.norm, RMSNorm):
+            y = self.norm(x) if residual is None else self.norm(x, residual)[0]
+            return linear_cross_entropy_pieces(
+                y, self.weight, labels, mask=mask, ignore_index=self.ignore_index,
+                num_label_tokens=num_label_tokens, reduction=reduction,
+                weight_grad_buffer=self.main_grad)
+        if residual is not None:
+            raise ValueError("residual needs a head with rms=True")
         return norm_linear_cross_entropy(
             x, self.norm.weight, self.norm.bias, self.weight, labels, eps=self.norm.eps,
             mask=mask, ignore_index=self.ignore_index, num_label_tokens=num_label_tokens,

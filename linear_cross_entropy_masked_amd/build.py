@@ -23,8 +23,9 @@ LIB_NAME = "liblce_masked.so"
 LIB_PATH = os.path.join(PKG, LIB_NAME)
 ARCH = "gfx950"
 
-SOURCES = ["capi.hip", "capi_ops.hip", "ce_kernels.hip", "embed_kernels.hip",
-           "flce_kernels.hip", "flce_pieces.hip", "norm_kernels.hip", "timing.hip"]
+SOURCES = ["beam_kernels.hip", "capi.hip", "capi_ops.hip", "capi_serve.hip", "ce_kernels.hip",
+           "embed_kernels.hip", "flce_kernels.hip", "flce_pieces.hip", "fp8_kernels.hip",
+           "norm_kernels.hip", "rms_kernels.hip", "timing.hip"]
 
 HIPCC_FLAGS = [
     f"--offload-arch={ARCH}",

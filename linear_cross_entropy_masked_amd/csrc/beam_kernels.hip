@@ -1,0 +1,537 @@
+// One step of a beam search for gfx950: the best continuations of each batch entry's beams, and
+// its states put in the order of their beams.
+//
+//   candidate (j, v): score_j + (z_jv − lse_j),  lse_j = log Σ_v exp(z_jv)
+//
+// taken best first, equal scores in the order (beam, logit, token). Two launches:
+//   rows  a workgroup holds a slice of one row of logits in registers, so that the row is read
+//         once for its maximum, its sum of exponentials and its best logits. The threads' own
+//         maxima give a threshold that at least `num` of them reach, which few logits do: those
+//         are put in LDS and ranked by counting. Where too many do (ties in plenty), the slice's
+//         best are taken one at a time.
+//   pick  a workgroup per batch entry: a wavefront merges a row's slices in the same way, then
+//         every candidate counts the better ones of each row by bisection.
+// Sums of exponentials are fp32 within a slice's threads, fp64 across slices, and scores are
+// compared in fp64. No atomics decide an order: the lists are filled by atomics and ranked by
+// keys that are all different.
+#include <algorithm>
+
+#include "common.h"
+#include "elem.h"
+#include "ops.h"
+
+namespace lce {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kList = 256;      // candidates of a slice that are ranked at once
+constexpr int kRowList = 440;   // the same of a row
+constexpr int kMost = BEAM_MAX_CANDIDATES;
+
+// Floats as integers of the same order; 0 is below all of them.
+__device__ __forceinline__ uint32_t ordered(float x) {
+  const uint32_t u = __float_as_uint(x);
+  return u & 0x80000000u ? ~u : u | 0x80000000u;
+}
+__device__ __forceinline__ float from_ordered(uint32_t u) {
+  return __uint_as_float(u & 0x80000000u ? u & 0x7fffffffu : ~u);
+}
+// A logit above minus infinity and its token as one key, better ones larger; 0: none.
+__device__ __forceinline__ uint64_t key_of(float z, uint32_t token) {
+  return uint64_t(ordered(z)) << 32 | uint32_t(~token);
+}
+
+// A threshold that at least `want` of the wavefront's PER · 64 values reach, and not many more
+// than that where the values differ; 0 where there are fewer. Bits are fixed from the top until
+// the number that reaches it is at most want + want / 4.
+template <int PER>
+__device__ __forceinline__ uint32_t threshold(const uint32_t (&x)[PER], int want) {
+  uint32_t t = 0;
+  for (int bit = 31; bit >= 0; --bit) {
+    const uint32_t c = t | 1u << bit;
+    int reach = 0;
+#pragma unroll
+    for (int k = 0; k < PER; ++k) reach += __popcll(__ballot(x[k] >= c));
+    if (reach >= want) {
+      t = c;
+      if (reach <= want + want / 4) break;
+    }
+  }
+  return t;
+}
+
+struct RowsK {
+  const void* logits;
+  int64_t v, ld;
+  int64_t splits;
+  int num;
+  uint64_t* keys;   // [rows, splits, num], best first, 0 where there are fewer
+  float2* sums;     // [rows, splits]: maximum, sum of exp(z − maximum)
+};
+
+template <class T, int EPT>
+__global__ void __launch_bounds__(kThreads) beam_rows_kernel(RowsK a) {
+  constexpr int NV = EPT / 8, kWaves = kThreads / 64;
+  __shared__ float top[kThreads];
+  __shared__ float wave_m[kWaves], wave_s[kWaves];
+  __shared__ uint32_t limit;
+  __shared__ int count;
+  __shared__ uint64_t list[kList];
+  __shared__ uint64_t best[kWaves];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int64_t row = blockIdx.x / a.splits, split = blockIdx.x % a.splits;
+  const int64_t at = split * (kThreads * EPT) + tid * 8;
+  const T* z = static_cast<const T*>(a.logits) + row * a.ld;
+  float x[NV][8];
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const int64_t c = at + int64_t(j) * kThreads * 8, cnt = a.v - c;
+    if (cnt >= 8) {
+      load_some<T, 8>(z + c, cnt, x[j]);
+    } else {
+#pragma unroll
+      for (int q = 0; q < 8; ++q) x[j][q] = q < cnt ? Elem<T>::to_f32(z[c + q]) : -INFINITY;
+    }
+  }
+  float m = -INFINITY;
+#pragma unroll
+  for (int j = 0; j < NV; ++j)
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      x[j][q] += 0.f;  // one zero: -0 becomes +0
+      m = fmaxf(m, x[j][q]);
+    }
+  top[tid] = m;
+  if (tid == 0) count = 0;
+  // the sum about the thread's own maximum (a finite number), then merged
+  float s = 0.f;
+  const float from = fmaxf(m, -3.4028234663852886e38f);
+#pragma unroll
+  for (int j = 0; j < NV; ++j)
+#pragma unroll
+    for (int q = 0; q < 8; ++q) s += fast_exp2((x[j][q] - from) * kLog2e);
+  const bool bad = __any(!(s >= 0.f));  // a NaN or +inf: the sum says so, whatever it meets
+  wave_lse_reduce(m, s);
+  if (lane == 0) {
+    wave_m[wave] = m;
+    wave_s[wave] = bad ? NAN : s;
+  }
+  __syncthreads();
+  if (wave == 0) {
+    uint32_t t[kWaves];
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) t[w] = ordered(top[64 * w + lane]);
+    const uint32_t lim = threshold<kWaves>(t, a.num);
+    if (lane == 0) limit = lim;
+  } else if (wave == 1 && lane == 0) {
+    float wm = wave_m[0], ws = wave_s[0];
+    bool nan = !(ws >= 0.f);
+#pragma unroll
+    for (int w = 1; w < kWaves; ++w) {
+      nan |= !(wave_s[w] >= 0.f);
+      lse_merge(wm, ws, wave_m[w], wave_s[w]);
+    }
+    a.sums[blockIdx.x] = float2{wm, nan ? NAN : ws};
+  }
+  __syncthreads();
+  const float lim = from_ordered(limit);
+  const bool all = limit <= ordered(-INFINITY);  // no threshold: every logit above -inf
+#pragma unroll
+  for (int j = 0; j < NV; ++j)
+#pragma unroll
+    for (int q = 0; q < 8; ++q)
+      if (x[j][q] > -INFINITY && (all || x[j][q] >= lim)) {
+        const int p = atomicAdd(&count, 1);
+        if (p < kList)
+          list[p] = key_of(x[j][q], uint32_t(at + int64_t(j) * kThreads * 8 + q));
+      }
+  __syncthreads();
+  uint64_t* out = a.keys + int64_t(blockIdx.x) * a.num;
+  const int c = count;
+  if (c <= kList) {
+    if (tid < c) {
+      const uint64_t k = list[tid];
+      int rank = 0;
+      for (int i = 0; i < c; ++i) rank += list[i] > k;
+      if (rank < a.num) out[rank] = k;
+    }
+    if (tid >= c && tid < a.num) out[tid] = 0;
+    return;
+  }
+  // one at a time: the best key below the last one taken
+  uint64_t last = ~uint64_t(0);
+  for (int r = 0; r < a.num; ++r) {
+    uint64_t k = 0;
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+      for (int q = 0; q < 8; ++q)
+        if (x[j][q] > -INFINITY) {
+          const uint64_t e = key_of(x[j][q], uint32_t(at + int64_t(j) * kThreads * 8 + q));
+          if (e < last && e > k) k = e;
+        }
+#pragma unroll
+    for (int off = 32; off >= 1; off >>= 1) {
+      const uint64_t o = __shfl_xor((unsigned long long)k, off, 64);
+      k = o > k ? o : k;
+    }
+    if (lane == 0) best[wave] = k;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) k = best[w] > k ? best[w] : k;
+    if (tid == 0) out[r] = k;
+    last = k;
+    __syncthreads();
+    // nothing is left: what follows is 0 too, since no key is below 0
+  }
+}
+
+struct PickK {
+  const float* scores;
+  const uint8_t* finished;
+  const uint64_t* keys;
+  const float2* sums;
+  int64_t splits;
+  int beams, num;
+  int32_t eos, ignore_index;
+  float* scores_out;
+  int32_t *parents_out, *tokens_out;
+  uint8_t* finished_out;
+  int32_t* status_out;
+};
+
+// What the wavefront's lanes wrote to LDS is there for all of them.
+__device__ __forceinline__ void wave_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+}
+
+// The best `num` keys of n at `in`, in order, into the wavefront's `out` (LDS); 0 behind the last.
+__device__ __forceinline__ void merge_row(const uint64_t* in, int64_t n, int num, uint64_t* list,
+                                          int* count, uint64_t* out) {
+  const int lane = threadIdx.x & 63;
+  uint32_t top[1] = {0};
+  for (int64_t i = lane; i < n; i += 64) {
+    const uint32_t v = uint32_t(in[i] >> 32);
+    top[0] = v > top[0] ? v : top[0];
+  }
+  const uint32_t lim = threshold<1>(top, num);
+  if (lane == 0) *count = 0;
+  wave_sync();
+  for (int64_t i = lane; i < n; i += 64) {
+    const uint64_t k = in[i];
+    if (k != 0 && uint32_t(k >> 32) >= lim) {
+      const int p = atomicAdd(count, 1);
+      if (p < kRowList) list[p] = k;
+    }
+  }
+  wave_sync();
+  const int c = *static_cast<volatile int*>(count);
+  for (int r = lane; r < num; r += 64)
+    if (r >= c) out[r] = 0;
+  if (c <= kRowList) {
+    for (int i = lane; i < c; i += 64) {
+      const uint64_t k = list[i];
+      int rank = 0;
+      for (int o = 0; o < c; ++o) rank += list[o] > k;
+      if (rank < num) out[rank] = k;
+    }
+  } else {
+    uint64_t last = ~uint64_t(0);
+    for (int r = 0; r < num; ++r) {
+      uint64_t k = 0;
+      for (int64_t i = lane; i < n; i += 64) {
+        const uint64_t e = in[i];
+        if (e < last && e > k) k = e;
+      }
+#pragma unroll
+      for (int off = 32; off >= 1; off >>= 1) {
+        const uint64_t o = __shfl_xor((unsigned long long)k, off, 64);
+        k = o > k ? o : k;
+      }
+      if (lane == 0) out[r] = k;
+      last = k;
+    }
+  }
+  wave_sync();
+}
+
+// Workgroup b: batch entry b. LDS: scores and tokens [beams, num], a list per wavefront.
+__global__ void __launch_bounds__(512) beam_pick_kernel(PickK a) {
+  extern __shared__ __attribute__((aligned(16))) char lds[];
+  const int waves = blockDim.x >> 6, wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  double* score = reinterpret_cast<double*>(lds);
+  uint64_t* lists = reinterpret_cast<uint64_t*>(score + a.beams * a.num);
+  uint64_t* sorted = lists + waves * kRowList;
+  int32_t* token = reinterpret_cast<int32_t*>(sorted + waves * kMost);
+  int* counts = token + a.beams * a.num;
+  const int64_t b = blockIdx.x;
+  for (int j = wave; j < a.beams; j += waves) {
+    const int64_t row = b * a.beams + j;
+    const float acc = a.scores[row];
+    const bool done = a.finished && a.finished[row];
+    double* sj = score + j * a.num;
+    int32_t* tj = token + j * a.num;
+    // the row's logsumexp, lanes in order of their distance
+    const float2* ms = a.sums + row * a.splits;
+    float m = -INFINITY;
+    bool nan = false;
+    for (int64_t i = lane; i < a.splits; i += 64) m = fmaxf(m, ms[i].x);
+#pragma unroll
+    for (int off = 32; off >= 1; off >>= 1) m = fmaxf(m, __shfl_xor(m, off, 64));
+    double s = 0.0;
+    for (int64_t i = lane; i < a.splits; i += 64) {
+      const float2 p = ms[i];
+      nan |= !(p.y >= 0.f) || p.x == INFINITY;
+      if (p.x > -INFINITY) s += double(p.y) * exp(double(p.x) - double(m));
+    }
+    s = wave_sum_f64(s);
+    const bool bad = __any(nan) || !(acc < INFINITY);  // a NaN or +inf among the logits or scores
+    if (bad && !done && a.status_out && lane == 0) atomicOr(a.status_out, LCE_STATUS_BAD_LOGITS);
+    if (done) {
+      for (int r = lane; r < a.num; r += 64) {
+        sj[r] = r == 0 && acc < INFINITY ? double(acc) : -INFINITY;
+        tj[r] = a.eos;
+      }
+      continue;
+    }
+    if (bad || !(m > -INFINITY) || !(acc > -INFINITY)) {
+      for (int r = lane; r < a.num; r += 64) sj[r] = -INFINITY;
+      continue;
+    }
+    uint64_t* out = sorted + wave * kMost;
+    merge_row(a.keys + row * a.splits * a.num, a.splits * a.num, a.num, lists + wave * kRowList,
+              counts + wave, out);
+    const double lse = double(m) + log(s);
+    for (int r = lane; r < a.num; r += 64) {
+      const uint64_t k = out[r];
+      sj[r] = k ? double(acc) + (double(from_ordered(uint32_t(k >> 32))) - lse) : -INFINITY;
+      tj[r] = int32_t(~uint32_t(k));
+    }
+  }
+  __syncthreads();
+  const int64_t to = b * a.num;
+  int found = 0;  // candidates there are, at most num of them counted
+  for (int j = 0; j < a.beams && found < a.num; ++j)
+    for (int r = 0; r < a.num && score[j * a.num + r] > -INFINITY; ++r) ++found;
+  for (int p = threadIdx.x; p < a.beams * a.num; p += blockDim.x) {
+    const int j = p / a.num, r = p % a.num;
+    const double s = score[p];
+    if (!(s > -INFINITY)) continue;
+    int rank = r;
+    for (int i = 0; i < a.beams && rank < a.num; ++i) {
+      if (i == j) continue;
+      // how many of row i come first: better ones, and equal ones of an earlier beam
+      int lo = 0, hi = a.num;
+      while (lo < hi) {
+        const int mid = (lo + hi) / 2;
+        const double o = score[i * a.num + mid];
+        if (o > s || (o == s && i < j))
+          lo = mid + 1;
+        else
+          hi = mid;
+      }
+      rank += lo;
+    }
+    if (rank >= a.num) continue;
+    const int32_t tok = token[p];
+    a.scores_out[to + rank] = float(s);
+    a.parents_out[to + rank] = j;
+    a.tokens_out[to + rank] = tok;
+    if (a.finished_out)
+      a.finished_out[to + rank] =
+          (a.finished && a.finished[b * a.beams + j]) || (a.eos >= 0 && tok == a.eos);
+  }
+  for (int r = threadIdx.x; r < a.num; r += blockDim.x) {
+    if (r < found) continue;
+    a.scores_out[to + r] = -INFINITY;
+    a.parents_out[to + r] = -1;
+    a.tokens_out[to + r] = a.ignore_index;
+    if (a.finished_out) a.finished_out[to + r] = 0;
+  }
+}
+
+// ------------------------------------------------------------------------------- states
+
+constexpr int kStates = 16;         // of a launch
+constexpr int kChunk = 16384;       // bytes of a segment that a workgroup copies
+constexpr int kTile = 32768;        // bytes of LDS where states are reordered in place
+
+struct StatesK {
+  lce_beam_state st[kStates];
+  int64_t first[kStates + 1];  // the first workgroup of each
+  int64_t chunks[kStates];     // of a segment
+  int count;
+  const int32_t* parents;
+  int64_t beams, slots;
+  int64_t chunk;
+};
+
+typedef uint32_t raw4_b1 __attribute__((ext_vector_type(4), aligned(1)));
+
+__device__ __forceinline__ void copy_bytes(char* to, const char* from, int64_t bytes) {
+  for (int64_t o = int64_t(threadIdx.x) * 16; o < bytes; o += kThreads * 16) {
+    if (o + 16 <= bytes) {
+      const raw4 v = from ? raw4(*reinterpret_cast<const raw4_b1*>(from + o)) : raw4{0, 0, 0, 0};
+      *reinterpret_cast<raw4_b1*>(to + o) = v;
+    } else {
+      for (int64_t i = o; i < bytes; ++i) to[i] = from ? from[i] : 0;
+    }
+  }
+}
+
+// Workgroup: a chunk of one segment of one slot, copied from its parent's.
+__global__ void __launch_bounds__(kThreads) beam_copy_kernel(StatesK a) {
+  int t = 0;
+  while (int64_t(blockIdx.x) >= a.first[t + 1]) ++t;
+  const lce_beam_state& st = a.st[t];
+  int64_t u = int64_t(blockIdx.x) - a.first[t];
+  const int64_t chunk = u % a.chunks[t];
+  u /= a.chunks[t];
+  const int64_t seg = u % st.segments;
+  u /= st.segments;
+  const int64_t slot = u % a.slots, b = u / a.slots;
+  const int32_t p = a.parents[b * a.slots + slot];
+  const int64_t at = chunk * a.chunk;
+  const int64_t left = st.segment_bytes - at, bytes = left < a.chunk ? left : a.chunk;
+  const char* from = nullptr;
+  if (p >= 0 && p < a.beams)
+    from = static_cast<const char*>(st.in) + b * st.in_entry + p * st.in_beam +
+           seg * st.in_segment + at;
+  copy_bytes(static_cast<char*>(st.out) + b * st.out_entry + slot * st.out_beam +
+                 seg * st.out_segment + at,
+             from, bytes);
+}
+
+// In place: a workgroup takes the same bytes of all of an entry's beams through LDS, reads those
+// that another slot wants and writes those that change.
+__global__ void __launch_bounds__(kThreads) beam_inplace_kernel(StatesK a) {
+  __shared__ __attribute__((aligned(16))) char tile[kTile];
+  int t = 0;
+  while (int64_t(blockIdx.x) >= a.first[t + 1]) ++t;
+  const lce_beam_state& st = a.st[t];
+  int64_t u = int64_t(blockIdx.x) - a.first[t];
+  const int64_t chunk = u % a.chunks[t];
+  u /= a.chunks[t];
+  const int64_t seg = u % st.segments, b = u / st.segments;
+  const int32_t* parents = a.parents + b * a.beams;
+  const int64_t at = chunk * a.chunk;
+  const int64_t left = st.segment_bytes - at, bytes = left < a.chunk ? left : a.chunk;
+  char* base = static_cast<char*>(st.out) + b * st.out_entry + seg * st.out_segment + at;
+  for (int j = 0; j < a.beams; ++j) {
+    bool wanted = false;
+    for (int i = 0; i < a.beams; ++i) wanted |= i != j && parents[i] == j;
+    if (wanted) copy_bytes(tile + j * a.chunk, base + j * st.out_beam, bytes);
+  }
+  __syncthreads();
+  for (int j = 0; j < a.beams; ++j) {
+    const int32_t p = parents[j];
+    if (p == j) continue;
+    copy_bytes(base + j * st.out_beam, p >= 0 && p < a.beams ? tile + p * a.chunk : nullptr, bytes);
+  }
+}
+
+int64_t slice_of(int64_t rows, int64_t v) {
+  if (rows * ((v + 8191) / 8192) >= 1024) return 8192;
+  if (rows * ((v + 4095) / 4096) >= 1024) return 4096;
+  return 2048;
+}
+
+size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
+
+template <class T>
+hipError_t run_rows(const RowsK& k, int64_t rows, int64_t slice, hipStream_t s) {
+  TimedLaunch t(s, K_BEAM_ROWS);
+  const dim3 grid(unsigned(rows * k.splits));
+  if (slice == 8192)
+    hipLaunchKernelGGL((beam_rows_kernel<T, 32>), grid, dim3(kThreads), 0, s, k);
+  else if (slice == 4096)
+    hipLaunchKernelGGL((beam_rows_kernel<T, 16>), grid, dim3(kThreads), 0, s, k);
+  else
+    hipLaunchKernelGGL((beam_rows_kernel<T, 8>), grid, dim3(kThreads), 0, s, k);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+int64_t beam_step_slices(int64_t rows, int64_t v) {
+  const int64_t slice = slice_of(rows, v);
+  return rows * ((v + slice - 1) / slice);
+}
+
+size_t beam_step_workspace_bytes(int64_t batch, int64_t beams, int64_t v, int64_t num) {
+  const size_t slices = size_t(beam_step_slices(batch * beams, v));
+  return align256(slices * size_t(num) * 8) + align256(slices * 8);
+}
+
+hipError_t beam_step_run(const BeamStepArgs& a, hipStream_t s) {
+  if (a.batch == 0) return hipSuccess;
+  const int64_t rows = a.batch * a.beams, slice = slice_of(rows, a.v);
+  const int64_t splits = (a.v + slice - 1) / slice;
+  uint64_t* keys = static_cast<uint64_t*>(a.workspace);
+  float2* sums = reinterpret_cast<float2*>(static_cast<char*>(a.workspace) +
+                                           align256(size_t(rows * splits * a.num) * 8));
+  const RowsK k{a.logits, a.v, a.ldl, splits, int(a.num), keys, sums};
+  hipError_t e;
+  switch (a.dtype) {
+    case kBF16: e = run_rows<Bf16>(k, rows, slice, s); break;
+    case kF16: e = run_rows<_Float16>(k, rows, slice, s); break;
+    default: e = run_rows<float>(k, rows, slice, s);
+  }
+  if (e != hipSuccess) return e;
+  const PickK p{a.scores,     a.finished,      keys,          sums,           splits,
+                int(a.beams), int(a.num),      a.eos,         a.ignore_index, a.scores_out,
+                a.parents_out, a.tokens_out,   a.finished_out, a.status_out};
+  // within 64 KiB of LDS: 65296 bytes at 64 beams and candidates
+  const int waves = int(std::min<int64_t>(a.beams, a.beams * a.num <= 2048 ? 8 : 4));
+  const size_t lds = size_t(a.beams * a.num) * 12 + size_t(waves) * (kRowList + kMost) * 8 +
+                     size_t(waves) * 4;
+  TimedLaunch t(s, K_BEAM_PICK);
+  hipLaunchKernelGGL(beam_pick_kernel, dim3(unsigned(a.batch)), dim3(64 * waves), lds, s, p);
+  return hipGetLastError();
+}
+
+int64_t beam_reorder_groups(const lce_beam_state& st, int64_t batch, int64_t beams, int64_t slots,
+                            bool inplace) {
+  const int64_t chunk = inplace ? kTile / beams / 16 * 16 : kChunk;
+  const int64_t chunks = (st.segment_bytes + chunk - 1) / chunk;
+  return batch * (inplace ? 1 : slots) * st.segments * chunks;
+}
+
+hipError_t beam_reorder_run(const lce_beam_state* states, int64_t count, const int32_t* parents,
+                            int64_t batch, int64_t beams, int64_t slots, bool inplace,
+                            hipStream_t s) {
+  for (int64_t at = 0; at < count;) {
+    StatesK k{};
+    k.parents = parents;
+    k.beams = beams;
+    k.slots = slots;
+    k.chunk = inplace ? kTile / beams / 16 * 16 : kChunk;
+    int64_t groups = 0;
+    while (at < count && k.count < kStates) {
+      const lce_beam_state& st = states[at];
+      const int64_t g = beam_reorder_groups(st, batch, beams, slots, inplace);
+      if (k.count > 0 && groups + g > (int64_t(1) << 23)) break;  // a launch's threads
+      ++at;
+      if (g == 0) continue;
+      k.st[k.count] = st;
+      k.first[k.count] = groups;
+      k.chunks[k.count] = (st.segment_bytes + k.chunk - 1) / k.chunk;
+      groups += g;
+      k.first[++k.count] = groups;
+    }
+    if (groups == 0) continue;
+    TimedLaunch t(s, K_BEAM_REORDER);
+    if (inplace)
+      hipLaunchKernelGGL(beam_inplace_kernel, dim3(unsigned(groups)), dim3(kThreads), 0, s, k);
+    else
+      hipLaunchKernelGGL(beam_copy_kernel, dim3(unsigned(groups)), dim3(kThreads), 0, s, k);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
+}  // namespace lce

@@ -126,6 +126,16 @@ enum KernelId {
   K_PIECE_GRAD_WEIGHT,
   K_PIECE_GRAD_FINISH,
   K_PIECE_GRADS,
+  K_RMS_FWD,
+  K_RMS_FP8_FWD,
+  K_RMS_BWD,
+  K_FP8_QUANTIZE,
+  K_FP8_MATMUL,
+  K_FP8_MATMUL_FEW,
+  K_FP8_JOIN,
+  K_BEAM_ROWS,
+  K_BEAM_PICK,
+  K_BEAM_REORDER,
   K_COUNT
 };
 

@@ -1,5 +1,6 @@
-// Internal interface of the embedding (embed_kernels.hip) and layer norm (norm_kernels.hip)
-// operators, between their C-ABI entry points and their launch code.
+// Internal interface of the embedding (embed_kernels.hip), norm (norm_kernels.hip, rms_kernels.hip),
+// 8-bit product (fp8_kernels.hip) and beam search (beam_kernels.hip) operators, between their
+// C-ABI entry points and their launch code.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -86,5 +87,108 @@ struct NormBwdArgs {
 };
 size_t layernorm_workspace_bytes(int64_t n, int64_t h);
 hipError_t layernorm_bwd_run(const NormBwdArgs& a, hipStream_t s);
+
+// Root-mean-square norm (rms_kernels.hip); scales: 8-bit outputs.
+struct RmsFwdArgs {
+  const void* x;
+  int dtype;
+  int64_t n, h, ldx;
+  const void* residual;
+  int64_t ldr;
+  const void* weight;
+  int param_dtype;
+  float eps;
+  void* y;
+  int64_t ldy;
+  void* residual_out;
+  int64_t ldro;
+  float* rstd_out;
+  void* scales;
+  int scale_dtype;
+  int64_t lds;
+};
+hipError_t rmsnorm_fwd_run(const RmsFwdArgs& a, hipStream_t s);
+
+struct RmsBwdArgs {
+  const void* grad;
+  int dtype;
+  int64_t ldg;
+  const void* x;
+  int64_t ldx;
+  const float* rstd;
+  const void* weight;
+  int param_dtype;
+  const void* grad_residual;
+  int64_t ldgr, n, h;
+  uint32_t flags;
+  void* grad_x;
+  int64_t lddx;
+  void* grad_weight;
+  int grad_param_dtype;
+  void* workspace;
+};
+size_t rmsnorm_workspace_bytes(int64_t n, int64_t h);
+hipError_t rmsnorm_bwd_run(const RmsBwdArgs& a, hipStream_t s);
+
+// 8-bit blocks and their product (fp8_kernels.hip).
+struct Fp8QuantizeArgs {
+  const void* x;
+  int dtype;
+  int64_t n, h, ldx, block_rows;
+  uint8_t* q;
+  int64_t ldq;
+  void* scales;
+  int scale_dtype;
+  int64_t lds;
+};
+hipError_t fp8_quantize_run(const Fp8QuantizeArgs& a, hipStream_t s);
+
+struct Fp8MatmulArgs {
+  const uint8_t* a;
+  int64_t lda;
+  const void* a_scales;
+  int64_t ldas;
+  const uint8_t* b;
+  int64_t ldb;
+  const void* b_scales;
+  int64_t ldbs;
+  int scale_dtype;
+  const float* bias;
+  int64_t m, n, k;
+  void* out;
+  int out_dtype;
+  int64_t ldo;
+  void* workspace;
+};
+size_t fp8_matmul_workspace_bytes(int64_t m, int64_t n, int64_t k);
+hipError_t fp8_matmul_run(const Fp8MatmulArgs& a, hipStream_t s);
+
+// A beam search's step (beam_kernels.hip).
+struct BeamStepArgs {
+  const void* logits;
+  int dtype;
+  int64_t batch, beams, v, ldl;
+  const float* scores;
+  const uint8_t* finished;
+  int32_t eos;
+  int64_t num;
+  int32_t ignore_index;
+  float* scores_out;
+  int32_t* parents_out;
+  int32_t* tokens_out;
+  uint8_t* finished_out;
+  int32_t* status_out;
+  void* workspace;
+};
+int64_t beam_step_slices(int64_t rows, int64_t v);  // workgroups over the logits
+size_t beam_step_workspace_bytes(int64_t batch, int64_t beams, int64_t v, int64_t num);
+hipError_t beam_step_run(const BeamStepArgs& a, hipStream_t s);
+
+// Workgroups of one state's reordering.
+int64_t beam_reorder_groups(const lce_beam_state& st, int64_t batch, int64_t beams, int64_t slots,
+                            bool inplace);
+hipError_t beam_reorder_run(const lce_beam_state* states, int64_t count, const int32_t* parents,
+                            int64_t batch, int64_t beams, int64_t slots, bool inplace,
+                            hipStream_t s);
 
 }  // namespace lce

@@ -1,0 +1,421 @@
+// Root-mean-square norm of a sum, forward (16- / 32-bit or 8-bit outputs) and backward for gfx950.
+//
+//   forward   s = x + residual, rounded to their type;  r = 1 / sqrt(mean(s²) + eps) per row
+//             y = s · r · w, or y in 8 bits with a scale for each block of 128 columns (fp8.h)
+//   backward  u = g · w,  ŝ = s · r
+//             ds = r · (u − ŝ · mean(u · ŝ)) + g_s          per row, g_s the gradient of s itself
+//             dw (=|+=) Σ_rows g · ŝ
+//
+// The norm is that of the rounded s: s is what the model carries on, and what the backward reads.
+// Memory-bound, as layer norm (norm_kernels.hip), and built like it: a row lives in the registers
+// of WPR wavefronts from its one read to its one write, the next row is loaded before the sums of
+// this, and dw goes through one partial row per workgroup, added in workgroup order. A block of 128
+// columns is 16 (fp32: 32) neighbouring lanes' vectors, so its largest element takes four or five
+// lane exchanges and no LDS.
+#include <algorithm>
+
+#include "common.h"
+#include "elem.h"
+#include "fp8.h"
+#include "norm_rows.h"
+#include "ops.h"
+
+namespace lce {
+
+namespace {
+
+constexpr int kFwdThreads = 512, kFwdElems = 32;
+constexpr int kBwdThreads = 256, kBwdElems = 16;
+constexpr int64_t kFwdGrid = 2048;
+constexpr int64_t kShortRow = 512, kPairRow = 256 * 24, kRegRow = 512 * 32;
+constexpr int64_t kColRows = 64;
+int64_t bwd_grid(int64_t h) { return h <= kShortRow ? 1024 : h <= kPairRow ? 512 : 256; }
+int64_t part_rows(int64_t n, int64_t h) {
+  return std::min(n, h > kRegRow ? kColRows : bwd_grid(h));
+}
+constexpr int64_t kStreamBytes = int64_t(512) << 20;
+
+// A weight of the rows' own type or of fp32, at a lane's columns.
+template <class T, class C, int VE>
+__device__ __forceinline__ void weight_at(const C& col, const void* w, bool wide, int j,
+                                          float (&x)[VE]) {
+  if (wide)
+    col.param(static_cast<const float*>(w), j, 1.f, x);
+  else
+    col.param(static_cast<const T*>(w), j, 1.f, x);
+}
+
+struct RmsFwd {
+  const void *x, *residual, *weight;
+  int64_t n, ldx, ldr;
+  int h;
+  bool wide;  // an fp32 weight
+  float eps;
+  void *y, *sum;  // y: rows of x's type, or 8-bit ones
+  int64_t ldy, ldsum;
+  float* rstd;
+  void* scales;  // 8-bit outputs
+  int64_t lds;
+  bool pow2;
+};
+
+template <bool POW2, class T, int VE, int NV, class C>
+__device__ __forceinline__ void store_row_fp8(const C& col, const RmsFwd& a, int64_t r, int lane,
+                                              int stride, const float (&y)[NV][VE]) {
+  constexpr int kLanes = kFp8Block / VE;  // of a block
+  uint8_t* q = static_cast<uint8_t*>(a.y) + r * a.ldy;
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    uint32_t top = 0;
+#pragma unroll
+    for (int e = 0; e < VE; ++e)
+      if (col.counts(j, e)) top = abs_bits(y[j][e]) > top ? abs_bits(y[j][e]) : top;
+    top = max_of_16<kLanes == 32>(top);
+    if (!col.live(j)) continue;
+    const BlockScale<POW2> s(top);
+    store_fp8<POW2, VE>(q + col.at[j], s, y[j], col.skip[j], a.h - col.at[j]);
+    if (lane % kLanes == 0) s.store(a.scales, int64_t((lane + j * stride) / kLanes) * a.lds + r);
+  }
+}
+
+template <class T, int WPR, int EPL, bool FULL, bool STREAM, bool FP8>
+__global__ void __launch_bounds__(norm_threads(WPR, kFwdThreads)) rmsnorm_fwd_kernel(RmsFwd a) {
+  // x, residual, sum and y may share rows: a row is in registers before any of it is written
+  constexpr int VE = Elem<T>::kVec, NV = EPL / VE, RG = norm_threads(WPR, kFwdThreads) / (64 * WPR);
+  __shared__ float red[2][norm_threads(WPR, kFwdThreads) / 64][1];
+  const int lane = threadIdx.x % (64 * WPR), group = threadIdx.x / (64 * WPR);
+  const float fh = float(a.h);
+  const T* x = static_cast<const T*>(a.x);
+  const T* add = static_cast<const T*>(a.residual);
+  const Columns<VE, NV, 64 * WPR, FULL> col(lane, a.h);
+  const int64_t step = int64_t(gridDim.x) * RG;
+  int64_t r = int64_t(blockIdx.x) * RG + group;
+  raw4 next[NV], nadd[NV];  // the row after the one being worked on
+  auto fetch = [&](int64_t row) {
+    row = row < a.n ? row : 0;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) next[j] = col.template load<STREAM>(x + row * a.ldx, j);
+    if (add) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j) nadd[j] = col.template load<STREAM>(add + row * a.ldr, j);
+    }
+  };
+  fetch(r);
+  int parity = 0;
+  for (int64_t base = int64_t(blockIdx.x) * RG; base < a.n; base += step, r += step) {
+    float v[NV][VE];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) Elem<T>::unpack(next[j], v[j]);
+    if (add) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        float b[VE];
+        Elem<T>::unpack(nadd[j], b);
+#pragma unroll
+        for (int q = 0; q < VE; ++q) v[j][q] += b[q];
+        Elem<T>::unpack(Elem<T>::pack(v[j]), v[j]);  // what is kept is what is normalised
+      }
+    }
+    if (base + step < a.n) fetch(r + step);
+    float s[1] = {0.f};
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+      for (int q = 0; q < VE; ++q) s[0] += col.counts(j, q) ? v[j][q] * v[j][q] : 0.f;
+    row_sums<WPR, 1>(s, red[parity]);
+    parity ^= 1;
+    const float rstd = 1.f / sqrtf(s[0] / fh + a.eps);
+    if (r >= a.n) continue;
+    if (a.sum) {
+      T* sr = static_cast<T*>(a.sum) + r * a.ldsum;
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+        if (col.live(j)) col.template store<STREAM>(sr, j, v[j]);
+    }
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      float w[VE];
+      weight_at<T>(col, a.weight, a.wide, j, w);
+#pragma unroll
+      for (int q = 0; q < VE; ++q) v[j][q] = v[j][q] * rstd * w[q];
+    }
+    if constexpr (FP8) {
+      if (a.pow2)
+        store_row_fp8<true, T>(col, a, r, lane, 64 * WPR, v);
+      else
+        store_row_fp8<false, T>(col, a, r, lane, 64 * WPR, v);
+    } else {
+      T* yr = static_cast<T*>(a.y) + r * a.ldy;
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+        if (col.live(j)) col.template store<STREAM>(yr, j, v[j]);
+    }
+    if (lane == 0 && a.rstd) a.rstd[r] = rstd;
+  }
+}
+
+struct RmsBwd {
+  const void *grad, *x, *weight, *grad_sum;
+  const float* rstd;
+  int64_t n, ldg, ldx, ldgs, lddx;
+  int h;
+  bool wide;
+  void* dx;
+  float* part;  // partial rows of dw, or NULL
+};
+
+// PARAMS: with the workgroup's partial row of dw, where a.part is given.
+template <class T, int WPR, int EPL, bool FULL, bool PARAMS>
+__global__ void __launch_bounds__(norm_threads(WPR, kBwdThreads)) rmsnorm_bwd_kernel(RmsBwd a) {
+  // grad, grad_sum and dx may be the same rows
+  constexpr int VE = Elem<T>::kVec, NV = EPL / VE, RG = norm_threads(WPR, kBwdThreads) / (64 * WPR);
+  __shared__ float red[2][norm_threads(WPR, kBwdThreads) / 64][1];
+  const int lane = threadIdx.x % (64 * WPR), group = threadIdx.x / (64 * WPR);
+  const float inv_h = 1.f / float(a.h);
+  const T* g = static_cast<const T*>(a.grad);
+  const T* x = static_cast<const T*>(a.x);
+  const T* gs = static_cast<const T*>(a.grad_sum);
+  T* dx = static_cast<T*>(a.dx);
+  const Columns<VE, NV, 64 * WPR, FULL> col(lane, a.h);
+  float dw[NV][VE] = {};
+  const int64_t step = int64_t(gridDim.x) * RG;
+  int64_t r = int64_t(blockIdx.x) * RG + group;
+  raw4 nx[NV], ng[NV], ns[NV];  // the row after the one being worked on
+  float nrs;
+  auto fetch = [&](int64_t row) {
+    row = row < a.n ? row : 0;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) nx[j] = col.load(x + row * a.ldx, j);
+#pragma unroll
+    for (int j = 0; j < NV; ++j) ng[j] = col.load(g + row * a.ldg, j);
+    if (gs) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j) ns[j] = col.load(gs + row * a.ldgs, j);
+    }
+    nrs = a.rstd[row];
+  };
+  fetch(r);
+  int parity = 0;
+  for (int64_t base = int64_t(blockIdx.x) * RG; base < a.n; base += step, r += step) {
+    const bool live = r < a.n;
+    const float rs = nrs;
+    float xh[NV][VE], u[NV][VE];
+    raw4 keep[NV];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      Elem<T>::unpack(nx[j], xh[j]);
+      Elem<T>::unpack(ng[j], u[j]);
+      keep[j] = ns[j];
+    }
+    if (base + step < a.n) fetch(r + step);
+    float s[1] = {0.f};
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      float w[VE];
+      weight_at<T>(col, a.weight, a.wide, j, w);
+#pragma unroll
+      for (int q = 0; q < VE; ++q) {
+        xh[j][q] *= rs;
+        if (PARAMS && live) dw[j][q] += u[j][q] * xh[j][q];
+        u[j][q] *= w[q];
+        s[0] += col.counts(j, q) ? u[j][q] * xh[j][q] : 0.f;
+      }
+    }
+    row_sums<WPR, 1>(s, red[parity]);
+    parity ^= 1;
+    if (!live || !dx) continue;
+    const float b = s[0] * inv_h;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      if (!col.live(j)) continue;
+#pragma unroll
+      for (int q = 0; q < VE; ++q) u[j][q] = rs * (u[j][q] - xh[j][q] * b);
+      if (gs) {
+        float k[VE];
+        Elem<T>::unpack(keep[j], k);
+#pragma unroll
+        for (int q = 0; q < VE; ++q) u[j][q] += k[q];
+      }
+      col.store(dx + r * a.lddx, j, u[j]);
+    }
+  }
+  if (!PARAMS || !a.part) return;
+  // this workgroup's partial row: its row groups added through LDS, in group order
+  if constexpr (RG > 1) {
+    constexpr int LANES = 64 * WPR;
+    __shared__ float sums[RG - 1][EPL][LANES];
+    if (group > 0) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int q = 0; q < VE; ++q) sums[group - 1][j * VE + q][lane] = dw[j][q];
+    }
+    __syncthreads();
+    if (group > 0) return;
+#pragma unroll
+    for (int k = 0; k < RG - 1; ++k)
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int q = 0; q < VE; ++q) dw[j][q] += sums[k][j * VE + q][lane];
+  }
+  float* pw = a.part + int64_t(blockIdx.x) * a.h;
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    if (col.skip[j] == 0 && (FULL || a.h >= VE)) {
+      store_some<float, VE>(pw + col.at[j], VE, dw[j]);
+    } else if (!FULL && col.live(j)) {  // the row's last vector, or a row shorter than one
+#pragma unroll
+      for (int q = 0; q < VE; ++q)
+        if (col.counts(j, q)) pw[col.at[j] + q] = dw[j][q];
+    }
+  }
+}
+
+// dw of long rows: a workgroup adds the rows blockIdx.y, blockIdx.y + gridDim.y, ... of its 256
+// vectors of columns into partial row blockIdx.y.
+constexpr int kColBatch = 4;  // rows in flight per lane
+template <class T>
+__global__ void __launch_bounds__(256) rms_columns_kernel(const T* __restrict__ g, int64_t ldg,
+                                                          const T* __restrict__ x, int64_t ldx,
+                                                          const float* __restrict__ rstd,
+                                                          int64_t n, int64_t h,
+                                                          float* __restrict__ part) {
+  constexpr int VE = Elem<T>::kVec;
+  const int64_t col = (int64_t(blockIdx.x) * 256 + threadIdx.x) * VE;
+  if (col >= h) return;
+  const int64_t cnt = h - col;
+  float dw[VE] = {};
+  for (int64_t r0 = blockIdx.y; r0 < n; r0 += int64_t(kColBatch) * gridDim.y) {
+    float xs[kColBatch][VE], gr[kColBatch][VE], rs[kColBatch];
+#pragma unroll
+    for (int k = 0; k < kColBatch; ++k) {
+      const int64_t r = r0 + int64_t(k) * gridDim.y;
+      if (r >= n) continue;
+      load_some<T, VE>(x + r * ldx + col, cnt, xs[k]);
+      load_some<T, VE>(g + r * ldg + col, cnt, gr[k]);
+      rs[k] = rstd[r];
+    }
+#pragma unroll
+    for (int k = 0; k < kColBatch; ++k) {
+      if (r0 + int64_t(k) * gridDim.y >= n) break;
+#pragma unroll
+      for (int q = 0; q < VE; ++q) dw[q] += gr[k][q] * (xs[k][q] * rs[k]);
+    }
+  }
+  float* pw = part + int64_t(blockIdx.y) * h + col;
+#pragma unroll
+  for (int q = 0; q < VE; ++q)
+    if (q < cnt) pw[q] = dw[q];
+}
+
+template <class T, bool FP8>
+hipError_t run_fwd(const RmsFwd& a, hipStream_t s) {
+  return with_shape<kFwdElems>(a.h, [&](auto wpr, auto epl) {
+    constexpr int WPR = decltype(wpr)::value, EPL = decltype(epl)::value;
+    constexpr int RG = norm_threads(WPR, kFwdThreads) / (64 * WPR);
+    const int64_t grid = std::min<int64_t>((a.n + RG - 1) / RG, kFwdGrid);
+    const int64_t moved = a.n * a.h * int64_t(sizeof(T)) * (a.residual ? 4 : 2);
+    TimedLaunch t(s, FP8 ? K_RMS_FP8_FWD : K_RMS_FWD);
+    auto launch = [&](auto kernel) {
+      hipLaunchKernelGGL(kernel, dim3(unsigned(grid)), dim3(norm_threads(WPR, kFwdThreads)), 0, s,
+                         a);
+    };
+    if (a.h % Elem<T>::kVec != 0)
+      launch(rmsnorm_fwd_kernel<T, WPR, EPL, false, false, FP8>);
+    else if (moved <= kStreamBytes)
+      launch(rmsnorm_fwd_kernel<T, WPR, EPL, true, false, FP8>);
+    else
+      launch(rmsnorm_fwd_kernel<T, WPR, EPL, true, true, FP8>);
+    return hipGetLastError();
+  });
+}
+
+template <class T>
+hipError_t run_bwd_rows(const RmsBwd& a, hipStream_t s) {
+  if (a.n == 0) return hipSuccess;
+  if (a.h > kRegRow && a.part) {
+    constexpr int VE = Elem<T>::kVec;
+    TimedLaunch t(s, K_RMS_BWD);
+    hipLaunchKernelGGL((rms_columns_kernel<T>),
+                       dim3(unsigned((a.h + 256 * VE - 1) / (256 * VE)),
+                            unsigned(part_rows(a.n, a.h))),
+                       dim3(256), 0, s, static_cast<const T*>(a.grad), a.ldg,
+                       static_cast<const T*>(a.x), a.ldx, a.rstd, a.n, int64_t(a.h), a.part);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess || !a.dx) return e;
+  }
+  return with_shape<kBwdElems>(a.h, [&](auto wpr, auto epl) {
+    constexpr int WPR = decltype(wpr)::value, EPL = decltype(epl)::value;
+    constexpr int RG = norm_threads(WPR, kBwdThreads) / (64 * WPR);
+    constexpr bool PARAMS = 64 * WPR * EPL <= kRegRow;
+    const int64_t grid = std::min<int64_t>((a.n + RG - 1) / RG, bwd_grid(a.h));
+    TimedLaunch t(s, K_RMS_BWD);
+    auto launch = [&](auto kernel) {
+      hipLaunchKernelGGL(kernel, dim3(unsigned(grid)), dim3(norm_threads(WPR, kBwdThreads)), 0, s,
+                         a);
+    };
+    if (a.h % Elem<T>::kVec == 0)
+      launch(rmsnorm_bwd_kernel<T, WPR, EPL, true, PARAMS>);
+    else
+      launch(rmsnorm_bwd_kernel<T, WPR, EPL, false, PARAMS>);
+    return hipGetLastError();
+  });
+}
+
+// Partial rows that run_bwd_rows() leaves.
+int64_t rows_left(int64_t n, int64_t h) {
+  if (n == 0 || h > kRegRow) return part_rows(n, h);
+  int64_t rows = 0;
+  (void)with_shape<kBwdElems>(h, [&](auto wpr, auto) {
+    constexpr int WPR = decltype(wpr)::value;
+    constexpr int RG = norm_threads(WPR, kBwdThreads) / (64 * WPR);
+    rows = std::min<int64_t>((n + RG - 1) / RG, bwd_grid(h));
+    return hipSuccess;
+  });
+  return rows;
+}
+
+}  // namespace
+
+hipError_t rmsnorm_fwd_run(const RmsFwdArgs& a, hipStream_t s) {
+  if (a.n == 0) return hipSuccess;
+  const RmsFwd k{a.x,   a.residual, a.weight,       a.n,      a.ldx,      a.ldr,
+                 int(a.h), a.param_dtype == kF32, a.eps, a.y, a.residual_out, a.ldy,
+                 a.ldro, a.rstd_out, a.scales,      a.lds,    a.scale_dtype == kScaleE8M0};
+  const bool fp8 = a.scales != nullptr;
+  switch (a.dtype) {
+    case kBF16: return fp8 ? run_fwd<Bf16, true>(k, s) : run_fwd<Bf16, false>(k, s);
+    case kF16: return fp8 ? run_fwd<_Float16, true>(k, s) : run_fwd<_Float16, false>(k, s);
+    default: return fp8 ? run_fwd<float, true>(k, s) : run_fwd<float, false>(k, s);
+  }
+}
+
+size_t rmsnorm_workspace_bytes(int64_t n, int64_t h) {
+  return std::max<size_t>(align256(size_t(part_rows(n, h)) * size_t(h) * 4), 256);
+}
+
+hipError_t rmsnorm_bwd_run(const RmsBwdArgs& a, hipStream_t s) {
+  const bool add = a.flags & RMSNORM_ACCUMULATE;
+  if (a.n == 0 && (!a.grad_weight || add)) return hipSuccess;
+  float* part = a.grad_weight ? static_cast<float*>(a.workspace) : nullptr;
+  const RmsBwd k{a.grad, a.x,    a.weight, a.grad_residual, a.rstd, a.n,
+                 a.ldg,  a.ldx,  a.ldgr,   a.lddx,          int(a.h), a.param_dtype == kF32,
+                 a.grad_x, part};
+  hipError_t e;
+  switch (a.dtype) {
+    case kBF16: e = run_bwd_rows<Bf16>(k, s); break;
+    case kF16: e = run_bwd_rows<_Float16>(k, s); break;
+    default: e = run_bwd_rows<float>(k, s);
+  }
+  if (e != hipSuccess || !part) return e;
+  const int64_t rows = rows_left(a.n, a.h);
+  switch (a.grad_param_dtype) {
+    case kBF16: return run_reduce<Bf16>(part, nullptr, rows, a.h, add, a.grad_weight, nullptr, s);
+    case kF16:
+      return run_reduce<_Float16>(part, nullptr, rows, a.h, add, a.grad_weight, nullptr, s);
+    default: return run_reduce<float>(part, nullptr, rows, a.h, add, a.grad_weight, nullptr, s);
+  }
+}
+
+}  // namespace lce
