@@ -170,8 +170,7 @@ struct MatmulK {
   const void *ca, *cb;
   const float* bias;
   int64_t m, n, k, lda, ldb, ldca, ldcb, ldo;
-  void* out;
-  float* part;     // fp32 [splits, m, n] where k is cut, else NULL
+  void* out;       // where k is cut: fp32 [splits, m, n], without the bias
   int64_t blocks;  // of 128 columns
   int64_t per;     // blocks of a split
   TileMap tm;
@@ -200,12 +199,15 @@ struct Cfg {
 __device__ __forceinline__ uint32_t limit32(int64_t bytes) {
   return bytes <= 0 ? 0u : bytes >= 0x7fffffffLL ? 0x7fffffffu : uint32_t(bytes);
 }
-__device__ __forceinline__ i32x4_t rsrc(const void* p, int64_t bytes) {
-  const uint64_t u = reinterpret_cast<uint64_t>(p);
-  const uint32_t lo = __builtin_amdgcn_readfirstlane(uint32_t(u));
-  const uint32_t hi = __builtin_amdgcn_readfirstlane(uint32_t(u >> 32));
-  const uint32_t n = __builtin_amdgcn_readfirstlane(limit32(bytes));
-  return i32x4_t{int(lo), int(hi & 0xffffu), int(n), 0x00020000};
+// The same value in all lanes, said so that it stays in scalar registers.
+__device__ __forceinline__ int64_t uniform(int64_t x) {
+  const uint32_t lo = __builtin_amdgcn_readfirstlane(uint32_t(x));
+  const uint32_t hi = __builtin_amdgcn_readfirstlane(uint32_t(uint64_t(x) >> 32));
+  return int64_t(uint64_t(lo) | uint64_t(hi) << 32);
+}
+__device__ __forceinline__ i32x4_t rsrc(int64_t p, int64_t bytes) {
+  return i32x4_t{int(uint32_t(p)), int(uint32_t(uint64_t(p) >> 32) & 0xffffu), int(limit32(bytes)),
+                 0x00020000};
 }
 
 // One dword (or zero-extended byte) per lane from global straight into LDS at m0 + 4 * lane.
@@ -230,19 +232,6 @@ __device__ __forceinline__ void dma_scale(i32x4_t rs, uint32_t voff, uint32_t m0
         : "=&s"(saved)
         : "s"(m0), "v"(voff), "s"(rs)
         : "memory");
-}
-
-// Byte offsets of a lane's P loads within a slice's window of rows of ld bytes, and the k each
-// starts at: 8 rows of eight 16-byte chunks an instruction.
-template <int P>
-__device__ __forceinline__ void slice_offsets(int64_t ld, uint32_t (&off)[P], uint32_t (&at)[P]) {
-  const int l = threadIdx.x & 63, w = threadIdx.x >> 6;
-#pragma unroll
-  for (int j = 0; j < P; ++j) {
-    const int r = 8 * (w * P + j) + l / 8;
-    at[j] = 16 * ((l % 8) ^ (r & 7));
-    off[j] = uint32_t(r * ld + at[j]);
-  }
 }
 
 constexpr uint32_t kPast = 0x80000000u;  // an offset past any window: reads as zero
@@ -279,62 +268,63 @@ __global__ void __launch_bounds__(C::THREADS, C::OCC) fp8_matmul_kernel(MatmulK 
   const uint32_t wave = __builtin_amdgcn_readfirstlane(uint32_t(threadIdx.x >> 6));
   const int wm = wave / C::WN, wn = wave % C::WN;
 
-  uint32_t offa[C::PA], offb[C::PB], ata[C::PA], atb[C::PB];
-  slice_offsets<C::PA>(a.lda, offa, ata);
-  slice_offsets<C::PB>(a.ldb, offb, atb);
+  // A load takes 8 rows of eight 16-byte chunks: a lane's byte offset in the window of rows of the
+  // first of its wavefront's loads, and the column it starts at, the same in all of them.
+  const uint32_t at = 16 * ((lane % 8) ^ (lane / 8));
+  const uint32_t off_a = uint32_t((8 * C::PA * wave + lane / 8) * a.lda) + at;
+  const uint32_t off_b = uint32_t((8 * C::PB * wave + lane / 8) * a.ldb) + at;
+  const uint32_t step_a = uint32_t(8 * a.lda), step_b = uint32_t(8 * a.ldb);
   const uint32_t lds0 =
       uint32_t(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) char*)lds));
-  // the window of slice i: bytes up to the end of the last row
-  const uint8_t* pa = a.a + m0 * a.lda + b0 * kFp8Block;
-  const uint8_t* pb = a.b + n0 * a.ldb + b0 * kFp8Block;
-  int64_t left_a = (a.m - 1 - m0) * a.lda + a.k - b0 * kFp8Block;
-  int64_t left_b = (a.n - 1 - n0) * a.ldb + a.k - b0 * kFp8Block;
+  // the window of a slice: its address and the bytes up to the end of the last row
+  int64_t pa = uniform(reinterpret_cast<int64_t>(a.a) + m0 * a.lda + b0 * kFp8Block);
+  int64_t pb = uniform(reinterpret_cast<int64_t>(a.b) + n0 * a.ldb + b0 * kFp8Block);
+  int64_t left_a = uniform((a.m - 1 - m0) * a.lda + a.k - b0 * kFp8Block);
+  int64_t left_b = uniform((a.n - 1 - n0) * a.ldb + a.k - b0 * kFp8Block);
+  int64_t left_k = uniform(a.k - b0 * kFp8Block);  // columns that exist
   // scales: wavefronts 0 .. BM / 64 - 1 take the rows' of A, the others the column blocks' of B
-  const bool of_a = wave < C::BM / 64;
-  const char* ps = static_cast<const char*>(of_a ? a.ca : a.cb);
-  int64_t left_s, step_s;
+  int64_t ps, left_s, step_s, less_s;
   uint32_t off_s, to_s;
-  if (of_a) {
-    ps += (b0 * a.ldca + m0) * SE;
+  if (wave < C::BM / 64) {
+    ps = reinterpret_cast<int64_t>(a.ca) + (b0 * a.ldca + m0) * SE;
     left_s = (a.m - m0) * SE;
     step_s = a.ldca * SE;
+    less_s = 0;
     off_s = (64 * wave + lane) * SE;
     to_s = C::ABytes + C::BBytes + 256 * wave;
   } else {
     const int64_t nb = n0 / kFp8Block, last = (a.n - 1) / kFp8Block;
-    ps += (nb * a.ldcb + b0) * SE;
+    ps = reinterpret_cast<int64_t>(a.cb) + (nb * a.ldcb + b0) * SE;
     left_s = ((last - nb) * a.ldcb + a.blocks - b0) * SE;
-    step_s = SE;
+    step_s = less_s = SE;
     off_s = lane < C::BN / 128 ? uint32_t(lane * a.ldcb * SE) : kPast;
     to_s = C::ABytes + C::BBytes + 4 * C::BM;
   }
+  ps = uniform(ps);
+  left_s = uniform(left_s);
+  step_s = uniform(step_s);
+  less_s = uniform(less_s);
+  to_s = __builtin_amdgcn_readfirstlane(to_s);
   int issued = 0, wslot = 0;
   auto issue = [&]() {
     const uint32_t o = lds0 + uint32_t(wslot * C::StageBytes);
     const i32x4_t ra = rsrc(pa, left_a), rb = rsrc(pb, left_b), rs = rsrc(ps, left_s);
-    const int64_t krem = a.k - (b0 + issued) * kFp8Block;  // columns of this slice that exist
-    if (krem >= kFp8Block) {
+    // chunks behind the last column read as zero
+    const uint32_t past = int64_t(at) < left_k ? 0u : kPast;
 #pragma unroll
-      for (int j = 0; j < C::PA; ++j) dma16(ra, offa[j], o + (wave * C::PA + j) * 1024u);
+    for (int j = 0; j < C::PA; ++j)
+      dma16(ra, (off_a + j * step_a) | past, o + (wave * C::PA + j) * 1024u);
 #pragma unroll
-      for (int j = 0; j < C::PB; ++j)
-        dma16(rb, offb[j], o + C::ABytes + (wave * C::PB + j) * 1024u);
-    } else {
-#pragma unroll
-      for (int j = 0; j < C::PA; ++j)
-        dma16(ra, int64_t(ata[j]) < krem ? offa[j] : kPast, o + (wave * C::PA + j) * 1024u);
-#pragma unroll
-      for (int j = 0; j < C::PB; ++j)
-        dma16(rb, int64_t(atb[j]) < krem ? offb[j] : kPast,
-              o + C::ABytes + (wave * C::PB + j) * 1024u);
-    }
+    for (int j = 0; j < C::PB; ++j)
+      dma16(rb, (off_b + j * step_b) | past, o + C::ABytes + (wave * C::PB + j) * 1024u);
     dma_scale<E8M0>(rs, off_s, o + to_s);
     pa += kFp8Block;
     pb += kFp8Block;
     ps += step_s;
     left_a -= kFp8Block;
     left_b -= kFp8Block;
-    if (!of_a) left_s -= step_s;
+    left_k -= kFp8Block;
+    left_s -= less_s;
     wslot = wslot + 1 == C::STAGES ? 0 : wslot + 1;
     ++issued;
   };
@@ -357,28 +347,32 @@ __global__ void __launch_bounds__(C::THREADS, C::OCC) fp8_matmul_kernel(MatmulK 
     const char* st = lds + rslot * C::StageBytes;
     rslot = rslot + 1 == C::STAGES ? 0 : rslot + 1;
     const char* sc = st + C::ABytes + C::BBytes;
-    const int g = lane >> 4;
-    auto frag = [&](const char* base, int r) {
-      const char* row = base + r * 128;
-      const v4i lo = *reinterpret_cast<const v4i*>(row + ((g ^ (r & 7)) << 4));
-      const v4i hi = *reinterpret_cast<const v4i*>(row + (((g + 4) ^ (r & 7)) << 4));
+    // a fragment: chunks g and g + 4 of a row, g = lane / 16, where the row's swizzle put them
+    const char* fr = st + (lane & 15) * 128 + (((lane >> 4) ^ (lane & 7)) << 4);
+    const char* fr4 = st + (lane & 15) * 128 + (((lane >> 4) ^ 4 ^ (lane & 7)) << 4);
+    auto frag = [&](int row) {  // of the slice's rows, B's behind A's; a multiple of 16
+      const v4i lo = *reinterpret_cast<const v4i*>(fr + row * 128);
+      const v4i hi = *reinterpret_cast<const v4i*>(fr4 + row * 128);
       return v8i{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
     };
-    v8i fb[TN], fa[TM];
-    uint32_t sa[TM];
+    const int ra = wm * (C::BM / C::WM), rb = C::BM + wn * (C::BN / C::WN);
+    auto scale_of = [&](int i) {
+      return *reinterpret_cast<const uint32_t*>(sc + 4 * (ra + 16 * i + (lane & 15)));
+    };
     const uint32_t sb =
         *reinterpret_cast<const uint32_t*>(sc + 4 * C::BM + 4 * (wn * (C::BN / C::WN) / 128));
+    v8i fb[TN];
 #pragma unroll
-    for (int j = 0; j < TN; ++j)
-      fb[j] = frag(st + C::ABytes, wn * (C::BN / C::WN) + 16 * j + (lane & 15));
-#pragma unroll
-    for (int i = 0; i < TM; ++i) {
-      const int r = wm * (C::BM / C::WM) + 16 * i + (lane & 15);
-      fa[i] = frag(st, r);
-      sa[i] = *reinterpret_cast<const uint32_t*>(sc + 4 * r);
-    }
-    __builtin_amdgcn_sched_barrier(0);
+    for (int j = 0; j < TN; ++j) fb[j] = frag(rb + 16 * j);
     if constexpr (PRECISE) {
+      v8i fa[TM];
+      uint32_t sa[TM];
+#pragma unroll
+      for (int i = 0; i < TM; ++i) {
+        fa[i] = frag(ra + 16 * i);
+        sa[i] = scale_of(i);
+      }
+      __builtin_amdgcn_sched_barrier(0);
       const float cb = scale_value<E8M0>(sb);
       Wide32 wb[TN];
 #pragma unroll
@@ -391,48 +385,97 @@ __global__ void __launch_bounds__(C::THREADS, C::OCC) fp8_matmul_kernel(MatmulK 
         for (int j = 0; j < TN; ++j) add_scaled(acc[i][j], block_sums(wb[j], wa), s);
       }
     } else {
+      // the fragments of AHEAD rows of tiles are in flight or at work at a time
+      constexpr int AHEAD = TM < 4 ? TM : 4;
+      v8i fa[AHEAD];
+      uint32_t sa[AHEAD];
+#pragma unroll
+      for (int i = 0; i < AHEAD; ++i) {
+        fa[i] = frag(ra + 16 * i);
+        sa[i] = scale_of(i);
+      }
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int i = 0; i < TM; ++i) {
-        const float s = __uint_as_float(sa[i]) * __uint_as_float(sb);
+        const v8i x = fa[i % AHEAD];
+        const uint32_t sx = sa[i % AHEAD];
+        const float s = __uint_as_float(sx) * __uint_as_float(sb);
 #pragma unroll
         for (int j = 0; j < TN; ++j) {
           if constexpr (E8M0)
             acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                fb[j], fa[i], acc[i][j], 0, 0, 0, int(sb), 0, int(sa[i]));
+                fb[j], x, acc[i][j], 0, 0, 0, int(sb), 0, int(sx));
           else
             add_scaled(acc[i][j],
                        __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                           fb[j], fa[i], f32x4_t{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 127, 0, 127),
+                           fb[j], x, f32x4_t{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 127, 0, 127),
                        s);
+        }
+        if (i + AHEAD < TM) {
+          fa[i % AHEAD] = frag(ra + 16 * (i + AHEAD));
+          sa[i % AHEAD] = scale_of(i + AHEAD);
+          __builtin_amdgcn_sched_barrier(0);
         }
       }
     }
   }
 
-  // a lane owns 4 consecutive columns of a row
+  // Epilogue. A lane owns 4 consecutive columns of a row, of which 16 rows would make a store of
+  // 32-byte pieces: the wavefront's sums go through LDS (its own part of the ring, the same
+  // swizzle) and leave as rows of whole lines.
+  constexpr int RowBytes = (C::BN / C::WN) * int(sizeof(T)), Rows = C::BM / C::WM;
+  constexpr int Chunks = RowBytes / 16, PerStore = 64 / Chunks, VE = 16 / int(sizeof(T));
+  static_assert(C::NW * Rows * RowBytes <= C::StageBytes * C::STAGES, "the ring holds the tile");
+  const int64_t nw = n0 + wn * (C::BN / C::WN), mw = m0 + wm * Rows;
+  const int g4 = 4 * (lane >> 4);
+  float bias[TN][4];
 #pragma unroll
-  for (int j = 0; j < TN; ++j) {
-    const int64_t gn = n0 + wn * (C::BN / C::WN) + 16 * j + 4 * (lane >> 4);
-    const int cnt = gn + 4 <= a.n ? 4 : int(a.n - gn);
-    if (cnt <= 0) continue;
-    float bias[4] = {0.f, 0.f, 0.f, 0.f};
-    if (a.bias && !a.part) {
+  for (int j = 0; j < TN; ++j)
 #pragma unroll
-      for (int q = 0; q < 4; ++q)
-        if (q < cnt) bias[q] = a.bias[gn + q];
+    for (int q = 0; q < 4; ++q) {
+      const int64_t gn = nw + 16 * j + g4 + q;
+      bias[j][q] = a.bias && gn < a.n ? a.bias[gn] : 0.f;
     }
+  __syncthreads();  // the ring has been read
+  char* tile = lds + wave * (Rows * RowBytes);
 #pragma unroll
-    for (int i = 0; i < TM; ++i) {
-      const int64_t gm = m0 + wm * (C::BM / C::WM) + 16 * i + (lane & 15);
-      if (gm >= a.m) continue;
+  for (int i = 0; i < TM; ++i) {
+    const int r = 16 * i + (lane & 15);
+#pragma unroll
+    for (int j = 0; j < TN; ++j) {
+      const int byte = (16 * j + g4) * int(sizeof(T));
       float x[4];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) x[q] = acc[i][j][q] + bias[q];
-      if (a.part)
-        store4(a.part + (tc.kz * a.m + gm) * a.n + gn, x, cnt);
-      else
-        store4(static_cast<T*>(a.out) + gm * a.ldo + gn, x, cnt);
+      for (int q = 0; q < 4; ++q) x[q] = acc[i][j][q] + bias[j][q];
+      store4(reinterpret_cast<T*>(tile + r * RowBytes +
+                                  (((byte >> 4) ^ (lane & 7)) << 4) + (byte & 15)), x, 4);
     }
+  }
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  const int chunk = lane % Chunks, rr = lane / Chunks;
+  const int64_t gn = nw + chunk * VE, cnt = a.n - gn;
+  T* out = static_cast<T*>(a.out) + (tc.kz * a.m + mw + rr) * a.ldo + gn;
+#pragma unroll 4
+  for (int s = 0; s < Rows / PerStore; ++s) {
+    const int r = s * PerStore + rr;
+    if (mw + r < a.m && cnt > 0) {
+      const raw4 v = *reinterpret_cast<const raw4*>(tile + r * RowBytes + ((chunk ^ (r & 7)) << 4));
+      if (cnt >= VE) {
+        store_raw(out, v);
+      } else {
+#pragma unroll
+        for (int k = 0; k < VE; ++k)
+          if (k < cnt) {
+            const uint32_t w = v[k * int(sizeof(T)) / 4] >> (8 * (k * int(sizeof(T)) % 4));
+            if constexpr (sizeof(T) == 4)
+              reinterpret_cast<uint32_t*>(out)[k] = w;
+            else
+              reinterpret_cast<uint16_t*>(out)[k] = uint16_t(w);
+          }
+      }
+    }
+    out += PerStore * a.ldo;
   }
 }
 
@@ -609,9 +652,9 @@ template <bool E8M0, class T>
 hipError_t run_matmul(const Fp8MatmulArgs& a, hipStream_t s) {
   constexpr bool kPrecise = !std::is_same_v<T, Bf16>;
   const Plan p = plan_of(a.m, a.n, a.k, kPrecise);
-  MatmulK k{a.a,   a.b,   a.a_scales, a.b_scales, a.bias, a.m,     a.n,     a.k, a.lda,
-            a.ldb, a.ldas, a.ldbs,    a.ldo,      a.out,  nullptr, (a.k + kFp8Block - 1) / kFp8Block,
-            p.per, TileMap{}};
+  MatmulK k{a.a,    a.b,    a.a_scales, a.b_scales, a.bias, a.m,
+            a.n,    a.k,    a.lda,      a.ldb,      a.ldas, a.ldbs,
+            a.ldo,  a.out,  (a.k + kFp8Block - 1) / kFp8Block, p.per, TileMap{}};
   if (p.few) {
     TimedLaunch t(s, K_FP8_MATMUL_FEW);
     const dim3 block(64 * kFewWaves);
@@ -631,13 +674,17 @@ hipError_t run_matmul(const Fp8MatmulArgs& a, hipStream_t s) {
       return launch_tiles<Wide, E8M0, false, T>(k, p, s);
     }
   }
-  if (p.splits > 1) k.part = static_cast<float*>(a.workspace);
-  hipError_t e = launch_tiles<Small, E8M0, kPrecise, T>(k, p, s);
-  if (e != hipSuccess || p.splits == 1) return e;
+  if (p.splits == 1) return launch_tiles<Small, E8M0, kPrecise, T>(k, p, s);
+  k.out = a.workspace;
+  k.ldo = a.n;
+  k.bias = nullptr;
+  const hipError_t e = launch_tiles<Small, E8M0, kPrecise, float>(k, p, s);
+  if (e != hipSuccess) return e;
   const int64_t threads = a.m * ((a.n + 3) / 4);
   TimedLaunch t(s, K_FP8_JOIN);
   hipLaunchKernelGGL((fp8_join_kernel<T>), dim3(unsigned((threads + 255) / 256)), dim3(256), 0, s,
-                     k.part, p.splits, a.m, a.n, a.bias, static_cast<T*>(a.out), a.ldo);
+                     static_cast<const float*>(a.workspace), p.splits, a.m, a.n, a.bias,
+                     static_cast<T*>(a.out), a.ldo);
   return hipGetLastError();
 }
 
