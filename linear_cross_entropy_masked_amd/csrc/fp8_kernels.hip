@@ -395,21 +395,30 @@ __global__ void __launch_bounds__(C::THREADS, C::OCC) fp8_matmul_kernel(MatmulK 
         sa[i] = scale_of(i);
       }
       __builtin_amdgcn_sched_barrier(0);
+      // fp32 scales: a tile's sums are added LAG tiles later, when they have left the pipeline
+      constexpr int LAG = 2;
+      f32x4_t t[LAG + 1];
+      float s[2];
+      auto add = [&](int n) {
+        if (!E8M0 && n >= 0)
+          add_scaled(acc[n / TN][n % TN], t[n % (LAG + 1)], s[n / TN % 2]);
+      };
 #pragma unroll
       for (int i = 0; i < TM; ++i) {
         const v8i x = fa[i % AHEAD];
         const uint32_t sx = sa[i % AHEAD];
-        const float s = __uint_as_float(sx) * __uint_as_float(sb);
+        s[i % 2] = __uint_as_float(sx) * __uint_as_float(sb);
 #pragma unroll
         for (int j = 0; j < TN; ++j) {
-          if constexpr (E8M0)
+          if constexpr (E8M0) {
             acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
                 fb[j], x, acc[i][j], 0, 0, 0, int(sb), 0, int(sx));
-          else
-            add_scaled(acc[i][j],
-                       __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                           fb[j], x, f32x4_t{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 127, 0, 127),
-                       s);
+          } else {
+            t[(i * TN + j) % (LAG + 1)] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                fb[j], x, f32x4_t{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 127, 0, 127);
+            __builtin_amdgcn_sched_barrier(0);
+            add(i * TN + j - LAG);
+          }
         }
         if (i + AHEAD < TM) {
           fa[i % AHEAD] = frag(ra + 16 * (i + AHEAD));
@@ -417,6 +426,8 @@ __global__ void __launch_bounds__(C::THREADS, C::OCC) fp8_matmul_kernel(MatmulK 
           __builtin_amdgcn_sched_barrier(0);
         }
       }
+#pragma unroll
+      for (int n = TM * TN - LAG; n < TM * TN; ++n) add(n);
     }
   }
 
@@ -624,8 +635,13 @@ Plan plan_of(int64_t m, int64_t n, int64_t k, bool precise) {
   p.splits = 1;
   p.per = blocks;
   if (p.few) return p;
-  const int64_t big = (m + 255) / 256 * ((n + 255) / 256);
-  p.wide = !precise && big >= 256;
+  // Rounds of tiles over the 256 CUs, one large or two small ones each: a round of small tiles
+  // takes 0.52 (768 columns) to 0.59 (4096) of the time of a round of large ones, so the large ones
+  // are for where they do not need that many rounds more (4096 x 4096 x 4096: 59 us and 70;
+  // 1003 x 32777 x 768, 516 of them: 57 us and 46).
+  const int64_t large = (m + 255) / 256 * ((n + 255) / 256);
+  const int64_t small = (m + 127) / 128 * ((n + 127) / 128);
+  p.wide = !precise && large >= 256 && 100 * ((large + 255) / 256) < 58 * ((small + 511) / 512);
   const int64_t bm = p.wide ? 256 : 128;
   p.m_tiles = (m + bm - 1) / bm;
   p.n_tiles = (n + bm - 1) / bm;
