@@ -15,6 +15,7 @@
 // compared in fp64. No atomics decide an order: the lists are filled by atomics and ranked by
 // keys that are all different.
 #include <algorithm>
+#include <type_traits>
 
 #include "common.h"
 #include "elem.h"
@@ -25,9 +26,12 @@ namespace lce {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kList = 256;      // candidates of a slice that are ranked at once
-constexpr int kRowList = 440;   // the same of a row
+constexpr int kHolders = 96;  // threads of a slice whose logits are looked through
+constexpr int kList = 256;    // candidates of a slice that are ranked at once
+constexpr int kRowList = 440; // the same of a row
 constexpr int kMost = BEAM_MAX_CANDIDATES;
+constexpr int kPairs = 880;   // candidates of an entry whose ranks fit one wavefront's list
+static_assert(kPairs * 4 <= kRowList * 8, "ranks take a list's place");
 
 // Floats as integers of the same order; 0 is below all of them.
 __device__ __forceinline__ uint32_t ordered(float x) {
@@ -42,13 +46,41 @@ __device__ __forceinline__ uint64_t key_of(float z, uint32_t token) {
   return uint64_t(ordered(z)) << 32 | uint32_t(~token);
 }
 
-// A threshold that at least `want` of the wavefront's PER · 64 values reach, and not many more
-// than that where the values differ; 0 where there are fewer. Bits are fixed from the top until
-// the number that reaches it is at most want + want / 4.
+// The largest (smallest) of the wavefront, in all lanes.
+template <bool MAX>
+__device__ __forceinline__ uint32_t wave_extreme(uint32_t x) {
+  auto pick = [](uint32_t a, uint32_t b) { return MAX == (a > b) ? a : b; };
+  auto lanes = [&](auto ctrl) {
+    constexpr int CTRL = decltype(ctrl)::value;
+    x = pick(x, uint32_t(__builtin_amdgcn_update_dpp(0, int(x), CTRL, 0xf, 0xf, true)));
+  };
+  lanes(std::integral_constant<int, 0xB1>{});   // lane ^ 1
+  lanes(std::integral_constant<int, 0x4E>{});   // lane ^ 2
+  lanes(std::integral_constant<int, 0x141>{});  // mirrored within 8
+  lanes(std::integral_constant<int, 0x140>{});  // mirrored within 16
+  const auto r = __builtin_amdgcn_permlane16_swap(int(x), int(x), false, false);
+  x = pick(uint32_t(r[0]), uint32_t(r[1]));
+  const auto h = __builtin_amdgcn_permlane32_swap(int(x), int(x), false, false);
+  return pick(uint32_t(h[0]), uint32_t(h[1]));
+}
+
+// A threshold that at least `want` of the wavefront's PER · 64 values reach (0 where there are
+// not so many), and not many more than that where the values differ. Bits are fixed from the first
+// in which any two values differ, until the number that reaches it is at most want + want / 4.
 template <int PER>
 __device__ __forceinline__ uint32_t threshold(const uint32_t (&x)[PER], int want) {
-  uint32_t t = 0;
-  for (int bit = 31; bit >= 0; --bit) {
+  if (want > 64 * PER) return 0;
+  uint32_t lo = x[0], hi = x[0];
+#pragma unroll
+  for (int k = 1; k < PER; ++k) {
+    lo = x[k] < lo ? x[k] : lo;
+    hi = x[k] > hi ? x[k] : hi;
+  }
+  hi = __builtin_amdgcn_readfirstlane(wave_extreme<true>(hi));
+  lo = __builtin_amdgcn_readfirstlane(wave_extreme<false>(lo));
+  int bit = 31 - __clz(int(hi ^ lo));  // -1: all the same
+  uint32_t t = bit < 0 ? hi : hi >> 1 >> bit << bit << 1;
+  for (; bit >= 0; --bit) {
     const uint32_t c = t | 1u << bit;
     int reach = 0;
 #pragma unroll
@@ -76,34 +108,41 @@ __global__ void __launch_bounds__(kThreads) beam_rows_kernel(RowsK a) {
   __shared__ float top[kThreads];
   __shared__ float wave_m[kWaves], wave_s[kWaves];
   __shared__ uint32_t limit;
-  __shared__ int count;
+  __shared__ int holders, count;
+  // the logits of the threads whose largest reaches the threshold, and where each one's start
+  __shared__ __attribute__((aligned(16))) float held[kHolders][EPT];
+  __shared__ int from_thread[kHolders];
   __shared__ uint64_t list[kList];
   __shared__ uint64_t best[kWaves];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int64_t row = blockIdx.x / a.splits, split = blockIdx.x % a.splits;
-  const int64_t at = split * (kThreads * EPT) + tid * 8;
+  const int64_t base = split * (kThreads * EPT), at = base + tid * 8;
   const T* z = static_cast<const T*>(a.logits) + row * a.ld;
   float x[NV][8];
+  if (base + kThreads * EPT <= a.v) {
 #pragma unroll
-  for (int j = 0; j < NV; ++j) {
-    const int64_t c = at + int64_t(j) * kThreads * 8, cnt = a.v - c;
-    if (cnt >= 8) {
-      load_some<T, 8>(z + c, cnt, x[j]);
-    } else {
+    for (int j = 0; j < NV; ++j) load_some<T, 8>(z + at + j * kThreads * 8, 8, x[j]);
+  } else {
 #pragma unroll
-      for (int q = 0; q < 8; ++q) x[j][q] = q < cnt ? Elem<T>::to_f32(z[c + q]) : -INFINITY;
+    for (int j = 0; j < NV; ++j) {
+      const int64_t c = at + int64_t(j) * kThreads * 8, cnt = a.v - c;
+      if (cnt >= 8) {
+        load_some<T, 8>(z + c, cnt, x[j]);
+      } else {
+#pragma unroll
+        for (int q = 0; q < 8; ++q) x[j][q] = q < cnt ? Elem<T>::to_f32(z[c + q]) : -INFINITY;
+      }
     }
   }
   float m = -INFINITY;
 #pragma unroll
   for (int j = 0; j < NV; ++j)
 #pragma unroll
-    for (int q = 0; q < 8; ++q) {
-      x[j][q] += 0.f;  // one zero: -0 becomes +0
-      m = fmaxf(m, x[j][q]);
-    }
+    for (int q = 0; q < 8; ++q) m = fmaxf(m, x[j][q]);
+  m += 0.f;  // one zero: -0 becomes +0
+  const float mine = m;
   top[tid] = m;
-  if (tid == 0) count = 0;
+  if (tid == 0) holders = count = 0;
   // the sum about the thread's own maximum (a finite number), then merged
   float s = 0.f;
   const float from = fmaxf(m, -3.4028234663852886e38f);
@@ -123,7 +162,8 @@ __global__ void __launch_bounds__(kThreads) beam_rows_kernel(RowsK a) {
 #pragma unroll
     for (int w = 0; w < kWaves; ++w) t[w] = ordered(top[64 * w + lane]);
     const uint32_t lim = threshold<kWaves>(t, a.num);
-    if (lane == 0) limit = lim;
+    // no logit at or below minus infinity is a candidate
+    if (lane == 0) limit = lim > ordered(-INFINITY) ? lim : ordered(-INFINITY) + 1;
   } else if (wave == 1 && lane == 0) {
     float wm = wave_m[0], ws = wave_s[0];
     bool nan = !(ws >= 0.f);
@@ -136,28 +176,42 @@ __global__ void __launch_bounds__(kThreads) beam_rows_kernel(RowsK a) {
   }
   __syncthreads();
   const float lim = from_ordered(limit);
-  const bool all = limit <= ordered(-INFINITY);  // no threshold: every logit above -inf
+  if (mine >= lim) {
+    const int p = atomicAdd(&holders, 1);
+    if (p < kHolders) {
+      from_thread[p] = tid;
 #pragma unroll
-  for (int j = 0; j < NV; ++j)
+      for (int j = 0; j < NV; ++j)
 #pragma unroll
-    for (int q = 0; q < 8; ++q)
-      if (x[j][q] > -INFINITY && (all || x[j][q] >= lim)) {
-        const int p = atomicAdd(&count, 1);
-        if (p < kList)
-          list[p] = key_of(x[j][q], uint32_t(at + int64_t(j) * kThreads * 8 + q));
-      }
-  __syncthreads();
-  uint64_t* out = a.keys + int64_t(blockIdx.x) * a.num;
-  const int c = count;
-  if (c <= kList) {
-    if (tid < c) {
-      const uint64_t k = list[tid];
-      int rank = 0;
-      for (int i = 0; i < c; ++i) rank += list[i] > k;
-      if (rank < a.num) out[rank] = k;
+        for (int q = 0; q < 8; ++q) held[p][j * 8 + q] = x[j][q];
     }
-    if (tid >= c && tid < a.num) out[tid] = 0;
-    return;
+  }
+  __syncthreads();
+  const int h = holders;
+  uint64_t* out = a.keys + int64_t(blockIdx.x) * a.num;
+  if (h <= kHolders) {
+    for (int i = tid; i < h * EPT; i += kThreads) {
+      const float v = held[i / EPT][i % EPT];
+      if (v >= lim) {
+        const int p = atomicAdd(&count, 1);
+        const int e = i % EPT;
+        if (p < kList)
+          list[p] = key_of(v + 0.f, uint32_t(base + (e / 8 * kThreads + from_thread[i / EPT]) * 8 +
+                                             e % 8));
+      }
+    }
+    __syncthreads();
+    const int c = count;
+    if (c <= kList) {
+      if (tid < c) {
+        const uint64_t k = list[tid];
+        int rank = 0;
+        for (int i = 0; i < c; ++i) rank += list[i] > k;
+        if (rank < a.num) out[rank] = k;
+      }
+      if (tid >= c && tid < a.num) out[tid] = 0;
+      return;
+    }
   }
   // one at a time: the best key below the last one taken
   uint64_t last = ~uint64_t(0);
@@ -168,7 +222,7 @@ __global__ void __launch_bounds__(kThreads) beam_rows_kernel(RowsK a) {
 #pragma unroll
       for (int q = 0; q < 8; ++q)
         if (x[j][q] > -INFINITY) {
-          const uint64_t e = key_of(x[j][q], uint32_t(at + int64_t(j) * kThreads * 8 + q));
+          const uint64_t e = key_of(x[j][q] + 0.f, uint32_t(at + j * kThreads * 8 + q));
           if (e < last && e > k) k = e;
         }
 #pragma unroll
@@ -209,24 +263,28 @@ __device__ __forceinline__ void wave_sync() {
 }
 
 // The best `num` keys of n at `in`, in order, into the wavefront's `out` (LDS); 0 behind the last.
-__device__ __forceinline__ void merge_row(const uint64_t* in, int64_t n, int num, uint64_t* list,
+// `have`: the lane's first kHeld keys, at in[lane], in[lane + 64], ...
+constexpr int kHeld = 4;
+__device__ __forceinline__ void merge_row(const uint64_t* in, int64_t n,
+                                          const uint64_t (&have)[kHeld], int num, uint64_t* list,
                                           int* count, uint64_t* out) {
   const int lane = threadIdx.x & 63;
   uint32_t top[1] = {0};
-  for (int64_t i = lane; i < n; i += 64) {
-    const uint32_t v = uint32_t(in[i] >> 32);
-    top[0] = v > top[0] ? v : top[0];
-  }
+  auto each = [&](auto&& f) {
+#pragma unroll
+    for (int k = 0; k < kHeld; ++k) f(have[k]);
+    for (int64_t i = lane + 64 * kHeld; i < n; i += 64) f(in[i]);
+  };
+  each([&](uint64_t k) { top[0] = uint32_t(k >> 32) > top[0] ? uint32_t(k >> 32) : top[0]; });
   const uint32_t lim = threshold<1>(top, num);
   if (lane == 0) *count = 0;
   wave_sync();
-  for (int64_t i = lane; i < n; i += 64) {
-    const uint64_t k = in[i];
+  each([&](uint64_t k) {
     if (k != 0 && uint32_t(k >> 32) >= lim) {
       const int p = atomicAdd(count, 1);
       if (p < kRowList) list[p] = k;
     }
-  }
+  });
   wave_sync();
   const int c = *static_cast<volatile int*>(count);
   for (int r = lane; r < num; r += 64)
@@ -242,10 +300,9 @@ __device__ __forceinline__ void merge_row(const uint64_t* in, int64_t n, int num
     uint64_t last = ~uint64_t(0);
     for (int r = 0; r < num; ++r) {
       uint64_t k = 0;
-      for (int64_t i = lane; i < n; i += 64) {
-        const uint64_t e = in[i];
+      each([&](uint64_t e) {
         if (e < last && e > k) k = e;
-      }
+      });
 #pragma unroll
       for (int off = 32; off >= 1; off >>= 1) {
         const uint64_t o = __shfl_xor((unsigned long long)k, off, 64);
@@ -258,31 +315,41 @@ __device__ __forceinline__ void merge_row(const uint64_t* in, int64_t n, int num
   wave_sync();
 }
 
-// Workgroup b: batch entry b. LDS: scores and tokens [beams, num], a list per wavefront.
+// Workgroup b: batch entry b. LDS: scores, tokens and ranks [beams, num], a list per wavefront.
 __global__ void __launch_bounds__(512) beam_pick_kernel(PickK a) {
   extern __shared__ __attribute__((aligned(16))) char lds[];
   const int waves = blockDim.x >> 6, wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const int all = a.beams * a.num;
   double* score = reinterpret_cast<double*>(lds);
-  uint64_t* lists = reinterpret_cast<uint64_t*>(score + a.beams * a.num);
+  uint64_t* lists = reinterpret_cast<uint64_t*>(score + all);
   uint64_t* sorted = lists + waves * kRowList;
   int32_t* token = reinterpret_cast<int32_t*>(sorted + waves * kMost);
-  int* counts = token + a.beams * a.num;
+  int* counts = token + all;
+  int* found = counts + waves;               // candidates there are
+  int* ranks = reinterpret_cast<int*>(lists);  // up to kPairs, once the lists are merged
   const int64_t b = blockIdx.x;
+  if (threadIdx.x == 0) *found = 0;
   for (int j = wave; j < a.beams; j += waves) {
-    const int64_t row = b * a.beams + j;
+    const int64_t row = b * a.beams + j, n = a.splits * a.num;
     const float acc = a.scores[row];
     const bool done = a.finished && a.finished[row];
     double* sj = score + j * a.num;
     int32_t* tj = token + j * a.num;
-    // the row's logsumexp, lanes in order of their distance
     const float2* ms = a.sums + row * a.splits;
-    float m = -INFINITY;
-    bool nan = false;
-    for (int64_t i = lane; i < a.splits; i += 64) m = fmaxf(m, ms[i].x);
+    const uint64_t* in = a.keys + row * n;
+    // everything that comes from memory is asked for at once
+    const float2 own = lane < a.splits ? ms[lane] : float2{-INFINITY, 0.f};
+    uint64_t have[kHeld];
+#pragma unroll
+    for (int k = 0; k < kHeld; ++k) have[k] = lane + 64 * k < n ? in[lane + 64 * k] : 0;
+    // the row's logsumexp, lanes in order of their distance
+    float m = own.x;
+    bool nan = !(own.y >= 0.f) || own.x == INFINITY;
+    for (int64_t i = lane + 64; i < a.splits; i += 64) m = fmaxf(m, ms[i].x);
 #pragma unroll
     for (int off = 32; off >= 1; off >>= 1) m = fmaxf(m, __shfl_xor(m, off, 64));
-    double s = 0.0;
-    for (int64_t i = lane; i < a.splits; i += 64) {
+    double s = own.x > -INFINITY ? double(own.y) * exp(double(own.x) - double(m)) : 0.0;
+    for (int64_t i = lane + 64; i < a.splits; i += 64) {
       const float2 p = ms[i];
       nan |= !(p.y >= 0.f) || p.x == INFINITY;
       if (p.x > -INFINITY) s += double(p.y) * exp(double(p.x) - double(m));
@@ -302,8 +369,7 @@ __global__ void __launch_bounds__(512) beam_pick_kernel(PickK a) {
       continue;
     }
     uint64_t* out = sorted + wave * kMost;
-    merge_row(a.keys + row * a.splits * a.num, a.splits * a.num, a.num, lists + wave * kRowList,
-              counts + wave, out);
+    merge_row(in, n, have, a.num, lists + wave * kRowList, counts + wave, out);
     const double lse = double(m) + log(s);
     for (int r = lane; r < a.num; r += 64) {
       const uint64_t k = out[r];
@@ -312,40 +378,61 @@ __global__ void __launch_bounds__(512) beam_pick_kernel(PickK a) {
     }
   }
   __syncthreads();
-  const int64_t to = b * a.num;
-  int found = 0;  // candidates there are, at most num of them counted
-  for (int j = 0; j < a.beams && found < a.num; ++j)
-    for (int r = 0; r < a.num && score[j * a.num + r] > -INFINITY; ++r) ++found;
-  for (int p = threadIdx.x; p < a.beams * a.num; p += blockDim.x) {
-    const int j = p / a.num, r = p % a.num;
+  // how many of beam i come before candidate p of another: better ones, and equal ones of an
+  // earlier beam. A beam's are in order, so they are found by bisection.
+  auto before = [&](int p, int i) {
     const double s = score[p];
-    if (!(s > -INFINITY)) continue;
-    int rank = r;
-    for (int i = 0; i < a.beams && rank < a.num; ++i) {
-      if (i == j) continue;
-      // how many of row i come first: better ones, and equal ones of an earlier beam
-      int lo = 0, hi = a.num;
-      while (lo < hi) {
-        const int mid = (lo + hi) / 2;
-        const double o = score[i * a.num + mid];
-        if (o > s || (o == s && i < j))
-          lo = mid + 1;
-        else
-          hi = mid;
-      }
-      rank += lo;
+    int lo = 0, hi = a.num;
+    while (lo < hi) {
+      const int mid = (lo + hi) / 2;
+      const double o = score[i * a.num + mid];
+      if (o > s || (o == s && i < p / a.num))
+        lo = mid + 1;
+      else
+        hi = mid;
     }
-    if (rank >= a.num) continue;
+    return lo;
+  };
+  const int64_t to = b * a.num;
+  auto put = [&](int p, int rank) {
+    if (rank >= a.num) return;
+    const int j = p / a.num;
     const int32_t tok = token[p];
-    a.scores_out[to + rank] = float(s);
+    a.scores_out[to + rank] = float(score[p]);
     a.parents_out[to + rank] = j;
     a.tokens_out[to + rank] = tok;
     if (a.finished_out)
       a.finished_out[to + rank] =
           (a.finished && a.finished[b * a.beams + j]) || (a.eos >= 0 && tok == a.eos);
+  };
+  if (all <= kPairs) {  // a thread takes a candidate and another beam at a time
+    for (int p = threadIdx.x; p < all; p += blockDim.x) {
+      ranks[p] = p % a.num;  // those of its own beam
+      if (score[p] > -INFINITY) atomicAdd(found, 1);
+    }
+    __syncthreads();
+    for (int u = threadIdx.x; u < all * a.beams; u += blockDim.x) {
+      const int p = u % all, i = u / all;
+      if (i == p / a.num || !(score[p] > -INFINITY)) continue;
+      const int n = before(p, i);
+      if (n > 0) atomicAdd(ranks + p, n);
+    }
+    __syncthreads();
+    for (int p = threadIdx.x; p < all; p += blockDim.x)
+      if (score[p] > -INFINITY) put(p, ranks[p]);
+  } else {  // too many for their ranks to be held
+    for (int p = threadIdx.x; p < all; p += blockDim.x) {
+      if (!(score[p] > -INFINITY)) continue;
+      atomicAdd(found, 1);
+      int rank = p % a.num;
+      for (int i = 0; i < a.beams && rank < a.num; ++i)
+        if (i != p / a.num) rank += before(p, i);
+      put(p, rank);
+    }
+    __syncthreads();
   }
   for (int r = threadIdx.x; r < a.num; r += blockDim.x) {
-    if (r < found) continue;
+    if (r < *found) continue;
     a.scores_out[to + r] = -INFINITY;
     a.parents_out[to + r] = -1;
     a.tokens_out[to + r] = a.ignore_index;
@@ -484,10 +571,10 @@ hipError_t beam_step_run(const BeamStepArgs& a, hipStream_t s) {
   const PickK p{a.scores,     a.finished,      keys,          sums,           splits,
                 int(a.beams), int(a.num),      a.eos,         a.ignore_index, a.scores_out,
                 a.parents_out, a.tokens_out,   a.finished_out, a.status_out};
-  // within 64 KiB of LDS: 65296 bytes at 64 beams and candidates
+  // within 64 KiB of LDS: 65300 bytes at 64 beams and candidates
   const int waves = int(std::min<int64_t>(a.beams, a.beams * a.num <= 2048 ? 8 : 4));
   const size_t lds = size_t(a.beams * a.num) * 12 + size_t(waves) * (kRowList + kMost) * 8 +
-                     size_t(waves) * 4;
+                     size_t(waves) * 4 + 4;
   TimedLaunch t(s, K_BEAM_PICK);
   hipLaunchKernelGGL(beam_pick_kernel, dim3(unsigned(a.batch)), dim3(64 * waves), lds, s, p);
   return hipGetLastError();
