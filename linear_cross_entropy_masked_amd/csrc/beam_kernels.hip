@@ -46,22 +46,31 @@ __device__ __forceinline__ uint64_t key_of(float z, uint32_t token) {
   return uint64_t(ordered(z)) << 32 | uint32_t(~token);
 }
 
-// The largest (smallest) of the wavefront, in all lanes.
-template <bool MAX>
-__device__ __forceinline__ uint32_t wave_extreme(uint32_t x) {
-  auto pick = [](uint32_t a, uint32_t b) { return MAX == (a > b) ? a : b; };
+// join() over the wavefront's values, the result in all lanes; no step goes through LDS.
+template <class F>
+__device__ __forceinline__ uint32_t wave_join(uint32_t x, F&& join) {
   auto lanes = [&](auto ctrl) {
     constexpr int CTRL = decltype(ctrl)::value;
-    x = pick(x, uint32_t(__builtin_amdgcn_update_dpp(0, int(x), CTRL, 0xf, 0xf, true)));
+    x = join(x, uint32_t(__builtin_amdgcn_update_dpp(0, int(x), CTRL, 0xf, 0xf, true)));
   };
   lanes(std::integral_constant<int, 0xB1>{});   // lane ^ 1
   lanes(std::integral_constant<int, 0x4E>{});   // lane ^ 2
   lanes(std::integral_constant<int, 0x141>{});  // mirrored within 8
   lanes(std::integral_constant<int, 0x140>{});  // mirrored within 16
   const auto r = __builtin_amdgcn_permlane16_swap(int(x), int(x), false, false);
-  x = pick(uint32_t(r[0]), uint32_t(r[1]));
+  x = join(uint32_t(r[0]), uint32_t(r[1]));
   const auto h = __builtin_amdgcn_permlane32_swap(int(x), int(x), false, false);
-  return pick(uint32_t(h[0]), uint32_t(h[1]));
+  return join(uint32_t(h[0]), uint32_t(h[1]));
+}
+__device__ __forceinline__ float wave_max(float x) {
+  return __uint_as_float(wave_join(__float_as_uint(x), [](uint32_t a, uint32_t b) {
+    return __float_as_uint(fmaxf(__uint_as_float(a), __uint_as_float(b)));
+  }));
+}
+__device__ __forceinline__ float wave_add(float x) {
+  return __uint_as_float(wave_join(__float_as_uint(x), [](uint32_t a, uint32_t b) {
+    return __float_as_uint(__uint_as_float(a) + __uint_as_float(b));
+  }));
 }
 
 // A threshold that at least `want` of the wavefront's PER · 64 values reach (0 where there are
@@ -76,8 +85,10 @@ __device__ __forceinline__ uint32_t threshold(const uint32_t (&x)[PER], int want
     lo = x[k] < lo ? x[k] : lo;
     hi = x[k] > hi ? x[k] : hi;
   }
-  hi = __builtin_amdgcn_readfirstlane(wave_extreme<true>(hi));
-  lo = __builtin_amdgcn_readfirstlane(wave_extreme<false>(lo));
+  hi = __builtin_amdgcn_readfirstlane(
+      wave_join(hi, [](uint32_t a, uint32_t b) { return a > b ? a : b; }));
+  lo = __builtin_amdgcn_readfirstlane(
+      wave_join(lo, [](uint32_t a, uint32_t b) { return a < b ? a : b; }));
   int bit = 31 - __clz(int(hi ^ lo));  // -1: all the same
   uint32_t t = bit < 0 ? hi : hi >> 1 >> bit << bit << 1;
   for (; bit >= 0; --bit) {
@@ -96,14 +107,49 @@ __device__ __forceinline__ uint32_t threshold(const uint32_t (&x)[PER], int want
 struct RowsK {
   const void* logits;
   int64_t v, ld;
-  int64_t splits;
+  uint32_t splits;
   int num;
   uint64_t* keys;   // [rows, splits, num], best first, 0 where there are fewer
   float2* sums;     // [rows, splits]: maximum, sum of exp(z − maximum)
 };
 
+// Eight logits of a thread as they are stored; minus infinity behind the row's end.
+template <class T>
+struct Logits8 {
+  static constexpr int kRaws = 8 / Elem<T>::kVec;
+  raw4 r[kRaws];
+  __device__ __forceinline__ void load(const T* p) {
+#pragma unroll
+    for (int k = 0; k < kRaws; ++k) r[k] = load_raw(p + k * Elem<T>::kVec);
+  }
+  __device__ __forceinline__ void load_some(const T* p, int64_t cnt) {
+    if (cnt >= 8) return load(p);
+    float x[8];
+#pragma unroll
+    for (int q = 0; q < 8; ++q) x[q] = q < cnt ? Elem<T>::to_f32(p[q]) : -INFINITY;
+#pragma unroll
+    for (int k = 0; k < kRaws; ++k) {
+      float y[Elem<T>::kVec];
+#pragma unroll
+      for (int q = 0; q < Elem<T>::kVec; ++q) y[q] = x[k * Elem<T>::kVec + q];
+      r[k] = Elem<T>::pack(y);
+    }
+  }
+  // Widened anew each time: kept, the numbers would take twice the registers.
+  __device__ __forceinline__ void get(float (&x)[8]) {
+#pragma unroll
+    for (int k = 0; k < kRaws; ++k) {
+      asm volatile("" : "+v"(r[k]));
+      float y[Elem<T>::kVec];
+      Elem<T>::unpack(r[k], y);
+#pragma unroll
+      for (int q = 0; q < Elem<T>::kVec; ++q) x[k * Elem<T>::kVec + q] = y[q];
+    }
+  }
+};
+
 template <class T, int EPT>
-__global__ void __launch_bounds__(kThreads) beam_rows_kernel(RowsK a) {
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 8 : 5) beam_rows_kernel(RowsK a) {
   constexpr int NV = EPT / 8, kWaves = kThreads / 64;
   __shared__ float top[kThreads];
   __shared__ float wave_m[kWaves], wave_s[kWaves];
@@ -115,45 +161,65 @@ __global__ void __launch_bounds__(kThreads) beam_rows_kernel(RowsK a) {
   __shared__ uint64_t list[kList];
   __shared__ uint64_t best[kWaves];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int64_t row = blockIdx.x / a.splits, split = blockIdx.x % a.splits;
-  const int64_t base = split * (kThreads * EPT), at = base + tid * 8;
-  const T* z = static_cast<const T*>(a.logits) + row * a.ld;
-  float x[NV][8];
+  const uint32_t row = blockIdx.x / a.splits, split = blockIdx.x - row * a.splits;
+  const int64_t base = int64_t(split) * (kThreads * EPT), at = base + tid * 8;
+  const T* z = static_cast<const T*>(a.logits) + int64_t(row) * a.ld;
+  // as they are stored, widened where they are used: half the registers for 16-bit types, which
+  // lets eight wavefronts share a SIMD instead of five
+  using Vec = Logits8<T>;
+  Vec raw[NV];
   if (base + kThreads * EPT <= a.v) {
 #pragma unroll
-    for (int j = 0; j < NV; ++j) load_some<T, 8>(z + at + j * kThreads * 8, 8, x[j]);
+    for (int j = 0; j < NV; ++j) raw[j].load(z + at + j * kThreads * 8);
   } else {
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int64_t c = at + int64_t(j) * kThreads * 8, cnt = a.v - c;
-      if (cnt >= 8) {
-        load_some<T, 8>(z + c, cnt, x[j]);
-      } else {
-#pragma unroll
-        for (int q = 0; q < 8; ++q) x[j][q] = q < cnt ? Elem<T>::to_f32(z[c + q]) : -INFINITY;
-      }
+      const int64_t c = at + int64_t(j) * kThreads * 8;
+      raw[j].load_some(z + c, a.v - c);
     }
   }
   float m = -INFINITY;
 #pragma unroll
-  for (int j = 0; j < NV; ++j)
+  for (int j = 0; j < NV; ++j) {
+    float x[8];
+    raw[j].get(x);
 #pragma unroll
-    for (int q = 0; q < 8; ++q) m = fmaxf(m, x[j][q]);
+    for (int q = 0; q < 8; ++q) m = fmaxf(m, x[q]);
+  }
   m += 0.f;  // one zero: -0 becomes +0
   const float mine = m;
   top[tid] = m;
   if (tid == 0) holders = count = 0;
-  // the sum about the thread's own maximum (a finite number), then merged
+  // The sum of exp(x - m) about the thread's own maximum m, each as 2^(x · L - c) with L = log2 e
+  // and c = m · L rounded: one operation instead of two. What the rounding of c makes of all terms
+  // alike is taken out of their sum, r = m · L - c being exact.
   float s = 0.f;
-  const float from = fmaxf(m, -3.4028234663852886e38f);
+  const bool any = m > -INFINITY;
+  if (__any(any && fabsf(m) > 0x1p126f)) {  // m · L may pass the largest number
+    const float from = any ? m : 0.f;
 #pragma unroll
-  for (int j = 0; j < NV; ++j)
+    for (int j = 0; j < NV; ++j) {
+      float x[8];
+      raw[j].get(x);
 #pragma unroll
-    for (int q = 0; q < 8; ++q) s += fast_exp2((x[j][q] - from) * kLog2e);
+      for (int q = 0; q < 8; ++q) s += fast_exp2((x[q] - from) * kLog2e);
+    }
+  } else {
+    const float from = any ? m : 0.f, c = from * kLog2e;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      float x[8];
+      raw[j].get(x);
+#pragma unroll
+      for (int q = 0; q < 8; ++q) s += fast_exp2(fmaf(x[q], kLog2e, -c));
+    }
+    s *= fast_exp2(-fmaf(from, kLog2e, -c));
+  }
   const bool bad = __any(!(s >= 0.f));  // a NaN or +inf: the sum says so, whatever it meets
-  wave_lse_reduce(m, s);
+  const float wm = wave_max(m);
+  s = wave_add(any ? s * fast_exp2((m - wm) * kLog2e) : 0.f);
   if (lane == 0) {
-    wave_m[wave] = m;
+    wave_m[wave] = wm;
     wave_s[wave] = bad ? NAN : s;
   }
   __syncthreads();
@@ -165,14 +231,14 @@ __global__ void __launch_bounds__(kThreads) beam_rows_kernel(RowsK a) {
     // no logit at or below minus infinity is a candidate
     if (lane == 0) limit = lim > ordered(-INFINITY) ? lim : ordered(-INFINITY) + 1;
   } else if (wave == 1 && lane == 0) {
-    float wm = wave_m[0], ws = wave_s[0];
-    bool nan = !(ws >= 0.f);
+    float gm = wave_m[0], gs = wave_s[0];
+    bool nan = !(gs >= 0.f);
 #pragma unroll
     for (int w = 1; w < kWaves; ++w) {
       nan |= !(wave_s[w] >= 0.f);
-      lse_merge(wm, ws, wave_m[w], wave_s[w]);
+      lse_merge(gm, gs, wave_m[w], wave_s[w]);
     }
-    a.sums[blockIdx.x] = float2{wm, nan ? NAN : ws};
+    a.sums[blockIdx.x] = float2{gm, nan ? NAN : gs};
   }
   __syncthreads();
   const float lim = from_ordered(limit);
@@ -181,9 +247,12 @@ __global__ void __launch_bounds__(kThreads) beam_rows_kernel(RowsK a) {
     if (p < kHolders) {
       from_thread[p] = tid;
 #pragma unroll
-      for (int j = 0; j < NV; ++j)
+      for (int j = 0; j < NV; ++j) {
+        float x[8];
+        raw[j].get(x);
 #pragma unroll
-        for (int q = 0; q < 8; ++q) held[p][j * 8 + q] = x[j][q];
+        for (int q = 0; q < 8; ++q) held[p][j * 8 + q] = x[q];
+      }
     }
   }
   __syncthreads();
@@ -218,13 +287,16 @@ __global__ void __launch_bounds__(kThreads) beam_rows_kernel(RowsK a) {
   for (int r = 0; r < a.num; ++r) {
     uint64_t k = 0;
 #pragma unroll
-    for (int j = 0; j < NV; ++j)
+    for (int j = 0; j < NV; ++j) {
+      float x[8];
+      raw[j].get(x);
 #pragma unroll
       for (int q = 0; q < 8; ++q)
-        if (x[j][q] > -INFINITY) {
-          const uint64_t e = key_of(x[j][q] + 0.f, uint32_t(at + j * kThreads * 8 + q));
+        if (x[q] > -INFINITY) {
+          const uint64_t e = key_of(x[q] + 0.f, uint32_t(at + j * kThreads * 8 + q));
           if (e < last && e > k) k = e;
         }
+    }
 #pragma unroll
     for (int off = 32; off >= 1; off >>= 1) {
       const uint64_t o = __shfl_xor((unsigned long long)k, off, 64);
@@ -560,7 +632,7 @@ hipError_t beam_step_run(const BeamStepArgs& a, hipStream_t s) {
   uint64_t* keys = static_cast<uint64_t*>(a.workspace);
   float2* sums = reinterpret_cast<float2*>(static_cast<char*>(a.workspace) +
                                            align256(size_t(rows * splits * a.num) * 8));
-  const RowsK k{a.logits, a.v, a.ldl, splits, int(a.num), keys, sums};
+  const RowsK k{a.logits, a.v, a.ldl, uint32_t(splits), int(a.num), keys, sums};
   hipError_t e;
   switch (a.dtype) {
     case kBF16: e = run_rows<Bf16>(k, rows, slice, s); break;
