@@ -49,25 +49,39 @@ typedef int v4i __attribute__((ext_vector_type(4)));
 // ------------------------------------------------------------------------------- quantiser
 
 // One scale per row: 16 lanes hold a block of 128 columns, 8 each; a workgroup holds 16 rows of
-// one block, so that neighbouring rows' scales are stored together.
+// up to kRowBlocks neighbouring blocks, so that neighbouring rows' scales are stored together and
+// a lane's loads are in flight together.
+constexpr int kRowBlocks = 2;
 template <class T, bool POW2>
 __global__ void __launch_bounds__(256) fp8_quantize_rows_kernel(
     const T* __restrict__ x, int64_t n, int64_t h, int64_t ldx, uint8_t* __restrict__ q,
     int64_t ldq, void* __restrict__ scales, int64_t lds, int64_t row_tiles) {
   const int64_t r = (blockIdx.x % row_tiles) * 16 + threadIdx.x / 16;
-  const int64_t b = blockIdx.x / row_tiles;
-  const int64_t c = b * kFp8Block + (threadIdx.x % 16) * 8;
-  const int64_t cnt = r < n ? h - c : 0;
-  float v[8];
-  load_some<T, 8>(x + r * ldx + c, cnt, v);
-  uint32_t top = 0;
+  const int64_t b0 = blockIdx.x / row_tiles * kRowBlocks;
+  const int64_t c0 = b0 * kFp8Block + (threadIdx.x % 16) * 8;
+  const T* from = x + (r < n ? r : 0) * ldx + c0;
+  float v[kRowBlocks][8];
+  if (r < n && c0 + (kRowBlocks - 1) * kFp8Block + 8 <= h) {
 #pragma unroll
-  for (int k = 0; k < 8; ++k) top = abs_bits(v[k]) > top ? abs_bits(v[k]) : top;
-  top = max_of_16<false>(top);
-  if (r >= n) return;
-  const BlockScale<POW2> s(top);
-  if (cnt > 0) store_fp8<POW2, 8>(q + r * ldq + c, s, v, 0, cnt < 8 ? int(cnt) : 8);
-  if (threadIdx.x % 16 == 0) s.store(scales, b * lds + r);
+    for (int k = 0; k < kRowBlocks; ++k) load_some<T, 8>(from + k * kFp8Block, 8, v[k]);
+  } else {
+#pragma unroll
+    for (int k = 0; k < kRowBlocks; ++k)
+      load_some<T, 8>(from + k * kFp8Block, r < n ? h - c0 - k * kFp8Block : 0, v[k]);
+  }
+#pragma unroll
+  for (int k = 0; k < kRowBlocks; ++k) {
+    uint32_t top = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) top = abs_bits(v[k][e]) > top ? abs_bits(v[k][e]) : top;
+    top = max_of_16<false>(top);
+    const int64_t cnt = h - c0 - k * kFp8Block;
+    if (r >= n || (b0 + k) * kFp8Block >= h) continue;
+    const BlockScale<POW2> s(top);
+    if (cnt > 0)
+      store_fp8<POW2, 8>(q + r * ldq + c0 + k * kFp8Block, s, v[k], 0, cnt < 8 ? int(cnt) : 8);
+    if (threadIdx.x % 16 == 0) s.store(scales, (b0 + k) * lds + r);
+  }
 }
 
 // One scale per 128 rows: a workgroup holds the block, 8 × 8 elements a lane.
@@ -112,9 +126,10 @@ hipError_t run_quantize(const Fp8QuantizeArgs& a, hipStream_t s) {
   const int64_t blocks = (a.h + kFp8Block - 1) / kFp8Block;
   const bool rows = a.block_rows == 1;
   const int64_t tiles = rows ? (a.n + 15) / 16 : (a.n + kFp8Block - 1) / kFp8Block;
+  const int64_t across = rows ? (blocks + kRowBlocks - 1) / kRowBlocks : blocks;
   TimedLaunch t(s, K_FP8_QUANTIZE);
   auto launch = [&](auto kernel) {
-    hipLaunchKernelGGL(kernel, dim3(unsigned(tiles * blocks)), dim3(256), 0, s,
+    hipLaunchKernelGGL(kernel, dim3(unsigned(tiles * across)), dim3(256), 0, s,
                        static_cast<const T*>(a.x), a.n, a.h, a.ldx, a.q, a.ldq, a.scales, a.lds,
                        tiles);
   };
@@ -520,15 +535,13 @@ __global__ void __launch_bounds__(256) fp8_join_kernel(const float* __restrict__
 
 // ------------------------------------------------------------------------------- few rows
 
-// Up to 16 · MT rows: bound by reading B once. A workgroup takes 16 · NT rows of B, its wavefronts
+// Up to 16 rows: bound by reading B once. A workgroup takes 16 · NT rows of B, its WAVES wavefronts
 // a part of the blocks each, straight from global memory into the MFMA's registers (16 rows of
 // whole 128-byte lines an instruction pair); their sums meet in LDS, in wavefront order.
-constexpr int kFewWaves = 4;
-
-template <int MT, int NT, bool E8M0, class T>
-__global__ void __launch_bounds__(64 * kFewWaves) fp8_few_kernel(MatmulK a) {
-  constexpr int SE = E8M0 ? 1 : 4;
-  __shared__ float red[kFewWaves - 1][MT * NT * 4][64];
+template <int NT, int WAVES, bool E8M0, class T>
+__global__ void __launch_bounds__(64 * WAVES) fp8_few_kernel(MatmulK a) {
+  constexpr int MT = 1, SE = E8M0 ? 1 : 4;
+  __shared__ float red[WAVES - 1][MT * NT * 4][64];
   const int lane = threadIdx.x & 63, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t n0 = int64_t(blockIdx.x) * (16 * NT);
@@ -562,7 +575,7 @@ __global__ void __launch_bounds__(64 * kFewWaves) fp8_few_kernel(MatmulK a) {
     return E8M0 ? uint32_t(*reinterpret_cast<const uint8_t*>(p))
                 : *reinterpret_cast<const uint32_t*>(p);
   };
-  for (int64_t b = wave; b < a.blocks; b += kFewWaves) {
+  for (int64_t b = wave; b < a.blocks; b += WAVES) {
     v8i fa[MT], fb[NT];
     uint32_t sa[MT];
     const uint32_t sb = scale(cb + b * SE);
@@ -607,7 +620,7 @@ __global__ void __launch_bounds__(64 * kFewWaves) fp8_few_kernel(MatmulK a) {
       for (int q = 0; q < 4; ++q) {
         x[q] = acc[i][j][q];
 #pragma unroll
-        for (int w = 0; w < kFewWaves - 1; ++w) x[q] += red[w][(i * NT + j) * 4 + q][lane];
+        for (int w = 0; w < WAVES - 1; ++w) x[q] += red[w][(i * NT + j) * 4 + q][lane];
         if (a.bias && q < cnt) x[q] += a.bias[gn + q];
       }
       const int64_t gm = 16 * i + (lane & 15);
@@ -620,11 +633,13 @@ __global__ void __launch_bounds__(64 * kFewWaves) fp8_few_kernel(MatmulK a) {
 
 using Wide = Cfg<256, 256, 2, 2, 4, 1>;
 using Small = Cfg<128, 128, 2, 2, 2, 2>;
+using Thin = Cfg<64, 128, 3, 2, 2, 2>;
 
-constexpr int64_t kFewRows = 64;
+constexpr int64_t kFewRows = 16, kThinRows = 64;
+constexpr int64_t kFewMany = 32768, kFewSome = 4096;
 
 struct Plan {
-  bool few, wide;
+  bool few, thin, wide;
   int64_t m_tiles, n_tiles, splits, per;
 };
 
@@ -635,6 +650,7 @@ Plan plan_of(int64_t m, int64_t n, int64_t k, bool precise) {
   p.splits = 1;
   p.per = blocks;
   if (p.few) return p;
+  p.thin = m <= kThinRows;
   // Rounds of tiles over the 256 CUs, one large or two small ones each: a round of small tiles
   // takes 0.52 (768 columns) to 0.59 (4096) of the time of a round of large ones, so the large ones
   // are for where they do not need that many rounds more (4096 x 4096 x 4096: 59 us and 70;
@@ -642,9 +658,9 @@ Plan plan_of(int64_t m, int64_t n, int64_t k, bool precise) {
   const int64_t large = (m + 255) / 256 * ((n + 255) / 256);
   const int64_t small = (m + 127) / 128 * ((n + 127) / 128);
   p.wide = !precise && large >= 256 && 100 * ((large + 255) / 256) < 58 * ((small + 511) / 512);
-  const int64_t bm = p.wide ? 256 : 128;
+  const int64_t bm = p.thin ? 64 : p.wide ? 256 : 128, bn = p.wide ? 256 : 128;
   p.m_tiles = (m + bm - 1) / bm;
-  p.n_tiles = (n + bm - 1) / bm;
+  p.n_tiles = (n + bn - 1) / bn;
   const int64_t tiles = p.m_tiles * p.n_tiles;
   if (!p.wide && tiles < 256) {  // K cut until two workgroups a CU are there, 4 blocks at least
     const int64_t want = std::min<int64_t>((512 + tiles - 1) / tiles, blocks / 4);
@@ -673,14 +689,16 @@ hipError_t run_matmul(const Fp8MatmulArgs& a, hipStream_t s) {
             a.ldo,  a.out,  (a.k + kFp8Block - 1) / kFp8Block, p.per, TileMap{}};
   if (p.few) {
     TimedLaunch t(s, K_FP8_MATMUL_FEW);
-    const dim3 block(64 * kFewWaves);
-    auto grid = [&](int nt) { return dim3(unsigned((a.n + 16 * nt - 1) / (16 * nt))); };
-    if (a.m <= 16)
-      hipLaunchKernelGGL((fp8_few_kernel<1, 2, E8M0, T>), grid(2), block, 0, s, k);
-    else if (a.m <= 32)
-      hipLaunchKernelGGL((fp8_few_kernel<2, 2, E8M0, T>), grid(2), block, 0, s, k);
+    auto launch = [&](auto kernel, int nt, int waves) {
+      hipLaunchKernelGGL(kernel, dim3(unsigned((a.n + 16 * nt - 1) / (16 * nt))), dim3(64 * waves),
+                         0, s, k);
+    };
+    if (a.n > kFewMany)
+      launch(fp8_few_kernel<4, 4, E8M0, T>, 4, 4);
+    else if (a.n > kFewSome)
+      launch(fp8_few_kernel<2, 8, E8M0, T>, 2, 8);
     else
-      hipLaunchKernelGGL((fp8_few_kernel<4, 2, E8M0, T>), grid(2), block, 0, s, k);
+      launch(fp8_few_kernel<1, 16, E8M0, T>, 1, 16);
     return hipGetLastError();
   }
   k.tm = TileMap{p.m_tiles, p.n_tiles, p.splits, true};
@@ -690,11 +708,14 @@ hipError_t run_matmul(const Fp8MatmulArgs& a, hipStream_t s) {
       return launch_tiles<Wide, E8M0, false, T>(k, p, s);
     }
   }
-  if (p.splits == 1) return launch_tiles<Small, E8M0, kPrecise, T>(k, p, s);
+  if (p.splits == 1)
+    return p.thin ? launch_tiles<Thin, E8M0, true, T>(k, p, s)
+                  : launch_tiles<Small, E8M0, kPrecise, T>(k, p, s);
   k.out = a.workspace;
   k.ldo = a.n;
   k.bias = nullptr;
-  const hipError_t e = launch_tiles<Small, E8M0, kPrecise, float>(k, p, s);
+  const hipError_t e = p.thin ? launch_tiles<Thin, E8M0, true, float>(k, p, s)
+                              : launch_tiles<Small, E8M0, kPrecise, float>(k, p, s);
   if (e != hipSuccess) return e;
   const int64_t threads = a.m * ((a.n + 3) / 4);
   TimedLaunch t(s, K_FP8_JOIN);
