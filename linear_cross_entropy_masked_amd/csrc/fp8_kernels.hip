@@ -270,59 +270,59 @@ __device__ __forceinline__ void store4(T* p, const float (&x)[4], int cnt) {
   }
 }
 
-template <class C, bool E8M0, bool PRECISE, class T>
-__global__ void __launch_bounds__(C::THREADS, C::OCC) fp8_matmul_kernel(MatmulK a) {
-  __shared__ __attribute__((aligned(1024))) char lds[C::StageBytes * C::STAGES];
-  constexpr int TM = C::TM, TN = C::TN, SE = E8M0 ? 1 : 4;
-  TileCoord tc;
-  if (!gemm::v2::tile_coord(a.tm, blockIdx.x, tc)) return;
-  const int64_t m0 = tc.mt * C::BM, n0 = tc.nt * C::BN;
-  const int64_t b0 = tc.kz * a.per;
-  const int nk = int(std::min(a.per, a.blocks - b0));
-  const int lane = threadIdx.x & 63;
-  const uint32_t wave = __builtin_amdgcn_readfirstlane(uint32_t(threadIdx.x >> 6));
-  const int wm = wave / C::WN, wn = wave % C::WN;
+// The loads of a tile's slices: windows over A's and B's rows and their scales, moved on by a
+// block of columns with each slice.
+template <class C, bool E8M0>
+struct Feed {
+  static constexpr int SE = E8M0 ? 1 : 4;
+  int64_t pa, pb, ps;                           // where the next slice starts
+  int64_t left_a, left_b, left_s, left_k;       // bytes up to the end of the last row; columns
+  int64_t step_s, less_s;
+  uint32_t lds0, wave, at, off_a, off_b, off_s, step_a, step_b, to_s;
 
-  // A load takes 8 rows of eight 16-byte chunks: a lane's byte offset in the window of rows of the
-  // first of its wavefront's loads, and the column it starts at, the same in all of them.
-  const uint32_t at = 16 * ((lane % 8) ^ (lane / 8));
-  const uint32_t off_a = uint32_t((8 * C::PA * wave + lane / 8) * a.lda) + at;
-  const uint32_t off_b = uint32_t((8 * C::PB * wave + lane / 8) * a.ldb) + at;
-  const uint32_t step_a = uint32_t(8 * a.lda), step_b = uint32_t(8 * a.ldb);
-  const uint32_t lds0 =
-      uint32_t(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) char*)lds));
-  // the window of a slice: its address and the bytes up to the end of the last row
-  int64_t pa = uniform(reinterpret_cast<int64_t>(a.a) + m0 * a.lda + b0 * kFp8Block);
-  int64_t pb = uniform(reinterpret_cast<int64_t>(a.b) + n0 * a.ldb + b0 * kFp8Block);
-  int64_t left_a = uniform((a.m - 1 - m0) * a.lda + a.k - b0 * kFp8Block);
-  int64_t left_b = uniform((a.n - 1 - n0) * a.ldb + a.k - b0 * kFp8Block);
-  int64_t left_k = uniform(a.k - b0 * kFp8Block);  // columns that exist
-  // scales: wavefronts 0 .. BM / 64 - 1 take the rows' of A, the others the column blocks' of B
-  int64_t ps, left_s, step_s, less_s;
-  uint32_t off_s, to_s;
-  if (wave < C::BM / 64) {
-    ps = reinterpret_cast<int64_t>(a.ca) + (b0 * a.ldca + m0) * SE;
-    left_s = (a.m - m0) * SE;
-    step_s = a.ldca * SE;
-    less_s = 0;
-    off_s = (64 * wave + lane) * SE;
-    to_s = C::ABytes + C::BBytes + 256 * wave;
-  } else {
-    const int64_t nb = n0 / kFp8Block, last = (a.n - 1) / kFp8Block;
-    ps = reinterpret_cast<int64_t>(a.cb) + (nb * a.ldcb + b0) * SE;
-    left_s = ((last - nb) * a.ldcb + a.blocks - b0) * SE;
-    step_s = less_s = SE;
-    off_s = lane < C::BN / 128 ? uint32_t(lane * a.ldcb * SE) : kPast;
-    to_s = C::ABytes + C::BBytes + 4 * C::BM;
+  __device__ __forceinline__ Feed(const MatmulK& a, const char* lds, uint32_t wave_) : wave(wave_) {
+    const int lane = threadIdx.x & 63;
+    lds0 = uint32_t(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) char*)lds));
+    // A load takes 8 rows of eight 16-byte chunks: a lane's byte offset in the window of rows of
+    // the first of its wavefront's loads, and the column it starts at, the same in all of them.
+    at = 16 * ((lane % 8) ^ (lane / 8));
+    off_a = uint32_t((8 * C::PA * wave + lane / 8) * a.lda) + at;
+    off_b = uint32_t((8 * C::PB * wave + lane / 8) * a.ldb) + at;
+    step_a = uint32_t(8 * a.lda);
+    step_b = uint32_t(8 * a.ldb);
+    // scales: wavefronts 0 .. BM / 64 - 1 take the rows' of A, the others the column blocks' of B
+    if (of_a()) {
+      off_s = (64 * wave + lane) * SE;
+      to_s = C::ABytes + C::BBytes + 256 * wave;
+      step_s = a.ldca * SE;
+      less_s = 0;
+    } else {
+      off_s = lane < C::BN / 128 ? uint32_t(lane * a.ldcb * SE) : kPast;
+      to_s = C::ABytes + C::BBytes + 4 * C::BM;
+      step_s = less_s = SE;
+    }
+    to_s = __builtin_amdgcn_readfirstlane(to_s);
+    step_s = uniform(step_s);
+    less_s = uniform(less_s);
   }
-  ps = uniform(ps);
-  left_s = uniform(left_s);
-  step_s = uniform(step_s);
-  less_s = uniform(less_s);
-  to_s = __builtin_amdgcn_readfirstlane(to_s);
-  int issued = 0, wslot = 0;
-  auto issue = [&]() {
-    const uint32_t o = lds0 + uint32_t(wslot * C::StageBytes);
+  __device__ __forceinline__ bool of_a() const { return wave < C::BM / 64; }
+
+  // To block b0 of the tile at (m0, n0).
+  __device__ __forceinline__ void start(const MatmulK& a, int64_t m0, int64_t n0, int64_t b0) {
+    pa = uniform(reinterpret_cast<int64_t>(a.a) + m0 * a.lda + b0 * kFp8Block);
+    pb = uniform(reinterpret_cast<int64_t>(a.b) + n0 * a.ldb + b0 * kFp8Block);
+    left_a = uniform((a.m - 1 - m0) * a.lda + a.k - b0 * kFp8Block);
+    left_b = uniform((a.n - 1 - n0) * a.ldb + a.k - b0 * kFp8Block);
+    left_k = uniform(a.k - b0 * kFp8Block);
+    const int64_t nb = n0 / kFp8Block, last = (a.n - 1) / kFp8Block;
+    ps = uniform(of_a() ? reinterpret_cast<int64_t>(a.ca) + (b0 * a.ldca + m0) * SE
+                        : reinterpret_cast<int64_t>(a.cb) + (nb * a.ldcb + b0) * SE);
+    left_s = uniform(of_a() ? (a.m - m0) * SE : ((last - nb) * a.ldcb + a.blocks - b0) * SE);
+  }
+
+  // The next slice into a slot of the ring.
+  __device__ __forceinline__ void issue(uint32_t slot) {
+    const uint32_t o = lds0 + slot * C::StageBytes;
     const i32x4_t ra = rsrc(pa, left_a), rb = rsrc(pb, left_b), rs = rsrc(ps, left_s);
     // chunks behind the last column read as zero
     const uint32_t past = int64_t(at) < left_k ? 0u : kPast;
@@ -340,16 +340,205 @@ __global__ void __launch_bounds__(C::THREADS, C::OCC) fp8_matmul_kernel(MatmulK 
     left_b -= kFp8Block;
     left_k -= kFp8Block;
     left_s -= less_s;
+  }
+};
+
+// A slice's products, added to the sums.
+template <class C, bool E8M0, bool PRECISE>
+__device__ __forceinline__ void multiply(const char* st, int wm, int wn, int lane,
+                                         f32x4_t (&acc)[C::TM][C::TN]) {
+  constexpr int TM = C::TM, TN = C::TN;
+      const char* sc = st + C::ABytes + C::BBytes;
+      // a fragment: chunks g and g + 4 of a row, g = lane / 16, where the row's swizzle put them
+      const char* fr = st + (lane & 15) * 128 + (((lane >> 4) ^ (lane & 7)) << 4);
+      const char* fr4 = st + (lane & 15) * 128 + (((lane >> 4) ^ 4 ^ (lane & 7)) << 4);
+      auto frag = [&](int row) {  // of the slice's rows, B's behind A's; a multiple of 16
+        const v4i lo = *reinterpret_cast<const v4i*>(fr + row * 128);
+        const v4i hi = *reinterpret_cast<const v4i*>(fr4 + row * 128);
+        return v8i{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+      };
+      const int ra = wm * (C::BM / C::WM), rb = C::BM + wn * (C::BN / C::WN);
+      auto scale_of = [&](int i) {
+        return *reinterpret_cast<const uint32_t*>(sc + 4 * (ra + 16 * i + (lane & 15)));
+      };
+      const uint32_t sb =
+          *reinterpret_cast<const uint32_t*>(sc + 4 * C::BM + 4 * (wn * (C::BN / C::WN) / 128));
+      v8i fb[TN];
+  #pragma unroll
+      for (int j = 0; j < TN; ++j) fb[j] = frag(rb + 16 * j);
+      if constexpr (PRECISE) {
+        v8i fa[TM];
+        uint32_t sa[TM];
+  #pragma unroll
+        for (int i = 0; i < TM; ++i) {
+          fa[i] = frag(ra + 16 * i);
+          sa[i] = scale_of(i);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        const float cb = scale_value<E8M0>(sb);
+        Wide32 wb[TN];
+  #pragma unroll
+        for (int j = 0; j < TN; ++j) wb[j] = widen(fb[j]);
+  #pragma unroll
+        for (int i = 0; i < TM; ++i) {
+          const Wide32 wa = widen(fa[i]);
+          const float s = scale_value<E8M0>(sa[i]) * cb;
+  #pragma unroll
+          for (int j = 0; j < TN; ++j) add_scaled(acc[i][j], block_sums(wb[j], wa), s);
+        }
+      } else {
+        // the fragments of AHEAD rows of tiles are in flight or at work at a time
+        constexpr int AHEAD = TM < 4 ? TM : 4;
+        v8i fa[AHEAD];
+        uint32_t sa[AHEAD];
+  #pragma unroll
+        for (int i = 0; i < AHEAD; ++i) {
+          fa[i] = frag(ra + 16 * i);
+          sa[i] = scale_of(i);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        // fp32 scales: a tile's sums are added LAG tiles later, when they have left the pipeline
+        constexpr int LAG = 2;
+        f32x4_t t[LAG + 1];
+        float s[2];
+        auto add = [&](int n) {
+          if (!E8M0 && n >= 0)
+            add_scaled(acc[n / TN][n % TN], t[n % (LAG + 1)], s[n / TN % 2]);
+        };
+  #pragma unroll
+        for (int i = 0; i < TM; ++i) {
+          const v8i x = fa[i % AHEAD];
+          const uint32_t sx = sa[i % AHEAD];
+          s[i % 2] = __uint_as_float(sx) * __uint_as_float(sb);
+  #pragma unroll
+          for (int j = 0; j < TN; ++j) {
+            if constexpr (E8M0) {
+              acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                  fb[j], x, acc[i][j], 0, 0, 0, int(sb), 0, int(sx));
+            } else {
+              t[(i * TN + j) % (LAG + 1)] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                  fb[j], x, f32x4_t{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 127, 0, 127);
+              __builtin_amdgcn_sched_barrier(0);
+              add(i * TN + j - LAG);
+            }
+          }
+          if (i + AHEAD < TM) {
+            fa[i % AHEAD] = frag(ra + 16 * (i + AHEAD));
+            sa[i % AHEAD] = scale_of(i + AHEAD);
+            __builtin_amdgcn_sched_barrier(0);
+          }
+        }
+  #pragma unroll
+        for (int n = TM * TN - LAG; n < TM * TN; ++n) add(n);
+      }
+}
+
+// A wavefront's sums to memory. A lane owns 4 consecutive columns of a row, of which 16 rows would
+// make a store of 32-byte pieces: the sums go through LDS (`tile`, the wavefront's own part of the
+// ring, with the same swizzle) and leave as rows of whole lines (8192 x 4096 x 128256: 40 us a
+// tile of 256 x 256 for pieces, 12 so).
+template <class C, class T>
+__device__ __forceinline__ void store_tile(const MatmulK& a, char* tile, int64_t mw, int64_t nw,
+                                           int64_t kz, int lane,
+                                           const f32x4_t (&acc)[C::TM][C::TN]) {
+  constexpr int TN = C::TN, RowBytes = (C::BN / C::WN) * int(sizeof(T)), Rows = 16 * C::TM;
+  constexpr int Chunks = RowBytes / 16, PerStore = 64 / Chunks, VE = 16 / int(sizeof(T));
+  const int g4 = 4 * (lane >> 4);
+#pragma unroll
+  for (int i = 0; i < C::TM; ++i) {
+    const int r = 16 * i + (lane & 15);
+#pragma unroll
+    for (int j = 0; j < TN; ++j) {
+      const int byte = (16 * j + g4) * int(sizeof(T));
+      const float x[4] = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
+      store4(reinterpret_cast<T*>(tile + r * RowBytes + (((byte >> 4) ^ (lane & 7)) << 4) +
+                                  (byte & 15)),
+             x, 4);
+    }
+  }
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  const int chunk = lane % Chunks, rr = lane / Chunks;
+  const int64_t gn = nw + chunk * VE, cnt = a.n - gn;
+  T* out = static_cast<T*>(a.out) + (kz * a.m + mw + rr) * a.ldo + gn;
+  if (mw + Rows <= a.m && nw + C::BN / C::WN <= a.n) {
+#pragma unroll 4
+    for (int s = 0; s < Rows / PerStore; ++s) {
+      const int r = s * PerStore + rr;
+      store_raw(out, *reinterpret_cast<const raw4*>(tile + r * RowBytes + ((chunk ^ (r & 7)) << 4)));
+      out += PerStore * a.ldo;
+    }
+  } else {
+    for (int s = 0; s < Rows / PerStore; ++s) {
+      const int r = s * PerStore + rr;
+      if (mw + r < a.m && cnt > 0) {
+        const raw4 v =
+            *reinterpret_cast<const raw4*>(tile + r * RowBytes + ((chunk ^ (r & 7)) << 4));
+        if (cnt >= VE) {
+          store_raw(out, v);
+        } else {
+#pragma unroll
+          for (int k = 0; k < VE; ++k)
+            if (k < cnt) {
+              const uint32_t w = v[k * int(sizeof(T)) / 4] >> (8 * (k * int(sizeof(T)) % 4));
+              if constexpr (sizeof(T) == 4)
+                reinterpret_cast<uint32_t*>(out)[k] = w;
+              else
+                reinterpret_cast<uint16_t*>(out)[k] = uint16_t(w);
+            }
+        }
+      }
+      out += PerStore * a.ldo;
+    }
+  }
+}
+
+template <class C>
+__device__ __forceinline__ void add_bias(const MatmulK& a, int64_t nw, int lane,
+                                         f32x4_t (&acc)[C::TM][C::TN]) {
+  if (!a.bias) return;
+#pragma unroll
+  for (int j = 0; j < C::TN; ++j)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int64_t gn = nw + 16 * j + 4 * (lane >> 4) + q;
+      const float x = gn < a.n ? a.bias[gn] : 0.f;
+#pragma unroll
+      for (int i = 0; i < C::TM; ++i) acc[i][j][q] += x;
+    }
+}
+
+template <class C>
+__device__ __forceinline__ void clear(f32x4_t (&acc)[C::TM][C::TN]) {
+#pragma unroll
+  for (int i = 0; i < C::TM; ++i)
+#pragma unroll
+    for (int j = 0; j < C::TN; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+}
+
+// A workgroup per tile (and range of blocks).
+template <class C, bool E8M0, bool PRECISE, class T>
+__global__ void __launch_bounds__(C::THREADS, C::OCC) fp8_matmul_kernel(MatmulK a) {
+  __shared__ __attribute__((aligned(1024))) char lds[C::StageBytes * C::STAGES];
+  TileCoord tc;
+  if (!gemm::v2::tile_coord(a.tm, blockIdx.x, tc)) return;
+  const int64_t m0 = tc.mt * C::BM, n0 = tc.nt * C::BN;
+  const int64_t b0 = tc.kz * a.per;
+  const int nk = int(std::min(a.per, a.blocks - b0));
+  const int lane = threadIdx.x & 63;
+  const uint32_t wave = __builtin_amdgcn_readfirstlane(uint32_t(threadIdx.x >> 6));
+  const int wm = wave / C::WN, wn = wave % C::WN;
+  Feed<C, E8M0> feed(a, lds, wave);
+  feed.start(a, m0, n0, b0);
+  f32x4_t acc[C::TM][C::TN];
+  clear<C>(acc);
+  int issued = 0;
+  uint32_t wslot = 0;
+  auto issue = [&]() {
+    feed.issue(wslot);
     wslot = wslot + 1 == C::STAGES ? 0 : wslot + 1;
     ++issued;
   };
-
-  f32x4_t acc[TM][TN];
-#pragma unroll
-  for (int i = 0; i < TM; ++i)
-#pragma unroll
-    for (int j = 0; j < TN; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-
 #pragma unroll
   for (int s = 0; s < C::STAGES - 1; ++s)
     if (s < nk) issue();
@@ -359,150 +548,15 @@ __global__ void __launch_bounds__(C::THREADS, C::OCC) fp8_matmul_kernel(MatmulK 
     wait_slices<C::PER, C::STAGES - 2>(issued - 1 - kt);
     __builtin_amdgcn_s_barrier();
     if (kt + C::STAGES - 1 < nk) issue();
-    const char* st = lds + rslot * C::StageBytes;
+    multiply<C, E8M0, PRECISE>(lds + rslot * C::StageBytes, wm, wn, lane, acc);
     rslot = rslot + 1 == C::STAGES ? 0 : rslot + 1;
-    const char* sc = st + C::ABytes + C::BBytes;
-    // a fragment: chunks g and g + 4 of a row, g = lane / 16, where the row's swizzle put them
-    const char* fr = st + (lane & 15) * 128 + (((lane >> 4) ^ (lane & 7)) << 4);
-    const char* fr4 = st + (lane & 15) * 128 + (((lane >> 4) ^ 4 ^ (lane & 7)) << 4);
-    auto frag = [&](int row) {  // of the slice's rows, B's behind A's; a multiple of 16
-      const v4i lo = *reinterpret_cast<const v4i*>(fr + row * 128);
-      const v4i hi = *reinterpret_cast<const v4i*>(fr4 + row * 128);
-      return v8i{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-    };
-    const int ra = wm * (C::BM / C::WM), rb = C::BM + wn * (C::BN / C::WN);
-    auto scale_of = [&](int i) {
-      return *reinterpret_cast<const uint32_t*>(sc + 4 * (ra + 16 * i + (lane & 15)));
-    };
-    const uint32_t sb =
-        *reinterpret_cast<const uint32_t*>(sc + 4 * C::BM + 4 * (wn * (C::BN / C::WN) / 128));
-    v8i fb[TN];
-#pragma unroll
-    for (int j = 0; j < TN; ++j) fb[j] = frag(rb + 16 * j);
-    if constexpr (PRECISE) {
-      v8i fa[TM];
-      uint32_t sa[TM];
-#pragma unroll
-      for (int i = 0; i < TM; ++i) {
-        fa[i] = frag(ra + 16 * i);
-        sa[i] = scale_of(i);
-      }
-      __builtin_amdgcn_sched_barrier(0);
-      const float cb = scale_value<E8M0>(sb);
-      Wide32 wb[TN];
-#pragma unroll
-      for (int j = 0; j < TN; ++j) wb[j] = widen(fb[j]);
-#pragma unroll
-      for (int i = 0; i < TM; ++i) {
-        const Wide32 wa = widen(fa[i]);
-        const float s = scale_value<E8M0>(sa[i]) * cb;
-#pragma unroll
-        for (int j = 0; j < TN; ++j) add_scaled(acc[i][j], block_sums(wb[j], wa), s);
-      }
-    } else {
-      // the fragments of AHEAD rows of tiles are in flight or at work at a time
-      constexpr int AHEAD = TM < 4 ? TM : 4;
-      v8i fa[AHEAD];
-      uint32_t sa[AHEAD];
-#pragma unroll
-      for (int i = 0; i < AHEAD; ++i) {
-        fa[i] = frag(ra + 16 * i);
-        sa[i] = scale_of(i);
-      }
-      __builtin_amdgcn_sched_barrier(0);
-      // fp32 scales: a tile's sums are added LAG tiles later, when they have left the pipeline
-      constexpr int LAG = 2;
-      f32x4_t t[LAG + 1];
-      float s[2];
-      auto add = [&](int n) {
-        if (!E8M0 && n >= 0)
-          add_scaled(acc[n / TN][n % TN], t[n % (LAG + 1)], s[n / TN % 2]);
-      };
-#pragma unroll
-      for (int i = 0; i < TM; ++i) {
-        const v8i x = fa[i % AHEAD];
-        const uint32_t sx = sa[i % AHEAD];
-        s[i % 2] = __uint_as_float(sx) * __uint_as_float(sb);
-#pragma unroll
-        for (int j = 0; j < TN; ++j) {
-          if constexpr (E8M0) {
-            acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                fb[j], x, acc[i][j], 0, 0, 0, int(sb), 0, int(sx));
-          } else {
-            t[(i * TN + j) % (LAG + 1)] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                fb[j], x, f32x4_t{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 127, 0, 127);
-            __builtin_amdgcn_sched_barrier(0);
-            add(i * TN + j - LAG);
-          }
-        }
-        if (i + AHEAD < TM) {
-          fa[i % AHEAD] = frag(ra + 16 * (i + AHEAD));
-          sa[i % AHEAD] = scale_of(i + AHEAD);
-          __builtin_amdgcn_sched_barrier(0);
-        }
-      }
-#pragma unroll
-      for (int n = TM * TN - LAG; n < TM * TN; ++n) add(n);
-    }
   }
-
-  // Epilogue. A lane owns 4 consecutive columns of a row, of which 16 rows would make a store of
-  // 32-byte pieces: the wavefront's sums go through LDS (its own part of the ring, the same
-  // swizzle) and leave as rows of whole lines.
-  constexpr int RowBytes = (C::BN / C::WN) * int(sizeof(T)), Rows = C::BM / C::WM;
-  constexpr int Chunks = RowBytes / 16, PerStore = 64 / Chunks, VE = 16 / int(sizeof(T));
-  static_assert(C::NW * Rows * RowBytes <= C::StageBytes * C::STAGES, "the ring holds the tile");
+  constexpr int Rows = C::BM / C::WM, WaveBytes = Rows * (C::BN / C::WN) * int(sizeof(T));
+  static_assert(C::NW * WaveBytes <= C::StageBytes * C::STAGES, "the ring holds the tile");
   const int64_t nw = n0 + wn * (C::BN / C::WN), mw = m0 + wm * Rows;
-  const int g4 = 4 * (lane >> 4);
-  float bias[TN][4];
-#pragma unroll
-  for (int j = 0; j < TN; ++j)
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const int64_t gn = nw + 16 * j + g4 + q;
-      bias[j][q] = a.bias && gn < a.n ? a.bias[gn] : 0.f;
-    }
+  add_bias<C>(a, nw, lane, acc);
   __syncthreads();  // the ring has been read
-  char* tile = lds + wave * (Rows * RowBytes);
-#pragma unroll
-  for (int i = 0; i < TM; ++i) {
-    const int r = 16 * i + (lane & 15);
-#pragma unroll
-    for (int j = 0; j < TN; ++j) {
-      const int byte = (16 * j + g4) * int(sizeof(T));
-      float x[4];
-#pragma unroll
-      for (int q = 0; q < 4; ++q) x[q] = acc[i][j][q] + bias[j][q];
-      store4(reinterpret_cast<T*>(tile + r * RowBytes +
-                                  (((byte >> 4) ^ (lane & 7)) << 4) + (byte & 15)), x, 4);
-    }
-  }
-  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-  __builtin_amdgcn_wave_barrier();
-  const int chunk = lane % Chunks, rr = lane / Chunks;
-  const int64_t gn = nw + chunk * VE, cnt = a.n - gn;
-  T* out = static_cast<T*>(a.out) + (tc.kz * a.m + mw + rr) * a.ldo + gn;
-#pragma unroll 4
-  for (int s = 0; s < Rows / PerStore; ++s) {
-    const int r = s * PerStore + rr;
-    if (mw + r < a.m && cnt > 0) {
-      const raw4 v = *reinterpret_cast<const raw4*>(tile + r * RowBytes + ((chunk ^ (r & 7)) << 4));
-      if (cnt >= VE) {
-        store_raw(out, v);
-      } else {
-#pragma unroll
-        for (int k = 0; k < VE; ++k)
-          if (k < cnt) {
-            const uint32_t w = v[k * int(sizeof(T)) / 4] >> (8 * (k * int(sizeof(T)) % 4));
-            if constexpr (sizeof(T) == 4)
-              reinterpret_cast<uint32_t*>(out)[k] = w;
-            else
-              reinterpret_cast<uint16_t*>(out)[k] = uint16_t(w);
-          }
-      }
-    }
-    out += PerStore * a.ldo;
-  }
+  store_tile<C, T>(a, lds + wave * WaveBytes, mw, nw, tc.kz, lane, acc);
 }
 
 // Sums of the K ranges in their order, bias and the rounding.
