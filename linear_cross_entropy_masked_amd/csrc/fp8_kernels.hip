@@ -348,89 +348,102 @@ template <class C, bool E8M0, bool PRECISE>
 __device__ __forceinline__ void multiply(const char* st, int wm, int wn, int lane,
                                          f32x4_t (&acc)[C::TM][C::TN]) {
   constexpr int TM = C::TM, TN = C::TN;
-      const char* sc = st + C::ABytes + C::BBytes;
-      // a fragment: chunks g and g + 4 of a row, g = lane / 16, where the row's swizzle put them
-      const char* fr = st + (lane & 15) * 128 + (((lane >> 4) ^ (lane & 7)) << 4);
-      const char* fr4 = st + (lane & 15) * 128 + (((lane >> 4) ^ 4 ^ (lane & 7)) << 4);
-      auto frag = [&](int row) {  // of the slice's rows, B's behind A's; a multiple of 16
-        const v4i lo = *reinterpret_cast<const v4i*>(fr + row * 128);
-        const v4i hi = *reinterpret_cast<const v4i*>(fr4 + row * 128);
-        return v8i{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-      };
-      const int ra = wm * (C::BM / C::WM), rb = C::BM + wn * (C::BN / C::WN);
-      auto scale_of = [&](int i) {
-        return *reinterpret_cast<const uint32_t*>(sc + 4 * (ra + 16 * i + (lane & 15)));
-      };
-      const uint32_t sb =
-          *reinterpret_cast<const uint32_t*>(sc + 4 * C::BM + 4 * (wn * (C::BN / C::WN) / 128));
-      v8i fb[TN];
-  #pragma unroll
-      for (int j = 0; j < TN; ++j) fb[j] = frag(rb + 16 * j);
-      if constexpr (PRECISE) {
-        v8i fa[TM];
-        uint32_t sa[TM];
-  #pragma unroll
-        for (int i = 0; i < TM; ++i) {
-          fa[i] = frag(ra + 16 * i);
-          sa[i] = scale_of(i);
+  const char* sc = st + C::ABytes + C::BBytes;
+  // a fragment: chunks g and g + 4 of a row, g = lane / 16, where the row's swizzle put them
+  const char* fr = st + (lane & 15) * 128 + (((lane >> 4) ^ (lane & 7)) << 4);
+  const char* fr4 = st + (lane & 15) * 128 + (((lane >> 4) ^ 4 ^ (lane & 7)) << 4);
+  auto frag = [&](int row) {  // of the slice's rows, B's behind A's; a multiple of 16
+    const v4i lo = *reinterpret_cast<const v4i*>(fr + row * 128);
+    const v4i hi = *reinterpret_cast<const v4i*>(fr4 + row * 128);
+    return v8i{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+  };
+  const int ra = wm * (C::BM / C::WM), rb = C::BM + wn * (C::BN / C::WN);
+  auto scale_of = [&](int i) {
+    return *reinterpret_cast<const uint32_t*>(sc + 4 * (ra + 16 * i + (lane & 15)));
+  };
+  const uint32_t sb =
+      *reinterpret_cast<const uint32_t*>(sc + 4 * C::BM + 4 * (wn * (C::BN / C::WN) / 128));
+  v8i fb[TN];
+#pragma unroll
+  for (int j = 0; j < TN; ++j) fb[j] = frag(rb + 16 * j);
+  if constexpr (PRECISE) {
+    v8i fa[TM];
+    uint32_t sa[TM];
+#pragma unroll
+    for (int i = 0; i < TM; ++i) {
+      fa[i] = frag(ra + 16 * i);
+      sa[i] = scale_of(i);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    const float cb = scale_value<E8M0>(sb);
+    Wide32 wb[TN];
+#pragma unroll
+    for (int j = 0; j < TN; ++j) wb[j] = widen(fb[j]);
+    // the tiles of a row side by side, so that no MFMA waits for the one before it
+#pragma unroll
+    for (int i = 0; i < TM; ++i) {
+      const Wide32 wa = widen(fa[i]);
+      const float s = scale_value<E8M0>(sa[i]) * cb;
+      f32x4_t t[TN];
+#pragma unroll
+      for (int j = 0; j < TN; ++j) t[j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int p = 0; p < 4; ++p)
+#pragma unroll
+        for (int j = 0; j < TN; ++j)
+          t[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wb[j].part[p], wa.part[p], t[j], 0, 0, 0);
+#pragma unroll
+      for (int j = 0; j < TN; ++j) add_scaled(acc[i][j], t[j], s);
+    }
+  } else {
+    // the fragments of AHEAD rows of tiles are in flight or at work at a time
+    constexpr int AHEAD = TM < 4 ? TM : 4;
+    v8i fa[AHEAD];
+    uint32_t sa[AHEAD];
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) {
+      fa[i] = frag(ra + 16 * i);
+      sa[i] = scale_of(i);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    // two workgroups share the CU: the one that multiplies goes first (2048 x 4096 x 4096 with fp32
+    // scales 39.7 us and 37.9; alone on its CU a workgroup gains nothing)
+    if (C::OCC > 1) __builtin_amdgcn_s_setprio(1);
+    // fp32 scales: a tile's sums are added LAG tiles later, when they have left the pipeline
+    constexpr int LAG = 2;
+    f32x4_t t[LAG + 1];
+    float s[2];
+    auto add = [&](int n) {
+      if (!E8M0 && n >= 0)
+        add_scaled(acc[n / TN][n % TN], t[n % (LAG + 1)], s[n / TN % 2]);
+    };
+#pragma unroll
+    for (int i = 0; i < TM; ++i) {
+      const v8i x = fa[i % AHEAD];
+      const uint32_t sx = sa[i % AHEAD];
+      s[i % 2] = __uint_as_float(sx) * __uint_as_float(sb);
+#pragma unroll
+      for (int j = 0; j < TN; ++j) {
+        if constexpr (E8M0) {
+          acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+              fb[j], x, acc[i][j], 0, 0, 0, int(sb), 0, int(sx));
+        } else {
+          t[(i * TN + j) % (LAG + 1)] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+              fb[j], x, f32x4_t{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 127, 0, 127);
+          __builtin_amdgcn_sched_barrier(0);
+          add(i * TN + j - LAG);
         }
-        __builtin_amdgcn_sched_barrier(0);
-        const float cb = scale_value<E8M0>(sb);
-        Wide32 wb[TN];
-  #pragma unroll
-        for (int j = 0; j < TN; ++j) wb[j] = widen(fb[j]);
-  #pragma unroll
-        for (int i = 0; i < TM; ++i) {
-          const Wide32 wa = widen(fa[i]);
-          const float s = scale_value<E8M0>(sa[i]) * cb;
-  #pragma unroll
-          for (int j = 0; j < TN; ++j) add_scaled(acc[i][j], block_sums(wb[j], wa), s);
-        }
-      } else {
-        // the fragments of AHEAD rows of tiles are in flight or at work at a time
-        constexpr int AHEAD = TM < 4 ? TM : 4;
-        v8i fa[AHEAD];
-        uint32_t sa[AHEAD];
-  #pragma unroll
-        for (int i = 0; i < AHEAD; ++i) {
-          fa[i] = frag(ra + 16 * i);
-          sa[i] = scale_of(i);
-        }
-        __builtin_amdgcn_sched_barrier(0);
-        // fp32 scales: a tile's sums are added LAG tiles later, when they have left the pipeline
-        constexpr int LAG = 2;
-        f32x4_t t[LAG + 1];
-        float s[2];
-        auto add = [&](int n) {
-          if (!E8M0 && n >= 0)
-            add_scaled(acc[n / TN][n % TN], t[n % (LAG + 1)], s[n / TN % 2]);
-        };
-  #pragma unroll
-        for (int i = 0; i < TM; ++i) {
-          const v8i x = fa[i % AHEAD];
-          const uint32_t sx = sa[i % AHEAD];
-          s[i % 2] = __uint_as_float(sx) * __uint_as_float(sb);
-  #pragma unroll
-          for (int j = 0; j < TN; ++j) {
-            if constexpr (E8M0) {
-              acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                  fb[j], x, acc[i][j], 0, 0, 0, int(sb), 0, int(sx));
-            } else {
-              t[(i * TN + j) % (LAG + 1)] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                  fb[j], x, f32x4_t{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 127, 0, 127);
-              __builtin_amdgcn_sched_barrier(0);
-              add(i * TN + j - LAG);
-            }
-          }
-          if (i + AHEAD < TM) {
-            fa[i % AHEAD] = frag(ra + 16 * (i + AHEAD));
-            sa[i % AHEAD] = scale_of(i + AHEAD);
-            __builtin_amdgcn_sched_barrier(0);
-          }
-        }
-  #pragma unroll
-        for (int n = TM * TN - LAG; n < TM * TN; ++n) add(n);
       }
+      if (i + AHEAD < TM) {
+        fa[i % AHEAD] = frag(ra + 16 * (i + AHEAD));
+        sa[i % AHEAD] = scale_of(i + AHEAD);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+#pragma unroll
+    for (int n = TM * TN - LAG; n < TM * TN; ++n) add(n);
+    if (C::OCC > 1) __builtin_amdgcn_s_setprio(0);
+  }
 }
 
 // A wavefront's sums to memory. A lane owns 4 consecutive columns of a row, of which 16 rows would
