@@ -698,11 +698,24 @@ __global__ void __launch_bounds__(64 * WAVES) fp8_few_kernel(MatmulK a) {
 
 // ------------------------------------------------------------------------------- host side
 
+// Large tiles are bound by what comes from L2 to LDS (64 KiB a slice and CU: alone it takes 1.33 us
+// of the slice's 1.6, the multiplications alone 1.14; with every line in L2 1.49 in all). Measured
+// on 8192 x 4096 x 128256 and not kept: four wavefronts of 128 x 128 (4.1 ms and 3.7), B's half
+// of a slot refilled while A's is read (4.0), loads spread between the rows of tiles (4.1), lines
+// asked for a slice ahead (4.0), workgroups that go from tile to tile (3.6 to 3.9). On 8192 x 8192
+// x 32768: 256 x 128 tiles in three slots (2.5 ms and 1.8).
 using Wide = Cfg<256, 256, 2, 2, 4, 1>;
 using Small = Cfg<128, 128, 2, 2, 2, 2>;
+// 17 to 64 rows: B passes through once, with two slices on the way in each of two workgroups
+// (64 x 4096 x 128256 122 us; through registers, as the fewest rows, 145 to 189).
 using Thin = Cfg<64, 128, 3, 2, 2, 2>;
 
+// A lane's rows are 16; two such groups of rows a wavefront took 109 us for 17 rows of 4096 x 128256
+// (thin tiles 117) and 19 for 32 of 4096 x 4096 (13).
 constexpr int64_t kFewRows = 16, kThinRows = 64;
+// Their workgroups: 64 columns and 4 wavefronts where that makes many of them, else fewer columns
+// and more wavefronts (16 rows of 4096 x 128256: 104 us with 64 columns, 114 with 32, 130 with 16;
+// x 32777: 34, 33, 37; x 4096: 13.5, 9.5, 9.2).
 constexpr int64_t kFewMany = 32768, kFewSome = 4096;
 
 struct Plan {

@@ -93,13 +93,14 @@ def operands(m, n, k, scale, dev, seed=0):
     return a, ca, b, cb
 
 
-def check_product(out, a, ca, b, cb, bias=None):
+def check_product(out, a, ca, b, cb, bias=None, few=None):
     (m, k), n = a.shape, b.shape[0]
+    few = m <= 64 if few is None else few
     ad = a.double() * spread(ca, 1, m, k)
     bd = b.double() * spread(cb, 128, n, k)
     exact, size = ad @ bd.t(), ad.abs() @ bd.abs().t()
     tol = 2 * (k + 8) * U * size
-    if out.dtype == torch.bfloat16 and m > 64:
+    if out.dtype == torch.bfloat16 and not few:
         a8, b8 = (torch.nn.functional.pad(t.abs(), (0, -k % 8)).view(len(t), -1, 8).amax(-1)
                   for t in (ad, bd))
         tol = tol + 2.0 ** -10 * (a8 @ b8.t())
@@ -206,6 +207,32 @@ def test_product_special_values(dev, scale):
         out = lce.fp8_matmul(a, ca, b, cb, dtype=torch.float32)
         nans = torch.isnan(out[fine])
         assert nans[:, 128:256].all() and not nans[:, :128].any() and not nans[:, 256:].any()
+
+
+@pytest.mark.parametrize("scale", SCALES)
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_product_scales_of_any_value(dev, scale, dtype):
+    """Scales that no quantiser made: NaN over finite values, the smallest exponent byte (2^-127),
+    scales far from one another whose product is an ordinary number."""
+    for m in (7, 80, 300):
+        n, k = 300, 400
+        a, ca, b, cb = operands(m, n, k, scale, dev)
+        ca, cb = ca.clone(), cb.clone()
+        if scale == E8M0:
+            ca, cb = ca.view(torch.uint8), cb.view(torch.uint8)
+            ca[:, 3], cb[1, :] = 0, 100 + 127  # 2^-127 beside 2^100
+            ca[1, 2], cb[2, 0] = 255, 255
+            ca, cb = ca.view(E8M0), cb.view(E8M0)
+        else:
+            ca[:, 3], cb[1, :] = 2.0 ** -120, 2.0 ** 100
+            ca[1, 2], cb[2, 0] = float("nan"), float("nan")
+        out = lce.fp8_matmul(a, ca, b, cb, dtype=torch.float32 if dtype == torch.float32 else None)
+        assert torch.isnan(out[2]).all() and torch.isnan(out[:, 256:]).all()
+        fine = torch.ones(m, dtype=torch.bool, device=dev)
+        fine[2] = False
+        check_product(out[fine, :256], a[fine], ca[:, fine] if scale != E8M0
+                      else ca.view(torch.uint8)[:, fine].view(E8M0), b[:256], cb[:2],
+                      few=m <= 64)
 
 
 def test_product_empty_and_last_block(dev):
