@@ -516,7 +516,8 @@ int rmsnorm_bwd(const void* grad, int dtype, int64_t ldg, const void* x, int64_t
  * columns, scales [ceil(h / 128), lds] block-major, lds >= n (an activation). block_rows 128: one
  * scale per 128 x 128 block, scales [ceil(n / 128), lds] row-major, lds >= ceil(h / 128) (a
  * weight). x dtype [n, ldx], q [n, ldq]; any strides >= h and any alignment of an element.
- * n < 2^31, h <= 2^20, n * h <= 2^34. */
+ * n < 2^31, h <= 2^20, n * h <= 2^34, fewer than 2^24 pieces of 16 rows by 256 columns
+ * (block_rows 1) or 128 by 128. */
 int fp8_quantize(const void* x, int dtype, int64_t n, int64_t h, int64_t ldx, int64_t block_rows,
                  uint8_t* q, int64_t ldq, void* scales, int scale_dtype, int64_t lds,
                  void* stream);
@@ -532,7 +533,7 @@ int fp8_matmul_workspace_size(int64_t m, int64_t n, int64_t k, size_t* bytes);
  *   a  [m, lda], b [n, ldb]  e4m3, first k columns; 16-byte aligned, lda and ldb multiples of 16
  *   a_scales  [ceil(k / 128), ldas]      b_scales  [ceil(n / 128), ldbs]
  *   bias  fp32 [n] or NULL               out  out_dtype [m, ldo], first n columns
- * k a multiple of 16; k <= 2^20, lda and ldb <= 2^22, m <= 2^23, n <= 2^28, fewer than 2^23 tiles
+ * k a multiple of 16; k <= 2^20, lda and ldb <= 2^22, m <= 2^23, n <= 2^28, fewer than 2^22 tiles
  * of 256 x 256. With fp32 scales the product of a row's and a column's scale is formed in fp32.
  * m == 0 is valid. */
 int fp8_matmul(const uint8_t* a, int64_t lda, const void* a_scales, int64_t ldas,
@@ -587,7 +588,9 @@ typedef struct {
  * parents[b, j] is outside 0 .. beams - 1. `states` is a host array; all of them share parents
  * (int32 [batch, slots]). in == out with the same strides and slots == beams reorders in place
  * (all states of a call or none); otherwise no out may share bytes with any in or other out.
- * Runs of one state do not overlap. beams and slots <= BEAM_MAX_BEAMS. */
+ * Runs of one out do not overlap. States without bytes are passed over. count <= 2^16, beams and
+ * slots <= BEAM_MAX_BEAMS, a state spans at most 2^50 bytes in at most 2^23 pieces of a run (of
+ * 16 KiB, in place of 32 KiB / beams). */
 int beam_reorder(const lce_beam_state* states, int64_t count, const int32_t* parents,
                  int64_t batch, int64_t beams, int64_t slots, void* stream);
 

@@ -1,6 +1,7 @@
 // extern "C" entry points of the root-mean-square norm, 8-bit product and beam search operators:
 // argument validation, all of it before any HIP call, then the launch code in rms_kernels.hip,
 // fp8_kernels.hip and beam_kernels.hip.
+#include <algorithm>
 #include <limits>
 #include <new>
 #include <utility>
@@ -89,7 +90,7 @@ int rms_fwd(const void* x, int dtype, int64_t n, int64_t h, int64_t ldx, const v
 int matmul_check_shape(int64_t m, int64_t n, int64_t k) {
   if (m < 0 || m > (int64_t(1) << 23) || n < 1 || n > (int64_t(1) << 28) || k < 16 ||
       k % 16 != 0 || k > (int64_t(1) << 20) ||
-      (m + 255) / 256 * ((n + 255) / 256) >= (int64_t(1) << 23))
+      (m + 255) / 256 * ((n + 255) / 256) >= (int64_t(1) << 22))  // small tiles: 2^32 threads
     return LCE_ERR_BAD_SHAPE;
   return LCE_OK;
 }
@@ -110,7 +111,7 @@ int64_t state_bytes(int64_t batch, int64_t slots, int64_t entry, int64_t beam, i
   const int64_t dims[] = {batch, slots, segments}, strides[] = {entry, beam, segment};
   int64_t total = bytes;
   for (int i = 0; i < 3; ++i) {
-    if (strides[i] < 0 || strides[i] > kMost || mul_overflows(dims[i], strides[i])) return -1;
+    if (strides[i] < 0 || (strides[i] > 0 && dims[i] - 1 > kMost / strides[i])) return -1;
     total += (dims[i] - 1) * strides[i];
     if (total > kMost) return -1;
   }
@@ -135,6 +136,23 @@ bool runs_apart(int64_t batch, int64_t slots, int64_t entry, int64_t beam, int64
     size += (dims[i] - 1) * strides[i];
   }
   return true;
+}
+
+// Whether a written range meets a read or another written one: in the order of their starts, a
+// range meets an earlier one that ends behind its start.
+struct Used {
+  Span at;
+  bool written;
+};
+bool written_meets(std::vector<Used>& all) {
+  std::sort(all.begin(), all.end(), [](const Used& a, const Used& b) { return a.at.lo < b.at.lo; });
+  uintptr_t read_to = 0, written_to = 0;
+  for (const Used& u : all) {
+    if (u.at.lo < written_to || (u.written && u.at.lo < read_to)) return true;
+    uintptr_t& to = u.written ? written_to : read_to;
+    to = std::max(to, u.at.hi);
+  }
+  return false;
 }
 
 }  // namespace
@@ -215,7 +233,8 @@ int fp8_quantize(const void* x, int dtype, int64_t n, int64_t h, int64_t ldx, in
                  uint8_t* q, int64_t ldq, void* scales, int scale_dtype, int64_t lds,
                  void* stream) {
   if (n < 0 || n > kI32Max || h < 1 || h > (int64_t(1) << 20) || n * h > (int64_t(1) << 34) ||
-      (block_rows != 1 && block_rows != 128))
+      (block_rows != 1 && block_rows != 128) ||
+      fp8_quantize_groups(n, h, block_rows) >= (int64_t(1) << 24))  // 2^32 threads
     return LCE_ERR_BAD_SHAPE;
   const int64_t el = dtype_size(dtype), sl = scale_size(scale_dtype);
   if (!el || !sl) return LCE_ERR_BAD_DTYPE;
@@ -335,15 +354,14 @@ int beam_reorder(const lce_beam_state* states, int64_t count, const int32_t* par
   if (count == 0 || batch == 0) return LCE_OK;
   if (!parents) return LCE_ERR_NULL_ARG;
   if (!aligned(parents, 4)) return LCE_ERR_ALIGNMENT;
-  const Span par = span(parents, 4 * batch * slots);
-  const bool inplace = states[0].in == states[0].out;
-  std::vector<Span> outs, ins;
+  std::vector<Used> used;
   try {
-    outs.reserve(size_t(count));
-    ins.reserve(size_t(count));
+    used.reserve(2 * size_t(count) + 1);
   } catch (const std::bad_alloc&) {
     return LCE_ERR_SCRATCH_LIMIT;
   }
+  used.push_back({span(parents, 4 * batch * slots), false});
+  bool inplace = false;
   for (int64_t i = 0; i < count; ++i) {
     const lce_beam_state& st = states[i];
     if (st.segments < 0 || st.segments > kI32Max || st.segment_bytes < 0 ||
@@ -351,6 +369,7 @@ int beam_reorder(const lce_beam_state* states, int64_t count, const int32_t* par
       return LCE_ERR_BAD_SHAPE;
     if (st.segments == 0 || st.segment_bytes == 0) continue;
     if (!st.in || !st.out) return LCE_ERR_NULL_ARG;
+    if (used.size() == 1) inplace = st.in == st.out;  // as the first state that holds something
     const int64_t bi = state_bytes(batch, beams, st.in_entry, st.in_beam, st.in_segment,
                                    st.segments, st.segment_bytes);
     const int64_t bo = state_bytes(batch, slots, st.out_entry, st.out_beam, st.out_segment,
@@ -364,16 +383,10 @@ int beam_reorder(const lce_beam_state* states, int64_t count, const int32_t* par
                       st.in_beam == st.out_beam && st.in_segment == st.out_segment &&
                       slots == beams;
     if (same != inplace) return LCE_ERR_OVERLAP;
-    outs.push_back(span(st.out, bo));
-    if (!inplace) ins.push_back(span(st.in, bi));
+    used.push_back({span(st.out, bo), true});
+    if (!inplace) used.push_back({span(st.in, bi), false});
   }
-  for (size_t i = 0; i < outs.size(); ++i) {
-    if (spans_meet(outs[i], par)) return LCE_ERR_OVERLAP;
-    for (const Span& in : ins)
-      if (spans_meet(outs[i], in)) return LCE_ERR_OVERLAP;
-    for (size_t j = i + 1; j < outs.size(); ++j)
-      if (spans_meet(outs[i], outs[j])) return LCE_ERR_OVERLAP;
-  }
+  if (written_meets(used)) return LCE_ERR_OVERLAP;
   const int rc = check_device();
   if (rc != LCE_OK) return rc;
   LCE_TRY_HIP(beam_reorder_run(states, count, parents, batch, beams, slots, inplace,

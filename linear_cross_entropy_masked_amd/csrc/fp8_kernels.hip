@@ -123,13 +123,12 @@ __global__ void __launch_bounds__(256) fp8_quantize_square_kernel(
 
 template <class T, bool POW2>
 hipError_t run_quantize(const Fp8QuantizeArgs& a, hipStream_t s) {
-  const int64_t blocks = (a.h + kFp8Block - 1) / kFp8Block;
   const bool rows = a.block_rows == 1;
   const int64_t tiles = rows ? (a.n + 15) / 16 : (a.n + kFp8Block - 1) / kFp8Block;
-  const int64_t across = rows ? (blocks + kRowBlocks - 1) / kRowBlocks : blocks;
+  const int64_t groups = fp8_quantize_groups(a.n, a.h, a.block_rows);
   TimedLaunch t(s, K_FP8_QUANTIZE);
   auto launch = [&](auto kernel) {
-    hipLaunchKernelGGL(kernel, dim3(unsigned(tiles * across)), dim3(256), 0, s,
+    hipLaunchKernelGGL(kernel, dim3(unsigned(groups)), dim3(256), 0, s,
                        static_cast<const T*>(a.x), a.n, a.h, a.ldx, a.q, a.ldq, a.scales, a.lds,
                        tiles);
   };
@@ -815,6 +814,12 @@ hipError_t run_matmul_type(const Fp8MatmulArgs& a, hipStream_t s) {
 }
 
 }  // namespace
+
+int64_t fp8_quantize_groups(int64_t n, int64_t h, int64_t block_rows) {
+  const int64_t blocks = (h + kFp8Block - 1) / kFp8Block;
+  return block_rows == 1 ? (n + 15) / 16 * ((blocks + kRowBlocks - 1) / kRowBlocks)
+                         : (n + kFp8Block - 1) / kFp8Block * blocks;
+}
 
 hipError_t fp8_quantize_run(const Fp8QuantizeArgs& a, hipStream_t s) {
   if (a.n == 0) return hipSuccess;

@@ -141,6 +141,7 @@ struct Fp8QuantizeArgs {
   int scale_dtype;
   int64_t lds;
 };
+int64_t fp8_quantize_groups(int64_t n, int64_t h, int64_t block_rows);  // workgroups
 hipError_t fp8_quantize_run(const Fp8QuantizeArgs& a, hipStream_t s);
 
 struct Fp8MatmulArgs {

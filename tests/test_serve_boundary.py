@@ -216,6 +216,48 @@ def test_beam_reorder_refusals(lib):
         assert call(({"segments": 5, "in_segment": 800, "out_segment": 800},)) in AT_DEVICE_CHECK
 
 
+def test_launch_size_refusals(lib):
+    """Sizes whose launches would pass 2^32 threads, and the largest below."""
+    quant = caller(lib.fp8_quantize, dict(x=1 << 40, dtype=0, n=300, h=1, ldx=1, rows=1, q=1 << 50,
+                                          ldq=1, scales=1 << 52, sd=0, lds=1 << 31, stream=None))
+    at = dict(n=(1 << 28) - 16), dict(n=(1 << 31) - 256, rows=128)
+    for kw in (dict(n=1 << 28), dict(n=(1 << 31) - 127, rows=128)):
+        assert quant(**kw) == BAD_SHAPE, kw
+    out = ctypes.c_size_t()
+    size = lib.fp8_matmul_workspace_size
+    assert size(1 << 15, 1 << 23, 16, ctypes.byref(out)) == BAD_SHAPE
+    assert size((1 << 15) - 256, 1 << 23, 16, ctypes.byref(out)) == OK
+    if no_gpu():
+        for kw in at:
+            assert quant(**kw) in AT_DEVICE_CHECK, kw
+
+
+def test_beam_reorder_many_states(lib):
+    """Overlaps among many states, a state without bytes ahead of one that has some, and strides
+    whose products pass 64 bits."""
+    def call(states, beams=4):
+        rows = (lce._BeamState * len(states))()
+        for r, (src, dst, kw) in zip(rows, states):
+            kw = dict(dict(src=src, dst=dst, in_entry=400, in_beam=100, out_entry=400,
+                           out_beam=100, segments=1, segment_bytes=100), **kw)
+            for name, value in kw.items():
+                setattr(r, name, value)
+        return lib.beam_reorder(rows, len(states), A[0], 2, beams, 4, None)
+    many = [(A[1] + 800 * i, A[2] + 800 * ((i * 7919) % 20000), {}) for i in range(20000)]
+    empty = (None, None, {"segment_bytes": 0})
+    for i, dst in ((19999, A[2] + 800 * 5 + 799), (3, A[1] + 800 * 19999 + 799), (7, A[0] + 28)):
+        bad = list(many)
+        bad[i] = (bad[i][0], dst, {})
+        assert call(bad) == OVERLAP, i
+    huge = {"segments": (1 << 31) - 1, "in_segment": 1 << 50, "out_segment": 1 << 50}
+    assert call([(A[1], A[2], huge)]) == BAD_SHAPE
+    assert call([(A[1], A[2], {"in_entry": 1 << 50, "out_entry": 1 << 50})]) == BAD_SHAPE
+    if no_gpu():
+        assert call(many) in AT_DEVICE_CHECK
+        assert call([empty, (A[1], A[2], {})]) in AT_DEVICE_CHECK
+        assert call([empty, (A[1], A[1], {})]) in AT_DEVICE_CHECK
+
+
 def test_binding_refusals():
     f8, e8 = torch.float8_e4m3fn, torch.float8_e8m0fnu
     x = torch.zeros(3, 32)
