@@ -192,10 +192,11 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 8 : 5) beam_rows_ke
   if (tid == 0) holders = count = 0;
   // The sum of exp(x - m) about the thread's own maximum m, each as 2^(x · L - c) with L = log2 e
   // and c = m · L rounded: one operation instead of two. What the rounding of c makes of all terms
-  // alike is taken out of their sum, r = m · L - c being exact.
+  // alike is taken out of their sum, r = m · L - c being exact; 2^r is near 1 up to |m| = 2^20
+  // (r up to 0.05), and further out the difference x - m comes first.
   float s = 0.f;
   const bool any = m > -INFINITY;
-  if (__any(any && fabsf(m) > 0x1p126f)) {  // m · L may pass the largest number
+  if (__any(any && fabsf(m) > 0x1p20f)) {
     const float from = any ? m : 0.f;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
@@ -428,7 +429,8 @@ __global__ void __launch_bounds__(512) beam_pick_kernel(PickK a) {
     }
     s = wave_sum_f64(s);
     const bool bad = __any(nan) || !(acc < INFINITY);  // a NaN or +inf among the logits or scores
-    if (bad && !done && a.status_out && lane == 0) atomicOr(a.status_out, LCE_STATUS_BAD_LOGITS);
+    if ((done ? !(acc < INFINITY) : bad) && a.status_out && lane == 0)
+      atomicOr(a.status_out, LCE_STATUS_BAD_LOGITS);
     if (done) {
       for (int r = lane; r < a.num; r += 64) {
         sj[r] = r == 0 && acc < INFINITY ? double(acc) : -INFINITY;
@@ -442,10 +444,11 @@ __global__ void __launch_bounds__(512) beam_pick_kernel(PickK a) {
     }
     uint64_t* out = sorted + wave * kMost;
     merge_row(in, n, have, a.num, lists + wave * kRowList, counts + wave, out);
-    const double lse = double(m) + log(s);
+    const double log_s = log(s);  // not added to m, beside which it may be lost
     for (int r = lane; r < a.num; r += 64) {
       const uint64_t k = out[r];
-      sj[r] = k ? double(acc) + (double(from_ordered(uint32_t(k >> 32))) - lse) : -INFINITY;
+      const double z = from_ordered(uint32_t(k >> 32));
+      sj[r] = k ? double(acc) + (z - double(m) - log_s) : -INFINITY;
       tj[r] = int32_t(~uint32_t(k));
     }
   }

@@ -50,8 +50,11 @@ def check_step(logits, scores, num, finished=None, eos=None, got=None, ignore_in
             else:
                 order = torch.sort(row, descending=True, stable=True).indices[:num]
                 order = order[row[order] > -INF]
-                lse = torch.logsumexp(row, 0)
-                cand.append(((acc + (row[order] - lse)).tolist(), order.tolist()))
+                # z − lse = (z − max) − log Σ exp(z − max): max + log Σ would lose the log beside a
+                # maximum above 2^53
+                far = row - row.max()
+                logp = far[order] - far.exp().sum().log()
+                cand.append(((acc + logp).tolist(), order.tolist()))
         flat = sorted((x for c in cand for x in c[0]), reverse=True)
         n = min(num, len(flat))
         taken = [0] * k
@@ -150,6 +153,42 @@ def test_step_masks(dev):
     check_step(z[..., :3].contiguous(), s, 16)
     low = torch.full((1, 2, 50), torch.finfo(torch.bfloat16).min, device=dev).bfloat16()
     check_step(low, torch.zeros(1, 2, device=dev), 5)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("base", [2.0 ** 25, -3e9, 3e9, 1e12, -1e30, 1e30, -8e37, 2e38])
+def test_step_large_logits(dev, dtype, base):
+    """Rows far from zero: a score is what lies between the logits, however large they are."""
+    v, num = 5000, 6
+    z = torch.full((1, 2, v), base, device=dev).to(dtype)
+    step = 2.0 ** (math.frexp(base)[1] - 1) * torch.finfo(dtype).eps
+    z[0, 0, 7::9] -= 3 * step  # one to all of the next lower values, as the type has them
+    z[0, 1, 11] += 5 * step
+    status = torch.zeros(1, dtype=torch.int32, device=dev)
+    s = torch.tensor([[-1.5, -2.0]], device=dev)
+    best, parents, tokens, _ = lce.beam_step(z, s, num=num, status=status)
+    assert status.item() == 0
+    d = z.cpu().double()
+    d = d - d.amax(-1, keepdim=True)
+    exact = s.cpu().double()[..., None] + (d - torch.log(torch.exp(d).sum(-1, keepdim=True)))
+    want = exact.flatten().sort(descending=True).values[:num]
+    got = exact[0, parents[0].long().cpu(), tokens[0].long().cpu()]
+    for r in range(num):
+        tol = 100 * U + abs(want[r].item()) * U
+        assert abs(got[r] - want[r]) <= 2 * tol and abs(best[0, r].item() - got[r]) <= tol, r
+
+
+def test_step_finished_without_a_score(dev):
+    """A finished beam whose score is no number has no candidate and is reported."""
+    z, s = data(2, 3, 100, torch.bfloat16, dev)
+    fin = torch.tensor([[False, True, False], [True, False, False]], device=dev)
+    for bad in (float("nan"), INF):
+        t = s.clone()
+        t[0, 1] = bad
+        status = torch.zeros(1, dtype=torch.int32, device=dev)
+        got = lce.beam_step(z, t, num=5, finished=fin, eos=3, status=status)
+        check_step(z, t, 5, fin, 3, got=got)
+        assert status.item() == lce.LCE_STATUS_BAD_LOGITS
 
 
 def test_step_bad_logits(dev):
