@@ -1061,8 +1061,8 @@ def beam_step(logits, scores, *, num: int | None = None, finished=None, eos: int
     if v > 1 and logits.numel() and logits.stride(2) != 1:
         raise ValueError("logits rows must be contiguous (stride(2) == 1)")
     ld = logits.stride(1) if beams > 1 else logits.stride(0) if batch > 1 else v
-    if batch > 1 and beams > 1 and logits.stride(0) != beams * ld:
-        logits, ld = logits.contiguous(), v
+    if ld < v or batch > 1 and beams > 1 and logits.stride(0) != beams * ld:
+        logits, ld = logits.contiguous(), v  # also one row expanded to several beams
     if tuple(scores.shape) != (batch, beams):
         raise ValueError(f"scores must have shape {(batch, beams)}, got {tuple(scores.shape)}")
     _require(scores, "scores", torch.float32, 2, dev)
@@ -1095,6 +1095,8 @@ def _runs(t, name):
     """(segments, segment stride, segment bytes) of what a state holds per beam: dimensions 2 on,
     as runs of contiguous elements at one stride."""
     el = t.element_size()
+    if t.is_contiguous() and t.numel():
+        return 1, 0, t.numel() // (t.shape[0] * t.shape[1]) * el
     run, seg, stride = 1, 1, 0
     for size, step in zip(reversed(t.shape[2:]), reversed(t.stride()[2:])):
         if size == 1:

@@ -229,6 +229,11 @@ def test_step_strides(dev):
     for view in (wide[..., 3:5004], gap[:, 1:5], z.transpose(0, 1).contiguous().transpose(0, 1)):
         for p, q in zip(ref[:3], lce.beam_step(view, s.t().contiguous().t())):
             assert torch.equal(p, q)
+    for same in (z[:1, :1].expand(1, 4, 5001), z[:, :1].expand(3, 4, 5001),
+                 z[:1, :1].expand(3, 1, 5001), z[:1, :1].expand(3, 4, 5001)):
+        t = s[:same.shape[0], :same.shape[1]]
+        for p, q in zip(lce.beam_step(same.contiguous(), t)[:3], lce.beam_step(same, t)):
+            assert torch.equal(p, q)
     one = lce.beam_step(wide[1:2, 2:3, 3:5004], s[1:2, 2:3], num=4)
     check_step(z[1:2, 2:3].contiguous(), s[1:2, 2:3], 4, got=one)
     empty = lce.beam_step(z[:0], s[:0], num=4, eos=1)
