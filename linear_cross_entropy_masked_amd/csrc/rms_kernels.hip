@@ -24,7 +24,17 @@ namespace lce {
 
 namespace {
 
-constexpr int kFwdThreads = 512, kFwdElems = 32;
+// Launch shapes, with x + residual read, their sum and a 16-bit (8-bit) y written, in us:
+//                                        [65536, 4096] bf16   [4096, 4096] bf16   [20001, 1025] fp16
+//   512 threads, 16 elements a lane         367  (300)            21.9 (21.9)         36.9 (45.1)
+//   512 threads, 32 elements                377  (340)            26.8 (27.0)         47.8 (53.4)
+//   256 threads, 16 elements                402  (311)            22.1 (22.5)         37.3 (40.8)
+//   256 threads, 32 elements                372  (301)            23.0 (23.8)         45.3 (48.8)
+// 367 us are 5.9 TB/s (a large copy: 4.9). The grid is what 2048 workgroups of 512 threads hold;
+// half or twice of that makes 362 and 408 us, 22.9 and 21.8. The backward ([8192, 4096] bf16 with the gradient of the sum, and [4099, 2051]
+// fp16): 256 threads and 512 workgroups 49.5 and 18.6 us, 513 workgroups 53.6 and 23.0, 768 50.1
+// and 20.0, 1024 58.5 and 20.2.
+constexpr int kFwdThreads = 512, kFwdElems = 16;
 constexpr int kBwdThreads = 256, kBwdElems = 16;
 constexpr int64_t kFwdGrid = 2048;
 constexpr int64_t kShortRow = 512, kPairRow = 256 * 24, kRegRow = 512 * 32;
@@ -33,7 +43,9 @@ int64_t bwd_grid(int64_t h) { return h <= kShortRow ? 1024 : h <= kPairRow ? 512
 int64_t part_rows(int64_t n, int64_t h) {
   return std::min(n, h > kRegRow ? kColRows : bwd_grid(h));
 }
-constexpr int64_t kStreamBytes = int64_t(512) << 20;
+// A forward of whole vectors that moves more than this passes by the caches (non-temporal loads and
+// stores): 512 MiB take 92 us so and 111 without, 128 MiB 22 either way, 64 MiB 17.4 and 16.3.
+constexpr int64_t kStreamBytes = int64_t(256) << 20;
 
 // A weight of the rows' own type or of fp32, at a lane's columns.
 template <class T, class C, int VE>
@@ -314,7 +326,8 @@ hipError_t run_fwd(const RmsFwd& a, hipStream_t s) {
   return with_shape<kFwdElems>(a.h, [&](auto wpr, auto epl) {
     constexpr int WPR = decltype(wpr)::value, EPL = decltype(epl)::value;
     constexpr int RG = norm_threads(WPR, kFwdThreads) / (64 * WPR);
-    const int64_t grid = std::min<int64_t>((a.n + RG - 1) / RG, kFwdGrid);
+    const int64_t grid = std::min<int64_t>((a.n + RG - 1) / RG,
+                                           kFwdGrid * 512 / norm_threads(WPR, kFwdThreads));
     const int64_t moved = a.n * a.h * int64_t(sizeof(T)) * (a.residual ? 4 : 2);
     TimedLaunch t(s, FP8 ? K_RMS_FP8_FWD : K_RMS_FWD);
     auto launch = [&](auto kernel) {
