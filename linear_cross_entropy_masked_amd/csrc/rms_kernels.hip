@@ -38,7 +38,7 @@ constexpr int kFwdThreads = 512, kFwdElems = 16;
 constexpr int kBwdThreads = 256, kBwdElems = 16;
 constexpr int64_t kFwdGrid = 2048;
 constexpr int64_t kShortRow = 512, kPairRow = 256 * 24, kRegRow = 512 * 32;
-constexpr int64_t kColRows = 64;
+constexpr int64_t kColRows = 64, kLongGrid = 512;
 int64_t bwd_grid(int64_t h) { return h <= kShortRow ? 1024 : h <= kPairRow ? 512 : 256; }
 int64_t part_rows(int64_t n, int64_t h) {
   return std::min(n, h > kRegRow ? kColRows : bwd_grid(h));
@@ -176,8 +176,8 @@ struct RmsBwd {
   float* part;  // partial rows of dw, or NULL
 };
 
-// PARAMS: with the workgroup's partial row of dw, where a.part is given.
-template <class T, int WPR, int EPL, bool FULL, bool PARAMS>
+// With the workgroup's partial row of dw, where a.part is given.
+template <class T, int WPR, int EPL, bool FULL>
 __global__ void __launch_bounds__(norm_threads(WPR, kBwdThreads)) rmsnorm_bwd_kernel(RmsBwd a) {
   // grad, grad_sum and dx may be the same rows
   constexpr int VE = Elem<T>::kVec, NV = EPL / VE, RG = norm_threads(WPR, kBwdThreads) / (64 * WPR);
@@ -228,7 +228,7 @@ __global__ void __launch_bounds__(norm_threads(WPR, kBwdThreads)) rmsnorm_bwd_ke
 #pragma unroll
       for (int q = 0; q < VE; ++q) {
         xh[j][q] *= rs;
-        if (PARAMS && live) dw[j][q] += u[j][q] * xh[j][q];
+        if (live) dw[j][q] += u[j][q] * xh[j][q];
         u[j][q] *= w[q];
         s[0] += col.counts(j, q) ? u[j][q] * xh[j][q] : 0.f;
       }
@@ -251,7 +251,7 @@ __global__ void __launch_bounds__(norm_threads(WPR, kBwdThreads)) rmsnorm_bwd_ke
       col.store(dx + r * a.lddx, j, u[j]);
     }
   }
-  if (!PARAMS || !a.part) return;
+  if (!a.part) return;
   // this workgroup's partial row: its row groups added through LDS, in group order
   if constexpr (RG > 1) {
     constexpr int LANES = 64 * WPR;
@@ -280,6 +280,70 @@ __global__ void __launch_bounds__(norm_threads(WPR, kBwdThreads)) rmsnorm_bwd_ke
 #pragma unroll
       for (int q = 0; q < VE; ++q)
         if (col.counts(j, q)) pw[col.at[j] + q] = dw[j][q];
+    }
+  }
+}
+
+// Rows past kRegRow: no sums of dw, and the row is widened anew for each of its two uses, since 32
+// numbers a lane of x and grad with the next row's do not fit the registers of sixteen wavefronts
+// ([4096, 20000] bf16 with the gradient of the sum: 146 us beside the 90 of its columns, and 287 as
+// the shorter rows are done).
+template <class T, int WPR, int EPL, bool FULL>
+__global__ void __launch_bounds__(64 * WPR) rmsnorm_bwd_long_kernel(RmsBwd a) {
+  constexpr int VE = Elem<T>::kVec, NV = EPL / VE;
+  __shared__ float red[2][WPR][1];
+  const int lane = threadIdx.x;
+  const float inv_h = 1.f / float(a.h);
+  const T* gs = static_cast<const T*>(a.grad_sum);
+  const Columns<VE, NV, 64 * WPR, FULL> col(lane, a.h);
+  int parity = 0;
+  for (int64_t r = blockIdx.x; r < a.n; r += gridDim.x) {
+    raw4 x[NV], g[NV];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) x[j] = col.load(static_cast<const T*>(a.x) + r * a.ldx, j);
+#pragma unroll
+    for (int j = 0; j < NV; ++j) g[j] = col.load(static_cast<const T*>(a.grad) + r * a.ldg, j);
+    const float rs = a.rstd[r];
+    // x · rstd and grad · weight of vector j
+    auto widen = [&](int j, float(&xh)[VE], float(&u)[VE]) {
+      float w[VE];
+      weight_at<T>(col, a.weight, a.wide, j, w);
+      asm volatile("" : "+v"(x[j]), "+v"(g[j]));
+      Elem<T>::unpack(x[j], xh);
+      Elem<T>::unpack(g[j], u);
+#pragma unroll
+      for (int q = 0; q < VE; ++q) {
+        xh[q] *= rs;
+        u[q] *= w[q];
+      }
+    };
+    float s[1] = {0.f};
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      float xh[VE], u[VE];
+      widen(j, xh, u);
+#pragma unroll
+      for (int q = 0; q < VE; ++q) s[0] += col.counts(j, q) ? u[q] * xh[q] : 0.f;
+    }
+    row_sums<WPR, 1>(s, red[parity]);
+    parity ^= 1;
+    const float b = s[0] * inv_h;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      if (!col.live(j)) continue;
+      float xh[VE], u[VE], k[VE] = {};
+      if (gs) Elem<T>::unpack(col.load(gs + r * a.ldgs, j), k);
+      widen(j, xh, u);
+#pragma unroll
+      for (int q = 0; q < VE; ++q) u[q] = rs * (u[q] - xh[q] * b) + k[q];
+      T* to = static_cast<T*>(a.dx) + r * a.lddx;
+      if (FULL || col.skip[j] == 0) {
+        col.store(to, j, u);
+      } else {  // the row's last vector: what grad_sum holds there may still be read by its owner
+#pragma unroll
+        for (int q = 0; q < VE; ++q)
+          if (col.counts(j, q)) to[col.at[j] + q] = Elem<T>::from_f32(u[q]);
+      }
     }
   }
 }
@@ -362,16 +426,23 @@ hipError_t run_bwd_rows(const RmsBwd& a, hipStream_t s) {
     constexpr int WPR = decltype(wpr)::value, EPL = decltype(epl)::value;
     constexpr int RG = norm_threads(WPR, kBwdThreads) / (64 * WPR);
     constexpr bool PARAMS = 64 * WPR * EPL <= kRegRow;
-    const int64_t grid = std::min<int64_t>((a.n + RG - 1) / RG, bwd_grid(a.h));
+    const int64_t grid = std::min<int64_t>((a.n + RG - 1) / RG, PARAMS ? bwd_grid(a.h) : kLongGrid);
     TimedLaunch t(s, K_RMS_BWD);
     auto launch = [&](auto kernel) {
       hipLaunchKernelGGL(kernel, dim3(unsigned(grid)), dim3(norm_threads(WPR, kBwdThreads)), 0, s,
                          a);
     };
-    if (a.h % Elem<T>::kVec == 0)
-      launch(rmsnorm_bwd_kernel<T, WPR, EPL, true, PARAMS>);
-    else
-      launch(rmsnorm_bwd_kernel<T, WPR, EPL, false, PARAMS>);
+    if constexpr (!PARAMS) {
+      if (a.h % Elem<T>::kVec == 0)
+        launch(rmsnorm_bwd_long_kernel<T, WPR, EPL, true>);
+      else
+        launch(rmsnorm_bwd_long_kernel<T, WPR, EPL, false>);
+    } else {
+      if (a.h % Elem<T>::kVec == 0)
+        launch(rmsnorm_bwd_kernel<T, WPR, EPL, true>);
+      else
+        launch(rmsnorm_bwd_kernel<T, WPR, EPL, false>);
+    }
     return hipGetLastError();
   });
 }

@@ -244,7 +244,7 @@ def test_backward(dev, h, dtype):
         assert torch.equal(dx, again[0]) and torch.equal(dw, again[1])
 
 
-@pytest.mark.parametrize("h", [96, 2051, 20000])
+@pytest.mark.parametrize("h", [96, 2051, 20000, 20003])
 def test_backward_outputs(dev, h):
     """In place, accumulated, skipped, empty; an fp32 gradient of a 16-bit weight; one tensor as
     both upstream gradients."""
@@ -270,8 +270,9 @@ def test_backward_outputs(dev, h):
     check_backward(g, x, rstd, w, g, got, None)
     _, zero = lce.rmsnorm_bwd(g[:0], x[:0], rstd[:0], w)
     assert (zero == 0).all()
+    was = buf.clone()
     lce.rmsnorm_bwd(g[:0], x[:0], rstd[:0], w, grad_weight=buf, accumulate=True)
-    assert torch.equal(buf, buf)
+    assert torch.equal(buf, was)
 
 
 def test_backward_against_differences(dev):
