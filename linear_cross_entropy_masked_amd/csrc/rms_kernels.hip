@@ -31,9 +31,11 @@ namespace {
 //   256 threads, 16 elements                402  (311)            22.1 (22.5)         37.3 (40.8)
 //   256 threads, 32 elements                372  (301)            23.0 (23.8)         45.3 (48.8)
 // 367 us are 5.9 TB/s (a large copy: 4.9). The grid is what 2048 workgroups of 512 threads hold;
-// half or twice of that makes 362 and 408 us, 22.9 and 21.8. The backward ([8192, 4096] bf16 with the gradient of the sum, and [4099, 2051]
-// fp16): 256 threads and 512 workgroups 49.5 and 18.6 us, 513 workgroups 53.6 and 23.0, 768 50.1
-// and 20.0, 1024 58.5 and 20.2.
+// half or twice of that makes 362 and 408 us, 22.9 and 21.8. The backward ([8192, 4096] bf16 with
+// the gradient of the sum, 5.1 TB/s, and [4099, 2051] fp16): 256 threads and 512 workgroups 49.5
+// and 18.6 us, 513 workgroups 53.6 and 23.0, 768 50.1 and 20.0, 1024 58.5 and 20.2; held as loaded
+// and widened for each use as long rows are, 54.1 and 20.4. Adding the partial rows takes 4.5 us
+// of both.
 constexpr int kFwdThreads = 512, kFwdElems = 16;
 constexpr int kBwdThreads = 256, kBwdElems = 16;
 constexpr int64_t kFwdGrid = 2048;
