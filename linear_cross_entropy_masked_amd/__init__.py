@@ -1136,20 +1136,29 @@ def beam_reorder(states, parents, *, out=None):
     if not states:
         return out
     beams = None
-    rows = (_BeamState * len(states))()
+    rows = []  # lce_beam_state's fields, state by state
     for k, (x, y) in enumerate(zip(states, out)):
-        if not isinstance(x, torch.Tensor) or not x.is_cuda or x.device != dev or x.dim() < 2:
+        if not isinstance(x, torch.Tensor) or x.device != dev or x.dim() < 2:
             raise ValueError(f"states[{k}] must be a [batch, beams, ...] tensor on {dev}")
-        if x.shape[0] != batch or (beams is not None and x.shape[1] != beams):
-            raise ValueError(f"states[{k}] has shape {tuple(x.shape)}, expected "
+        shape = x.shape
+        if shape[0] != batch or (beams is not None and shape[1] != beams):
+            raise ValueError(f"states[{k}] has shape {tuple(shape)}, expected "
                              f"{(batch, beams or 'beams')} first")
-        beams = x.shape[1]
-        shape = (batch, slots, *x.shape[2:])
+        beams = shape[1]
+        if slots != beams:
+            shape = (batch, slots, *shape[2:])
         if y is None:
             y = out[k] = torch.empty(shape, dtype=x.dtype, device=dev)
-        _require(y, f"out[{k}]", x.dtype, x.dim(), dev)
-        if tuple(y.shape) != shape:
-            raise ValueError(f"out[{k}] must have shape {shape}, got {tuple(y.shape)}")
+        elif y is not x or slots != beams:
+            _require(y, f"out[{k}]", x.dtype, x.dim(), dev)
+            if y.shape != shape:
+                raise ValueError(f"out[{k}] must have shape {tuple(shape)}, got {tuple(y.shape)}")
+        el = x.element_size()
+        if x.is_contiguous() and y.is_contiguous() and x.numel():
+            size = x.numel() // (batch * beams) * el
+            rows += (x.data_ptr(), y.data_ptr(), beams * size, size, 0, slots * size, size, 0, 1,
+                     size)
+            continue
         (seg, sin, size), (seg_out, sout, size_out) = _runs(x, f"states[{k}]"), _runs(y, f"out[{k}]")
         if size != size_out:  # runs of one may be several of the other
             small = min(size, size_out)
@@ -1160,21 +1169,11 @@ def beam_reorder(states, parents, *, out=None):
                 seg, sin, size = size // small, small, small
             else:
                 seg_out, sout, size_out = size_out // small, small, small
-        el = x.element_size()
-        r = rows[k]
-        r.src, r.dst, r.segments, r.segment_bytes = x.data_ptr(), y.data_ptr(), seg, size
-        r.in_entry, r.in_beam, r.in_segment = x.stride(0) * el, x.stride(1) * el, sin
-        r.out_entry, r.out_beam, r.out_segment = y.stride(0) * el, y.stride(1) * el, sout
-    _call("beam_reorder", dev, rows, len(states), parents.data_ptr(), batch, beams, slots)
+        rows += (x.data_ptr(), y.data_ptr(), x.stride(0) * el, x.stride(1) * el, sin,
+                 y.stride(0) * el, y.stride(1) * el, sout, seg, size)
+    _call("beam_reorder", dev, (ctypes.c_int64 * len(rows))(*rows), len(states),
+          parents.data_ptr(), batch, beams, slots)
     return out
-
-
-class _BeamState(ctypes.Structure):
-    """lce_beam_state of the C ABI."""
-    _fields_ = [("src", ctypes.c_void_p), ("dst", ctypes.c_void_p)] + [
-        (name, ctypes.c_int64) for name in
-        ("in_entry", "in_beam", "in_segment", "out_entry", "out_beam", "out_segment", "segments",
-         "segment_bytes")]
 
 
 def flce_piece_fwd_workspace_size(n: int, h: int, v: int) -> int:

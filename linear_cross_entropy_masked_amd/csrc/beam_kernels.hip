@@ -341,8 +341,15 @@ __device__ __forceinline__ void wave_sync() {
 }
 
 // The best `num` keys of n at `in`, in order, into the wavefront's `out` (LDS); 0 behind the last.
-// `have`: the lane's first kHeld keys, at in[lane], in[lane + 64], ...
-constexpr int kHeld = 4;
+// `have`: the lane's first kHeld keys, at in[place(lane, 0)], in[place(lane, 1)], ...
+// A row's keys are its slices' lists, each in order: a lane that took every 64th of them would hold
+// the same few ranks of all lists, one lane all of the best, and the threshold that enough lanes
+// reach would let most keys pass (4 x 16 rows of 46491 x 32 candidates: 216 us, one key at a time).
+// So each 64 are turned by kTurn lanes against the 64 before.
+constexpr int kHeld = 8, kTurn = 21;
+__device__ __forceinline__ int64_t place(int lane, int64_t k) {
+  return 64 * k + ((lane + kTurn * uint32_t(k)) & 63);
+}
 __device__ __forceinline__ void merge_row(const uint64_t* in, int64_t n,
                                           const uint64_t (&have)[kHeld], int num, uint64_t* list,
                                           int* count, uint64_t* out) {
@@ -351,7 +358,13 @@ __device__ __forceinline__ void merge_row(const uint64_t* in, int64_t n,
   auto each = [&](auto&& f) {
 #pragma unroll
     for (int k = 0; k < kHeld; ++k) f(have[k]);
-    for (int64_t i = lane + 64 * kHeld; i < n; i += 64) f(in[i]);
+    for (int64_t k0 = kHeld; 64 * k0 < n; k0 += kHeld) {
+      uint64_t x[kHeld];
+#pragma unroll
+      for (int k = 0; k < kHeld; ++k) x[k] = place(lane, k0 + k) < n ? in[place(lane, k0 + k)] : 0;
+#pragma unroll
+      for (int k = 0; k < kHeld; ++k) f(x[k]);
+    }
   };
   each([&](uint64_t k) { top[0] = uint32_t(k >> 32) > top[0] ? uint32_t(k >> 32) : top[0]; });
   const uint32_t lim = threshold<1>(top, num);
@@ -419,7 +432,7 @@ __global__ void __launch_bounds__(512) beam_pick_kernel(PickK a) {
     const float2 own = lane < a.splits ? ms[lane] : float2{-INFINITY, 0.f};
     uint64_t have[kHeld];
 #pragma unroll
-    for (int k = 0; k < kHeld; ++k) have[k] = lane + 64 * k < n ? in[lane + 64 * k] : 0;
+    for (int k = 0; k < kHeld; ++k) have[k] = place(lane, k) < n ? in[place(lane, k)] : 0;
     // the row's logsumexp, lanes in order of their distance
     float m = own.x;
     bool nan = !(own.y >= 0.f) || own.x == INFINITY;
@@ -603,10 +616,12 @@ __global__ void __launch_bounds__(kThreads) beam_inplace_kernel(StatesK a) {
 
 // Logits of a slice. Long ones leave the pick less (32 x 8 rows of 128256 x 16 candidates: rows and
 // pick 17.8 + 9.2 us in slices of 8192, 23.1 + 17.9 of 4096, 32.8 + 36.9 of 2048), short ones
-// spread few rows over the CUs.
+// spread few rows over the CUs: the longest of which there are 512. Asking for 1024, 512 and 256 of
+// them takes 44, 32 and 31 us for 4 x 16 rows of 46491 x 32 candidates, 29.7, 23.2 and 22.7 for
+// 2 x 16 of 118257 x 16, 15.4, 16.4 and 16.5 for 16 x 8 of 32777 x 8.
 int64_t slice_of(int64_t rows, int64_t v) {
-  if (rows * ((v + 8191) / 8192) >= 1024) return 8192;
-  if (rows * ((v + 4095) / 4096) >= 1024) return 4096;
+  if (rows * ((v + 8191) / 8192) >= 512) return 8192;
+  if (rows * ((v + 4095) / 4096) >= 512) return 4096;
   return 2048;
 }
 

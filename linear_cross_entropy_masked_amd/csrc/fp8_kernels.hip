@@ -560,6 +560,7 @@ __global__ void __launch_bounds__(C::THREADS, C::OCC) fp8_matmul_kernel(MatmulK 
     // slice kt has landed once only later slices' loads are pending
     wait_slices<C::PER, C::STAGES - 2>(issued - 1 - kt);
     __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");  // no read of the slice is moved ahead of it
     if (kt + C::STAGES - 1 < nk) issue();
     multiply<C, E8M0, PRECISE>(lds + rslot * C::StageBytes, wm, wn, lane, acc);
     rslot = rslot + 1 == C::STAGES ? 0 : rslot + 1;

@@ -16,6 +16,14 @@ AT_DEVICE_CHECK = (HIP, DEVICE)
 BIG = 1 << 30
 
 
+class BeamState(ctypes.Structure):
+    """lce_beam_state of the C ABI."""
+    _fields_ = [("src", ctypes.c_void_p), ("dst", ctypes.c_void_p)] + [
+        (name, ctypes.c_int64) for name in
+        ("in_entry", "in_beam", "in_segment", "out_entry", "out_beam", "out_segment", "segments",
+         "segment_bytes")]
+
+
 def no_gpu():
     return torch.cuda.device_count() == 0
 
@@ -182,7 +190,7 @@ def test_beam_step_refusals(lib):
 
 def test_beam_reorder_refusals(lib):
     def call(states=({},), parents=A[0], batch=2, beams=4, slots=4, count=None):
-        rows = (lce._BeamState * max(1, len(states)))()
+        rows = (BeamState * max(1, len(states)))()
         for r, kw in zip(rows, states):
             kw = dict(dict(src=A[1], dst=A[2], in_entry=400, in_beam=100, in_segment=0,
                            out_entry=400, out_beam=100, out_segment=0, segments=1,
@@ -236,7 +244,7 @@ def test_beam_reorder_many_states(lib):
     """Overlaps among many states, a state without bytes ahead of one that has some, and strides
     whose products pass 64 bits."""
     def call(states, beams=4):
-        rows = (lce._BeamState * len(states))()
+        rows = (BeamState * len(states))()
         for r, (src, dst, kw) in zip(rows, states):
             kw = dict(dict(src=src, dst=dst, in_entry=400, in_beam=100, out_entry=400,
                            out_beam=100, segments=1, segment_bytes=100), **kw)
