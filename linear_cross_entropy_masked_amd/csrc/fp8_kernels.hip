@@ -22,7 +22,7 @@
 // read fall in different banks. The scales of a slice (one dword a row) come the same way. A lane
 // feeds its MFMA chunks g and g + 4 of its row (g = lane / 16) from both operands: the order of k
 // within a block is free, since the block shares its scales.
-// Few rows (up to 64): see fp8_few_kernel.
+// Up to 16 rows: see fp8_few_kernel; up to 64: tiles of 64 rows.
 #include <algorithm>
 #include <type_traits>
 
@@ -478,7 +478,8 @@ __device__ __forceinline__ void store_tile(const MatmulK& a, char* tile, int64_t
 #pragma unroll 4
     for (int s = 0; s < Rows / PerStore; ++s) {
       const int r = s * PerStore + rr;
-      store_raw(out, *reinterpret_cast<const raw4*>(tile + r * RowBytes + ((chunk ^ (r & 7)) << 4)));
+      store_raw(out,
+                *reinterpret_cast<const raw4*>(tile + r * RowBytes + ((chunk ^ (r & 7)) << 4)));
       out += PerStore * a.ldo;
     }
   } else {
@@ -608,29 +609,22 @@ __global__ void __launch_bounds__(256) fp8_join_kernel(const float* __restrict__
 // whole 128-byte lines an instruction pair); their sums meet in LDS, in wavefront order.
 template <int NT, int WAVES, bool E8M0, class T>
 __global__ void __launch_bounds__(64 * WAVES) fp8_few_kernel(MatmulK a) {
-  constexpr int MT = 1, SE = E8M0 ? 1 : 4;
-  __shared__ float red[WAVES - 1][MT * NT * 4][64];
+  constexpr int SE = E8M0 ? 1 : 4;
+  __shared__ float red[WAVES - 1][NT * 4][64];
   const int lane = threadIdx.x & 63, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t n0 = int64_t(blockIdx.x) * (16 * NT);
   // rows past the last read the last one's: what comes of them is not stored
-  const uint8_t *pa[MT], *pb[NT];
-  const char* ca[MT];
-#pragma unroll
-  for (int i = 0; i < MT; ++i) {
-    const int64_t r = std::min<int64_t>(16 * i + (lane & 15), a.m - 1);
-    pa[i] = a.a + r * a.lda + 16 * g;
-    ca[i] = static_cast<const char*>(a.ca) + r * SE;
-  }
+  const int64_t row = std::min<int64_t>(lane & 15, a.m - 1);
+  const uint8_t *pa = a.a + row * a.lda + 16 * g, *pb[NT];
+  const char* ca = static_cast<const char*>(a.ca) + row * SE;
 #pragma unroll
   for (int j = 0; j < NT; ++j)
     pb[j] = a.b + std::min<int64_t>(n0 + 16 * j + (lane & 15), a.n - 1) * a.ldb + 16 * g;
   const char* cb = static_cast<const char*>(a.cb) + n0 / kFp8Block * a.ldcb * SE;
-  f32x4_t acc[MT][NT];
+  f32x4_t acc[NT];
 #pragma unroll
-  for (int i = 0; i < MT; ++i)
-#pragma unroll
-    for (int j = 0; j < NT; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  for (int j = 0; j < NT; ++j) acc[j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
   auto load32 = [&](const uint8_t* p, int64_t b) {
     // chunks g and g + 4 of block b, zero behind column k
     const int64_t c = b * kFp8Block + 16 * g;
@@ -644,56 +638,44 @@ __global__ void __launch_bounds__(64 * WAVES) fp8_few_kernel(MatmulK a) {
                 : *reinterpret_cast<const uint32_t*>(p);
   };
   for (int64_t b = wave; b < a.blocks; b += WAVES) {
-    v8i fa[MT], fb[NT];
-    uint32_t sa[MT];
+    v8i fb[NT];
     const uint32_t sb = scale(cb + b * SE);
 #pragma unroll
     for (int j = 0; j < NT; ++j) fb[j] = load32(pb[j], b);
-#pragma unroll
-    for (int i = 0; i < MT; ++i) {
-      fa[i] = load32(pa[i], b);
-      sa[i] = scale(ca[i] + b * a.ldca * SE);
-    }
+    const v8i fa = load32(pa, b);
+    const uint32_t sa = scale(ca + b * a.ldca * SE);
     Wide32 wb[NT];
 #pragma unroll
     for (int j = 0; j < NT; ++j) wb[j] = widen(fb[j]);
     const float cs = scale_value<E8M0>(sb);
+    const Wide32 wa = widen(fa);
+    const float s = scale_value<E8M0>(sa) * cs;
 #pragma unroll
-    for (int i = 0; i < MT; ++i) {
-      const Wide32 wa = widen(fa[i]);
-      const float s = scale_value<E8M0>(sa[i]) * cs;
-#pragma unroll
-      for (int j = 0; j < NT; ++j) add_scaled(acc[i][j], block_sums(wb[j], wa), s);
-    }
+    for (int j = 0; j < NT; ++j) add_scaled(acc[j], block_sums(wb[j], wa), s);
   }
   if (wave > 0) {
 #pragma unroll
-    for (int i = 0; i < MT; ++i)
+    for (int j = 0; j < NT; ++j)
 #pragma unroll
-      for (int j = 0; j < NT; ++j)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) red[wave - 1][(i * NT + j) * 4 + q][lane] = acc[i][j][q];
+      for (int q = 0; q < 4; ++q) red[wave - 1][j * 4 + q][lane] = acc[j][q];
   }
   __syncthreads();
   if (wave > 0) return;
+  const int64_t gm = lane & 15;
 #pragma unroll
   for (int j = 0; j < NT; ++j) {
     const int64_t gn = n0 + 16 * j + 4 * g;
     const int cnt = gn + 4 <= a.n ? 4 : int(a.n - gn);
     if (cnt <= 0) continue;
+    float x[4];
 #pragma unroll
-    for (int i = 0; i < MT; ++i) {
-      float x[4];
+    for (int q = 0; q < 4; ++q) {
+      x[q] = acc[j][q];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        x[q] = acc[i][j][q];
-#pragma unroll
-        for (int w = 0; w < WAVES - 1; ++w) x[q] += red[w][(i * NT + j) * 4 + q][lane];
-        if (a.bias && q < cnt) x[q] += a.bias[gn + q];
-      }
-      const int64_t gm = 16 * i + (lane & 15);
-      if (gm < a.m) store4(static_cast<T*>(a.out) + gm * a.ldo + gn, x, cnt);
+      for (int w = 0; w < WAVES - 1; ++w) x[q] += red[w][j * 4 + q][lane];
+      if (a.bias && q < cnt) x[q] += a.bias[gn + q];
     }
+    if (gm < a.m) store4(static_cast<T*>(a.out) + gm * a.ldo + gn, x, cnt);
   }
 }
 
@@ -703,7 +685,9 @@ __global__ void __launch_bounds__(64 * WAVES) fp8_few_kernel(MatmulK a) {
 // of the slice's 1.6, the multiplications alone 1.14; with every line in L2 1.49 in all). Measured
 // on 8192 x 4096 x 128256 and not kept: four wavefronts of 128 x 128 (4.1 ms and 3.7), B's half
 // of a slot refilled while A's is read (4.0), loads spread between the rows of tiles (4.1), lines
-// asked for a slice ahead (4.0), workgroups that go from tile to tile (3.6 to 3.9). On 8192 x 8192
+// asked for a slice ahead (4.0; each by one of the workgroups that share it, no change), the two
+// wavefronts of a SIMD half a slice apart (3.83 and 3.73), workgroups that go from tile to tile
+// (3.6 to 3.9). On 8192 x 8192
 // x 32768: 256 x 128 tiles in three slots (2.5 ms and 1.8), which also take 42.5 us for 2048 x
 // 4096 x 4096 (small tiles 41).
 using Wide = Cfg<256, 256, 2, 2, 4, 1>;
@@ -712,8 +696,8 @@ using Small = Cfg<128, 128, 2, 2, 2, 2>;
 // (64 x 4096 x 128256 122 us; through registers, as the fewest rows, 145 to 189).
 using Thin = Cfg<64, 128, 3, 2, 2, 2>;
 
-// A lane's rows are 16; two such groups of rows a wavefront took 109 us for 17 rows of 4096 x 128256
-// (thin tiles 117) and 19 for 32 of 4096 x 4096 (13).
+// An instruction's rows are 16; two such groups a wavefront took 109 us for 17 rows of 4096 x
+// 128256 (thin tiles 117) and 19 for 32 of 4096 x 4096 (13).
 constexpr int64_t kFewRows = 16, kThinRows = 64;
 // Their workgroups: 64 columns and 4 wavefronts where that makes many of them, else fewer columns
 // and more wavefronts (16 rows of 4096 x 128256: 104 us with 64 columns, 114 with 32, 130 with 16;
