@@ -41,9 +41,14 @@ constexpr int kBwdThreads = 256, kBwdElems = 16;
 constexpr int64_t kFwdGrid = 2048;
 constexpr int64_t kShortRow = 512, kPairRow = 256 * 24, kRegRow = 512 * 32;
 constexpr int64_t kColRows = 64, kLongGrid = 512;
+// Of fp32 rows, half as many numbers with their dw fit a workgroup's registers ([1538, 12728] fp32
+// with the gradient of the sum: 104 us as long rows, 138 else).
+template <class T>
+constexpr int64_t kRegRowOf = sizeof(T) == 4 ? kRegRow / 2 : kRegRow;
 int64_t bwd_grid(int64_t h) { return h <= kShortRow ? 1024 : h <= kPairRow ? 512 : 256; }
+template <class T>
 int64_t part_rows(int64_t n, int64_t h) {
-  return std::min(n, h > kRegRow ? kColRows : bwd_grid(h));
+  return std::min(n, h > kRegRowOf<T> ? kColRows : bwd_grid(h));
 }
 // A forward of whole vectors that moves more than this passes by the caches (non-temporal loads and
 // stores): 512 MiB take 92 us so and 111 without, 128 MiB 22 either way, 64 MiB 17.4 and 16.3.
@@ -58,6 +63,34 @@ __device__ __forceinline__ void weight_at(const C& col, const void* w, bool wide
   else
     col.param(static_cast<const T*>(w), j, 1.f, x);
 }
+
+// The weight at a lane's columns: held from the start (HOLD), so that no row waits for it behind its
+// sums, or loaded where a row needs it, in a forward of sixteen wavefronts a row, which has no
+// registers to spare, and in one to 16 bits that passes by the caches, where the wavefronts that
+// the registers cost matter more. Held and not: to 8 bits [3000, 6000] bf16 27.4 and 30.7 us,
+// without a residual 16.6 and 21.2, [65536, 4096] 292 and 300; 16 bits [20001, 1025] fp16 34.9 and
+// 36.8, [65536, 4096] 388 and 366; backward [8192, 4096] bf16 52.9 and 55.3, [4099, 2051] fp16 18.3
+// and 21.3, [20001, 1025] 40.0 and 48.5.
+template <class T, class C, int VE, int NV, bool HOLD>
+struct Weight {
+  const void* p;
+  bool wide;
+  float held[HOLD ? NV : 1][VE];
+  __device__ __forceinline__ Weight(const C& col, const void* p_, bool wide_) : p(p_), wide(wide_) {
+    if constexpr (HOLD) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j) weight_at<T>(col, p, wide, j, held[j]);
+    }
+  }
+  __device__ __forceinline__ void get(const C& col, int j, float (&x)[VE]) const {
+    if constexpr (HOLD) {
+#pragma unroll
+      for (int q = 0; q < VE; ++q) x[q] = held[j][q];
+    } else {
+      weight_at<T>(col, p, wide, j, x);
+    }
+  }
+};
 
 struct RmsFwd {
   const void *x, *residual, *weight;
@@ -95,6 +128,7 @@ __device__ __forceinline__ void store_row_fp8(const C& col, const RmsFwd& a, int
 template <class T, int WPR, int EPL, bool FULL, bool STREAM, bool FP8>
 __global__ void __launch_bounds__(norm_threads(WPR, kFwdThreads)) rmsnorm_fwd_kernel(RmsFwd a) {
   // x, residual, sum and y may share rows: a row is in registers before any of it is written
+  constexpr bool kHold = WPR < 16 && (FP8 || !STREAM);
   constexpr int VE = Elem<T>::kVec, NV = EPL / VE, RG = norm_threads(WPR, kFwdThreads) / (64 * WPR);
   __shared__ float red[2][norm_threads(WPR, kFwdThreads) / 64][1];
   const int lane = threadIdx.x % (64 * WPR), group = threadIdx.x / (64 * WPR);
@@ -102,6 +136,7 @@ __global__ void __launch_bounds__(norm_threads(WPR, kFwdThreads)) rmsnorm_fwd_ke
   const T* x = static_cast<const T*>(a.x);
   const T* add = static_cast<const T*>(a.residual);
   const Columns<VE, NV, 64 * WPR, FULL> col(lane, a.h);
+  const Weight<T, Columns<VE, NV, 64 * WPR, FULL>, VE, NV, kHold> weight(col, a.weight, a.wide);
   const int64_t step = int64_t(gridDim.x) * RG;
   int64_t r = int64_t(blockIdx.x) * RG + group;
   raw4 next[NV], nadd[NV];  // the row after the one being worked on
@@ -149,7 +184,7 @@ __global__ void __launch_bounds__(norm_threads(WPR, kFwdThreads)) rmsnorm_fwd_ke
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       float w[VE];
-      weight_at<T>(col, a.weight, a.wide, j, w);
+      weight.get(col, j, w);
 #pragma unroll
       for (int q = 0; q < VE; ++q) v[j][q] = v[j][q] * rstd * w[q];
     }
@@ -191,6 +226,7 @@ __global__ void __launch_bounds__(norm_threads(WPR, kBwdThreads)) rmsnorm_bwd_ke
   const T* gs = static_cast<const T*>(a.grad_sum);
   T* dx = static_cast<T*>(a.dx);
   const Columns<VE, NV, 64 * WPR, FULL> col(lane, a.h);
+  const Weight<T, Columns<VE, NV, 64 * WPR, FULL>, VE, NV, true> weight(col, a.weight, a.wide);
   float dw[NV][VE] = {};
   const int64_t step = int64_t(gridDim.x) * RG;
   int64_t r = int64_t(blockIdx.x) * RG + group;
@@ -226,7 +262,7 @@ __global__ void __launch_bounds__(norm_threads(WPR, kBwdThreads)) rmsnorm_bwd_ke
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       float w[VE];
-      weight_at<T>(col, a.weight, a.wide, j, w);
+      weight.get(col, j, w);
 #pragma unroll
       for (int q = 0; q < VE; ++q) {
         xh[j][q] *= rs;
@@ -286,7 +322,7 @@ __global__ void __launch_bounds__(norm_threads(WPR, kBwdThreads)) rmsnorm_bwd_ke
   }
 }
 
-// Rows past kRegRow: no sums of dw, and the row is widened anew for each of its two uses, since 32
+// Rows past kRegRowOf: no sums of dw, and the row is widened anew for each of its two uses, since 32
 // numbers a lane of x and grad with the next row's do not fit the registers of sixteen wavefronts
 // ([4096, 20000] bf16 with the gradient of the sum: 146 us beside the 90 of its columns, and 287 as
 // the shorter rows are done).
@@ -413,12 +449,12 @@ hipError_t run_fwd(const RmsFwd& a, hipStream_t s) {
 template <class T>
 hipError_t run_bwd_rows(const RmsBwd& a, hipStream_t s) {
   if (a.n == 0) return hipSuccess;
-  if (a.h > kRegRow && a.part) {
+  if (a.h > kRegRowOf<T> && a.part) {
     constexpr int VE = Elem<T>::kVec;
     TimedLaunch t(s, K_RMS_BWD);
     hipLaunchKernelGGL((rms_columns_kernel<T>),
                        dim3(unsigned((a.h + 256 * VE - 1) / (256 * VE)),
-                            unsigned(part_rows(a.n, a.h))),
+                            unsigned(part_rows<T>(a.n, a.h))),
                        dim3(256), 0, s, static_cast<const T*>(a.grad), a.ldg,
                        static_cast<const T*>(a.x), a.ldx, a.rstd, a.n, int64_t(a.h), a.part);
     const hipError_t e = hipGetLastError();
@@ -427,7 +463,7 @@ hipError_t run_bwd_rows(const RmsBwd& a, hipStream_t s) {
   return with_shape<kBwdElems>(a.h, [&](auto wpr, auto epl) {
     constexpr int WPR = decltype(wpr)::value, EPL = decltype(epl)::value;
     constexpr int RG = norm_threads(WPR, kBwdThreads) / (64 * WPR);
-    constexpr bool PARAMS = 64 * WPR * EPL <= kRegRow;
+    constexpr bool PARAMS = 64 * WPR * EPL <= kRegRowOf<T>;
     const int64_t grid = std::min<int64_t>((a.n + RG - 1) / RG, PARAMS ? bwd_grid(a.h) : kLongGrid);
     TimedLaunch t(s, K_RMS_BWD);
     auto launch = [&](auto kernel) {
@@ -450,8 +486,9 @@ hipError_t run_bwd_rows(const RmsBwd& a, hipStream_t s) {
 }
 
 // Partial rows that run_bwd_rows() leaves.
+template <class T>
 int64_t rows_left(int64_t n, int64_t h) {
-  if (n == 0 || h > kRegRow) return part_rows(n, h);
+  if (n == 0 || h > kRegRowOf<T>) return part_rows<T>(n, h);
   int64_t rows = 0;
   (void)with_shape<kBwdElems>(h, [&](auto wpr, auto) {
     constexpr int WPR = decltype(wpr)::value;
@@ -478,7 +515,8 @@ hipError_t rmsnorm_fwd_run(const RmsFwdArgs& a, hipStream_t s) {
 }
 
 size_t rmsnorm_workspace_bytes(int64_t n, int64_t h) {
-  return std::max<size_t>(align256(size_t(part_rows(n, h)) * size_t(h) * 4), 256);
+  // the 16-bit types' partial rows are no fewer than fp32's
+  return std::max<size_t>(align256(size_t(part_rows<Bf16>(n, h)) * size_t(h) * 4), 256);
 }
 
 hipError_t rmsnorm_bwd_run(const RmsBwdArgs& a, hipStream_t s) {
@@ -495,7 +533,7 @@ hipError_t rmsnorm_bwd_run(const RmsBwdArgs& a, hipStream_t s) {
     default: e = run_bwd_rows<float>(k, s);
   }
   if (e != hipSuccess || !part) return e;
-  const int64_t rows = rows_left(a.n, a.h);
+  const int64_t rows = a.dtype == kF32 ? rows_left<float>(a.n, a.h) : rows_left<Bf16>(a.n, a.h);
   switch (a.grad_param_dtype) {
     case kBF16: return run_reduce<Bf16>(part, nullptr, rows, a.h, add, a.grad_weight, nullptr, s);
     case kF16:
