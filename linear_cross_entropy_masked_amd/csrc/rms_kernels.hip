@@ -13,6 +13,7 @@
 // columns is 16 (fp32: 32) neighbouring lanes' vectors, so its largest element takes four or five
 // lane exchanges and no LDS.
 #include <algorithm>
+#include <type_traits>
 
 #include "common.h"
 #include "elem.h"
@@ -67,10 +68,9 @@ __device__ __forceinline__ void weight_at(const C& col, const void* w, bool wide
 // The weight at a lane's columns: held from the start (HOLD), so that no row waits for it behind its
 // sums, or loaded where a row needs it, in a forward of sixteen wavefronts a row, which has no
 // registers to spare, and in one to 16 bits that passes by the caches, where the wavefronts that
-// the registers cost matter more. Held and not: to 8 bits [3000, 6000] bf16 27.4 and 30.7 us,
-// without a residual 16.6 and 21.2, [65536, 4096] 292 and 300; 16 bits [20001, 1025] fp16 34.9 and
-// 36.8, [65536, 4096] 388 and 366; backward [8192, 4096] bf16 52.9 and 55.3, [4099, 2051] fp16 18.3
-// and 21.3, [20001, 1025] 40.0 and 48.5.
+// the registers cost matter more. Held and not: to 8 bits [8192, 8192] bf16 76.5 and 82.0 us, [65536,
+// 4096] 292 and 300; 16 bits [20001, 1025] fp16 34.9 and 36.8, [65536, 4096] 388 and 366; backward
+// [8192, 4096] bf16 52.9 and 55.3, [4099, 2051] fp16 18.3 and 21.3, [20001, 1025] 40.0 and 48.5.
 template <class T, class C, int VE, int NV, bool HOLD>
 struct Weight {
   const void* p;
@@ -106,31 +106,100 @@ struct RmsFwd {
   bool pow2;
 };
 
-template <bool POW2, class T, int VE, int NV, class C>
+// The wavefront's sum in all lanes; no step goes through LDS.
+__device__ __forceinline__ double wave_add_f64(double x) {
+  auto lanes = [&](auto ctrl) {
+    constexpr int CTRL = decltype(ctrl)::value;
+    const uint64_t u = __double_as_longlong(x);
+    const uint32_t lo = __builtin_amdgcn_update_dpp(0, int(u), CTRL, 0xf, 0xf, true);
+    const uint32_t hi = __builtin_amdgcn_update_dpp(0, int(u >> 32), CTRL, 0xf, 0xf, true);
+    x += __longlong_as_double(uint64_t(hi) << 32 | lo);
+  };
+  lanes(std::integral_constant<int, 0xB1>{});   // lane ^ 1
+  lanes(std::integral_constant<int, 0x4E>{});   // lane ^ 2
+  lanes(std::integral_constant<int, 0x141>{});  // mirrored within 8
+  lanes(std::integral_constant<int, 0x140>{});  // mirrored within 16
+  auto halves = [&](auto swap) {
+    const uint64_t u = __double_as_longlong(x);
+    const auto lo = swap(int(u)), hi = swap(int(u >> 32));
+    x = __longlong_as_double(uint64_t(uint32_t(hi[0])) << 32 | uint32_t(lo[0])) +
+        __longlong_as_double(uint64_t(uint32_t(hi[1])) << 32 | uint32_t(lo[1]));
+  };
+  halves([](int v) { return __builtin_amdgcn_permlane16_swap(v, v, false, false); });
+  halves([](int v) { return __builtin_amdgcn_permlane32_swap(v, v, false, false); });
+  return x;
+}
+
+// The sum over the WPR wavefronts that share a row, in wavefront order; `red` as for row_sums().
+// In fp64 from the lanes' fp32 sums on, so that what it is off by is their few roundings averaged
+// over all lanes.
+template <int WPR>
+__device__ __forceinline__ double row_sum_f64(double x, double* red) {
+  x = wave_add_f64(x);
+  if constexpr (WPR > 1) {
+    const int wave = threadIdx.x >> 6;
+    if ((threadIdx.x & 63) == 0) red[wave] = x;
+    __syncthreads();
+    const int w0 = wave / WPR * WPR;
+    x = red[w0];
+#pragma unroll
+    for (int w = 1; w < WPR; ++w) x += red[w0 + w];
+  }
+  return x;
+}
+
+// A row's sums v as y = v · rstd · weight in 8 bits. A block whose largest y lies within rounding of
+// 448 · 2^k, where a scale that is a power of two doubles, has that y formed again in fp64 from
+// the sum of squares `sum`: one in 500 000 blocks, of which fp32 would put some on the wrong side,
+// with twice or half the definition's scale. The registers of that, kept to 128 by the launch
+// bounds, cost rows of 24 elements a lane a tenth ([3000, 6000] bf16 30.0 us, 27.4 without), those
+// of 16 nothing.
+template <bool POW2, class T, int VE, int NV, class C, class W>
 __device__ __forceinline__ void store_row_fp8(const C& col, const RmsFwd& a, int64_t r, int lane,
-                                              int stride, const float (&y)[NV][VE]) {
+                                              int stride, const float (&v)[NV][VE], const W& weight,
+                                              float rstd, double sum) {
   constexpr int kLanes = kFp8Block / VE;  // of a block
+  constexpr uint32_t kNear = 8;           // fp32 steps, of which rstd and two products are off by 3
   uint8_t* q = static_cast<uint8_t*>(a.y) + r * a.ldy;
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
+    float w[VE], y[VE];
+    weight.get(col, j, w);
     uint32_t top = 0;
 #pragma unroll
-    for (int e = 0; e < VE; ++e)
-      if (col.counts(j, e)) top = abs_bits(y[j][e]) > top ? abs_bits(y[j][e]) : top;
+    for (int e = 0; e < VE; ++e) {
+      y[e] = v[j][e] * rstd * w[e];
+      if (col.counts(j, e)) top = abs_bits(y[e]) > top ? abs_bits(y[e]) : top;
+    }
     top = max_of_16<kLanes == 32>(top);
+    if constexpr (POW2) {
+      const bool near = top < kInfBits && (top & 0x7fffffu) - (0x600000u - kNear) <= 2 * kNear;
+      if (__any(near)) {
+        const double r64 = 1.0 / sqrt(sum / a.h + a.eps);
+        double big = 0.0;
+#pragma unroll
+        for (int e = 0; e < VE; ++e)
+          if (col.counts(j, e)) big = fmax(big, fabs(double(v[j][e]) * r64 * w[e]));
+#pragma unroll
+        for (int off = 1; off < kLanes; off <<= 1) big = fmax(big, __shfl_xor(big, off, 64));
+        // times 448 it stays on its side of the power of two
+        if (near) top = abs_bits(float(big / kFp8Max) * kFp8Max);
+      }
+    }
     if (!col.live(j)) continue;
     const BlockScale<POW2> s(top);
-    store_fp8<POW2, VE>(q + col.at[j], s, y[j], col.skip[j], a.h - col.at[j]);
+    store_fp8<POW2, VE>(q + col.at[j], s, y, col.skip[j], a.h - col.at[j]);
     if (lane % kLanes == 0) s.store(a.scales, int64_t((lane + j * stride) / kLanes) * a.lds + r);
   }
 }
 
 template <class T, int WPR, int EPL, bool FULL, bool STREAM, bool FP8>
-__global__ void __launch_bounds__(norm_threads(WPR, kFwdThreads)) rmsnorm_fwd_kernel(RmsFwd a) {
+__global__ void __launch_bounds__(norm_threads(WPR, kFwdThreads), FP8 && EPL <= 24 ? 4 : 1)
+    rmsnorm_fwd_kernel(RmsFwd a) {
   // x, residual, sum and y may share rows: a row is in registers before any of it is written
   constexpr bool kHold = WPR < 16 && (FP8 || !STREAM);
   constexpr int VE = Elem<T>::kVec, NV = EPL / VE, RG = norm_threads(WPR, kFwdThreads) / (64 * WPR);
-  __shared__ float red[2][norm_threads(WPR, kFwdThreads) / 64][1];
+  __shared__ double red[2][norm_threads(WPR, kFwdThreads) / 64];
   const int lane = threadIdx.x % (64 * WPR), group = threadIdx.x / (64 * WPR);
   const float fh = float(a.h);
   const T* x = static_cast<const T*>(a.x);
@@ -166,14 +235,14 @@ __global__ void __launch_bounds__(norm_threads(WPR, kFwdThreads)) rmsnorm_fwd_ke
       }
     }
     if (base + step < a.n) fetch(r + step);
-    float s[1] = {0.f};
+    float s = 0.f;
 #pragma unroll
     for (int j = 0; j < NV; ++j)
 #pragma unroll
-      for (int q = 0; q < VE; ++q) s[0] += col.counts(j, q) ? v[j][q] * v[j][q] : 0.f;
-    row_sums<WPR, 1>(s, red[parity]);
+      for (int q = 0; q < VE; ++q) s += col.counts(j, q) ? v[j][q] * v[j][q] : 0.f;
+    const double sum = row_sum_f64<WPR>(s, red[parity]);
     parity ^= 1;
-    const float rstd = 1.f / sqrtf(s[0] / fh + a.eps);
+    const float rstd = 1.f / sqrtf(float(sum) / fh + a.eps);
     if (r >= a.n) continue;
     if (a.sum) {
       T* sr = static_cast<T*>(a.sum) + r * a.ldsum;
@@ -181,23 +250,21 @@ __global__ void __launch_bounds__(norm_threads(WPR, kFwdThreads)) rmsnorm_fwd_ke
       for (int j = 0; j < NV; ++j)
         if (col.live(j)) col.template store<STREAM>(sr, j, v[j]);
     }
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      float w[VE];
-      weight.get(col, j, w);
-#pragma unroll
-      for (int q = 0; q < VE; ++q) v[j][q] = v[j][q] * rstd * w[q];
-    }
     if constexpr (FP8) {
       if (a.pow2)
-        store_row_fp8<true, T>(col, a, r, lane, 64 * WPR, v);
+        store_row_fp8<true, T>(col, a, r, lane, 64 * WPR, v, weight, rstd, sum);
       else
-        store_row_fp8<false, T>(col, a, r, lane, 64 * WPR, v);
+        store_row_fp8<false, T>(col, a, r, lane, 64 * WPR, v, weight, rstd, sum);
     } else {
       T* yr = static_cast<T*>(a.y) + r * a.ldy;
 #pragma unroll
-      for (int j = 0; j < NV; ++j)
-        if (col.live(j)) col.template store<STREAM>(yr, j, v[j]);
+      for (int j = 0; j < NV; ++j) {
+        float w[VE];
+        weight.get(col, j, w);
+#pragma unroll
+        for (int q = 0; q < VE; ++q) w[q] = v[j][q] * rstd * w[q];
+        if (col.live(j)) col.template store<STREAM>(yr, j, w);
+      }
     }
     if (lane == 0 && a.rstd) a.rstd[r] = rstd;
   }

@@ -157,6 +157,29 @@ def test_fp8_forward(dev, h, dtype, scale):
         check_fp8(exact_norm(s, w)[0], q, c)
 
 
+@pytest.mark.parametrize("h", [4096, 8200, 32768])
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_fp8_scales_beside_powers_of_two(dev, h, dtype):
+    """Blocks whose largest y / 448 lies within a few fp32 steps of a power of two get the scale of
+    the definition. The rows are whole numbers, so that their sums of squares are exact."""
+    gen = torch.Generator().manual_seed(h)
+    x = torch.randint(-2, 3, (40, h), generator=gen).double()
+    at = torch.arange(0, h, 128) + torch.randint(0, 128 if h % 128 == 0 else 8, (-(-h // 128),),
+                                                 generator=gen)
+    x[:, at] = torch.randint(3, 8, (40, len(at)), generator=gen).double()
+    r = 1 / torch.sqrt((x * x).mean(1, keepdim=True) + torch.tensor(EPS).double())
+    for row in range(0, 40, 4):
+        w = torch.zeros(h)
+        steps = torch.randint(-3, 4, (len(at),), generator=gen).double() * 2.0 ** -23
+        scale = 2.0 ** torch.randint(-12, 3, (len(at),), generator=gen).double()
+        w[at] = (448 * scale / (x * r)[row, at] * (1 + steps)).float()
+        q, c, _ = lce.rmsnorm_fp8_fwd(x.to(dtype).to(dev), w.to(dev), eps=EPS)
+        top = torch.nn.functional.pad((x * r * w.double()).abs(), (0, -h % 128)).view(40, -1, 128)
+        exact = (top.amax(-1) / 448).float().double()
+        assert torch.equal(c.view(torch.uint8).t().cpu().double(),
+                           torch.ceil(torch.log2(exact)) + 127)
+
+
 def test_fp8_is_the_quantised_norm(dev):
     """In fp32 rows nothing is rounded between: the 8-bit form is the quantiser of the norm."""
     x, r, w, _ = inputs(37, 1000, torch.float32, torch.float32, dev)
