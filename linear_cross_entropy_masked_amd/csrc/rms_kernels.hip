@@ -148,19 +148,33 @@ __device__ __forceinline__ double row_sum_f64(double x, double* red) {
   return x;
 }
 
-// A row's sums v as y = v · rstd · weight in 8 bits. A block whose largest y lies within rounding of
-// 448 · 2^k, where a scale that is a power of two doubles, has that y formed again in fp64 from
-// the sum of squares `sum`: one in 500 000 blocks, of which fp32 would put some on the wrong side,
-// with twice or half the definition's scale. The registers of that, kept to 128 by the launch
-// bounds, cost rows of 24 elements a lane a tenth ([3000, 6000] bf16 30.0 us, 27.4 without), those
-// of 16 nothing.
+// 1 / sqrt(mean + eps) in two parts, and v times it times w rounded once.
+struct Rstd {
+  double exact;
+  float hi, lo;
+  __device__ __forceinline__ Rstd(double sum, const RmsFwd& a)
+      : exact(1.0 / sqrt(sum / a.h + a.eps)), hi(float(exact)), lo(float(exact - hi)) {}
+  __device__ __forceinline__ float times(float v, float w) const {
+    const float p = v * hi;
+    if (!(hi < INFINITY)) return p * w;  // eps and all of the row 0
+    return fmaf(p, w, fmaf(v, lo, fmaf(v, hi, -p)) * w);
+  }
+};
+
+// A row's sums v as y = v · rstd · weight in 8 bits. With rstd in two parts and what the product
+// with v is off by carried along, y is the real number rounded once to fp32, so that no second
+// rounding moves it past a tie of the 8-bit numbers (one in 200 000). A block whose largest y then
+// lies beside 448 · 2^k, where a scale that is a power of two doubles, has it formed in fp64. The
+// registers of that, kept to 128 by the launch bounds, cost rows of 24 elements a lane a tenth
+// ([3000, 6000] bf16 30.0 us, 27.4 without), those of 16 nothing.
 template <bool POW2, class T, int VE, int NV, class C, class W>
 __device__ __forceinline__ void store_row_fp8(const C& col, const RmsFwd& a, int64_t r, int lane,
                                               int stride, const float (&v)[NV][VE], const W& weight,
-                                              float rstd, double sum) {
+                                              double sum) {
   constexpr int kLanes = kFp8Block / VE;  // of a block
-  constexpr uint32_t kNear = 8;           // fp32 steps, of which rstd and two products are off by 3
+  constexpr uint32_t kNear = 2;           // fp32 steps
   uint8_t* q = static_cast<uint8_t*>(a.y) + r * a.ldy;
+  const Rstd rs(sum, a);
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
     float w[VE], y[VE];
@@ -168,18 +182,17 @@ __device__ __forceinline__ void store_row_fp8(const C& col, const RmsFwd& a, int
     uint32_t top = 0;
 #pragma unroll
     for (int e = 0; e < VE; ++e) {
-      y[e] = v[j][e] * rstd * w[e];
+      y[e] = rs.times(v[j][e], w[e]);
       if (col.counts(j, e)) top = abs_bits(y[e]) > top ? abs_bits(y[e]) : top;
     }
     top = max_of_16<kLanes == 32>(top);
     if constexpr (POW2) {
       const bool near = top < kInfBits && (top & 0x7fffffu) - (0x600000u - kNear) <= 2 * kNear;
       if (__any(near)) {
-        const double r64 = 1.0 / sqrt(sum / a.h + a.eps);
         double big = 0.0;
 #pragma unroll
         for (int e = 0; e < VE; ++e)
-          if (col.counts(j, e)) big = fmax(big, fabs(double(v[j][e]) * r64 * w[e]));
+          if (col.counts(j, e)) big = fmax(big, fabs(double(v[j][e]) * rs.exact * w[e]));
 #pragma unroll
         for (int off = 1; off < kLanes; off <<= 1) big = fmax(big, __shfl_xor(big, off, 64));
         // times 448 it stays on its side of the power of two
@@ -252,17 +265,19 @@ __global__ void __launch_bounds__(norm_threads(WPR, kFwdThreads), FP8 && EPL <= 
     }
     if constexpr (FP8) {
       if (a.pow2)
-        store_row_fp8<true, T>(col, a, r, lane, 64 * WPR, v, weight, rstd, sum);
+        store_row_fp8<true, T>(col, a, r, lane, 64 * WPR, v, weight, sum);
       else
-        store_row_fp8<false, T>(col, a, r, lane, 64 * WPR, v, weight, rstd, sum);
+        store_row_fp8<false, T>(col, a, r, lane, 64 * WPR, v, weight, sum);
     } else {
       T* yr = static_cast<T*>(a.y) + r * a.ldy;
+      const Rstd rs(sum, a);  // fp32 rows: the numbers that the 8-bit form rounds
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
         float w[VE];
         weight.get(col, j, w);
 #pragma unroll
-        for (int q = 0; q < VE; ++q) w[q] = v[j][q] * rstd * w[q];
+        for (int q = 0; q < VE; ++q)
+          w[q] = sizeof(T) == 4 ? rs.times(v[j][q], w[q]) : v[j][q] * rstd * w[q];
         if (col.live(j)) col.template store<STREAM>(yr, j, w);
       }
     }
