@@ -501,7 +501,8 @@ int rmsnorm_workspace_size(int64_t n, int64_t h, size_t* bytes);
  * that depends on n and h alone, without atomics.
  *   grad, x, grad_residual, grad_x  dtype, row strides >= h. grad_residual: the gradient of s
  *                 where the model uses it further, or NULL. grad_x may be NULL, or the rows of
- *                 grad or of grad_residual (same pointer, same stride)
+ *                 grad or of grad_residual (same pointer, same stride). Without grad_x and
+ *                 grad_weight nothing is launched
  *   grad_weight   grad_param_dtype [h] or NULL; param_dtype or LCE_DTYPE_F32. With n == 0 it is
  *                 set to 0, or left as it is with RMSNORM_ACCUMULATE */
 int rmsnorm_bwd(const void* grad, int dtype, int64_t ldg, const void* x, int64_t ldx,
