@@ -159,6 +159,11 @@ struct Rstd {
     if (!(hi < INFINITY)) return p * w;  // eps and all of the row 0
     return fmaf(p, w, fmaf(v, lo, fmaf(v, hi, -p)) * w);
   }
+  // The same for a weight that may be infinite, beside which what p is off by would count as 0 · inf
+  // or inf - inf. A block of 8 bits is NaN throughout either way.
+  __device__ __forceinline__ float times_any(float v, float w) const {
+    return fabsf(w) < INFINITY ? times(v, w) : v * hi * w;
+  }
 };
 
 // A row's sums v as y = v · rstd · weight in 8 bits. With rstd in two parts and what the product
@@ -277,7 +282,7 @@ __global__ void __launch_bounds__(norm_threads(WPR, kFwdThreads), FP8 && EPL <= 
         weight.get(col, j, w);
 #pragma unroll
         for (int q = 0; q < VE; ++q)
-          w[q] = sizeof(T) == 4 ? rs.times(v[j][q], w[q]) : v[j][q] * rstd * w[q];
+          w[q] = sizeof(T) == 4 ? rs.times_any(v[j][q], w[q]) : v[j][q] * rstd * w[q];
         if (col.live(j)) col.template store<STREAM>(yr, j, w);
       }
     }

@@ -39,3 +39,36 @@ def test_backward_of_nothing(dev, h, dtype):
     dx, dw = lce.rmsnorm_bwd(g, x, rstd, w)
     assert torch.equal(lce.rmsnorm_bwd(g, x, rstd, w, grad_weight=False)[0], dx)
     assert torch.equal(lce.rmsnorm_bwd(g, x, rstd, w, grad_x=False)[1], dw)
+
+
+@pytest.mark.parametrize("h", [48, 1000, 4096, 20003])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
+def test_special_weights(dev, h, dtype):
+    """Weights that are infinite, NaN, zero, or so large that some results overflow: y is s · rstd ·
+    weight of the definition in 64 bits, rounded to its type. Finite results: the tolerance of
+    test_rmsnorm_gpu.py, 36 roundings of 2^-24 for rstd and the products, and half a step."""
+    gen = torch.Generator().manual_seed(h)
+    x = (torch.randn(7, h, generator=gen) * 2).to(dtype)
+    x[3, ::5] = 0
+    w = 1 + 0.2 * torch.randn(h, generator=gen)
+    inf, big = float("inf"), torch.finfo(dtype).max
+    for k, value in enumerate((inf, -inf, float("nan"), 0.0, big, -big)):
+        w[k::40] = value
+    x, w = x.to(dev), w.to(dtype).to(dev)
+    for weight in (w, w.float()):
+        y, _, _ = lce.rmsnorm_fwd(x, weight, eps=EPS)
+        sd = x.double()
+        exact = sd * ((sd * sd).mean(1, keepdim=True) + EPS).rsqrt() * weight.double()
+        nan = torch.isnan(exact)
+        assert torch.equal(torch.isnan(y), nan)
+        # beside the largest number either side of the overflow is right
+        near = (exact.abs() / big - 1).abs() < 2 * torch.finfo(dtype).eps
+        far = exact.abs() > big
+        some = ~nan & ~near
+        assert torch.equal(y[some & far], torch.copysign(torch.full_like(y, inf),
+                                                         exact.to(y.dtype))[some & far])
+        few = some & ~far
+        f = torch.finfo(dtype)
+        half = torch.clamp(exact.abs() * (f.eps / 2), min=f.smallest_normal * f.eps / 2)
+        err = (y.double() - exact).abs()
+        assert (err[few] <= (1.01 * (36 * 2.0 ** -24 * exact.abs() + half))[few]).all()
