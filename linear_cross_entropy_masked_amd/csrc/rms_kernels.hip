@@ -160,9 +160,14 @@ struct Rstd {
     return fmaf(p, w, fmaf(v, lo, fmaf(v, hi, -p)) * w);
   }
   // The same for a weight that may be infinite, beside which what p is off by would count as 0 · inf
-  // or inf - inf. A block of 8 bits is NaN throughout either way.
+  // or inf - inf: kept finite (a NaN among the three becomes the least), which a finite weight's is.
+  // A block of 8 bits is NaN throughout either way. A branch on the weight instead cost [20001, 1025]
+  // fp32 71.0 us, 66.5 without it.
   __device__ __forceinline__ float times_any(float v, float w) const {
-    return fabsf(w) < INFINITY ? times(v, w) : v * hi * w;
+    const float p = v * hi;
+    if (!(hi < INFINITY)) return p * w;
+    const float off = fmaf(v, lo, fmaf(v, hi, -p)) * w;
+    return fmaf(p, w, __builtin_amdgcn_fmed3f(off, -__FLT_MAX__, __FLT_MAX__));
   }
 };
 
