@@ -535,7 +535,8 @@ int fp8_matmul_workspace_size(int64_t m, int64_t n, int64_t k, size_t* bytes);
  *   a_scales  [ceil(k / 128), ldas]      b_scales  [ceil(n / 128), ldbs]
  *   bias  fp32 [n] or NULL               out  out_dtype [m, ldo], first n columns
  * k a multiple of 16; k <= 2^20, lda and ldb <= 2^22, m <= 2^23, n <= 2^28, fewer than 2^22 tiles
- * of 256 x 256. With fp32 scales the product of a row's and a column's scale is formed in fp32.
+ * of 256 x 256. With fp32 scales the product of a row's and a column's scale is formed in fp32; with
+ * powers of two it may leave fp32 where the block's term of the result does not.
  * m == 0 is valid. */
 int fp8_matmul(const uint8_t* a, int64_t lda, const void* a_scales, int64_t ldas,
                const uint8_t* b, int64_t ldb, const void* b_scales, int64_t ldbs, int scale_dtype,

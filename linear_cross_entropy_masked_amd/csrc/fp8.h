@@ -19,6 +19,7 @@ constexpr int kFp8Block = 128;
 constexpr float kFp8Max = 448.f;
 constexpr uint32_t kInfBits = 0x7f800000u;
 constexpr uint32_t kNanBits = 0x7fc00000u;
+constexpr uint32_t kOneBits = 0x3f800000u;
 
 // |x| as an integer that orders like the number, NaN above infinity: the largest of a block then
 // keeps a NaN, which a floating-point maximum drops.
