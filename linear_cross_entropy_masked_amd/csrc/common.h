@@ -131,6 +131,7 @@ enum KernelId {
   K_RMS_BWD,
   K_FP8_QUANTIZE,
   K_FP8_MATMUL,
+  K_FP8_MATMUL_LARGE,
   K_FP8_MATMUL_FEW,
   K_FP8_JOIN,
   K_BEAM_ROWS,

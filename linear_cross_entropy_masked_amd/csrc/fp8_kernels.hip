@@ -771,7 +771,7 @@ Plan plan_of(int64_t m, int64_t n, int64_t k, bool precise) {
 
 template <class C, bool E8M0, bool PRECISE, class T>
 hipError_t launch_tiles(const MatmulK& k, const Plan& p, hipStream_t s) {
-  TimedLaunch t(s, K_FP8_MATMUL);
+  TimedLaunch t(s, C::BM == Wide::BM ? K_FP8_MATMUL_LARGE : K_FP8_MATMUL);
   hipLaunchKernelGGL((fp8_matmul_kernel<C, E8M0, PRECISE, T>),
                      dim3(unsigned(p.m_tiles * p.n_tiles * p.splits)), dim3(C::THREADS), 0, s, k);
   return hipGetLastError();

@@ -47,9 +47,9 @@ const char* kNames[K_COUNT] = {
     "piece_state",        "piece_grad_logits",     "piece_grad_hidden",
     "piece_grad_weight",  "piece_grad_finish",   "piece_grads",
     "rmsnorm_fwd",        "rmsnorm_fp8_fwd",       "rmsnorm_bwd",
-    "fp8_quantize",       "fp8_matmul",            "fp8_matmul_few",
-    "fp8_join",           "beam_rows",             "beam_pick",
-    "beam_reorder",
+    "fp8_quantize",       "fp8_matmul",            "fp8_matmul_large",
+    "fp8_matmul_few",     "fp8_join",              "beam_rows",
+    "beam_pick",          "beam_reorder",
 };
 
 }  // namespace
