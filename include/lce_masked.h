@@ -529,8 +529,15 @@ int fp8_matmul_workspace_size(int64_t m, int64_t n, int64_t k, size_t* bytes);
 
 /* out[m, n] = sum_b a_scales[b, m] * b_scales[n / 128, b] * (sum over the columns k of block b of
  * a[m, k] * b[n, k]) + bias[n], the product of two matrices as fp8_quantize leaves them (a with
- * block_rows 1, b with 128, both scale types alike). fp32 sums, rounded once to out_dtype. The
- * logits of a head held in 8 bits; no gradients.
+ * block_rows 1, b with 128, both scale types alike), rounded once to out_dtype. The logits of a
+ * head held in 8 bits; no gradients. The sums are fp32, with one exception: those of bf16 outputs
+ * of more than 64 rows are formed by 8-bit matrix instructions, which add the products of eight
+ * neighbouring columns on a grid of 2^-13 of the largest one's power of two, cutting what lies below,
+ * and only the sums of eight in fp32. Each group of eight columns then adds an error of up to 2^-10 of
+ * the product of the group's largest |a| and |b| (scales included): for normally distributed
+ * operands 1.4e-5 of the result's size, a hundredth of a bf16 step; where large products cancel, far
+ * more of the result than fp32 sums lose. fp8_matmul_precise forms fp32 sums whatever out_dtype and
+ * m, in 1.2 to 2.2 times the time of such outputs, with the same workspace.
  *   a  [m, lda], b [n, ldb]  e4m3, first k columns; 16-byte aligned, lda and ldb multiples of 16
  *   a_scales  [ceil(k / 128), ldas]      b_scales  [ceil(n / 128), ldbs]
  *   bias  fp32 [n] or NULL               out  out_dtype [m, ldo], first n columns
@@ -542,6 +549,11 @@ int fp8_matmul(const uint8_t* a, int64_t lda, const void* a_scales, int64_t ldas
                const uint8_t* b, int64_t ldb, const void* b_scales, int64_t ldbs, int scale_dtype,
                const float* bias, int64_t m, int64_t n, int64_t k, void* out, int out_dtype,
                int64_t ldo, void* workspace, size_t workspace_bytes, void* stream);
+int fp8_matmul_precise(const uint8_t* a, int64_t lda, const void* a_scales, int64_t ldas,
+                       const uint8_t* b, int64_t ldb, const void* b_scales, int64_t ldbs,
+                       int scale_dtype, const float* bias, int64_t m, int64_t n, int64_t k,
+                       void* out, int out_dtype, int64_t ldo, void* workspace,
+                       size_t workspace_bytes, void* stream);
 
 /* ------------------------------------------------------------------ beam search */
 

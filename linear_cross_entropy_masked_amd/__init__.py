@@ -9,8 +9,8 @@ function whose library is missing raises.
 Entry points (same names as the C ABI):
     ce_chunked_fwd, ce_chunked_bwd, ce_chunked_bwd_inplace, flce_fwd_bwd, flce_fwd, flce_bwd,
     flce_piece_fwd, flce_piece_loss, flce_piece_bwd, embed_fwd, embed_bwd, layernorm_fwd,
-    layernorm_bwd, rmsnorm_fwd, rmsnorm_fp8_fwd, rmsnorm_bwd, fp8_quantize, fp8_matmul, beam_step,
-    beam_reorder,
+    layernorm_bwd, rmsnorm_fwd, rmsnorm_fp8_fwd, rmsnorm_bwd, fp8_quantize, fp8_matmul
+    (fp8_matmul_precise), beam_step, beam_reorder,
     ce_chunked_workspace_size, flce_workspace_size, embed_workspace_size,
     layernorm_workspace_size, flce_piece_{fwd,loss,bwd}_workspace_size, rmsnorm_workspace_size,
     fp8_matmul_workspace_size, beam_step_workspace_size, lce_status_str
@@ -139,6 +139,8 @@ def load_library() -> ctypes.CDLL:
         "fp8_matmul_workspace_size": (ctypes.c_int, [i64, i64, i64, psz]),
         "fp8_matmul": (ctypes.c_int, [vp, i64, vp, i64, vp, i64, vp, i64, dt, vp, i64, i64, i64, vp,
                                       dt, i64, vp, sz, vp]),
+        "fp8_matmul_precise": (ctypes.c_int, [vp, i64, vp, i64, vp, i64, vp, i64, dt, vp, i64, i64,
+                                              i64, vp, dt, i64, vp, sz, vp]),
         "beam_step_workspace_size": (ctypes.c_int, [i64, i64, i64, i64, psz]),
         "beam_step": (ctypes.c_int, [vp, dt, i64, i64, i64, i64, vp, vp, i32, i64, i32, vp, vp, vp,
                                      vp, vp, vp, sz, vp]),
@@ -997,11 +999,18 @@ def fp8_matmul_workspace_size(m: int, n: int, k: int) -> int:
     return _size("fp8_matmul_workspace_size", m, n, k)
 
 
-def fp8_matmul(a, a_scales, b, b_scales, bias=None, *, out=None, dtype=None, workspace=None):
+def fp8_matmul(a, a_scales, b, b_scales, bias=None, *, out=None, dtype=None, precise: bool = False,
+               workspace=None):
     """a · bᵀ (+ bias) of 8-bit blocks as :func:`fp8_quantize` leaves them: a [m, k] with scales
     [ceil(k / 128), m], b [n, k] with scales [ceil(n / 128), ceil(k / 128)], both scales of one
     type; bias fp32 [n] or None. k is a multiple of 16, and rows start at multiples of 16 bytes.
-    Returns ``out`` [m, n], of ``dtype`` (default bfloat16; float16 or float32). No gradients."""
+    Returns ``out`` [m, n], of ``dtype`` (default bfloat16; float16 or float32). No gradients.
+
+    Sums are fp32, except those of bfloat16 outputs of more than 64 rows: there the products of eight
+    neighbouring columns are added on a grid of 2^-13 of the largest one, which is off by up to 2^-10
+    of the product of the eight's largest |a| and |b| (1.4e-5 of the result's size for normally
+    distributed operands; far more of it where large products cancel). ``precise``: fp32 sums there
+    too, in 1.2 to 2.2 times the time."""
     import torch
     _require(a, "a", torch.float8_e4m3fn, 2)
     dev = a.device
@@ -1029,9 +1038,10 @@ def fp8_matmul(a, a_scales, b, b_scales, bias=None, *, out=None, dtype=None, wor
     ocode = _dtype_code(out.dtype, "out")
     need = fp8_matmul_workspace_size(m, n, k)
     ws = _workspace(need, dev, workspace) if need else None
-    _call("fp8_matmul", dev, a.data_ptr(), lda, a_scales.data_ptr(), ldas, b.data_ptr(), ldb,
-          b_scales.data_ptr(), ldbs, scode, _adr(bias), m, n, k, out.data_ptr(), ocode, ldo,
-          _adr(ws), 0 if ws is None else _bytes_of(ws))
+    _call("fp8_matmul_precise" if precise else "fp8_matmul", dev, a.data_ptr(), lda,
+          a_scales.data_ptr(), ldas, b.data_ptr(), ldb, b_scales.data_ptr(), ldbs, scode,
+          _adr(bias), m, n, k, out.data_ptr(), ocode, ldo, _adr(ws),
+          0 if ws is None else _bytes_of(ws))
     return out
 
 

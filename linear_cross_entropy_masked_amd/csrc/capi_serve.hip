@@ -95,6 +95,41 @@ int matmul_check_shape(int64_t m, int64_t n, int64_t k) {
   return LCE_OK;
 }
 
+int matmul(const uint8_t* a, int64_t lda, const void* a_scales, int64_t ldas, const uint8_t* b,
+           int64_t ldb, const void* b_scales, int64_t ldbs, int scale_dtype, const float* bias,
+           int64_t m, int64_t n, int64_t k, void* out, int out_dtype, int64_t ldo, void* workspace,
+           size_t workspace_bytes, bool precise, void* stream) {
+  int rc = matmul_check_shape(m, n, k);
+  if (rc != LCE_OK) return rc;
+  const int64_t sl = scale_size(scale_dtype), ol = dtype_size(out_dtype);
+  if (!sl || !ol) return LCE_ERR_BAD_DTYPE;
+  const int64_t blocks = blocks_of(k), widest = int64_t(1) << 22;
+  if (lda < k || lda > widest || lda % 16 != 0 || ldb < k || ldb > widest || ldb % 16 != 0 ||
+      ldo < n || ldas < m || ldbs < blocks || !matrix_fits(m, ldo) || !matrix_fits(blocks, ldas) ||
+      !matrix_fits(blocks_of(n), ldbs) || ldbs > widest)
+    return LCE_ERR_BAD_SHAPE;
+  if (!b || !b_scales || (m > 0 && (!a || !a_scales || !out))) return LCE_ERR_NULL_ARG;
+  const size_t need = fp8_matmul_workspace_bytes(m, n, k);
+  if (need > 0 && (!workspace || workspace_bytes < need)) return LCE_ERR_WORKSPACE;
+  if (!aligned(a, 16) || !aligned(b, 16) || !aligned(a_scales, sl) || !aligned(b_scales, sl) ||
+      !aligned(bias, 4) || !aligned(out, ol) || (need > 0 && !aligned(workspace, 256)))
+    return LCE_ERR_ALIGNMENT;
+  {
+    const Span wr[] = {span(need > 0 ? workspace : nullptr, int64_t(need)),
+                       span(out, matrix_bytes(m, ldo, n, ol))};
+    const Span rd[] = {span(a, matrix_bytes(m, lda, k, 1)), span(b, matrix_bytes(n, ldb, k, 1)),
+                       span(a_scales, m > 0 ? matrix_bytes(blocks, ldas, m, sl) : 0),
+                       span(b_scales, matrix_bytes(blocks_of(n), ldbs, blocks, sl)),
+                       span(bias, 4 * n)};
+    if ((rc = check_disjoint(wr, rd)) != LCE_OK) return rc;
+  }
+  if ((rc = check_device()) != LCE_OK) return rc;
+  const Fp8MatmulArgs args{a,    lda, a_scales, ldas, b,   ldb,       b_scales, ldbs,      scale_dtype,
+                           bias, m,   n,        k,    out, out_dtype, ldo,      workspace, precise};
+  LCE_TRY_HIP(fp8_matmul_run(args, static_cast<hipStream_t>(stream)));
+  return LCE_OK;
+}
+
 int beam_check_shape(int64_t batch, int64_t beams, int64_t v, int64_t num) {
   if (batch < 0 || batch > kI32Max || beams < 1 || beams > BEAM_MAX_BEAMS || v < 1 ||
       v > kI32Max || num < 1 || num > BEAM_MAX_CANDIDATES)
@@ -270,35 +305,17 @@ int fp8_matmul(const uint8_t* a, int64_t lda, const void* a_scales, int64_t ldas
                const uint8_t* b, int64_t ldb, const void* b_scales, int64_t ldbs, int scale_dtype,
                const float* bias, int64_t m, int64_t n, int64_t k, void* out, int out_dtype,
                int64_t ldo, void* workspace, size_t workspace_bytes, void* stream) {
-  int rc = matmul_check_shape(m, n, k);
-  if (rc != LCE_OK) return rc;
-  const int64_t sl = scale_size(scale_dtype), ol = dtype_size(out_dtype);
-  if (!sl || !ol) return LCE_ERR_BAD_DTYPE;
-  const int64_t blocks = blocks_of(k), widest = int64_t(1) << 22;
-  if (lda < k || lda > widest || lda % 16 != 0 || ldb < k || ldb > widest || ldb % 16 != 0 ||
-      ldo < n || ldas < m || ldbs < blocks || !matrix_fits(m, ldo) || !matrix_fits(blocks, ldas) ||
-      !matrix_fits(blocks_of(n), ldbs) || ldbs > widest)
-    return LCE_ERR_BAD_SHAPE;
-  if (!b || !b_scales || (m > 0 && (!a || !a_scales || !out))) return LCE_ERR_NULL_ARG;
-  const size_t need = fp8_matmul_workspace_bytes(m, n, k);
-  if (need > 0 && (!workspace || workspace_bytes < need)) return LCE_ERR_WORKSPACE;
-  if (!aligned(a, 16) || !aligned(b, 16) || !aligned(a_scales, sl) || !aligned(b_scales, sl) ||
-      !aligned(bias, 4) || !aligned(out, ol) || (need > 0 && !aligned(workspace, 256)))
-    return LCE_ERR_ALIGNMENT;
-  {
-    const Span wr[] = {span(need > 0 ? workspace : nullptr, int64_t(need)),
-                       span(out, matrix_bytes(m, ldo, n, ol))};
-    const Span rd[] = {span(a, matrix_bytes(m, lda, k, 1)), span(b, matrix_bytes(n, ldb, k, 1)),
-                       span(a_scales, m > 0 ? matrix_bytes(blocks, ldas, m, sl) : 0),
-                       span(b_scales, matrix_bytes(blocks_of(n), ldbs, blocks, sl)),
-                       span(bias, 4 * n)};
-    if ((rc = check_disjoint(wr, rd)) != LCE_OK) return rc;
-  }
-  if ((rc = check_device()) != LCE_OK) return rc;
-  const Fp8MatmulArgs args{a,    lda, a_scales, ldas, b,   ldb,       b_scales, ldbs, scale_dtype,
-                           bias, m,   n,        k,    out, out_dtype, ldo,      workspace};
-  LCE_TRY_HIP(fp8_matmul_run(args, static_cast<hipStream_t>(stream)));
-  return LCE_OK;
+  return matmul(a, lda, a_scales, ldas, b, ldb, b_scales, ldbs, scale_dtype, bias, m, n, k, out,
+                out_dtype, ldo, workspace, workspace_bytes, false, stream);
+}
+
+int fp8_matmul_precise(const uint8_t* a, int64_t lda, const void* a_scales, int64_t ldas,
+                       const uint8_t* b, int64_t ldb, const void* b_scales, int64_t ldbs,
+                       int scale_dtype, const float* bias, int64_t m, int64_t n, int64_t k,
+                       void* out, int out_dtype, int64_t ldo, void* workspace,
+                       size_t workspace_bytes, void* stream) {
+  return matmul(a, lda, a_scales, ldas, b, ldb, b_scales, ldbs, scale_dtype, bias, m, n, k, out,
+                out_dtype, ldo, workspace, workspace_bytes, true, stream);
 }
 
 int beam_step_workspace_size(int64_t batch, int64_t beams, int64_t v, int64_t num, size_t* bytes) {

@@ -14,7 +14,9 @@
 //   precise  the operands widened to bf16, which holds every e4m3 number, and four bf16 MFMAs per
 //            block: exact products and fp32 sums (1e-8), at half the rate. fp16 and fp32 outputs,
 //            which would show the difference, and the products of few rows, which wait for
-//            memory anyway, take it.
+//            memory anyway, take it, and all where the caller asks for it: where large products
+//            cancel, what the fast form cuts is not small beside the result (bf16 outputs of 8192 x
+//            4096 x 128256 in 8.3 ms instead of 3.7, of 1003 x 768 x 32777 in 59 us instead of 42).
 // All other sums are fp32.
 //
 // Tiles: A and B go global -> LDS directly (buffer_load ... lds, 16 bytes a lane) into a ring of
@@ -779,8 +781,9 @@ hipError_t launch_tiles(const MatmulK& k, const Plan& p, hipStream_t s) {
 
 template <bool E8M0, class T>
 hipError_t run_matmul(const Fp8MatmulArgs& a, hipStream_t s) {
-  constexpr bool kPrecise = !std::is_same_v<T, Bf16>;
-  const Plan p = plan_of(a.m, a.n, a.k, kPrecise);
+  constexpr bool kMayBeFast = std::is_same_v<T, Bf16>;
+  const bool precise = !kMayBeFast || a.precise;
+  const Plan p = plan_of(a.m, a.n, a.k, precise);
   MatmulK k{a.a,    a.b,    a.a_scales, a.b_scales, a.bias, a.m,
             a.n,    a.k,    a.lda,      a.ldb,      a.ldas, a.ldbs,
             a.ldo,  a.out,  (a.k + kFp8Block - 1) / kFp8Block, p.per, TileMap{}};
@@ -799,20 +802,26 @@ hipError_t run_matmul(const Fp8MatmulArgs& a, hipStream_t s) {
     return hipGetLastError();
   }
   k.tm = TileMap{p.m_tiles, p.n_tiles, p.splits, true};
-  if constexpr (!kPrecise) {
+  if constexpr (kMayBeFast) {
     if (p.wide) {
       k.tm.band = 8;
       return launch_tiles<Wide, E8M0, false, T>(k, p, s);
     }
   }
-  if (p.splits == 1)
-    return p.thin ? launch_tiles<Thin, E8M0, true, T>(k, p, s)
-                  : launch_tiles<Small, E8M0, kPrecise, T>(k, p, s);
+  // tiles that leave numbers of type To
+  auto tiles = [&](auto to) {
+    using To = decltype(to);
+    if (p.thin) return launch_tiles<Thin, E8M0, true, To>(k, p, s);
+    if constexpr (kMayBeFast) {
+      if (!precise) return launch_tiles<Small, E8M0, false, To>(k, p, s);
+    }
+    return launch_tiles<Small, E8M0, true, To>(k, p, s);
+  };
+  if (p.splits == 1) return tiles(T{});
   k.out = a.workspace;
   k.ldo = a.n;
   k.bias = nullptr;
-  const hipError_t e = p.thin ? launch_tiles<Thin, E8M0, true, float>(k, p, s)
-                              : launch_tiles<Small, E8M0, kPrecise, float>(k, p, s);
+  const hipError_t e = tiles(0.f);
   if (e != hipSuccess) return e;
   const int64_t threads = a.m * ((a.n + 3) / 4);
   TimedLaunch t(s, K_FP8_JOIN);
@@ -852,7 +861,7 @@ hipError_t fp8_quantize_run(const Fp8QuantizeArgs& a, hipStream_t s) {
 
 size_t fp8_matmul_workspace_bytes(int64_t m, int64_t n, int64_t k) {
   if (m == 0) return 0;
-  // the larger of both ways: the query does not know the output's type
+  // the larger of both ways: the query does not know the output's type, nor which is asked for
   const int64_t splits = std::max(plan_of(m, n, k, true).splits, plan_of(m, n, k, false).splits);
   return splits > 1 ? size_t(splits) * size_t(m) * size_t(n) * 4 : 0;
 }

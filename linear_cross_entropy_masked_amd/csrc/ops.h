@@ -160,6 +160,7 @@ struct Fp8MatmulArgs {
   int out_dtype;
   int64_t ldo;
   void* workspace;
+  bool precise;  // fp32 sums whatever the output's type
 };
 size_t fp8_matmul_workspace_bytes(int64_t m, int64_t n, int64_t k);
 hipError_t fp8_matmul_run(const Fp8MatmulArgs& a, hipStream_t s);

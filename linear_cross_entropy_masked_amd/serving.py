@@ -17,15 +17,16 @@ class Fp8Head(torch.nn.Module):
     """A final root-mean-square norm and a head [V, H] in 8 bits with a scale per 128 x 128 block
     (powers of two, or any number with ``scale_dtype=torch.float32``). ``weight`` in bf16, fp16 or
     fp32, H a multiple of 16; ``norm_weight`` [H] of the hidden states' type or fp32, or None;
-    ``bias`` fp32 [V] or None (minus infinity bans a token)."""
+    ``bias`` fp32 [V] or None (minus infinity bans a token). ``precise``: bf16 logits of more than 64
+    rows from fp32 sums, as all others are (see :func:`fp8_matmul`)."""
 
     def __init__(self, weight, norm_weight=None, bias=None, *, eps: float = 1e-6,
-                 scale_dtype=None, logits_dtype=torch.bfloat16):
+                 scale_dtype=None, logits_dtype=torch.bfloat16, precise: bool = False):
         super().__init__()
         if weight.dim() != 2 or weight.shape[1] % 16:
             raise ValueError("weight must be [V, H] with H a multiple of 16, got "
                              f"{tuple(weight.shape)}")
-        self.eps, self.logits_dtype = eps, logits_dtype
+        self.eps, self.logits_dtype, self.precise = eps, logits_dtype, precise
         q, scales = fp8_quantize(weight.detach().contiguous(), block_rows=128,
                                  scale_dtype=scale_dtype)
         self.register_buffer("weight", q)
@@ -50,7 +51,8 @@ class Fp8Head(torch.nn.Module):
         add = None if residual is None else residual.reshape(-1, h)
         q, c, s = rmsnorm_fp8_fwd(flat, self.norm_weight, add, eps=self.eps,
                                   scale_dtype=self.scales.dtype)
-        z = fp8_matmul(q, c, self.weight, self.scales, self.bias, dtype=self.logits_dtype)
+        z = fp8_matmul(q, c, self.weight, self.scales, self.bias, dtype=self.logits_dtype,
+                       precise=self.precise)
         return z.view(*x.shape[:-1], z.shape[1]), s.view(x.shape)
 
     @torch.no_grad()

@@ -59,3 +59,65 @@ def test_scales_whose_product_leaves_fp32(dev, m, n, k, dtype):
     byte[0, 2] = 255
     out = lce.fp8_matmul(a8, ca8, b8, cb8, dtype=dtype)
     assert torch.isnan(out[2]).all() and not torch.isnan(out[:2]).any()
+
+
+def cancelling(m, n, k, dev):
+    """Whole numbers under scales of 1: six ordinary columns of each eight beside two large ones that
+    cancel, in the first 80 eights. No partial sum, in whatever order, reaches 2^24 (80 · 448^2 and
+    64 k), so that sums in fp32 are exact."""
+    gen = torch.Generator().manual_seed(m + n + k)
+    a = torch.randint(-8, 9, (m, k), generator=gen).float()
+    b = torch.randint(-8, 9, (n, k), generator=gen).float()
+    a[:, 0:640:8], a[:, 1:640:8] = 448.0, -448.0
+    b[:, 0:640:8] = b[:, 1:640:8] = 448.0
+    ca = torch.full((-(-k // 128), m), 127, dtype=torch.uint8)
+    cb = torch.full((-(-n // 128), -(-k // 128)), 127, dtype=torch.uint8)
+    return (a.to(dev).to(E4M3), ca.to(dev).view(E8M0), b.to(dev).to(E4M3), cb.to(dev).view(E8M0))
+
+
+@pytest.mark.parametrize("scale", [E8M0, torch.float32])
+@pytest.mark.parametrize("m,n,k", [(9, 300, 272), (64, 129, 1040), (65, 130, 16), (65, 300, 1040),
+                                   (300, 1003, 272), (1003, 2051, 640), (3850, 4095, 656)])
+def test_precise(dev, m, n, k, scale):
+    """bf16 results of fp32 sums, whatever the rows: those of cancelling() are exact and rounded
+    once. Without it they are within what is documented: 2^-10 of the product of the largest
+    magnitudes of each eight columns."""
+    a, ca, b, cb = cancelling(m, n, k, dev)
+    if scale == torch.float32:
+        ca, cb = torch.ones(ca.shape, device=dev), torch.ones(cb.shape, device=dev)
+    bias = torch.randint(-9, 10, (n,), device=dev).float()
+    exact = a.double() @ b.double().t() + bias.double()
+    out = lce.fp8_matmul(a, ca, b, cb, bias, precise=True)
+    assert torch.equal(out, exact.float().bfloat16())
+    fast = lce.fp8_matmul(a, ca, b, cb, bias)
+    if m <= 64:
+        assert torch.equal(fast, out)
+    else:
+        a8, b8 = (torch.nn.functional.pad(t.double().abs(), (0, -k % 8)).view(len(t), -1, 8).amax(-1)
+                  for t in (a, b))
+        tol = 2.0 ** -10 * (a8 @ b8.t()) + exact.abs() * 2.0 ** -8
+        assert ((fast.double() - exact).abs() <= 1.01 * tol).all()
+    for dtype in (torch.float16, torch.float32):  # nothing to choose
+        plain, asked = (lce.fp8_matmul(a, ca, b, cb, bias, dtype=dtype, precise=p)
+                        for p in (False, True))
+        assert torch.equal(plain, asked) and torch.equal(plain, exact.to(dtype))
+
+
+def test_precise_into_graph_and_head(dev):
+    from linear_cross_entropy_masked_amd.serving import Fp8Head
+    a, ca, b, cb = cancelling(300, 700, 1040, dev)
+    out = torch.empty(300, 707, device=dev, dtype=torch.bfloat16)[:, 3:703]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        lce.fp8_matmul(a, ca, b, cb, out=out, precise=True)
+    ref = lce.fp8_matmul(a, ca, b, cb, dtype=torch.float32).bfloat16()
+    for _ in range(3):
+        out.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, ref)
+    torch.manual_seed(0)
+    w, x = torch.randn(700, 256, device=dev).bfloat16(), torch.randn(100, 256, device=dev).bfloat16()
+    z, _ = Fp8Head(w, precise=True)(x)
+    fp32, _ = Fp8Head(w, logits_dtype=torch.float32)(x)
+    assert z.dtype == torch.bfloat16 and torch.equal(z, fp32.bfloat16())
