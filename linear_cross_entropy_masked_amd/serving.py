@@ -18,7 +18,8 @@ class Fp8Head(torch.nn.Module):
     (powers of two, or any number with ``scale_dtype=torch.float32``). ``weight`` in bf16, fp16 or
     fp32, H a multiple of 16; ``norm_weight`` [H] of the hidden states' type or fp32, or None;
     ``bias`` fp32 [V] or None (minus infinity bans a token). ``precise``: bf16 logits of more than 64
-    rows from fp32 sums, as all others are (see :func:`fp8_matmul`)."""
+    rows from fp32 sums, as all others are (see :func:`fp8_matmul`). A cast of the module, or of a
+    model that holds it, reaches ``norm_weight`` alone."""
 
     def __init__(self, weight, norm_weight=None, bias=None, *, eps: float = 1e-6,
                  scale_dtype=None, logits_dtype=torch.bfloat16, precise: bool = False):
@@ -34,6 +35,26 @@ class Fp8Head(torch.nn.Module):
         self.register_buffer("norm_weight", None if norm_weight is None
                              else norm_weight.detach().clone())
         self.register_buffer("bias", None if bias is None else bias.detach().clone())
+
+    def _apply(self, fn, *args, **kw):
+        """Moves are a module's; a cast, of this module or of a model around it, is for what follows
+        the hidden states' type and leaves the 8-bit weight, its scales and the fp32 bias as they
+        are. torch takes 8-bit numbers and exponent bytes for floating point, so they pass as
+        integers."""
+        held = {}
+        for name in ("weight", "scales", "bias"):
+            t = self._buffers[name]
+            if t is not None:
+                as_bits = t.view(torch.uint8 if t.element_size() == 1 else torch.int32)
+                held[name], self._buffers[name] = (t.dtype, as_bits), as_bits
+        try:
+            return super()._apply(fn, *args, **kw)
+        finally:
+            for name, (dtype, as_bits) in held.items():
+                t = self._buffers[name]
+                if t.dtype != as_bits.dtype:  # Module.type casts integers as well
+                    t = as_bits.to(t.device)
+                self._buffers[name] = t.view(dtype)
 
     @classmethod
     def of(cls, head, **kw):

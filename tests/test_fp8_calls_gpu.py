@@ -121,3 +121,18 @@ def test_precise_into_graph_and_head(dev):
     z, _ = Fp8Head(w, precise=True)(x)
     fp32, _ = Fp8Head(w, logits_dtype=torch.float32)(x)
     assert z.dtype == torch.bfloat16 and torch.equal(z, fp32.bfloat16())
+
+
+@pytest.mark.parametrize("scale", [None, torch.float32])
+def test_head_in_a_cast_model(dev, scale):
+    """A model around a head that is cast to the type of its hidden states answers as before."""
+    from linear_cross_entropy_masked_amd.serving import Fp8Head
+    torch.manual_seed(0)
+    w, nw = torch.randn(700, 256, device=dev), torch.rand(256, device=dev) + 0.5
+    model = torch.nn.ModuleDict({"head": Fp8Head(w, nw.bfloat16().float(),
+                                                 torch.randn(700, device=dev), scale_dtype=scale)})
+    x = torch.randn(20, 256, device=dev).bfloat16()
+    before, _ = model["head"](x)
+    after, _ = model.to(torch.bfloat16)["head"](x)
+    assert torch.equal(before, after) and model["head"].norm_weight.dtype == torch.bfloat16
+    assert torch.equal(model.cpu().to(dev)["head"](x)[0], before)
