@@ -905,18 +905,22 @@ def _fp8_outputs(out, scales, scale_dtype, n, h, rows, cols, device):
 
 
 def rmsnorm_fp8_fwd(x, weight=None, residual=None, *, eps: float = 1e-6, scale_dtype=None,
-                    out=None, scales=None, residual_out=None):
+                    out=None, scales=None, residual_out=None, return_rstd: bool = False):
     """:func:`rmsnorm_fwd` with its result in 8 bits (float8_e4m3fn) and a scale per row and block
     of 128 columns: float8_e8m0fnu (the default, powers of two) or float32, [ceil(h / 128), n].
-    The left operand of :func:`fp8_matmul`. Returns (q, scales, s)."""
+    The left operand of :func:`fp8_matmul`. Returns (q, scales, s), and with ``return_rstd`` rstd
+    fp32 [n] as a fourth, for :func:`rmsnorm_bwd`."""
+    import torch
     code, dev, n, h, ldx, ldr, weight, pcode, total, ldro = _rms_inputs(x, weight, residual,
                                                                         residual_out)
     out, ldq, scales, scode, lds = _fp8_outputs(out, scales, scale_dtype, n, h,
                                                 -(-h // FP8_BLOCK), n, dev)
+    rstd = torch.empty(n, dtype=torch.float32, device=dev) if return_rstd else None
     _call("rmsnorm_fp8_fwd", dev, x.data_ptr(), code, n, h, ldx, _adr(residual), ldr,
           _adr(weight), pcode, eps, out.data_ptr(), ldq, scales.data_ptr(), scode, lds,
-          _adr(total), ldro, None)
-    return out, scales, (x if total is None else total)
+          _adr(total), ldro, _adr(rstd))
+    total = x if total is None else total
+    return (out, scales, total, rstd) if return_rstd else (out, scales, total)
 
 
 def rmsnorm_workspace_size(n: int, h: int) -> int:

@@ -72,3 +72,24 @@ def test_special_weights(dev, h, dtype):
         half = torch.clamp(exact.abs() * (f.eps / 2), min=f.smallest_normal * f.eps / 2)
         err = (y.double() - exact).abs()
         assert (err[few] <= (1.01 * (36 * 2.0 ** -24 * exact.abs() + half))[few]).all()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
+@pytest.mark.parametrize("h", [7, 128, 2051, 4096, 20003])
+def test_rstd_of_the_8_bit_form(dev, h, dtype):
+    """The statistics beside 8-bit rows are those of the 16-bit form, and serve the backward."""
+    x = (torch.randn(33, h, device=dev) * 2).to(dtype)
+    r = torch.randn(33, h, device=dev).to(dtype)
+    w, g = torch.rand(h, device=dev).to(dtype) + 0.5, torch.randn(33, h, device=dev).to(dtype)
+    for scale in (None, torch.float32):
+        q, c, s, rstd = lce.rmsnorm_fp8_fwd(x, w, r, eps=EPS, scale_dtype=scale, return_rstd=True)
+        _, total, stats = lce.rmsnorm_fwd(x, w, r, eps=EPS)
+        assert torch.equal(s, total) and torch.equal(rstd, stats)
+        plain = lce.rmsnorm_fp8_fwd(x, w, r, eps=EPS, scale_dtype=scale)
+        assert len(plain) == 3
+        for a, b in zip(plain[:2], (q, c)):
+            assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+        for a, b in zip(lce.rmsnorm_bwd(g, s, rstd, w), lce.rmsnorm_bwd(g, total, stats, w)):
+            assert torch.equal(a, b)
+    *_, rstd = lce.rmsnorm_fp8_fwd(x[:0], w, return_rstd=True)
+    assert rstd.shape == (0,)
