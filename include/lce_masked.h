@@ -602,6 +602,8 @@ typedef struct {
  * parents[b, j] is outside 0 .. beams - 1. `states` is a host array; all of them share parents
  * (int32 [batch, slots]). in == out with the same strides and slots == beams reorders in place
  * (all states of a call or none); otherwise no out may share bytes with any in or other out.
+ * States may interlace, such as keys and values [batch, beams, 2, length, dim] in one tensor, in
+ * place or not; calls that interlace thousands of them are refused.
  * Runs of one out do not overlap. States without bytes are passed over. count <= 2^16, beams and
  * slots <= BEAM_MAX_BEAMS, a state spans at most 2^50 bytes in at most 2^23 pieces of a run (of
  * 16 KiB, in place of 32 KiB / beams). */

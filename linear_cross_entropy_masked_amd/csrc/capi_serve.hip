@@ -173,17 +173,99 @@ bool runs_apart(int64_t batch, int64_t slots, int64_t entry, int64_t beam, int64
   return true;
 }
 
-// Whether a written range meets a read or another written one: in the order of their starts, a
-// range meets an earlier one that ends behind its start.
+// What a call reads or writes of one state: runs of `bytes` bytes at at.lo plus multiples of the
+// strides.
 struct Used {
-  Span at;
+  Span at;  // from the first byte to behind the last
   bool written;
+  int64_t bytes;
+  int64_t dims[3], strides[3];
 };
-bool written_meets(std::vector<Used>& all) {
-  std::sort(all.begin(), all.end(), [](const Used& a, const Used& b) { return a.at.lo < b.at.lo; });
+
+// Whether two such sets share a byte. A run of one at offset x of its start and one of the other at
+// offset y meet where x - y lies in (d - a.bytes, d + b.bytes), d the distance of the starts; x - y
+// is a sum of multiples of the strides. They are tried from the longest stride on, as far as the
+// shorter ones can make up for it: for strides that hold what the shorter ones span, two or three
+// multiples of each. `steps` bounds the work of a call; without any left the answer is yes.
+struct Meet {
+  int64_t strides[6], least[6], most[6];  // and the multiples of each
+  int64_t low[7], high[7];                // what a stride and the shorter ones may add up to
+  int terms = 0;
+  int64_t* steps;
+
+  void add(int64_t stride, int64_t from, int64_t to) {
+    if (stride == 0 || from == to) return;
+    int k = 0;
+    while (k < terms && strides[k] != stride) ++k;
+    if (k == terms) {
+      strides[terms] = stride;
+      least[terms] = most[terms] = 0;
+      ++terms;
+    }
+    least[k] += from;
+    most[k] += to;
+  }
+  // Whether some sum of the terms from k on lies in [from, to].
+  bool some(int k, int64_t from, int64_t to) const {
+    if (from > high[k] || to < low[k]) return false;
+    if (k == terms) return true;  // the empty sum, 0
+    if (--*steps < 0) return true;
+    const int64_t s = strides[k];
+    // from - high[k + 1] <= t s <= to - low[k + 1]
+    const int64_t a = from - high[k + 1], b = to - low[k + 1];
+    const int64_t first = std::max(least[k], a >= 0 ? (a + s - 1) / s : -(-a / s));
+    const int64_t last = std::min(most[k], b >= 0 ? b / s : -((-b + s - 1) / s));
+    for (int64_t t = first; t <= last; ++t)
+      if (some(k + 1, from - t * s, to - t * s)) return true;
+    return false;
+  }
+};
+bool share_bytes(const Used& a, const Used& b, int64_t* steps) {
+  Meet m;
+  m.steps = steps;
+  for (int i = 0; i < 3; ++i) {
+    m.add(a.strides[i], 0, a.dims[i] - 1);
+    m.add(b.strides[i], 1 - b.dims[i], 0);
+  }
+  for (int i = 0; i < m.terms; ++i)
+    for (int j = 0; j + 1 < m.terms - i; ++j)
+      if (m.strides[j] < m.strides[j + 1]) {
+        std::swap(m.strides[j], m.strides[j + 1]);
+        std::swap(m.least[j], m.least[j + 1]);
+        std::swap(m.most[j], m.most[j + 1]);
+      }
+  m.low[m.terms] = m.high[m.terms] = 0;
+  for (int k = m.terms - 1; k >= 0; --k) {
+    m.low[k] = m.low[k + 1] + m.least[k] * m.strides[k];
+    m.high[k] = m.high[k + 1] + m.most[k] * m.strides[k];
+  }
+  const int64_t d = b.at.lo >= a.at.lo ? int64_t(b.at.lo - a.at.lo) : -int64_t(a.at.lo - b.at.lo);
+  return m.some(0, d - a.bytes + 1, d + b.bytes - 1);
+}
+
+// Whether anything written shares a byte with what is read or with another that is written. In the
+// order of their starts a range that meets an earlier one starts before that one's end: where none
+// does, that is all. States that interlace (keys and values in one tensor, say) are then looked at
+// pair by pair; too many of them for kMeetSteps count as sharing.
+// `open`: room for as many indices, those of the ranges that have not ended.
+constexpr int64_t kMeetSteps = int64_t(1) << 20;
+bool written_meets(std::vector<Used>& all, std::vector<size_t>& open) {
+  std::sort(all.begin(), all.end(),
+            [](const Used& a, const Used& b) { return a.at.lo < b.at.lo; });
   uintptr_t read_to = 0, written_to = 0;
-  for (const Used& u : all) {
-    if (u.at.lo < written_to || (u.written && u.at.lo < read_to)) return true;
+  int64_t steps = kMeetSteps;
+  for (size_t i = 0; i < all.size(); ++i) {
+    const Used& u = all[i];
+    if (u.at.lo < written_to || (u.written && u.at.lo < read_to)) {
+      open.erase(std::remove_if(open.begin(), open.end(),
+                                [&](size_t j) { return all[j].at.hi <= u.at.lo; }),
+                 open.end());
+      for (size_t j : open) {
+        if (--steps < 0) return true;
+        if ((u.written || all[j].written) && share_bytes(all[j], u, &steps)) return true;
+      }
+    }
+    open.push_back(i);
     uintptr_t& to = u.written ? written_to : read_to;
     to = std::max(to, u.at.hi);
   }
@@ -372,12 +454,14 @@ int beam_reorder(const lce_beam_state* states, int64_t count, const int32_t* par
   if (!parents) return LCE_ERR_NULL_ARG;
   if (!aligned(parents, 4)) return LCE_ERR_ALIGNMENT;
   std::vector<Used> used;
+  std::vector<size_t> open;
   try {
     used.reserve(2 * size_t(count) + 1);
+    open.reserve(2 * size_t(count) + 1);
   } catch (const std::bad_alloc&) {
     return LCE_ERR_SCRATCH_LIMIT;
   }
-  used.push_back({span(parents, 4 * batch * slots), false});
+  used.push_back({span(parents, 4 * batch * slots), false, 4 * batch * slots, {1, 1, 1}, {}});
   bool inplace = false;
   for (int64_t i = 0; i < count; ++i) {
     const lce_beam_state& st = states[i];
@@ -400,10 +484,13 @@ int beam_reorder(const lce_beam_state* states, int64_t count, const int32_t* par
                       st.in_beam == st.out_beam && st.in_segment == st.out_segment &&
                       slots == beams;
     if (same != inplace) return LCE_ERR_OVERLAP;
-    used.push_back({span(st.out, bo), true});
-    if (!inplace) used.push_back({span(st.in, bi), false});
+    used.push_back({span(st.out, bo), true, st.segment_bytes, {batch, slots, st.segments},
+                    {st.out_entry, st.out_beam, st.out_segment}});
+    if (!inplace)
+      used.push_back({span(st.in, bi), false, st.segment_bytes, {batch, beams, st.segments},
+                      {st.in_entry, st.in_beam, st.in_segment}});
   }
-  if (written_meets(used)) return LCE_ERR_OVERLAP;
+  if (written_meets(used, open)) return LCE_ERR_OVERLAP;
   const int rc = check_device();
   if (rc != LCE_OK) return rc;
   LCE_TRY_HIP(beam_reorder_run(states, count, parents, batch, beams, slots, inplace,
