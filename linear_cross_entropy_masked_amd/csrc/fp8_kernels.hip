@@ -722,7 +722,8 @@ __global__ void __launch_bounds__(64 * WAVES) fp8_few_kernel(MatmulK a) {
 // wavefronts of a SIMD half a slice apart (3.83 and 3.73), workgroups that go from tile to tile
 // (3.6 to 3.9). On 8192 x 8192
 // x 32768: 256 x 128 tiles in three slots (2.5 ms and 1.8), which also take 42.5 us for 2048 x
-// 4096 x 4096 (small tiles 41).
+// 4096 x 4096 (small tiles 41). Non-temporal stores: 3.67 ms and 3.69, but 49 us and 44 for 1003 x 768 x
+// 32777.
 using Wide = Cfg<256, 256, 2, 2, 4, 1>;
 using Small = Cfg<128, 128, 2, 2, 2, 2>;
 // 17 to 64 rows: B passes through once, with two slices on the way in each of two workgroups
@@ -750,10 +751,12 @@ Plan plan_of(int64_t m, int64_t n, int64_t k, bool precise) {
   p.per = blocks;
   if (p.few) return p;
   p.thin = m <= kThinRows;
-  // Rounds of tiles over the 256 CUs, one large or two small ones each: a round of small tiles
-  // takes 0.52 (768 columns) to 0.59 (4096) of the time of a round of large ones, so the large ones
-  // are for where they do not need that many rounds more (4096 x 4096 x 4096: 59 us and 70;
-  // 1003 x 32777 x 768, 516 of them: 57 us and 46).
+  // Rounds of tiles over the 256 CUs, one large or two small ones each: a round of small tiles takes
+  // 0.54 to 0.69 of the time of a round of large ones, so the large ones are for where they do not
+  // need that many rounds more. Small and large tiles with fp32 scales, in us: 1003 x 768 x 32777 44
+  // and 49, 2048 x 4096 x 4096 40 and 59, 4096 x 4096 x 4096 80 and 65, 8192 x 768 x 4096 49 and 35,
+  // 8192 x 4096 x 128256 5310 and 4050; with e8m0 scales: 1003 x 768 x 32777 39 and 46, 4100 x 768 x
+  // 4095 27 and 31, 4096 x 4096 x 4096 68 and 59, 8192 x 4096 x 128256 5300 and 3690.
   const int64_t large = (m + 255) / 256 * ((n + 255) / 256);
   const int64_t small = (m + 127) / 128 * ((n + 127) / 128);
   p.wide = !precise && large >= 256 && 100 * ((large + 255) / 256) < 58 * ((small + 511) / 512);
