@@ -12,6 +12,8 @@ from . import beam_reorder, beam_step, fp8_matmul, fp8_quantize, rmsnorm_fp8_fwd
 
 __all__ = ["Fp8Head", "beam_reorder", "beam_step"]
 
+_INTEGERS = {1: torch.uint8, 2: torch.int16, 4: torch.int32, 8: torch.int64}  # by bytes
+
 
 class Fp8Head(torch.nn.Module):
     """A final root-mean-square norm and a head [V, H] in 8 bits with a scale per 128 x 128 block
@@ -20,6 +22,8 @@ class Fp8Head(torch.nn.Module):
     ``bias`` fp32 [V] or None (minus infinity bans a token). ``precise``: bf16 logits of more than 64
     rows from fp32 sums, as all others are (see :func:`fp8_matmul`). A cast of the module, or of a
     model that holds it, reaches ``norm_weight`` alone."""
+
+    precise = False  # of a head that was pickled without it
 
     def __init__(self, weight, norm_weight=None, bias=None, *, eps: float = 1e-6,
                  scale_dtype=None, logits_dtype=torch.bfloat16, precise: bool = False):
@@ -45,7 +49,7 @@ class Fp8Head(torch.nn.Module):
         for name in ("weight", "scales", "bias"):
             t = self._buffers[name]
             if t is not None:
-                as_bits = t.view(torch.uint8 if t.element_size() == 1 else torch.int32)
+                as_bits = t.view(_INTEGERS[t.element_size()])
                 held[name], self._buffers[name] = (t.dtype, as_bits), as_bits
         try:
             return super()._apply(fn, *args, **kw)
