@@ -189,8 +189,8 @@ struct PairScale {
   }
 };
 // The same where the multiplications are what takes time and not memory: the shift goes into the row
-// as it is widened, as far as bf16 holds its numbers and fp32 their products (448 · 2^118, 2^-18 ·
-// 2^-96), and what is left, 1 for scales nearer to one another, onto the sums. 8192 x 4096 x 32768 with
+// as it is widened, as far as fp32 holds any sum of a block's products (128 · 448^2 · 2^102) and each of
+// them (2^-18 · 2^-96), and what is left, 1 for scales nearer to one another, onto the sums. 8192 x 4096 x 32768 with
 // fp32 outputs: 2.12 ms, 2% more than a product in fp32 that may be lost; shifted sums take 6% more
 // than that, a branch for products that leave fp32 12%.
 template <bool E8M0>
@@ -199,7 +199,7 @@ struct RowScale {
   __device__ __forceinline__ RowScale(uint32_t sa, uint32_t sb) {
     if constexpr (E8M0) {
       const int e = int(sa + sb) - 254;
-      const int in = min(max(e, -96), 118), out = min(max(e - in, -127), 127);  // 2^-127: as 0
+      const int in = min(max(e, -96), 102), out = min(max(e - in, -127), 127);  // 2^-127: as 0
       row = __uint_as_float(uint32_t(in + 127) << 23);
       sum = __uint_as_float(sa == 255u || sb == 255u ? kNanBits : uint32_t(out + 127) << 23);
     } else {

@@ -136,3 +136,33 @@ def test_head_in_a_cast_model(dev, scale):
     after, _ = model.to(torch.bfloat16)["head"](x)
     assert torch.equal(before, after) and model["head"].norm_weight.dtype == torch.bfloat16
     assert torch.equal(model.cpu().to(dev)["head"](x)[0], before)
+
+
+@pytest.mark.parametrize("m,n,k", [(13, 256, 128), (52, 200, 272), (130, 256, 128),
+                                   (300, 300, 1040)])
+def test_large_scales_over_sums_that_cancel(dev, m, n, k):
+    """Products of 448^2 that cancel within a block, all 128 of them in pairs but two of 0 and 2^-18,
+    under scales up to 2^145: fp32 holds the block's sum in any order (126 · 448^2 < 2^25), so the
+    scale may not meet the products before they are added where it would carry them past fp32, and
+    nothing is NaN. Exact is 2^-18 times the scale, but beside 448^2 fp32 has steps of 2^-6, so the
+    sum of 128 products is off by up to 2 (128 + 8) 2^-24 of the sum of their magnitudes, 410; times
+    the scale that is finite up to 2^118."""
+    powers = torch.tensor([0, 60, 90, 100, 102, 103, 104, 110, 111, 118, 125, 140, 145], device=dev)
+    e = powers[torch.arange(m, device=dev) % len(powers)]
+    a = torch.zeros(m, k, device=dev)
+    a[:, 0:126:2], a[:, 1:126:2] = 448.0, -448.0
+    a[:, 127] = 2.0 ** -9
+    b = torch.full((n, k), 448.0, device=dev)
+    b[:, 127] = 2.0 ** -9
+    ca = torch.full((-(-k // 128), m), 127, dtype=torch.uint8, device=dev)
+    ca[0] = (e - 40 + 127).to(torch.uint8)
+    cb = torch.full((-(-n // 128), -(-k // 128)), 127, dtype=torch.uint8, device=dev)
+    cb[:, 0] = 127 + 40
+    args = a.to(E4M3), ca.view(E8M0), b.to(E4M3), cb.view(E8M0)
+    exact = torch.exp2(e.double() - 18)[:, None].expand(m, n)
+    for dtype in (torch.float32, torch.bfloat16):
+        out = lce.fp8_matmul(*args, dtype=dtype, precise=True)
+        assert not torch.isnan(out).any(), e[torch.isnan(out).any(1)].unique()
+        tol = 2 * 136 * 2.0 ** -24 * 126 * 448.0 ** 2 * torch.exp2(e.double())[:, None]
+        near = (out.double() - exact).abs() <= tol + exact * torch.finfo(dtype).eps
+        assert near[e <= 118].all()
