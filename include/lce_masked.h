@@ -537,8 +537,8 @@ int fp8_matmul_workspace_size(int64_t m, int64_t n, int64_t k, size_t* bytes);
  * the product of the group's largest |a| and |b| (scales included): for normally distributed
  * operands 1.4e-5 of the result's size, a hundredth of a bf16 step; where large products cancel, far
  * more of the result than fp32 sums lose. Powers of two scale these products before they are added:
- * above 2^100 that may carry them past fp32 where they cancel. fp8_matmul_precise forms fp32 sums whatever out_dtype and
- * m, in 1.2 to 2.2 times the time of such outputs, with the same workspace.
+ * above 2^100 that may carry them past fp32 where they cancel. fp8_matmul_precise forms fp32 sums
+ * whatever out_dtype and m, in 1.2 to 2.2 times the time of such outputs, with the same workspace.
  *   a  [m, lda], b [n, ldb]  e4m3, first k columns; 16-byte aligned, lda and ldb multiples of 16
  *   a_scales  [ceil(k / 128), ldas]      b_scales  [ceil(n / 128), ldbs]
  *   bias  fp32 [n] or NULL               out  out_dtype [m, ldo], first n columns
